@@ -362,6 +362,185 @@ sp_status_t sp_norm_bwd_bitmask(const void* const* dy, const void* const* z,
                                 void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                 void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators between g and the next g*.
+ *
+ * There each rank holds the whole sequence and its own slice of the channels
+ * or heads (the column-parallel linear's output), so a tensor is an array of
+ * t device pointers, every one of the same shape.  Conventions as above, with
+ * these additions:
+ *  - dtype: the element type of every activation and of gamma / beta; states,
+ *    statistics and parameter gradients are float32.  Arithmetic is float32,
+ *    each stored value rounded once (to nearest even).
+ *  - Row strides ("*_ld") count elements between consecutive tokens, so that
+ *    a slice of a wider (fused) projection can be passed as it is; a batch row
+ *    follows the last row of the one before it.  Multiples of 8 elements, at
+ *    least the row's width.
+ *  - cu_seqlens as above: NULL (dense) or the packed sequences' prefix sums,
+ *    with b == 1.  Sequences without tokens are allowed.  What the outputs
+ *    hold is undefined where the device check fails, but no access leaves the
+ *    buffers.
+ *  - Results do not depend on timing: sums and scans are joined in a fixed
+ *    order.
+ * ------------------------------------------------------------------------ */
+
+typedef enum sp_dtype { SP_BF16 = 0, SP_F16 = 1, SP_F32 = 2 } sp_dtype_t;
+
+typedef enum sp_act {
+  SP_ACT_NONE = 0,
+  SP_ACT_SILU = 1            /* q * sigmoid(q) */
+} sp_act_t;
+
+typedef enum sp_rope_layout {
+  SP_ROPE_HALF = 0,          /* pair i = elements i and i + rot_dim / 2 of the head */
+  SP_ROPE_INTERLEAVED = 1    /* pair i = elements 2i and 2i + 1 */
+} sp_rope_layout_t;
+
+typedef enum sp_rope_scaling {
+  SP_ROPE_PLAIN = 0,         /* w_i = base^(-2i / rot_dim) */
+  SP_ROPE_LINEAR = 1,        /* w_i / factor: positions squeezed */
+  SP_ROPE_BASE = 2,          /* base * factor^(rot_dim / (rot_dim - 2)): the slowest pair
+                                turns 1 / factor as fast, the fastest as before */
+  SP_ROPE_PARTS = 3          /* w_i (g + (1 - g) / factor), g = clamp((n_i - low) / (high - low),
+                                0, 1), n_i = the turns of pair i over original_len positions:
+                                fast pairs stay, slow ones are squeezed */
+} sp_rope_scaling_t;
+
+#define SP_ROPE_MAX_PAIRS 256
+#define SP_ROPE_MAX_HEADS 4096
+#define SP_MAX_GROUP_CHANNELS 4096
+
+/* The frequencies of a head's pairs, filled by sp_rope_table (host memory). */
+typedef struct sp_rope_table {
+  int32_t pairs;                        /* rot_dim / 2 */
+  float mscale;                         /* factor on cosine and sine */
+  uint64_t turns[SP_ROPE_MAX_PAIRS];    /* turns per position, in units of 2^-64 */
+} sp_rope_table_t;
+
+/*
+ * sp_rope_table -- frequencies of rotary positions, on the host.  Nothing is
+ * enqueued.  rot_dim: rotated elements of a head, even, 2 .. 512; base >= 1;
+ * factor >= 1 (ignored by SP_ROPE_PLAIN); SP_ROPE_BASE needs rot_dim > 2;
+ * original_len > 0 and high_turns > low_turns for SP_ROPE_PARTS (else ignored).
+ */
+sp_status_t sp_rope_table(int32_t rot_dim, double base, sp_rope_scaling_t scaling, double factor,
+                          int64_t original_len, double low_turns, double high_turns, double mscale,
+                          sp_rope_table_t* out);
+
+/*
+ * sp_rope_fwd -- rotary positions on the heads of all ranks.
+ *   (u, v) -> mscale (u cos x - v sin x, v cos x + u sin x),  x = position * w_i
+ * for the rotated pairs of every head; the d - rot_dim elements after them are
+ * copied.  Angles are exact modulo one turn for positions of any size.
+ *
+ * x, y [t] (b, s, heads, d)  rank r's heads; x_ld, y_ld between tokens,
+ *                    x_head, y_head between heads (elements, >= d; row strides
+ *                    of any value >= heads' extent)
+ * positions          device int64 (b, s), or NULL: the token's index in its batch
+ *                    row, or with cu_seqlens in its packed sequence,
+ * first_position     plus this (ignored with positions)
+ * y[r] == x[r] with equal strides rotates in place (what is not rotated is then
+ * not touched); no other overlap.
+ */
+sp_status_t sp_rope_fwd(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, int64_t s,
+                        int64_t heads, int64_t d, int32_t t, sp_dtype_t dtype,
+                        const sp_rope_table_t* table, sp_rope_layout_t layout,
+                        const int64_t* positions, int64_t first_position,
+                        const int32_t* cu_seqlens, int32_t n_seqs, void* const* y, int64_t y_ld,
+                        int64_t y_head, int32_t* dev_status, void* stream);
+
+/* sp_rope_bwd -- the transpose: x is dy, y is dx, the rotation goes back. */
+sp_status_t sp_rope_bwd(const void* const* dy, int64_t dy_ld, int64_t dy_head, int64_t b,
+                        int64_t s, int64_t heads, int64_t d, int32_t t, sp_dtype_t dtype,
+                        const sp_rope_table_t* table, sp_rope_layout_t layout,
+                        const int64_t* positions, int64_t first_position,
+                        const int32_t* cu_seqlens, int32_t n_seqs, void* const* dx, int64_t dx_ld,
+                        int64_t dx_head, int32_t* dev_status, void* stream);
+
+/*
+ * sp_gated_scan_fwd -- gated linear recurrence along every sequence, each
+ * channel on its own:
+ *   a = sigmoid(gate), k = sigmoid(-gate) = 1 - a
+ *   h[i] = a[i] h[i-1] + k[i] value[i]   (tied != 0)
+ *   h[i] = a[i] h[i-1] + value[i]        (tied == 0)
+ *   y[i] = h[i],  h[-1] = h0 of the sequence (0 without h0)
+ *
+ * gate, value, y [t] (b, s, c)      c a multiple of 8, at most SP_MAX_HIDDEN
+ * h0, hT         [t] (n, c) float32 or NULL arrays: the state before and after each
+ *                    sequence, n = n_seqs or b; hT[r] == h0[r] is allowed
+ *                    (a sequence without tokens: hT = h0)
+ * states         [t] (b, ceil(s / 16), c) float32 or a NULL array: the states the
+ *                    backward starts from (output); their contents are internal
+ * s == 1 without cu_seqlens is a decoding step of b sequences.
+ */
+sp_status_t sp_gated_scan_fwd(const void* const* gate, int64_t gate_ld, const void* const* value,
+                              int64_t value_ld, const float* const* h0, int64_t b, int64_t s,
+                              int64_t c, int32_t t, sp_dtype_t dtype, int32_t tied,
+                              const int32_t* cu_seqlens, int32_t n_seqs, void* const* y,
+                              int64_t y_ld, float* const* hT, float* const* states,
+                              int32_t* dev_status, void* stream);
+
+/*
+ * sp_gated_scan_bwd -- gradients of sp_gated_scan_fwd called with the same
+ * gate, value, h0 and shape, from the states it saved.
+ *
+ * dy     [t] (b, s, c)        gradient of y
+ * dhT    [t] (n, c) float32   gradient of hT, or a NULL array (zero)
+ * dgate, dvalue [t] (b, s, c) outputs
+ * dh0    [t] (n, c) float32   output or a NULL array; dh0[r] == dhT[r] is allowed
+ */
+sp_status_t sp_gated_scan_bwd(const void* const* gate, int64_t gate_ld, const void* const* value,
+                              int64_t value_ld, const float* const* h0,
+                              const float* const* states, const void* const* dy, int64_t dy_ld,
+                              const float* const* dhT, int64_t b, int64_t s, int64_t c, int32_t t,
+                              sp_dtype_t dtype, int32_t tied, const int32_t* cu_seqlens,
+                              int32_t n_seqs, void* const* dgate, int64_t dgate_ld,
+                              void* const* dvalue, int64_t dvalue_ld, float* const* dh0,
+                              int32_t* dev_status, void* stream);
+
+/*
+ * sp_group_norm_fwd -- group norm with an activation, channels last.
+ *
+ * x, y   [t] (n, l, c)   n samples of l rows; c a multiple of 8.  The statistics of a
+ *                        group span the l rows and c / groups channels of a sample:
+ *                        l == 1 is the per-token norm of every head.  c / groups is a
+ *                        multiple of 8, at most SP_MAX_GROUP_CHANNELS.
+ * gamma, beta (t * c)    rank r's at r * c; beta for LayerNorm only
+ * SP_NORM_LAYERNORM: z = (x - mean) rstd;   SP_NORM_RMSNORM: z = x rstd
+ *   with rstd as in sp_rs_norm_fwd (biased variance, eps inside the root);
+ *   y = act(z gamma + beta)
+ * mean, rstd [t] (n, groups) float32 outputs (mean: LayerNorm, else NULL)
+ */
+sp_status_t sp_group_norm_fwd(const void* const* x, int64_t x_ld, const void* gamma,
+                              const void* beta, int64_t n, int64_t l, int64_t c, int64_t groups,
+                              int32_t t, sp_dtype_t dtype, float eps, sp_norm_t norm, sp_act_t act,
+                              void* const* y, int64_t y_ld, float* const* mean,
+                              float* const* rstd, void* stream);
+
+/* Bytes of the workspace of sp_group_norm_bwd (0 for an invalid shape). */
+size_t sp_group_norm_bwd_workspace_bytes(int64_t n, int64_t l, int64_t c, int64_t groups,
+                                         int32_t t, sp_dtype_t dtype);
+
+/*
+ * sp_group_norm_bwd -- gradients of sp_group_norm_fwd from its input and saved
+ * statistics.
+ *
+ * dy, dx [t] (n, l, c)          gradient of y; output
+ * dgamma, dbeta (t * c) float32 outputs, each may be NULL (dbeta: LayerNorm)
+ * workspace                     device scratch of the size above (may be NULL if
+ *                               neither parameter gradient is wanted); used until the
+ *                               call's work on `stream` is done, so calls that may run
+ *                               at the same time (captured graphs among them) need
+ *                               one each
+ */
+sp_status_t sp_group_norm_bwd(const void* const* dy, int64_t dy_ld, const void* const* x,
+                              int64_t x_ld, const float* const* mean, const float* const* rstd,
+                              const void* gamma, const void* beta, int64_t n, int64_t l, int64_t c,
+                              int64_t groups, int32_t t, sp_dtype_t dtype, sp_norm_t norm,
+                              sp_act_t act, void* const* dx, int64_t dx_ld, float* dgamma,
+                              float* dbeta, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Thread-local text of the last non-OK status returned on this thread. */
 const char* sp_last_error(void);
 

@@ -42,6 +42,9 @@ Modules and what pins each one (tests under ``tests/test_oracle_*.py``):
   term dropped, doubled or negated), by the oracle's magnitudes staying tight
   enough that the floor rarely exceeds one ulp, and by a float32 LayerNorm
   passing the bar with few elements accepted through the floor alone.
+* ``region``      -- rotary positions, the gated recurrence and group norm.
+  Pinned by complex products, the closed form, torch's group_norm and central
+  differences.
 
 Parity unpinned: none of the functions above.  (Throughput has no page
 figure to pin against; it is measured, not compared.)

@@ -29,6 +29,18 @@ _PP = ctypes.POINTER(ctypes.c_void_p)
 
 _lib = None
 
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTS = {"none": 0, "silu": 1}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+SCAN_RUN = 16               # tokens per saved state of the gated recurrence
+
+
+class RopeTable(ctypes.Structure):
+    """Frequencies of a head's rotated pairs, made by sp_rope_table."""
+    _fields_ = [("pairs", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * 256)]
+
 
 class SpError(RuntimeError):
     def __init__(self, code, message):
@@ -82,6 +94,32 @@ def load():
     lib.sp_norm_bwd_noalloc.argtypes = [
         _PP, _PP, _PP, _PP, _PP, _vp, _PP, _i64, _i64, _i64, _i32, ctypes.c_double, _vp, _i32,
         _i32, _PP, _PP, _i32, _vp, _vp, _vp, _vp, _vp]
+    tab = ctypes.POINTER(RopeTable)
+    lib.sp_rope_table.restype = _i32
+    lib.sp_rope_table.argtypes = [_i32, ctypes.c_double, _i32, ctypes.c_double, _i64,
+                                  ctypes.c_double, ctypes.c_double, ctypes.c_double, tab]
+    for fn in (lib.sp_rope_fwd, lib.sp_rope_bwd):
+        fn.restype = _i32
+        fn.argtypes = [_vp, _i64, _i64, _i64, _i64, _i64, _i64, _i32, _i32, tab, _i32, _vp, _i64,
+                       _vp, _i32, _vp, _i64, _i64, _vp, _vp]
+    lib.sp_gated_scan_fwd.restype = _i32
+    lib.sp_gated_scan_fwd.argtypes = [
+        _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _i64,
+        _vp, _vp, _vp, _vp]
+    lib.sp_gated_scan_bwd.restype = _i32
+    lib.sp_gated_scan_bwd.argtypes = [
+        _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp,
+        _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp]
+    lib.sp_group_norm_fwd.restype = _i32
+    lib.sp_group_norm_fwd.argtypes = [
+        _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _i32, ctypes.c_float, _i32, _i32, _vp,
+        _i64, _vp, _vp, _vp]
+    lib.sp_group_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.sp_group_norm_bwd_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, _i32, _i32]
+    lib.sp_group_norm_bwd.restype = _i32
+    lib.sp_group_norm_bwd.argtypes = [
+        _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _i32,
+        _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.sp_last_error.restype = ctypes.c_char_p
     lib.sp_last_error.argtypes = []
     lib.sp_abi_version.restype = _i32
@@ -520,6 +558,298 @@ def sp_norm_bwd_noalloc(dy, z, mask, mean, rstd, gamma, dz_skip=None, *, s, p, c
             NORMS[norm], _ptr_array(dresidual), _ptr_array(dgathered), len(dgathered),
             _ptr(dgamma), _ptr(dbeta) if ln else None, _ptr(dbias), _ptr(st), _stream(dev))
     _check(code)
+
+
+# ------------------------------------------------ between g and the next g* --
+# Tensors there are lists of t rank buffers of one shape.  Rows may be slices
+# of a wider buffer: the last dimension is contiguous, and the leading ones
+# follow each other with one stride between rows, the same for every rank.
+
+def _row_stride(x, what):
+    """Elements between the rows of x (rows = every dimension but the last)."""
+    if x.is_contiguous():
+        return x.shape[-1]
+    st, sh = x.stride(), x.shape
+    if sh[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    ld, span = None, 1
+    for n, stride in zip(reversed(sh[:-1]), reversed(st[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != ld * span:
+            raise ValueError(f"{what}: rows of strides {st} do not follow each other evenly")
+        span *= n
+    return sh[-1] if ld is None else ld
+
+
+def _rank_rows(xs, shape, dtype, device, t, what):
+    """Pointer array and row stride of t rank buffers."""
+    if len(xs) != t:
+        raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
+    arr, ld = (_vp * t)(), None
+    for i, x in enumerate(xs):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{what}[{i}] must be a torch.Tensor")
+        if x.shape != shape:
+            raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(shape)}")
+        if x.dtype is not dtype:
+            raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {dtype}")
+        if x.device != device:
+            raise ValueError(f"{what}[{i}]: on {x.device}, expected {device}")
+        if i == 0:
+            ld = _row_stride(x, what)
+        elif (shape[-1] if x.is_contiguous() else _row_stride(x, what)) != ld:
+            raise ValueError(f"{what}: every rank needs the same row stride")
+        arr[i] = x.data_ptr()
+    return arr, ld
+
+
+def _rank_dense(xs, shape, dtype, device, t, what):
+    """Pointer array of t dense rank buffers (None: no array)."""
+    if xs is None:
+        return None
+    if len(xs) != t:
+        raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
+    arr = (_vp * t)()
+    for i, x in enumerate(xs):
+        if (not isinstance(x, torch.Tensor) or x.shape != shape or x.dtype is not dtype
+                or x.device != device or not x.is_contiguous()):
+            _need(x, shape, dtype, device, f"{what}[{i}]")
+        arr[i] = x.data_ptr()
+    return arr
+
+
+def _first(xs, dims, what):
+    """Ranks, dtype code and device of a list of rank buffers."""
+    t = len(xs)
+    if not 1 <= t <= MAX_RANKS:
+        raise ValueError("1 <= t <= 16")
+    x = xs[0]
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{what}[0] must be a torch.Tensor")
+    if x.dim() != dims:
+        raise ValueError(f"{what}[0]: {x.dim()} dimensions, expected {dims}")
+    if x.dtype not in DTYPES:
+        raise ValueError(f"{what}[0]: dtype {x.dtype} is not bfloat16, float16 or float32")
+    return t, x, DTYPES[x.dtype]
+
+
+def _call(dev, fn, *args):
+    """The call on the tensors' device and its current stream (the last argument)."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors on {dev}: the kernels need a CUDA device")
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, stream))
+    else:
+        with _on_device(dev):
+            _check(fn(*args, stream))
+
+
+def _choice(table, key, what):
+    if key not in table:
+        raise ValueError(f"{what}: {key!r} is not one of {sorted(table)}")
+    return table[key]
+
+
+def sp_rope_table(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original_len=0,
+                  low_turns=1.0, high_turns=32.0, mscale=1.0):
+    """Frequencies of rotary positions for heads of which rot_dim elements turn
+    (kept by the caller, one per model).  scaling: "none", "linear" (positions
+    divided by factor), "base" (base * factor^(rot_dim / (rot_dim - 2))) or
+    "parts" (pairs that turn at most low_turns times over original_len positions
+    are slowed by factor, those of high_turns or more are not, linear between);
+    mscale multiplies cosine and sine."""
+    out = RopeTable()
+    _check(load().sp_rope_table(int(rot_dim), float(base),
+                                _choice(ROPE_SCALINGS, scaling, "scaling"), float(factor),
+                                int(original_len), float(low_turns), float(high_turns),
+                                float(mscale), ctypes.byref(out)))
+    return out
+
+
+def _rope_strides(xs, shape, dtype, device, t, what):
+    """Pointer array, token stride and head stride of (b, s, heads, d) buffers."""
+    if len(xs) != t:
+        raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
+    b, s, heads, d = shape
+    arr, got = (_vp * t)(), None
+    for i, x in enumerate(xs):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError(f"{what}[{i}] must be a torch.Tensor")
+        if x.shape != shape:
+            raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(shape)}")
+        if x.dtype is not dtype:
+            raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {dtype}")
+        if x.device != device:
+            raise ValueError(f"{what}[{i}]: on {x.device}, expected {device}")
+        s0, s1, s2, s3 = x.stride()
+        if d > 1 and s3 != 1:
+            raise ValueError(f"{what}[{i}]: the last dimension must be contiguous")
+        if heads == 1:
+            s2 = d
+        if s > 1:
+            ld = s1
+            if b > 1 and s0 != s * s1:
+                raise ValueError(f"{what}[{i}]: batch rows must follow each other")
+        else:
+            ld = s0 if b > 1 else max(s1, heads * s2)
+        if got is None:
+            got = (ld, s2)
+        elif got != (ld, s2):
+            raise ValueError(f"{what}: every rank needs the same strides")
+        arr[i] = x.data_ptr()
+    return arr, got[0], got[1]
+
+
+def _rope_call(entry, x, table, layout, positions, first_position, cu_seqlens, y, status):
+    lib = load()
+    t, x0, dt = _first(x, 4, "x")
+    b, s, heads, d = x0.shape
+    dev, dtype = x0.device, x0.dtype
+    if not isinstance(table, RopeTable):
+        raise TypeError("table must come from sp_rope_table")
+    xa, x_ld, x_head = _rope_strides(x, x0.shape, dtype, dev, t, "x")
+    ya, y_ld, y_head = _rope_strides(y, x0.shape, dtype, dev, t, "y")
+    if positions is not None:
+        _need(positions, (b, s), torch.int64, dev, "positions")
+    cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
+    st = device_status(dev) if status is None else status
+    _call(dev, getattr(lib, entry), xa, x_ld, x_head, b, s, heads, d, t, dt, ctypes.byref(table),
+          _choice(ROPE_LAYOUTS, layout, "layout"), _ptr(positions), int(first_position), cu,
+          n_seqs, ya, y_ld, y_head, st.data_ptr())
+
+
+def sp_rope_fwd(x, table, *, layout="half", positions=None, first_position=0, cu_seqlens=None, y,
+                status=None):
+    """Rotary positions: turns the pairs of every head of the (b, s, heads, d) rank
+    buffers x into y (y may be x: in place).  Strides between tokens and heads are
+    free.  A token's position: positions (int64 (b, s)), else first_position plus its
+    index in its batch row, or with cu_seqlens in its packed sequence."""
+    _rope_call("sp_rope_fwd", x, table, layout, positions, first_position, cu_seqlens, y, status)
+
+
+def sp_rope_bwd(dy, table, *, layout="half", positions=None, first_position=0, cu_seqlens=None,
+                dx, status=None):
+    """Gradient of sp_rope_fwd (dx may be dy)."""
+    _rope_call("sp_rope_bwd", dy, table, layout, positions, first_position, cu_seqlens, dx, status)
+
+
+def sp_gated_scan_states_shape(b, s, c):
+    """Shape of one rank's float32 states buffer of sp_gated_scan_fwd."""
+    return (b, (s + SCAN_RUN - 1) // SCAN_RUN, c)
+
+
+def sp_gated_scan_fwd(gate, value, *, h0=None, tied=True, cu_seqlens=None, y, hT=None, states=None,
+                      status=None):
+    """Gated linear recurrence along s of (b, s, c) rank buffers:
+    h = sigmoid(gate) h + (sigmoid(-gate) value if tied else value), y = h.
+    h0, hT: float32 (sequences, c) states before and after each sequence (hT may be
+    h0); states: sp_gated_scan_states_shape buffers that sp_gated_scan_bwd needs."""
+    lib = load()
+    t, x0, dt = _first(gate, 3, "gate")
+    b, s, c = x0.shape
+    dev, dtype, f32 = x0.device, x0.dtype, torch.float32
+    ga, g_ld = _rank_rows(gate, x0.shape, dtype, dev, t, "gate")
+    va, v_ld = _rank_rows(value, x0.shape, dtype, dev, t, "value")
+    ya, y_ld = _rank_rows(y, x0.shape, dtype, dev, t, "y")
+    cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
+    n = b if cu is None else n_seqs
+    ha = _rank_dense(h0, (n, c), f32, dev, t, "h0")
+    ta = _rank_dense(hT, (n, c), f32, dev, t, "hT")
+    sa = _rank_dense(states, sp_gated_scan_states_shape(b, s, c), f32, dev, t, "states")
+    st = device_status(dev) if status is None else status
+    _call(dev, lib.sp_gated_scan_fwd, ga, g_ld, va, v_ld, ha, b, s, c, t, dt, int(bool(tied)), cu,
+          n_seqs, ya, y_ld, ta, sa, st.data_ptr())
+
+
+def sp_gated_scan_bwd(gate, value, states, dy, *, h0=None, dhT=None, tied=True, cu_seqlens=None,
+                      dgate, dvalue, dh0=None, status=None):
+    """Gradients of sp_gated_scan_fwd (same gate, value, h0, tied, cu_seqlens) from
+    the states it saved; dhT: gradient of hT, dh0 (may be dhT): gradient of h0."""
+    lib = load()
+    t, x0, dt = _first(gate, 3, "gate")
+    b, s, c = x0.shape
+    dev, dtype, f32 = x0.device, x0.dtype, torch.float32
+    ga, g_ld = _rank_rows(gate, x0.shape, dtype, dev, t, "gate")
+    va, v_ld = _rank_rows(value, x0.shape, dtype, dev, t, "value")
+    da, d_ld = _rank_rows(dy, x0.shape, dtype, dev, t, "dy")
+    dga, dg_ld = _rank_rows(dgate, x0.shape, dtype, dev, t, "dgate")
+    dva, dv_ld = _rank_rows(dvalue, x0.shape, dtype, dev, t, "dvalue")
+    cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
+    n = b if cu is None else n_seqs
+    ha = _rank_dense(h0, (n, c), f32, dev, t, "h0")
+    ta = _rank_dense(dhT, (n, c), f32, dev, t, "dhT")
+    oa = _rank_dense(dh0, (n, c), f32, dev, t, "dh0")
+    sa = _rank_dense(states, sp_gated_scan_states_shape(b, s, c), f32, dev, t, "states")
+    st = device_status(dev) if status is None else status
+    _call(dev, lib.sp_gated_scan_bwd, ga, g_ld, va, v_ld, ha, sa, da, d_ld, ta, b, s, c, t, dt,
+          int(bool(tied)), cu, n_seqs, dga, dg_ld, dva, dv_ld, oa, st.data_ptr())
+
+
+def sp_group_norm_fwd(x, gamma, beta=None, *, groups, eps, norm="layernorm", act="none", y,
+                      mean=None, rstd):
+    """Group norm with an activation ("none" or "silu") of (n, l, c) rank buffers,
+    channels last; the statistics of each of the `groups` groups of a rank span the l
+    rows of a sample (l = 1: per token).  gamma, beta: (t * c).  mean (LayerNorm) and
+    rstd: float32 (n, groups) per rank, written for the backward."""
+    lib = load()
+    t, x0, dt = _first(x, 3, "x")
+    n, l, c = x0.shape
+    dev, dtype = x0.device, x0.dtype
+    ln = norm == "layernorm"
+    xa, x_ld = _rank_rows(x, x0.shape, dtype, dev, t, "x")
+    ya, y_ld = _rank_rows(y, x0.shape, dtype, dev, t, "y")
+    _need(gamma, (t * c,), dtype, dev, "gamma")
+    if ln:
+        _need(beta, (t * c,), dtype, dev, "beta")
+        if mean is None:
+            raise ValueError("mean is required for layernorm")
+    ma = _rank_dense(mean, (n, groups), torch.float32, dev, t, "mean") if ln else None
+    ra = _rank_dense(rstd, (n, groups), torch.float32, dev, t, "rstd")
+    _call(dev, lib.sp_group_norm_fwd, xa, x_ld, gamma.data_ptr(), beta.data_ptr() if ln else None,
+          n, l, c, groups, t, dt, float(eps), _choice(NORMS, norm, "norm"),
+          _choice(ACTS, act, "act"), ya, y_ld, ma, ra)
+
+
+def sp_group_norm_bwd_workspace_bytes(n, l, c, groups, t, dtype=torch.bfloat16):
+    """Bytes of sp_group_norm_bwd's workspace on the current device."""
+    return int(load().sp_group_norm_bwd_workspace_bytes(n, l, c, groups, t, DTYPES[dtype]))
+
+
+def sp_group_norm_bwd(dy, x, mean, rstd, gamma, beta=None, *, groups, norm="layernorm",
+                      act="none", dx, dgamma=None, dbeta=None, workspace=None):
+    """Gradients of sp_group_norm_fwd from its input and saved statistics: dx, and
+    where given the float32 (t * c) dgamma and dbeta (these need the workspace of
+    sp_group_norm_bwd_workspace_bytes, one per call that may run at the same time)."""
+    lib = load()
+    t, x0, dt = _first(x, 3, "x")
+    n, l, c = x0.shape
+    dev, dtype = x0.device, x0.dtype
+    ln = norm == "layernorm"
+    da, d_ld = _rank_rows(dy, x0.shape, dtype, dev, t, "dy")
+    xa, x_ld = _rank_rows(x, x0.shape, dtype, dev, t, "x")
+    oa, o_ld = _rank_rows(dx, x0.shape, dtype, dev, t, "dx")
+    _need(gamma, (t * c,), dtype, dev, "gamma")
+    if ln:
+        _need(beta, (t * c,), dtype, dev, "beta")
+        if mean is None:
+            raise ValueError("mean is required for layernorm")
+    ma = _rank_dense(mean, (n, groups), torch.float32, dev, t, "mean") if ln else None
+    ra = _rank_dense(rstd, (n, groups), torch.float32, dev, t, "rstd")
+    for name, v in (("dgamma", dgamma), ("dbeta", dbeta)):
+        if v is not None:
+            _need(v, (t * c,), torch.float32, dev, name)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(dev, lib.sp_group_norm_bwd, da, d_ld, xa, x_ld, ma, ra, gamma.data_ptr(),
+          beta.data_ptr() if ln else None, n, l, c, groups, t, dt, _choice(NORMS, norm, "norm"),
+          _choice(ACTS, act, "act"), oa, o_ld, dgamma.data_ptr() if dgamma is not None else None,
+          dbeta.data_ptr() if dbeta is not None and ln else None,
+          workspace.data_ptr() if workspace is not None else None, size)
 
 
 def sp_debug_inject(code):

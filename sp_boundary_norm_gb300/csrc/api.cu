@@ -7,8 +7,8 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <vector>
 
+#include "host_common.h"
 #include "sp_internal.h"
 
 namespace spb {
@@ -22,6 +22,8 @@ std::atomic<int> g_inject{SP_OK};
 std::atomic<int> g_tune[2][4] = {{{0}, {0}, {0}, {0}}, {{0}, {0}, {0}, {0}}};
 // The launch shape of this thread's last forward (0) and backward (1) call.
 thread_local LaunchShape g_last_shape[2] = {};
+
+}  // namespace
 
 sp_status_t fail(sp_status_t code, const char* fmt, ...) {
   va_list ap;
@@ -45,6 +47,8 @@ bool take_injected(sp_status_t* out) {
   return true;
 }
 
+namespace {
+
 // An injected SP_ERR_TIMEOUT is not returned by the host: the next forward
 // launches with its device-side withhold hook set instead (block 0's copy
 // producer never stages its first chunk, so that block's waits run out and
@@ -53,36 +57,6 @@ bool take_injected_timeout() {
   int expect = SP_ERR_TIMEOUT;
   return g_inject.compare_exchange_strong(expect, SP_OK);
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// A list of device byte ranges; outputs must not overlap anything else.
-struct Ranges {
-  struct R {
-    uintptr_t lo, hi;
-    bool out;
-    const char* what;
-    int idx;
-  };
-  std::vector<R> v;
-  void add(const void* p, size_t bytes, bool out, const char* what, int idx) {
-    if (p == nullptr || bytes == 0) return;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    v.push_back({lo, lo + bytes, out, what, idx});
-  }
-  sp_status_t check() const {
-    for (size_t i = 0; i < v.size(); ++i) {
-      if (!v[i].out) continue;
-      for (size_t j = 0; j < v.size(); ++j) {
-        if (i == j) continue;
-        if (v[i].lo < v[j].hi && v[j].lo < v[i].hi)
-          return fail(SP_ERR_OVERLAP, "output %s[%d] overlaps %s[%d]", v[i].what, v[i].idx,
-                      v[j].what, v[j].idx);
-      }
-    }
-    return SP_OK;
-  }
-};
 
 // Shapes common to every entry point.
 sp_status_t check_shape(int64_t b, int64_t s, int64_t h, int32_t t, const int32_t* cu_seqlens,
@@ -174,6 +148,8 @@ struct AttrCache {
 };
 AttrCache g_attr;
 
+}  // namespace
+
 cudaError_t ensure_smem_attr(const void* fn, size_t smem) {
   const int dev = current_device();
   std::lock_guard<std::mutex> lock(g_attr.mu);
@@ -193,6 +169,8 @@ cudaError_t ensure_smem_attr(const void* fn, size_t smem) {
   g_attr.smem[i] = smem;
   return cudaSuccess;
 }
+
+namespace {
 
 // Launch shapes are pure functions of (kernel kind, rows, h, t, flags, device,
 // tuning overrides); caching them keeps the per-call host cost to the

@@ -1,0 +1,133 @@
+// Device helpers of the operators between g and the next g* (rotary
+// positions, gated recurrence, group norm): element types and packed loads.
+//
+// These tensors hold the whole sequence and one rank's channels.  DT is an
+// sp_dtype_t: bf16, fp16 or float32 elements; all arithmetic is float32, each
+// stored value rounded once.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "host_common.h"
+#include "region.h"
+#include "sp_device.cuh"
+
+namespace spb {
+
+template <int DT>
+struct ElemSize {
+  static constexpr int value = DT == SP_F32 ? 4 : 2;
+};
+
+// N consecutive elements as 32-bit words (N * size >= 4) or one 16-bit value.
+template <int DT, int N>
+struct Pack {
+  static constexpr int kBytes = N * ElemSize<DT>::value;
+  static constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
+  uint32_t w[kWords];
+};
+
+// Read-once / write-once accesses of a pack in pieces of at most 16 bytes
+// (plain coherent loads: an output may be the input itself where an entry
+// point allows it).
+template <int DT, int N>
+__device__ __forceinline__ void load_pack(Pack<DT, N>& p, const char* src) {
+  constexpr int B = Pack<DT, N>::kBytes;
+  if constexpr (B >= 16) {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+      p.w[4 * i] = v.x;
+      p.w[4 * i + 1] = v.y;
+      p.w[4 * i + 2] = v.z;
+      p.w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (B == 8) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src));
+    p.w[0] = v.x;
+    p.w[1] = v.y;
+  } else if constexpr (B == 4) {
+    p.w[0] = __ldcs(reinterpret_cast<const unsigned int*>(src));
+  } else {
+    p.w[0] = __ldcs(reinterpret_cast<const unsigned short*>(src));
+  }
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void store_pack(char* dst, const Pack<DT, N>& p) {
+  constexpr int B = Pack<DT, N>::kBytes;
+  if constexpr (B >= 16) {
+#pragma unroll
+    for (int i = 0; i < B / 16; ++i)
+      __stcs(reinterpret_cast<uint4*>(dst) + i,
+             make_uint4(p.w[4 * i], p.w[4 * i + 1], p.w[4 * i + 2], p.w[4 * i + 3]));
+  } else if constexpr (B == 8) {
+    __stcs(reinterpret_cast<uint2*>(dst), make_uint2(p.w[0], p.w[1]));
+  } else if constexpr (B == 4) {
+    __stcs(reinterpret_cast<unsigned int*>(dst), p.w[0]);
+  } else {
+    __stcs(reinterpret_cast<unsigned short*>(dst), static_cast<unsigned short>(p.w[0]));
+  }
+}
+
+__device__ __forceinline__ float half_bits(uint32_t v) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void unpack(const Pack<DT, N>& p, float (&f)[N]) {
+  if constexpr (DT == SP_F32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __uint_as_float(p.w[i]);
+  } else if constexpr (DT == SP_BF16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      f[i] = __uint_as_float((i & 1) ? (p.w[i / 2] & 0xFFFF0000u) : (p.w[i / 2] << 16));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = half_bits((i & 1) ? (p.w[i / 2] >> 16) : p.w[i / 2]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pair_bits(float lo, float hi) {
+  uint32_t r;
+  if constexpr (DT == SP_BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void pack(Pack<DT, N>& p, const float (&f)[N]) {
+  if constexpr (DT == SP_F32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.w[i] = __float_as_uint(f[i]);
+  } else if constexpr (N == 1) {
+    p.w[0] = pair_bits<DT>(f[0], 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) p.w[i] = pair_bits<DT>(f[2 * i], f[2 * i + 1]);
+  }
+}
+
+// The packed sequence of token `tok`: the largest j < n with cu[j] <= tok (the
+// last of several sequences that begin there: the others are empty).  One
+// warp, 32 probes a step; in bounds whatever cu holds.
+__device__ __forceinline__ int seq_of_token(const int32_t* cu, int n, int64_t tok) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int at = lo + lane * step;
+    const bool le = at < lo + len && static_cast<int64_t>(__ldg(cu + at)) <= tok;
+    const int cnt = __popc(__ballot_sync(0xFFFFFFFFu, le));
+    const int skip = cnt > 0 ? (cnt - 1) * step : 0;
+    lo += skip;
+    len = len - skip < step ? len - skip : step;
+  }
+  return lo;
+}
+
+}  // namespace spb

@@ -1,0 +1,183 @@
+// Rotary positions: every rotated pair (u, v) of a head becomes
+//   (m (u cos x - v sin x), m (v cos x + u sin x)),   x = position * frequency,
+// and the backward is the same with -sin (the transpose of a rotation, times m).
+//
+// The angle is reduced exactly: a frequency is held as a 64-bit fraction of a
+// turn, position * fraction mod 2^64 is the exact part of a turn however far
+// the position (one wide integer multiply), its top 32 bits become a float in
+// [-1, 1) half-turns for sincospif.
+//
+// One warp takes one token and a piece of its heads over all ranks: the lanes
+// compute the token's sines and cosines once into shared memory, each lane
+// keeps those of its own vector of pairs in registers and walks the heads, so
+// a pair costs one rotation and its share of two loads and two stores.
+// Bound by HBM: reads x once, writes y once.
+#include "region.cuh"
+
+namespace spb {
+
+constexpr int kRopeWarps = 8;
+constexpr int kRopeUnroll = 4;
+
+// V elements a load.  Half layout: a lane's item is V pairs (V elements of
+// each half).  Interleaved: V / 2 pairs that lie together, or for V = 1 one
+// pair by two loads.
+__device__ __forceinline__ int rank_of_head(const RopeParams& P, int hh) {
+  return P.heads == 1 ? hh : static_cast<int>(__umulhi(static_cast<uint32_t>(hh), P.heads_magic));
+}
+
+template <int DT, int V, int LAYOUT>
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams P) {
+  constexpr int E = ElemSize<DT>::value;
+  constexpr bool kTwo = LAYOUT == SP_ROPE_HALF || V == 1;   // an item is two loads
+  constexpr int kPairs = kTwo ? V : V / 2;
+  __shared__ float2 cs[kRopeWarps][SP_ROPE_MAX_PAIRS];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0 && warp == 0)
+    check_cu_seqlens(P.cu_seqlens, P.n_seqs, P.s, P.status);
+  const int items = P.half / kPairs;                 // of a head
+  const int width = items < 32 ? items : 32;         // lanes of a head
+  const int abreast = 32 / width;                    // heads side by side
+  const int my = lane % width, sub = lane / width;
+  // bytes from an item's first load to its second
+  const int64_t second = LAYOUT == SP_ROPE_HALF ? static_cast<int64_t>(P.half) * E : E;
+  const int64_t n_tasks = P.tokens * P.chunks;
+  for (int64_t task = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; task < n_tasks;
+       task += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
+    const int64_t tok = P.chunks == 1 ? task : task / P.chunks;
+    const int chunk = static_cast<int>(task - tok * P.chunks);
+    const int h0 = chunk * P.chunk_heads;
+    const int h1 = h0 + P.chunk_heads < P.all_heads ? h0 + P.chunk_heads : P.all_heads;
+    int64_t pos;
+    if (P.positions != nullptr) {
+      pos = __ldg(P.positions + tok);
+    } else if (P.cu_seqlens != nullptr) {
+      pos = tok - __ldg(P.cu_seqlens + seq_of_token(P.cu_seqlens, P.n_seqs, tok)) + P.first;
+    } else {
+      pos = (P.tokens == P.s ? tok : tok % P.s) + P.first;
+    }
+    __syncwarp();
+    for (int i = lane; i < P.half; i += 32) {
+      const uint64_t turn = static_cast<uint64_t>(pos) * P.turns[i];
+      const float half_turns =
+          static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+      float sn, cn;
+      sincospif(half_turns, &sn, &cn);
+      cs[warp][i] = make_float2(cn * P.cos_scale, sn * P.sin_scale);
+    }
+    __syncwarp();
+    for (int v0 = 0; v0 < items; v0 += width) {
+      const int item = v0 + my;
+      const bool on = sub < abreast && item < items;
+      float cn[kPairs], sn[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 v = on ? cs[warp][item * kPairs + i] : make_float2(0.f, 0.f);
+        cn[i] = v.x;
+        sn[i] = v.y;
+      }
+      const int64_t at = static_cast<int64_t>(item) * (V == 1 && LAYOUT != SP_ROPE_HALF ? 2 : V) * E;
+      for (int hb = h0; hb < h1; hb += abreast * kRopeUnroll) {
+        Pack<DT, V> a[kRopeUnroll], b[kRopeUnroll];
+#pragma unroll
+        for (int k = 0; k < kRopeUnroll; ++k) {
+          const int hh = hb + k * abreast + sub;
+          if (on && hh < h1) {
+            const int r = rank_of_head(P, hh);
+            const char* src = P.x[r] + tok * P.x_row + (hh - r * P.heads) * P.x_head + at;
+            load_pack(a[k], src);
+            if constexpr (kTwo) load_pack(b[k], src + second);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kRopeUnroll; ++k) {
+          const int hh = hb + k * abreast + sub;
+          if (on && hh < h1) {
+            const int r = rank_of_head(P, hh);
+            char* dst = P.y[r] + tok * P.y_row + (hh - r * P.heads) * P.y_head + at;
+            float x[V];
+            unpack(a[k], x);
+            if constexpr (kTwo) {
+              float z[V];
+              unpack(b[k], z);
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                const float u = x[i], w = z[i];
+                x[i] = u * cn[i] - w * sn[i];
+                z[i] = w * cn[i] + u * sn[i];
+              }
+              pack(a[k], x);
+              pack(b[k], z);
+              store_pack(dst, a[k]);
+              store_pack(dst + second, b[k]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kPairs; ++i) {
+                const float u = x[2 * i], w = x[2 * i + 1];
+                x[2 * i] = u * cn[i] - w * sn[i];
+                x[2 * i + 1] = w * cn[i] + u * sn[i];
+              }
+              pack(a[k], x);
+              store_pack(dst, a[k]);
+            }
+          }
+        }
+      }
+    }
+    // the part of the heads that is not rotated
+    const int tail = P.rest / V;
+    for (int i = lane; i < tail * (h1 - h0); i += 32) {
+      const int hh = h0 + i / tail;
+      const int r = rank_of_head(P, hh);
+      const int64_t at = static_cast<int64_t>(P.rest_at + (i % tail) * V) * E;
+      Pack<DT, V> a;
+      load_pack(a, P.x[r] + tok * P.x_row + (hh - r * P.heads) * P.x_head + at);
+      store_pack(P.y[r] + tok * P.y_row + (hh - r * P.heads) * P.y_head + at, a);
+    }
+  }
+}
+
+template <int DT, int V>
+static const void* rope_fn(int layout) {
+  return layout == SP_ROPE_HALF ? reinterpret_cast<const void*>(&rope_kernel<DT, V, SP_ROPE_HALF>)
+                                : reinterpret_cast<const void*>(
+                                      &rope_kernel<DT, V, SP_ROPE_INTERLEAVED>);
+}
+
+template <int DT>
+static const void* rope_fn(int layout, int vec) {
+  switch (vec) {
+    case 1: return rope_fn<DT, 1>(layout);
+    case 2: return rope_fn<DT, 2>(layout);
+    case 4: return rope_fn<DT, 4>(layout);
+    default:
+      if constexpr (DT == SP_F32) return nullptr;
+      else return rope_fn<DT, 8>(layout);
+  }
+}
+
+cudaError_t launch_rope(RopeParams p, int dtype, int vec, cudaStream_t st) {
+  // One warp a token, or few tokens' heads cut into pieces of whole lane rounds
+  // until every SM has its warps.
+  const int pairs = vec == 1 || p.layout == SP_ROPE_HALF ? vec : vec / 2;
+  const int items = p.half / pairs;
+  const int abreast = 32 / (items < 32 ? items : 32);
+  const int rounds = (p.all_heads + abreast - 1) / abreast;
+  const int64_t want = static_cast<int64_t>(device_sm_count()) * 8 * kRopeWarps;
+  int64_t chunks = p.tokens < want ? (want + p.tokens - 1) / p.tokens : 1;
+  if (chunks > rounds) chunks = rounds;
+  p.chunk_heads = static_cast<int>((rounds + chunks - 1) / chunks) * abreast;
+  p.chunks = (p.all_heads + p.chunk_heads - 1) / p.chunk_heads;
+  const void* fn = dtype == SP_BF16  ? rope_fn<SP_BF16>(p.layout, vec)
+                   : dtype == SP_F16 ? rope_fn<SP_F16>(p.layout, vec)
+                                     : rope_fn<SP_F32>(p.layout, vec);
+  if (fn == nullptr) return cudaErrorInvalidValue;
+  const int64_t blocks = (p.tokens * p.chunks + kRopeWarps - 1) / kRopeWarps;
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 8;
+  void* args[] = {&p};
+  return launch_pdl(fn, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)),
+                    dim3(32 * kRopeWarps), 0, args, st);
+}
+
+}  // namespace spb
