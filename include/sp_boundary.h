@@ -487,7 +487,7 @@ sp_status_t sp_gated_scan_fwd(const void* const* gate, int64_t gate_ld, const vo
  * dy     [t] (b, s, c)        gradient of y
  * dhT    [t] (n, c) float32   gradient of hT, or a NULL array (zero)
  * dgate, dvalue [t] (b, s, c) outputs
- * dh0    [t] (n, c) float32   output or a NULL array; dh0[r] == dhT[r] is allowed
+ * dh0    [t] (n, c) float32   output or a NULL array
  */
 sp_status_t sp_gated_scan_bwd(const void* const* gate, int64_t gate_ld, const void* const* value,
                               int64_t value_ld, const float* const* h0,

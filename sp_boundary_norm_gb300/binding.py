@@ -768,7 +768,7 @@ def sp_gated_scan_fwd(gate, value, *, h0=None, tied=True, cu_seqlens=None, y, hT
 def sp_gated_scan_bwd(gate, value, states, dy, *, h0=None, dhT=None, tied=True, cu_seqlens=None,
                       dgate, dvalue, dh0=None, status=None):
     """Gradients of sp_gated_scan_fwd (same gate, value, h0, tied, cu_seqlens) from
-    the states it saved; dhT: gradient of hT, dh0 (may be dhT): gradient of h0."""
+    the states it saved; dhT: gradient of hT, dh0: gradient of h0."""
     lib = load()
     t, x0, dt = _first(gate, 3, "gate")
     b, s, c = x0.shape

@@ -170,6 +170,52 @@ cudaError_t ensure_smem_attr(const void* fn, size_t smem) {
   return cudaSuccess;
 }
 
+cudaError_t max_clusters(const void* fn, int threads, size_t smem, int cluster, int* fit) {
+  struct Entry {
+    const void* fn;
+    size_t smem;
+    int threads, cluster, device, fit;
+  };
+  constexpr int kSlots = 1024;
+  static std::mutex mu;
+  static Entry known[kSlots];
+  static int used = 0;
+  cudaError_t e = ensure_smem_attr(fn, smem);
+  if (e != cudaSuccess) return e;
+  const int dev = current_device();
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < used; ++i) {
+    const Entry& k = known[i];
+    if (k.fn == fn && k.smem == smem && k.threads == threads && k.cluster == cluster &&
+        k.device == dev) {
+      *fit = k.fit;
+      return cudaSuccess;
+    }
+  }
+  *fit = 0;
+  if (cluster > 8) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(fit, fn, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    *fit = 0;                    // this size does not run here
+  }
+  if (used < kSlots) known[used++] = Entry{fn, smem, threads, cluster, dev, *fit};
+  return cudaSuccess;
+}
+
 namespace {
 
 // Launch shapes are pure functions of (kernel kind, rows, h, t, flags, device,

@@ -69,4 +69,8 @@ struct Ranges {
 // Raises a kernel's dynamic shared-memory limit on the current device to `smem`.
 cudaError_t ensure_smem_attr(const void* fn, size_t smem);
 
+// Prepares kernel `fn` for clusters of `cluster` blocks of that size on the
+// current device; *fit: how many the GPU holds at once.  Remembered.
+cudaError_t max_clusters(const void* fn, int threads, size_t smem, int cluster, int* fit);
+
 }  // namespace spb

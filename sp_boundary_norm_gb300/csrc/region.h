@@ -36,7 +36,7 @@ cudaError_t launch_rope(RopeParams p, int dtype, int vec, cudaStream_t st);
 // ---------------------------------------------------------- gated recurrence --
 constexpr int kScanRun = 16;        // tokens of one thread, and of one saved state
 constexpr int kScanChannels = 64;   // channels of a block: two a lane
-constexpr int kScanMaxWarps = 16;
+constexpr int kScanWarps = 4;       // of a block, at most
 constexpr int kScanMaxCluster = 16;
 
 struct ScanParams {
@@ -49,7 +49,7 @@ struct ScanParams {
   const float* dhT[SP_MAX_RANKS];     // NULL: zero
   float* hT[SP_MAX_RANKS];            // forward: hT; backward: dh0; NULL: not wanted
   float* states[SP_MAX_RANKS];        // NULL (forward): not wanted
-  int64_t ld_gate, ld_value, ld_dy, ld_out, ld_dvalue;   // bytes between tokens
+  uint32_t ld_gate, ld_value, ld_dy, ld_out, ld_dvalue;   // bytes between tokens
   int64_t s;
   int32_t b, c, t, slabs;
   int32_t tied, cluster;
@@ -60,9 +60,6 @@ struct ScanParams {
 
 cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st);
 cudaError_t launch_scan_bwd(ScanParams p, int dtype, cudaStream_t st);
-// warps per block and blocks per cluster of a call
-void scan_shape(const ScanParams& p, int* warps, int* cluster);
-
 // -------------------------------------------------------------- group norm --
 constexpr int kGroupThreads = 512;      // most threads of a block: cols <= this
 constexpr int kGroupMaxCluster = 16;

@@ -48,6 +48,8 @@ sp_status_t check_ranks(T* const* arr, int t, const char* what) {
   return SP_OK;
 }
 
+constexpr int64_t kMostLd = int64_t(1) << 28;   // a row stride in bytes fits 32 bits
+
 // A row stride: a multiple of 8 elements, at least the row, no overflow.
 sp_status_t check_ld(int64_t ld, int64_t width, int64_t rows, const char* what) {
   if (ld < width || ld % 8 != 0)
@@ -55,6 +57,9 @@ sp_status_t check_ld(int64_t ld, int64_t width, int64_t rows, const char* what) 
                 (long long)ld, (long long)width);
   if (rows > 0 && ld > kMostElements / rows)
     return fail(SP_ERR_INVALID_ARG, "%s: the tensor's extent overflows", what);
+  if (ld > kMostLd)
+    return fail(SP_ERR_UNSUPPORTED, "%s = %lld above %lld", what, (long long)ld,
+                (long long)kMostLd);
   return SP_OK;
 }
 
@@ -199,8 +204,8 @@ void fill_scan(ScanParams* P, const ScanCall& k, const void* const* gate, int64_
     P->value[r] = static_cast<const char*>(value[r]);
     P->h0[r] = h0 != nullptr ? h0[r] : nullptr;
   }
-  P->ld_gate = gate_ld * size;
-  P->ld_value = value_ld * size;
+  P->ld_gate = static_cast<uint32_t>(gate_ld * size);
+  P->ld_value = static_cast<uint32_t>(value_ld * size);
   P->s = k.s;
   P->b = static_cast<int32_t>(k.b);
   P->c = static_cast<int32_t>(k.c);
@@ -389,7 +394,7 @@ sp_status_t sp_gated_scan_fwd(const void* const* gate, int64_t gate_ld, const vo
     P.hT[r] = hT != nullptr ? hT[r] : nullptr;
     P.states[r] = states != nullptr ? states[r] : nullptr;
   }
-  P.ld_out = y_ld * size;
+  P.ld_out = static_cast<uint32_t>(y_ld * size);
   const cudaError_t e = launch_scan_fwd(P, dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SP_OK : fail_cuda(e, "sp_gated_scan_fwd launch");
 }
@@ -437,8 +442,7 @@ sp_status_t sp_gated_scan_bwd(const void* const* gate, int64_t gate_ld, const vo
       rg.add_rows(dvalue[r], rows, dvalue_ld * size, c * size, true, "dvalue", r);
     }
     if (h0 != nullptr) rg.add(h0[r], state_bytes, false, "h0", r);
-    if (dhT != nullptr && !(dh0 != nullptr && dh0[r] == dhT[r]))
-      rg.add(dhT[r], state_bytes, false, "dhT", r);
+    if (dhT != nullptr) rg.add(dhT[r], state_bytes, false, "dhT", r);
     if (dh0 != nullptr) rg.add(dh0[r], state_bytes, true, "dh0", r);
   }
   if (cu_seqlens != nullptr) rg.add(cu_seqlens, (n_seqs + size_t(1)) * 4, false, "cu_seqlens", 0);
@@ -455,9 +459,9 @@ sp_status_t sp_gated_scan_bwd(const void* const* gate, int64_t gate_ld, const vo
     P.hT[r] = dh0 != nullptr ? dh0[r] : nullptr;
     P.states[r] = const_cast<float*>(states[r]);
   }
-  P.ld_dy = dy_ld * size;
-  P.ld_out = dgate_ld * size;
-  P.ld_dvalue = dvalue_ld * size;
+  P.ld_dy = static_cast<uint32_t>(dy_ld * size);
+  P.ld_out = static_cast<uint32_t>(dgate_ld * size);
+  P.ld_dvalue = static_cast<uint32_t>(dvalue_ld * size);
   const cudaError_t e = launch_scan_bwd(P, dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SP_OK : fail_cuda(e, "sp_gated_scan_bwd launch");
 }

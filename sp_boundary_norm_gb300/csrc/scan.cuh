@@ -3,14 +3,20 @@
 //   h[i] = a[i] h[i-1] + k[i] v[i]   (tied)   or   a[i] h[i-1] + v[i]   (free)
 // along the tokens of a sequence, each channel on its own.
 //
-// A block takes 64 channels, two a lane, and 16 tokens a warp (a "run"): lane
-// and warp read whole 128-byte row pieces, a thread scans its run in registers
-// and knows it as an affine map h -> A h + H.  The maps are joined over the
-// block's warps in shared memory and over the blocks of a cluster by
-// distributed shared memory, always in token order, so results do not depend
-// on timing; then the cluster steps to the next stretch of the sequence with
-// the state in registers.  Nothing is read twice and no block waits for
-// another but its cluster's.
+// A block takes 64 channels, two a lane, and 16 tokens a warp (a "run"): a
+// thread scans its run in registers and knows it as an affine map h -> A h + H.
+// The maps are joined over the block's warps in shared memory and over the
+// blocks of a cluster by asynchronous stores into every block's shared memory,
+// always in token order, so results do not depend on timing; then the cluster
+// steps to the next stretch of the sequence with the state in registers.  The
+// next stretch's rows are on their way (16-byte cp.async, four rows an
+// instruction) from the moment the present ones are in registers.  Nothing is
+// read twice and no block waits for another but its cluster's.
+//
+// Two exponentials' worth of special functions, a scan and a correction an
+// element sit between 6 and 10 bytes of traffic, so instructions count as much
+// as bytes: the two channels of a lane go through packed float32 arithmetic,
+// and whole runs inside one sequence take code without its checks.
 #pragma once
 
 #include "region.cuh"
@@ -21,43 +27,119 @@ namespace spb {
 template <int DT>
 using Two = Pack<DT, 2>;
 
-// sigmoid(g) and sigmoid(-g), each with a small relative error: with
-// e = exp(g), k = 1 / (1 + e) and a = e k.  The exponent is capped where k is
-// the smallest normal float (exp would overflow); NaN stays NaN.
+// Packed pairs of floats (two channels): one instruction for both.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 template <int DT>
-__device__ __forceinline__ void gate_of(float g, float& a, float& k) {
-  float e;
+__device__ __forceinline__ F2 unpack2(const Two<DT>& p) {
+  float f[2];
+  unpack(p, f);
+  return f2(f[0], f[1]);
+}
+template <int DT>
+__device__ __forceinline__ Two<DT> pack2(F2 v) {
+  const float2 f = split(v);
+  const float w[2] = {f.x, f.y};
+  Two<DT> p;
+  pack(p, w);
+  return p;
+}
+
+// -k = -sigmoid(-g) = -1 / (1 + e), e = exp(g): small k keep their digits, and
+// h + k (v - h) and h - k h need no more.  An exponential that overflows gives
+// k = 0; CAP holds it below that, for a = e k.  NaN stays NaN.
+template <int DT, bool CAP>
+__device__ __forceinline__ F2 neg_k(F2 g, F2& e) {
+  float2 x;
   if constexpr (DT == SP_F32) {
-    asm("min.NaN.f32 %0, %1, 0f42AE0000;" : "=f"(g) : "f"(g));   // 87
-    e = expf(g);
-    k = __frcp_rn(1.f + e);
+    x = split(g);
+    if constexpr (CAP) {
+      asm("min.NaN.f32 %0, %0, 0f42AE0000;" : "+f"(x.x));   // 87
+      asm("min.NaN.f32 %0, %0, 0f42AE0000;" : "+f"(x.y));
+    }
+    x = make_float2(expf(x.x), expf(x.y));
+    e = f2(x.x, x.y);
+    return f2(-__frcp_rn(1.f + x.x), -__frcp_rn(1.f + x.y));
   } else {
     // 16-bit gates: the fast exponential's error (a few 1e-7) is far below
     // the rounding of the outputs
-    asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(g) : "f"(g * 1.4426950408889634f));   // 126
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(k) : "f"(1.f + e));
+    x = split(mul2(g, f2(1.4426950408889634f, 1.4426950408889634f)));
+    if constexpr (CAP) {
+      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.x));   // 126
+      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.y));
+    }
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+    e = f2(x.x, x.y);
+    x = split(fma2(e, f2(-1.f, -1.f), f2(-1.f, -1.f)));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+    return f2(x.x, x.y);
   }
-  a = e * k;
 }
 
-// The affine maps of a thread's two channels over some tokens.
+// The state after a token: h + k (v - h), or h - k h + v.  d: h - v (tied).
+template <bool TIED>
+__device__ __forceinline__ F2 next_state(F2 nk, F2 h, F2 v, F2& d) {
+  if constexpr (TIED) {
+    d = fma2(v, f2(-1.f, -1.f), h);
+    return fma2(nk, d, h);
+  } else {
+    d = h;
+    return add2(fma2(nk, h, h), v);
+  }
+}
+
+// The affine maps of a thread's two channels over some tokens: x -> a x + h.
 struct alignas(16) Map2 {
-  float a0, a1, h0, h1;
+  F2 a, h;
 };
 
-// later(earlier(h)) of one channel.  A sequence that begins inside the later
-// part cuts the earlier one off: its factor is exactly zero, and what the
-// earlier part holds (an infinity, a NaN) must not pass.
-template <bool PACKED>
-__device__ __forceinline__ float through(float a, float h, float x) {
-  return PACKED && a == 0.f ? h : fmaf(a, x, h);
+// The map's value at x.  CUT: a sequence that begins inside the map's tokens
+// cuts off what comes before them: the factor is exactly zero, and what x holds
+// (an infinity, a NaN) must not pass.
+template <bool CUT>
+__device__ __forceinline__ F2 through(F2 a, F2 h, F2 x) {
+  const F2 y = fma2(a, x, h);
+  if constexpr (!CUT) return y;
+  const float2 f = split(a), g = split(h), w = split(y);
+  return f2(f.x == 0.f ? g.x : w.x, f.y == 0.f ? g.y : w.y);
 }
 
-__device__ __forceinline__ void st_cluster_map(uint32_t cluster_addr, const Map2& m) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(m.a0),
-               "f"(m.a1), "f"(m.h0), "f"(m.h1)
-               : "memory");
+// Map m into the cluster address `to`, counted in bytes on the mbarrier `bar`
+// (also a cluster address) of the same block.
+__device__ __forceinline__ void st_async_map(uint32_t to, const Map2& m, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+          to),
+      "l"(m.a), "l"(m.h), "r"(bar)
+      : "memory");
 }
 
 // Which of the run's tokens tok0 .. tok0 + 15 begin a sequence, and which end one.
@@ -65,19 +147,54 @@ struct RunMarks {
   uint32_t starts, ends;
 };
 
+// What a warp knows of a packed batch: 32 consecutive entries of cu_seqlens, one
+// a lane, and of the sequence that its last marked run began in the tokens
+// [lo, hi).  Runs inside it take two comparisons, others within the entries a
+// few votes; only the rest go back to memory.
+struct SeqWindow {
+  int base, at;        // first entry; this lane's (INT_MAX behind the last)
+  int seq, lo, hi;
+};
+
+__device__ __forceinline__ SeqWindow no_window() { return SeqWindow{0, 0x7FFFFFFF, 0, 0, 0}; }
+
+// `first`: 16 words of the warp's shared memory, set for every start bit to the
+// sequence that begins there (the last of several: the others are empty).
+// `back`: entries to keep before the run's (a walk towards the beginning).
 template <bool PACKED>
-__device__ __forceinline__ RunMarks run_marks(const ScanParams& P, int64_t tok0) {
+__device__ __forceinline__ RunMarks run_marks(const ScanParams& P, int64_t tok0, SeqWindow& win,
+                                              int* first, int back) {
   if (tok0 >= P.s) return RunMarks{0u, 0u};
   // bit i: token tok0 + i is the first of a sequence, or the first after the call's last
   uint32_t m = tok0 == 0 ? 1u : 0u;
   if constexpr (PACKED) {
-    const int64_t end = tok0 + kScanRun < P.s - 1 ? tok0 + kScanRun : P.s - 1;
-    const int lane = threadIdx.x & 31;
-    for (int j = seq_of_token(P.cu_seqlens, P.n_seqs, tok0); j < P.n_seqs; j += 32) {
-      const int64_t at = j + lane < P.n_seqs ? __ldg(P.cu_seqlens + j + lane) : end + 1;
-      const bool in = at >= tok0 && at <= end;
-      m |= __reduce_or_sync(0xFFFFFFFFu, in ? 1u << static_cast<int>(at - tok0) : 0u);
-      if (__any_sync(0xFFFFFFFFu, at > end)) break;
+    const int tok = static_cast<int>(tok0), n = P.n_seqs;
+    if (tok <= win.lo || static_cast<int64_t>(tok) + kScanRun >= win.hi) {
+      const int lane = threadIdx.x & 31;
+      const int end = P.s - tok0 > kScanRun ? tok + kScanRun : static_cast<int>(P.s - 1);
+      const int w0 = __shfl_sync(0xFFFFFFFFu, win.at, 0), w31 = __shfl_sync(0xFFFFFFFFu, win.at, 31);
+      if (w0 > tok || w31 <= end) {
+        const int j = seq_of_token(P.cu_seqlens, n, tok0);
+        win.base = j > back ? j - back : 0;
+        win.at = win.base + lane <= n ? __ldg(P.cu_seqlens + win.base + lane) : 0x7FFFFFFF;
+      }
+      const uint32_t le = __ballot_sync(0xFFFFFFFFu, win.at <= tok && win.base + lane < n);
+      const int k = le != 0u ? 31 - __clz(le) : 0;
+      win.seq = win.base + k;
+      win.lo = __shfl_sync(0xFFFFFFFFu, win.at, k);
+      win.hi = __shfl_sync(0xFFFFFFFFu, win.at, k < 31 ? k + 1 : 31);
+      __syncwarp();                   // every lane is done with the run before
+      if (lane < kScanRun) first[lane] = win.seq;
+      __syncwarp();
+      for (int j = win.base; j < n; j += 32) {     // one round unless 32 sequences begin here
+        const int at = j == win.base ? win.at
+                       : j + lane < n ? __ldg(P.cu_seqlens + j + lane) : 0x7FFFFFFF;
+        const bool in = at >= tok && at <= end && j + lane < n;
+        m |= __reduce_or_sync(0xFFFFFFFFu, in ? 1u << (at - tok) : 0u);
+        if (in && at - tok < kScanRun) atomicMax(first + (at - tok), j + lane);
+        if (__any_sync(0xFFFFFFFFu, at > end)) break;
+      }
+      __syncwarp();
     }
   }
   const int left = P.s - tok0 <= kScanRun ? static_cast<int>(P.s - tok0) : kScanRun + 1;
@@ -86,45 +203,26 @@ __device__ __forceinline__ RunMarks run_marks(const ScanParams& P, int64_t tok0)
   return RunMarks{starts, (m >> 1) & 0xFFFFu};
 }
 
+// The sequence of the run's token i.
 template <bool PACKED>
-__device__ __forceinline__ int seq_at(const ScanParams& P, int bi, int64_t tok) {
-  if constexpr (PACKED) return seq_of_token(P.cu_seqlens, P.n_seqs, tok);
-  return bi;
+__device__ __forceinline__ int seq_of_run(const SeqWindow& win, const int* first, uint32_t starts,
+                                          int bi, int i) {
+  if constexpr (!PACKED) return bi;
+  const uint32_t m = starts & ((2u << i) - 1u);
+  return m != 0u ? first[31 - __clz(m)] : win.seq;
 }
 
-// The two channels' values of each marked token's sequence, from `src`
-// (float32 [sequences][c], NULL = zeros) into the thread's slots.
-template <bool PACKED>
-__device__ __forceinline__ void fetch_states(const ScanParams& P, const float* src, uint32_t marks,
-                                             int64_t tok0, int bi, int ch, bool on,
-                                             float2 (*slot)[32]) {
-  const int lane = threadIdx.x & 31;
-  while (marks != 0) {
-    const int i = __ffs(marks) - 1;
-    marks &= marks - 1;
-    float2 v = make_float2(0.f, 0.f);
-    if (src != nullptr) {
-      const int seq = seq_at<PACKED>(P, bi, tok0 + i);
-      if (on)
-        v = *reinterpret_cast<const float2*>(src + static_cast<int64_t>(seq) * P.c + ch);
-    }
-    slot[i][lane] = v;
-  }
+// A thread's two channels (from `ch`) of a sequence's state; NULL = zeros.
+__device__ __forceinline__ F2 load_state(const ScanParams& P, const float* src, int seq, int ch,
+                                         bool on) {
+  if (src == nullptr || !on) return f2(0.f, 0.f);
+  const float2 v = *reinterpret_cast<const float2*>(src + static_cast<int64_t>(seq) * P.c + ch);
+  return f2(v.x, v.y);
 }
-
-// The reverse: the slots of the marked tokens to their sequences in `dst`.
-template <bool PACKED>
-__device__ __forceinline__ void put_states(const ScanParams& P, float* dst, uint32_t marks,
-                                           int64_t tok0, int bi, int ch, bool on,
-                                           float2 (*slot)[32]) {
-  const int lane = threadIdx.x & 31;
-  while (marks != 0) {
-    const int i = __ffs(marks) - 1;
-    marks &= marks - 1;
-    const int seq = seq_at<PACKED>(P, bi, tok0 + i);
-    if (on)
-      *reinterpret_cast<float2*>(dst + static_cast<int64_t>(seq) * P.c + ch) = slot[i][lane];
-  }
+__device__ __forceinline__ void store_state(const ScanParams& P, float* dst, int seq, int ch,
+                                            bool on, F2 v) {
+  if (dst != nullptr && on)
+    *reinterpret_cast<float2*>(dst + static_cast<int64_t>(seq) * P.c + ch) = split(v);
 }
 
 // A sequence without tokens passes its state (or its gradient) on.  By one
@@ -140,63 +238,183 @@ __device__ __forceinline__ void pass_empty(const ScanParams& P, const float* src
   }
 }
 
-// Joins the runs' maps in token order (TIME = +1) or against it (-1).  `mine`:
-// this thread's run; returns the value entering it, from the value `carry`
-// that enters the cluster's stretch, and moves `carry` behind the stretch.
-// One block barrier and one cluster barrier; the buffers alternate, so the
-// next call writes the other pair.
-struct ScanShared {
-  Map2 run[2][kScanMaxWarps][32];
-  Map2 block[2][kScanMaxCluster][32];
+// Joins the runs' maps in token order (TIME = +1) or against it (-1): from the
+// value that enters the cluster's stretch (`carry`, which moves behind the
+// stretch) the value that enters this thread's run, whose map is `mine`.
+//
+// The maps of a block meet in `run`; a warp folds those before its own, and the
+// last one's fold, the block's map, goes to every block of the cluster by
+// asynchronous stores that count their bytes on the receiver's mbarrier.
+// Buffers and mbarriers alternate between two; a block's map of step n + 2 is
+// sent after all maps of step n + 1 have arrived, which their blocks sent after
+// they had read step n's, so nothing is overwritten before it is read.  The
+// wait is bounded: `alive` turns false when it ran out, and no later step waits.
+struct JoinBuffers {
+  Map2* run;        // [2][warps][32]
+  Map2* block;      // [2][cluster][32]
+  uint64_t* bar;    // [2]
 };
 
-template <bool PACKED, int TIME>
-__device__ __forceinline__ float2 join_runs(ScanShared& sh, int par, const Map2& mine, int C,
-                                            int rank, float2& carry) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  sh.run[par][warp][lane] = mine;
-  __syncthreads();
-  float2 in = carry;
-  if (C > 1) {
-    if (warp < C) {
-      Map2 b = sh.run[par][TIME > 0 ? 0 : nw - 1][lane];
-      for (int k = 1; k < nw; ++k) {
-        const Map2 m = sh.run[par][TIME > 0 ? k : nw - 1 - k][lane];
-        b.h0 = through<PACKED>(m.a0, m.h0, b.h0);
-        b.h1 = through<PACKED>(m.a1, m.h1, b.h1);
-        b.a0 = through<PACKED>(m.a0, 0.f, b.a0);
-        b.a1 = through<PACKED>(m.a1, 0.f, b.a1);
-      }
-      for (int peer = warp; peer < C; peer += nw)
-        st_cluster_map(cluster_map(&sh.block[par][rank][lane], peer), b);
+constexpr int kFold = 4;    // maps read at once
+constexpr int kStages = 2;  // runs of a warp on their way
+
+// The value x taken through n maps (`at`: this lane's of the first one in
+// time; `step` from one to the next); *in: the value before map `place`.
+template <bool CUT>
+__device__ __forceinline__ F2 fold_value(const Map2* at, int step, int n, int place, F2 x, F2* in) {
+  for (int k0 = 0; k0 < n; k0 += kFold) {
+    Map2 m[kFold];
+#pragma unroll
+    for (int u = 0; u < kFold; ++u)
+      if (k0 + u < n) m[u] = at[(k0 + u) * step];
+#pragma unroll
+    for (int u = 0; u < kFold; ++u) {
+      if (k0 + u == place) *in = x;
+      if (k0 + u < n) x = through<CUT>(m[u].a, m[u].h, x);
     }
-    cluster_sync_all();
-    float2 x = carry;
-    for (int k = 0; k < C; ++k) {
-      const int r = TIME > 0 ? k : C - 1 - k;
-      if (r == rank) in = x;
-      const Map2 m = sh.block[par][r][lane];
-      x.x = through<PACKED>(m.a0, m.h0, x.x);
-      x.y = through<PACKED>(m.a1, m.h1, x.y);
-    }
-    carry = x;
   }
-  float2 x = in, got = in;
-  const int upto = C > 1 ? (TIME > 0 ? warp : nw - 1 - warp) : nw;
-  for (int k = 0; k < upto; ++k) {
-    const int w = TIME > 0 ? k : nw - 1 - k;
-    if (w == warp) got = x;
-    const Map2 m = sh.run[par][w][lane];
-    x.x = through<PACKED>(m.a0, m.h0, x.x);
-    x.y = through<PACKED>(m.a1, m.h1, x.y);
-  }
-  if (C > 1) return x;
-  carry = x;
-  return got;
+  return x;
 }
 
-// Launches a scan kernel: `warps` warps a block, p.cluster blocks a cluster.
-cudaError_t launch_scan(const void* fn, const ScanParams& p, int warps, void** args,
+// Map `acc` followed by map m.
+template <bool CUT>
+__device__ __forceinline__ void fold_map(Map2& acc, const Map2& m) {
+  acc.h = through<CUT>(m.a, m.h, acc.h);
+  acc.a = through<CUT>(m.a, f2(0.f, 0.f), acc.a);
+}
+template <bool CUT>
+__device__ __forceinline__ Map2 fold_maps(const Map2* at, int step, int n) {
+  Map2 acc{f2(1.f, 1.f), f2(0.f, 0.f)};
+  for (int k0 = 0; k0 < n; k0 += kFold) {
+    Map2 m[kFold];
+#pragma unroll
+    for (int u = 0; u < kFold; ++u)
+      if (k0 + u < n) m[u] = at[(k0 + u) * step];
+#pragma unroll
+    for (int u = 0; u < kFold; ++u)
+      if (k0 + u < n) fold_map<CUT>(acc, m[u]);
+  }
+  return acc;
+}
+
+template <bool CUT, int TIME>
+__device__ __forceinline__ F2 join_runs(const JoinBuffers& sh, int step, const Map2& mine, int C,
+                                        int rank, int warp, int nw, F2& carry, bool& alive) {
+  const int lane = threadIdx.x & 31;
+  const int par = step & 1;
+  Map2* run = sh.run + par * nw * 32 + lane;
+  run[warp * 32] = mine;
+  if (C > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(&sh.bar[par], C * 32 * sizeof(Map2));
+  __syncthreads();
+  const int place = TIME > 0 ? warp : nw - 1 - warp;
+  const Map2* run0 = TIME > 0 ? run : run + (nw - 1) * 32;
+  F2 in = carry;
+  if (C == 1) {
+    // values in place of maps: the carry is known
+    carry = fold_value<CUT>(run0, TIME * 32, nw, place, carry, &in);
+    return in;
+  }
+  const Map2 before = fold_maps<CUT>(run0, TIME * 32, place);
+  Map2* block = sh.block + par * C * 32 + lane;
+  if (place == nw - 1) {
+    Map2 all = before;
+    fold_map<CUT>(all, mine);
+    for (int peer = 0; peer < C; ++peer)
+      st_async_map(cluster_map(block + rank * 32, peer), all, cluster_map(&sh.bar[par], peer));
+  }
+  if (alive) alive = mbar_wait_cluster(&sh.bar[par], (step >> 1) & 1);
+  const int place_c = TIME > 0 ? rank : C - 1 - rank;
+  const Map2* block0 = TIME > 0 ? block : block + (C - 1) * 32;
+  carry = fold_value<CUT>(block0, TIME * 32, C, place_c, carry, &in);
+  return through<CUT>(before.a, before.h, in);
+}
+
+// The shared memory of a block: the ring of `tensors` inputs' runs, the joins'
+// buffers and mbarriers, the runs' sequences.
+__host__ __device__ constexpr size_t scan_smem(int elem, int tensors, int warps, int cluster) {
+  return static_cast<size_t>(warps) * (32 * (static_cast<size_t>(kStages) * tensors * kScanRun * 2 *
+                                                 elem + 2 * sizeof(Map2)) +
+                                       kScanRun * sizeof(int)) +
+         static_cast<size_t>(cluster) * 64 * sizeof(Map2) + 2 * sizeof(uint64_t);
+}
+
+template <int E, int TENSORS>
+struct ScanShared {
+  char* ring;                // this warp's rows
+  int* first;                // sequences that begin in this warp's run
+  JoinBuffers join;
+  static constexpr int kRow = kScanChannels * E;      // bytes of a row piece
+  static constexpr int kTensor = kScanRun * kRow;
+  static constexpr int kStage = TENSORS * kTensor;
+  // Called by every thread; the caller synchronises the block (or cluster).
+  __device__ __forceinline__ ScanShared(char* base, int warp, int nw, int C) {
+    ring = base + warp * kStages * kStage;
+    base += nw * kStages * kStage;
+    join.run = reinterpret_cast<Map2*>(base);
+    join.block = join.run + 2 * nw * 32;
+    base = reinterpret_cast<char*>(join.block + 2 * C * 32);
+    join.bar = reinterpret_cast<uint64_t*>(base);
+    first = reinterpret_cast<int*>(join.bar + 2) + warp * kScanRun;
+    if (threadIdx.x == 0) {
+      mbar_init(&join.bar[0], 1);
+      mbar_init(&join.bar[1], 1);
+      mbar_fence_init();
+    }
+  }
+  template <int DT>
+  __device__ __forceinline__ Two<DT> raw(int stage, int tensor, int i) const {
+    const char* at = ring + stage * kStage + tensor * kTensor + i * kRow + (threadIdx.x & 31) * 2 * E;
+    Two<DT> p;
+    if constexpr (E == 4) {
+      const uint2 v = lds8(at);
+      p.w[0] = v.x;
+      p.w[1] = v.y;
+    } else {
+      p.w[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
+    return p;
+  }
+  template <int DT>
+  __device__ __forceinline__ F2 row(int stage, int tensor, int i) const {
+    return unpack2<DT>(raw<DT>(stage, tensor, i));
+  }
+  // Starts the copies into a stage of rows tok0 .. tok0 + 15 of a tensor (`src`: this slab's
+  // first channel of token 0), zeros for rows and channels that do not exist.
+  // `bytes`: of the slab's row pieces.
+  __device__ __forceinline__ void copy(int stage, int tensor, const char* src, uint32_t ld, int64_t tok0,
+                                       int64_t s, int bytes) const {
+    constexpr int kLanes = kRow / 16, kRows = 32 / kLanes;    // lanes a row, rows at once
+    const int lane = threadIdx.x & 31, col = lane % kLanes * 16, row0 = lane / kLanes;
+    const uint32_t to = smem_addr(ring) + stage * kStage + tensor * kTensor + row0 * kRow + col;
+    const int rows = col >= bytes || tok0 >= s || tok0 < 0 ? 0
+                     : s - tok0 < kScanRun ? static_cast<int>(s - tok0) : kScanRun;
+    const char* at = src + (rows > 0 ? tok0 * ld + col : 0);
+#pragma unroll
+    for (int i = 0; i < kScanRun / kRows; ++i) {
+      const int row = row0 + i * kRows;
+      const bool ok = row < rows;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * kRows * kRow),
+                   "l"(at + static_cast<uint64_t>(ok ? row : 0) * ld), "r"(ok ? 16 : 0)
+                   : "memory");
+    }
+  }
+  // The oldest stage's copies are there for every lane.
+  __device__ __forceinline__ void wait() const {
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+  }
+};
+
+// How a direction's time depends on the split of a call, measured on a GB300
+// in microseconds: the shortest step of a lone block, and of a cluster of C
+// (cluster + C per_block); its tensors read, and read or written.
+struct ScanCost {
+  double lone, cluster, per_block;
+  int tensors, passes;
+};
+
+// Chooses the split of a call and launches kernel `fn`.
+cudaError_t launch_scan(const void* fn, ScanParams& p, int elem, const ScanCost& cost, void** args,
                         cudaStream_t st);
 
 }  // namespace spb

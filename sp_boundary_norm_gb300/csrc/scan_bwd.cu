@@ -11,14 +11,55 @@
 
 namespace spb {
 
+constexpr int kBwdBlocks = 3;   // blocks an SM that the registers are held to
+
+// The run's factors, from its rows in shared memory: nk = -k, and dg = dgate
+// without its factor dh.  begin(i): the state before token i where a sequence
+// begins.
+template <int DT, bool TIED, bool MARKS, typename Shared, typename Begin>
+__device__ __forceinline__ void back_factors(const Shared& sh, int stage, uint32_t starts,
+                                             F2 h,
+                                             F2 (&nk)[kScanRun], F2 (&dg)[kScanRun],
+                                             Two<DT> (&dy)[kScanRun], Begin begin) {
+#pragma unroll
+  for (int i = 0; i < kScanRun; ++i) {
+    if (MARKS && ((starts >> i) & 1u)) h = begin(i);
+    F2 e, d;
+    nk[i] = neg_k<DT, true>(sh.template row<DT>(stage, 0, i), e);
+    h = next_state<TIED>(nk[i], h, sh.template row<DT>(stage, 1, i), d);
+    dg[i] = mul2(mul2(mul2(nk[i], nk[i]), e), d);            // a k d, a = e k
+    dy[i] = sh.template raw<DT>(stage, 2, i);
+  }
+}
+
+// q leaving the run's first token as a map of the q entering its last one.
+// end(i): the q entering token i where a sequence ends.
+template <int DT, bool MARKS, typename End>
+__device__ __forceinline__ Map2 back_map(uint32_t ends, const F2 (&nk)[kScanRun],
+                                         const Two<DT> (&dy)[kScanRun], End end) {
+  F2 q = f2(0.f, 0.f), fac = f2(1.f, 1.f);
+#pragma unroll
+  for (int i = kScanRun - 1; i >= 0; --i) {
+    if (MARKS && ((ends >> i) & 1u)) {
+      q = end(i);
+      fac = f2(0.f, 0.f);
+    }
+    const F2 x = add2(unpack2<DT>(dy[i]), q);
+    q = fma2(nk[i], x, x);                                   // a x
+    fac = fma2(nk[i], fac, fac);
+  }
+  return Map2{fac, q};
+}
+
 template <int DT, bool TIED, bool PACKED>
-__global__ void __launch_bounds__(32 * kScanMaxWarps) scan_bwd_kernel(const ScanParams P) {
+__global__ void __launch_bounds__(32 * kScanWarps, kBwdBlocks) scan_bwd_kernel(const ScanParams P) {
   constexpr int E = ElemSize<DT>::value;
-  extern __shared__ float2 slots[];                  // [warps][16][32]
-  __shared__ ScanShared sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+  const int nw = blockDim.x >> 5;
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  if (C > 1) cluster_sync_all();                     // the partners run: their shared memory is there
+  const ScanShared<E, 3> sh(smem, warp, nw, C);
+  if (C > 1) cluster_sync_all(); else __syncthreads();   // mbarriers (and partners) are ready
   pdl_wait();
   int unit = static_cast<int>(blockIdx.x) / C;
   if (PACKED && blockIdx.x == 0 && warp == 0)
@@ -26,129 +67,108 @@ __global__ void __launch_bounds__(32 * kScanMaxWarps) scan_bwd_kernel(const Scan
   const int slab = unit % P.slabs;
   unit /= P.slabs;
   const int r = unit % P.t, bi = unit / P.t;
-  const int ch = slab * kScanChannels + 2 * lane;
+  const int ch0 = slab * kScanChannels, ch = ch0 + 2 * lane;
   const bool on = ch < P.c;
+  const int bytes = (P.c - ch0 < kScanChannels ? P.c - ch0 : kScanChannels) * E;
+  const int64_t row0 = bi * P.s, col0 = static_cast<int64_t>(ch0) * E;
   const int64_t col = static_cast<int64_t>(ch) * E;
-  const char* gate = P.gate[r] + bi * P.s * P.ld_gate + col;
-  const char* value = P.value[r] + bi * P.s * P.ld_value + col;
-  const char* dy = P.dy[r] + bi * P.s * P.ld_dy + col;
-  char* dgate = P.out[r] + bi * P.s * P.ld_out + col;
-  char* dvalue = P.dvalue[r] + bi * P.s * P.ld_dvalue + col;
+  const char* gate = P.gate[r] + row0 * P.ld_gate + col0;
+  const char* value = P.value[r] + row0 * P.ld_value + col0;
+  const char* dy_at = P.dy[r] + row0 * P.ld_dy + col0;
+  char* dgate = P.out[r] + row0 * P.ld_out + col;
+  char* dvalue = P.dvalue[r] + row0 * P.ld_dvalue + col;
   const int64_t n_runs = (P.s + kScanRun - 1) / kScanRun;
   const float* states = P.states[r] + bi * n_runs * P.c + ch;
-  float2(*slot)[32] = reinterpret_cast<float2(*)[32]>(slots + warp * kScanRun * 32);
   if (PACKED && rank == 0) pass_empty(P, P.dhT[r], P.hT[r], ch, on);
 
   const int64_t stretch = static_cast<int64_t>(C) * nw * kScanRun;
   const int64_t last = (P.s - 1) / stretch * stretch;
-  float2 carry = make_float2(0.f, 0.f);
-  int par = 0;
-  for (int64_t base = last; base >= 0; base -= stretch, par ^= 1) {
-    const int64_t tok0 = base + static_cast<int64_t>(rank * nw + warp) * kScanRun;
-    Two<DT> draw[kScanRun];
-    float k[kScanRun][2], dg[kScanRun][2];           // k, and dgate without its factor dh
-    const RunMarks marks = run_marks<PACKED>(P, tok0);
-    fetch_states<PACKED>(P, P.h0[r], marks.starts, tok0, bi, ch, on, slot);
-    {
-      Two<DT> graw[kScanRun], vraw[kScanRun];
-      float2 st = make_float2(0.f, 0.f);
-      // tokens after the last one take part as zeros
+  int64_t tok0 = last + static_cast<int64_t>(rank * nw + warp) * kScanRun;
+  // tokens after the last one take part as zeros
+  auto fetch = [&](int stage, int64_t at) {
+    sh.copy(stage, 0, gate, P.ld_gate, at, P.s, bytes);
+    sh.copy(stage, 1, value, P.ld_value, at, P.s, bytes);
+    sh.copy(stage, 2, dy_at, P.ld_dy, at, P.s, bytes);
+    cp_async_commit();
+  };
+  float2 entering = make_float2(0.f, 0.f);           // the state entering the next run
+  auto fetch_entering = [&](int64_t at) {
+    if (on && at >= 0 && at < P.s)
+      entering = __ldcs(reinterpret_cast<const float2*>(states + (at / kScanRun) * P.c));
+  };
 #pragma unroll
-      for (int i = 0; i < kScanRun; ++i) {
-        graw[i] = vraw[i] = draw[i] = Two<DT>{};
-        if (on && tok0 + i < P.s) {
-          load_pack(graw[i], gate + (tok0 + i) * P.ld_gate);
-          load_pack(vraw[i], value + (tok0 + i) * P.ld_value);
-          load_pack(draw[i], dy + (tok0 + i) * P.ld_dy);
-        }
-      }
-      if (on && tok0 < P.s)
-        st = __ldcs(reinterpret_cast<const float2*>(states + (tok0 / kScanRun) * P.c));
-      float h[2] = {st.x, st.y};
-#pragma unroll
-      for (int i = 0; i < kScanRun; ++i) {
-        if ((marks.starts >> i) & 1u) {
-          const float2 v = slot[i][lane];
-          h[0] = v.x;
-          h[1] = v.y;
-        }
-        float g[2], v[2];
-        unpack(graw[i], g);
-        unpack(vraw[i], v);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float a;
-          gate_of<DT>(g[e], a, k[i][e]);
-          const float d = TIED ? v[e] - h[e] : h[e];
-          dg[i][e] = a * k[i][e] * (TIED ? -d : d);
-          h[e] = TIED ? fmaf(k[i][e], d, h[e]) : fmaf(a, d, v[e]);
-        }
-      }
-    }
-    fetch_states<PACKED>(P, P.dhT[r], marks.ends, tok0, bi, ch, on, slot);
-    // q leaving the run's first token as a map of the q entering its last one
-    float q[2] = {0.f, 0.f}, fac[2] = {1.f, 1.f};
-#pragma unroll
-    for (int i = kScanRun - 1; i >= 0; --i) {
-      if ((marks.ends >> i) & 1u) {
-        const float2 v = slot[i][lane];
-        q[0] = v.x;
-        q[1] = v.y;
-        fac[0] = fac[1] = 0.f;
-      }
-      float d[2];
-      unpack(draw[i], d);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = d[e] + q[e];
-        q[e] = fmaf(-k[i][e], x, x);                 // a x
-        fac[e] = fmaf(-k[i][e], fac[e], fac[e]);
-      }
-    }
-    const Map2 mine{fac[0], fac[1], q[0], q[1]};
-    float2 in = join_runs<PACKED, -1>(sh, par, mine, C, rank, carry);
+  for (int k = 0; k < kStages; ++k) fetch(k, tok0 - k * stretch);
+  fetch_entering(tok0);
+  F2 carry = f2(0.f, 0.f);
+  SeqWindow win = no_window();
+  int step = 0;
+  bool alive = true;
+  for (int64_t base = last; base >= 0; base -= stretch, tok0 -= stretch, ++step) {
+    const RunMarks marks = run_marks<PACKED>(P, tok0, win, sh.first, 15);
+    const bool plain = (marks.starts | marks.ends) == 0u;    // and then all 16 tokens exist
+    auto seq = [&](int i) { return seq_of_run<PACKED>(win, sh.first, marks.starts, bi, i); };
+    auto begin = [&](int i) { return load_state(P, P.h0[r], seq(i), ch, on); };
+    auto end = [&](int i) { return load_state(P, P.dhT[r], seq(i), ch, on); };
+    Two<DT> dy[kScanRun];
+    F2 nk[kScanRun], dg[kScanRun];
+    sh.wait();
+    const int stage = step % kStages;
+    const F2 h = f2(entering.x, entering.y);
+    if (plain)
+      back_factors<DT, TIED, false>(sh, stage, 0u, h, nk, dg, dy, begin);
+    else
+      back_factors<DT, TIED, true>(sh, stage, marks.starts, h, nk, dg, dy, begin);
+    __syncwarp();                     // every lane has read the rows
+    fetch(stage, tok0 - kStages * stretch);
+    fetch_entering(tok0 - stretch);
+    const Map2 mine = plain ? back_map<DT, false>(0u, nk, dy, end)
+                            : back_map<DT, true>(marks.ends, nk, dy, end);
+    F2 into = join_runs<PACKED, -1>(sh.join, step, mine, C, rank, warp, nw, carry, alive);
     if (tok0 >= P.s) continue;
+    char* at_g = dgate + tok0 * P.ld_out;
+    char* at_v = dvalue + tok0 * P.ld_dvalue;
+    const F2 minus = f2(-1.f, -1.f);
+    if (plain) {
+      if (on) {
+#pragma unroll
+        for (int i = kScanRun - 1; i >= 0; --i) {
+          const F2 dh = add2(unpack2<DT>(dy[i]), into);
+          into = fma2(nk[i], dh, dh);
+          store_pack(at_g + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(mul2(dh, dg[i])));
+          store_pack(at_v + static_cast<uint64_t>(P.ld_dvalue) * i,
+                     pack2<DT>(TIED ? mul2(mul2(dh, minus), nk[i]) : dh));
+        }
+      }
+      continue;
+    }
+    const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
 #pragma unroll
     for (int i = kScanRun - 1; i >= 0; --i) {
-      if ((marks.ends >> i) & 1u) in = slot[i][lane];
-      float d[2], o[2];
-      unpack(draw[i], d);
-      d[0] += in.x;
-      d[1] += in.y;
-      in.x = fmaf(-k[i][0], d[0], d[0]);
-      in.y = fmaf(-k[i][1], d[1], d[1]);
-      if ((marks.starts >> i) & 1u) slot[i][lane] = make_float2(d[0], d[1]);
-      if (on && tok0 + i < P.s) {
-        Two<DT> w;
-        o[0] = d[0] * dg[i][0];
-        o[1] = d[1] * dg[i][1];
-        pack(w, o);
-        store_pack(dgate + (tok0 + i) * P.ld_out, w);
-        o[0] = TIED ? d[0] * k[i][0] : d[0];
-        o[1] = TIED ? d[1] * k[i][1] : d[1];
-        pack(w, o);
-        store_pack(dvalue + (tok0 + i) * P.ld_dvalue, w);
+      if ((marks.ends >> i) & 1u) into = end(i);
+      const F2 dh = add2(unpack2<DT>(dy[i]), into);
+      into = fma2(nk[i], dh, dh);
+      if ((marks.starts >> i) & 1u) store_state(P, P.hT[r], seq(i), ch, on, dh);
+      if (on && i < rows) {
+        store_pack(at_g + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(mul2(dh, dg[i])));
+        store_pack(at_v + static_cast<uint64_t>(P.ld_dvalue) * i,
+                   pack2<DT>(TIED ? mul2(mul2(dh, minus), nk[i]) : dh));
       }
     }
-    if (P.hT[r] != nullptr && marks.starts != 0) {
-      // dh0 = a dh: a from the gate again, where 1 - k would lose a small one
-      uint32_t left = marks.starts;
-      while (left != 0) {
-        const int i = __ffs(left) - 1;
-        left &= left - 1;
-        if (!on) continue;
+    if (P.hT[r] != nullptr && on) {
+      // dh0 = a dh: a = e k from the gate again, where 1 - k would lose a small one
+      for (uint32_t left = marks.starts; left != 0; left &= left - 1) {
+        const int i = __ffs(left) - 1, j = seq(i);
         Two<DT> graw;
-        load_pack(graw, gate + (tok0 + i) * P.ld_gate);
-        float g[2], a[2], kk;
-        unpack(graw, g);
-        gate_of<DT>(g[0], a[0], kk);
-        gate_of<DT>(g[1], a[1], kk);
-        const float2 d = slot[i][lane];
-        slot[i][lane] = make_float2(a[0] * d.x, a[1] * d.y);
+        load_pack(graw, P.gate[r] + (row0 + tok0 + i) * P.ld_gate + col);
+        F2 e;
+        const F2 a = mul2(neg_k<DT, true>(unpack2<DT>(graw), e), e);
+        store_state(P, P.hT[r], j, ch, on, mul2(mul2(a, minus), load_state(P, P.hT[r], j, ch, on)));
       }
-      put_states<PACKED>(P, P.hT[r], marks.starts, tok0, bi, ch, on, slot);
     }
   }
+  cp_async_wait<0>();
+  if (!alive && P.status != nullptr) *P.status = SP_ERR_TIMEOUT;
+  if (C > 1) cluster_sync_all();                     // no partner still writes here
 }
 
 template <int DT>
@@ -163,12 +183,11 @@ static const void* scan_bwd_fn(bool tied, bool packed) {
 cudaError_t launch_scan_bwd(ScanParams p, int dtype, cudaStream_t st) {
   void* args[] = {&p};
   const bool packed = p.cu_seqlens != nullptr;
-  int warps;
-  scan_shape(p, &warps, &p.cluster);
   const void* fn = dtype == SP_BF16  ? scan_bwd_fn<SP_BF16>(p.tied, packed)
                    : dtype == SP_F16 ? scan_bwd_fn<SP_F16>(p.tied, packed)
                                      : scan_bwd_fn<SP_F32>(p.tied, packed);
-  return launch_scan(fn, p, warps, args, st);
+  const ScanCost cost{1.4, 1.9, 0.08, 3, 5};
+  return launch_scan(fn, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
 }
 
 }  // namespace spb

@@ -5,14 +5,39 @@
 
 namespace spb {
 
+constexpr int kFwdBlocks = 4;   // blocks an SM that the registers are held to
+
+// One run: h[i], f[i] with h[i] + f[i] * (state entering the run) the state
+// after token i.  begin(i): the state before token i where a sequence begins.
+template <int DT, bool TIED, bool MARKS, typename Shared, typename Begin>
+__device__ __forceinline__ Map2 scan_run(const Shared& sh, int stage, uint32_t starts,
+                                         F2 (&h)[kScanRun], F2 (&f)[kScanRun], Begin begin) {
+  F2 cur = f2(0.f, 0.f), fac = f2(1.f, 1.f);
+#pragma unroll
+  for (int i = 0; i < kScanRun; ++i) {
+    if (MARKS && ((starts >> i) & 1u)) {
+      cur = begin(i);
+      fac = f2(0.f, 0.f);
+    }
+    F2 e, d;
+    const F2 nk = neg_k<DT, false>(sh.template row<DT>(stage, 0, i), e);
+    cur = next_state<TIED>(nk, cur, sh.template row<DT>(stage, 1, i), d);
+    fac = fma2(nk, fac, fac);
+    h[i] = cur;
+    f[i] = fac;
+  }
+  return Map2{fac, cur};
+}
+
 template <int DT, bool TIED, bool PACKED>
-__global__ void __launch_bounds__(32 * kScanMaxWarps) scan_fwd_kernel(const ScanParams P) {
+__global__ void __launch_bounds__(32 * kScanWarps, kFwdBlocks) scan_fwd_kernel(const ScanParams P) {
   constexpr int E = ElemSize<DT>::value;
-  extern __shared__ float2 slots[];                  // [warps][16][32]
-  __shared__ ScanShared sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+  const int nw = blockDim.x >> 5;
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  if (C > 1) cluster_sync_all();                     // the partners run: their shared memory is there
+  const ScanShared<E, 2> sh(smem, warp, nw, C);
+  if (C > 1) cluster_sync_all(); else __syncthreads();   // mbarriers (and partners) are ready
   pdl_wait();
   int unit = static_cast<int>(blockIdx.x) / C;
   if (PACKED && blockIdx.x == 0 && warp == 0)
@@ -20,79 +45,67 @@ __global__ void __launch_bounds__(32 * kScanMaxWarps) scan_fwd_kernel(const Scan
   const int slab = unit % P.slabs;
   unit /= P.slabs;
   const int r = unit % P.t, bi = unit / P.t;
-  const int ch = slab * kScanChannels + 2 * lane;
+  const int ch0 = slab * kScanChannels, ch = ch0 + 2 * lane;
   const bool on = ch < P.c;
-  const char* gate = P.gate[r] + bi * P.s * P.ld_gate + static_cast<int64_t>(ch) * E;
-  const char* value = P.value[r] + bi * P.s * P.ld_value + static_cast<int64_t>(ch) * E;
-  char* out = P.out[r] + bi * P.s * P.ld_out + static_cast<int64_t>(ch) * E;
+  const int bytes = (P.c - ch0 < kScanChannels ? P.c - ch0 : kScanChannels) * E;
+  const int64_t row0 = bi * P.s;
+  const char* gate = P.gate[r] + row0 * P.ld_gate + static_cast<int64_t>(ch0) * E;
+  const char* value = P.value[r] + row0 * P.ld_value + static_cast<int64_t>(ch0) * E;
+  char* out = P.out[r] + row0 * P.ld_out + static_cast<int64_t>(ch) * E;
   const int64_t n_runs = (P.s + kScanRun - 1) / kScanRun;
   float* states = P.states[r];
   if (states != nullptr) states += bi * n_runs * P.c + ch;
-  float2(*slot)[32] = reinterpret_cast<float2(*)[32]>(slots + warp * kScanRun * 32);
   if (PACKED && rank == 0) pass_empty(P, P.h0[r], P.hT[r], ch, on);
 
-  Two<DT> graw[kScanRun], vraw[kScanRun];
   const int64_t stretch = static_cast<int64_t>(C) * nw * kScanRun;
   int64_t tok0 = static_cast<int64_t>(rank * nw + warp) * kScanRun;
-  auto fetch = [&](int64_t at) {
-#pragma unroll
-    for (int i = 0; i < kScanRun; ++i) {
-      if (on && at + i < P.s) {
-        load_pack(graw[i], gate + (at + i) * P.ld_gate);
-        load_pack(vraw[i], value + (at + i) * P.ld_value);
-      }
-    }
+  auto fetch = [&](int stage, int64_t at) {
+    sh.copy(stage, 0, gate, P.ld_gate, at, P.s, bytes);
+    sh.copy(stage, 1, value, P.ld_value, at, P.s, bytes);
+    cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kScanRun; ++i) graw[i] = vraw[i] = Two<DT>{};
-  fetch(tok0);
-  float2 carry = make_float2(0.f, 0.f);
-  int par = 0;
-  for (int64_t base = 0; base < P.s; base += stretch, tok0 += stretch, par ^= 1) {
-    const RunMarks marks = run_marks<PACKED>(P, tok0);
-    fetch_states<PACKED>(P, P.h0[r], marks.starts, tok0, bi, ch, on, slot);
-    float h[kScanRun][2], f[kScanRun][2];            // h = h[i] + f[i] * (state entering)
-    float cur[2] = {0.f, 0.f}, fac[2] = {1.f, 1.f};
-#pragma unroll
-    for (int i = 0; i < kScanRun; ++i) {
-      if ((marks.starts >> i) & 1u) {
-        const float2 v = slot[i][lane];
-        cur[0] = v.x;
-        cur[1] = v.y;
-        fac[0] = fac[1] = 0.f;
-      }
-      float g[2], v[2];
-      unpack(graw[i], g);
-      unpack(vraw[i], v);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float a, k;
-        gate_of<DT>(g[e], a, k);
-        cur[e] = TIED ? fmaf(k, v[e] - cur[e], cur[e]) : fmaf(a, cur[e], v[e]);
-        fac[e] = fac[e] * a;
-        h[i][e] = cur[e];
-        f[i][e] = fac[e];
-      }
-    }
-    fetch(tok0 + stretch);
-    const Map2 mine{fac[0], fac[1], cur[0], cur[1]};
-    const float2 in = join_runs<PACKED, 1>(sh, par, mine, C, rank, carry);
+  for (int k = 0; k < kStages; ++k) fetch(k, tok0 + k * stretch);
+  F2 carry = f2(0.f, 0.f);
+  SeqWindow win = no_window();
+  int step = 0;
+  bool alive = true;
+  for (int64_t base = 0; base < P.s; base += stretch, tok0 += stretch, ++step) {
+    const RunMarks marks = run_marks<PACKED>(P, tok0, win, sh.first, 0);
+    const bool plain = (marks.starts | marks.ends) == 0u;    // and then all 16 tokens exist
+    auto seq = [&](int i) { return seq_of_run<PACKED>(win, sh.first, marks.starts, bi, i); };
+    auto begin = [&](int i) { return load_state(P, P.h0[r], seq(i), ch, on); };
+    F2 h[kScanRun], f[kScanRun];
+    sh.wait();
+    const int stage = step % kStages;
+    const Map2 mine = plain ? scan_run<DT, TIED, false>(sh, stage, 0u, h, f, begin)
+                            : scan_run<DT, TIED, true>(sh, stage, marks.starts, h, f, begin);
+    __syncwarp();                     // every lane has read the rows
+    fetch(stage, tok0 + kStages * stretch);
+    const F2 entry = join_runs<PACKED, 1>(sh.join, step, mine, C, rank, warp, nw, carry, alive);
     if (tok0 >= P.s) continue;
     if (states != nullptr && on)
-      __stcs(reinterpret_cast<float2*>(states + (tok0 / kScanRun) * P.c), in);
-    const uint32_t ends = P.hT[r] != nullptr ? marks.ends : 0u;
+      __stcs(reinterpret_cast<float2*>(states + (tok0 / kScanRun) * P.c), split(entry));
+    char* at = out + tok0 * P.ld_out;
+    if (plain) {
+      if (on) {
+#pragma unroll
+        for (int i = 0; i < kScanRun; ++i)
+          store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(fma2(f[i], entry, h[i])));
+      }
+      continue;
+    }
+    const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
 #pragma unroll
     for (int i = 0; i < kScanRun; ++i) {
-      float y[2] = {through<PACKED>(f[i][0], h[i][0], in.x), through<PACKED>(f[i][1], h[i][1], in.y)};
-      if ((ends >> i) & 1u) slot[i][lane] = make_float2(y[0], y[1]);
-      if (on && tok0 + i < P.s) {
-        Two<DT> o;
-        pack(o, y);
-        store_pack(out + (tok0 + i) * P.ld_out, o);
-      }
+      const F2 y = through<PACKED>(f[i], h[i], entry);
+      if ((marks.ends >> i) & 1u) store_state(P, P.hT[r], seq(i), ch, on, y);
+      if (on && i < rows) store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(y));
     }
-    put_states<PACKED>(P, P.hT[r], ends, tok0, bi, ch, on, slot);
   }
+  cp_async_wait<0>();
+  if (!alive && P.status != nullptr) *P.status = SP_ERR_TIMEOUT;
+  if (C > 1) cluster_sync_all();                     // no partner still writes here
 }
 
 // One token a sequence: nothing to join.  Eight channels a thread.
@@ -119,10 +132,14 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams P) {
     unpack(vraw, v);
     unpack(h, x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float a, k;
-      gate_of<DT>(g[e], a, k);
-      x[e] = P.tied ? fmaf(k, v[e] - x[e], x[e]) : fmaf(a, x[e], v[e]);
+    for (int i = 0; i < 8; i += 2) {
+      F2 e, d;
+      const F2 nk = neg_k<DT, false>(f2(g[i], g[i + 1]), e);
+      const F2 old = f2(x[i], x[i + 1]), val = f2(v[i], v[i + 1]);
+      const float2 y = split(P.tied ? next_state<true>(nk, old, val, d)
+                                    : next_state<false>(nk, old, val, d));
+      x[i] = y.x;
+      x[i + 1] = y.y;
     }
     pack(o, x);
     store_pack(P.out[r] + bi * P.ld_out + static_cast<int64_t>(ch) * E, o);
@@ -134,18 +151,6 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams P) {
   }
 }
 
-void scan_shape(const ScanParams& p, int* warps, int* cluster) {
-  const int64_t runs = (p.s + kScanRun - 1) / kScanRun;
-  int w = 1;
-  while (w < 8 && w < runs) w *= 2;
-  const int64_t units = static_cast<int64_t>(p.slabs) * p.t * p.b;
-  const int64_t want = 2 * static_cast<int64_t>(device_sm_count());
-  int c = 1;
-  while (c < kScanMaxCluster && units * c < want && static_cast<int64_t>(c) * w < runs) c *= 2;
-  *warps = w;
-  *cluster = c;
-}
-
 template <int DT>
 static const void* scan_fwd_fn(bool tied, bool packed) {
   if (tied)
@@ -155,17 +160,49 @@ static const void* scan_fwd_fn(bool tied, bool packed) {
                 : reinterpret_cast<const void*>(&scan_fwd_kernel<DT, false, false>);
 }
 
-cudaError_t launch_scan(const void* fn, const ScanParams& p, int warps, void** args,
+// Blocks of up to four warps; C blocks a cluster, for the C with the least
+// expected time: the clusters that fit the GPU at once run in waves, and a step
+// of a wave takes its shortest time or that of its bytes at 6.0 TB/s, whichever
+// is longer.  (16,384 tokens, 8192 channels, bf16, forward: C = 1 244 us, 2
+// 210, 3 165, 4 146, 8 162; backward: 1 371, 2 272, 3 231, 4 294, 8 264.  1024
+// channels: C = 8 61 us, 12 49, 16 39; backward 70, 55, 52.)
+cudaError_t launch_scan(const void* fn, ScanParams& p, int elem, const ScanCost& cost, void** args,
                         cudaStream_t st) {
-  const size_t smem = static_cast<size_t>(warps) * kScanRun * 32 * sizeof(float2);
-  cudaError_t e = ensure_smem_attr(fn, smem);
-  if (e == cudaSuccess && p.cluster > 8)
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = static_cast<int64_t>(p.slabs) * p.t * p.b * p.cluster;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl(fn, dim3(static_cast<unsigned>(blocks)), dim3(32 * warps), smem, args, st,
-                    p.cluster);
+  const int64_t runs = (p.s + kScanRun - 1) / kScanRun;
+  const int64_t units = static_cast<int64_t>(p.slabs) * p.t * p.b;
+  int warps = 1;
+  while (warps < kScanWarps && warps < runs) warps *= 2;
+  static const int kClusters[] = {1, 2, 3, 4, 6, 8, 12, kScanMaxCluster};
+  double best = 0;
+  size_t smem = 0;
+  for (int c : kClusters) {
+    if (c > 1 && static_cast<int64_t>(c - 1) * warps >= runs) break;
+    const size_t need = scan_smem(elem, cost.tensors, warps, c);
+    int fit = 0;
+    const cudaError_t e = max_clusters(fn, 32 * warps, need, c, &fit);
+    if (e != cudaSuccess) return e;
+    if (fit < 1) continue;
+    const double bytes = static_cast<double>(c) * warps * kScanRun * kScanChannels * elem *
+                         cost.passes;
+    auto step = [&](int64_t clusters) {
+      const double least = c == 1 ? cost.lone : cost.cluster + c * cost.per_block;
+      const double moved = static_cast<double>(clusters) * bytes / 6.0e6;
+      return least > moved ? least : moved;
+    };
+    const int64_t steps = (runs + static_cast<int64_t>(c) * warps - 1) / (c * warps);
+    const double start = c == 1 ? 2.0 : 3.0;    // a wave's launch and first rows
+    const double time =
+        static_cast<double>(units / fit) * (start + static_cast<double>(steps) * step(fit)) +
+        (units % fit != 0 ? start + static_cast<double>(steps) * step(units % fit) : 0.0);
+    if (smem == 0 || time < best) {
+      best = time;
+      smem = need;
+      p.cluster = c;
+    }
+  }
+  if (smem == 0 || units * p.cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(fn, dim3(static_cast<unsigned>(units * p.cluster)), dim3(32 * warps), smem,
+                    args, st, p.cluster);
 }
 
 cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st) {
@@ -180,12 +217,11 @@ cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st) {
     return launch_pdl(fn, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(128), 0,
                       args, st);
   }
-  int warps;
-  scan_shape(p, &warps, &p.cluster);
   const void* fn = dtype == SP_BF16  ? scan_fwd_fn<SP_BF16>(p.tied, packed)
                    : dtype == SP_F16 ? scan_fwd_fn<SP_F16>(p.tied, packed)
                                      : scan_fwd_fn<SP_F32>(p.tied, packed);
-  return launch_scan(fn, p, warps, args, st);
+  const ScanCost cost{1.0, 1.5, 0.055, 2, 3};
+  return launch_scan(fn, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
 }
 
 }  // namespace spb

@@ -136,6 +136,7 @@ def test_scan_refuses_overlapping_states():
     assert _scan(True, dvalue=_ptrs(2, 2)) == 7                 # dvalue over dgate
     assert _scan(True, dvalue=_ptrs(2, 2, 64)) == 7             # beside it, rows too narrow
     assert _scan(True, dh0=_ptrs(2, 9), h0=_ptrs(2, 9)) == 7
+    assert _scan(True, dh0=_ptrs(2, 9), dhT=_ptrs(2, 9)) == 7
     # slices of one buffer whose rows overlap by eight elements
     assert _scan(True, ld=120, dvalue=_ptrs(2, 2, 112)) == 7
 
