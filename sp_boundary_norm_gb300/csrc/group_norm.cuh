@@ -23,94 +23,242 @@ namespace spb {
 template <int DT>
 using Vec8 = Pack<DT, 8>;
 
+constexpr int kTileRows = 4;        // vectors a thread holds (tiles, forward)
+constexpr int kBackTileRows = 2;    // of x and of dy (tiles, backward)
+
+__device__ __forceinline__ F2 both(float v) { return f2(v, v); }
+
 template <int DT>
-__device__ __forceinline__ float sigmoid_of(float q) {
+__device__ __forceinline__ F2 sigmoid_of(F2 q) {
+  float2 e;
   if constexpr (DT == SP_F32) {
-    return __frcp_rn(1.f + expf(-q));
+    e = split(q);
+    return f2(__frcp_rn(1.f + expf(-e.x)), __frcp_rn(1.f + expf(-e.y)));
   } else {
     // 16-bit results: the fast exponential's error is far below their rounding
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(q * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
-    return s;
+    e = split(mul2(q, both(-1.4426950408889634f)));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    e = split(add2(f2(e.x, e.y), both(1.f)));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    return f2(e.x, e.y);
   }
 }
 
 // The parameters of a thread's column.
 template <int DT>
 struct Column {
-  float gamma[8], beta[8];
+  F2 gamma[4], beta[4];
   __device__ __forceinline__ void read(const GroupNormParams& P, int64_t ch, bool on) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) gamma[i] = beta[i] = 0.f;
+    for (int i = 0; i < 4; ++i) gamma[i] = beta[i] = both(0.f);
     if (!on) return;
     Vec8<DT> v;
     load_pack(v, P.gamma + ch * ElemSize<DT>::value);
-    unpack(v, gamma);
+    unpack_pairs(v, gamma);
     if (P.norm == SP_NORM_LAYERNORM) {
       load_pack(v, P.beta + ch * ElemSize<DT>::value);
-      unpack(v, beta);
+      unpack_pairs(v, beta);
     }
   }
 };
 
-// Sum over `width` neighbouring lanes (a power of two, aligned).
-__device__ __forceinline__ float lanes_sum(float v, int width) {
-  for (int d = width >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  return v;
-}
-
-template <int DT>
-__device__ __forceinline__ void norm_act(const float (&x)[8], float mean, float rstd,
-                                         const Column<DT>& col, bool silu, Vec8<DT>& o) {
-  float y[8];
+// Sums over `width` neighbouring lanes (a power of two, aligned), N at once.
+template <int N>
+__device__ __forceinline__ void lanes_sum(float (&v)[N], int width) {
+  for (int d = width >> 1; d > 0; d >>= 1) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = fmaf((x[i] - mean) * rstd, col.gamma[i], col.beta[i]);
-    y[i] = silu ? q * sigmoid_of<DT>(q) : q;
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
   }
-  pack(o, y);
+}
+__device__ __forceinline__ float lanes_sum(float v, int width) {
+  float w[1] = {v};
+  lanes_sum(w, width);
+  return w[0];
 }
 
-// Backward of one vector: z and dq gamma (the gradient of z) from x and dy,
-// adding the vector's part of the parameter gradients.
-template <int DT>
-__device__ __forceinline__ void back_act(const float (&x)[8], const float (&dy)[8], float mean,
-                                         float rstd, const Column<DT>& col, bool silu,
-                                         float (&z)[8], float (&dq)[8]) {
+// n rows dealt to `parts` in turn: the k-th gets count(k), its first is first(k)
+// when they are dealt in one piece each.  32-bit arithmetic: a 64-bit division
+// costs a hundred instructions.
+struct Deal {
+  int each, extra;
+  __device__ __forceinline__ Deal(int n, int parts) : each(n / parts), extra(n % parts) {}
+  __device__ __forceinline__ int count(int k) const { return each + (k < extra ? 1 : 0); }
+  __device__ __forceinline__ int first(int k) const { return k * each + (k < extra ? k : extra); }
+};
+
+// The vectors that a thread keeps in shared memory, T to a row (x; x and dy):
+// its own slots, filled by its own copies, so no other thread waits for them.
+template <int DT, int T>
+struct Kept {
+  static constexpr int kPer = ElemSize<DT>::value == 4 ? 2 : 1;   // 16-byte pieces
+  const char* base;          // of this thread's first slot
+  uint32_t addr, piece;      // its shared address; bytes from one piece to the next
+  __device__ __forceinline__ Kept(void* smem) {
+    base = static_cast<char*>(smem) + threadIdx.x * 16;
+    addr = smem_addr(base);
+    piece = blockDim.x * 16;
+  }
+  __device__ __forceinline__ uint32_t offset(int i, int k) const {
+    return static_cast<uint32_t>(i * T + k) * kPer * piece;
+  }
+  __device__ __forceinline__ void copy(int i, int k, const char* src) const {
+    const uint32_t to = addr + offset(i, k);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    z[i] = (x[i] - mean) * rstd;
-    dq[i] = dy[i];
-    if (silu) {
-      const float q = fmaf(z[i], col.gamma[i], col.beta[i]);
-      const float s = sigmoid_of<DT>(q);
-      dq[i] *= s * fmaf(q, 1.f - s, 1.f);
+    for (int j = 0; j < kPer; ++j)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * piece),
+                   "l"(src + 16 * j)
+                   : "memory");
+  }
+  __device__ __forceinline__ Vec8<DT> get(int i, int k) const {
+    const char* from = base + offset(i, k);
+    Vec8<DT> v;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint4 w = lds16(from + j * piece);
+      v.w[4 * j] = w.x;
+      v.w[4 * j + 1] = w.y;
+      v.w[4 * j + 2] = w.z;
+      v.w[4 * j + 3] = w.w;
+    }
+    return v;
+  }
+};
+
+// At most n of the thread's groups of copies are still on their way.
+__device__ __forceinline__ void keep_wait(int n) {
+  if (n == 0) cp_async_wait<0>();
+  else if (n == 1) cp_async_wait<1>();
+  else if (n == 2) cp_async_wait<2>();
+  else cp_async_wait<3>();
+}
+
+__device__ __forceinline__ float pair_sum(const F2 (&v)[4]) {
+  const float2 w = split(add2(add2(v[0], v[1]), add2(v[2], v[3])));
+  return w.x + w.y;
+}
+
+// Sum of (x - m)^2 of a vector.
+__device__ __forceinline__ float spread_sum(const F2 (&x)[4], float m) {
+  F2 d = add2(x[0], both(-m)), s = mul2(d, d);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    d = add2(x[i], both(-m));
+    s = fma2(d, d, s);
+  }
+  const float2 w = split(s);
+  return w.x + w.y;
+}
+
+// z = (x - mean) rstd.  For 16-bit inputs as x rstd - mean rstd, one operation:
+// its rounding, 2^-24 of |mean| rstd, is below the inputs' own, 2^-11 of it.
+template <int DT>
+__device__ __forceinline__ F2 standard(F2 x, float mean, float rstd) {
+  if constexpr (DT == SP_F32) return mul2(add2(x, both(-mean)), both(rstd));
+  return fma2(x, both(rstd), both(-mean * rstd));
+}
+
+// One vector's result.
+template <int DT>
+__device__ __forceinline__ Vec8<DT> norm_act(const F2 (&x)[4], float mean, float rstd,
+                                             const Column<DT>& col, bool silu) {
+  F2 y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = fma2(standard<DT>(x[i], mean, rstd), col.gamma[i], col.beta[i]);
+  if (silu) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], sigmoid_of<DT>(y[i]));
+  }
+  Vec8<DT> o;
+  pack_pairs(o, y);
+  return o;
+}
+
+// Backward of one vector: z and dq (the gradient of q) in place of x and dy.
+template <int DT>
+__device__ __forceinline__ void back_act(F2 (&x)[4], F2 (&dy)[4], float mean, float rstd,
+                                         const Column<DT>& col, bool silu) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = standard<DT>(x[i], mean, rstd);
+  if (silu) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 q = fma2(x[i], col.gamma[i], col.beta[i]);
+      const F2 s = sigmoid_of<DT>(q);
+      const F2 t = fma2(mul2(s, both(-1.f)), s, s);          // s (1 - s)
+      dy[i] = mul2(dy[i], fma2(q, t, s));                    // s + q s (1 - s)
     }
   }
 }
 
-// Adds the rows' parts of a column's parameter gradients (acc[0..7] dgamma,
-// acc[8..15] dbeta) over the block in row order and writes the block's part.
+// dx of one vector from its z and dq and the group's means of dz and dz z.
+template <int DT>
+__device__ __forceinline__ Vec8<DT> back_out(const F2 (&z)[4], const F2 (&dq)[4], float rstd,
+                                             const Column<DT>& col, float m1, float m2) {
+  F2 y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = mul2(fma2(z[i], both(-m2), fma2(dq[i], col.gamma[i], both(-m1))), both(rstd));
+  Vec8<DT> o;
+  pack_pairs(o, y);
+  return o;
+}
+
+// Adds the rows' parts of a column's parameter gradients (acc[0..3] dgamma,
+// acc[4..7] dbeta) over the block in row order and writes the block's part.
+// ch0, channels: the slab's first one and how many exist.
 // buf: [rows][cols][17] floats of shared memory (17: the columns' banks differ).
-__device__ __forceinline__ void put_param_part(const GroupNormParams& P, const float (&acc)[16],
-                                               float* buf, int cx, int ry, bool on, int64_t ch,
-                                               int64_t part) {
+__device__ __forceinline__ void put_param_part(const GroupNormParams& P, const F2 (&acc)[8],
+                                               float* buf, int cx, int ry, int64_t ch0,
+                                               int channels, int64_t part) {
   __syncthreads();
   if (ry < P.rows) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) buf[(ry * P.cols + cx) * 17 + i] = acc[i];
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = split(acc[i]);
+      buf[(ry * P.cols + cx) * 17 + 2 * i] = v.x;
+      buf[(ry * P.cols + cx) * 17 + 2 * i + 1] = v.y;
+    }
   }
   __syncthreads();
-  if (ry != 0 || !on) return;
   const int64_t width = static_cast<int64_t>(P.t) * P.c;
-  float* ws = P.ws + part * 2 * width + ch;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  float* ws = P.ws + part * 2 * width + ch0;
+  const int wide = P.cols * 8;
+  for (int o = threadIdx.x; o < 2 * wide; o += blockDim.x) {
+    const int beta = o >= wide ? 1 : 0, c = o - beta * wide;
+    if (c >= channels) continue;
+    const float* at = buf + (c >> 3) * 17 + beta * 8 + (c & 7);
     float v = 0.f;
-    for (int k = 0; k < P.rows; ++k) v += buf[(k * P.cols + cx) * 17 + i];
-    ws[(i / 8) * width + (i & 7)] = v;
+#pragma unroll 8
+    for (int k = 0; k < P.rows; ++k) v += at[k * P.cols * 17];
+    ws[beta * width + c] = v;
   }
+}
+
+// Calls use(index) for a lane's share of the rows x q entries of group g in
+// [rows][cols] shared memory: a lane a row where there are many rows, else the
+// lanes along the group.
+template <typename Use>
+__device__ __forceinline__ void group_entries(const GroupNormParams& P, int g, Use use) {
+  const int lane = threadIdx.x & 31;
+  if (P.rows >= 16) {
+    for (int y = lane; y < P.rows; y += 32)
+      for (int j = 0; j < P.q; ++j) use(y, y * P.cols + g * P.q + j);
+  } else {
+    for (int y = 0; y < P.rows; ++y)
+      for (int j = lane; j < P.q; j += 32) use(y, y * P.cols + g * P.q + j);
+  }
+}
+
+// The two halves of a cluster barrier: between them a block may not touch a
+// partner's shared memory, but goes on with its own work.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 }  // namespace spb

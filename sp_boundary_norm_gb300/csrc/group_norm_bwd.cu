@@ -10,22 +10,22 @@
 
 namespace spb {
 
-constexpr int kBackTileRows = 4;    // vectors of x and dy a thread holds (tiles)
-constexpr int kBackUnitBatch = 4;   // vectors of each a thread reads at once (units)
+constexpr int kBackUnitBatch = 2;   // vectors of each of one batch (units)
 
 template <int DT, bool SHFL>
-__global__ void __launch_bounds__(kGroupThreads) group_tile_bwd_kernel(const GroupNormParams P) {
+__global__ void __launch_bounds__(SHFL ? 256 : kGroupThreads, SHFL ? 2 : 1)
+group_tile_bwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ float2 dyn2[];             // [tile rows][cols] sums, then [pairs]
   pdl_wait();
   const int cx = threadIdx.x % P.cols, ry = threadIdx.x / P.cols;
   const int slab = blockIdx.x % P.slabs;
   const int r = blockIdx.x / P.slabs % P.t;
-  const int64_t part = blockIdx.x / (P.slabs * P.t);
+  const int part = static_cast<int>(blockIdx.x) / (P.slabs * P.t);
   const int vec = slab * P.cols + cx;
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
-  const int64_t ch = static_cast<int64_t>(r) * P.c + vec * 8;
+  const int64_t ch0 = static_cast<int64_t>(r) * P.c + slab * P.cols * 8, ch = ch0 + cx * 8;
   Column<DT> col;
   col.read(P, ch, on);
   const int64_t at = static_cast<int64_t>(vec) * 8 * E;
@@ -37,59 +37,70 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_bwd_kernel(const Gro
   const int pairs = P.samples * slab_groups;
   float2* stat = dyn2 + P.rows * kBackTileRows * P.cols;
   const int group = vec / P.q;
-  float acc[16];
+  const int64_t all_rows = P.n * P.l, step = P.parts * P.samples;
+  F2 acc[8];                                   // dgamma, dbeta of the column
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
 
-  for (int64_t s0 = part * P.samples; s0 < P.n; s0 += P.parts * P.samples) {
-    const int64_t row0 = s0 * P.l;
-    const int64_t left = P.n * P.l - row0;
-    const int here = left < tile_rows ? static_cast<int>(left) : tile_rows;
-    Vec8<DT> xraw[kBackTileRows], draw[kBackTileRows];
-    float mean[kBackTileRows], rstd[kBackTileRows];
+  Vec8<DT> xraw[kBackTileRows], draw[kBackTileRows];
+  float mean_next[kBackTileRows], rstd_next[kBackTileRows];
+  auto fetch = [&](int64_t s0) {
+    const int64_t row0 = s0 * P.l, left = all_rows - row0;
+    const int here = left < tile_rows ? static_cast<int>(left < 0 ? 0 : left) : tile_rows;
 #pragma unroll
     for (int u = 0; u < kBackTileRows; ++u) {
       xraw[u] = draw[u] = Vec8<DT>{};
-      mean[u] = rstd[u] = 0.f;
+      mean_next[u] = rstd_next[u] = 0.f;
       const int row = ry + u * P.rows;
       if (on && row < here) {
         load_pack(xraw[u], x + (row0 + row) * P.ld_x);
         load_pack(draw[u], dy + (row0 + row) * P.ld_dy);
         const int64_t st = (SHFL ? row0 + row : s0 + row / static_cast<int>(P.l)) * P.groups + group;
-        if (ln) mean[u] = __ldg(P.mean[r] + st);
-        rstd[u] = __ldg(P.rstd[r] + st);
+        if (ln) mean_next[u] = __ldg(P.mean[r] + st);
+        rstd_next[u] = __ldg(P.rstd[r] + st);
       }
     }
-    float2 sum[kBackTileRows];                 // sums of dz and of dz z
+  };
+  fetch(static_cast<int64_t>(part) * P.samples);
+  for (int64_t s0 = static_cast<int64_t>(part) * P.samples; s0 < P.n; s0 += step) {
+    const int64_t row0 = s0 * P.l;
+    const int64_t left = all_rows - row0;
+    const int here = left < tile_rows ? static_cast<int>(left) : tile_rows;
+    F2 z[kBackTileRows][4], dq[kBackTileRows][4];
+    float rstd[kBackTileRows];
+    float sum[2 * kBackTileRows];              // of dz and of dz z
 #pragma unroll
     for (int u = 0; u < kBackTileRows; ++u) {
-      float f[8], d[8], z[8], dq[8];
-      unpack(xraw[u], f);
-      unpack(draw[u], d);
-      back_act<DT>(f, d, mean[u], rstd[u], col, silu, z, dq);
-      sum[u] = make_float2(0.f, 0.f);
+      unpack_pairs(xraw[u], z[u]);
+      unpack_pairs(draw[u], dq[u]);
+      rstd[u] = rstd_next[u];
+      back_act<DT>(z[u], dq[u], mean_next[u], rstd[u], col, silu);
+      F2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[i] = fmaf(dq[i], z[i], acc[i]);
-        acc[8 + i] += dq[i];
-        const float dz = dq[i] * col.gamma[i];
-        sum[u].x += dz;
-        sum[u].y = fmaf(dz, z[i], sum[u].y);
+      for (int i = 0; i < 4; ++i) {
+        acc[i] = fma2(dq[u][i], z[u][i], acc[i]);
+        acc[4 + i] = add2(acc[4 + i], dq[u][i]);
+        const F2 dz = mul2(dq[u][i], col.gamma[i]);
+        s1 = add2(s1, dz);
+        s2 = fma2(dz, z[u][i], s2);
       }
-      if constexpr (SHFL) {
-        sum[u].x = lanes_sum(sum[u].x, P.q);
-        sum[u].y = lanes_sum(sum[u].y, P.q);
-      }
+      const float2 w1 = split(s1), w2 = split(s2);
+      sum[2 * u] = w1.x + w1.y;
+      sum[2 * u + 1] = w2.x + w2.y;
     }
-    if constexpr (!SHFL) {
+    fetch(s0 + step);
+    if constexpr (SHFL) {
+      lanes_sum(sum, P.q);
+    } else {
 #pragma unroll
       for (int u = 0; u < kBackTileRows; ++u)
-        if (ry < P.rows) dyn2[(ry + u * P.rows) * P.cols + cx] = sum[u];
+        if (ry < P.rows)
+          dyn2[(ry + u * P.rows) * P.cols + cx] = make_float2(sum[2 * u], sum[2 * u + 1]);
       __syncthreads();
-      const int lane = threadIdx.x % P.lanes, step = blockDim.x / P.lanes;
-      for (int p0 = 0; p0 < pairs; p0 += step) {
+      const int lane = threadIdx.x % P.lanes, teams = blockDim.x / P.lanes;
+      for (int p0 = 0; p0 < pairs; p0 += teams) {
         const int p = p0 + threadIdx.x / P.lanes;
-        float2 v = make_float2(0.f, 0.f);
+        float v[2] = {0.f, 0.f};
         if (p < pairs) {
           const int s = p / slab_groups, g = p - s * slab_groups;
           const int terms = static_cast<int>(P.l) * P.q;
@@ -97,139 +108,145 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_bwd_kernel(const Gro
             const int i = e / P.q;
             const float2 w =
                 dyn2[(s * static_cast<int>(P.l) + i) * P.cols + g * P.q + (e - i * P.q)];
-            v.x += w.x;
-            v.y += w.y;
+            v[0] += w.x;
+            v[1] += w.y;
           }
         }
-        v.x = lanes_sum(v.x, P.lanes);
-        v.y = lanes_sum(v.y, P.lanes);
-        if (p < pairs && lane == 0) stat[p] = v;
+        lanes_sum(v, P.lanes);
+        if (p < pairs && lane == 0) stat[p] = make_float2(v[0], v[1]);
       }
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < kBackTileRows; ++u) {
         const int row = ry + u * P.rows;
-        if (row < tile_rows)
-          sum[u] = stat[row / static_cast<int>(P.l) * slab_groups + cx / P.q];
+        if (row < tile_rows) {
+          const float2 w = stat[row / static_cast<int>(P.l) * slab_groups + cx / P.q];
+          sum[2 * u] = w.x;
+          sum[2 * u + 1] = w.y;
+        }
       }
     }
 #pragma unroll
     for (int u = 0; u < kBackTileRows; ++u) {
       const int row = ry + u * P.rows;
       if (!on || row >= here) continue;
-      float f[8], d[8], z[8], dq[8];
-      unpack(xraw[u], f);
-      unpack(draw[u], d);
-      back_act<DT>(f, d, mean[u], rstd[u], col, silu, z, dq);
-      const float m1 = ln ? sum[u].x * P.count_inv : 0.f, m2 = sum[u].y * P.count_inv;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        f[i] = rstd[u] * (fmaf(dq[i], col.gamma[i], -m1) - z[i] * m2);
-      Vec8<DT> o;
-      pack(o, f);
-      store_pack(out + (row0 + row) * P.ld_out, o);
+      const float m1 = ln ? sum[2 * u] * P.count_inv : 0.f, m2 = sum[2 * u + 1] * P.count_inv;
+      store_pack(out + (row0 + row) * P.ld_out,
+                 back_out<DT>(z[u], dq[u], rstd[u], col, m1, m2));
     }
     if constexpr (!SHFL) __syncthreads();
   }
   if (P.has_params)
-    put_param_part(P, acc, reinterpret_cast<float*>(dyn2), cx, ry, on, ch, part);
+    put_param_part(P, acc, reinterpret_cast<float*>(dyn2), cx, ry, ch0, P.c - slab * P.cols * 8, part);
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kGroupThreads) group_unit_bwd_kernel(const GroupNormParams P) {
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : 2)
+group_unit_bwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
-  extern __shared__ uint4 kept[];              // [keep][x, dy][threads] vectors, then the sums
+  extern __shared__ uint4 dyn16[];             // [keep][x, dy][threads] vectors, then the sums
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  if (C > 1) cluster_sync_all();               // the partners run: their shared memory is there
+  if (C > 1) cluster_arrive();                 // waited for before the first remote store
   pdl_wait();
   const int cx = threadIdx.x % P.cols, ry = threadIdx.x / P.cols;
   int unit = static_cast<int>(blockIdx.x) / C;
   const int slab = unit % P.slabs;
   unit /= P.slabs;
   const int r = unit % P.t;
-  const int64_t sample = unit / P.t;
+  const int sample = unit / P.t;
   const int vec = slab * P.cols + cx;
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
   const int slab_groups = P.cols / P.q;
-  constexpr int kPer = E == 4 ? 2 : 1;         // 16-byte pieces of a vector
-  float2* sums = reinterpret_cast<float2*>(kept + static_cast<int64_t>(P.keep) * 2 * kPer *
-                                                      blockDim.x);
+  const Kept<DT, 2> kept(dyn16);
+  float2* sums = reinterpret_cast<float2*>(dyn16 + static_cast<int64_t>(P.keep) * 2 *
+                                                       Kept<DT, 2>::kPer * blockDim.x);
   float2* joined = sums + blockDim.x;          // [cluster][slab groups] sums of each block
   float2* stat = joined + C * slab_groups;     // [slab groups] group means of dz and dz z
-  const int64_t ch = static_cast<int64_t>(r) * P.c + vec * 8;
-  Column<DT> col;
-  col.read(P, ch, on);
-  const int64_t b0 = P.l * rank / C, b1 = P.l * (rank + 1) / C;
-  const int mine =
-      on && b1 - b0 > ry ? static_cast<int>((b1 - b0 - ry + P.rows - 1) / P.rows) : 0;
+  const int64_t ch0 = static_cast<int64_t>(r) * P.c + slab * P.cols * 8, ch = ch0 + cx * 8;
+  const Deal blocks(static_cast<int>(P.l), C);
+  const int b0 = blocks.first(rank), block_rows = blocks.count(rank);
+  const Deal lanes(block_rows, P.rows);
+  const int mine = on ? lanes.count(ry) : 0;
+  const int held = mine < P.keep ? mine : P.keep;
   const int64_t row0 = sample * P.l + b0 + ry;
   const int64_t at = static_cast<int64_t>(vec) * 8 * E;
   const char* x = P.x[r] + row0 * P.ld_x + at;
   const char* dy = P.dy[r] + row0 * P.ld_dy + at;
   char* out = P.out[r] + row0 * P.ld_out + at;
   const int64_t step_x = P.ld_x * P.rows, step_dy = P.ld_dy * P.rows, step_out = P.ld_out * P.rows;
+  const int quarter = ((held + 3) / 4 + kBackUnitBatch - 1) / kBackUnitBatch * kBackUnitBatch;
+  {
+    const char *from = x, *dfrom = dy;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
+      for (int i = k * quarter; i < to; ++i, from += step_x, dfrom += step_dy) {
+        kept.copy(i, 0, from);
+        kept.copy(i, 1, dfrom);
+      }
+      cp_async_commit();
+    }
+  }
+  Column<DT> col;
+  col.read(P, ch, on);
   float mean = 0.f, rstd = 0.f;
   if (on) {
     const int64_t g = sample * P.groups + vec / P.q;
     if (ln) mean = __ldg(P.mean[r] + g);
     rstd = __ldg(P.rstd[r] + g);
   }
-  float acc[16];
+  F2 acc[8];                                   // dgamma, dbeta of the column
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int i0 = 0; i0 < mine; i0 += kBackUnitBatch) {
+  for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
+  auto add = [&](const Vec8<DT>& xr, const Vec8<DT>& dr) {
+    F2 z[4], dq[4];
+    unpack_pairs(xr, z);
+    unpack_pairs(dr, dq);
+    back_act<DT>(z, dq, mean, rstd, col, silu);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i] = fma2(dq[i], z[i], acc[i]);
+      acc[4 + i] = add2(acc[4 + i], dq[i]);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    keep_wait(3 - k);
+    const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
+#pragma unroll 2
+    for (int i = k * quarter; i < to; ++i) add(kept.get(i, 0), kept.get(i, 1));
+  }
+  for (int i0 = held; i0 < mine; i0 += kBackUnitBatch) {
+    const char *from = x + i0 * step_x, *dfrom = dy + i0 * step_dy;
     Vec8<DT> xraw[kBackUnitBatch], draw[kBackUnitBatch];
 #pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u) {
-      xraw[u] = draw[u] = Vec8<DT>{};
+    for (int u = 0; u < kBackUnitBatch; ++u, from += step_x, dfrom += step_dy)
       if (i0 + u < mine) {
-        load_pack(xraw[u], x + (i0 + u) * step_x);
-        load_pack(draw[u], dy + (i0 + u) * step_dy);
+        load_pack(xraw[u], from);
+        load_pack(draw[u], dfrom);
       }
-    }
 #pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u) {
-      if (i0 + u >= mine) continue;
-      if (i0 + u < P.keep) {
-        uint4* to = kept + static_cast<int64_t>(i0 + u) * 2 * kPer * blockDim.x + threadIdx.x;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          to[k * blockDim.x] = make_uint4(xraw[u].w[4 * k], xraw[u].w[4 * k + 1],
-                                          xraw[u].w[4 * k + 2], xraw[u].w[4 * k + 3]);
-          to[(kPer + k) * blockDim.x] = make_uint4(draw[u].w[4 * k], draw[u].w[4 * k + 1],
-                                                   draw[u].w[4 * k + 2], draw[u].w[4 * k + 3]);
-        }
-      }
-      float f[8], d[8], z[8], dq[8];
-      unpack(xraw[u], f);
-      unpack(draw[u], d);
-      back_act<DT>(f, d, mean, rstd, col, silu, z, dq);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[i] = fmaf(dq[i], z[i], acc[i]);
-        acc[8 + i] += dq[i];
-      }
-    }
+    for (int u = 0; u < kBackUnitBatch; ++u)
+      if (i0 + u < mine) add(xraw[u], draw[u]);
   }
-  float2 own = make_float2(0.f, 0.f);
+  F2 own1 = both(0.f), own2 = both(0.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    own.x = fmaf(col.gamma[i], acc[8 + i], own.x);
-    own.y = fmaf(col.gamma[i], acc[i], own.y);
+  for (int i = 0; i < 4; ++i) {
+    own1 = fma2(col.gamma[i], acc[4 + i], own1);
+    own2 = fma2(col.gamma[i], acc[i], own2);
   }
-  if (ry < P.rows) sums[threadIdx.x] = own;
+  const float2 w1 = split(own1), w2 = split(own2);
+  if (ry < P.rows) sums[threadIdx.x] = make_float2(w1.x + w1.y, w2.x + w2.y);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int terms = P.rows * P.q;
+  if (C > 1) cluster_wait();                   // the partners run: their shared memory is there
   for (int g = warp; g < slab_groups; g += nw) {
     float2 v = make_float2(0.f, 0.f);
-    for (int e = lane; e < terms; e += 32) {
-      const int y = e / P.q;
-      const float2 w = sums[y * P.cols + g * P.q + (e - y * P.q)];
-      v.x += w.x;
-      v.y += w.y;
-    }
+    group_entries(P, g, [&](int, int at) {
+      v.x += sums[at].x;
+      v.y += sums[at].y;
+    });
     v.x = warp_sum(v.x);
     v.y = warp_sum(v.y);
     if (C == 1) {
@@ -251,48 +268,31 @@ __global__ void __launch_bounds__(kGroupThreads) group_unit_bwd_kernel(const Gro
   }
   __syncthreads();
   const float2 m = stat[cx / P.q];
-  for (int i0 = 0; i0 < mine; i0 += kBackUnitBatch) {
+  auto finish = [&](const Vec8<DT>& xr, const Vec8<DT>& dr, char* to) {
+    F2 z[4], dq[4];
+    unpack_pairs(xr, z);
+    unpack_pairs(dr, dq);
+    back_act<DT>(z, dq, mean, rstd, col, silu);
+    store_pack(to, back_out<DT>(z, dq, rstd, col, m.x, m.y));
+  };
+#pragma unroll 2
+  for (int i = 0; i < held; ++i, out += step_out) finish(kept.get(i, 0), kept.get(i, 1), out);
+  for (int i0 = held; i0 < mine; i0 += kBackUnitBatch) {
+    const char *from = x + i0 * step_x, *dfrom = dy + i0 * step_dy;
     Vec8<DT> xraw[kBackUnitBatch], draw[kBackUnitBatch];
 #pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u) {
-      const int i = i0 + u;
-      if (i >= mine) continue;
-      if (i < P.keep) {
-        const uint4* from = kept + static_cast<int64_t>(i) * 2 * kPer * blockDim.x + threadIdx.x;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const uint4 v = from[k * blockDim.x], w = from[(kPer + k) * blockDim.x];
-          xraw[u].w[4 * k] = v.x;
-          xraw[u].w[4 * k + 1] = v.y;
-          xraw[u].w[4 * k + 2] = v.z;
-          xraw[u].w[4 * k + 3] = v.w;
-          draw[u].w[4 * k] = w.x;
-          draw[u].w[4 * k + 1] = w.y;
-          draw[u].w[4 * k + 2] = w.z;
-          draw[u].w[4 * k + 3] = w.w;
-        }
-      } else {
-        load_pack(xraw[u], x + i * step_x);
-        load_pack(draw[u], dy + i * step_dy);
+    for (int u = 0; u < kBackUnitBatch; ++u, from += step_x, dfrom += step_dy)
+      if (i0 + u < mine) {
+        load_pack(xraw[u], from);
+        load_pack(draw[u], dfrom);
       }
-    }
 #pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u) {
-      if (i0 + u >= mine) continue;
-      float f[8], d[8], z[8], dq[8];
-      unpack(xraw[u], f);
-      unpack(draw[u], d);
-      back_act<DT>(f, d, mean, rstd, col, silu, z, dq);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        f[i] = rstd * (fmaf(dq[i], col.gamma[i], -m.x) - z[i] * m.y);
-      Vec8<DT> o;
-      pack(o, f);
-      store_pack(out + (i0 + u) * step_out, o);
-    }
+    for (int u = 0; u < kBackUnitBatch; ++u, out += step_out)
+      if (i0 + u < mine) finish(xraw[u], draw[u], out);
   }
   if (P.has_params)
-    put_param_part(P, acc, reinterpret_cast<float*>(kept), cx, ry, on, ch, sample * C + rank);
+    put_param_part(P, acc, reinterpret_cast<float*>(dyn16), cx, ry, ch0, P.c - slab * P.cols * 8,
+                   static_cast<int64_t>(sample) * C + rank);
 }
 
 // dgamma / dbeta: the parts added in order, one warp lane a channel, eight
@@ -329,7 +329,10 @@ static cudaError_t run_bwd(GroupNormParams* p, cudaStream_t st, int dtype) {
   const GroupShape s = group_norm_shape(p->n, p->l, p->c, p->groups, p->t, dtype, true);
   const void* tile = s.shuffle ? reinterpret_cast<const void*>(&group_tile_bwd_kernel<DT, true>)
                                : reinterpret_cast<const void*>(&group_tile_bwd_kernel<DT, false>);
-  return launch_group(tile, reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT>), p, s, st);
+  const void* unit = s.threads > 256
+                         ? reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT, true>)
+                         : reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT, false>);
+  return launch_group(tile, unit, p, s, st);
 }
 
 cudaError_t launch_group_norm_bwd(GroupNormParams p, int dtype, float* dgamma, float* dbeta,

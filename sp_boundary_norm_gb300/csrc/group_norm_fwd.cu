@@ -4,20 +4,22 @@
 
 namespace spb {
 
-constexpr int kTileRows = 4;    // vectors a thread holds (tiles)
-constexpr int kUnitBatch = 8;   // vectors a thread reads at once (units)
+constexpr int kUnitBatch = 4;       // vectors of one batch (units)
+constexpr int kFwdUnitBlocks = 3;   // blocks an SM that the registers are held to
 
 // SHFL: one row a sample and a power of two up to 32 vectors a group: the sums
-// stay within neighbouring lanes.  Else through shared memory.
+// stay within neighbouring lanes (blocks of at most 256 threads).  Else through
+// shared memory.  The next tile's vectors are read while this one's are used.
 template <int DT, bool SHFL>
-__global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const GroupNormParams P) {
+__global__ void __launch_bounds__(SHFL ? 256 : kGroupThreads, SHFL ? 3 : 1)
+group_tile_fwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ float dyn[];               // [tile rows][cols] sums, then [pairs] statistics
   pdl_wait();
   const int cx = threadIdx.x % P.cols, ry = threadIdx.x / P.cols;
   const int slab = blockIdx.x % P.slabs;
   const int r = blockIdx.x / P.slabs % P.t;
-  const int64_t part = blockIdx.x / (P.slabs * P.t);
+  const int part = static_cast<int>(blockIdx.x) / (P.slabs * P.t);
   const int vec = slab * P.cols + cx;
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
@@ -30,19 +32,30 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
   const int pairs = P.samples * slab_groups;
   float* stat = dyn + P.rows * kTileRows * P.cols;     // mean then rstd of each pair
   const int group = vec / P.q;
+  const int64_t all_rows = P.n * P.l, step = P.parts * P.samples;
 
-  for (int64_t s0 = part * P.samples; s0 < P.n; s0 += P.parts * P.samples) {
-    const int64_t row0 = s0 * P.l;
-    const int64_t left = P.n * P.l - row0;
-    const int here = left < tile_rows ? static_cast<int>(left) : tile_rows;
-    Vec8<DT> raw[kTileRows];
-    float mean[kTileRows], rstd[kTileRows];
+  Vec8<DT> raw[kTileRows];
+  auto fetch = [&](int64_t s0) {
+    const char* at = x + s0 * P.l * P.ld_x;
+    const int64_t left = all_rows - s0 * P.l;
+    const int here = left < tile_rows ? static_cast<int>(left < 0 ? 0 : left) : tile_rows;
 #pragma unroll
     for (int u = 0; u < kTileRows; ++u) {
-      raw[u] = Vec8<DT>{};
       const int row = ry + u * P.rows;
-      if (on && row < here) load_pack(raw[u], x + (row0 + row) * P.ld_x);
+      raw[u] = Vec8<DT>{};
+      if (on && row < here) load_pack(raw[u], at + row * P.ld_x);
     }
+  };
+  fetch(static_cast<int64_t>(part) * P.samples);
+  for (int64_t s0 = static_cast<int64_t>(part) * P.samples; s0 < P.n; s0 += step) {
+    const int64_t row0 = s0 * P.l;
+    const int64_t left = all_rows - row0;
+    const int here = left < tile_rows ? static_cast<int>(left) : tile_rows;
+    F2 v[kTileRows][4];
+#pragma unroll
+    for (int u = 0; u < kTileRows; ++u) unpack_pairs(raw[u], v[u]);
+    fetch(s0 + step);
+    float mean[kTileRows], rstd[kTileRows];
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
       // pass 0: the mean (LayerNorm); pass 1: the mean square around it
@@ -53,36 +66,35 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
       }
       float sum[kTileRows];
 #pragma unroll
-      for (int u = 0; u < kTileRows; ++u) {
-        float f[8];
-        unpack(raw[u], f);
-        sum[u] = 0.f;
+      for (int u = 0; u < kTileRows; ++u)
+        sum[u] = pass == 0 ? pair_sum(v[u]) : spread_sum(v[u], mean[u]);
+      if constexpr (SHFL) {
+        lanes_sum(sum, P.q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float d = pass == 0 ? f[i] : f[i] - mean[u];
-          sum[u] = pass == 0 ? sum[u] + d : fmaf(d, d, sum[u]);
+        for (int u = 0; u < kTileRows; ++u) {
+          if (pass == 0) mean[u] = sum[u] * P.count_inv;
+          else rstd[u] = rsqrtf(sum[u] * P.count_inv + P.eps);
         }
-        if constexpr (SHFL) sum[u] = lanes_sum(sum[u], P.q);
-      }
-      if constexpr (!SHFL) {
+      } else {
+        // (vectors that do not exist hold zeros, not part of any group's sum)
 #pragma unroll
         for (int u = 0; u < kTileRows; ++u)
           if (ry < P.rows) dyn[(ry + u * P.rows) * P.cols + cx] = sum[u];
         __syncthreads();
-        const int lane = threadIdx.x % P.lanes, step = blockDim.x / P.lanes;
-        for (int p0 = 0; p0 < pairs; p0 += step) {
+        const int lane = threadIdx.x % P.lanes, teams = blockDim.x / P.lanes;
+        for (int p0 = 0; p0 < pairs; p0 += teams) {
           const int p = p0 + threadIdx.x / P.lanes;
-          float v = 0.f;
+          float w = 0.f;
           if (p < pairs) {
             const int s = p / slab_groups, g = p - s * slab_groups;
             const int terms = static_cast<int>(P.l) * P.q;
             for (int e = lane; e < terms; e += P.lanes) {
               const int i = e / P.q;
-              v += dyn[(s * static_cast<int>(P.l) + i) * P.cols + g * P.q + (e - i * P.q)];
+              w += dyn[(s * static_cast<int>(P.l) + i) * P.cols + g * P.q + (e - i * P.q)];
             }
           }
-          v = lanes_sum(v, P.lanes) * P.count_inv;
-          if (p < pairs && lane == 0) stat[pass * pairs + p] = pass == 0 ? v : rsqrtf(v + P.eps);
+          w = lanes_sum(w, P.lanes) * P.count_inv;
+          if (p < pairs && lane == 0) stat[pass * pairs + p] = pass == 0 ? w : rsqrtf(w + P.eps);
         }
         __syncthreads();
 #pragma unroll
@@ -92,25 +104,16 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
                             ? row / static_cast<int>(P.l) * slab_groups + cx / P.q : 0;
           (pass == 0 ? mean : rstd)[u] = stat[pass * pairs + p];
         }
-      } else {
-#pragma unroll
-        for (int u = 0; u < kTileRows; ++u) {
-          if (pass == 0) mean[u] = sum[u] * P.count_inv;
-          else rstd[u] = rsqrtf(sum[u] * P.count_inv + P.eps);
-        }
       }
     }
+    char* to = out + row0 * P.ld_out;
 #pragma unroll
     for (int u = 0; u < kTileRows; ++u) {
       const int row = ry + u * P.rows;
       if (!on || row >= here) continue;
-      float f[8];
-      unpack(raw[u], f);
-      Vec8<DT> o;
-      norm_act<DT>(f, mean[u], rstd[u], col, silu, o);
-      store_pack(out + (row0 + row) * P.ld_out, o);
-      if (vec % P.q == 0 && row % P.l == 0) {
-        const int64_t at = (s0 + row / static_cast<int>(P.l)) * P.groups + group;
+      store_pack(to + row * P.ld_out, norm_act<DT>(v[u], mean[u], rstd[u], col, silu));
+      if (vec % P.q == 0 && (SHFL || row % static_cast<int>(P.l) == 0)) {
+        const int64_t at = (s0 + (SHFL ? row : row / static_cast<int>(P.l))) * P.groups + group;
         if (ln) P.mean[r][at] = mean[u];
         P.rstd[r][at] = rstd[u];
       }
@@ -119,107 +122,117 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
   }
 }
 
-// One cluster per (sample, rank, slab).
-template <int DT>
-__global__ void __launch_bounds__(kGroupThreads) group_unit_fwd_kernel(const GroupNormParams P) {
+// One cluster per (sample, rank, slab).  A thread's first `keep` vectors are
+// all asked for at once, into its own slots of shared memory, and are used from
+// there twice; what does not fit is read twice.  WIDE: groups of more than 256
+// vectors, blocks of up to 512 threads.
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kFwdUnitBlocks)
+group_unit_fwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
-  extern __shared__ uint4 kept[];              // [keep][threads] vectors, then the sums below
+  extern __shared__ uint4 dyn16[];             // [keep][threads] vectors, then the sums below
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  if (C > 1) cluster_sync_all();               // the partners run: their shared memory is there
+  if (C > 1) cluster_arrive();                 // waited for before the first remote store
   pdl_wait();
   const int cx = threadIdx.x % P.cols, ry = threadIdx.x / P.cols;
   int unit = static_cast<int>(blockIdx.x) / C;
   const int slab = unit % P.slabs;
   unit /= P.slabs;
   const int r = unit % P.t;
-  const int64_t sample = unit / P.t;
+  const int sample = unit / P.t;
   const int vec = slab * P.cols + cx;
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
   const int slab_groups = P.cols / P.q;
-  constexpr int kPer = E == 4 ? 2 : 1;         // 16-byte pieces of a vector
-  float2* sums = reinterpret_cast<float2*>(kept + static_cast<int64_t>(P.keep) * kPer * blockDim.x);
+  const Kept<DT, 1> kept(dyn16);
+  float2* sums = reinterpret_cast<float2*>(dyn16 + static_cast<int64_t>(P.keep) *
+                                                       Kept<DT, 1>::kPer * blockDim.x);
   float2* joined = sums + blockDim.x;          // [cluster][slab groups] mean, M2 of each block
   float2* stat = joined + C * slab_groups;     // [slab groups] mean, rstd
-  Column<DT> col;
-  col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
   // this block's rows of the sample, and this thread's: ry, ry + rows, ...
-  const int64_t b0 = P.l * rank / C, b1 = P.l * (rank + 1) / C;
-  const int mine = b1 - b0 > ry ? static_cast<int>((b1 - b0 - ry + P.rows - 1) / P.rows) : 0;
+  const Deal blocks(static_cast<int>(P.l), C);
+  const int b0 = blocks.first(rank), block_rows = blocks.count(rank);
+  const Deal lanes(block_rows, P.rows);
+  const int mine = on ? lanes.count(ry) : 0;
+  const int held = mine < P.keep ? mine : P.keep;
   const int64_t row0 = sample * P.l + b0 + ry;
   const char* x = P.x[r] + row0 * P.ld_x + static_cast<int64_t>(vec) * 8 * E;
   char* out = P.out[r] + row0 * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
   const int64_t step_x = P.ld_x * P.rows, step_out = P.ld_out * P.rows;
+  const int quarter = ((held + 3) / 4 + kUnitBatch - 1) / kUnitBatch * kUnitBatch;
+  {
+    const char* from = x;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
+      for (int i = k * quarter; i < to; ++i, from += step_x) kept.copy(i, 0, from);
+      cp_async_commit();
+    }
+  }
+  Column<DT> col;
+  col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
 
   // (count, mean, M2) of the thread's values, batch by batch
   float cnt = 0.f, mean = 0.f, m2 = 0.f;
-  for (int i0 = 0; on && i0 < mine; i0 += kUnitBatch) {
-    Vec8<DT> raw[kUnitBatch];
+  auto batch = [&](const Vec8<DT> (&raw)[kUnitBatch], int nb) {
+    F2 v[kUnitBatch][4];
+    F2 s2 = both(0.f);
 #pragma unroll
     for (int u = 0; u < kUnitBatch; ++u) {
-      raw[u] = Vec8<DT>{};
-      if (i0 + u < mine) load_pack(raw[u], x + (i0 + u) * step_x);
+      unpack_pairs(raw[u], v[u]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s2 = add2(s2, v[u][i]);
     }
-    const int nb = (mine - i0 < kUnitBatch ? mine - i0 : kUnitBatch);
-    float s = 0.f;
-#pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u) {
-      float f[8];
-      unpack(raw[u], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += f[i];
-      if (i0 + u < P.keep && u < nb) {
-        uint4* to = kept + static_cast<int64_t>(i0 + u) * kPer * blockDim.x + threadIdx.x;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          to[k * blockDim.x] = make_uint4(raw[u].w[4 * k], raw[u].w[4 * k + 1],
-                                          raw[u].w[4 * k + 2], raw[u].w[4 * k + 3]);
-      }
-    }
-    const float nf = 8.f * static_cast<float>(nb);
-    const float mb = ln ? __fdividef(s, nf) : 0.f;
+    const float2 sw = split(s2);
+    const float nf = 8.f * static_cast<float>(nb), all = cnt + nf;
+    const float mb = ln ? __fdividef(sw.x + sw.y, nf) : 0.f;
     float q2 = 0.f;
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u) {
-      if (u < nb) {
-        float f[8];
-        unpack(raw[u], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float d = f[i] - mb;
-          q2 = fmaf(d, d, q2);
-        }
-      }
-    }
-    const float d = mb - mean, all = cnt + nf;
-    mean += d * __fdividef(nf, all);
-    m2 += q2 + d * d * __fdividef(cnt * nf, all);
+    for (int u = 0; u < kUnitBatch; ++u)
+      if (u < nb) q2 += spread_sum(v[u], mb);
+    const float d = mb - mean, part = __fdividef(nf, all);
+    mean = fmaf(d, part, mean);
+    m2 += fmaf(d * d, cnt * part, q2);
     cnt = all;
+  };
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    keep_wait(3 - k);
+    const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
+    for (int i0 = k * quarter; i0 < to; i0 += kUnitBatch) {
+      Vec8<DT> raw[kUnitBatch];
+#pragma unroll
+      for (int u = 0; u < kUnitBatch; ++u) {
+        raw[u] = Vec8<DT>{};
+        if (i0 + u < to) raw[u] = kept.get(i0 + u, 0);
+      }
+      batch(raw, to - i0 < kUnitBatch ? to - i0 : kUnitBatch);
+    }
+  }
+  for (int i0 = held; i0 < mine; i0 += kUnitBatch) {
+    const char* from = x + i0 * step_x;
+    Vec8<DT> raw[kUnitBatch];
+#pragma unroll
+    for (int u = 0; u < kUnitBatch; ++u, from += step_x) {
+      raw[u] = Vec8<DT>{};
+      if (i0 + u < mine) load_pack(raw[u], from);
+    }
+    batch(raw, mine - i0 < kUnitBatch ? mine - i0 : kUnitBatch);
   }
   // the block's mean and M2 of each group of the slab, one warp a group
   if (ry < P.rows) sums[threadIdx.x] = make_float2(mean, m2);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int terms = P.rows * P.q;
-  auto rows_of = [&](int y) {
-    return b1 - b0 > y ? static_cast<float>((b1 - b0 - y + P.rows - 1) / P.rows) * 8.f : 0.f;
-  };
-  const float block_count = static_cast<float>(b1 - b0) * 8.f * P.q;
+  const float block_count = static_cast<float>(block_rows) * 8.f * P.q;
+  if (C > 1) cluster_wait();                   // the partners run: their shared memory is there
   for (int g = warp; g < slab_groups; g += nw) {
-    float s = 0.f;
-    if (ln)
-      for (int e = lane; e < terms; e += 32) {
-        const int y = e / P.q;
-        s += rows_of(y) * sums[y * P.cols + g * P.q + (e - y * P.q)].x;
-      }
+    float s = 0.f, v = 0.f;
+    if (ln) group_entries(P, g, [&](int y, int at) { s += 8.f * lanes.count(y) * sums[at].x; });
     const float m = block_count > 0.f ? warp_sum(s) / block_count : 0.f;
-    float v = 0.f;
-    for (int e = lane; e < terms; e += 32) {
-      const int y = e / P.q;
-      const float2 w = sums[y * P.cols + g * P.q + (e - y * P.q)];
-      const float d = w.x - m;
-      v += w.y + rows_of(y) * d * d;
-    }
+    group_entries(P, g, [&](int y, int at) {
+      const float d = sums[at].x - m;
+      v += sums[at].y + 8.f * lanes.count(y) * d * d;
+    });
     v = warp_sum(v);
     if (C == 1) {
       if (lane == 0) joined[g] = make_float2(m, v);
@@ -233,13 +246,12 @@ __global__ void __launch_bounds__(kGroupThreads) group_unit_fwd_kernel(const Gro
   for (int g = threadIdx.x; g < slab_groups; g += blockDim.x) {
     float m = 0.f, v = 0.f;
     for (int k = 0; k < C; ++k)
-      m += joined[k * slab_groups + g].x *
-           static_cast<float>(P.l * (k + 1) / C - P.l * k / C);
+      m += joined[k * slab_groups + g].x * static_cast<float>(blocks.count(k));
     m /= static_cast<float>(P.l);
     for (int k = 0; k < C; ++k) {
       const float2 w = joined[k * slab_groups + g];
       const float d = w.x - m;
-      v += w.y + static_cast<float>(P.l * (k + 1) / C - P.l * k / C) * 8.f * P.q * d * d;
+      v += w.y + static_cast<float>(blocks.count(k)) * 8.f * P.q * d * d;
     }
     const float2 st = make_float2(m, rsqrtf(v * P.count_inv + P.eps));
     stat[g] = st;
@@ -252,34 +264,24 @@ __global__ void __launch_bounds__(kGroupThreads) group_unit_fwd_kernel(const Gro
   __syncthreads();
   if (!on) return;
   const float2 st = stat[cx / P.q];
-  for (int i0 = 0; i0 < mine; i0 += kUnitBatch) {
+#pragma unroll 2
+  for (int i = 0; i < held; ++i, out += step_out) {
+    F2 v[4];
+    unpack_pairs(kept.get(i, 0), v);
+    store_pack(out, norm_act<DT>(v, st.x, st.y, col, silu));
+  }
+  for (int i0 = held; i0 < mine; i0 += kUnitBatch) {
+    const char* from = x + i0 * step_x;
     Vec8<DT> raw[kUnitBatch];
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u) {
-      const int i = i0 + u;
-      if (i >= mine) continue;
-      if (i < P.keep) {
-        const uint4* from = kept + static_cast<int64_t>(i) * kPer * blockDim.x + threadIdx.x;
+    for (int u = 0; u < kUnitBatch; ++u, from += step_x)
+      if (i0 + u < mine) load_pack(raw[u], from);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const uint4 v = from[k * blockDim.x];
-          raw[u].w[4 * k] = v.x;
-          raw[u].w[4 * k + 1] = v.y;
-          raw[u].w[4 * k + 2] = v.z;
-          raw[u].w[4 * k + 3] = v.w;
-        }
-      } else {
-        load_pack(raw[u], x + i * step_x);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u) {
+    for (int u = 0; u < kUnitBatch; ++u, out += step_out) {
       if (i0 + u >= mine) continue;
-      float f[8];
-      unpack(raw[u], f);
-      Vec8<DT> o;
-      norm_act<DT>(f, st.x, st.y, col, silu, o);
-      store_pack(out + (i0 + u) * step_out, o);
+      F2 v[4];
+      unpack_pairs(raw[u], v);
+      store_pack(out, norm_act<DT>(v, st.x, st.y, col, silu));
     }
   }
 }
@@ -291,7 +293,7 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   const int size = dtype == SP_F32 ? 4 : 2;
   const int nvec = c / 8, q = nvec / groups;
   const int sms = device_sm_count();
-  // tiles while a block of up to 256 threads holds a whole sample in its registers
+  const int held_rows = bwd ? kBackTileRows : kTileRows;
   auto fit_cols = [&](int most) {
     int g = most / q;
     if (g < 1) g = 1;
@@ -299,56 +301,67 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     s.cols = g * q;
     s.slabs = div_up(groups, g);
   };
+  // tiles while a block of up to 256 threads holds a whole sample in its registers
   fit_cols(256);
   s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
-  if (l > static_cast<int64_t>(s.rows) * kTileRows && l <= 64 && q <= 32) {
+  if (l > static_cast<int64_t>(s.rows) * held_rows && l <= 16 * held_rows && q <= 32) {
     fit_cols(32);     // fewer columns abreast: more rows of a sample in one block
     s.rows = 256 / s.cols;
   }
-  s.tile = l <= static_cast<int64_t>(s.rows) * kTileRows;
+  s.tile = l <= static_cast<int64_t>(s.rows) * held_rows;
   s.cluster = 1;
   if (s.tile) {
     s.threads = (s.rows * s.cols + 31) / 32 * 32;
     s.shuffle = l == 1 && q <= 32 && (q & (q - 1)) == 0;
-    s.samples = static_cast<int>(s.rows * kTileRows / l);
+    s.samples = static_cast<int>(s.rows * held_rows / l);
     // fewer samples a tile while that leaves SMs without one
-    while (s.samples > 1 && s.rows > 1 &&
-           static_cast<int64_t>(s.slabs) * t * div_up(n, s.samples) < 2 * sms) {
+    while (s.samples > 1 && static_cast<int64_t>(s.slabs) * t * div_up(n, s.samples) < 2 * sms)
       s.samples = (s.samples + 1) / 2;
-    }
     const int64_t tiles = (n + s.samples - 1) / s.samples;
-    const int64_t cap = (static_cast<int64_t>(sms) * 8 + s.slabs * t - 1) / (s.slabs * t);
-    s.parts = tiles < cap ? tiles : cap;
+    const int resident = s.shuffle ? (bwd ? 2 : 3) * 256 / s.threads : 2;
+    const int64_t cap = (static_cast<int64_t>(sms) * resident) / (s.slabs * t);
+    s.parts = cap < 1 ? 1 : tiles < cap ? tiles : cap;
     const int pairs = s.samples * (s.cols / q);
     s.lanes = 1;
     while (s.lanes < 32 && s.lanes < l * q && pairs * s.lanes < s.threads) s.lanes *= 2;
     const int sums = bwd ? 2 : 1;
     s.smem = s.shuffle ? 0
-                       : (static_cast<size_t>(s.rows) * kTileRows * s.cols * sums + 2 * pairs) * 4;
+                       : (static_cast<size_t>(s.rows) * held_rows * s.cols * sums + 2 * pairs) * 4;
     if (bwd) {
       const size_t part = static_cast<size_t>(s.rows) * s.cols * 17 * 4;
       if (s.smem < part) s.smem = part;
     }
     return s;
   }
-  // units: narrow slabs (at least 128 bytes of a row), many rows abreast
-  fit_cols(q >= 8 ? q : 16);
+  // units: narrow slabs of at least 128 bytes of a row, whole 32-byte sectors
+  // where that takes two groups at most, and many rows abreast
+  fit_cols(q >= 8 ? q : (8 + q - 1) / q * q);
+  if (s.cols % 2 != 0 && 2 * s.cols <= nvec) fit_cols(2 * s.cols);
   s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
   s.threads = (s.rows * s.cols + 31) / 32 * 32;
-  const int64_t units = n * t * s.slabs;
-  while (s.cluster < kGroupMaxCluster && units * s.cluster < 4 * sms &&
-         static_cast<int64_t>(s.rows) * kUnitBatch * s.cluster < l)
-    s.cluster *= 2;
-  const int64_t need = (l + static_cast<int64_t>(s.rows) * s.cluster - 1) /
-                       (static_cast<int64_t>(s.rows) * s.cluster);
+  // the fewest blocks a cluster that keep a sample's slab in shared memory with
+  // `resident` blocks on an SM, and give every SM its blocks
   const int slab_groups = s.cols / q;
+  const size_t vec = static_cast<size_t>(s.threads) * 8 * size * (bwd ? 2 : 1);
+  const int resident = bwd ? 2 : 3;
+  const size_t room = (bwd ? 100 : 66) * 1024;
+  auto need = [&](int cl) {
+    const int64_t per = (l + cl - 1) / cl;
+    return (per + s.rows - 1) / s.rows;
+  };
+  static const int kClusters[] = {1, 2, 3, 4, 6, 8, 10, 12, kGroupMaxCluster};
+  for (int cl : kClusters) {
+    if (cl > l) break;
+    s.cluster = cl;
+    if (need(cl) * vec <= room && (n * t * s.slabs * cl >= resident * sms || need(cl) <= kUnitBatch))
+      break;
+  }
   const size_t fixed = static_cast<size_t>(s.threads) * 8 +
                        static_cast<size_t>(s.cluster + 1) * slab_groups * 8;
-  const size_t vec = static_cast<size_t>(s.threads) * 8 * size * (bwd ? 2 : 1);
-  size_t room = 100 * 1024;
-  if (room < fixed) room = fixed;
-  int64_t keep = static_cast<int64_t>((room - fixed) / vec);
-  if (keep > need) keep = need;
+  int64_t keep = need(s.cluster);
+  // what is not kept is read again: up to a whole SM's memory a block then
+  const size_t most = need(s.cluster) * vec > room ? 110 * 1024 : room + fixed;
+  if (keep * vec + fixed > most) keep = most > fixed ? static_cast<int64_t>((most - fixed) / vec) : 0;
   s.keep = static_cast<int>(keep);
   s.smem = s.keep * vec + fixed;
   if (bwd) {
@@ -376,13 +389,13 @@ cudaError_t launch_group(const void* tile, const void* unit, GroupNormParams* p,
   fill_shape(p, s);
   void* args[] = {p};
   const void* fn = s.tile ? tile : unit;
-  cudaError_t e = ensure_smem_attr(fn, s.smem);
-  if (e == cudaSuccess && s.cluster > 8)
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  int fit = 0;
+  const cudaError_t e = s.tile ? ensure_smem_attr(fn, s.smem)
+                               : max_clusters(fn, s.threads, s.smem, s.cluster, &fit);
   if (e != cudaSuccess) return e;
   const int64_t blocks = static_cast<int64_t>(s.slabs) * p->t *
                          (s.tile ? s.parts : p->n * s.cluster);
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  if ((!s.tile && fit < 1) || blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_pdl(fn, dim3(static_cast<unsigned>(blocks)), dim3(s.threads), s.smem, args, st,
                     s.cluster);
 }
@@ -392,7 +405,10 @@ static cudaError_t run_fwd(GroupNormParams* p, cudaStream_t st, int dtype) {
   const GroupShape s = group_norm_shape(p->n, p->l, p->c, p->groups, p->t, dtype, false);
   const void* tile = s.shuffle ? reinterpret_cast<const void*>(&group_tile_fwd_kernel<DT, true>)
                                : reinterpret_cast<const void*>(&group_tile_fwd_kernel<DT, false>);
-  return launch_group(tile, reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT>), p, s, st);
+  const void* unit = s.threads > 256
+                         ? reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT, true>)
+                         : reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT, false>);
+  return launch_group(tile, unit, p, s, st);
 }
 
 cudaError_t launch_group_norm_fwd(GroupNormParams p, int dtype, cudaStream_t st) {

@@ -112,6 +112,55 @@ __device__ __forceinline__ void pack(Pack<DT, N>& p, const float (&f)[N]) {
   }
 }
 
+// Packed pairs of floats: one instruction for both.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// N elements as N / 2 pairs, and back (each rounded once).
+template <int DT, int N>
+__device__ __forceinline__ void unpack_pairs(const Pack<DT, N>& p, F2 (&v)[N / 2]) {
+  float f[N];
+  unpack(p, f);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+template <int DT, int N>
+__device__ __forceinline__ void pack_pairs(Pack<DT, N>& p, const F2 (&v)[N / 2]) {
+  float f[N];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 w = split(v[i]);
+    f[2 * i] = w.x;
+    f[2 * i + 1] = w.y;
+  }
+  pack(p, f);
+}
+
 // The packed sequence of token `tok`: the largest j < n with cu[j] <= tok (the
 // last of several sequences that begin there: the others are empty).  One
 // warp, 32 probes a step; in bounds whatever cu holds.

@@ -19,6 +19,15 @@ namespace spb {
 constexpr int kRopeWarps = 8;
 constexpr int kRopeUnroll = 4;
 
+// a / b for 0 <= a < most: in 32 bits where they do (a 64-bit division costs a
+// hundred instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t most) {
+  if (b == 1) return a;
+  if (b >= most) return 0;
+  if (most <= 0x7FFFFFFF) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // V elements a load.  Half layout: a lane's item is V pairs (V elements of
 // each half).  Interleaved: V / 2 pairs that lie together, or for V = 1 one
 // pair by two loads.
@@ -45,7 +54,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
   const int64_t n_tasks = P.tokens * P.chunks;
   for (int64_t task = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; task < n_tasks;
        task += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
-    const int64_t tok = P.chunks == 1 ? task : task / P.chunks;
+    const int64_t tok = divide(task, P.chunks, n_tasks);
     const int chunk = static_cast<int>(task - tok * P.chunks);
     const int h0 = chunk * P.chunk_heads;
     const int h1 = h0 + P.chunk_heads < P.all_heads ? h0 + P.chunk_heads : P.all_heads;
@@ -55,7 +64,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
     } else if (P.cu_seqlens != nullptr) {
       pos = tok - __ldg(P.cu_seqlens + seq_of_token(P.cu_seqlens, P.n_seqs, tok)) + P.first;
     } else {
-      pos = (P.tokens == P.s ? tok : tok % P.s) + P.first;
+      pos = tok - divide(tok, P.s, P.tokens) * P.s + P.first;
     }
     __syncwarp();
     for (int i = lane; i < P.half; i += 32) {
