@@ -3,8 +3,10 @@
 //   one sample,  q = z gamma + beta,  y = q or q sigmoid(q).
 //
 // A thread owns one vector of 8 channels (its column; all of one group) and
-// walks rows, so the parameters and their gradients stay in registers.  Two
+// walks rows, so the parameters and their gradients stay in registers.  Three
 // forms, by the size of a sample:
+//  - rows: samples of one row (the per-token norm of heads); a warp, or for wide
+//    groups the warps of a group, takes whole groups of several rows at once;
 //  - tiles: a block takes whole samples of few rows; every thread holds its
 //    vectors in registers between the statistics and the result;
 //  - units: a cluster of blocks takes one sample's slab of groups, keeps the
@@ -23,8 +25,16 @@ namespace spb {
 template <int DT>
 using Vec8 = Pack<DT, 8>;
 
-constexpr int kTileRows = 4;        // vectors a thread holds (tiles, forward)
-constexpr int kBackTileRows = 2;    // of x and of dy (tiles, backward)
+constexpr int kTileRows = 4;        // vectors a thread holds (rows, tiles; forward)
+constexpr int kBackTileRows = 2;    // of x and of dy (rows, tiles; backward)
+constexpr int kRowWarps = 8;        // of a block (rows), more for groups beyond 256 vectors
+constexpr int kRowMaxWarps = kGroupThreads / 32;
+
+// How the lanes of a group add up (rows form): a power of two of neighbouring
+// lanes by shuffles; other widths up to 31 through the warp's shared memory,
+// every lane adding its group's values; wider groups in their warps, then over
+// the warps (a team) through shared memory.
+constexpr int kSumLanes = 0, kSumWarp = 1, kSumTeam = 2;
 
 __device__ __forceinline__ F2 both(float v) { return f2(v, v); }
 
@@ -236,6 +246,53 @@ __device__ __forceinline__ void put_param_part(const GroupNormParams& P, const F
     ws[beta * width + c] = v;
   }
 }
+
+template <int MODE, int N>
+struct RowSums {
+  float values[MODE == kSumWarp ? kRowWarps : MODE == kSumTeam ? kRowMaxWarps : 1]
+              [MODE == kSumWarp ? N : MODE == kSumTeam ? 2 * N : 1][MODE == kSumWarp ? 32 : 1];
+};
+
+// Sums v over the lanes (and warps) of the calling thread's group.
+template <int MODE, int N>
+struct RowGroup {
+  RowSums<MODE, N>* sh;
+  int q, warp, first_lane;            // first_lane: of the group (kSumWarp)
+  int team_warps, team, parity = 0;   // kSumTeam
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (MODE == kSumLanes) {
+      lanes_sum(v, q);
+    } else if constexpr (MODE == kSumWarp) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        sh->values[warp][i][lane] = v[i];
+        v[i] = 0.f;
+      }
+      __syncwarp();
+      for (int j = 0; j < q; ++j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += sh->values[warp][i][first_lane + j];
+      }
+    } else {
+      lanes_sum(v, 32);
+      const int at = parity * N;      // two buffers: the next sum may begin at once
+      parity ^= 1;
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sh->values[warp][at + i][0] = v[i];
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(team_warps * 32) : "memory");
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.f;
+      for (int w = 0; w < team_warps; ++w) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += sh->values[team * team_warps + w][at + i][0];
+      }
+    }
+  }
+};
 
 // Calls use(index) for a lane's share of the rows x q entries of group g in
 // [rows][cols] shared memory: a lane a row where there are many rows, else the

@@ -12,9 +12,113 @@ namespace spb {
 
 constexpr int kBackUnitBatch = 2;   // vectors of each of one batch (units)
 
-template <int DT, bool SHFL>
-__global__ void __launch_bounds__(SHFL ? 256 : kGroupThreads, SHFL ? 2 : 1)
-group_tile_bwd_kernel(const GroupNormParams P) {
+// z and dq in place of a vector's x and dy, its parts of the column's parameter
+// gradients added to acc; its sums of dz and of dz z.
+template <int DT>
+__device__ __forceinline__ void back_vector(F2 (&z)[4], F2 (&dq)[4], float mean, float rstd,
+                                            const Column<DT>& col, bool silu, F2 (&acc)[8],
+                                            float& sum1, float& sum2) {
+  back_act<DT>(z, dq, mean, rstd, col, silu);
+  F2 s1 = both(0.f), s2 = both(0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[i] = fma2(dq[i], z[i], acc[i]);
+    acc[4 + i] = add2(acc[4 + i], dq[i]);
+    const F2 dz = mul2(dq[i], col.gamma[i]);
+    s1 = add2(s1, dz);
+    s2 = fma2(dz, z[i], s2);
+  }
+  const float2 w1 = split(s1), w2 = split(s2);
+  sum1 = w1.x + w1.y;
+  sum2 = w2.x + w2.y;
+}
+
+// Rows (as in the forward).
+template <int DT, int MODE>
+__global__ void __launch_bounds__(MODE == kSumTeam ? kGroupThreads : 32 * kRowWarps,
+                                  MODE == kSumTeam ? 1 : 2)
+group_row_bwd_kernel(const GroupNormParams P) {
+  constexpr int E = ElemSize<DT>::value;
+  extern __shared__ float2 dyn2[];             // the parameter gradients' parts
+  __shared__ RowSums<MODE, 2 * kBackTileRows> sh;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team_warps = MODE == kSumTeam ? (P.cols + 31) / 32 : 1;
+  const int team = warp / team_warps, cx = (warp - team * team_warps) * 32 + lane;
+  const int slab = blockIdx.x % P.slabs;
+  const int r = blockIdx.x / P.slabs % P.t;
+  const int part = static_cast<int>(blockIdx.x) / (P.slabs * P.t);
+  const int vec = slab * P.cols + cx;
+  const bool on = cx < P.cols && vec * 8 < P.c;
+  const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
+  const int in_slab = cx < P.cols ? cx / P.q : 0;
+  RowGroup<MODE, 2 * kBackTileRows> group{&sh, P.q, warp, in_slab * P.q, team_warps, team};
+  const int64_t ch0 = static_cast<int64_t>(r) * P.c + slab * P.cols * 8, ch = ch0 + cx * 8;
+  Column<DT> col;
+  col.read(P, ch, on);
+  const int64_t at = static_cast<int64_t>(vec) * 8 * E;
+  const int64_t first = (static_cast<int64_t>(part) * P.rows + team) * kBackTileRows;
+  const int64_t step = P.parts * P.rows * kBackTileRows;
+  const char* x = P.x[r] + first * P.ld_x + at;
+  const char* dy = P.dy[r] + first * P.ld_dy + at;
+  char* out = P.out[r] + first * P.ld_out + at;
+  const float* mean_at = ln ? P.mean[r] + first * P.groups + vec / P.q : nullptr;
+  const float* rstd_at = P.rstd[r] + first * P.groups + vec / P.q;
+  const int64_t step_x = step * P.ld_x, step_dy = step * P.ld_dy, step_out = step * P.ld_out;
+  const int64_t step_stat = step * P.groups;
+  F2 acc[8];                                   // dgamma, dbeta of the column
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
+
+  Vec8<DT> xraw[kBackTileRows], draw[kBackTileRows];
+  float mean_next[kBackTileRows], rstd_next[kBackTileRows];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int u = 0; u < kBackTileRows; ++u) {
+      xraw[u] = draw[u] = Vec8<DT>{};
+      mean_next[u] = rstd_next[u] = 0.f;
+      if (on && row + u < P.n) {
+        load_pack(xraw[u], x + u * P.ld_x);
+        load_pack(draw[u], dy + u * P.ld_dy);
+        if (ln) mean_next[u] = __ldg(mean_at + u * P.groups);
+        rstd_next[u] = __ldg(rstd_at + u * P.groups);
+      }
+    }
+    x += step_x;
+    dy += step_dy;
+    if (ln) mean_at += step_stat;
+    rstd_at += step_stat;
+  };
+  fetch(first);
+  for (int64_t row = first; row < P.n; row += step, out += step_out) {
+    F2 z[kBackTileRows][4], dq[kBackTileRows][4];
+    float rstd[kBackTileRows];
+    float sum[2 * kBackTileRows];              // of dz and of dz z
+#pragma unroll
+    for (int u = 0; u < kBackTileRows; ++u) {
+      unpack_pairs(xraw[u], z[u]);
+      unpack_pairs(draw[u], dq[u]);
+      rstd[u] = rstd_next[u];
+      back_vector<DT>(z[u], dq[u], mean_next[u], rstd[u], col, silu, acc, sum[2 * u],
+                      sum[2 * u + 1]);
+    }
+    fetch(row + step);
+    group.sum(sum);
+#pragma unroll
+    for (int u = 0; u < kBackTileRows; ++u) {
+      if (!on || row + u >= P.n) continue;
+      const float m1 = ln ? sum[2 * u] * P.count_inv : 0.f, m2 = sum[2 * u + 1] * P.count_inv;
+      store_pack(out + u * P.ld_out, back_out<DT>(z[u], dq[u], rstd[u], col, m1, m2));
+    }
+  }
+  if (P.has_params)
+    put_param_part(P, acc, reinterpret_cast<float*>(dyn2), cx, on ? team : P.rows, ch0,
+                   P.c - slab * P.cols * 8, part);
+}
+
+// Tiles: samples of a few rows.
+template <int DT>
+__global__ void __launch_bounds__(kGroupThreads) group_tile_bwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ float2 dyn2[];             // [tile rows][cols] sums, then [pairs]
   pdl_wait();
@@ -32,12 +136,19 @@ group_tile_bwd_kernel(const GroupNormParams P) {
   const char* x = P.x[r] + at;
   const char* dy = P.dy[r] + at;
   char* out = P.out[r] + at;
-  const int tile_rows = static_cast<int>(P.samples * P.l);
+  const int l = static_cast<int>(P.l), tile_rows = P.samples * l;
   const int slab_groups = P.cols / P.q;
   const int pairs = P.samples * slab_groups;
   float2* stat = dyn2 + P.rows * kBackTileRows * P.cols;
   const int group = vec / P.q;
   const int64_t all_rows = P.n * P.l, step = P.parts * P.samples;
+  int pair[kBackTileRows], sample[kBackTileRows];
+#pragma unroll
+  for (int u = 0; u < kBackTileRows; ++u) {
+    const int row = ry + u * P.rows;
+    sample[u] = row / l;
+    pair[u] = row < tile_rows ? sample[u] * slab_groups + cx / P.q : 0;
+  }
   F2 acc[8];                                   // dgamma, dbeta of the column
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
@@ -55,89 +166,62 @@ group_tile_bwd_kernel(const GroupNormParams P) {
       if (on && row < here) {
         load_pack(xraw[u], x + (row0 + row) * P.ld_x);
         load_pack(draw[u], dy + (row0 + row) * P.ld_dy);
-        const int64_t st = (SHFL ? row0 + row : s0 + row / static_cast<int>(P.l)) * P.groups + group;
+        const int64_t st = (s0 + sample[u]) * P.groups + group;
         if (ln) mean_next[u] = __ldg(P.mean[r] + st);
         rstd_next[u] = __ldg(P.rstd[r] + st);
       }
     }
   };
-  fetch(static_cast<int64_t>(part) * P.samples);
-  for (int64_t s0 = static_cast<int64_t>(part) * P.samples; s0 < P.n; s0 += step) {
+  const int64_t s_first = static_cast<int64_t>(part) * P.samples;
+  fetch(s_first);
+  for (int64_t s0 = s_first; s0 < P.n; s0 += step) {
     const int64_t row0 = s0 * P.l;
     const int64_t left = all_rows - row0;
     const int here = left < tile_rows ? static_cast<int>(left) : tile_rows;
     F2 z[kBackTileRows][4], dq[kBackTileRows][4];
     float rstd[kBackTileRows];
-    float sum[2 * kBackTileRows];              // of dz and of dz z
 #pragma unroll
     for (int u = 0; u < kBackTileRows; ++u) {
       unpack_pairs(xraw[u], z[u]);
       unpack_pairs(draw[u], dq[u]);
       rstd[u] = rstd_next[u];
-      back_act<DT>(z[u], dq[u], mean_next[u], rstd[u], col, silu);
-      F2 s1 = both(0.f), s2 = both(0.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] = fma2(dq[u][i], z[u][i], acc[i]);
-        acc[4 + i] = add2(acc[4 + i], dq[u][i]);
-        const F2 dz = mul2(dq[u][i], col.gamma[i]);
-        s1 = add2(s1, dz);
-        s2 = fma2(dz, z[u][i], s2);
-      }
-      const float2 w1 = split(s1), w2 = split(s2);
-      sum[2 * u] = w1.x + w1.y;
-      sum[2 * u + 1] = w2.x + w2.y;
+      float2 sum;
+      back_vector<DT>(z[u], dq[u], mean_next[u], rstd[u], col, silu, acc, sum.x, sum.y);
+      if (ry < P.rows) dyn2[(ry + u * P.rows) * P.cols + cx] = sum;
     }
     fetch(s0 + step);
-    if constexpr (SHFL) {
-      lanes_sum(sum, P.q);
-    } else {
-#pragma unroll
-      for (int u = 0; u < kBackTileRows; ++u)
-        if (ry < P.rows)
-          dyn2[(ry + u * P.rows) * P.cols + cx] = make_float2(sum[2 * u], sum[2 * u + 1]);
-      __syncthreads();
-      const int lane = threadIdx.x % P.lanes, teams = blockDim.x / P.lanes;
-      for (int p0 = 0; p0 < pairs; p0 += teams) {
-        const int p = p0 + threadIdx.x / P.lanes;
-        float v[2] = {0.f, 0.f};
-        if (p < pairs) {
-          const int s = p / slab_groups, g = p - s * slab_groups;
-          const int terms = static_cast<int>(P.l) * P.q;
-          for (int e = lane; e < terms; e += P.lanes) {
-            const int i = e / P.q;
-            const float2 w =
-                dyn2[(s * static_cast<int>(P.l) + i) * P.cols + g * P.q + (e - i * P.q)];
-            v[0] += w.x;
-            v[1] += w.y;
+    __syncthreads();
+    const int lane = threadIdx.x % P.lanes, teams = blockDim.x / P.lanes;
+    for (int p0 = 0; p0 < pairs; p0 += teams) {
+      const int p = p0 + threadIdx.x / P.lanes;
+      float v[2] = {0.f, 0.f};
+      if (p < pairs) {
+        const int s = p / slab_groups;
+        const float2* from = dyn2 + s * l * P.cols + (p - s * slab_groups) * P.q;
+        for (int i = 0; i < l; ++i, from += P.cols)
+          for (int j = lane; j < P.q; j += P.lanes) {
+            v[0] += from[j].x;
+            v[1] += from[j].y;
           }
-        }
-        lanes_sum(v, P.lanes);
-        if (p < pairs && lane == 0) stat[p] = make_float2(v[0], v[1]);
       }
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kBackTileRows; ++u) {
-        const int row = ry + u * P.rows;
-        if (row < tile_rows) {
-          const float2 w = stat[row / static_cast<int>(P.l) * slab_groups + cx / P.q];
-          sum[2 * u] = w.x;
-          sum[2 * u + 1] = w.y;
-        }
-      }
+      lanes_sum(v, P.lanes);
+      if (p < pairs && lane == 0) stat[p] = make_float2(v[0], v[1]);
     }
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < kBackTileRows; ++u) {
       const int row = ry + u * P.rows;
       if (!on || row >= here) continue;
-      const float m1 = ln ? sum[2 * u] * P.count_inv : 0.f, m2 = sum[2 * u + 1] * P.count_inv;
+      const float2 w = stat[pair[u]];
+      const float m1 = ln ? w.x * P.count_inv : 0.f, m2 = w.y * P.count_inv;
       store_pack(out + (row0 + row) * P.ld_out,
                  back_out<DT>(z[u], dq[u], rstd[u], col, m1, m2));
     }
-    if constexpr (!SHFL) __syncthreads();
+    __syncthreads();                           // the next tile's sums replace these
   }
   if (P.has_params)
-    put_param_part(P, acc, reinterpret_cast<float*>(dyn2), cx, ry, ch0, P.c - slab * P.cols * 8, part);
+    put_param_part(P, acc, reinterpret_cast<float*>(dyn2), cx, ry, ch0, P.c - slab * P.cols * 8,
+                   part);
 }
 
 template <int DT, bool WIDE>
@@ -325,22 +409,24 @@ __global__ void __launch_bounds__(256) group_params_kernel(const float* ws, int6
 }
 
 template <int DT>
-static cudaError_t run_bwd(GroupNormParams* p, cudaStream_t st, int dtype) {
-  const GroupShape s = group_norm_shape(p->n, p->l, p->c, p->groups, p->t, dtype, true);
-  const void* tile = s.shuffle ? reinterpret_cast<const void*>(&group_tile_bwd_kernel<DT, true>)
-                               : reinterpret_cast<const void*>(&group_tile_bwd_kernel<DT, false>);
-  const void* unit = s.threads > 256
-                         ? reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT, true>)
+static const void* bwd_fn(const GroupShape& s) {
+  if (s.form == kRowForm)
+    return s.mode == kSumLanes  ? reinterpret_cast<const void*>(&group_row_bwd_kernel<DT, kSumLanes>)
+           : s.mode == kSumWarp ? reinterpret_cast<const void*>(&group_row_bwd_kernel<DT, kSumWarp>)
+                                : reinterpret_cast<const void*>(&group_row_bwd_kernel<DT, kSumTeam>);
+  if (s.form == kTileForm) return reinterpret_cast<const void*>(&group_tile_bwd_kernel<DT>);
+  return s.threads > 256 ? reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT, true>)
                          : reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT, false>);
-  return launch_group(tile, unit, p, s, st);
 }
 
 cudaError_t launch_group_norm_bwd(GroupNormParams p, int dtype, float* dgamma, float* dbeta,
                                   cudaStream_t st) {
   p.has_params = dgamma != nullptr || dbeta != nullptr;
-  cudaError_t e = dtype == SP_BF16  ? run_bwd<SP_BF16>(&p, st, dtype)
-                  : dtype == SP_F16 ? run_bwd<SP_F16>(&p, st, dtype)
-                                    : run_bwd<SP_F32>(&p, st, dtype);
+  const GroupShape s = group_norm_shape(p.n, p.l, p.c, p.groups, p.t, dtype, true);
+  const void* fn = dtype == SP_BF16  ? bwd_fn<SP_BF16>(s)
+                   : dtype == SP_F16 ? bwd_fn<SP_F16>(s)
+                                     : bwd_fn<SP_F32>(s);
+  const cudaError_t e = launch_group(fn, &p, s, st);
   if (e != cudaSuccess || !p.has_params) return e;
   const float* ws = p.ws;
   int64_t parts = p.parts, width = static_cast<int64_t>(p.t) * p.c;

@@ -7,12 +7,83 @@ namespace spb {
 constexpr int kUnitBatch = 4;       // vectors of one batch (units)
 constexpr int kFwdUnitBlocks = 3;   // blocks an SM that the registers are held to
 
-// SHFL: one row a sample and a power of two up to 32 vectors a group: the sums
-// stay within neighbouring lanes (blocks of at most 256 threads).  Else through
-// shared memory.  The next tile's vectors are read while this one's are used.
-template <int DT, bool SHFL>
-__global__ void __launch_bounds__(SHFL ? 256 : kGroupThreads, SHFL ? 3 : 1)
-group_tile_fwd_kernel(const GroupNormParams P) {
+// Rows: a team takes kTileRows rows of its slab at a time; the next ones are on
+// their way meanwhile.
+template <int DT, int MODE>
+__global__ void __launch_bounds__(MODE == kSumTeam ? kGroupThreads : 32 * kRowWarps,
+                                  MODE == kSumTeam ? 1 : 3)
+group_row_fwd_kernel(const GroupNormParams P) {
+  constexpr int E = ElemSize<DT>::value;
+  __shared__ RowSums<MODE, kTileRows> sh;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team_warps = MODE == kSumTeam ? (P.cols + 31) / 32 : 1;
+  const int team = warp / team_warps, cx = (warp - team * team_warps) * 32 + lane;
+  const int slab = blockIdx.x % P.slabs;
+  const int r = blockIdx.x / P.slabs % P.t;
+  const int part = static_cast<int>(blockIdx.x) / (P.slabs * P.t);
+  const int vec = slab * P.cols + cx;
+  const bool on = cx < P.cols && vec * 8 < P.c;
+  const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
+  const int in_slab = cx < P.cols ? cx / P.q : 0;
+  RowGroup<MODE, kTileRows> group{&sh, P.q, warp, in_slab * P.q, team_warps, team};
+  Column<DT> col;
+  col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
+  const bool tells = on && cx == in_slab * P.q;          // writes its group's statistics
+  const int64_t stat = vec / P.q;
+  const int64_t first = (static_cast<int64_t>(part) * P.rows + team) * kTileRows;
+  const int64_t step = P.parts * P.rows * kTileRows;
+  const char* x = P.x[r] + first * P.ld_x + static_cast<int64_t>(vec) * 8 * E;
+  char* out = P.out[r] + first * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
+  const int64_t step_x = step * P.ld_x, step_out = step * P.ld_out;
+
+  Vec8<DT> raw[kTileRows];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int u = 0; u < kTileRows; ++u) {
+      raw[u] = Vec8<DT>{};
+      if (on && row + u < P.n) load_pack(raw[u], x + u * P.ld_x);
+    }
+    x += step_x;
+  };
+  fetch(first);
+  for (int64_t row = first; row < P.n; row += step, out += step_out) {
+    F2 v[kTileRows][4];
+#pragma unroll
+    for (int u = 0; u < kTileRows; ++u) unpack_pairs(raw[u], v[u]);
+    fetch(row + step);
+    float mean[kTileRows], rstd[kTileRows];
+#pragma unroll
+    for (int u = 0; u < kTileRows; ++u) mean[u] = 0.f;
+    if (ln) {
+#pragma unroll
+      for (int u = 0; u < kTileRows; ++u) mean[u] = pair_sum(v[u]);
+      group.sum(mean);
+#pragma unroll
+      for (int u = 0; u < kTileRows; ++u) mean[u] *= P.count_inv;
+    }
+    // (lanes that hold no vector hold zeros: they add nothing)
+#pragma unroll
+    for (int u = 0; u < kTileRows; ++u) rstd[u] = on ? spread_sum(v[u], mean[u]) : 0.f;
+    group.sum(rstd);
+#pragma unroll
+    for (int u = 0; u < kTileRows; ++u) rstd[u] = rsqrtf(rstd[u] * P.count_inv + P.eps);
+#pragma unroll
+    for (int u = 0; u < kTileRows; ++u) {
+      if (!on || row + u >= P.n) continue;
+      store_pack(out + u * P.ld_out, norm_act<DT>(v[u], mean[u], rstd[u], col, silu));
+      if (tells) {
+        const int64_t at = (row + u) * P.groups + stat;
+        if (ln) P.mean[r][at] = mean[u];
+        P.rstd[r][at] = rstd[u];
+      }
+    }
+  }
+}
+
+// Tiles: samples of a few rows.
+template <int DT>
+__global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ float dyn[];               // [tile rows][cols] sums, then [pairs] statistics
   pdl_wait();
@@ -27,12 +98,20 @@ group_tile_fwd_kernel(const GroupNormParams P) {
   col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
   const char* x = P.x[r] + static_cast<int64_t>(vec) * 8 * E;
   char* out = P.out[r] + static_cast<int64_t>(vec) * 8 * E;
-  const int tile_rows = static_cast<int>(P.samples * P.l);
+  const int l = static_cast<int>(P.l), tile_rows = P.samples * l;
   const int slab_groups = P.cols / P.q;
   const int pairs = P.samples * slab_groups;
   float* stat = dyn + P.rows * kTileRows * P.cols;     // mean then rstd of each pair
   const int group = vec / P.q;
   const int64_t all_rows = P.n * P.l, step = P.parts * P.samples;
+  int pair[kTileRows];                         // of this thread's rows; 0 for none
+  bool leads[kTileRows];                       // the first row and column of a pair
+#pragma unroll
+  for (int u = 0; u < kTileRows; ++u) {
+    const int row = ry + u * P.rows, s = row / l;
+    pair[u] = row < tile_rows ? s * slab_groups + cx / P.q : 0;
+    leads[u] = vec % P.q == 0 && row == s * l;
+  }
 
   Vec8<DT> raw[kTileRows];
   auto fetch = [&](int64_t s0) {
@@ -46,8 +125,9 @@ group_tile_fwd_kernel(const GroupNormParams P) {
       if (on && row < here) load_pack(raw[u], at + row * P.ld_x);
     }
   };
-  fetch(static_cast<int64_t>(part) * P.samples);
-  for (int64_t s0 = static_cast<int64_t>(part) * P.samples; s0 < P.n; s0 += step) {
+  const int64_t s_first = static_cast<int64_t>(part) * P.samples;
+  fetch(s_first);
+  for (int64_t s0 = s_first; s0 < P.n; s0 += step) {
     const int64_t row0 = s0 * P.l;
     const int64_t left = all_rows - row0;
     const int here = left < tile_rows ? static_cast<int>(left) : tile_rows;
@@ -57,54 +137,33 @@ group_tile_fwd_kernel(const GroupNormParams P) {
     fetch(s0 + step);
     float mean[kTileRows], rstd[kTileRows];
 #pragma unroll
+    for (int u = 0; u < kTileRows; ++u) mean[u] = 0.f;
+#pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
       // pass 0: the mean (LayerNorm); pass 1: the mean square around it
-      if (pass == 0 && !ln) {
-#pragma unroll
-        for (int u = 0; u < kTileRows; ++u) mean[u] = 0.f;
-        continue;
-      }
-      float sum[kTileRows];
+      if (pass == 0 && !ln) continue;
 #pragma unroll
       for (int u = 0; u < kTileRows; ++u)
-        sum[u] = pass == 0 ? pair_sum(v[u]) : spread_sum(v[u], mean[u]);
-      if constexpr (SHFL) {
-        lanes_sum(sum, P.q);
-#pragma unroll
-        for (int u = 0; u < kTileRows; ++u) {
-          if (pass == 0) mean[u] = sum[u] * P.count_inv;
-          else rstd[u] = rsqrtf(sum[u] * P.count_inv + P.eps);
+        if (ry < P.rows)
+          dyn[(ry + u * P.rows) * P.cols + cx] =
+              pass == 0 ? pair_sum(v[u]) : spread_sum(v[u], mean[u]);
+      __syncthreads();
+      const int lane = threadIdx.x % P.lanes, teams = blockDim.x / P.lanes;
+      for (int p0 = 0; p0 < pairs; p0 += teams) {
+        const int p = p0 + threadIdx.x / P.lanes;
+        float w = 0.f;
+        if (p < pairs) {
+          const int s = p / slab_groups;
+          const float* at = dyn + s * l * P.cols + (p - s * slab_groups) * P.q;
+          for (int i = 0; i < l; ++i, at += P.cols)
+            for (int j = lane; j < P.q; j += P.lanes) w += at[j];
         }
-      } else {
-        // (vectors that do not exist hold zeros, not part of any group's sum)
-#pragma unroll
-        for (int u = 0; u < kTileRows; ++u)
-          if (ry < P.rows) dyn[(ry + u * P.rows) * P.cols + cx] = sum[u];
-        __syncthreads();
-        const int lane = threadIdx.x % P.lanes, teams = blockDim.x / P.lanes;
-        for (int p0 = 0; p0 < pairs; p0 += teams) {
-          const int p = p0 + threadIdx.x / P.lanes;
-          float w = 0.f;
-          if (p < pairs) {
-            const int s = p / slab_groups, g = p - s * slab_groups;
-            const int terms = static_cast<int>(P.l) * P.q;
-            for (int e = lane; e < terms; e += P.lanes) {
-              const int i = e / P.q;
-              w += dyn[(s * static_cast<int>(P.l) + i) * P.cols + g * P.q + (e - i * P.q)];
-            }
-          }
-          w = lanes_sum(w, P.lanes) * P.count_inv;
-          if (p < pairs && lane == 0) stat[pass * pairs + p] = pass == 0 ? w : rsqrtf(w + P.eps);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kTileRows; ++u) {
-          const int row = ry + u * P.rows;
-          const int p = row < tile_rows
-                            ? row / static_cast<int>(P.l) * slab_groups + cx / P.q : 0;
-          (pass == 0 ? mean : rstd)[u] = stat[pass * pairs + p];
-        }
+        w = lanes_sum(w, P.lanes) * P.count_inv;
+        if (p < pairs && lane == 0) stat[pass * pairs + p] = pass == 0 ? w : rsqrtf(w + P.eps);
       }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kTileRows; ++u) (pass == 0 ? mean : rstd)[u] = stat[pass * pairs + pair[u]];
     }
     char* to = out + row0 * P.ld_out;
 #pragma unroll
@@ -112,13 +171,13 @@ group_tile_fwd_kernel(const GroupNormParams P) {
       const int row = ry + u * P.rows;
       if (!on || row >= here) continue;
       store_pack(to + row * P.ld_out, norm_act<DT>(v[u], mean[u], rstd[u], col, silu));
-      if (vec % P.q == 0 && (SHFL || row % static_cast<int>(P.l) == 0)) {
-        const int64_t at = (s0 + (SHFL ? row : row / static_cast<int>(P.l))) * P.groups + group;
+      if (leads[u]) {
+        const int64_t at = (s0 + row / l) * P.groups + group;
         if (ln) P.mean[r][at] = mean[u];
         P.rstd[r][at] = rstd[u];
       }
     }
-    if constexpr (!SHFL) __syncthreads();   // the next tile's sums replace this one's statistics
+    __syncthreads();                           // the next tile's sums replace this one's statistics
   }
 }
 
@@ -301,6 +360,21 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     s.cols = g * q;
     s.slabs = div_up(groups, g);
   };
+  s.cluster = 1;
+  if (l == 1) {
+    // rows: whole groups of up to 32 vectors a warp, wider ones a team of warps
+    s.form = kRowForm;
+    s.mode = q > 32 ? kSumTeam : (q & (q - 1)) == 0 ? kSumLanes : kSumWarp;
+    fit_cols(32);
+    const int team = (s.cols + 31) / 32;
+    s.rows = team < kRowWarps ? kRowWarps / team : 1;
+    s.threads = s.rows * team * 32;
+    const int64_t tiles = div_up(n, static_cast<int64_t>(s.rows) * held_rows);
+    const int64_t cap = static_cast<int64_t>(sms) * (bwd ? 2 : 3) / (s.slabs * t);
+    s.parts = cap < 1 ? 1 : tiles < cap ? tiles : cap;
+    s.smem = bwd ? static_cast<size_t>(s.rows) * s.cols * 17 * 4 : 0;
+    return s;
+  }
   // tiles while a block of up to 256 threads holds a whole sample in its registers
   fit_cols(256);
   s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
@@ -308,31 +382,28 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     fit_cols(32);     // fewer columns abreast: more rows of a sample in one block
     s.rows = 256 / s.cols;
   }
-  s.tile = l <= static_cast<int64_t>(s.rows) * held_rows;
-  s.cluster = 1;
-  if (s.tile) {
+  if (l <= static_cast<int64_t>(s.rows) * held_rows) {
+    s.form = kTileForm;
     s.threads = (s.rows * s.cols + 31) / 32 * 32;
-    s.shuffle = l == 1 && q <= 32 && (q & (q - 1)) == 0;
     s.samples = static_cast<int>(s.rows * held_rows / l);
     // fewer samples a tile while that leaves SMs without one
     while (s.samples > 1 && static_cast<int64_t>(s.slabs) * t * div_up(n, s.samples) < 2 * sms)
       s.samples = (s.samples + 1) / 2;
     const int64_t tiles = (n + s.samples - 1) / s.samples;
-    const int resident = s.shuffle ? (bwd ? 2 : 3) * 256 / s.threads : 2;
-    const int64_t cap = (static_cast<int64_t>(sms) * resident) / (s.slabs * t);
+    const int64_t cap = static_cast<int64_t>(sms) * 2 / (s.slabs * t);
     s.parts = cap < 1 ? 1 : tiles < cap ? tiles : cap;
     const int pairs = s.samples * (s.cols / q);
     s.lanes = 1;
-    while (s.lanes < 32 && s.lanes < l * q && pairs * s.lanes < s.threads) s.lanes *= 2;
+    while (s.lanes < 32 && s.lanes < q && pairs * s.lanes < s.threads) s.lanes *= 2;
     const int sums = bwd ? 2 : 1;
-    s.smem = s.shuffle ? 0
-                       : (static_cast<size_t>(s.rows) * held_rows * s.cols * sums + 2 * pairs) * 4;
+    s.smem = (static_cast<size_t>(s.rows) * held_rows * s.cols * sums + 2 * pairs) * 4;
     if (bwd) {
       const size_t part = static_cast<size_t>(s.rows) * s.cols * 17 * 4;
       if (s.smem < part) s.smem = part;
     }
     return s;
   }
+  s.form = kUnitForm;
   // units: narrow slabs of at least 128 bytes of a row, whole 32-byte sectors
   // where that takes two groups at most, and many rows abreast
   fit_cols(q >= 8 ? q : (8 + q - 1) / q * q);
@@ -384,37 +455,37 @@ static void fill_shape(GroupNormParams* p, const GroupShape& s) {
   p->keep = s.keep;
 }
 
-cudaError_t launch_group(const void* tile, const void* unit, GroupNormParams* p,
-                         const GroupShape& s, cudaStream_t st) {
+cudaError_t launch_group(const void* fn, GroupNormParams* p, const GroupShape& s, cudaStream_t st) {
   fill_shape(p, s);
   void* args[] = {p};
-  const void* fn = s.tile ? tile : unit;
-  int fit = 0;
-  const cudaError_t e = s.tile ? ensure_smem_attr(fn, s.smem)
-                               : max_clusters(fn, s.threads, s.smem, s.cluster, &fit);
+  int fit = 1;
+  const bool unit = s.form == kUnitForm;
+  const cudaError_t e = unit ? max_clusters(fn, s.threads, s.smem, s.cluster, &fit)
+                             : ensure_smem_attr(fn, s.smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = static_cast<int64_t>(s.slabs) * p->t *
-                         (s.tile ? s.parts : p->n * s.cluster);
-  if ((!s.tile && fit < 1) || blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const int64_t blocks = static_cast<int64_t>(s.slabs) * p->t * (unit ? p->n * s.cluster : s.parts);
+  if (fit < 1 || blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_pdl(fn, dim3(static_cast<unsigned>(blocks)), dim3(s.threads), s.smem, args, st,
                     s.cluster);
 }
 
 template <int DT>
-static cudaError_t run_fwd(GroupNormParams* p, cudaStream_t st, int dtype) {
-  const GroupShape s = group_norm_shape(p->n, p->l, p->c, p->groups, p->t, dtype, false);
-  const void* tile = s.shuffle ? reinterpret_cast<const void*>(&group_tile_fwd_kernel<DT, true>)
-                               : reinterpret_cast<const void*>(&group_tile_fwd_kernel<DT, false>);
-  const void* unit = s.threads > 256
-                         ? reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT, true>)
+static const void* fwd_fn(const GroupShape& s) {
+  if (s.form == kRowForm)
+    return s.mode == kSumLanes  ? reinterpret_cast<const void*>(&group_row_fwd_kernel<DT, kSumLanes>)
+           : s.mode == kSumWarp ? reinterpret_cast<const void*>(&group_row_fwd_kernel<DT, kSumWarp>)
+                                : reinterpret_cast<const void*>(&group_row_fwd_kernel<DT, kSumTeam>);
+  if (s.form == kTileForm) return reinterpret_cast<const void*>(&group_tile_fwd_kernel<DT>);
+  return s.threads > 256 ? reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT, true>)
                          : reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT, false>);
-  return launch_group(tile, unit, p, s, st);
 }
 
 cudaError_t launch_group_norm_fwd(GroupNormParams p, int dtype, cudaStream_t st) {
-  if (dtype == SP_BF16) return run_fwd<SP_BF16>(&p, st, dtype);
-  if (dtype == SP_F16) return run_fwd<SP_F16>(&p, st, dtype);
-  return run_fwd<SP_F32>(&p, st, dtype);
+  const GroupShape s = group_norm_shape(p.n, p.l, p.c, p.groups, p.t, dtype, false);
+  const void* fn = dtype == SP_BF16  ? fwd_fn<SP_BF16>(s)
+                   : dtype == SP_F16 ? fwd_fn<SP_F16>(s)
+                                     : fwd_fn<SP_F32>(s);
+  return launch_group(fn, &p, s, st);
 }
 
 }  // namespace spb

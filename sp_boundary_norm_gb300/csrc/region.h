@@ -89,17 +89,17 @@ struct GroupNormParams {
 };
 
 // The split of a call (see GroupNormParams).
+constexpr int kRowForm = 0, kTileForm = 1, kUnitForm = 2;
 struct GroupShape {
+  int form, mode;
   int cols, slabs, rows, threads, samples, lanes, cluster, keep;
   int64_t parts;
-  bool tile, shuffle;
   size_t smem;
 };
 
 GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int dtype, bool bwd);
-// Launches the tile or the unit kernel of a direction, filling p's split.
-cudaError_t launch_group(const void* tile, const void* unit, GroupNormParams* p,
-                         const GroupShape& s, cudaStream_t st);
+// Launches a form's kernel, filling p's split.
+cudaError_t launch_group(const void* fn, GroupNormParams* p, const GroupShape& s, cudaStream_t st);
 cudaError_t launch_group_norm_fwd(GroupNormParams p, int dtype, cudaStream_t st);
 cudaError_t launch_group_norm_bwd(GroupNormParams p, int dtype, float* dgamma, float* dbeta,
                                   cudaStream_t st);
