@@ -8,6 +8,7 @@ the library is not built, ``load()`` raises.
 """
 import contextlib
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -565,30 +566,63 @@ def sp_norm_bwd_noalloc(dy, z, mask, mean, rstd, gamma, dz_skip=None, *, s, p, c
 # of a wider buffer: the last dimension is contiguous, and the leading ones
 # follow each other with one stride between rows, the same for every rank.
 
-def _row_stride(x, what):
-    """Elements between the rows of x (rows = every dimension but the last)."""
-    if x.is_contiguous():
-        return x.shape[-1]
-    st, sh = x.stride(), x.shape
-    if sh[-1] > 1 and st[-1] != 1:
+def _dense(shape, strides):
+    """Whether strides are those of a contiguous tensor."""
+    step = 1
+    for n, stride in zip(reversed(shape), reversed(strides)):
+        if n != 1 and stride != step:
+            return 0 in shape
+        step *= n
+    return True
+
+
+def _row_stride(shape, strides, what):
+    """Elements between the rows (every dimension but the last)."""
+    if _dense(shape, strides):
+        return shape[-1]
+    if shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     ld, span = None, 1
-    for n, stride in zip(reversed(sh[:-1]), reversed(st[:-1])):
+    for n, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
         if ld is None:
             ld = stride
         elif stride != ld * span:
-            raise ValueError(f"{what}: rows of strides {st} do not follow each other evenly")
+            raise ValueError(f"{what}: rows of strides {tuple(strides)} do not follow each other "
+                             "evenly")
         span *= n
-    return sh[-1] if ld is None else ld
+    return shape[-1] if ld is None else ld
+
+
+_module = None
+
+
+def _matching(xs, shape, dtype, device):
+    """Pointer array and common strides of rank buffers, or None where they are not
+    all tensors of that shape and type on that device with equal strides."""
+    global _module
+    if _module is None:
+        if not os.path.exists(_build.MODULE_PATH):
+            raise RuntimeError(f"{_build.MODULE_PATH} is missing: build the library first")
+        spec = importlib.util.spec_from_file_location("_sptensors", _build.MODULE_PATH)
+        _module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_module)
+    return _module.same(xs, shape, DTYPES[dtype], -1 if device.index is None else device.index)
+
+
+def _pointers(xs):
+    return (_vp * len(xs))(*[x.data_ptr() for x in xs])
 
 
 def _rank_rows(xs, shape, dtype, device, t, what):
     """Pointer array and row stride of t rank buffers."""
+    got = _matching(xs, shape, dtype, device)
+    if got is not None and len(xs) == t:
+        return got[0], _row_stride(shape, got[1], what)
     if len(xs) != t:
         raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
-    arr, ld = (_vp * t)(), None
+    ld = None
     for i, x in enumerate(xs):
         if not isinstance(x, torch.Tensor):
             raise TypeError(f"{what}[{i}] must be a torch.Tensor")
@@ -598,27 +632,25 @@ def _rank_rows(xs, shape, dtype, device, t, what):
             raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {dtype}")
         if x.device != device:
             raise ValueError(f"{what}[{i}]: on {x.device}, expected {device}")
-        if i == 0:
-            ld = _row_stride(x, what)
-        elif (shape[-1] if x.is_contiguous() else _row_stride(x, what)) != ld:
+        got = _row_stride(x.shape, x.stride(), what)
+        if ld is not None and got != ld:
             raise ValueError(f"{what}: every rank needs the same row stride")
-        arr[i] = x.data_ptr()
-    return arr, ld
+        ld = got
+    return _pointers(xs), ld
 
 
 def _rank_dense(xs, shape, dtype, device, t, what):
     """Pointer array of t dense rank buffers (None: no array)."""
     if xs is None:
         return None
+    got = _matching(xs, shape, dtype, device)
+    if got is not None and len(xs) == t and _dense(shape, got[1]):
+        return got[0]
     if len(xs) != t:
         raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
-    arr = (_vp * t)()
     for i, x in enumerate(xs):
-        if (not isinstance(x, torch.Tensor) or x.shape != shape or x.dtype is not dtype
-                or x.device != device or not x.is_contiguous()):
-            _need(x, shape, dtype, device, f"{what}[{i}]")
-        arr[i] = x.data_ptr()
-    return arr
+        _need(x, shape, dtype, device, f"{what}[{i}]")
+    return _pointers(xs)
 
 
 def _first(xs, dims, what):
@@ -634,6 +666,10 @@ def _first(xs, dims, what):
     if x.dtype not in DTYPES:
         raise ValueError(f"{what}[0]: dtype {x.dtype} is not bfloat16, float16 or float32")
     return t, x, DTYPES[x.dtype]
+
+
+def _status_word(dev):
+    return _status[dev] if dev in _status else device_status(dev)
 
 
 def _call(dev, fn, *args):
@@ -672,36 +708,37 @@ def sp_rope_table(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original
 
 def _rope_strides(xs, shape, dtype, device, t, what):
     """Pointer array, token stride and head stride of (b, s, heads, d) buffers."""
-    if len(xs) != t:
-        raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
     b, s, heads, d = shape
-    arr, got = (_vp * t)(), None
-    for i, x in enumerate(xs):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError(f"{what}[{i}] must be a torch.Tensor")
-        if x.shape != shape:
-            raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(shape)}")
-        if x.dtype is not dtype:
-            raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {dtype}")
-        if x.device != device:
-            raise ValueError(f"{what}[{i}]: on {x.device}, expected {device}")
-        s0, s1, s2, s3 = x.stride()
-        if d > 1 and s3 != 1:
-            raise ValueError(f"{what}[{i}]: the last dimension must be contiguous")
-        if heads == 1:
-            s2 = d
-        if s > 1:
-            ld = s1
-            if b > 1 and s0 != s * s1:
-                raise ValueError(f"{what}[{i}]: batch rows must follow each other")
-        else:
-            ld = s0 if b > 1 else max(s1, heads * s2)
-        if got is None:
-            got = (ld, s2)
-        elif got != (ld, s2):
-            raise ValueError(f"{what}: every rank needs the same strides")
-        arr[i] = x.data_ptr()
-    return arr, got[0], got[1]
+    got = _matching(xs, shape, dtype, device)
+    if got is None or len(xs) != t:
+        if len(xs) != t:
+            raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
+        for i, x in enumerate(xs):
+            if not isinstance(x, torch.Tensor):
+                raise TypeError(f"{what}[{i}] must be a torch.Tensor")
+            if x.shape != shape:
+                raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(shape)}")
+            if x.dtype is not dtype:
+                raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {dtype}")
+            if x.device != device:
+                raise ValueError(f"{what}[{i}]: on {x.device}, expected {device}")
+            if x.stride() != xs[0].stride():
+                raise ValueError(f"{what}: every rank needs the same strides")
+        got = _pointers(xs), xs[0].stride()
+    if _dense(shape, got[1]):
+        return got[0], heads * d, d
+    s0, s1, s2, s3 = got[1]
+    if d > 1 and s3 != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if heads == 1:
+        s2 = d
+    if s > 1:
+        ld = s1
+        if b > 1 and s0 != s * s1:
+            raise ValueError(f"{what}: batch rows must follow each other")
+    else:
+        ld = s0 if b > 1 else max(s1, heads * s2)
+    return got[0], ld, s2
 
 
 def _rope_call(entry, x, table, layout, positions, first_position, cu_seqlens, y, status):
@@ -716,7 +753,7 @@ def _rope_call(entry, x, table, layout, positions, first_position, cu_seqlens, y
     if positions is not None:
         _need(positions, (b, s), torch.int64, dev, "positions")
     cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
-    st = device_status(dev) if status is None else status
+    st = _status_word(dev) if status is None else status
     _call(dev, getattr(lib, entry), xa, x_ld, x_head, b, s, heads, d, t, dt, ctypes.byref(table),
           _choice(ROPE_LAYOUTS, layout, "layout"), _ptr(positions), int(first_position), cu,
           n_seqs, ya, y_ld, y_head, st.data_ptr())
@@ -760,7 +797,7 @@ def sp_gated_scan_fwd(gate, value, *, h0=None, tied=True, cu_seqlens=None, y, hT
     ha = _rank_dense(h0, (n, c), f32, dev, t, "h0")
     ta = _rank_dense(hT, (n, c), f32, dev, t, "hT")
     sa = _rank_dense(states, sp_gated_scan_states_shape(b, s, c), f32, dev, t, "states")
-    st = device_status(dev) if status is None else status
+    st = _status_word(dev) if status is None else status
     _call(dev, lib.sp_gated_scan_fwd, ga, g_ld, va, v_ld, ha, b, s, c, t, dt, int(bool(tied)), cu,
           n_seqs, ya, y_ld, ta, sa, st.data_ptr())
 
@@ -784,7 +821,7 @@ def sp_gated_scan_bwd(gate, value, states, dy, *, h0=None, dhT=None, tied=True, 
     ta = _rank_dense(dhT, (n, c), f32, dev, t, "dhT")
     oa = _rank_dense(dh0, (n, c), f32, dev, t, "dh0")
     sa = _rank_dense(states, sp_gated_scan_states_shape(b, s, c), f32, dev, t, "states")
-    st = device_status(dev) if status is None else status
+    st = _status_word(dev) if status is None else status
     _call(dev, lib.sp_gated_scan_bwd, ga, g_ld, va, v_ld, ha, sa, da, d_ld, ta, b, s, c, t, dt,
           int(bool(tied)), cu, n_seqs, dga, dg_ld, dva, dv_ld, oa, st.data_ptr())
 

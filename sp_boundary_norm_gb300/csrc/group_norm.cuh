@@ -25,8 +25,18 @@ namespace spb {
 template <int DT>
 using Vec8 = Pack<DT, 8>;
 
-constexpr int kTileRows = 4;        // vectors a thread holds (rows, tiles; forward)
-constexpr int kBackTileRows = 2;    // of x and of dy (rows, tiles; backward)
+constexpr int kTileRows = 4;        // vectors a thread holds (tiles; forward)
+constexpr int kBackTileRows = 2;    // of x and of dy (tiles; backward)
+// Vectors of x a thread holds in the rows form, and blocks an SM that the
+// registers are held to (16,384 rows of 8 x 1024, RMS: 4 and 2 95 us, 2 and 4
+// 93, 2 and 3 97, 4 and 3 116 with spilled registers; wider groups and odd ones
+// want the four; float32 2 and 3 95 us, 4 and 2 111).
+template <int DT>
+constexpr int kRowRows = DT == SP_F32 ? 2 : 4;
+template <int DT>
+constexpr int kRowBlocks = DT == SP_F32 ? 3 : 2;
+constexpr int kBackRowRows = 2;     // of x and of dy, with two blocks an SM
+constexpr int kBackRowBlocks = 2;
 constexpr int kRowWarps = 8;        // of a block (rows), more for groups beyond 256 vectors
 constexpr int kRowMaxWarps = kGroupThreads / 32;
 
@@ -169,14 +179,30 @@ __device__ __forceinline__ F2 standard(F2 x, float mean, float rstd) {
   return fma2(x, both(rstd), both(-mean * rstd));
 }
 
-// One vector's result.
+__device__ __forceinline__ F2 neg(F2 v) { return mul2(v, both(-1.f)); }
+
+// The column's parameters with a group's statistics folded in, for many vectors
+// of that group: q = x gamma + beta then (16-bit inputs; else as they are).
 template <int DT>
+__device__ __forceinline__ void fold_stats(Column<DT>& col, float mean, float rstd) {
+  if constexpr (DT == SP_F32) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    col.gamma[i] = mul2(col.gamma[i], both(rstd));
+    col.beta[i] = fma2(neg(col.gamma[i]), both(mean), col.beta[i]);
+  }
+}
+
+// One vector's result; FOLDED: the column's parameters hold the statistics.
+template <int DT, bool FOLDED = false>
 __device__ __forceinline__ Vec8<DT> norm_act(const F2 (&x)[4], float mean, float rstd,
                                              const Column<DT>& col, bool silu) {
   F2 y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    y[i] = fma2(standard<DT>(x[i], mean, rstd), col.gamma[i], col.beta[i]);
+  for (int i = 0; i < 4; ++i) {
+    const F2 z = FOLDED && DT != SP_F32 ? x[i] : standard<DT>(x[i], mean, rstd);
+    y[i] = fma2(z, col.gamma[i], col.beta[i]);
+  }
   if (silu) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], sigmoid_of<DT>(y[i]));
@@ -185,6 +211,60 @@ __device__ __forceinline__ Vec8<DT> norm_act(const F2 (&x)[4], float mean, float
   pack_pairs(o, y);
   return o;
 }
+
+// Running (count, mean, M2) of a thread's values.  A stretch of up to kStretch
+// vectors sums x - k and its square for each of the 8 channels, k the
+// stretch's first vector: one of the values themselves, so (x - k)^2 sums to at
+// most the count times the spread, and no mean, however far from zero, costs
+// digits.  Stretches then join by their means.
+constexpr int kStretch = 64;
+struct Moments {
+  F2 k[4], s[4], q[4];
+  int n = 0;                          // vectors of the stretch
+  float cnt = 0.f, mean = 0.f, m2 = 0.f;
+  __device__ __forceinline__ void add(const F2 (&v)[4], bool centred) {
+    if (n == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        k[i] = centred ? neg(v[i]) : both(0.f);
+        s[i] = q[i] = both(0.f);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 d = add2(v[i], k[i]);
+      s[i] = add2(s[i], d);
+      q[i] = fma2(d, d, q[i]);
+    }
+    ++n;
+  }
+  // Ends the stretch.  Not centred: mean stays 0 and M2 is the sum of squares.
+  __device__ __forceinline__ void join(bool centred) {
+    if (n == 0) return;
+    const float nf = static_cast<float>(n), inv = __fdividef(1.f, nf);
+    F2 mc[4], sum = both(0.f), rest = both(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mc[i] = fma2(s[i], both(inv), neg(k[i]));              // the channel's mean
+      sum = add2(sum, mc[i]);
+      rest = add2(rest, centred ? fma2(neg(mul2(s[i], both(inv))), s[i], q[i]) : q[i]);
+    }
+    const float2 a = split(sum);
+    const float mb = centred ? (a.x + a.y) * 0.125f : 0.f;
+    F2 apart = both(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 d = add2(mc[i], both(-mb));
+      apart = fma2(d, d, apart);
+    }
+    const float2 r = split(rest), w = split(apart);
+    const float nb = 8.f * nf, all = cnt + nb, part = __fdividef(nb, all), d = mb - mean;
+    mean = fmaf(d, part, mean);
+    m2 += (r.x + r.y) + (centred ? nf * (w.x + w.y) : 0.f) + d * d * cnt * part;
+    cnt = all;
+    n = 0;
+  }
+};
 
 // Backward of one vector: z and dq (the gradient of q) in place of x and dy.
 template <int DT>

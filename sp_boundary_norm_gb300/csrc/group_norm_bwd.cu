@@ -36,11 +36,11 @@ __device__ __forceinline__ void back_vector(F2 (&z)[4], F2 (&dq)[4], float mean,
 // Rows (as in the forward).
 template <int DT, int MODE>
 __global__ void __launch_bounds__(MODE == kSumTeam ? kGroupThreads : 32 * kRowWarps,
-                                  MODE == kSumTeam ? 1 : 2)
+                                  MODE == kSumTeam ? 1 : kBackRowBlocks)
 group_row_bwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ float2 dyn2[];             // the parameter gradients' parts
-  __shared__ RowSums<MODE, 2 * kBackTileRows> sh;
+  __shared__ RowSums<MODE, 2 * kBackRowRows> sh;
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team_warps = MODE == kSumTeam ? (P.cols + 31) / 32 : 1;
@@ -52,13 +52,13 @@ group_row_bwd_kernel(const GroupNormParams P) {
   const bool on = cx < P.cols && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
   const int in_slab = cx < P.cols ? cx / P.q : 0;
-  RowGroup<MODE, 2 * kBackTileRows> group{&sh, P.q, warp, in_slab * P.q, team_warps, team};
+  RowGroup<MODE, 2 * kBackRowRows> group{&sh, P.q, warp, in_slab * P.q, team_warps, team};
   const int64_t ch0 = static_cast<int64_t>(r) * P.c + slab * P.cols * 8, ch = ch0 + cx * 8;
   Column<DT> col;
   col.read(P, ch, on);
   const int64_t at = static_cast<int64_t>(vec) * 8 * E;
-  const int64_t first = (static_cast<int64_t>(part) * P.rows + team) * kBackTileRows;
-  const int64_t step = P.parts * P.rows * kBackTileRows;
+  const int64_t first = (static_cast<int64_t>(part) * P.rows + team) * kBackRowRows;
+  const int64_t step = P.parts * P.rows * kBackRowRows;
   const char* x = P.x[r] + first * P.ld_x + at;
   const char* dy = P.dy[r] + first * P.ld_dy + at;
   char* out = P.out[r] + first * P.ld_out + at;
@@ -70,11 +70,11 @@ group_row_bwd_kernel(const GroupNormParams P) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
 
-  Vec8<DT> xraw[kBackTileRows], draw[kBackTileRows];
-  float mean_next[kBackTileRows], rstd_next[kBackTileRows];
+  Vec8<DT> xraw[kBackRowRows], draw[kBackRowRows];
+  float mean_next[kBackRowRows], rstd_next[kBackRowRows];
   auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int u = 0; u < kBackTileRows; ++u) {
+    for (int u = 0; u < kBackRowRows; ++u) {
       xraw[u] = draw[u] = Vec8<DT>{};
       mean_next[u] = rstd_next[u] = 0.f;
       if (on && row + u < P.n) {
@@ -91,11 +91,11 @@ group_row_bwd_kernel(const GroupNormParams P) {
   };
   fetch(first);
   for (int64_t row = first; row < P.n; row += step, out += step_out) {
-    F2 z[kBackTileRows][4], dq[kBackTileRows][4];
-    float rstd[kBackTileRows];
-    float sum[2 * kBackTileRows];              // of dz and of dz z
+    F2 z[kBackRowRows][4], dq[kBackRowRows][4];
+    float rstd[kBackRowRows];
+    float sum[2 * kBackRowRows];              // of dz and of dz z
 #pragma unroll
-    for (int u = 0; u < kBackTileRows; ++u) {
+    for (int u = 0; u < kBackRowRows; ++u) {
       unpack_pairs(xraw[u], z[u]);
       unpack_pairs(draw[u], dq[u]);
       rstd[u] = rstd_next[u];
@@ -105,7 +105,7 @@ group_row_bwd_kernel(const GroupNormParams P) {
     fetch(row + step);
     group.sum(sum);
 #pragma unroll
-    for (int u = 0; u < kBackTileRows; ++u) {
+    for (int u = 0; u < kBackRowRows; ++u) {
       if (!on || row + u >= P.n) continue;
       const float m1 = ln ? sum[2 * u] * P.count_inv : 0.f, m2 = sum[2 * u + 1] * P.count_inv;
       store_pack(out + u * P.ld_out, back_out<DT>(z[u], dq[u], rstd[u], col, m1, m2));

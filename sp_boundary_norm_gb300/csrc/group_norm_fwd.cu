@@ -11,10 +11,10 @@ constexpr int kFwdUnitBlocks = 3;   // blocks an SM that the registers are held 
 // their way meanwhile.
 template <int DT, int MODE>
 __global__ void __launch_bounds__(MODE == kSumTeam ? kGroupThreads : 32 * kRowWarps,
-                                  MODE == kSumTeam ? 1 : 3)
+                                  MODE == kSumTeam ? 1 : kRowBlocks<DT>)
 group_row_fwd_kernel(const GroupNormParams P) {
-  constexpr int E = ElemSize<DT>::value;
-  __shared__ RowSums<MODE, kTileRows> sh;
+  constexpr int E = ElemSize<DT>::value, kRows = kRowRows<DT>;
+  __shared__ RowSums<MODE, kRows> sh;
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team_warps = MODE == kSumTeam ? (P.cols + 31) / 32 : 1;
@@ -26,21 +26,21 @@ group_row_fwd_kernel(const GroupNormParams P) {
   const bool on = cx < P.cols && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
   const int in_slab = cx < P.cols ? cx / P.q : 0;
-  RowGroup<MODE, kTileRows> group{&sh, P.q, warp, in_slab * P.q, team_warps, team};
+  RowGroup<MODE, kRows> group{&sh, P.q, warp, in_slab * P.q, team_warps, team};
   Column<DT> col;
   col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
   const bool tells = on && cx == in_slab * P.q;          // writes its group's statistics
   const int64_t stat = vec / P.q;
-  const int64_t first = (static_cast<int64_t>(part) * P.rows + team) * kTileRows;
-  const int64_t step = P.parts * P.rows * kTileRows;
+  const int64_t first = (static_cast<int64_t>(part) * P.rows + team) * kRows;
+  const int64_t step = P.parts * P.rows * kRows;
   const char* x = P.x[r] + first * P.ld_x + static_cast<int64_t>(vec) * 8 * E;
   char* out = P.out[r] + first * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
   const int64_t step_x = step * P.ld_x, step_out = step * P.ld_out;
 
-  Vec8<DT> raw[kTileRows];
+  Vec8<DT> raw[kRows];
   auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int u = 0; u < kTileRows; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       raw[u] = Vec8<DT>{};
       if (on && row + u < P.n) load_pack(raw[u], x + u * P.ld_x);
     }
@@ -48,28 +48,28 @@ group_row_fwd_kernel(const GroupNormParams P) {
   };
   fetch(first);
   for (int64_t row = first; row < P.n; row += step, out += step_out) {
-    F2 v[kTileRows][4];
+    F2 v[kRows][4];
 #pragma unroll
-    for (int u = 0; u < kTileRows; ++u) unpack_pairs(raw[u], v[u]);
+    for (int u = 0; u < kRows; ++u) unpack_pairs(raw[u], v[u]);
     fetch(row + step);
-    float mean[kTileRows], rstd[kTileRows];
+    float mean[kRows], rstd[kRows];
 #pragma unroll
-    for (int u = 0; u < kTileRows; ++u) mean[u] = 0.f;
+    for (int u = 0; u < kRows; ++u) mean[u] = 0.f;
     if (ln) {
 #pragma unroll
-      for (int u = 0; u < kTileRows; ++u) mean[u] = pair_sum(v[u]);
+      for (int u = 0; u < kRows; ++u) mean[u] = pair_sum(v[u]);
       group.sum(mean);
 #pragma unroll
-      for (int u = 0; u < kTileRows; ++u) mean[u] *= P.count_inv;
+      for (int u = 0; u < kRows; ++u) mean[u] *= P.count_inv;
     }
     // (lanes that hold no vector hold zeros: they add nothing)
 #pragma unroll
-    for (int u = 0; u < kTileRows; ++u) rstd[u] = on ? spread_sum(v[u], mean[u]) : 0.f;
+    for (int u = 0; u < kRows; ++u) rstd[u] = on ? spread_sum(v[u], mean[u]) : 0.f;
     group.sum(rstd);
 #pragma unroll
-    for (int u = 0; u < kTileRows; ++u) rstd[u] = rsqrtf(rstd[u] * P.count_inv + P.eps);
+    for (int u = 0; u < kRows; ++u) rstd[u] = rsqrtf(rstd[u] * P.count_inv + P.eps);
 #pragma unroll
-    for (int u = 0; u < kTileRows; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       if (!on || row + u >= P.n) continue;
       store_pack(out + u * P.ld_out, norm_act<DT>(v[u], mean[u], rstd[u], col, silu));
       if (tells) {
@@ -231,55 +231,37 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   Column<DT> col;
   col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
 
-  // (count, mean, M2) of the thread's values, batch by batch
-  float cnt = 0.f, mean = 0.f, m2 = 0.f;
-  auto batch = [&](const Vec8<DT> (&raw)[kUnitBatch], int nb) {
-    F2 v[kUnitBatch][4];
-    F2 s2 = both(0.f);
-#pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u) {
-      unpack_pairs(raw[u], v[u]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s2 = add2(s2, v[u][i]);
-    }
-    const float2 sw = split(s2);
-    const float nf = 8.f * static_cast<float>(nb), all = cnt + nf;
-    const float mb = ln ? __fdividef(sw.x + sw.y, nf) : 0.f;
-    float q2 = 0.f;
-#pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u)
-      if (u < nb) q2 += spread_sum(v[u], mb);
-    const float d = mb - mean, part = __fdividef(nf, all);
-    mean = fmaf(d, part, mean);
-    m2 += fmaf(d * d, cnt * part, q2);
-    cnt = all;
-  };
+  Moments mom;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     keep_wait(3 - k);
     const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
-    for (int i0 = k * quarter; i0 < to; i0 += kUnitBatch) {
-      Vec8<DT> raw[kUnitBatch];
-#pragma unroll
-      for (int u = 0; u < kUnitBatch; ++u) {
-        raw[u] = Vec8<DT>{};
-        if (i0 + u < to) raw[u] = kept.get(i0 + u, 0);
-      }
-      batch(raw, to - i0 < kUnitBatch ? to - i0 : kUnitBatch);
+#pragma unroll 4
+    for (int i = k * quarter; i < to; ++i) {
+      F2 v[4];
+      unpack_pairs(kept.get(i, 0), v);
+      mom.add(v, ln);
     }
+    if (mom.n >= kStretch / 2) mom.join(ln);
   }
   for (int i0 = held; i0 < mine; i0 += kUnitBatch) {
     const char* from = x + i0 * step_x;
     Vec8<DT> raw[kUnitBatch];
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u, from += step_x) {
-      raw[u] = Vec8<DT>{};
+    for (int u = 0; u < kUnitBatch; ++u, from += step_x)
       if (i0 + u < mine) load_pack(raw[u], from);
-    }
-    batch(raw, mine - i0 < kUnitBatch ? mine - i0 : kUnitBatch);
+#pragma unroll
+    for (int u = 0; u < kUnitBatch; ++u)
+      if (i0 + u < mine) {
+        F2 v[4];
+        unpack_pairs(raw[u], v);
+        mom.add(v, ln);
+      }
+    if (mom.n >= kStretch - kUnitBatch) mom.join(ln);
   }
+  mom.join(ln);
   // the block's mean and M2 of each group of the slab, one warp a group
-  if (ry < P.rows) sums[threadIdx.x] = make_float2(mean, m2);
+  if (ry < P.rows) sums[threadIdx.x] = make_float2(mom.mean, mom.m2);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const float block_count = static_cast<float>(block_rows) * 8.f * P.q;
@@ -323,11 +305,12 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   __syncthreads();
   if (!on) return;
   const float2 st = stat[cx / P.q];
+  fold_stats(col, st.x, st.y);
 #pragma unroll 2
   for (int i = 0; i < held; ++i, out += step_out) {
     F2 v[4];
     unpack_pairs(kept.get(i, 0), v);
-    store_pack(out, norm_act<DT>(v, st.x, st.y, col, silu));
+    store_pack(out, norm_act<DT, true>(v, st.x, st.y, col, silu));
   }
   for (int i0 = held; i0 < mine; i0 += kUnitBatch) {
     const char* from = x + i0 * step_x;
@@ -340,7 +323,7 @@ group_unit_fwd_kernel(const GroupNormParams P) {
       if (i0 + u >= mine) continue;
       F2 v[4];
       unpack_pairs(raw[u], v);
-      store_pack(out, norm_act<DT>(v, st.x, st.y, col, silu));
+      store_pack(out, norm_act<DT, true>(v, st.x, st.y, col, silu));
     }
   }
 }
@@ -369,8 +352,10 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     const int team = (s.cols + 31) / 32;
     s.rows = team < kRowWarps ? kRowWarps / team : 1;
     s.threads = s.rows * team * 32;
-    const int64_t tiles = div_up(n, static_cast<int64_t>(s.rows) * held_rows);
-    const int64_t cap = static_cast<int64_t>(sms) * (bwd ? 2 : 3) / (s.slabs * t);
+    const int row_rows = bwd ? kBackRowRows : size == 4 ? kRowRows<SP_F32> : kRowRows<SP_BF16>;
+    const int blocks = bwd ? kBackRowBlocks : size == 4 ? kRowBlocks<SP_F32> : kRowBlocks<SP_BF16>;
+    const int64_t tiles = div_up(n, static_cast<int64_t>(s.rows) * row_rows);
+    const int64_t cap = static_cast<int64_t>(sms) * blocks / (s.slabs * t);
     s.parts = cap < 1 ? 1 : tiles < cap ? tiles : cap;
     s.smem = bwd ? static_cast<size_t>(s.rows) * s.cols * 17 * 4 : 0;
     return s;
@@ -415,7 +400,7 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   const int slab_groups = s.cols / q;
   const size_t vec = static_cast<size_t>(s.threads) * 8 * size * (bwd ? 2 : 1);
   const int resident = bwd ? 2 : 3;
-  const size_t room = (bwd ? 100 : 66) * 1024;
+  const size_t room = (bwd ? 112 : 66) * 1024;
   auto need = [&](int cl) {
     const int64_t per = (l + cl - 1) / cl;
     return (per + s.rows - 1) / s.rows;
@@ -430,8 +415,9 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   const size_t fixed = static_cast<size_t>(s.threads) * 8 +
                        static_cast<size_t>(s.cluster + 1) * slab_groups * 8;
   int64_t keep = need(s.cluster);
-  // what is not kept is read again: up to a whole SM's memory a block then
-  const size_t most = need(s.cluster) * vec > room ? 110 * 1024 : room + fixed;
+  // What is not kept is read again.  Calls of few blocks keep no more than lets
+  // all of them run at once.
+  const size_t most = n * t * s.slabs * s.cluster <= 2 * sms ? 50 * 1024 : room;
   if (keep * vec + fixed > most) keep = most > fixed ? static_cast<int64_t>((most - fixed) / vec) : 0;
   s.keep = static_cast<int>(keep);
   s.smem = s.keep * vec + fixed;

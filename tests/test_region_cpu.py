@@ -259,10 +259,27 @@ def test_binding_refuses_before_the_library():
 
 def test_row_strides():
     x = torch.zeros(3, 5, 48)
-    assert sp._row_stride(x, "x") == 48
-    assert sp._row_stride(x[..., :16], "x") == 48
-    assert sp._row_stride(x[:, :1, 16:32], "x") == 240       # one row a sample: the samples' stride
-    assert sp._row_stride(x[:1, :1, :16], "x") == 16
-    assert sp._row_stride(x[:1, ::2, :16], "x") == 96
+    row = lambda y: sp._row_stride(y.shape, y.stride(), "x")
+    assert row(x) == 48
+    assert row(x[..., :16]) == 48
+    assert row(x[:, :1, 16:32]) == 240       # one row a sample: the samples' stride
+    assert row(x[:1, :1, :16]) == 16
+    assert row(x[:1, ::2, :16]) == 96
     with pytest.raises(ValueError):
-        sp._row_stride(x[:, ::2, :16], "x")
+        row(x[:, ::2, :16])
+
+
+def test_list_reader_takes_only_matching_cuda_tensors():
+    """Everything that is not a list of equal CUDA tensors is left to the binding's
+    own checks (None), whatever it is; wrong calls of the reader raise."""
+    x = torch.zeros(2, 3, dtype=torch.bfloat16)
+    sp._matching([x], (2, 3), torch.bfloat16, x.device)
+    same = sp._module.same
+    for xs, shape in (([x], (2, 3)), ([], (2, 3)), ([None], (2, 3)), ([3], (2,)), ("ab", (2, 3)),
+                      (None, (2, 3)), ([x] * 65, (2, 3)), ([x], None), ([x], ("a", 3)),
+                      ([x], (1,) * 9), ([x], (2, 1 << 70)), ((x, x), x.shape)):
+        assert same(xs, shape, 0, 0) is None
+    with pytest.raises(TypeError):
+        same([x])
+    with pytest.raises(TypeError):
+        same([x], (2, 3), "bf16", 0)
