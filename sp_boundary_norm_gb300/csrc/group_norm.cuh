@@ -9,10 +9,13 @@
 //    groups the warps of a group, takes whole groups of several rows at once;
 //  - tiles: a block takes whole samples of few rows; every thread holds its
 //    vectors in registers between the statistics and the result;
-//  - units: a cluster of blocks takes one sample's slab of groups, keeps the
-//    rows it can in shared memory and reads the rest again (from L2 where the
-//    cluster's share fits it), and joins its statistics through distributed
-//    shared memory.
+//  - units: a cluster of blocks takes one sample's slab of groups, reads it for
+//    the statistics, joins them through distributed shared memory, and reads it
+//    again, from L2 as far as the clusters at work fit it, for the result.  (Kept
+//    in shared memory instead, the slab left so few warps an SM that the
+//    arithmetic took longer than the second reading: 8 samples of 4096 x 1280
+//    in 48 us forward and 90 backward, persistent blocks with the next sample's
+//    copies beneath the stores 57 and 107.)
 // Sums run in a fixed order: results do not depend on timing.  Statistics are
 // two-pass (of values held in registers) and joined as (count, mean, M2), so a
 // mean far above the spread costs no digits.
@@ -39,6 +42,11 @@ constexpr int kBackRowRows = 2;     // of x and of dy, with two blocks an SM
 constexpr int kBackRowBlocks = 2;
 constexpr int kRowWarps = 8;        // of a block (rows), more for groups beyond 256 vectors
 constexpr int kRowMaxWarps = kGroupThreads / 32;
+
+constexpr int kUnitBlocks = 2;      // units: blocks an SM that the registers are held to
+constexpr int kUnitBatch = 4;       // vectors a thread reads at once (forward),
+template <int DT>                   // and of x and dy each (backward)
+constexpr int kBackUnitBatch = DT == SP_F32 ? 2 : 3;
 
 // How the lanes of a group add up (rows form): a power of two of neighbouring
 // lanes by shuffles; other widths up to 31 through the warp's shared memory,
@@ -108,50 +116,18 @@ struct Deal {
   __device__ __forceinline__ int first(int k) const { return k * each + (k < extra ? k : extra); }
 };
 
-// The vectors that a thread keeps in shared memory, T to a row (x; x and dy):
-// its own slots, filled by its own copies, so no other thread waits for them.
-template <int DT, int T>
-struct Kept {
-  static constexpr int kPer = ElemSize<DT>::value == 4 ? 2 : 1;   // 16-byte pieces
-  const char* base;          // of this thread's first slot
-  uint32_t addr, piece;      // its shared address; bytes from one piece to the next
-  __device__ __forceinline__ Kept(void* smem) {
-    base = static_cast<char*>(smem) + threadIdx.x * 16;
-    addr = smem_addr(base);
-    piece = blockDim.x * 16;
-  }
-  __device__ __forceinline__ uint32_t offset(int i, int k) const {
-    return static_cast<uint32_t>(i * T + k) * kPer * piece;
-  }
-  __device__ __forceinline__ void copy(int i, int k, const char* src) const {
-    const uint32_t to = addr + offset(i, k);
+// A vector that will be read once more before long: kept in L2 (load_pack's
+// streaming loads give their lines up first).
+template <int DT>
+__device__ __forceinline__ void load_again(Vec8<DT>& p, const char* src) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * piece),
-                   "l"(src + 16 * j)
-                   : "memory");
+  for (int i = 0; i < Vec8<DT>::kBytes / 16; ++i) {
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src) + i);
+    p.w[4 * i] = v.x;
+    p.w[4 * i + 1] = v.y;
+    p.w[4 * i + 2] = v.z;
+    p.w[4 * i + 3] = v.w;
   }
-  __device__ __forceinline__ Vec8<DT> get(int i, int k) const {
-    const char* from = base + offset(i, k);
-    Vec8<DT> v;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint4 w = lds16(from + j * piece);
-      v.w[4 * j] = w.x;
-      v.w[4 * j + 1] = w.y;
-      v.w[4 * j + 2] = w.z;
-      v.w[4 * j + 3] = w.w;
-    }
-    return v;
-  }
-};
-
-// At most n of the thread's groups of copies are still on their way.
-__device__ __forceinline__ void keep_wait(int n) {
-  if (n == 0) cp_async_wait<0>();
-  else if (n == 1) cp_async_wait<1>();
-  else if (n == 2) cp_async_wait<2>();
-  else cp_async_wait<3>();
 }
 
 __device__ __forceinline__ float pair_sum(const F2 (&v)[4]) {

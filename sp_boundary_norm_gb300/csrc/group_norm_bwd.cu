@@ -10,7 +10,6 @@
 
 namespace spb {
 
-constexpr int kBackUnitBatch = 2;   // vectors of each of one batch (units)
 
 // z and dq in place of a vector's x and dy, its parts of the column's parameter
 // gradients added to acc; its sums of dz and of dz z.
@@ -225,10 +224,10 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_bwd_kernel(const Gro
 }
 
 template <int DT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : 2)
+__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kUnitBlocks)
 group_unit_bwd_kernel(const GroupNormParams P) {
-  constexpr int E = ElemSize<DT>::value;
-  extern __shared__ uint4 dyn16[];             // [keep][x, dy][threads] vectors, then the sums
+  constexpr int E = ElemSize<DT>::value, kBatch = kBackUnitBatch<DT>;
+  extern __shared__ float2 sums[];             // [threads] sums of dz and dz z
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (C > 1) cluster_arrive();                 // waited for before the first remote store
   pdl_wait();
@@ -242,9 +241,6 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
   const int slab_groups = P.cols / P.q;
-  const Kept<DT, 2> kept(dyn16);
-  float2* sums = reinterpret_cast<float2*>(dyn16 + static_cast<int64_t>(P.keep) * 2 *
-                                                       Kept<DT, 2>::kPer * blockDim.x);
   float2* joined = sums + blockDim.x;          // [cluster][slab groups] sums of each block
   float2* stat = joined + C * slab_groups;     // [slab groups] group means of dz and dz z
   const int64_t ch0 = static_cast<int64_t>(r) * P.c + slab * P.cols * 8, ch = ch0 + cx * 8;
@@ -252,26 +248,12 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   const int b0 = blocks.first(rank), block_rows = blocks.count(rank);
   const Deal lanes(block_rows, P.rows);
   const int mine = on ? lanes.count(ry) : 0;
-  const int held = mine < P.keep ? mine : P.keep;
   const int64_t row0 = sample * P.l + b0 + ry;
   const int64_t at = static_cast<int64_t>(vec) * 8 * E;
   const char* x = P.x[r] + row0 * P.ld_x + at;
   const char* dy = P.dy[r] + row0 * P.ld_dy + at;
   char* out = P.out[r] + row0 * P.ld_out + at;
   const int64_t step_x = P.ld_x * P.rows, step_dy = P.ld_dy * P.rows, step_out = P.ld_out * P.rows;
-  const int quarter = ((held + 3) / 4 + kBackUnitBatch - 1) / kBackUnitBatch * kBackUnitBatch;
-  {
-    const char *from = x, *dfrom = dy;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
-      for (int i = k * quarter; i < to; ++i, from += step_x, dfrom += step_dy) {
-        kept.copy(i, 0, from);
-        kept.copy(i, 1, dfrom);
-      }
-      cp_async_commit();
-    }
-  }
   Column<DT> col;
   col.read(P, ch, on);
   float mean = 0.f, rstd = 0.f;
@@ -283,37 +265,48 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   F2 acc[8];                                   // dgamma, dbeta of the column
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
-  auto add = [&](const Vec8<DT>& xr, const Vec8<DT>& dr) {
-    F2 z[4], dq[4];
-    unpack_pairs(xr, z);
-    unpack_pairs(dr, dq);
-    back_act<DT>(z, dq, mean, rstd, col, silu);
+  // a batch of vectors is on its way while the one before is used
+  Vec8<DT> xraw[kBatch], draw[kBatch];
+  const char *from = x, *dfrom = dy;
+  auto fetch = [&](int i0, bool again) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      acc[i] = fma2(dq[i], z[i], acc[i]);
-      acc[4 + i] = add2(acc[4 + i], dq[i]);
-    }
-  };
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    keep_wait(3 - k);
-    const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
-#pragma unroll 2
-    for (int i = k * quarter; i < to; ++i) add(kept.get(i, 0), kept.get(i, 1));
-  }
-  for (int i0 = held; i0 < mine; i0 += kBackUnitBatch) {
-    const char *from = x + i0 * step_x, *dfrom = dy + i0 * step_dy;
-    Vec8<DT> xraw[kBackUnitBatch], draw[kBackUnitBatch];
-#pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u, from += step_x, dfrom += step_dy)
+    for (int u = 0; u < kBatch; ++u, from += step_x, dfrom += step_dy)
       if (i0 + u < mine) {
-        load_pack(xraw[u], from);
-        load_pack(draw[u], dfrom);
+        if (again) {
+          load_again<DT>(xraw[u], from);
+          load_again<DT>(draw[u], dfrom);
+        } else {
+          load_pack(xraw[u], from);
+          load_pack(draw[u], dfrom);
+        }
       }
+  };
+  F2 z[kBatch][4], dq[kBatch][4];
+  auto take = [&](int i0, bool again) {
 #pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u)
-      if (i0 + u < mine) add(xraw[u], draw[u]);
+    for (int u = 0; u < kBatch; ++u) {
+      unpack_pairs(xraw[u], z[u]);
+      unpack_pairs(draw[u], dq[u]);
+    }
+    fetch(i0 + kBatch, again);
+  };
+  fetch(0, true);
+  for (int i0 = 0; i0 < mine; i0 += kBatch) {
+    take(i0, true);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (i0 + u >= mine) continue;
+      back_act<DT>(z[u], dq[u], mean, rstd, col, silu);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] = fma2(dq[u][i], z[u][i], acc[i]);
+        acc[4 + i] = add2(acc[4 + i], dq[u][i]);
+      }
+    }
   }
+  from = x;
+  dfrom = dy;
+  fetch(0, false);
   F2 own1 = both(0.f), own2 = both(0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -352,30 +345,17 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   }
   __syncthreads();
   const float2 m = stat[cx / P.q];
-  auto finish = [&](const Vec8<DT>& xr, const Vec8<DT>& dr, char* to) {
-    F2 z[4], dq[4];
-    unpack_pairs(xr, z);
-    unpack_pairs(dr, dq);
-    back_act<DT>(z, dq, mean, rstd, col, silu);
-    store_pack(to, back_out<DT>(z, dq, rstd, col, m.x, m.y));
-  };
-#pragma unroll 2
-  for (int i = 0; i < held; ++i, out += step_out) finish(kept.get(i, 0), kept.get(i, 1), out);
-  for (int i0 = held; i0 < mine; i0 += kBackUnitBatch) {
-    const char *from = x + i0 * step_x, *dfrom = dy + i0 * step_dy;
-    Vec8<DT> xraw[kBackUnitBatch], draw[kBackUnitBatch];
+  for (int i0 = 0; i0 < mine; i0 += kBatch) {
+    take(i0, false);
 #pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u, from += step_x, dfrom += step_dy)
-      if (i0 + u < mine) {
-        load_pack(xraw[u], from);
-        load_pack(draw[u], dfrom);
-      }
-#pragma unroll
-    for (int u = 0; u < kBackUnitBatch; ++u, out += step_out)
-      if (i0 + u < mine) finish(xraw[u], draw[u], out);
+    for (int u = 0; u < kBatch; ++u, out += step_out) {
+      if (i0 + u >= mine) continue;
+      back_act<DT>(z[u], dq[u], mean, rstd, col, silu);
+      store_pack(out, back_out<DT>(z[u], dq[u], rstd, col, m.x, m.y));
+    }
   }
   if (P.has_params)
-    put_param_part(P, acc, reinterpret_cast<float*>(dyn16), cx, ry, ch0, P.c - slab * P.cols * 8,
+    put_param_part(P, acc, reinterpret_cast<float*>(sums), cx, ry, ch0, P.c - slab * P.cols * 8,
                    static_cast<int64_t>(sample) * C + rank);
 }
 

@@ -4,8 +4,6 @@
 
 namespace spb {
 
-constexpr int kUnitBatch = 4;       // vectors of one batch (units)
-constexpr int kFwdUnitBlocks = 3;   // blocks an SM that the registers are held to
 
 // Rows: a team takes kTileRows rows of its slab at a time; the next ones are on
 // their way meanwhile.
@@ -181,15 +179,13 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
   }
 }
 
-// One cluster per (sample, rank, slab).  A thread's first `keep` vectors are
-// all asked for at once, into its own slots of shared memory, and are used from
-// there twice; what does not fit is read twice.  WIDE: groups of more than 256
-// vectors, blocks of up to 512 threads.
+// One cluster per (sample, rank, slab).  WIDE: groups of more than 256 vectors,
+// blocks of up to 512 threads.
 template <int DT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kFwdUnitBlocks)
+__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kUnitBlocks)
 group_unit_fwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value;
-  extern __shared__ uint4 dyn16[];             // [keep][threads] vectors, then the sums below
+  extern __shared__ float2 sums[];             // [threads] mean, M2
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (C > 1) cluster_arrive();                 // waited for before the first remote store
   pdl_wait();
@@ -203,9 +199,6 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
   const int slab_groups = P.cols / P.q;
-  const Kept<DT, 1> kept(dyn16);
-  float2* sums = reinterpret_cast<float2*>(dyn16 + static_cast<int64_t>(P.keep) *
-                                                       Kept<DT, 1>::kPer * blockDim.x);
   float2* joined = sums + blockDim.x;          // [cluster][slab groups] mean, M2 of each block
   float2* stat = joined + C * slab_groups;     // [slab groups] mean, rstd
   // this block's rows of the sample, and this thread's: ry, ry + rows, ...
@@ -213,53 +206,35 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   const int b0 = blocks.first(rank), block_rows = blocks.count(rank);
   const Deal lanes(block_rows, P.rows);
   const int mine = on ? lanes.count(ry) : 0;
-  const int held = mine < P.keep ? mine : P.keep;
   const int64_t row0 = sample * P.l + b0 + ry;
   const char* x = P.x[r] + row0 * P.ld_x + static_cast<int64_t>(vec) * 8 * E;
-  char* out = P.out[r] + row0 * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
   const int64_t step_x = P.ld_x * P.rows, step_out = P.ld_out * P.rows;
-  const int quarter = ((held + 3) / 4 + kUnitBatch - 1) / kUnitBatch * kUnitBatch;
-  {
-    const char* from = x;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
-      for (int i = k * quarter; i < to; ++i, from += step_x) kept.copy(i, 0, from);
-      cp_async_commit();
-    }
-  }
-  Column<DT> col;
-  col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
-
   Moments mom;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    keep_wait(3 - k);
-    const int to = (k + 1) * quarter < held ? (k + 1) * quarter : held;
-#pragma unroll 4
-    for (int i = k * quarter; i < to; ++i) {
-      F2 v[4];
-      unpack_pairs(kept.get(i, 0), v);
-      mom.add(v, ln);
-    }
-    if (mom.n >= kStretch / 2) mom.join(ln);
-  }
-  for (int i0 = held; i0 < mine; i0 += kUnitBatch) {
-    const char* from = x + i0 * step_x;
-    Vec8<DT> raw[kUnitBatch];
+  // a batch of vectors is on its way while the one before is used
+  Vec8<DT> raw[kUnitBatch];
+  const char* from = x;
+  auto fetch = [&](int i0, bool again) {
 #pragma unroll
     for (int u = 0; u < kUnitBatch; ++u, from += step_x)
-      if (i0 + u < mine) load_pack(raw[u], from);
+      if (i0 + u < mine) {
+        if (again) load_again<DT>(raw[u], from);
+        else load_pack(raw[u], from);
+      }
+  };
+  fetch(0, true);
+  for (int i0 = 0; i0 < mine; i0 += kUnitBatch) {
+    F2 v[kUnitBatch][4];
+#pragma unroll
+    for (int u = 0; u < kUnitBatch; ++u) unpack_pairs(raw[u], v[u]);
+    fetch(i0 + kUnitBatch, true);
 #pragma unroll
     for (int u = 0; u < kUnitBatch; ++u)
-      if (i0 + u < mine) {
-        F2 v[4];
-        unpack_pairs(raw[u], v);
-        mom.add(v, ln);
-      }
+      if (i0 + u < mine) mom.add(v[u], ln);
     if (mom.n >= kStretch - kUnitBatch) mom.join(ln);
   }
   mom.join(ln);
+  from = x;
+  fetch(0, false);
   // the block's mean and M2 of each group of the slab, one warp a group
   if (ry < P.rows) sums[threadIdx.x] = make_float2(mom.mean, mom.m2);
   __syncthreads();
@@ -305,26 +280,18 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   __syncthreads();
   if (!on) return;
   const float2 st = stat[cx / P.q];
+  Column<DT> col;
+  col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
   fold_stats(col, st.x, st.y);
-#pragma unroll 2
-  for (int i = 0; i < held; ++i, out += step_out) {
-    F2 v[4];
-    unpack_pairs(kept.get(i, 0), v);
-    store_pack(out, norm_act<DT, true>(v, st.x, st.y, col, silu));
-  }
-  for (int i0 = held; i0 < mine; i0 += kUnitBatch) {
-    const char* from = x + i0 * step_x;
-    Vec8<DT> raw[kUnitBatch];
+  char* out = P.out[r] + row0 * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
+  for (int i0 = 0; i0 < mine; i0 += kUnitBatch) {
+    F2 v[kUnitBatch][4];
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u, from += step_x)
-      if (i0 + u < mine) load_pack(raw[u], from);
+    for (int u = 0; u < kUnitBatch; ++u) unpack_pairs(raw[u], v[u]);
+    fetch(i0 + kUnitBatch, false);
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u, out += step_out) {
-      if (i0 + u >= mine) continue;
-      F2 v[4];
-      unpack_pairs(raw[u], v);
-      store_pack(out, norm_act<DT, true>(v, st.x, st.y, col, silu));
-    }
+    for (int u = 0; u < kUnitBatch; ++u, out += step_out)
+      if (i0 + u < mine) store_pack(out, norm_act<DT, true>(v[u], st.x, st.y, col, silu));
   }
 }
 
@@ -395,32 +362,22 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   if (s.cols % 2 != 0 && 2 * s.cols <= nvec) fit_cols(2 * s.cols);
   s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
   s.threads = (s.rows * s.cols + 31) / 32 * 32;
-  // the fewest blocks a cluster that keep a sample's slab in shared memory with
-  // `resident` blocks on an SM, and give every SM its blocks
+  // The fewest blocks a cluster that fill the SMs one and a half times over and
+  // leave what the blocks at work read inside L2 (129 MB).  (8 samples of 4096 x
+  // 1280: clusters of 4 47 us forward and 82 backward, 8 52 and 86, 12 61 and 91;
+  // 64 samples of 256: 1 22 us, 2 34, 4 48.)
   const int slab_groups = s.cols / q;
-  const size_t vec = static_cast<size_t>(s.threads) * 8 * size * (bwd ? 2 : 1);
-  const int resident = bwd ? 2 : 3;
-  const size_t room = (bwd ? 112 : 66) * 1024;
-  auto need = [&](int cl) {
-    const int64_t per = (l + cl - 1) / cl;
-    return (per + s.rows - 1) / s.rows;
-  };
+  const int64_t resident = static_cast<int64_t>(kUnitBlocks) * sms;
+  const int64_t slab_bytes = l * s.cols * 8 * size * (bwd ? 2 : 1);
+  const int64_t units = n * t * s.slabs;
   static const int kClusters[] = {1, 2, 3, 4, 6, 8, 10, 12, kGroupMaxCluster};
   for (int cl : kClusters) {
-    if (cl > l) break;
+    if (cl > 1 && (l < static_cast<int64_t>(cl) * s.rows)) break;
     s.cluster = cl;
-    if (need(cl) * vec <= room && (n * t * s.slabs * cl >= resident * sms || need(cl) <= kUnitBatch))
-      break;
+    const int64_t at_once = resident / cl < units ? resident / cl : units;
+    if (2 * units * cl >= 3 * resident && at_once * slab_bytes <= (int64_t(128) << 20)) break;
   }
-  const size_t fixed = static_cast<size_t>(s.threads) * 8 +
-                       static_cast<size_t>(s.cluster + 1) * slab_groups * 8;
-  int64_t keep = need(s.cluster);
-  // What is not kept is read again.  Calls of few blocks keep no more than lets
-  // all of them run at once.
-  const size_t most = n * t * s.slabs * s.cluster <= 2 * sms ? 50 * 1024 : room;
-  if (keep * vec + fixed > most) keep = most > fixed ? static_cast<int64_t>((most - fixed) / vec) : 0;
-  s.keep = static_cast<int>(keep);
-  s.smem = s.keep * vec + fixed;
+  s.smem = (static_cast<size_t>(s.threads) + static_cast<size_t>(s.cluster + 1) * slab_groups) * 8;
   if (bwd) {
     const size_t part = static_cast<size_t>(s.rows) * s.cols * 17 * 4;
     if (s.smem < part) s.smem = part;
@@ -438,7 +395,6 @@ static void fill_shape(GroupNormParams* p, const GroupShape& s) {
   p->lanes = s.lanes;
   p->parts = s.parts;
   p->cluster = s.cluster;
-  p->keep = s.keep;
 }
 
 cudaError_t launch_group(const void* fn, GroupNormParams* p, const GroupShape& s, cudaStream_t st) {

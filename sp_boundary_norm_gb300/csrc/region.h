@@ -82,8 +82,8 @@ struct GroupNormParams {
   int32_t rows;                         // rows side by side in a block
   int32_t samples;                      // tiles: samples of a tile
   int32_t lanes;                        // tiles: lanes that sum one group of one sample
-  int64_t parts;                        // tiles: blocks of a slab; units: blocks of all samples
-  int32_t cluster, keep;                // units: blocks of a sample, rows a thread keeps
+  int64_t parts;                        // blocks of one rank's slab (units: of all samples)
+  int32_t cluster;                      // units: blocks of a sample
   float* ws;                            // backward: [parts][2][t * c]
   int32_t has_params;                   // backward: dgamma / dbeta wanted
 };
@@ -92,7 +92,7 @@ struct GroupNormParams {
 constexpr int kRowForm = 0, kTileForm = 1, kUnitForm = 2;
 struct GroupShape {
   int form, mode;
-  int cols, slabs, rows, threads, samples, lanes, cluster, keep;
+  int cols, slabs, rows, threads, samples, lanes, cluster;
   int64_t parts;
   size_t smem;
 };
