@@ -676,7 +676,7 @@ def _call(dev, fn, *args):
     """The call on the tensors' device and its current stream (the last argument)."""
     if dev.type != "cuda":
         raise ValueError(f"tensors on {dev}: the kernels need a CUDA device")
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)   # the current stream's handle
     if torch.cuda.current_device() == dev.index:
         _check(fn(*args, stream))
     else:

@@ -183,17 +183,26 @@ __device__ __forceinline__ int seq_of_run(const SeqWindow& win, const int* first
   return m != 0u ? first[31 - __clz(m)] : win.seq;
 }
 
-// A thread's two channels (from `ch`) of a sequence's state; NULL = zeros.
-__device__ __forceinline__ F2 load_state(const ScanParams& P, const float* src, int seq, int ch,
-                                         bool on) {
+// A thread's two channels (from `ch`) of a sequence's state; NULL = zeros.  (Not
+// inlined: a run with several marks asks for them from many places.)
+static __device__ __noinline__ F2 load_state(const float* src, int seq, int c, int ch, bool on) {
   if (src == nullptr || !on) return f2(0.f, 0.f);
-  const float2 v = *reinterpret_cast<const float2*>(src + static_cast<int64_t>(seq) * P.c + ch);
+  const float2 v = *reinterpret_cast<const float2*>(src + static_cast<int64_t>(seq) * c + ch);
   return f2(v.x, v.y);
 }
-__device__ __forceinline__ void store_state(const ScanParams& P, float* dst, int seq, int ch,
-                                            bool on, F2 v) {
+static __device__ __noinline__ void store_state(float* dst, int seq, int c, int ch, bool on, F2 v) {
   if (dst != nullptr && on)
-    *reinterpret_cast<float2*>(dst + static_cast<int64_t>(seq) * P.c + ch) = split(v);
+    *reinterpret_cast<float2*>(dst + static_cast<int64_t>(seq) * c + ch) = split(v);
+}
+
+// What a run has to look out for: nothing (whole and inside one sequence); at
+// most one beginning and one end, all 16 tokens there (their states come in
+// registers); anything.
+constexpr int kPlainRun = 0, kSingleRun = 1, kAnyRun = 2;
+
+__device__ __forceinline__ int run_kind(const RunMarks& m, int64_t left) {
+  if ((m.starts | m.ends) == 0u) return kPlainRun;
+  return __popc(m.starts) <= 1 && __popc(m.ends) <= 1 && left >= kScanRun ? kSingleRun : kAnyRun;
 }
 
 // A sequence without tokens passes its state (or its gradient) on.  By one

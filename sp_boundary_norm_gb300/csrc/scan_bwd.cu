@@ -14,33 +14,42 @@ namespace spb {
 constexpr int kBwdBlocks = 3;   // blocks an SM that the registers are held to
 
 // The run's factors, from its rows in shared memory: nk = -k, and dg = dgate
-// without its factor dh.  begin(i): the state before token i where a sequence
-// begins.
-template <int DT, bool TIED, bool MARKS, typename Shared, typename Begin>
+// without its factor dh.  i0, h0: the first token that begins a sequence and the
+// state before it, a0 its a; begin(i): the state before any other.
+template <int DT, bool TIED, int KIND, typename Shared, typename Begin>
 __device__ __forceinline__ void back_factors(const Shared& sh, int stage, uint32_t starts,
-                                             F2 h,
+                                             int i0, F2 h0, F2 h,
                                              F2 (&nk)[kScanRun], F2 (&dg)[kScanRun],
-                                             Two<DT> (&dy)[kScanRun], Begin begin) {
+                                             Two<DT> (&dy)[kScanRun], F2& a0,
+                                             Begin begin) {
 #pragma unroll
   for (int i = 0; i < kScanRun; ++i) {
-    if (MARKS && ((starts >> i) & 1u)) h = begin(i);
+    if (KIND == kSingleRun && i == i0) h = h0;
+    if (KIND == kAnyRun && ((starts >> i) & 1u)) h = begin(i);
     F2 e, d;
     nk[i] = neg_k<DT, true>(sh.template row<DT>(stage, 0, i), e);
     h = next_state<TIED>(nk[i], h, sh.template row<DT>(stage, 1, i), d);
     dg[i] = mul2(mul2(mul2(nk[i], nk[i]), e), d);            // a k d, a = e k
+    // a from e: 1 - k would lose a small one
+    if (KIND != kPlainRun && i == i0) a0 = mul2(mul2(e, nk[i]), f2(-1.f, -1.f));
     dy[i] = sh.template raw<DT>(stage, 2, i);
   }
 }
 
 // q leaving the run's first token as a map of the q entering its last one.
-// end(i): the q entering token i where a sequence ends.
-template <int DT, bool MARKS, typename End>
-__device__ __forceinline__ Map2 back_map(uint32_t ends, const F2 (&nk)[kScanRun],
+// i1, q1: the last token that ends a sequence and the q entering it; end(i): the
+// q entering any other.
+template <int DT, int KIND, typename End>
+__device__ __forceinline__ Map2 back_map(uint32_t ends, int i1, F2 q1, const F2 (&nk)[kScanRun],
                                          const Two<DT> (&dy)[kScanRun], End end) {
   F2 q = f2(0.f, 0.f), fac = f2(1.f, 1.f);
 #pragma unroll
   for (int i = kScanRun - 1; i >= 0; --i) {
-    if (MARKS && ((ends >> i) & 1u)) {
+    if (KIND == kSingleRun && i == i1) {
+      q = q1;
+      fac = f2(0.f, 0.f);
+    }
+    if (KIND == kAnyRun && ((ends >> i) & 1u)) {
       q = end(i);
       fac = f2(0.f, 0.f);
     }
@@ -105,64 +114,86 @@ __global__ void __launch_bounds__(32 * kScanWarps, kBwdBlocks) scan_bwd_kernel(c
   bool alive = true;
   for (int64_t base = last; base >= 0; base -= stretch, tok0 -= stretch, ++step) {
     const RunMarks marks = run_marks<PACKED>(P, tok0, win, sh.first, 15);
-    const bool plain = (marks.starts | marks.ends) == 0u;    // and then all 16 tokens exist
+    const int kind = run_kind(marks, P.s - tok0);
     auto seq = [&](int i) { return seq_of_run<PACKED>(win, sh.first, marks.starts, bi, i); };
-    auto begin = [&](int i) { return load_state(P, P.h0[r], seq(i), ch, on); };
-    auto end = [&](int i) { return load_state(P, P.dhT[r], seq(i), ch, on); };
+    auto begin = [&](int i) { return load_state(P.h0[r], seq(i), P.c, ch, on); };
+    auto end = [&](int i) { return load_state(P.dhT[r], seq(i), P.c, ch, on); };
+    // (the first beginning's state and the last end's gradient are asked for
+    // beneath the wait for the rows)
+    const int i0 = __ffs(marks.starts) - 1, i1 = 31 - __clz(marks.ends);
+    F2 h0 = f2(0.f, 0.f), q1 = h0;
+    if (i0 >= 0) h0 = begin(i0);
+    if (i1 >= 0) q1 = end(i1);
     Two<DT> dy[kScanRun];
-    F2 nk[kScanRun], dg[kScanRun];
+    F2 nk[kScanRun], dg[kScanRun], a0 = f2(0.f, 0.f);
     sh.wait();
     const int stage = step % kStages;
     const F2 h = f2(entering.x, entering.y);
-    if (plain)
-      back_factors<DT, TIED, false>(sh, stage, 0u, h, nk, dg, dy, begin);
+    if (kind == kPlainRun)
+      back_factors<DT, TIED, kPlainRun>(sh, stage, 0u, 0, h0, h, nk, dg, dy, a0, begin);
+    else if (kind == kSingleRun)
+      back_factors<DT, TIED, kSingleRun>(sh, stage, 0u, i0, h0, h, nk, dg, dy, a0, begin);
     else
-      back_factors<DT, TIED, true>(sh, stage, marks.starts, h, nk, dg, dy, begin);
+      back_factors<DT, TIED, kAnyRun>(sh, stage, marks.starts, i0, h0, h, nk, dg, dy, a0, begin);
     __syncwarp();                     // every lane has read the rows
     fetch(stage, tok0 - kStages * stretch);
     fetch_entering(tok0 - stretch);
-    const Map2 mine = plain ? back_map<DT, false>(0u, nk, dy, end)
-                            : back_map<DT, true>(marks.ends, nk, dy, end);
+    Map2 mine;
+    if (kind == kPlainRun) mine = back_map<DT, kPlainRun>(0u, 0, q1, nk, dy, end);
+    else if (kind == kSingleRun) mine = back_map<DT, kSingleRun>(0u, i1, q1, nk, dy, end);
+    else mine = back_map<DT, kAnyRun>(marks.ends, 0, q1, nk, dy, end);
     F2 into = join_runs<PACKED, -1>(sh.join, step, mine, C, rank, warp, nw, carry, alive);
     if (tok0 >= P.s) continue;
     char* at_g = dgate + tok0 * P.ld_out;
     char* at_v = dvalue + tok0 * P.ld_dvalue;
     const F2 minus = f2(-1.f, -1.f);
-    if (plain) {
+    auto put = [&](int i, F2 dh) {
+      store_pack(at_g + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(mul2(dh, dg[i])));
+      store_pack(at_v + static_cast<uint64_t>(P.ld_dvalue) * i,
+                 pack2<DT>(TIED ? mul2(mul2(dh, minus), nk[i]) : dh));
+    };
+    if (kind == kPlainRun) {
       if (on) {
 #pragma unroll
         for (int i = kScanRun - 1; i >= 0; --i) {
           const F2 dh = add2(unpack2<DT>(dy[i]), into);
           into = fma2(nk[i], dh, dh);
-          store_pack(at_g + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(mul2(dh, dg[i])));
-          store_pack(at_v + static_cast<uint64_t>(P.ld_dvalue) * i,
-                     pack2<DT>(TIED ? mul2(mul2(dh, minus), nk[i]) : dh));
+          put(i, dh);
         }
       }
-      continue;
-    }
-    const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
+    } else if (kind == kSingleRun) {
+      F2 first = f2(0.f, 0.f);
 #pragma unroll
-    for (int i = kScanRun - 1; i >= 0; --i) {
-      if ((marks.ends >> i) & 1u) into = end(i);
-      const F2 dh = add2(unpack2<DT>(dy[i]), into);
-      into = fma2(nk[i], dh, dh);
-      if ((marks.starts >> i) & 1u) store_state(P, P.hT[r], seq(i), ch, on, dh);
-      if (on && i < rows) {
-        store_pack(at_g + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(mul2(dh, dg[i])));
-        store_pack(at_v + static_cast<uint64_t>(P.ld_dvalue) * i,
-                   pack2<DT>(TIED ? mul2(mul2(dh, minus), nk[i]) : dh));
+      for (int i = kScanRun - 1; i >= 0; --i) {
+        if (i == i1) into = q1;
+        const F2 dh = add2(unpack2<DT>(dy[i]), into);
+        into = fma2(nk[i], dh, dh);
+        if (i == i0) first = dh;
+        if (on) put(i, dh);
       }
-    }
-    if (P.hT[r] != nullptr && on) {
-      // dh0 = a dh: a = e k from the gate again, where 1 - k would lose a small one
-      for (uint32_t left = marks.starts; left != 0; left &= left - 1) {
-        const int i = __ffs(left) - 1, j = seq(i);
-        Two<DT> graw;
-        load_pack(graw, P.gate[r] + (row0 + tok0 + i) * P.ld_gate + col);
-        F2 e;
-        const F2 a = mul2(neg_k<DT, true>(unpack2<DT>(graw), e), e);
-        store_state(P, P.hT[r], j, ch, on, mul2(mul2(a, minus), load_state(P, P.hT[r], j, ch, on)));
+      if (i0 >= 0) store_state(P.hT[r], seq(i0), P.c, ch, on, mul2(a0, first));
+    } else {
+      const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
+#pragma unroll
+      for (int i = kScanRun - 1; i >= 0; --i) {
+        if ((marks.ends >> i) & 1u) into = end(i);
+        const F2 dh = add2(unpack2<DT>(dy[i]), into);
+        into = fma2(nk[i], dh, dh);
+        if ((marks.starts >> i) & 1u)
+          store_state(P.hT[r], seq(i), P.c, ch, on, i == i0 ? mul2(a0, dh) : dh);
+        if (on && i < rows) put(i, dh);
+      }
+      if (P.hT[r] != nullptr && on) {
+        // further beginnings in the run: dh0 = a dh with a from the gate again
+        for (uint32_t left = marks.starts & (marks.starts - 1u); left != 0; left &= left - 1) {
+          const int i = __ffs(left) - 1, j = seq(i);
+          Two<DT> graw;
+          load_pack(graw, P.gate[r] + (row0 + tok0 + i) * P.ld_gate + col);
+          F2 e;
+          const F2 a = mul2(neg_k<DT, true>(unpack2<DT>(graw), e), e);
+          store_state(P.hT[r], j, P.c, ch, on,
+                      mul2(mul2(a, minus), load_state(P.hT[r], j, P.c, ch, on)));
+        }
       }
     }
   }

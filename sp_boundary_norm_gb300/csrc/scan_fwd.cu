@@ -8,14 +8,20 @@ namespace spb {
 constexpr int kFwdBlocks = 4;   // blocks an SM that the registers are held to
 
 // One run: h[i], f[i] with h[i] + f[i] * (state entering the run) the state
-// after token i.  begin(i): the state before token i where a sequence begins.
-template <int DT, bool TIED, bool MARKS, typename Shared, typename Begin>
-__device__ __forceinline__ Map2 scan_run(const Shared& sh, int stage, uint32_t starts,
-                                         F2 (&h)[kScanRun], F2 (&f)[kScanRun], Begin begin) {
+// after token i.  i0, h0: the first token that begins a sequence and the state
+// before it; begin(i): that of any other.
+template <int DT, bool TIED, int KIND, typename Shared, typename Begin>
+__device__ __forceinline__ Map2 scan_run(const Shared& sh, int stage, uint32_t starts, int i0,
+                                         F2 h0, F2 (&h)[kScanRun], F2 (&f)[kScanRun],
+                                         Begin begin) {
   F2 cur = f2(0.f, 0.f), fac = f2(1.f, 1.f);
 #pragma unroll
   for (int i = 0; i < kScanRun; ++i) {
-    if (MARKS && ((starts >> i) & 1u)) {
+    if (KIND == kSingleRun && i == i0) {
+      cur = h0;
+      fac = f2(0.f, 0.f);
+    }
+    if (KIND == kAnyRun && ((starts >> i) & 1u)) {
       cur = begin(i);
       fac = f2(0.f, 0.f);
     }
@@ -30,7 +36,8 @@ __device__ __forceinline__ Map2 scan_run(const Shared& sh, int stage, uint32_t s
 }
 
 template <int DT, bool TIED, bool PACKED>
-__global__ void __launch_bounds__(32 * kScanWarps, kFwdBlocks) scan_fwd_kernel(const ScanParams P) {
+__global__ void __launch_bounds__(32 * kScanWarps, PACKED ? kFwdBlocks - 1 : kFwdBlocks)
+scan_fwd_kernel(const ScanParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
@@ -72,14 +79,23 @@ __global__ void __launch_bounds__(32 * kScanWarps, kFwdBlocks) scan_fwd_kernel(c
   bool alive = true;
   for (int64_t base = 0; base < P.s; base += stretch, tok0 += stretch, ++step) {
     const RunMarks marks = run_marks<PACKED>(P, tok0, win, sh.first, 0);
-    const bool plain = (marks.starts | marks.ends) == 0u;    // and then all 16 tokens exist
+    const int kind = run_kind(marks, P.s - tok0);
     auto seq = [&](int i) { return seq_of_run<PACKED>(win, sh.first, marks.starts, bi, i); };
-    auto begin = [&](int i) { return load_state(P, P.h0[r], seq(i), ch, on); };
+    auto begin = [&](int i) { return load_state(P.h0[r], seq(i), P.c, ch, on); };
+    // (the first beginning's state is asked for beneath the wait for the rows)
+    const int i0 = __ffs(marks.starts) - 1, i1 = 31 - __clz(marks.ends);
+    F2 h0 = f2(0.f, 0.f);
+    if (i0 >= 0) h0 = begin(i0);
     F2 h[kScanRun], f[kScanRun];
     sh.wait();
     const int stage = step % kStages;
-    const Map2 mine = plain ? scan_run<DT, TIED, false>(sh, stage, 0u, h, f, begin)
-                            : scan_run<DT, TIED, true>(sh, stage, marks.starts, h, f, begin);
+    Map2 mine;
+    if (kind == kPlainRun)
+      mine = scan_run<DT, TIED, kPlainRun>(sh, stage, 0u, 0, h0, h, f, begin);
+    else if (kind == kSingleRun)
+      mine = scan_run<DT, TIED, kSingleRun>(sh, stage, 0u, i0, h0, h, f, begin);
+    else
+      mine = scan_run<DT, TIED, kAnyRun>(sh, stage, marks.starts, 0, h0, h, f, begin);
     __syncwarp();                     // every lane has read the rows
     fetch(stage, tok0 + kStages * stretch);
     const F2 entry = join_runs<PACKED, 1>(sh.join, step, mine, C, rank, warp, nw, carry, alive);
@@ -87,20 +103,29 @@ __global__ void __launch_bounds__(32 * kScanWarps, kFwdBlocks) scan_fwd_kernel(c
     if (states != nullptr && on)
       __stcs(reinterpret_cast<float2*>(states + (tok0 / kScanRun) * P.c), split(entry));
     char* at = out + tok0 * P.ld_out;
-    if (plain) {
+    if (kind == kPlainRun) {
       if (on) {
 #pragma unroll
         for (int i = 0; i < kScanRun; ++i)
           store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(fma2(f[i], entry, h[i])));
       }
-      continue;
-    }
-    const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
+    } else if (kind == kSingleRun) {
+      F2 last = f2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kScanRun; ++i) {
-      const F2 y = through<PACKED>(f[i], h[i], entry);
-      if ((marks.ends >> i) & 1u) store_state(P, P.hT[r], seq(i), ch, on, y);
-      if (on && i < rows) store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(y));
+      for (int i = 0; i < kScanRun; ++i) {
+        const F2 y = through<PACKED>(f[i], h[i], entry);
+        if (i == i1) last = y;
+        if (on) store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(y));
+      }
+      if (i1 >= 0) store_state(P.hT[r], seq(i1), P.c, ch, on, last);
+    } else {
+      const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
+#pragma unroll
+      for (int i = 0; i < kScanRun; ++i) {
+        const F2 y = through<PACKED>(f[i], h[i], entry);
+        if ((marks.ends >> i) & 1u) store_state(P.hT[r], seq(i), P.c, ch, on, y);
+        if (on && i < rows) store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(y));
+      }
     }
   }
   cp_async_wait<0>();
