@@ -18,8 +18,8 @@ struct RopeParams {
   int32_t all_heads, heads;               // over all ranks, of one rank
   uint32_t heads_magic;                   // ceil(2^32 / heads)
   int32_t half;                           // rotated pairs of a head
-  int32_t rest;                           // elements after them to copy (0 in place)
-  int32_t rest_at;                        // first of them
+  int32_t rest, rest_at, rest_bytes;      // bytes after them to copy (0 in place), the first,
+                                          // bytes of one access
   int32_t chunks, chunk_heads;            // pieces of a token's heads, one warp each
   int32_t layout;
   const int64_t* positions;

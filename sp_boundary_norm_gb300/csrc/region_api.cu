@@ -120,7 +120,7 @@ sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, 
   // the widest accesses that the sizes and strides allow
   const int64_t block = layout == SP_ROPE_HALF ? table->pairs : rot;
   int vec = 16 / size;
-  while (vec > 1 && (block % vec != 0 || d % vec != 0 || x_ld % vec != 0 || x_head % vec != 0 ||
+  while (vec > 1 && (block % vec != 0 || x_ld % vec != 0 || x_head % vec != 0 ||
                      y_ld % vec != 0 || y_head % vec != 0))
     vec /= 2;
 
@@ -140,8 +140,13 @@ sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, 
   P.heads_magic = heads == 1 ? 0u
                              : static_cast<uint32_t>(((uint64_t(1) << 32) + heads - 1) / heads);
   P.half = table->pairs;
-  P.rest_at = static_cast<int32_t>(rot);
-  P.rest = in_place ? 0 : static_cast<int32_t>(d - rot);
+  P.rest_at = static_cast<int32_t>(rot) * size;
+  P.rest = in_place ? 0 : static_cast<int32_t>(d - rot) * size;
+  P.rest_bytes = 16;
+  while (P.rest_bytes > size && (P.rest_at % P.rest_bytes != 0 || P.rest % P.rest_bytes != 0 ||
+                                 P.x_row % P.rest_bytes != 0 || P.x_head % P.rest_bytes != 0 ||
+                                 P.y_row % P.rest_bytes != 0 || P.y_head % P.rest_bytes != 0))
+    P.rest_bytes /= 2;
   P.layout = layout;
   P.positions = positions;
   P.first = first;

@@ -17,7 +17,7 @@
 namespace spb {
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeUnroll = 4;
+constexpr int kRopeRounds = 4;    // of heads side by side that a lane reads at once
 
 // a / b for 0 <= a < most: in 32 bits where they do (a 64-bit division costs a
 // hundred instructions).
@@ -28,17 +28,58 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t most) {
   return a / b;
 }
 
-// V elements a load.  Half layout: a lane's item is V pairs (V elements of
-// each half).  Interleaved: V / 2 pairs that lie together, or for V = 1 one
-// pair by two loads.
 __device__ __forceinline__ int rank_of_head(const RopeParams& P, int hh) {
   return P.heads == 1 ? hh : static_cast<int>(__umulhi(static_cast<uint32_t>(hh), P.heads_magic));
 }
 
+// Blocks an SM that the registers are held to: by what a lane has on its way.
+constexpr int rope_blocks(int dt, int v, int layout) {
+  const int bytes = v * (dt == SP_F32 ? 4 : 2) * (layout == SP_ROPE_HALF || v == 1 ? 2 : 1);
+  return bytes >= 32 ? 2 : 4;
+}
+
+// Copies what follows the rotated elements of a token's heads h0 .. h1 - 1, B
+// bytes a lane, several heads side by side and four rounds at once.
+template <int B>
+__device__ __forceinline__ void copy_rest(const RopeParams& P, int64_t tok, int h0, int h1) {
+  constexpr int kRounds = 4;
+  const int lane = threadIdx.x & 31;
+  const int items = P.rest / B, width = items < 32 ? items : 32, abreast = 32 / width;
+  const int my = lane % width, sub = lane / width;
+  for (int item = my; item < items; item += width) {
+    for (int hb = h0; hb < h1; hb += abreast * kRounds) {
+      Pack<SP_BF16, B / 2> p[kRounds];
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k) {
+        const int hh = hb + k * abreast + sub;
+        if (sub < abreast && hh < h1) {
+          const int r = rank_of_head(P, hh);
+          load_pack(p[k], P.x[r] + tok * P.x_row + (hh - r * P.heads) * P.x_head + P.rest_at +
+                              item * B);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kRounds; ++k) {
+        const int hh = hb + k * abreast + sub;
+        if (sub < abreast && hh < h1) {
+          const int r = rank_of_head(P, hh);
+          store_pack(P.y[r] + tok * P.y_row + (hh - r * P.heads) * P.y_head + P.rest_at + item * B,
+                     p[k]);
+        }
+      }
+    }
+  }
+}
+
+// V elements a load.  Half layout: a lane's item is V pairs (V elements of
+// each half).  Interleaved: V / 2 pairs that lie together, or for V = 1 one
+// pair by two loads.
 template <int DT, int V, int LAYOUT>
-__global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams P) {
+__global__ void __launch_bounds__(32 * kRopeWarps, rope_blocks(DT, V, LAYOUT))
+rope_kernel(const RopeParams P) {
   constexpr int E = ElemSize<DT>::value;
   constexpr bool kTwo = LAYOUT == SP_ROPE_HALF || V == 1;   // an item is two loads
+  constexpr int U = kTwo || V * E < 16 ? kRopeRounds : 2 * kRopeRounds;
   constexpr int kPairs = kTwo ? V : V / 2;
   __shared__ float2 cs[kRopeWarps][SP_ROPE_MAX_PAIRS];
   pdl_wait();
@@ -49,8 +90,9 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
   const int width = items < 32 ? items : 32;         // lanes of a head
   const int abreast = 32 / width;                    // heads side by side
   const int my = lane % width, sub = lane / width;
+  constexpr int kStep = (V == 1 && LAYOUT != SP_ROPE_HALF ? 2 : V) * E;   // bytes between items
   // bytes from an item's first load to its second
-  const int64_t second = LAYOUT == SP_ROPE_HALF ? static_cast<int64_t>(P.half) * E : E;
+  const uint32_t second = LAYOUT == SP_ROPE_HALF ? static_cast<uint32_t>(P.half) * E : E;
   const int64_t n_tasks = P.tokens * P.chunks;
   for (int64_t task = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; task < n_tasks;
        task += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
@@ -58,6 +100,21 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
     const int chunk = static_cast<int>(task - tok * P.chunks);
     const int h0 = chunk * P.chunk_heads;
     const int h1 = h0 + P.chunk_heads < P.all_heads ? h0 + P.chunk_heads : P.all_heads;
+    Pack<DT, V> a[U], b[U];
+    auto fetch = [&](int hb, int item) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int hh = hb + k * abreast + sub;
+        if (sub < abreast && item < items && hh < h1) {
+          const int r = rank_of_head(P, hh);
+          const char* src = P.x[r] + tok * P.x_row + (hh - r * P.heads) * P.x_head + item * kStep;
+          load_pack(a[k], src);
+          if constexpr (kTwo) load_pack(b[k], src + second);
+        }
+      }
+    };
+    // the first heads are on their way while the angles are computed
+    fetch(h0, my);
     int64_t pos;
     if (P.positions != nullptr) {
       pos = __ldg(P.positions + tok);
@@ -86,25 +143,14 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
         cn[i] = v.x;
         sn[i] = v.y;
       }
-      const int64_t at = static_cast<int64_t>(item) * (V == 1 && LAYOUT != SP_ROPE_HALF ? 2 : V) * E;
-      for (int hb = h0; hb < h1; hb += abreast * kRopeUnroll) {
-        Pack<DT, V> a[kRopeUnroll], b[kRopeUnroll];
+      for (int hb = h0; hb < h1; hb += abreast * U) {
+        if (v0 > 0 || hb > h0) fetch(hb, item);
 #pragma unroll
-        for (int k = 0; k < kRopeUnroll; ++k) {
+        for (int k = 0; k < U; ++k) {
           const int hh = hb + k * abreast + sub;
           if (on && hh < h1) {
             const int r = rank_of_head(P, hh);
-            const char* src = P.x[r] + tok * P.x_row + (hh - r * P.heads) * P.x_head + at;
-            load_pack(a[k], src);
-            if constexpr (kTwo) load_pack(b[k], src + second);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kRopeUnroll; ++k) {
-          const int hh = hb + k * abreast + sub;
-          if (on && hh < h1) {
-            const int r = rank_of_head(P, hh);
-            char* dst = P.y[r] + tok * P.y_row + (hh - r * P.heads) * P.y_head + at;
+            char* dst = P.y[r] + tok * P.y_row + (hh - r * P.heads) * P.y_head + item * kStep;
             float x[V];
             unpack(a[k], x);
             if constexpr (kTwo) {
@@ -135,14 +181,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeParams 
       }
     }
     // the part of the heads that is not rotated
-    const int tail = P.rest / V;
-    for (int i = lane; i < tail * (h1 - h0); i += 32) {
-      const int hh = h0 + i / tail;
-      const int r = rank_of_head(P, hh);
-      const int64_t at = static_cast<int64_t>(P.rest_at + (i % tail) * V) * E;
-      Pack<DT, V> a;
-      load_pack(a, P.x[r] + tok * P.x_row + (hh - r * P.heads) * P.x_head + at);
-      store_pack(P.y[r] + tok * P.y_row + (hh - r * P.heads) * P.y_head + at, a);
+    if (P.rest > 0) {
+      if (P.rest_bytes == 16) copy_rest<16>(P, tok, h0, h1);
+      else if (P.rest_bytes == 8) copy_rest<8>(P, tok, h0, h1);
+      else if (P.rest_bytes == 4) copy_rest<4>(P, tok, h0, h1);
+      else copy_rest<2>(P, tok, h0, h1);
     }
   }
 }

@@ -161,6 +161,42 @@ def test_rope_packed_positions_and_strides():
     assert (odd.as_strided((7, 5), (208, 41), 40) == 0).all()
 
 
+@pytest.mark.parametrize("t,heads,d,rot,layout,dtype", [
+    (1, 5, 80, 20, "half", BF), (1, 5, 80, 20, "interleaved", FP), (2, 1, 32, 32, "half", F32),
+    (1, 1, 8, 2, "interleaved", BF), (1, 3, 15, 6, "half", BF), (1, 2, 128, 128, "half", BF),
+    (1, 1, 512, 512, "interleaved", FP)])
+@pytest.mark.parametrize("where", ["dense", "packed", "positions"])
+def test_rope_many_small_tokens(t, heads, d, rot, layout, dtype, where):
+    """Enough tokens that a warp takes several at once, the last group cut short; a
+    sample of them against the oracle."""
+    gen = torch.Generator().manual_seed(19)
+    b, s = (1, 40003) if where == "packed" else (3, 13339)
+    x = [rand((b, s, heads, d), gen, dtype) for _ in range(t)]
+    y = [torch.full_like(q, float("nan")) for q in x]
+    rng = np.random.default_rng(3)
+    cu = pos = None
+    want_pos = orc.positions(b, s, 9)
+    if where == "packed":
+        cu = np.concatenate(([0, 0, 1], np.sort(rng.integers(1, s, 300)), [s]))
+        want_pos = orc.positions(1, s, 9, cu)
+        cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    if where == "positions":
+        want_pos = rng.integers(0, 1 << 20, (b, s))
+        pos = torch.tensor(want_pos, device=DEV)
+    tab = sp.sp_rope_table(rot)
+    how = dict(layout=layout, positions=pos, first_position=9, cu_seqlens=cu)
+    sp.sp_rope_fwd(x, tab, y=y, **how)
+    at = np.unique(np.concatenate((rng.integers(0, s, 300), np.arange(20), np.arange(s - 20, s))))
+    for r in range(t):
+        want, mag = orc.rope(f64(x[r])[:, at], want_pos[:, at], orc.frequencies(rot), layout)
+        close(y[r][:, at], want, mag, 2.0 ** -21, where)
+    back = [torch.empty_like(q) for q in x]
+    sp.sp_rope_bwd(x, tab, dx=back, **how)
+    for r in range(t):
+        want, mag = orc.rope(f64(x[r])[:, at], want_pos[:, at], orc.frequencies(rot), layout, back=True)
+        close(back[r][:, at], want, mag, 2.0 ** -21, where)
+
+
 def test_rope_many_sequences():
     """More packed sequences than one search step reaches."""
     rng = np.random.default_rng(1)
