@@ -598,9 +598,8 @@ def _row_stride(shape, strides, what):
 _module = None
 
 
-def _matching(xs, shape, dtype, device):
-    """Pointer array and common strides of rank buffers, or None where they are not
-    all tensors of that shape and type on that device with equal strides."""
+def _readers():
+    """The compiled readers of lists of rank buffers."""
     global _module
     if _module is None:
         if not os.path.exists(_build.MODULE_PATH):
@@ -608,49 +607,60 @@ def _matching(xs, shape, dtype, device):
         spec = importlib.util.spec_from_file_location("_sptensors", _build.MODULE_PATH)
         _module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_module)
-    return _module.same(xs, shape, DTYPES[dtype], -1 if device.index is None else device.index)
+    return _module
 
 
 def _pointers(xs):
     return (_vp * len(xs))(*[x.data_ptr() for x in xs])
 
 
-def _rank_rows(xs, shape, dtype, device, t, what):
-    """Pointer array and row stride of t rank buffers."""
-    got = _matching(xs, shape, dtype, device)
-    if got is not None and len(xs) == t:
-        return got[0], _row_stride(shape, got[1], what)
+def _rank_buffers(xs, x0, t, what):
+    """Checks that xs are t buffers of x0's shape, type and device, one by one."""
     if len(xs) != t:
         raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
-    ld = None
     for i, x in enumerate(xs):
         if not isinstance(x, torch.Tensor):
             raise TypeError(f"{what}[{i}] must be a torch.Tensor")
-        if x.shape != shape:
-            raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(shape)}")
-        if x.dtype is not dtype:
-            raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {dtype}")
-        if x.device != device:
-            raise ValueError(f"{what}[{i}]: on {x.device}, expected {device}")
-        got = _row_stride(x.shape, x.stride(), what)
-        if ld is not None and got != ld:
+        if x.shape != x0.shape:
+            raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(x0.shape)}")
+        if x.dtype is not x0.dtype:
+            raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {x0.dtype}")
+        if x.device != x0.device:
+            raise ValueError(f"{what}[{i}]: on {x.device}, expected {x0.device}")
+
+
+def _rank_rows(x0, t, **lists):
+    """Pointer array and row stride of each list of t rank buffers, which are of x0's
+    shape, type and device."""
+    got = _readers().rows(x0, t, *lists.values())
+    if got is not None:
+        return got
+    out = []
+    for what, xs in lists.items():
+        _rank_buffers(xs, x0, t, what)
+        lds = [_row_stride(x.shape, x.stride(), what) for x in xs]
+        if any(ld != lds[0] for ld in lds):
             raise ValueError(f"{what}: every rank needs the same row stride")
-        ld = got
-    return _pointers(xs), ld
+        out += [_pointers(xs), lds[0]]
+    return out
 
 
-def _rank_dense(xs, shape, dtype, device, t, what):
-    """Pointer array of t dense rank buffers (None: no array)."""
-    if xs is None:
-        return None
-    got = _matching(xs, shape, dtype, device)
-    if got is not None and len(xs) == t and _dense(shape, got[1]):
-        return got[0]
-    if len(xs) != t:
-        raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
-    for i, x in enumerate(xs):
-        _need(x, shape, dtype, device, f"{what}[{i}]")
-    return _pointers(xs)
+def _rank_floats(x0, t, shape, **lists):
+    """Pointer array of each list of t dense float32 rank buffers (None: no array)."""
+    got = _readers().floats(x0, t, shape, *lists.values())
+    if got is not None:
+        return got
+    out = []
+    for what, xs in lists.items():
+        if xs is None:
+            out.append(None)
+            continue
+        if len(xs) != t:
+            raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
+        for i, x in enumerate(xs):
+            _need(x, shape, torch.float32, x0.device, f"{what}[{i}]")
+        out.append(_pointers(xs))
+    return out
 
 
 def _first(xs, dims, what):
@@ -706,50 +716,47 @@ def sp_rope_table(rot_dim, *, base=10000.0, scaling="none", factor=1.0, original
     return out
 
 
-def _rope_strides(xs, shape, dtype, device, t, what):
-    """Pointer array, token stride and head stride of (b, s, heads, d) buffers."""
-    b, s, heads, d = shape
-    got = _matching(xs, shape, dtype, device)
-    if got is None or len(xs) != t:
-        if len(xs) != t:
-            raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
-        for i, x in enumerate(xs):
-            if not isinstance(x, torch.Tensor):
-                raise TypeError(f"{what}[{i}] must be a torch.Tensor")
-            if x.shape != shape:
-                raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(shape)}")
-            if x.dtype is not dtype:
-                raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {dtype}")
-            if x.device != device:
-                raise ValueError(f"{what}[{i}]: on {x.device}, expected {device}")
-            if x.stride() != xs[0].stride():
-                raise ValueError(f"{what}: every rank needs the same strides")
-        got = _pointers(xs), xs[0].stride()
-    if _dense(shape, got[1]):
-        return got[0], heads * d, d
-    s0, s1, s2, s3 = got[1]
+def _head_strides(x, what):
+    """Token stride and head stride of a (b, s, heads, d) buffer."""
+    b, s, heads, d = x.shape
+    if _dense(x.shape, x.stride()):
+        return heads * d, d
+    s0, s1, s2, s3 = x.stride()
     if d > 1 and s3 != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     if heads == 1:
         s2 = d
     if s > 1:
-        ld = s1
         if b > 1 and s0 != s * s1:
             raise ValueError(f"{what}: batch rows must follow each other")
-    else:
-        ld = s0 if b > 1 else max(s1, heads * s2)
-    return got[0], ld, s2
+        return s1, s2
+    return (s0 if b > 1 else max(s1, heads * s2)), s2
+
+
+def _rank_heads(x0, t, **lists):
+    """Pointer array, token stride and head stride of each list of t (b, s, heads, d)
+    rank buffers, which are of x0's shape, type and device."""
+    got = _readers().heads(x0, t, *lists.values())
+    if got is not None:
+        return got
+    out = []
+    for what, xs in lists.items():
+        _rank_buffers(xs, x0, t, what)
+        strides = [_head_strides(x, what) for x in xs]
+        if any(st != strides[0] for st in strides):
+            raise ValueError(f"{what}: every rank needs the same strides")
+        out += [_pointers(xs), *strides[0]]
+    return out
 
 
 def _rope_call(entry, x, table, layout, positions, first_position, cu_seqlens, y, status):
     lib = load()
     t, x0, dt = _first(x, 4, "x")
     b, s, heads, d = x0.shape
-    dev, dtype = x0.device, x0.dtype
+    dev = x0.device
     if not isinstance(table, RopeTable):
         raise TypeError("table must come from sp_rope_table")
-    xa, x_ld, x_head = _rope_strides(x, x0.shape, dtype, dev, t, "x")
-    ya, y_ld, y_head = _rope_strides(y, x0.shape, dtype, dev, t, "y")
+    xa, x_ld, x_head, ya, y_ld, y_head = _rank_heads(x0, t, x=x, y=y)
     if positions is not None:
         _need(positions, (b, s), torch.int64, dev, "positions")
     cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
@@ -788,15 +795,14 @@ def sp_gated_scan_fwd(gate, value, *, h0=None, tied=True, cu_seqlens=None, y, hT
     lib = load()
     t, x0, dt = _first(gate, 3, "gate")
     b, s, c = x0.shape
-    dev, dtype, f32 = x0.device, x0.dtype, torch.float32
-    ga, g_ld = _rank_rows(gate, x0.shape, dtype, dev, t, "gate")
-    va, v_ld = _rank_rows(value, x0.shape, dtype, dev, t, "value")
-    ya, y_ld = _rank_rows(y, x0.shape, dtype, dev, t, "y")
+    dev = x0.device
+    ga, g_ld, va, v_ld, ya, y_ld = _rank_rows(x0, t, gate=gate, value=value, y=y)
     cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
     n = b if cu is None else n_seqs
-    ha = _rank_dense(h0, (n, c), f32, dev, t, "h0")
-    ta = _rank_dense(hT, (n, c), f32, dev, t, "hT")
-    sa = _rank_dense(states, sp_gated_scan_states_shape(b, s, c), f32, dev, t, "states")
+    ha, ta = _rank_floats(x0, t, (n, c), h0=h0, hT=hT)
+    sa = None
+    if states is not None:
+        sa, = _rank_floats(x0, t, sp_gated_scan_states_shape(b, s, c), states=states)
     st = _status_word(dev) if status is None else status
     _call(dev, lib.sp_gated_scan_fwd, ga, g_ld, va, v_ld, ha, b, s, c, t, dt, int(bool(tied)), cu,
           n_seqs, ya, y_ld, ta, sa, st.data_ptr())
@@ -809,18 +815,13 @@ def sp_gated_scan_bwd(gate, value, states, dy, *, h0=None, dhT=None, tied=True, 
     lib = load()
     t, x0, dt = _first(gate, 3, "gate")
     b, s, c = x0.shape
-    dev, dtype, f32 = x0.device, x0.dtype, torch.float32
-    ga, g_ld = _rank_rows(gate, x0.shape, dtype, dev, t, "gate")
-    va, v_ld = _rank_rows(value, x0.shape, dtype, dev, t, "value")
-    da, d_ld = _rank_rows(dy, x0.shape, dtype, dev, t, "dy")
-    dga, dg_ld = _rank_rows(dgate, x0.shape, dtype, dev, t, "dgate")
-    dva, dv_ld = _rank_rows(dvalue, x0.shape, dtype, dev, t, "dvalue")
+    dev = x0.device
+    ga, g_ld, va, v_ld, da, d_ld, dga, dg_ld, dva, dv_ld = _rank_rows(
+        x0, t, gate=gate, value=value, dy=dy, dgate=dgate, dvalue=dvalue)
     cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
     n = b if cu is None else n_seqs
-    ha = _rank_dense(h0, (n, c), f32, dev, t, "h0")
-    ta = _rank_dense(dhT, (n, c), f32, dev, t, "dhT")
-    oa = _rank_dense(dh0, (n, c), f32, dev, t, "dh0")
-    sa = _rank_dense(states, sp_gated_scan_states_shape(b, s, c), f32, dev, t, "states")
+    ha, ta, oa = _rank_floats(x0, t, (n, c), h0=h0, dhT=dhT, dh0=dh0)
+    sa, = _rank_floats(x0, t, sp_gated_scan_states_shape(b, s, c), states=states)
     st = _status_word(dev) if status is None else status
     _call(dev, lib.sp_gated_scan_bwd, ga, g_ld, va, v_ld, ha, sa, da, d_ld, ta, b, s, c, t, dt,
           int(bool(tied)), cu, n_seqs, dga, dg_ld, dva, dv_ld, oa, st.data_ptr())
@@ -837,15 +838,13 @@ def sp_group_norm_fwd(x, gamma, beta=None, *, groups, eps, norm="layernorm", act
     n, l, c = x0.shape
     dev, dtype = x0.device, x0.dtype
     ln = norm == "layernorm"
-    xa, x_ld = _rank_rows(x, x0.shape, dtype, dev, t, "x")
-    ya, y_ld = _rank_rows(y, x0.shape, dtype, dev, t, "y")
+    xa, x_ld, ya, y_ld = _rank_rows(x0, t, x=x, y=y)
     _need(gamma, (t * c,), dtype, dev, "gamma")
     if ln:
         _need(beta, (t * c,), dtype, dev, "beta")
         if mean is None:
             raise ValueError("mean is required for layernorm")
-    ma = _rank_dense(mean, (n, groups), torch.float32, dev, t, "mean") if ln else None
-    ra = _rank_dense(rstd, (n, groups), torch.float32, dev, t, "rstd")
+    ma, ra = _rank_floats(x0, t, (n, groups), mean=mean if ln else None, rstd=rstd)
     _call(dev, lib.sp_group_norm_fwd, xa, x_ld, gamma.data_ptr(), beta.data_ptr() if ln else None,
           n, l, c, groups, t, dt, float(eps), _choice(NORMS, norm, "norm"),
           _choice(ACTS, act, "act"), ya, y_ld, ma, ra)
@@ -866,16 +865,13 @@ def sp_group_norm_bwd(dy, x, mean, rstd, gamma, beta=None, *, groups, norm="laye
     n, l, c = x0.shape
     dev, dtype = x0.device, x0.dtype
     ln = norm == "layernorm"
-    da, d_ld = _rank_rows(dy, x0.shape, dtype, dev, t, "dy")
-    xa, x_ld = _rank_rows(x, x0.shape, dtype, dev, t, "x")
-    oa, o_ld = _rank_rows(dx, x0.shape, dtype, dev, t, "dx")
+    da, d_ld, xa, x_ld, oa, o_ld = _rank_rows(x0, t, dy=dy, x=x, dx=dx)
     _need(gamma, (t * c,), dtype, dev, "gamma")
     if ln:
         _need(beta, (t * c,), dtype, dev, "beta")
         if mean is None:
             raise ValueError("mean is required for layernorm")
-    ma = _rank_dense(mean, (n, groups), torch.float32, dev, t, "mean") if ln else None
-    ra = _rank_dense(rstd, (n, groups), torch.float32, dev, t, "rstd")
+    ma, ra = _rank_floats(x0, t, (n, groups), mean=mean if ln else None, rstd=rstd)
     for name, v in (("dgamma", dgamma), ("dbeta", dbeta)):
         if v is not None:
             _need(v, (t * c,), torch.float32, dev, name)

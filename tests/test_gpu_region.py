@@ -20,6 +20,7 @@ a multiple of 2^-24 of the magnitude that the oracle returns beside the value:
   whose products hold two such sums.  dgamma and dbeta add up to 2^9 terms in a row
   per thread and block: 2^-14 of the sum of magnitudes.
 """
+import itertools
 import numpy as np
 import pytest
 import torch
@@ -678,3 +679,41 @@ def test_two_streams_at_once():
             for k, v in w.items():
                 if v is not None and k != "states":
                     assert same(v, g[k]) if isinstance(v, list) else same([v], [g[k]]), k
+
+
+def test_list_readers_agree_with_the_checks():
+    """The compiled readers find the strides that the checks of single buffers find,
+    and give None where those refuse."""
+    base = torch.zeros(3, 6, 5, 64, dtype=torch.bfloat16, device="cuda")
+    whole = [slice(None), slice(None, 1), slice(1, None), slice(None, None, 2), slice(2, 2)]
+    last = [slice(None), slice(16, 32), slice(None, None, 2), slice(7, 8)]
+    read, seen = sp._readers(), {True: 0, False: 0}
+    for i, j, k, m in itertools.product(whole, whole, whole, last):
+        x = base[i, j, k, m]
+        for v in (x, x.transpose(1, 2), x.transpose(0, 1)):
+            try:
+                want = sp._head_strides(v, "x")
+            except ValueError:
+                want = None
+            got = read.heads(v, 2, [v, v], (v, v))
+            assert (got is None) == (want is None)
+            if got is not None:
+                assert tuple(got[1:3]) == tuple(want) and got[1:3] == got[4:]
+                assert got[0] == bytes(sp._pointers([v, v])) == got[3]
+            for y in (v, v[:, :, 0], v[0, :, :1]) if 0 not in v.shape else (v,):
+                try:
+                    want = sp._row_stride(y.shape, y.stride(), "x")
+                except ValueError:
+                    want = None
+                got = read.rows(y, 1, [y])
+                assert (got is None) == (want is None)
+                assert got is None or got[1] == want
+                f = y.float()[..., :1]
+                dense = read.floats(y, 1, tuple(y.shape[:-1]) + (1,), [f], None)
+                assert (dense is not None) == f.is_contiguous() and (not dense or dense[1] is None)
+                seen[want is None] += 1
+    assert min(seen.values()) > 50
+    x = base[0, 0]
+    for bad in (x.half(), x[:4], x.cpu(), x.t(), x[None], x.float()):
+        assert read.rows(x, 2, [x, bad]) is None
+    assert read.rows(x, 1, [x, x]) is None and read.rows(x, 2, [x, x[:, ::2]]) is None

@@ -269,17 +269,18 @@ def test_row_strides():
         row(x[:, ::2, :16])
 
 
-def test_list_reader_takes_only_matching_cuda_tensors():
-    """Everything that is not a list of equal CUDA tensors is left to the binding's
-    own checks (None), whatever it is; wrong calls of the reader raise."""
+def test_list_readers_take_only_matching_cuda_tensors():
+    """Everything that is not lists of equal CUDA tensors is left to the binding's
+    own checks (None), whatever it is."""
     x = torch.zeros(2, 3, dtype=torch.bfloat16)
-    sp._matching([x], (2, 3), torch.bfloat16, x.device)
-    same = sp._module.same
-    for xs, shape in (([x], (2, 3)), ([], (2, 3)), ([None], (2, 3)), ([3], (2,)), ("ab", (2, 3)),
-                      (None, (2, 3)), ([x] * 65, (2, 3)), ([x], None), ([x], ("a", 3)),
-                      ([x], (1,) * 9), ([x], (2, 1 << 70)), ((x, x), x.shape)):
-        assert same(xs, shape, 0, 0) is None
-    with pytest.raises(TypeError):
-        same([x])
-    with pytest.raises(TypeError):
-        same([x], (2, 3), "bf16", 0)
+    read = sp._readers()
+    for xs in ([x], [], [None], [3], "a", None, [x] * 65, (x,)):
+        assert read.rows(x, 1, xs) is None
+        assert read.heads(x[None, None], 1, xs) is None
+        assert read.floats(x, 1, (2, 3), xs) is None
+    for args in ((), (x,), (x, 1), (None, 1, [x]), (x, "a", [x]), (x, 0, []), (x, 1 << 70, [x]),
+                 (x[0, 0], 1, [x[0, 0]])):
+        assert read.rows(*args) is None
+        assert read.heads(*args) is None
+    for shape in (None, ("a", 3), (1,) * 9, (2, 1 << 70), (-1, 3), ()):
+        assert read.floats(x, 1, shape, [x]) is None
