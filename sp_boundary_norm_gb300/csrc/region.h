@@ -37,6 +37,8 @@ cudaError_t launch_rope(RopeParams p, int dtype, int vec, cudaStream_t st);
 constexpr int kScanRun = 16;        // tokens of one thread, and of one saved state
 constexpr int kScanChannels = 64;   // channels of a block: two a lane
 constexpr int kScanWarps = 4;       // of a block, at most
+constexpr int kScanWideWarps = 12;  // of a block that has an SM to itself
+constexpr size_t kScanMaxShared = 232448;   // bytes that a block may ask for
 constexpr int kScanMaxCluster = 16;
 
 struct ScanParams {

@@ -60,8 +60,9 @@ __device__ __forceinline__ Map2 back_map(uint32_t ends, int i1, F2 q1, const F2 
   return Map2{fac, q};
 }
 
-template <int DT, bool TIED, bool PACKED>
-__global__ void __launch_bounds__(32 * kScanWarps, kBwdBlocks) scan_bwd_kernel(const ScanParams P) {
+template <int DT, bool TIED, bool PACKED, bool WIDE>
+__global__ void __launch_bounds__(32 * (WIDE ? kScanWideWarps : kScanWarps), WIDE ? 1 : kBwdBlocks)
+scan_bwd_kernel(const ScanParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
@@ -202,23 +203,29 @@ __global__ void __launch_bounds__(32 * kScanWarps, kBwdBlocks) scan_bwd_kernel(c
   if (C > 1) cluster_sync_all();                     // no partner still writes here
 }
 
-template <int DT>
+template <int DT, bool WIDE>
 static const void* scan_bwd_fn(bool tied, bool packed) {
   if (tied)
-    return packed ? reinterpret_cast<const void*>(&scan_bwd_kernel<DT, true, true>)
-                  : reinterpret_cast<const void*>(&scan_bwd_kernel<DT, true, false>);
-  return packed ? reinterpret_cast<const void*>(&scan_bwd_kernel<DT, false, true>)
-                : reinterpret_cast<const void*>(&scan_bwd_kernel<DT, false, false>);
+    return packed ? reinterpret_cast<const void*>(&scan_bwd_kernel<DT, true, true, WIDE>)
+                  : reinterpret_cast<const void*>(&scan_bwd_kernel<DT, true, false, WIDE>);
+  return packed ? reinterpret_cast<const void*>(&scan_bwd_kernel<DT, false, true, WIDE>)
+                : reinterpret_cast<const void*>(&scan_bwd_kernel<DT, false, false, WIDE>);
+}
+
+template <bool WIDE>
+static const void* scan_bwd_fn(int dtype, bool tied, bool packed) {
+  return dtype == SP_BF16  ? scan_bwd_fn<SP_BF16, WIDE>(tied, packed)
+         : dtype == SP_F16 ? scan_bwd_fn<SP_F16, WIDE>(tied, packed)
+                           : scan_bwd_fn<SP_F32, WIDE>(tied, packed);
 }
 
 cudaError_t launch_scan_bwd(ScanParams p, int dtype, cudaStream_t st) {
   void* args[] = {&p};
   const bool packed = p.cu_seqlens != nullptr;
-  const void* fn = dtype == SP_BF16  ? scan_bwd_fn<SP_BF16>(p.tied, packed)
-                   : dtype == SP_F16 ? scan_bwd_fn<SP_F16>(p.tied, packed)
-                                     : scan_bwd_fn<SP_F32>(p.tied, packed);
-  const ScanCost cost{1.4, 1.9, 0.08, 3, 5};
-  return launch_scan(fn, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
+  const void* fn = scan_bwd_fn<false>(dtype, p.tied, packed);
+  const void* wide = scan_bwd_fn<true>(dtype, p.tied, packed);
+  const ScanCost cost{0.6, 0.7, 0.045, 0.2, 3, 5};
+  return launch_scan(fn, wide, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
 }
 
 }  // namespace spb

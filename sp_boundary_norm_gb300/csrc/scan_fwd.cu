@@ -1,6 +1,8 @@
 // Gated recurrence, forward: y, the last state of every sequence, and the
 // state entering every run of 16 tokens for the backward.  One token of every
 // sequence (a decoding step) takes a kernel without the joins.
+#include <cmath>
+
 #include "scan.cuh"
 
 namespace spb {
@@ -35,8 +37,9 @@ __device__ __forceinline__ Map2 scan_run(const Shared& sh, int stage, uint32_t s
   return Map2{fac, cur};
 }
 
-template <int DT, bool TIED, bool PACKED>
-__global__ void __launch_bounds__(32 * kScanWarps, PACKED ? kFwdBlocks - 1 : kFwdBlocks)
+template <int DT, bool TIED, bool PACKED, bool WIDE>
+__global__ void __launch_bounds__(32 * (WIDE ? kScanWideWarps : kScanWarps),
+                                  WIDE ? 1 : PACKED ? kFwdBlocks - 1 : kFwdBlocks)
 scan_fwd_kernel(const ScanParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ __align__(16) char smem[];
@@ -176,58 +179,81 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams P) {
   }
 }
 
-template <int DT>
+template <int DT, bool WIDE>
 static const void* scan_fwd_fn(bool tied, bool packed) {
   if (tied)
-    return packed ? reinterpret_cast<const void*>(&scan_fwd_kernel<DT, true, true>)
-                  : reinterpret_cast<const void*>(&scan_fwd_kernel<DT, true, false>);
-  return packed ? reinterpret_cast<const void*>(&scan_fwd_kernel<DT, false, true>)
-                : reinterpret_cast<const void*>(&scan_fwd_kernel<DT, false, false>);
+    return packed ? reinterpret_cast<const void*>(&scan_fwd_kernel<DT, true, true, WIDE>)
+                  : reinterpret_cast<const void*>(&scan_fwd_kernel<DT, true, false, WIDE>);
+  return packed ? reinterpret_cast<const void*>(&scan_fwd_kernel<DT, false, true, WIDE>)
+                : reinterpret_cast<const void*>(&scan_fwd_kernel<DT, false, false, WIDE>);
 }
 
-// Blocks of up to four warps; C blocks a cluster, for the C with the least
-// expected time: the clusters that fit the GPU at once run in waves, and a step
-// of a wave takes its shortest time or that of its bytes at 6.0 TB/s, whichever
-// is longer.  (16,384 tokens, 8192 channels, bf16, forward: C = 1 244 us, 2
-// 210, 3 165, 4 146, 8 162; backward: 1 371, 2 272, 3 231, 4 294, 8 264.  1024
-// channels: C = 8 61 us, 12 49, 16 39; backward 70, 55, 52.)
-cudaError_t launch_scan(const void* fn, ScanParams& p, int elem, const ScanCost& cost, void** args,
-                        cudaStream_t st) {
+template <bool WIDE>
+static const void* scan_fwd_fn(int dtype, bool tied, bool packed) {
+  return dtype == SP_BF16  ? scan_fwd_fn<SP_BF16, WIDE>(tied, packed)
+         : dtype == SP_F16 ? scan_fwd_fn<SP_F16, WIDE>(tied, packed)
+                           : scan_fwd_fn<SP_F32, WIDE>(tied, packed);
+}
+
+// Blocks of up to four warps, of which an SM takes several, or of 8 or 12 that
+// have an SM to themselves (kernel `wide`); C blocks a cluster, for the split
+// with the least expected time: the clusters that fit the GPU at once run in
+// waves, and a step of a wave takes its shortest time and that of its bytes at
+// 6.0 TB/s (the cubes add up: the longer one rules).  Many channels fill the GPU with small blocks,
+// whose steps overlap; few channels need long steps, because what a step costs
+// hardly grows with its warps.  Measured, bf16, forward and backward in us:
+//   16,384 tokens of 8192 channels: 4 warps, C = 3 172, 235; C = 4 151, 296;
+//     12 warps, C = 1 150, 246; C = 2 187, 273
+//   16,384 of 1024: 4 warps, C = 16 40, 53; 8, C = 12 47, 68; 12, C = 6 37, 55
+//   65,537 of 512: 4 warps, C = 16 141, 158; 8, C = 12 85, 119; 12, C = 12 75, 112
+cudaError_t launch_scan(const void* fn, const void* wide, ScanParams& p, int elem,
+                        const ScanCost& cost, void** args, cudaStream_t st) {
   const int64_t runs = (p.s + kScanRun - 1) / kScanRun;
   const int64_t units = static_cast<int64_t>(p.slabs) * p.t * p.b;
-  int warps = 1;
-  while (warps < kScanWarps && warps < runs) warps *= 2;
   static const int kClusters[] = {1, 2, 3, 4, 6, 8, 12, kScanMaxCluster};
+  int few = 1;
+  while (few < kScanWarps && few < runs) few *= 2;
+  const int blocks[] = {few, 8, kScanWideWarps};
   double best = 0;
   size_t smem = 0;
-  for (int c : kClusters) {
-    if (c > 1 && static_cast<int64_t>(c - 1) * warps >= runs) break;
-    const size_t need = scan_smem(elem, cost.tensors, warps, c);
-    int fit = 0;
-    const cudaError_t e = max_clusters(fn, 32 * warps, need, c, &fit);
-    if (e != cudaSuccess) return e;
-    if (fit < 1) continue;
-    const double bytes = static_cast<double>(c) * warps * kScanRun * kScanChannels * elem *
-                         cost.passes;
-    auto step = [&](int64_t clusters) {
-      const double least = c == 1 ? cost.lone : cost.cluster + c * cost.per_block;
-      const double moved = static_cast<double>(clusters) * bytes / 6.0e6;
-      return least > moved ? least : moved;
-    };
-    const int64_t steps = (runs + static_cast<int64_t>(c) * warps - 1) / (c * warps);
-    const double start = c == 1 ? 2.0 : 3.0;    // a wave's launch and first rows
-    const double time =
-        static_cast<double>(units / fit) * (start + static_cast<double>(steps) * step(fit)) +
-        (units % fit != 0 ? start + static_cast<double>(steps) * step(units % fit) : 0.0);
-    if (smem == 0 || time < best) {
-      best = time;
-      smem = need;
-      p.cluster = c;
+  int threads = 0;
+  for (const int warps : blocks) {
+    if (warps > kScanWarps && runs <= kScanWarps) break;
+    const void* kernel = warps > kScanWarps ? wide : fn;
+    for (const int c : kClusters) {
+      if (c > 1 && static_cast<int64_t>(c - 1) * warps >= runs) break;
+      const size_t need = scan_smem(elem, cost.tensors, warps, c);
+      if (need > kScanMaxShared) break;
+      const double bytes = static_cast<double>(c) * warps * kScanRun * kScanChannels * elem *
+                           cost.passes;
+      const double least = (c == 1 ? cost.lone : cost.cluster + c * cost.per_block) +
+                           warps * cost.per_warp;
+      const int64_t steps = (runs + static_cast<int64_t>(c) * warps - 1) / (c * warps);
+      const double start = c == 1 ? 2.0 : 3.0;    // a wave's launch and first rows
+      auto wave = [&](int64_t clusters) {
+        const double moved = static_cast<double>(clusters) * bytes / 6.0e6;
+        return start + static_cast<double>(steps) *
+                           std::cbrt(least * least * least + moved * moved * moved);
+      };
+      if (smem != 0 && wave(0) >= best) continue;
+      int fit = 0;
+      const cudaError_t e = max_clusters(kernel, 32 * warps, need, c, &fit);
+      if (e != cudaSuccess) return e;
+      if (fit < 1) continue;
+      const double time = static_cast<double>(units / fit) * wave(fit) +
+                          (units % fit != 0 ? wave(units % fit) : 0.0);
+      if (smem == 0 || time < best) {
+        best = time;
+        smem = need;
+        threads = 32 * warps;
+        p.cluster = c;
+      }
     }
   }
   if (smem == 0 || units * p.cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl(fn, dim3(static_cast<unsigned>(units * p.cluster)), dim3(32 * warps), smem,
-                    args, st, p.cluster);
+  return launch_pdl(threads > 32 * kScanWarps ? wide : fn,
+                    dim3(static_cast<unsigned>(units * p.cluster)), dim3(threads), smem, args, st,
+                    p.cluster);
 }
 
 cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st) {
@@ -242,11 +268,10 @@ cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st) {
     return launch_pdl(fn, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(128), 0,
                       args, st);
   }
-  const void* fn = dtype == SP_BF16  ? scan_fwd_fn<SP_BF16>(p.tied, packed)
-                   : dtype == SP_F16 ? scan_fwd_fn<SP_F16>(p.tied, packed)
-                                     : scan_fwd_fn<SP_F32>(p.tied, packed);
-  const ScanCost cost{1.0, 1.5, 0.055, 2, 3};
-  return launch_scan(fn, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
+  const void* fn = scan_fwd_fn<false>(dtype, p.tied, packed);
+  const void* wide = scan_fwd_fn<true>(dtype, p.tied, packed);
+  const ScanCost cost{0.66, 0.85, 0.06, 0.085, 2, 3};
+  return launch_scan(fn, wide, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
 }
 
 }  // namespace spb

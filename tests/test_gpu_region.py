@@ -305,6 +305,19 @@ def test_scan_packed(lens, tied, dtype, c, state):
     check_scan(i, o, tied, lens, max(lens), state)
 
 
+@pytest.mark.parametrize("lens", [None, [1, 1700, 0, 15, 17, 2767], [4500]], ids=["dense", "q6", "q1"])
+@pytest.mark.parametrize("tied", [True, False])
+@pytest.mark.parametrize("dtype,t,s,c", [(BF, 1, 4500, 72), (FP, 1, 4500, 64), (F32, 1, 4500, 72),
+                                         (BF, 2, 4500, 520), (F32, 3, 4500, 264)])
+def test_scan_few_channels(lens, tied, dtype, t, s, c):
+    """Long sequences of few channels: large blocks, long clusters."""
+    n = 1 if lens is None else len(lens)
+    cu = None if lens is None else torch.tensor(np.concatenate(([0], np.cumsum(lens))),
+                                                dtype=torch.int32, device=DEV)
+    i = scan_inputs(t, n, 1, s, c, dtype, 77 + c, True)
+    check_scan(i, run_scan(i, n, tied, cu, True), tied, lens, s, True)
+
+
 def test_scan_no_token():
     """s == 0 and packed sequences that are all empty: states and their gradients pass."""
     for cu, b, n in ((None, 3, 3), (torch.zeros(5, dtype=torch.int32, device=DEV), 1, 4)):
