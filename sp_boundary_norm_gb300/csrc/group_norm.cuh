@@ -58,20 +58,7 @@ __device__ __forceinline__ F2 both(float v) { return f2(v, v); }
 
 template <int DT>
 __device__ __forceinline__ F2 sigmoid_of(F2 q) {
-  float2 e;
-  if constexpr (DT == SP_F32) {
-    e = split(q);
-    return f2(__frcp_rn(1.f + expf(-e.x)), __frcp_rn(1.f + expf(-e.y)));
-  } else {
-    // 16-bit results: the fast exponential's error is far below their rounding
-    e = split(mul2(q, both(-1.4426950408889634f)));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-    e = split(add2(f2(e.x, e.y), both(1.f)));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-    return f2(e.x, e.y);
-  }
+  return rcp2(add2(exp2_of<DT, false>(mul2(q, both(-1.f))), both(1.f)));
 }
 
 // The parameters of a thread's column.

@@ -179,4 +179,56 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu, int n, int64_t to
   return lo;
 }
 
+// 1 / v of both, within an ulp; subnormal results are flushed.
+__device__ __forceinline__ F2 rcp2(F2 v) {
+  float2 x = split(v);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+  return f2(x.x, x.y);
+}
+
+// exp of both, for results of type DT: 2^t with t = g log2(e) rounded.  The
+// rounding's part, 2^-24 of t, is far below 16-bit results' own; for float32 ones
+// 2^t is multiplied by 1 + r ln 2, where r = g log2(e) - t from a product in two
+// parts, and the power's own error of 2^-22 stays (the library's exponential and
+// reciprocal took half as long again for the whole recurrence: 4 x 65,536 tokens of
+// 256 float32 channels 244 us, so 168).  Float32 arguments are held where the
+// products are finite: 1 / (1 + exp(88.7)) is flushed to zero already, and
+// exp(-104) too.  CAP: below exp(87), 2^126, whose reciprocal is still normal.
+template <int DT, bool CAP>
+__device__ __forceinline__ F2 exp2_of(F2 g) {
+  const F2 log2e = f2(1.4426950408889634f, 1.4426950408889634f);
+  float2 x;
+  F2 rest = f2(0.f, 0.f);
+  if constexpr (DT == SP_F32) {
+    x = split(g);
+    asm("max.NaN.f32 %0, %0, 0fC2D00000;" : "+f"(x.x));     // -104
+    asm("max.NaN.f32 %0, %0, 0fC2D00000;" : "+f"(x.y));
+    if constexpr (CAP) {
+      asm("min.NaN.f32 %0, %0, 0f42AE0000;" : "+f"(x.x));   // 87
+      asm("min.NaN.f32 %0, %0, 0f42AE0000;" : "+f"(x.y));
+    } else {
+      asm("min.NaN.f32 %0, %0, 0f42B16666;" : "+f"(x.x));   // 88.7
+      asm("min.NaN.f32 %0, %0, 0f42B16666;" : "+f"(x.y));
+    }
+    g = f2(x.x, x.y);
+    const F2 t = mul2(g, log2e);
+    rest = fma2(g, f2(-1.4426950408889634f, -1.4426950408889634f), t);
+    rest = fma2(g, f2(-1.92596299e-8f, -1.92596299e-8f), rest);
+    rest = mul2(rest, f2(-0.69314718f, -0.69314718f));
+    x = split(t);
+  } else {
+    x = split(mul2(g, log2e));
+    if constexpr (CAP) {
+      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.x));   // 126
+      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.y));
+    }
+  }
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+  const F2 e = f2(x.x, x.y);
+  if constexpr (DT == SP_F32) return fma2(e, rest, e);
+  return e;
+}
+
 }  // namespace spb

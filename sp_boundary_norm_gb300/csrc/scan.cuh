@@ -43,53 +43,13 @@ __device__ __forceinline__ Two<DT> pack2(F2 v) {
 }
 
 // -k = -sigmoid(-g) = -1 / (1 + e), e = exp(g): small k keep their digits, and
-// h + k (v - h) and h - k h need no more.  An exponential that overflows gives
-// k = 0 (subnormal reciprocals are flushed); CAP holds it below that, for
-// a = e k.  NaN stays NaN.
-//
-// exp(g) = 2^t with t = g log2(e) rounded.  The rounding's part of e is far below
-// that of 16-bit outputs; for float32 ones 2^t is multiplied by 1 + r ln 2, where
-// r = g log2(e) - t from a product in two parts.  What stays is the error of the
-// power and of the reciprocal, 2 and 1 units of 2^-23.
+// h + k (v - h) and h - k h need no more.  An exponential that overflows (or
+// nearly: subnormal reciprocals are flushed) gives k = 0; CAP holds it below
+// that, for a = e k.  NaN stays NaN.
 template <int DT, bool CAP>
 __device__ __forceinline__ F2 neg_k(F2 g, F2& e) {
-  const F2 log2e = f2(1.4426950408889634f, 1.4426950408889634f);
-  float2 x;
-  F2 rest = f2(0.f, 0.f);
-  if constexpr (DT == SP_F32) {
-    // finite products for the rest's sake: exp(88.7) is below the largest
-    // float32, exp(-104) is zero after the flush
-    x = split(g);
-    asm("max.NaN.f32 %0, %0, 0fC2D00000;" : "+f"(x.x));     // -104
-    asm("max.NaN.f32 %0, %0, 0fC2D00000;" : "+f"(x.y));
-    if constexpr (CAP) {
-      asm("min.NaN.f32 %0, %0, 0f42AE0000;" : "+f"(x.x));   // 87
-      asm("min.NaN.f32 %0, %0, 0f42AE0000;" : "+f"(x.y));
-    } else {
-      asm("min.NaN.f32 %0, %0, 0f42B16666;" : "+f"(x.x));   // 88.7
-      asm("min.NaN.f32 %0, %0, 0f42B16666;" : "+f"(x.y));
-    }
-    g = f2(x.x, x.y);
-    const F2 t = mul2(g, log2e);
-    rest = fma2(g, f2(-1.4426950408889634f, -1.4426950408889634f), t);
-    rest = fma2(g, f2(-1.92596299e-8f, -1.92596299e-8f), rest);
-    rest = mul2(rest, f2(-0.69314718f, -0.69314718f));
-    x = split(t);
-  } else {
-    x = split(mul2(g, log2e));
-    if constexpr (CAP) {
-      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.x));   // 126
-      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.y));
-    }
-  }
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));
-  e = f2(x.x, x.y);
-  if constexpr (DT == SP_F32) e = fma2(e, rest, e);
-  x = split(fma2(e, f2(-1.f, -1.f), f2(-1.f, -1.f)));
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
-  return f2(x.x, x.y);
+  e = exp2_of<DT, CAP>(g);
+  return rcp2(fma2(e, f2(-1.f, -1.f), f2(-1.f, -1.f)));
 }
 
 // The state after a token: h + k (v - h), or h - k h + v.  d: h - v (tied).
