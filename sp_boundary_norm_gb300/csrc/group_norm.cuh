@@ -48,6 +48,12 @@ constexpr int kUnitBatch = 4;       // vectors a thread reads at once (forward),
 template <int DT>                   // and of x and dy each (backward)
 constexpr int kBackUnitBatch = DT == SP_F32 ? 2 : 3;
 
+// Held: vectors a thread keeps (forward), and of x and dy each (backward).
+template <int DT>
+constexpr int kHold = DT == SP_F32 ? 6 : 12;
+template <int DT>
+constexpr int kBackHold = DT == SP_F32 ? 3 : 6;
+
 // How the lanes of a group add up (rows form): a power of two of neighbouring
 // lanes by shuffles; other widths up to 31 through the warp's shared memory,
 // every lane adding its group's values; wider groups in their warps, then over

@@ -223,6 +223,122 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_bwd_kernel(const Gro
                    part);
 }
 
+// A cluster's group means of dz and dz z of its sample's slab from `sums`, those
+// of each thread's values.
+__device__ __forceinline__ void join_sums(const GroupNormParams& P, int C, int rank,
+                                          const float2* sums, float2* joined, float2* stat) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int slab_groups = P.cols / P.q;
+  const bool ln = P.norm == SP_NORM_LAYERNORM;
+  __syncthreads();
+  if (C > 1) cluster_wait();                   // the partners run: their shared memory is there
+  for (int g = warp; g < slab_groups; g += nw) {
+    float2 v = make_float2(0.f, 0.f);
+    group_entries(P, g, [&](int, int at) {
+      v.x += sums[at].x;
+      v.y += sums[at].y;
+    });
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (C == 1) {
+      if (lane == 0) stat[g] = make_float2(ln ? v.x * P.count_inv : 0.f, v.y * P.count_inv);
+    } else if (lane < C) {
+      const uint32_t to = cluster_map(&joined[rank * slab_groups + g], lane);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y)
+                   : "memory");
+    }
+  }
+  if (C > 1) {
+    cluster_sync_all();
+    for (int g = threadIdx.x; g < slab_groups; g += blockDim.x) {
+      float2 v = make_float2(0.f, 0.f);
+      for (int k = 0; k < C; ++k) {
+        v.x += joined[k * slab_groups + g].x;
+        v.y += joined[k * slab_groups + g].y;
+      }
+      stat[g] = make_float2(ln ? v.x * P.count_inv : 0.f, v.y * P.count_inv);
+    }
+  }
+  __syncthreads();
+}
+
+// Held (as in the forward).
+template <int DT>
+__global__ void __launch_bounds__(256, kUnitBlocks) group_held_bwd_kernel(const GroupNormParams P) {
+  constexpr int E = ElemSize<DT>::value, kMost = kBackHold<DT>;
+  extern __shared__ float2 sums[];             // [threads] sums of dz and dz z
+  pdl_wait();
+  const int cx = threadIdx.x % P.cols, ry = threadIdx.x / P.cols;
+  const int slab = blockIdx.x % P.slabs;
+  const int r = blockIdx.x / P.slabs % P.t;
+  const int part = static_cast<int>(blockIdx.x) / (P.slabs * P.t);
+  const int vec = slab * P.cols + cx;
+  const bool on = ry < P.rows && vec * 8 < P.c;
+  const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
+  float2* stat = sums + blockDim.x;            // [slab groups] group means of dz and dz z
+  const int64_t ch0 = static_cast<int64_t>(r) * P.c + slab * P.cols * 8, ch = ch0 + cx * 8;
+  const Deal lanes(static_cast<int>(P.l), P.rows);
+  const int mine = on ? lanes.count(ry) : 0;
+  const int64_t row0 = part * P.l + ry;
+  const int64_t at = static_cast<int64_t>(vec) * 8 * E;
+  const char* x = P.x[r] + row0 * P.ld_x + at;
+  const char* dy = P.dy[r] + row0 * P.ld_dy + at;
+  char* out = P.out[r] + row0 * P.ld_out + at;
+  const int64_t step_x = P.ld_x * P.rows, step_dy = P.ld_dy * P.rows, step_out = P.ld_out * P.rows;
+  const int64_t skip = P.parts * P.l;          // rows from sample to sample
+  Column<DT> col;
+  col.read(P, ch, on);
+  F2 acc[8];                                   // dgamma, dbeta of the column
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
+  for (int64_t sample = part; sample < P.n; sample += P.parts) {
+    Vec8<DT> xraw[kMost], draw[kMost];
+    const char *from = x, *dfrom = dy;
+#pragma unroll
+    for (int u = 0; u < kMost; ++u, from += step_x, dfrom += step_dy)
+      if (u < mine) {
+        load_pack(xraw[u], from);
+        load_pack(draw[u], dfrom);
+      }
+    float mean = 0.f, rstd = 0.f;
+    if (on) {
+      const int64_t g = sample * P.groups + vec / P.q;
+      if (ln) mean = __ldg(P.mean[r] + g);
+      rstd = __ldg(P.rstd[r] + g);
+    }
+    F2 z[4], dq[4];
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kMost; ++u)
+      if (u < mine) {
+        unpack_pairs(xraw[u], z);
+        unpack_pairs(draw[u], dq);
+        float s1, s2;
+        back_vector<DT>(z, dq, mean, rstd, col, silu, acc, s1, s2);
+        sum.x += s1;
+        sum.y += s2;
+      }
+    if (ry < P.rows) sums[threadIdx.x] = sum;
+    join_sums(P, 1, 0, sums, nullptr, stat);
+    const float2 m = stat[on ? cx / P.q : 0];
+    char* to = out;
+#pragma unroll
+    for (int u = 0; u < kMost; ++u, to += step_out)
+      if (u < mine) {
+        unpack_pairs(xraw[u], z);
+        unpack_pairs(draw[u], dq);
+        back_act<DT>(z, dq, mean, rstd, col, silu);
+        store_pack(to, back_out<DT>(z, dq, rstd, col, m.x, m.y));
+      }
+    x += skip * P.ld_x;
+    dy += skip * P.ld_dy;
+    out += skip * P.ld_out;
+  }
+  if (P.has_params)
+    put_param_part(P, acc, reinterpret_cast<float*>(sums), cx, ry, ch0, P.c - slab * P.cols * 8,
+                   part);
+}
+
 template <int DT, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kUnitBlocks)
 group_unit_bwd_kernel(const GroupNormParams P) {
@@ -240,9 +356,8 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   const int vec = slab * P.cols + cx;
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
-  const int slab_groups = P.cols / P.q;
   float2* joined = sums + blockDim.x;          // [cluster][slab groups] sums of each block
-  float2* stat = joined + C * slab_groups;     // [slab groups] group means of dz and dz z
+  float2* stat = joined + C * (P.cols / P.q);  // [slab groups] group means of dz and dz z
   const int64_t ch0 = static_cast<int64_t>(r) * P.c + slab * P.cols * 8, ch = ch0 + cx * 8;
   const Deal blocks(static_cast<int>(P.l), C);
   const int b0 = blocks.first(rank), block_rows = blocks.count(rank);
@@ -315,35 +430,7 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   }
   const float2 w1 = split(own1), w2 = split(own2);
   if (ry < P.rows) sums[threadIdx.x] = make_float2(w1.x + w1.y, w2.x + w2.y);
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  if (C > 1) cluster_wait();                   // the partners run: their shared memory is there
-  for (int g = warp; g < slab_groups; g += nw) {
-    float2 v = make_float2(0.f, 0.f);
-    group_entries(P, g, [&](int, int at) {
-      v.x += sums[at].x;
-      v.y += sums[at].y;
-    });
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (C == 1) {
-      if (lane == 0) joined[g] = v;
-    } else if (lane < C) {
-      const uint32_t to = cluster_map(&joined[rank * slab_groups + g], lane);
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y)
-                   : "memory");
-    }
-  }
-  if (C > 1) cluster_sync_all(); else __syncthreads();
-  for (int g = threadIdx.x; g < slab_groups; g += blockDim.x) {
-    float2 v = make_float2(0.f, 0.f);
-    for (int k = 0; k < C; ++k) {
-      v.x += joined[k * slab_groups + g].x;
-      v.y += joined[k * slab_groups + g].y;
-    }
-    stat[g] = make_float2(ln ? v.x * P.count_inv : 0.f, v.y * P.count_inv);
-  }
-  __syncthreads();
+  join_sums(P, C, rank, sums, joined, stat);
   const float2 m = stat[cx / P.q];
   for (int i0 = 0; i0 < mine; i0 += kBatch) {
     take(i0, false);
@@ -395,6 +482,7 @@ static const void* bwd_fn(const GroupShape& s) {
            : s.mode == kSumWarp ? reinterpret_cast<const void*>(&group_row_bwd_kernel<DT, kSumWarp>)
                                 : reinterpret_cast<const void*>(&group_row_bwd_kernel<DT, kSumTeam>);
   if (s.form == kTileForm) return reinterpret_cast<const void*>(&group_tile_bwd_kernel<DT>);
+  if (s.form == kHeldForm) return reinterpret_cast<const void*>(&group_held_bwd_kernel<DT>);
   return s.threads > 256 ? reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT, true>)
                          : reinterpret_cast<const void*>(&group_unit_bwd_kernel<DT, false>);
 }

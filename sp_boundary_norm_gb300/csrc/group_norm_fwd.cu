@@ -179,6 +179,127 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
   }
 }
 
+// A cluster's statistics of its sample's slab from `sums`, (mean, M2) of each
+// thread's values: stat[g] = (mean, rstd).  `blocks`: the sample's rows dealt to
+// the blocks, `lanes`: this block's to its threads' rows.
+__device__ __forceinline__ void join_moments(const GroupNormParams& P, int C, int rank, int slab,
+                                             int r, int64_t sample, const Deal& blocks,
+                                             const Deal& lanes, const float2* sums,
+                                             float2* joined, float2* stat) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int slab_groups = P.cols / P.q;
+  const bool ln = P.norm == SP_NORM_LAYERNORM;
+  const float block_count = static_cast<float>(blocks.count(rank)) * 8.f * P.q;
+  auto put = [&](int g, float m, float v) {
+    const float2 st = make_float2(m, rsqrtf(v * P.count_inv + P.eps));
+    stat[g] = st;
+    const int group = slab * slab_groups + g;
+    if (rank == 0 && group < P.groups) {
+      if (ln) P.mean[r][sample * P.groups + group] = st.x;
+      P.rstd[r][sample * P.groups + group] = st.y;
+    }
+  };
+  __syncthreads();
+  if (C > 1) cluster_wait();                   // the partners run: their shared memory is there
+  // one warp a group
+  for (int g = warp; g < slab_groups; g += nw) {
+    float s = 0.f, v = 0.f;
+    if (ln) group_entries(P, g, [&](int y, int at) { s += 8.f * lanes.count(y) * sums[at].x; });
+    const float m = ln && block_count > 0.f ? warp_sum(s) / block_count : 0.f;
+    group_entries(P, g, [&](int y, int at) {
+      const float d = sums[at].x - m;
+      v += sums[at].y + 8.f * lanes.count(y) * d * d;
+    });
+    v = warp_sum(v);
+    if (C == 1) {
+      if (lane == 0) put(g, m, v);
+    } else if (lane < C) {
+      const uint32_t to = cluster_map(&joined[rank * slab_groups + g], lane);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(v)
+                   : "memory");
+    }
+  }
+  if (C > 1) {
+    cluster_sync_all();
+    for (int g = threadIdx.x; g < slab_groups; g += blockDim.x) {
+      float m = 0.f, v = 0.f;
+      for (int k = 0; k < C; ++k)
+        m += joined[k * slab_groups + g].x * static_cast<float>(blocks.count(k));
+      m /= static_cast<float>(P.l);
+      for (int k = 0; k < C; ++k) {
+        const float2 w = joined[k * slab_groups + g];
+        const float d = w.x - m;
+        v += w.y + static_cast<float>(blocks.count(k)) * 8.f * P.q * d * d;
+      }
+      put(g, m, v);
+    }
+  }
+  __syncthreads();
+}
+
+// Held: a block keeps its sample's slab in registers, and takes one sample after
+// the other.
+template <int DT>
+__global__ void __launch_bounds__(256, kUnitBlocks) group_held_fwd_kernel(const GroupNormParams P) {
+  constexpr int E = ElemSize<DT>::value, kMost = kHold<DT>;
+  extern __shared__ float2 sums[];             // [threads] mean, M2
+  pdl_wait();
+  const int cx = threadIdx.x % P.cols, ry = threadIdx.x / P.cols;
+  const int slab = blockIdx.x % P.slabs;
+  const int r = blockIdx.x / P.slabs % P.t;
+  const int part = static_cast<int>(blockIdx.x) / (P.slabs * P.t);
+  const int vec = slab * P.cols + cx;
+  const bool on = ry < P.rows && vec * 8 < P.c;
+  const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
+  float2* stat = sums + blockDim.x;            // [slab groups] mean, rstd
+  const Deal blocks(static_cast<int>(P.l), 1), lanes(static_cast<int>(P.l), P.rows);
+  const int mine = on ? lanes.count(ry) : 0;
+  const int64_t row0 = part * P.l + ry;
+  const char* x = P.x[r] + row0 * P.ld_x + static_cast<int64_t>(vec) * 8 * E;
+  char* out = P.out[r] + row0 * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
+  const int64_t step_x = P.ld_x * P.rows, step_out = P.ld_out * P.rows;
+  const int64_t skip_x = P.parts * P.l * P.ld_x, skip_out = P.parts * P.l * P.ld_out;
+  Column<DT> col;
+  col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
+  const float each = mine > 0 ? 0.125f / static_cast<float>(mine) : 0.f;
+  for (int64_t sample = part; sample < P.n; sample += P.parts, x += skip_x, out += skip_out) {
+    Vec8<DT> raw[kMost];
+    const char* from = x;
+#pragma unroll
+    for (int u = 0; u < kMost; ++u, from += step_x)
+      if (u < mine) load_pack(raw[u], from);
+    float2 mom = make_float2(0.f, 0.f);
+    if (ln) {
+#pragma unroll
+      for (int u = 0; u < kMost; ++u)
+        if (u < mine) {
+          F2 v[4];
+          unpack_pairs(raw[u], v);
+          mom.x += pair_sum(v);
+        }
+      mom.x *= each;
+    }
+#pragma unroll
+    for (int u = 0; u < kMost; ++u)
+      if (u < mine) {
+        F2 v[4];
+        unpack_pairs(raw[u], v);
+        mom.y += spread_sum(v, mom.x);
+      }
+    if (ry < P.rows) sums[threadIdx.x] = mom;
+    join_moments(P, 1, 0, slab, r, sample, blocks, lanes, sums, nullptr, stat);
+    const float2 st = stat[on ? cx / P.q : 0];
+    char* to = out;
+#pragma unroll
+    for (int u = 0; u < kMost; ++u, to += step_out)
+      if (u < mine) {
+        F2 v[4];
+        unpack_pairs(raw[u], v);
+        store_pack(to, norm_act<DT>(v, st.x, st.y, col, silu));
+      }
+  }
+}
+
 // One cluster per (sample, rank, slab).  WIDE: groups of more than 256 vectors,
 // blocks of up to 512 threads.
 template <int DT, bool WIDE>
@@ -198,9 +319,8 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   const int vec = slab * P.cols + cx;
   const bool on = ry < P.rows && vec * 8 < P.c;
   const bool ln = P.norm == SP_NORM_LAYERNORM, silu = P.act == SP_ACT_SILU;
-  const int slab_groups = P.cols / P.q;
   float2* joined = sums + blockDim.x;          // [cluster][slab groups] mean, M2 of each block
-  float2* stat = joined + C * slab_groups;     // [slab groups] mean, rstd
+  float2* stat = joined + C * (P.cols / P.q);  // [slab groups] mean, rstd
   // this block's rows of the sample, and this thread's: ry, ry + rows, ...
   const Deal blocks(static_cast<int>(P.l), C);
   const int b0 = blocks.first(rank), block_rows = blocks.count(rank);
@@ -235,49 +355,8 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   mom.join(ln);
   from = x;
   fetch(0, false);
-  // the block's mean and M2 of each group of the slab, one warp a group
   if (ry < P.rows) sums[threadIdx.x] = make_float2(mom.mean, mom.m2);
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const float block_count = static_cast<float>(block_rows) * 8.f * P.q;
-  if (C > 1) cluster_wait();                   // the partners run: their shared memory is there
-  for (int g = warp; g < slab_groups; g += nw) {
-    float s = 0.f, v = 0.f;
-    if (ln) group_entries(P, g, [&](int y, int at) { s += 8.f * lanes.count(y) * sums[at].x; });
-    const float m = block_count > 0.f ? warp_sum(s) / block_count : 0.f;
-    group_entries(P, g, [&](int y, int at) {
-      const float d = sums[at].x - m;
-      v += sums[at].y + 8.f * lanes.count(y) * d * d;
-    });
-    v = warp_sum(v);
-    if (C == 1) {
-      if (lane == 0) joined[g] = make_float2(m, v);
-    } else if (lane < C) {
-      const uint32_t to = cluster_map(&joined[rank * slab_groups + g], lane);
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(v)
-                   : "memory");
-    }
-  }
-  if (C > 1) cluster_sync_all(); else __syncthreads();
-  for (int g = threadIdx.x; g < slab_groups; g += blockDim.x) {
-    float m = 0.f, v = 0.f;
-    for (int k = 0; k < C; ++k)
-      m += joined[k * slab_groups + g].x * static_cast<float>(blocks.count(k));
-    m /= static_cast<float>(P.l);
-    for (int k = 0; k < C; ++k) {
-      const float2 w = joined[k * slab_groups + g];
-      const float d = w.x - m;
-      v += w.y + static_cast<float>(blocks.count(k)) * 8.f * P.q * d * d;
-    }
-    const float2 st = make_float2(m, rsqrtf(v * P.count_inv + P.eps));
-    stat[g] = st;
-    const int group = slab * slab_groups + g;
-    if (rank == 0 && group < P.groups) {
-      if (ln) P.mean[r][sample * P.groups + group] = st.x;
-      P.rstd[r][sample * P.groups + group] = st.y;
-    }
-  }
-  __syncthreads();
+  join_moments(P, C, rank, slab, r, sample, blocks, lanes, sums, joined, stat);
   if (!on) return;
   const float2 st = stat[cx / P.q];
   Column<DT> col;
@@ -327,10 +406,48 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     s.smem = bwd ? static_cast<size_t>(s.rows) * s.cols * 17 * 4 : 0;
     return s;
   }
+  static const int kClusters[] = {1, 2, 3, 4, 6, 8, 10, 12, kGroupMaxCluster};
+  auto narrow = [&]() {
+    // narrow slabs of at least 128 bytes of a row, whole 32-byte sectors where
+    // that takes two groups at most, and many rows abreast
+    fit_cols(q >= 8 ? q : (8 + q - 1) / q * q);
+    if (s.cols % 2 != 0 && 2 * s.cols <= nvec) fit_cols(2 * s.cols);
+    s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
+  };
+  // held: samples of some rows whose slab, 160 to 1024 vectors, fits the registers
+  // of a block of up to 256 threads, as few threads as hold it (blocks of one warp
+  // overlap best) unless that leaves the SMs half empty.  Fewer vectors a sample
+  // than that hide the joins' latency badly, more leave the loads without
+  // overlap.  (64 MB of bf16 in 8 groups of 512 channels, held against the other
+  // forms, forward and backward in us: samples of 12 rows 86, 87 against 70, 88;
+  // 16 rows 69, 77 against 65, 78; 24 rows 53, 72 against 97, 317; 48 rows 40, 75
+  // against 133, 178; 128 rows 66, 86 against 64, 96; 200 rows 56, 110 against
+  // 55, 81.)
+  const int hold = bwd ? (size == 4 ? kBackHold<SP_F32> : kBackHold<SP_BF16>)
+                       : (size == 4 ? kHold<SP_F32> : kHold<SP_BF16>);
+  narrow();
+  if (l * s.cols >= 160 && l * s.cols <= 1024 && s.cols <= 256 &&
+      l <= static_cast<int64_t>(s.rows) * hold) {
+    s.form = kHeldForm;
+    const int64_t units = n * t * s.slabs;
+    const int most = s.rows;
+    s.rows = div_up(l, hold);
+    if (s.rows < 32 / s.cols) s.rows = 32 / s.cols;
+    while (2 * s.rows <= most && units * s.rows * s.cols < int64_t(256) * sms) s.rows *= 2;
+    s.threads = (s.rows * s.cols + 31) / 32 * 32;
+    const int64_t cap = static_cast<int64_t>(sms) * kUnitBlocks * (256 / s.threads) / (s.slabs * t);
+    s.parts = cap < 1 ? 1 : n < cap ? n : cap;
+    s.smem = (static_cast<size_t>(s.threads) + s.cols / q) * 8;
+    if (bwd) {
+      const size_t part = static_cast<size_t>(s.rows) * s.cols * 17 * 4;
+      if (s.smem < part) s.smem = part;
+    }
+    return s;
+  }
   // tiles while a block of up to 256 threads holds a whole sample in its registers
   fit_cols(256);
   s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
-  if (l > static_cast<int64_t>(s.rows) * held_rows && l <= 16 * held_rows && q <= 32) {
+  if (l > static_cast<int64_t>(s.rows) * held_rows && l * q < 160 && q <= 32) {
     fit_cols(32);     // fewer columns abreast: more rows of a sample in one block
     s.rows = 256 / s.cols;
   }
@@ -356,11 +473,7 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     return s;
   }
   s.form = kUnitForm;
-  // units: narrow slabs of at least 128 bytes of a row, whole 32-byte sectors
-  // where that takes two groups at most, and many rows abreast
-  fit_cols(q >= 8 ? q : (8 + q - 1) / q * q);
-  if (s.cols % 2 != 0 && 2 * s.cols <= nvec) fit_cols(2 * s.cols);
-  s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
+  narrow();
   s.threads = (s.rows * s.cols + 31) / 32 * 32;
   // The fewest blocks a cluster that fill the SMs one and a half times over and
   // leave what the blocks at work read inside L2 (129 MB).  (8 samples of 4096 x
@@ -370,7 +483,6 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   const int64_t resident = static_cast<int64_t>(kUnitBlocks) * sms;
   const int64_t slab_bytes = l * s.cols * 8 * size * (bwd ? 2 : 1);
   const int64_t units = n * t * s.slabs;
-  static const int kClusters[] = {1, 2, 3, 4, 6, 8, 10, 12, kGroupMaxCluster};
   for (int cl : kClusters) {
     if (cl > 1 && (l < static_cast<int64_t>(cl) * s.rows)) break;
     s.cluster = cl;
@@ -401,11 +513,10 @@ cudaError_t launch_group(const void* fn, GroupNormParams* p, const GroupShape& s
   fill_shape(p, s);
   void* args[] = {p};
   int fit = 1;
-  const bool unit = s.form == kUnitForm;
-  const cudaError_t e = unit ? max_clusters(fn, s.threads, s.smem, s.cluster, &fit)
+  const cudaError_t e = s.form == kUnitForm ? max_clusters(fn, s.threads, s.smem, s.cluster, &fit)
                              : ensure_smem_attr(fn, s.smem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = static_cast<int64_t>(s.slabs) * p->t * (unit ? p->n * s.cluster : s.parts);
+  const int64_t blocks = static_cast<int64_t>(s.slabs) * p->t * s.parts;
   if (fit < 1 || blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_pdl(fn, dim3(static_cast<unsigned>(blocks)), dim3(s.threads), s.smem, args, st,
                     s.cluster);
@@ -418,6 +529,7 @@ static const void* fwd_fn(const GroupShape& s) {
            : s.mode == kSumWarp ? reinterpret_cast<const void*>(&group_row_fwd_kernel<DT, kSumWarp>)
                                 : reinterpret_cast<const void*>(&group_row_fwd_kernel<DT, kSumTeam>);
   if (s.form == kTileForm) return reinterpret_cast<const void*>(&group_tile_fwd_kernel<DT>);
+  if (s.form == kHeldForm) return reinterpret_cast<const void*>(&group_held_fwd_kernel<DT>);
   return s.threads > 256 ? reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT, true>)
                          : reinterpret_cast<const void*>(&group_unit_fwd_kernel<DT, false>);
 }

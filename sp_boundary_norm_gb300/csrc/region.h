@@ -91,7 +91,7 @@ struct GroupNormParams {
 };
 
 // The split of a call (see GroupNormParams).
-constexpr int kRowForm = 0, kTileForm = 1, kUnitForm = 2;
+constexpr int kRowForm = 0, kTileForm = 1, kHeldForm = 2, kUnitForm = 3;
 struct GroupShape {
   int form, mode;
   int cols, slabs, rows, threads, samples, lanes, cluster;

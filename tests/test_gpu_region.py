@@ -453,7 +453,9 @@ NORM = [
     (2, 3, 1, 16384, 64, BF), (1, 4, 2, 64, 2, BF), (1, 3, 7, 80, 2, F32), (2, 6, 32, 512, 16, BF),
     (1, 2, 33, 24, 3, FP), (1, 2, 64, 2048, 8, BF), (1, 2, 65, 4096, 1, BF), (1, 1, 700, 40, 1, F32),
     (2, 3, 513, 320, 8, BF), (1, 1, 5001, 64, 8, BF), (1, 40, 100, 72, 9, FP), (1, 2, 2000, 1280, 32, BF),
-    (1, 1, 9000, 4096, 2, BF), (1, 1, 3001, 3200, 1, F32),
+    (1, 1, 9000, 4096, 2, BF), (1, 1, 3001, 3200, 1, F32), (2, 700, 21, 512, 8, BF),
+    (1, 900, 24, 40, 5, FP), (1, 500, 17, 1280, 16, F32), (1, 11, 5, 1600, 1, F32),
+    (3, 5, 50, 1360, 17, BF), (1, 3, 4, 2048, 1, BF), (1, 5, 3, 4096, 16, FP),
 ]
 
 
