@@ -43,10 +43,13 @@ constexpr int kBackRowBlocks = 2;
 constexpr int kRowWarps = 8;        // of a block (rows), more for groups beyond 256 vectors
 constexpr int kRowMaxWarps = kGroupThreads / 32;
 
-constexpr int kUnitBlocks = 2;      // units: blocks an SM that the registers are held to
-constexpr int kUnitBatch = 4;       // vectors a thread reads at once (forward),
-template <int DT>                   // and of x and dy each (backward)
-constexpr int kBackUnitBatch = DT == SP_F32 ? 2 : 3;
+constexpr int kUnitBlocks = 3;      // units, forward: blocks an SM that the registers are
+constexpr int kBackUnitBlocks = 2;  // held to, and backward
+constexpr int kHeldBlocks = 2;
+template <int DT>                   // vectors on their way to a thread (forward), of x and
+constexpr int kUnitRing = DT == SP_F32 ? 3 : 6;
+template <int DT>                   // dy each (backward)
+constexpr int kBackUnitRing = DT == SP_F32 ? 2 : 4;
 
 // Held: vectors a thread keeps (forward), and of x and dy each (backward).
 template <int DT>
@@ -64,7 +67,7 @@ __device__ __forceinline__ F2 both(float v) { return f2(v, v); }
 
 template <int DT>
 __device__ __forceinline__ F2 sigmoid_of(F2 q) {
-  return rcp2(add2(exp2_of<DT, false>(mul2(q, both(-1.f))), both(1.f)));
+  return rcp2(add2(exp2_of<DT, false, -1>(q), both(1.f)));
 }
 
 // The parameters of a thread's column.

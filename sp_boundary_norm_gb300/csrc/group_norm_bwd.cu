@@ -264,7 +264,7 @@ __device__ __forceinline__ void join_sums(const GroupNormParams& P, int C, int r
 
 // Held (as in the forward).
 template <int DT>
-__global__ void __launch_bounds__(256, kUnitBlocks) group_held_bwd_kernel(const GroupNormParams P) {
+__global__ void __launch_bounds__(256, kHeldBlocks) group_held_bwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value, kMost = kBackHold<DT>;
   extern __shared__ float2 sums[];             // [threads] sums of dz and dz z
   pdl_wait();
@@ -340,9 +340,9 @@ __global__ void __launch_bounds__(256, kUnitBlocks) group_held_bwd_kernel(const 
 }
 
 template <int DT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kUnitBlocks)
+__global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kBackUnitBlocks)
 group_unit_bwd_kernel(const GroupNormParams P) {
-  constexpr int E = ElemSize<DT>::value, kBatch = kBackUnitBatch<DT>;
+  constexpr int E = ElemSize<DT>::value, kRing = kBackUnitRing<DT>;
   extern __shared__ float2 sums[];             // [threads] sums of dz and dz z
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (C > 1) cluster_arrive();                 // waited for before the first remote store
@@ -380,48 +380,44 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   F2 acc[8];                                   // dgamma, dbeta of the column
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = both(0.f);
-  // a batch of vectors is on its way while the one before is used
-  Vec8<DT> xraw[kBatch], draw[kBatch];
+  // a vector's place is filled again as soon as it is used
+  Vec8<DT> xraw[kRing], draw[kRing];
   const char *from = x, *dfrom = dy;
-  auto fetch = [&](int i0, bool again) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u, from += step_x, dfrom += step_dy)
-      if (i0 + u < mine) {
-        if (again) {
-          load_again<DT>(xraw[u], from);
-          load_again<DT>(draw[u], dfrom);
-        } else {
-          load_pack(xraw[u], from);
-          load_pack(draw[u], dfrom);
-        }
+  auto fetch = [&](int u, int i, bool again) {
+    if (i < mine) {
+      if (again) {
+        load_again<DT>(xraw[u], from);
+        load_again<DT>(draw[u], dfrom);
+      } else {
+        load_pack(xraw[u], from);
+        load_pack(draw[u], dfrom);
       }
-  };
-  F2 z[kBatch][4], dq[kBatch][4];
-  auto take = [&](int i0, bool again) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      unpack_pairs(xraw[u], z[u]);
-      unpack_pairs(draw[u], dq[u]);
     }
-    fetch(i0 + kBatch, again);
+    from += step_x;
+    dfrom += step_dy;
   };
-  fetch(0, true);
-  for (int i0 = 0; i0 < mine; i0 += kBatch) {
-    take(i0, true);
+  F2 z[4], dq[4];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+  for (int u = 0; u < kRing; ++u) fetch(u, u, true);
+  for (int i0 = 0; i0 < mine; i0 += kRing) {
+#pragma unroll
+    for (int u = 0; u < kRing; ++u) {
+      unpack_pairs(xraw[u], z);
+      unpack_pairs(draw[u], dq);
+      fetch(u, i0 + kRing + u, true);
       if (i0 + u >= mine) continue;
-      back_act<DT>(z[u], dq[u], mean, rstd, col, silu);
+      back_act<DT>(z, dq, mean, rstd, col, silu);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[i] = fma2(dq[u][i], z[u][i], acc[i]);
-        acc[4 + i] = add2(acc[4 + i], dq[u][i]);
+        acc[i] = fma2(dq[i], z[i], acc[i]);
+        acc[4 + i] = add2(acc[4 + i], dq[i]);
       }
     }
   }
   from = x;
   dfrom = dy;
-  fetch(0, false);
+#pragma unroll
+  for (int u = 0; u < kRing; ++u) fetch(u, u, false);
   F2 own1 = both(0.f), own2 = both(0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -432,13 +428,15 @@ group_unit_bwd_kernel(const GroupNormParams P) {
   if (ry < P.rows) sums[threadIdx.x] = make_float2(w1.x + w1.y, w2.x + w2.y);
   join_sums(P, C, rank, sums, joined, stat);
   const float2 m = stat[cx / P.q];
-  for (int i0 = 0; i0 < mine; i0 += kBatch) {
-    take(i0, false);
+  for (int i0 = 0; i0 < mine; i0 += kRing) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u, out += step_out) {
+    for (int u = 0; u < kRing; ++u, out += step_out) {
+      unpack_pairs(xraw[u], z);
+      unpack_pairs(draw[u], dq);
+      fetch(u, i0 + kRing + u, false);
       if (i0 + u >= mine) continue;
-      back_act<DT>(z[u], dq[u], mean, rstd, col, silu);
-      store_pack(out, back_out<DT>(z[u], dq[u], rstd, col, m.x, m.y));
+      back_act<DT>(z, dq, mean, rstd, col, silu);
+      store_pack(out, back_out<DT>(z, dq, rstd, col, m.x, m.y));
     }
   }
   if (P.has_params)

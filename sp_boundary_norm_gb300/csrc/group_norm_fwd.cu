@@ -240,7 +240,7 @@ __device__ __forceinline__ void join_moments(const GroupNormParams& P, int C, in
 // Held: a block keeps its sample's slab in registers, and takes one sample after
 // the other.
 template <int DT>
-__global__ void __launch_bounds__(256, kUnitBlocks) group_held_fwd_kernel(const GroupNormParams P) {
+__global__ void __launch_bounds__(256, kHeldBlocks) group_held_fwd_kernel(const GroupNormParams P) {
   constexpr int E = ElemSize<DT>::value, kMost = kHold<DT>;
   extern __shared__ float2 sums[];             // [threads] mean, M2
   pdl_wait();
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(256, kUnitBlocks) group_held_fwd_kernel(const 
 template <int DT, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kGroupThreads : 256, WIDE ? 1 : kUnitBlocks)
 group_unit_fwd_kernel(const GroupNormParams P) {
-  constexpr int E = ElemSize<DT>::value;
+  constexpr int E = ElemSize<DT>::value, kRing = kUnitRing<DT>;
   extern __shared__ float2 sums[];             // [threads] mean, M2
   const int C = P.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (C > 1) cluster_arrive();                 // waited for before the first remote store
@@ -330,31 +330,32 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   const char* x = P.x[r] + row0 * P.ld_x + static_cast<int64_t>(vec) * 8 * E;
   const int64_t step_x = P.ld_x * P.rows, step_out = P.ld_out * P.rows;
   Moments mom;
-  // a batch of vectors is on its way while the one before is used
-  Vec8<DT> raw[kUnitBatch];
+  // a vector's place is filled again as soon as it is used
+  Vec8<DT> raw[kRing];
   const char* from = x;
-  auto fetch = [&](int i0, bool again) {
-#pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u, from += step_x)
-      if (i0 + u < mine) {
-        if (again) load_again<DT>(raw[u], from);
-        else load_pack(raw[u], from);
-      }
+  auto fetch = [&](int u, int i, bool again) {
+    if (i < mine) {
+      if (again) load_again<DT>(raw[u], from);
+      else load_pack(raw[u], from);
+    }
+    from += step_x;
   };
-  fetch(0, true);
-  for (int i0 = 0; i0 < mine; i0 += kUnitBatch) {
-    F2 v[kUnitBatch][4];
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u) unpack_pairs(raw[u], v[u]);
-    fetch(i0 + kUnitBatch, true);
+  for (int u = 0; u < kRing; ++u) fetch(u, u, true);
+  for (int i0 = 0; i0 < mine; i0 += kRing) {
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u)
-      if (i0 + u < mine) mom.add(v[u], ln);
-    if (mom.n >= kStretch - kUnitBatch) mom.join(ln);
+    for (int u = 0; u < kRing; ++u) {
+      F2 v[4];
+      unpack_pairs(raw[u], v);
+      if (i0 + u < mine) mom.add(v, ln);
+      fetch(u, i0 + kRing + u, true);
+    }
+    if (mom.n >= kStretch - kRing) mom.join(ln);
   }
   mom.join(ln);
   from = x;
-  fetch(0, false);
+#pragma unroll
+  for (int u = 0; u < kRing; ++u) fetch(u, u, false);
   if (ry < P.rows) sums[threadIdx.x] = make_float2(mom.mean, mom.m2);
   join_moments(P, C, rank, slab, r, sample, blocks, lanes, sums, joined, stat);
   if (!on) return;
@@ -363,14 +364,14 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
   fold_stats(col, st.x, st.y);
   char* out = P.out[r] + row0 * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
-  for (int i0 = 0; i0 < mine; i0 += kUnitBatch) {
-    F2 v[kUnitBatch][4];
+  for (int i0 = 0; i0 < mine; i0 += kRing) {
 #pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u) unpack_pairs(raw[u], v[u]);
-    fetch(i0 + kUnitBatch, false);
-#pragma unroll
-    for (int u = 0; u < kUnitBatch; ++u, out += step_out)
-      if (i0 + u < mine) store_pack(out, norm_act<DT, true>(v[u], st.x, st.y, col, silu));
+    for (int u = 0; u < kRing; ++u, out += step_out) {
+      F2 v[4];
+      unpack_pairs(raw[u], v);
+      fetch(u, i0 + kRing + u, false);
+      if (i0 + u < mine) store_pack(out, norm_act<DT, true>(v, st.x, st.y, col, silu));
+    }
   }
 }
 
@@ -435,7 +436,7 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     if (s.rows < 32 / s.cols) s.rows = 32 / s.cols;
     while (2 * s.rows <= most && units * s.rows * s.cols < int64_t(256) * sms) s.rows *= 2;
     s.threads = (s.rows * s.cols + 31) / 32 * 32;
-    const int64_t cap = static_cast<int64_t>(sms) * kUnitBlocks * (256 / s.threads) / (s.slabs * t);
+    const int64_t cap = static_cast<int64_t>(sms) * kHeldBlocks * (256 / s.threads) / (s.slabs * t);
     s.parts = cap < 1 ? 1 : n < cap ? n : cap;
     s.smem = (static_cast<size_t>(s.threads) + s.cols / q) * 8;
     if (bwd) {
@@ -475,21 +476,30 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   s.form = kUnitForm;
   narrow();
   s.threads = (s.rows * s.cols + 31) / 32 * 32;
-  // The fewest blocks a cluster that fill the SMs one and a half times over and
-  // leave what the blocks at work read inside L2 (129 MB).  (8 samples of 4096 x
-  // 1280: clusters of 4 47 us forward and 82 backward, 8 52 and 86, 12 61 and 91;
-  // 64 samples of 256: 1 22 us, 2 34, 4 48.)
-  const int slab_groups = s.cols / q;
-  const int64_t resident = static_cast<int64_t>(kUnitBlocks) * sms;
+  // Of the clusters that leave what the blocks at work read inside L2 (129 MB) the
+  // one with the least waves x (3 us + 0.2 us a vector of a thread): short rows of
+  // waves that are full.  (Forward and backward in us, bf16.  32 samples of 1024 x
+  // 320 in 5 groups: C = 1 17, 28; 2 14, 29; 3 18, 27; 6 21, 37.  8 of 4096 x 1280 in
+  // 32: 1 68, 111; 2 49, 78; 3 45, 95; 4 52, 79; 6 45, 81; 12 53, 93.  8 ranks' 4 of
+  // 2048 x 2048 in 8: 1 146, 228; 3 134, 233; 6 130, 230; 16 195, 311.)
+  const int64_t resident = static_cast<int64_t>(bwd ? kBackUnitBlocks : kUnitBlocks) * sms;
   const int64_t slab_bytes = l * s.cols * 8 * size * (bwd ? 2 : 1);
   const int64_t units = n * t * s.slabs;
+  double best = 0;
   for (int cl : kClusters) {
-    if (cl > 1 && (l < static_cast<int64_t>(cl) * s.rows)) break;
+    if (cl > 1 && l < static_cast<int64_t>(cl) * s.rows) break;
+    // long clusters leave some SMs without a block: they lie within one part of the GPU
+    int64_t fit = resident * (cl < 6 ? 95 : cl < kGroupMaxCluster ? 85 : 70) / (100 * cl);
+    if (fit < 1) fit = 1;
+    const int64_t at_once = fit < units ? fit : units;
+    const bool inside = at_once * slab_bytes <= int64_t(128) << 20;
+    const double time = static_cast<double>((units + fit - 1) / fit) *
+                        (3.0 + 0.2 * static_cast<double>(l) / (cl * s.rows));
+    if (best > 0 && (!inside || time >= best)) continue;
+    best = inside ? time : 0;                  // a later one replaces what L2 does not hold
     s.cluster = cl;
-    const int64_t at_once = resident / cl < units ? resident / cl : units;
-    if (2 * units * cl >= 3 * resident && at_once * slab_bytes <= (int64_t(128) << 20)) break;
   }
-  s.smem = (static_cast<size_t>(s.threads) + static_cast<size_t>(s.cluster + 1) * slab_groups) * 8;
+  s.smem = (static_cast<size_t>(s.threads) + static_cast<size_t>(s.cluster + 1) * (s.cols / q)) * 8;
   if (bwd) {
     const size_t part = static_cast<size_t>(s.rows) * s.cols * 17 * 4;
     if (s.smem < part) s.smem = part;

@@ -195,12 +195,15 @@ __device__ __forceinline__ F2 rcp2(F2 v) {
 // 256 float32 channels 244 us, so 168).  Float32 arguments are held where the
 // products are finite: 1 / (1 + exp(88.7)) is flushed to zero already, and
 // exp(-104) too.  CAP: below exp(87), 2^126, whose reciprocal is still normal.
-template <int DT, bool CAP>
+// SIGN: of exp(SIGN g).
+template <int DT, bool CAP, int SIGN = 1>
 __device__ __forceinline__ F2 exp2_of(F2 g) {
-  const F2 log2e = f2(1.4426950408889634f, 1.4426950408889634f);
+  const F2 log2e = f2(SIGN * 1.4426950408889634f, SIGN * 1.4426950408889634f);
   float2 x;
   F2 rest = f2(0.f, 0.f);
   if constexpr (DT == SP_F32) {
+    static_assert(SIGN == 1 || !CAP, "the bounds are those of exp(g)");
+    if constexpr (SIGN < 0) g = mul2(g, f2(-1.f, -1.f));
     x = split(g);
     asm("max.NaN.f32 %0, %0, 0fC2D00000;" : "+f"(x.x));     // -104
     asm("max.NaN.f32 %0, %0, 0fC2D00000;" : "+f"(x.y));
@@ -212,7 +215,7 @@ __device__ __forceinline__ F2 exp2_of(F2 g) {
       asm("min.NaN.f32 %0, %0, 0f42B16666;" : "+f"(x.y));
     }
     g = f2(x.x, x.y);
-    const F2 t = mul2(g, log2e);
+    const F2 t = mul2(g, f2(1.4426950408889634f, 1.4426950408889634f));
     rest = fma2(g, f2(-1.4426950408889634f, -1.4426950408889634f), t);
     rest = fma2(g, f2(-1.92596299e-8f, -1.92596299e-8f), rest);
     rest = mul2(rest, f2(-0.69314718f, -0.69314718f));
