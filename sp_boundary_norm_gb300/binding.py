@@ -663,6 +663,17 @@ def _rank_floats(x0, t, shape, **lists):
     return out
 
 
+def _params(x0, n, **vectors):
+    """Address of each contiguous vector of n elements of x0's type (None: none)."""
+    got = _readers().params(x0, n, *vectors.values())
+    if got is not None:
+        return got
+    for what, v in vectors.items():
+        if v is not None:
+            _need(v, (n,), x0.dtype, x0.device, what)
+    return [_ptr(v) for v in vectors.values()]
+
+
 def _first(xs, dims, what):
     """Ranks, dtype code and device of a list of rank buffers."""
     t = len(xs)
@@ -687,7 +698,7 @@ def _call(dev, fn, *args):
     if dev.type != "cuda":
         raise ValueError(f"tensors on {dev}: the kernels need a CUDA device")
     stream = torch._C._cuda_getCurrentRawStream(dev.index)   # the current stream's handle
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         _check(fn(*args, stream))
     else:
         with _on_device(dev):
@@ -836,18 +847,17 @@ def sp_group_norm_fwd(x, gamma, beta=None, *, groups, eps, norm="layernorm", act
     lib = load()
     t, x0, dt = _first(x, 3, "x")
     n, l, c = x0.shape
-    dev, dtype = x0.device, x0.dtype
+    dev = x0.device
     ln = norm == "layernorm"
     xa, x_ld, ya, y_ld = _rank_rows(x0, t, x=x, y=y)
-    _need(gamma, (t * c,), dtype, dev, "gamma")
-    if ln:
-        _need(beta, (t * c,), dtype, dev, "beta")
-        if mean is None:
-            raise ValueError("mean is required for layernorm")
+    if gamma is None or ln and beta is None:
+        raise TypeError("gamma (and beta for layernorm) must be a torch.Tensor")
+    gp, bp = _params(x0, t * c, gamma=gamma, beta=beta if ln else None)
+    if ln and mean is None:
+        raise ValueError("mean is required for layernorm")
     ma, ra = _rank_floats(x0, t, (n, groups), mean=mean if ln else None, rstd=rstd)
-    _call(dev, lib.sp_group_norm_fwd, xa, x_ld, gamma.data_ptr(), beta.data_ptr() if ln else None,
-          n, l, c, groups, t, dt, float(eps), _choice(NORMS, norm, "norm"),
-          _choice(ACTS, act, "act"), ya, y_ld, ma, ra)
+    _call(dev, lib.sp_group_norm_fwd, xa, x_ld, gp, bp, n, l, c, groups, t, dt, float(eps),
+          _choice(NORMS, norm, "norm"), _choice(ACTS, act, "act"), ya, y_ld, ma, ra)
 
 
 def sp_group_norm_bwd_workspace_bytes(n, l, c, groups, t, dtype=torch.bfloat16):
@@ -863,14 +873,14 @@ def sp_group_norm_bwd(dy, x, mean, rstd, gamma, beta=None, *, groups, norm="laye
     lib = load()
     t, x0, dt = _first(x, 3, "x")
     n, l, c = x0.shape
-    dev, dtype = x0.device, x0.dtype
+    dev = x0.device
     ln = norm == "layernorm"
     da, d_ld, xa, x_ld, oa, o_ld = _rank_rows(x0, t, dy=dy, x=x, dx=dx)
-    _need(gamma, (t * c,), dtype, dev, "gamma")
-    if ln:
-        _need(beta, (t * c,), dtype, dev, "beta")
-        if mean is None:
-            raise ValueError("mean is required for layernorm")
+    if gamma is None or ln and beta is None:
+        raise TypeError("gamma (and beta for layernorm) must be a torch.Tensor")
+    gp, bp = _params(x0, t * c, gamma=gamma, beta=beta if ln else None)
+    if ln and mean is None:
+        raise ValueError("mean is required for layernorm")
     ma, ra = _rank_floats(x0, t, (n, groups), mean=mean if ln else None, rstd=rstd)
     for name, v in (("dgamma", dgamma), ("dbeta", dbeta)):
         if v is not None:
@@ -878,9 +888,9 @@ def sp_group_norm_bwd(dy, x, mean, rstd, gamma, beta=None, *, groups, norm="laye
     if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(dev, lib.sp_group_norm_bwd, da, d_ld, xa, x_ld, ma, ra, gamma.data_ptr(),
-          beta.data_ptr() if ln else None, n, l, c, groups, t, dt, _choice(NORMS, norm, "norm"),
-          _choice(ACTS, act, "act"), oa, o_ld, dgamma.data_ptr() if dgamma is not None else None,
+    _call(dev, lib.sp_group_norm_bwd, da, d_ld, xa, x_ld, ma, ra, gp, bp, n, l, c, groups, t, dt,
+          _choice(NORMS, norm, "norm"), _choice(ACTS, act, "act"), oa, o_ld,
+          dgamma.data_ptr() if dgamma is not None else None,
           dbeta.data_ptr() if dbeta is not None and ln else None,
           workspace.data_ptr() if workspace is not None else None, size)
 

@@ -195,6 +195,37 @@ PyObject* floats(PyObject* const* args, Py_ssize_t n_args) {
   return out;
 }
 
+// params(like, n, tensor or None, ...) -> (address or None, ...): contiguous
+// vectors of n elements of the first argument's type, on its device.
+PyObject* params(PyObject* const* args, Py_ssize_t n_args) {
+  Want want;
+  if (n_args < 3 || !like(args[0], 1, &want)) return nullptr;
+  const long long n = PyLong_AsLongLong(args[1]);
+  if (n < 0) return nullptr;
+  PyObject* out = PyTuple_New(n_args - 2);
+  if (out == nullptr) return nullptr;
+  for (Py_ssize_t i = 2; i < n_args; ++i) {
+    if (args[i] == Py_None) {
+      Py_INCREF(Py_None);
+      PyTuple_SET_ITEM(out, i - 2, Py_None);
+      continue;
+    }
+    bool ok = THPVariable_Check(args[i]);
+    if (ok) {
+      const at::Tensor& x = THPVariable_Unpack(args[i]);
+      ok = x.defined() && x.layout() == at::kStrided && x.dim() == 1 && x.size(0) == n &&
+           (n <= 1 || x.stride(0) == 1) && x.scalar_type() == want.type &&
+           x.device() == want.device &&
+           put(out, i - 2, PyLong_FromVoidPtr(x.data_ptr()));
+    }
+    if (!ok) {
+      Py_DECREF(out);
+      return nullptr;
+    }
+  }
+  return out;
+}
+
 // A call that found something else, or met a C++ exception (a tensor subclass
 // without storage, say), gives None.
 template <PyObject* (*kCall)(PyObject* const*, Py_ssize_t)>
@@ -222,6 +253,7 @@ PyMethodDef kMethods[] = {
                   "heads(like, t, list, ...) -> (addresses, token stride, head stride, ...) or None"),
     method<floats>("floats",
                    "floats(like, t, shape, list or None, ...) -> (addresses or None, ...) or None"),
+    method<params>("params", "params(like, n, tensor or None, ...) -> (address or None, ...) or None"),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_sptensors", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -732,3 +732,8 @@ def test_list_readers_agree_with_the_checks():
     for bad in (x.half(), x[:4], x.cpu(), x.t(), x[None], x.float()):
         assert read.rows(x, 2, [x, bad]) is None
     assert read.rows(x, 1, [x, x]) is None and read.rows(x, 2, [x, x[:, ::2]]) is None
+    v = torch.zeros(6, dtype=torch.bfloat16, device="cuda")
+    assert read.params(x, 6, v, None) == (v.data_ptr(), None)
+    assert read.params(x, 1, v[::7]) == (v.data_ptr(),)
+    for bad in (v[:5], v.half(), v.cpu(), torch.zeros(12, dtype=v.dtype, device="cuda")[::2], v[None]):
+        assert read.params(x, 6, bad) is None

@@ -278,6 +278,8 @@ def test_list_readers_take_only_matching_cuda_tensors():
         assert read.rows(x, 1, xs) is None
         assert read.heads(x[None, None], 1, xs) is None
         assert read.floats(x, 1, (2, 3), xs) is None
+    for v in (x, x[0], None, 3, torch.zeros(3)):
+        assert read.params(x, 3, v) is None
     for args in ((), (x,), (x, 1), (None, 1, [x]), (x, "a", [x]), (x, 0, []), (x, 1 << 70, [x]),
                  (x[0, 0], 1, [x[0, 0]])):
         assert read.rows(*args) is None
