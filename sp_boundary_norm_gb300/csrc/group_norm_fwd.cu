@@ -475,6 +475,15 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   }
   s.form = kUnitForm;
   narrow();
+  const int64_t units = n * t * s.slabs;
+  // Few long slabs, whose longest clusters leave SMs free, take blocks of twice the
+  // threads.  (Forward and backward in us: 65,536 rows of one group of 64 29, 48
+  // against 41, 62; 20,000 float32 rows of one of 320 86, 122 against 99, 160.  From 10
+  // units on the longest clusters of such blocks do not all fit: 32,771 rows of 2 x
+  // 640 in 5 groups 76, 81 against 56, 78.)
+  if (units * kGroupMaxCluster * 10 <= int64_t(9) * sms && 2 * s.cols <= kGroupThreads &&
+      l >= int64_t(64) * s.rows)
+    s.rows = kGroupThreads / s.cols;
   s.threads = (s.rows * s.cols + 31) / 32 * 32;
   // Of the clusters that leave what the blocks at work read inside L2 (129 MB) the
   // one with the least waves x (3 us + 0.2 us a vector of a thread): short rows of
@@ -482,9 +491,9 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
   // 320 in 5 groups: C = 1 17, 28; 2 14, 29; 3 18, 27; 6 21, 37.  8 of 4096 x 1280 in
   // 32: 1 68, 111; 2 49, 78; 3 45, 95; 4 52, 79; 6 45, 81; 12 53, 93.  8 ranks' 4 of
   // 2048 x 2048 in 8: 1 146, 228; 3 134, 233; 6 130, 230; 16 195, 311.)
-  const int64_t resident = static_cast<int64_t>(bwd ? kBackUnitBlocks : kUnitBlocks) * sms;
+  const int64_t resident =
+      static_cast<int64_t>(s.threads > 256 ? 1 : bwd ? kBackUnitBlocks : kUnitBlocks) * sms;
   const int64_t slab_bytes = l * s.cols * 8 * size * (bwd ? 2 : 1);
-  const int64_t units = n * t * s.slabs;
   double best = 0;
   for (int cl : kClusters) {
     if (cl > 1 && l < static_cast<int64_t>(cl) * s.rows) break;
