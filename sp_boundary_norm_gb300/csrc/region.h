@@ -97,6 +97,7 @@ struct GroupShape {
   int cols, slabs, rows, threads, samples, lanes, cluster;
   int64_t parts;
   size_t smem;
+  bool roomy;                           // units: an SM holds two blocks at most
 };
 
 GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int dtype, bool bwd);
