@@ -11,13 +11,19 @@
 // compute the token's sines and cosines once into shared memory, each lane
 // keeps those of its own vector of pairs in registers and walks the heads, so
 // a pair costs one rotation and its share of two loads and two stores.
-// Bound by HBM: reads x once, writes y once.
+// Bound by HBM: reads x once, writes y once.  Measured on a GB300, bf16, packed
+// sequences of 16,384 tokens: 8 ranks of 9 heads of 128 95 us, 6.4 TB/s, 94 % of
+// the measured copy rate (interleaved 97); 16 heads of 256 of which 64 turn 57;
+// 64 tokens of 8 ranks' 8 heads 3.1, which is the launch and one trip to memory.
 #include "region.cuh"
 
 namespace spb {
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeRounds = 4;    // of heads side by side that a lane reads at once
+// Rounds of heads side by side that a lane reads at once; twice as many where an
+// item is one 16-byte load (interleaved, 8 ranks of 9 heads of 128: 97 us, with
+// four 101).
+constexpr int kRopeRounds = 4;
 
 // a / b for 0 <= a < most: in 32 bits where they do (a 64-bit division costs a
 // hundred instructions).
@@ -32,7 +38,10 @@ __device__ __forceinline__ int rank_of_head(const RopeParams& P, int hh) {
   return P.heads == 1 ? hh : static_cast<int>(__umulhi(static_cast<uint32_t>(hh), P.heads_magic));
 }
 
-// Blocks an SM that the registers are held to: by what a lane has on its way.
+// Blocks an SM that the registers are held to, by what a lane has on its way: two
+// where an item is two 16-byte loads (half layout, 9 heads of 128 95 us, with four
+// 100; 16 heads of 256 of which 64 turn 57 against 77), else four (5 heads of 80 of
+// which 20 turn 26 us, with two 34).
 constexpr int rope_blocks(int dt, int v, int layout) {
   const int bytes = v * (dt == SP_F32 ? 4 : 2) * (layout == SP_ROPE_HALF || v == 1 ? 2 : 1);
   return bytes >= 32 ? 2 : 4;

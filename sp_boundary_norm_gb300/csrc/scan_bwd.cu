@@ -6,12 +6,17 @@
 //   dvalue[i] = dh[i] k[i]                      (tied)   or  dh[i]
 // The states h are computed again from the forward's state at the start of
 // each run, in float32: that reads a quarter byte an element instead of the
-// two of the rounded output, and the difference h - v keeps its digits.
+// two of the rounded output, and the difference h - v keeps its digits.  Bound by
+// HBM for many channels, 84 % of the measured copy rate (scan.cuh has the
+// figures); three blocks an SM, because a run's 48 factors stay in registers
+// between the two directions.
 #include "scan.cuh"
 
 namespace spb {
 
-constexpr int kBwdBlocks = 3;   // blocks an SM that the registers are held to
+// Blocks an SM that the registers are held to (16,384 tokens x 8 ranks of 1024
+// channels: three 235 us, two 262, four, with spilled registers, 377).
+constexpr int kBwdBlocks = 3;
 
 // The run's factors, from its rows in shared memory: nk = -k, and dg = dgate
 // without its factor dh.  i0, h0: the first token that begins a sequence and the
