@@ -375,7 +375,7 @@ sp_status_t sp_norm_bwd_bitmask(const void* const* dy, const void* const* z,
  *  - Row strides ("*_ld") count elements between consecutive tokens, so that
  *    a slice of a wider (fused) projection can be passed as it is; a batch row
  *    follows the last row of the one before it.  Multiples of 8 elements, at
- *    least the row's width.
+ *    least the row's width, at most 2^28 (else SP_ERR_UNSUPPORTED).
  *  - cu_seqlens as above: NULL (dense) or the packed sequences' prefix sums,
  *    with b == 1.  Sequences without tokens are allowed.  What the outputs
  *    hold is undefined where the device check fails, but no access leaves the
@@ -472,6 +472,8 @@ sp_status_t sp_rope_bwd(const void* const* dy, int64_t dy_ld, int64_t dy_head, i
  * states         [t] (b, ceil(s / 16), c) float32 or a NULL array: the states the
  *                    backward starts from (output); their contents are internal
  * s == 1 without cu_seqlens is a decoding step of b sequences.
+ * dev_status reads SP_ERR_TIMEOUT (forward and backward) should a bounded wait
+ * for another block of the same sequence run out; y is undefined then.
  */
 sp_status_t sp_gated_scan_fwd(const void* const* gate, int64_t gate_ld, const void* const* value,
                               int64_t value_ld, const float* const* h0, int64_t b, int64_t s,
@@ -487,7 +489,7 @@ sp_status_t sp_gated_scan_fwd(const void* const* gate, int64_t gate_ld, const vo
  * dy     [t] (b, s, c)        gradient of y
  * dhT    [t] (n, c) float32   gradient of hT, or a NULL array (zero)
  * dgate, dvalue [t] (b, s, c) outputs
- * dh0    [t] (n, c) float32   output or a NULL array
+ * dh0    [t] (n, c) float32   output or a NULL array (dhT may not be the same buffer)
  */
 sp_status_t sp_gated_scan_bwd(const void* const* gate, int64_t gate_ld, const void* const* value,
                               int64_t value_ld, const float* const* h0,
@@ -517,7 +519,8 @@ sp_status_t sp_group_norm_fwd(const void* const* x, int64_t x_ld, const void* ga
                               void* const* y, int64_t y_ld, float* const* mean,
                               float* const* rstd, void* stream);
 
-/* Bytes of the workspace of sp_group_norm_bwd (0 for an invalid shape). */
+/* Bytes of the workspace of sp_group_norm_bwd on the current device (0 for an
+ * invalid shape). */
 size_t sp_group_norm_bwd_workspace_bytes(int64_t n, int64_t l, int64_t c, int64_t groups,
                                          int32_t t, sp_dtype_t dtype);
 
