@@ -176,21 +176,22 @@ cudaError_t max_clusters(const void* fn, int threads, size_t smem, int cluster, 
     size_t smem;
     int threads, cluster, device, fit;
   };
-  constexpr int kSlots = 1024;
+  // A slot by hash; another entry's is taken over.
+  constexpr size_t kSlots = 4096;
   static std::mutex mu;
   static Entry known[kSlots];
-  static int used = 0;
   cudaError_t e = ensure_smem_attr(fn, smem);
   if (e != cudaSuccess) return e;
   const int dev = current_device();
+  const size_t mix = (reinterpret_cast<uintptr_t>(fn) >> 4) * 31 + smem * 17 +
+                     static_cast<size_t>(threads) * 7 + static_cast<size_t>(cluster) * 257 +
+                     static_cast<size_t>(dev) * 1021;
+  Entry& slot = known[(mix ^ (mix >> 12)) % kSlots];
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < used; ++i) {
-    const Entry& k = known[i];
-    if (k.fn == fn && k.smem == smem && k.threads == threads && k.cluster == cluster &&
-        k.device == dev) {
-      *fit = k.fit;
-      return cudaSuccess;
-    }
+  if (slot.fn == fn && slot.smem == smem && slot.threads == threads && slot.cluster == cluster &&
+      slot.device == dev) {
+    *fit = slot.fit;
+    return cudaSuccess;
   }
   *fit = 0;
   if (cluster > 8) {
@@ -212,7 +213,7 @@ cudaError_t max_clusters(const void* fn, int threads, size_t smem, int cluster, 
     cudaGetLastError();
     *fit = 0;                    // this size does not run here
   }
-  if (used < kSlots) known[used++] = Entry{fn, smem, threads, cluster, dev, *fit};
+  slot = Entry{fn, smem, threads, cluster, dev, *fit};
   return cudaSuccess;
 }
 

@@ -737,3 +737,61 @@ def test_list_readers_agree_with_the_checks():
     assert read.params(x, 1, v[::7]) == (v.data_ptr(),)
     for bad in (v[:5], v.half(), v.cpu(), torch.zeros(12, dtype=v.dtype, device="cuda")[::2], v[None]):
         assert read.params(x, 6, bad) is None
+
+
+def test_offsets_beyond_32_bits():
+    """Rows so far apart that elements and bytes pass 2^32: the same bits as dense
+    rows, whatever the form; slices of one buffer beside each other."""
+    rows, ld = 4400, 1 << 20
+    wide = torch.empty(rows * ld, dtype=BF, device=DEV)        # 9.2 GB
+    assert wide.numel() > 2 ** 32
+    gen = torch.Generator().manual_seed(91)
+    at = iter(range(0, ld, 1024))
+
+    def far(x):
+        """A copy of (b, s, c) x as a slice of the wide buffer."""
+        b, s, c = x.shape
+        v = wide.as_strided((b, s, c), (s * ld, ld, 1), next(at))
+        v.copy_(x)
+        return v
+
+    def near(b, s, c):
+        return rand((b, s, c), gen, BF)
+
+    # rotary
+    x, tab = near(1, rows, 3 * 64), sp.sp_rope_table(48)
+    y, v = torch.empty_like(x), far(x)
+    w = far(torch.zeros_like(x))
+    heads = lambda z: [z.unflatten(2, (3, 64))]
+    sp.sp_rope_fwd(heads(x), tab, y=heads(y))
+    sp.sp_rope_fwd(heads(v), tab, y=heads(w))
+    assert same([y], [w])
+    # recurrence, dense and packed
+    cu = torch.tensor([0, 7, 4000, rows], dtype=torch.int32, device=DEV)
+    for b, s, how in ((1, rows, None), (4, rows // 4, None), (1, rows, cu)):
+        n = b if how is None else 3
+        i = scan_inputs(1, n, b, s, 72, BF, 92, True)
+        want = run_scan(i, n, True, how, True)
+        i.update({k: [far(i[k][0])] for k in ("gate", "value", "dy")})
+        o = {k: [far(torch.zeros_like(want[k][0]))]
+             for k in ("y", "dgate", "dvalue")}
+        o.update({k: [torch.empty_like(want[k][0])] for k in ("hT", "states", "dh0")})
+        sp.sp_gated_scan_fwd(i["gate"], i["value"], h0=i["h0"], cu_seqlens=how, y=o["y"],
+                             hT=o["hT"], states=o["states"])
+        sp.sp_gated_scan_bwd(i["gate"], i["value"], o["states"], i["dy"], h0=i["h0"],
+                             dhT=i["dhT"], cu_seqlens=how, dgate=o["dgate"], dvalue=o["dvalue"],
+                             dh0=o["dh0"])
+        for k in ("y", "dgate", "dvalue", "hT", "dh0"):
+            assert same(o[k], want[k]), (b, k)
+    # group norm: rows, tiles, held, units
+    for n, l in ((rows, 1), (rows // 4, 4), (rows // 50, 50), (2, rows // 2)):
+        i = norm_inputs(1, n, l, 128, BF, 93)
+        want = run_norm(i, 4, "layernorm", "silu")
+        i["x"], i["dy"] = [far(i["x"][0])], [far(i["dy"][0])]
+        y, dx = [far(torch.zeros_like(want["y"][0]))], [far(torch.zeros_like(want["y"][0]))]
+        mean, rstd = (torch.empty((n, 4), device=DEV) for _ in range(2))
+        sp.sp_group_norm_fwd(i["x"], i["gamma"], i["beta"], groups=4, eps=1e-5, act="silu", y=y,
+                             mean=[mean], rstd=[rstd])
+        sp.sp_group_norm_bwd(i["dy"], i["x"], [mean], [rstd], i["gamma"], i["beta"], groups=4,
+                             act="silu", dx=dx)
+        assert same(y, want["y"]) and same(dx, want["dx"]), (n, l)
