@@ -109,7 +109,9 @@ struct Column {
 // Sums over `width` neighbouring lanes (a power of two, aligned), N at once.
 template <int N>
 __device__ __forceinline__ void lanes_sum(float (&v)[N], int width) {
-  for (int d = width >> 1; d > 0; d >>= 1) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    if (d >= width) continue;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], d);
   }

@@ -27,12 +27,13 @@ group_row_fwd_kernel(const GroupNormParams P) {
   Column<DT> col;
   col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
   const bool tells = on && cx == in_slab * P.q;          // writes its group's statistics
-  const int64_t stat = vec / P.q;
   const int64_t first = (static_cast<int64_t>(part) * P.rows + team) * kRows;
   const int64_t step = P.parts * P.rows * kRows;
   const char* x = P.x[r] + first * P.ld_x + static_cast<int64_t>(vec) * 8 * E;
   char* out = P.out[r] + first * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
-  const int64_t step_x = step * P.ld_x, step_out = step * P.ld_out;
+  const int64_t step_x = step * P.ld_x, step_out = step * P.ld_out, step_stat = step * P.groups;
+  float* rstd_at = P.rstd[r] + first * P.groups + vec / P.q;
+  float* mean_at = ln ? P.mean[r] + first * P.groups + vec / P.q : nullptr;
 
   Vec8<DT> raw[kRows];
   auto fetch = [&](int64_t row) {
@@ -70,11 +71,12 @@ group_row_fwd_kernel(const GroupNormParams P) {
       if (!on || row + u >= P.n) continue;
       store_pack(out + u * P.ld_out, norm_act<DT>(v[u], mean[u], rstd[u], col, silu));
       if (tells) {
-        const int64_t at = (row + u) * P.groups + stat;
-        if (ln) P.mean[r][at] = mean[u];
-        P.rstd[r][at] = rstd[u];
+        rstd_at[u * P.groups] = rstd[u];
+        if (ln) mean_at[u * P.groups] = mean[u];
       }
     }
+    rstd_at += step_stat;
+    if (ln) mean_at += step_stat;
   }
 }
 
