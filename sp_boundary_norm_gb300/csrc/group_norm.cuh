@@ -20,7 +20,7 @@
 //    copies beneath the stores 57 and 107.)
 // Measured on a GB300, bf16, LayerNorm and SiLU, forward and backward (the floor
 // is the time of x, y and dy, dx at the measured copy rate, 6.8 TB/s):
-//   rows: 16,384 of 8 ranks' 8 groups of 128, RMS 95 and 157 us (floor 79, 119),
+//   rows: 16,384 of 8 ranks' 8 groups of 128, RMS 93 and 158 us (floor 79, 119),
 //     bound by the arithmetic's latency at two blocks an SM, two thirds of the
 //     issue slots taken;
 //   tiles: 16,384 samples of 4 rows of 512 50 and 61 (20, 30), bound by the
@@ -44,9 +44,9 @@ using Vec8 = Pack<DT, 8>;
 constexpr int kTileRows = 4;        // vectors a thread holds (tiles; forward)
 constexpr int kBackTileRows = 2;    // of x and of dy (tiles; backward)
 // Vectors of x a thread holds in the rows form, and blocks an SM that the
-// registers are held to (16,384 rows of 8 x 1024, RMS: 4 and 2 95 us, 2 and 4
-// 93, 2 and 3 97, 4 and 3 116 with spilled registers; wider groups and odd ones
-// want the four; float32 2 and 3 95 us, 4 and 2 111).
+// registers are held to (16,384 rows of 8 x 1024, RMS, of an earlier state of the
+// kernel: 4 and 2 95 us, 2 and 4 93, 2 and 3 97, 4 and 3 116 with spilled registers;
+// wider groups and odd ones want the four; float32 2 and 3 95 us, 4 and 2 111).
 template <int DT>
 constexpr int kRowRows = DT == SP_F32 ? 2 : 4;
 template <int DT>

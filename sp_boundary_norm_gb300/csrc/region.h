@@ -36,7 +36,7 @@ cudaError_t launch_rope(RopeParams p, int dtype, int vec, cudaStream_t st);
 // ---------------------------------------------------------- gated recurrence --
 constexpr int kScanRun = 16;        // tokens of one thread, and of one saved state
 constexpr int kScanChannels = 64;   // channels of a block: two a lane
-constexpr int kScanWarps = 4;       // of a block, at most
+constexpr int kScanWarps = 4;       // of a small block, at most
 constexpr int kScanWideWarps = 12;  // of a block that has an SM to itself
 constexpr size_t kScanMaxShared = 232448;   // bytes that a block may ask for
 constexpr int kScanMaxCluster = 16;
@@ -81,10 +81,10 @@ struct GroupNormParams {
   // the split of a call, chosen on the host
   int32_t q;                            // 8-channel vectors of a group
   int32_t cols, slabs;                  // vectors of a slab (whole groups), slabs of a row
-  int32_t rows;                         // rows side by side in a block
+  int32_t rows;                         // rows (rows form: teams) side by side in a block
   int32_t samples;                      // tiles: samples of a tile
   int32_t lanes;                        // tiles: lanes that sum one group of one sample
-  int64_t parts;                        // blocks of one rank's slab (units: of all samples)
+  int64_t parts;                        // blocks of one rank's slab (units: of all its samples)
   int32_t cluster;                      // units: blocks of a sample
   float* ws;                            // backward: [parts][2][t * c]
   int32_t has_params;                   // backward: dgamma / dbeta wanted

@@ -378,7 +378,7 @@ struct ScanCost {
 };
 
 // Chooses the split of a call and launches kernel `fn` (or `wide`).
-cudaError_t launch_scan(const void* fn, const void* wide, ScanParams& p, int elem, const ScanCost& cost, void** args,
-                        cudaStream_t st);
+cudaError_t launch_scan(const void* fn, const void* wide, ScanParams& p, int elem,
+                        const ScanCost& cost, void** args, cudaStream_t st);
 
 }  // namespace spb

@@ -205,9 +205,10 @@ static const void* scan_fwd_fn(int dtype, bool tied, bool packed) {
 // have an SM to themselves (kernel `wide`); C blocks a cluster, for the split
 // with the least expected time: the clusters that fit the GPU at once run in
 // waves, and a step of a wave takes its shortest time and that of its bytes at
-// 6.0 TB/s (the cubes add up: the longer one rules).  Many channels fill the GPU with small blocks,
-// whose steps overlap; few channels need long steps, because what a step costs
-// hardly grows with its warps.  Measured, bf16, forward and backward in us:
+// 6.0 TB/s (the cubes add up: the longer one rules).  Many channels fill the GPU
+// with small blocks, whose steps overlap; few channels need long steps, because
+// what a step costs grows less than its warps.  Measured, bf16, forward and
+// backward in us:
 //   16,384 tokens of 8192 channels: 4 warps, C = 3 172, 235; C = 4 151, 296;
 //     12 warps, C = 1 150, 246; C = 2 187, 273
 //   16,384 of 1024: 4 warps, C = 16 40, 53; 8, C = 12 47, 68; 12, C = 6 37, 55
