@@ -66,7 +66,7 @@ def _build_module():
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
            "-I", os.path.join(root, "include"), "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
-           MODULE_SRC, "-o", MODULE_PATH + ".tmp", "-L", os.path.join(root, "lib"),
+           "-I", INCLUDE, MODULE_SRC, "-o", MODULE_PATH + ".tmp", "-L", os.path.join(root, "lib"),
            "-ltorch_python", "-ltorch", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -598,15 +598,23 @@ def _row_stride(shape, strides, what):
 _module = None
 
 
-def _readers():
-    """The compiled readers of lists of rank buffers."""
+def _quick():
+    """The compiled short way: calls an entry point whose arguments are exactly right
+    (its status), or gives None."""
     global _module
     if _module is None:
+        lib = load()
         if not os.path.exists(_build.MODULE_PATH):
             raise RuntimeError(f"{_build.MODULE_PATH} is missing: build the library first")
         spec = importlib.util.spec_from_file_location("_sptensors", _build.MODULE_PATH)
-        _module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_module)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+            entries = (lib.sp_rope_fwd, lib.sp_rope_bwd, lib.sp_gated_scan_fwd,
+                       lib.sp_gated_scan_bwd, lib.sp_group_norm_fwd, lib.sp_group_norm_bwd)
+            module.setup(tuple(ctypes.cast(e, _vp).value for e in entries),
+                         torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _module = module
     return _module
 
 
@@ -632,9 +640,6 @@ def _rank_buffers(xs, x0, t, what):
 def _rank_rows(x0, t, **lists):
     """Pointer array and row stride of each list of t rank buffers, which are of x0's
     shape, type and device."""
-    got = _readers().rows(x0, t, *lists.values())
-    if got is not None:
-        return got
     out = []
     for what, xs in lists.items():
         _rank_buffers(xs, x0, t, what)
@@ -647,9 +652,6 @@ def _rank_rows(x0, t, **lists):
 
 def _rank_floats(x0, t, shape, **lists):
     """Pointer array of each list of t dense float32 rank buffers (None: no array)."""
-    got = _readers().floats(x0, t, shape, *lists.values())
-    if got is not None:
-        return got
     out = []
     for what, xs in lists.items():
         if xs is None:
@@ -665,9 +667,6 @@ def _rank_floats(x0, t, shape, **lists):
 
 def _params(x0, n, **vectors):
     """Address of each contiguous vector of n elements of x0's type (None: none)."""
-    got = _readers().params(x0, n, *vectors.values())
-    if got is not None:
-        return got
     for what, v in vectors.items():
         if v is not None:
             _need(v, (n,), x0.dtype, x0.device, what)
@@ -689,8 +688,16 @@ def _first(xs, dims, what):
     return t, x, DTYPES[x.dtype]
 
 
-def _status_word(dev):
-    return _status[dev] if dev in _status else device_status(dev)
+def _status_word(dev, status):
+    """Address of the caller's status word, or of the binding's own of the device."""
+    if status is not None:
+        if status.device != dev or status.dtype != torch.int32 or status.numel() < 1:
+            raise ValueError(f"status must be an int32 tensor on {dev}")
+        return status.data_ptr()
+    st = device_status(dev)
+    if dev.type == "cuda":
+        _quick().status(dev.index, st.data_ptr())     # the short way knows it from now on
+    return st.data_ptr()
 
 
 def _call(dev, fn, *args):
@@ -747,9 +754,6 @@ def _head_strides(x, what):
 def _rank_heads(x0, t, **lists):
     """Pointer array, token stride and head stride of each list of t (b, s, heads, d)
     rank buffers, which are of x0's shape, type and device."""
-    got = _readers().heads(x0, t, *lists.values())
-    if got is not None:
-        return got
     out = []
     for what, xs in lists.items():
         _rank_buffers(xs, x0, t, what)
@@ -761,6 +765,12 @@ def _rank_heads(x0, t, **lists):
 
 
 def _rope_call(entry, x, table, layout, positions, first_position, cu_seqlens, y, status):
+    if type(table) is RopeTable:
+        code = _quick().rope(entry == "sp_rope_bwd", x, ctypes.addressof(table),
+                             ROPE_LAYOUTS.get(layout), positions, first_position, cu_seqlens, y,
+                             status)
+        if code is not None:
+            return _check(code)
     lib = load()
     t, x0, dt = _first(x, 4, "x")
     b, s, heads, d = x0.shape
@@ -771,10 +781,10 @@ def _rope_call(entry, x, table, layout, positions, first_position, cu_seqlens, y
     if positions is not None:
         _need(positions, (b, s), torch.int64, dev, "positions")
     cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
-    st = _status_word(dev) if status is None else status
+    st = _status_word(dev, status)
     _call(dev, getattr(lib, entry), xa, x_ld, x_head, b, s, heads, d, t, dt, ctypes.byref(table),
           _choice(ROPE_LAYOUTS, layout, "layout"), _ptr(positions), int(first_position), cu,
-          n_seqs, ya, y_ld, y_head, st.data_ptr())
+          n_seqs, ya, y_ld, y_head, st)
 
 
 def sp_rope_fwd(x, table, *, layout="half", positions=None, first_position=0, cu_seqlens=None, y,
@@ -803,6 +813,9 @@ def sp_gated_scan_fwd(gate, value, *, h0=None, tied=True, cu_seqlens=None, y, hT
     h = sigmoid(gate) h + (sigmoid(-gate) value if tied else value), y = h.
     h0, hT: float32 (sequences, c) states before and after each sequence (hT may be
     h0); states: sp_gated_scan_states_shape buffers that sp_gated_scan_bwd needs."""
+    code = _quick().scan_fwd(gate, value, h0, tied, cu_seqlens, y, hT, states, status)
+    if code is not None:
+        return _check(code)
     lib = load()
     t, x0, dt = _first(gate, 3, "gate")
     b, s, c = x0.shape
@@ -814,15 +827,19 @@ def sp_gated_scan_fwd(gate, value, *, h0=None, tied=True, cu_seqlens=None, y, hT
     sa = None
     if states is not None:
         sa, = _rank_floats(x0, t, sp_gated_scan_states_shape(b, s, c), states=states)
-    st = _status_word(dev) if status is None else status
+    st = _status_word(dev, status)
     _call(dev, lib.sp_gated_scan_fwd, ga, g_ld, va, v_ld, ha, b, s, c, t, dt, int(bool(tied)), cu,
-          n_seqs, ya, y_ld, ta, sa, st.data_ptr())
+          n_seqs, ya, y_ld, ta, sa, st)
 
 
 def sp_gated_scan_bwd(gate, value, states, dy, *, h0=None, dhT=None, tied=True, cu_seqlens=None,
                       dgate, dvalue, dh0=None, status=None):
     """Gradients of sp_gated_scan_fwd (same gate, value, h0, tied, cu_seqlens) from
     the states it saved; dhT: gradient of hT, dh0: gradient of h0."""
+    code = _quick().scan_bwd(gate, value, h0, tied, cu_seqlens, states, dy, dhT, dgate, dvalue, dh0,
+                             status)
+    if code is not None:
+        return _check(code)
     lib = load()
     t, x0, dt = _first(gate, 3, "gate")
     b, s, c = x0.shape
@@ -833,9 +850,9 @@ def sp_gated_scan_bwd(gate, value, states, dy, *, h0=None, dhT=None, tied=True, 
     n = b if cu is None else n_seqs
     ha, ta, oa = _rank_floats(x0, t, (n, c), h0=h0, dhT=dhT, dh0=dh0)
     sa, = _rank_floats(x0, t, sp_gated_scan_states_shape(b, s, c), states=states)
-    st = _status_word(dev) if status is None else status
+    st = _status_word(dev, status)
     _call(dev, lib.sp_gated_scan_bwd, ga, g_ld, va, v_ld, ha, sa, da, d_ld, ta, b, s, c, t, dt,
-          int(bool(tied)), cu, n_seqs, dga, dg_ld, dva, dv_ld, oa, st.data_ptr())
+          int(bool(tied)), cu, n_seqs, dga, dg_ld, dva, dv_ld, oa, st)
 
 
 def sp_group_norm_fwd(x, gamma, beta=None, *, groups, eps, norm="layernorm", act="none", y,
@@ -844,6 +861,10 @@ def sp_group_norm_fwd(x, gamma, beta=None, *, groups, eps, norm="layernorm", act
     channels last; the statistics of each of the `groups` groups of a rank span the l
     rows of a sample (l = 1: per token).  gamma, beta: (t * c).  mean (LayerNorm) and
     rstd: float32 (n, groups) per rank, written for the backward."""
+    code = _quick().norm_fwd(x, gamma, beta, groups, eps, NORMS.get(norm), ACTS.get(act), y, mean,
+                             rstd)
+    if code is not None:
+        return _check(code)
     lib = load()
     t, x0, dt = _first(x, 3, "x")
     n, l, c = x0.shape
@@ -870,6 +891,10 @@ def sp_group_norm_bwd(dy, x, mean, rstd, gamma, beta=None, *, groups, norm="laye
     """Gradients of sp_group_norm_fwd from its input and saved statistics: dx, and
     where given the float32 (t * c) dgamma and dbeta (these need the workspace of
     sp_group_norm_bwd_workspace_bytes, one per call that may run at the same time)."""
+    code = _quick().norm_bwd(dy, x, mean, rstd, gamma, beta, groups, NORMS.get(norm), ACTS.get(act),
+                             dx, dgamma, dbeta, workspace)
+    if code is not None:
+        return _check(code)
     lib = load()
     t, x0, dt = _first(x, 3, "x")
     n, l, c = x0.shape

@@ -1,9 +1,13 @@
-// Reads lists of rank buffers at once for the Python binding: their addresses
-// and common strides, if every tensor has the wanted shape, type and device.  A
-// call of the boundary's operators over t ranks passes dozens of buffers;
-// checking each from Python costs half a microsecond a buffer, several times
-// the kernel of a decoding step.  Anything else than lists of matching tensors
-// gives None: the binding then looks at them one by one and says what is wrong.
+// The Python binding's short way to the operators between g and the next g*: it
+// reads the tensors of a call, finds their strides and the current stream, and
+// calls the entry point.  A call over t ranks passes dozens of buffers; looking at
+// each from Python costs half a microsecond a buffer and the call through ctypes
+// two, several times the kernel of a decoding step (64 tokens, 8 ranks, any operator:
+// 10 to 14 us a call otherwise, 4 to 6 this way).
+//
+// Only what is exactly right is taken: lists of equal CUDA tensors on the current
+// device, of the documented shapes and types.  Anything else gives None, and the
+// binding goes through the call itself and says what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -12,9 +16,21 @@
 
 #include <cstdint>
 
+#include "sp_boundary.h"
+
 namespace {
 
-constexpr Py_ssize_t kMostRanks = 64, kMostDims = 8;
+constexpr Py_ssize_t kMostDims = 4;
+constexpr int kMostDevices = 64;
+
+// What setup() and status() were given.
+decltype(&sp_rope_fwd) g_rope_fwd, g_rope_bwd;
+decltype(&sp_gated_scan_fwd) g_scan_fwd;
+decltype(&sp_gated_scan_bwd) g_scan_bwd;
+decltype(&sp_group_norm_fwd) g_norm_fwd;
+decltype(&sp_group_norm_bwd) g_norm_bwd;
+PyObject *g_get_device, *g_get_stream;
+int32_t* g_status[kMostDevices];
 
 // What the buffers of a call have to be.
 struct Want {
@@ -25,26 +41,36 @@ struct Want {
 };
 
 struct Buffers {
-  uint64_t address[kMostRanks];
+  void* address[SP_MAX_RANKS];
   int64_t strides[kMostDims];   // of every buffer
+  int64_t ld, head;
+  // the array as the entry points take it
+  template <typename T>
+  T* const* as() const {
+    return reinterpret_cast<T* const*>(address);
+  }
 };
+
+const at::Tensor* tensor(PyObject* v) {
+  if (!THPVariable_Check(v)) return nullptr;
+  const at::Tensor& x = THPVariable_Unpack(v);
+  return x.defined() && x.layout() == at::kStrided ? &x : nullptr;
+}
 
 bool read_list(PyObject* list, const Want& want, Buffers* out) {
   if (!PyList_Check(list) && !PyTuple_Check(list)) return false;
   if (PySequence_Fast_GET_SIZE(list) != want.t) return false;
   for (Py_ssize_t i = 0; i < want.t; ++i) {
-    PyObject* item = PySequence_Fast_GET_ITEM(list, i);
-    if (!THPVariable_Check(item)) return false;
-    const at::Tensor& x = THPVariable_Unpack(item);
-    if (!x.defined() || x.layout() != at::kStrided || x.dim() != want.dims ||
-        x.scalar_type() != want.type || x.device() != want.device)
+    const at::Tensor* x = tensor(PySequence_Fast_GET_ITEM(list, i));
+    if (x == nullptr || x->dim() != want.dims || x->scalar_type() != want.type ||
+        x->device() != want.device)
       return false;
-    const auto sizes = x.sizes(), steps = x.strides();
+    const auto sizes = x->sizes(), steps = x->strides();
     for (Py_ssize_t d = 0; d < want.dims; ++d) {
       if (sizes[d] != want.sizes[d] || (i > 0 && steps[d] != out->strides[d])) return false;
       out->strides[d] = steps[d];
     }
-    out->address[i] = reinterpret_cast<uint64_t>(x.data_ptr());
+    out->address[i] = x->data_ptr();
   }
   return true;
 }
@@ -61,169 +87,293 @@ bool dense(const Want& want, const int64_t* strides) {
   return yes;
 }
 
-// One stride from row to row of the leading dimensions, the last contiguous.
-bool row_stride(const Want& want, const int64_t* strides, int64_t* ld) {
+// Rank buffers with one stride from row to row of the leading dimensions, the
+// last contiguous.
+bool rows(PyObject* list, const Want& want, Buffers* out) {
+  if (!read_list(list, want, out)) return false;
+  const int64_t* strides = out->strides;
   const Py_ssize_t last = want.dims - 1;
-  *ld = want.sizes[last];
+  out->ld = want.sizes[last];
   if (dense(want, strides)) return true;
   if (want.sizes[last] > 1 && strides[last] != 1) return false;
   int64_t span = 1;
   bool known = false;
   for (Py_ssize_t d = last - 1; d >= 0; --d) {
     if (want.sizes[d] == 1) continue;
-    if (!known) *ld = strides[d];
-    else if (strides[d] != *ld * span) return false;
+    if (!known) out->ld = strides[d];
+    else if (strides[d] != out->ld * span) return false;
     known = true;
     span *= want.sizes[d];
   }
   return true;
 }
 
-// Strides from token to token and head to head of (b, s, heads, d).
-bool head_strides(const Want& want, const int64_t* strides, int64_t* ld, int64_t* head) {
-  const int64_t b = want.sizes[0], s = want.sizes[1], heads = want.sizes[2], d = want.sizes[3];
-  *ld = heads * d;
-  *head = d;
+// (b, s, heads, d) rank buffers: strides from token to token and head to head.
+bool heads(PyObject* list, const Want& want, Buffers* out) {
+  if (!read_list(list, want, out)) return false;
+  const int64_t b = want.sizes[0], s = want.sizes[1], n = want.sizes[2], d = want.sizes[3];
+  const int64_t* strides = out->strides;
+  out->ld = n * d;
+  out->head = d;
   if (dense(want, strides)) return true;
   if (d > 1 && strides[3] != 1) return false;
-  if (heads > 1) *head = strides[2];
+  if (n > 1) out->head = strides[2];
   if (s > 1) {
     if (b > 1 && strides[0] != s * strides[1]) return false;
-    *ld = strides[1];
+    out->ld = strides[1];
   } else if (b > 1) {
-    *ld = strides[0];
+    out->ld = strides[0];
   } else {
-    *ld = strides[1] > heads * *head ? strides[1] : heads * *head;
+    out->ld = strides[1] > n * out->head ? strides[1] : n * out->head;
   }
   return true;
 }
 
-// Puts a new reference into the tuple; false where it could not be made.
-bool put(PyObject* tuple, Py_ssize_t at, PyObject* v) {
-  if (v == nullptr) return false;
-  PyTuple_SET_ITEM(tuple, at, v);
-  return true;
-}
-
-PyObject* addresses(const Buffers& got, Py_ssize_t t) {
-  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(got.address), t * 8);
-}
-
-// Fills `want` from the first rank buffer of the call.
-bool like(PyObject* x, Py_ssize_t t, Want* want) {
-  if (!THPVariable_Check(x) || t < 1 || t > kMostRanks) return false;
-  const at::Tensor& v = THPVariable_Unpack(x);
-  if (!v.defined() || v.layout() != at::kStrided || v.dim() < 1 || v.dim() > kMostDims ||
-      !v.is_cuda())
-    return false;
-  want->t = t;
-  want->dims = v.dim();
-  for (Py_ssize_t d = 0; d < want->dims; ++d) want->sizes[d] = v.sizes()[d];
-  want->type = v.scalar_type();
-  want->device = v.device();
-  return true;
-}
-
-// rows(like, t, list, ...) -> (addresses, row stride, ...): buffers of the first
-// argument's shape, type and device.
-PyObject* rows(PyObject* const* args, Py_ssize_t n_args) {
-  Want want;
-  if (n_args < 3 || !like(args[0], PyLong_AsSsize_t(args[1]), &want)) return nullptr;
-  PyObject* out = PyTuple_New(2 * (n_args - 2));
-  if (out == nullptr) return nullptr;
-  for (Py_ssize_t i = 2; i < n_args; ++i) {
-    Buffers got;
-    int64_t ld = 0;
-    if (!read_list(args[i], want, &got) || !row_stride(want, got.strides, &ld) ||
-        !put(out, 2 * (i - 2), addresses(got, want.t)) ||
-        !put(out, 2 * (i - 2) + 1, PyLong_FromLongLong(ld))) {
-      Py_DECREF(out);
-      return nullptr;
-    }
-  }
-  return out;
-}
-
-// heads(like, t, list, ...) -> (addresses, token stride, head stride, ...): the
-// same for (b, s, heads, d) buffers.
-PyObject* heads(PyObject* const* args, Py_ssize_t n_args) {
-  Want want;
-  if (n_args < 3 || !like(args[0], PyLong_AsSsize_t(args[1]), &want) || want.dims != 4)
-    return nullptr;
-  PyObject* out = PyTuple_New(3 * (n_args - 2));
-  if (out == nullptr) return nullptr;
-  for (Py_ssize_t i = 2; i < n_args; ++i) {
-    Buffers got;
-    int64_t ld = 0, head = 0;
-    if (!read_list(args[i], want, &got) || !head_strides(want, got.strides, &ld, &head) ||
-        !put(out, 3 * (i - 2), addresses(got, want.t)) ||
-        !put(out, 3 * (i - 2) + 1, PyLong_FromLongLong(ld)) ||
-        !put(out, 3 * (i - 2) + 2, PyLong_FromLongLong(head))) {
-      Py_DECREF(out);
-      return nullptr;
-    }
-  }
-  return out;
-}
-
-// floats(like, t, shape, list or None, ...) -> (addresses or None, ...): dense
-// float32 buffers of that shape on the first argument's device.
-PyObject* floats(PyObject* const* args, Py_ssize_t n_args) {
-  Want want;
-  if (n_args < 4 || !like(args[0], PyLong_AsSsize_t(args[1]), &want) || !PyTuple_Check(args[2]))
-    return nullptr;
+// Dense float32 rank buffers of that shape, or None: *at is their array or NULL.
+bool floats(PyObject* list, const Want& like, std::initializer_list<int64_t> shape, Buffers* out,
+            float* const** at) {
+  *at = nullptr;
+  if (list == Py_None) return true;
+  Want want = like;
   want.type = at::kFloat;
-  want.dims = PyTuple_GET_SIZE(args[2]);
-  if (want.dims > kMostDims) return nullptr;
-  for (Py_ssize_t d = 0; d < want.dims; ++d) {
-    want.sizes[d] = PyLong_AsLongLong(PyTuple_GET_ITEM(args[2], d));
-    if (want.sizes[d] < 0) return nullptr;
-  }
-  PyObject* out = PyTuple_New(n_args - 3);
-  if (out == nullptr) return nullptr;
-  for (Py_ssize_t i = 3; i < n_args; ++i) {
-    Buffers got;
-    if (args[i] == Py_None) {
-      Py_INCREF(Py_None);
-      PyTuple_SET_ITEM(out, i - 3, Py_None);
-    } else if (!read_list(args[i], want, &got) || !dense(want, got.strides) ||
-               !put(out, i - 3, addresses(got, want.t))) {
-      Py_DECREF(out);
-      return nullptr;
-    }
-  }
-  return out;
+  want.dims = 0;
+  for (const int64_t n : shape) want.sizes[want.dims++] = n;
+  if (!read_list(list, want, out) || !dense(want, out->strides)) return false;
+  *at = out->as<float>();
+  return true;
 }
 
-// params(like, n, tensor or None, ...) -> (address or None, ...): contiguous
-// vectors of n elements of the first argument's type, on its device.
-PyObject* params(PyObject* const* args, Py_ssize_t n_args) {
+// A contiguous vector of n elements on the call's device, or None.
+bool vector(PyObject* v, const Want& like, at::ScalarType type, int64_t n, void** at) {
+  *at = nullptr;
+  if (v == Py_None) return true;
+  const at::Tensor* x = tensor(v);
+  if (x == nullptr || x->dim() != 1 || x->size(0) != n || (n > 1 && x->stride(0) != 1) ||
+      x->scalar_type() != type || x->device() != like.device)
+    return false;
+  *at = x->data_ptr();
+  return true;
+}
+
+// The call's shape, type and device from its first buffer, which has to be on the
+// current device; its stream.
+struct Call {
   Want want;
-  if (n_args < 3 || !like(args[0], 1, &want)) return nullptr;
-  const long long n = PyLong_AsLongLong(args[1]);
-  if (n < 0) return nullptr;
-  PyObject* out = PyTuple_New(n_args - 2);
-  if (out == nullptr) return nullptr;
-  for (Py_ssize_t i = 2; i < n_args; ++i) {
-    if (args[i] == Py_None) {
-      Py_INCREF(Py_None);
-      PyTuple_SET_ITEM(out, i - 2, Py_None);
-      continue;
-    }
-    bool ok = THPVariable_Check(args[i]);
-    if (ok) {
-      const at::Tensor& x = THPVariable_Unpack(args[i]);
-      ok = x.defined() && x.layout() == at::kStrided && x.dim() == 1 && x.size(0) == n &&
-           (n <= 1 || x.stride(0) == 1) && x.scalar_type() == want.type &&
-           x.device() == want.device &&
-           put(out, i - 2, PyLong_FromVoidPtr(x.data_ptr()));
-    }
-    if (!ok) {
-      Py_DECREF(out);
-      return nullptr;
-    }
+  sp_dtype_t dtype;
+  void* stream;
+  int32_t t() const { return static_cast<int32_t>(want.t); }
+  bool open(PyObject* list, Py_ssize_t dims) {
+    if (g_get_stream == nullptr || (!PyList_Check(list) && !PyTuple_Check(list))) return false;
+    want.t = PySequence_Fast_GET_SIZE(list);
+    if (want.t < 1 || want.t > SP_MAX_RANKS) return false;
+    const at::Tensor* x = tensor(PySequence_Fast_GET_ITEM(list, 0));
+    if (x == nullptr || x->dim() != dims || !x->is_cuda()) return false;
+    want.dims = dims;
+    for (Py_ssize_t d = 0; d < dims; ++d) want.sizes[d] = x->sizes()[d];
+    want.type = x->scalar_type();
+    want.device = x->device();
+    if (want.type == at::kBFloat16) dtype = SP_BF16;
+    else if (want.type == at::kHalf) dtype = SP_F16;
+    else if (want.type == at::kFloat) dtype = SP_F32;
+    else return false;
+    PyObject* now = PyObject_CallNoArgs(g_get_device);
+    if (now == nullptr) return false;
+    const long device = PyLong_AsLong(now);
+    Py_DECREF(now);
+    if (device < 0 || device != want.device.index()) return false;
+    PyObject* index = PyLong_FromLong(device);
+    PyObject* raw = index != nullptr ? PyObject_CallOneArg(g_get_stream, index) : nullptr;
+    Py_XDECREF(index);
+    if (raw == nullptr) return false;
+    stream = PyLong_AsVoidPtr(raw);
+    Py_DECREF(raw);
+    return PyErr_Occurred() == nullptr;
   }
-  return out;
+  // The status word: the caller's, or the binding's own of the device.
+  bool status(PyObject* v, int32_t** at) const {
+    if (v == Py_None) {
+      const int i = want.device.index();
+      *at = i >= 0 && i < kMostDevices ? g_status[i] : nullptr;
+      return *at != nullptr;
+    }
+    const at::Tensor* x = tensor(v);
+    if (x == nullptr || x->scalar_type() != at::kInt || x->device() != want.device ||
+        x->numel() < 1)
+      return false;
+    *at = static_cast<int32_t*>(x->data_ptr());
+    return true;
+  }
+  // Packed sequences' prefix sums, with one batch row; n: sequences of the call.
+  bool seqs(PyObject* v, const int32_t** cu, int32_t* n_seqs, int64_t* n) const {
+    *cu = nullptr;
+    *n_seqs = 0;
+    *n = want.sizes[0];
+    if (v == Py_None) return true;
+    const at::Tensor* x = tensor(v);
+    if (x == nullptr || want.sizes[0] != 1 || x->dim() != 1 || x->size(0) < 2 ||
+        x->size(0) > 0x7FFFFFFF)
+      return false;
+    void* at = nullptr;
+    if (!vector(v, want, at::kInt, x->size(0), &at)) return false;
+    *cu = static_cast<const int32_t*>(at);
+    *n_seqs = static_cast<int32_t>(x->size(0) - 1);
+    *n = *n_seqs;
+    return true;
+  }
+};
+
+bool number(PyObject* v, int64_t* out) {
+  *out = PyLong_AsLongLong(v);
+  return *out != -1 || PyErr_Occurred() == nullptr;
+}
+template <typename T>
+bool choice(PyObject* v, T* out) {
+  int64_t n = 0;
+  if (!number(v, &n) || n < 0 || n > 16) return false;
+  *out = static_cast<T>(n);
+  return true;
+}
+
+PyObject* code(sp_status_t st) { return PyLong_FromLong(static_cast<long>(st)); }
+
+// rope(back, x, table address, layout, positions, first position, cu_seqlens, y, status)
+PyObject* rope(PyObject* const* a, Py_ssize_t n_args) {
+  Call c;
+  Buffers x, y;
+  sp_rope_layout_t layout;
+  int64_t first, n;
+  const int32_t* cu;
+  int32_t n_seqs, *status;
+  if (n_args != 9 || !c.open(a[1], 4) || !heads(a[1], c.want, &x) || !heads(a[7], c.want, &y) ||
+      !choice(a[3], &layout) || !number(a[5], &first) || !c.seqs(a[6], &cu, &n_seqs, &n) ||
+      !c.status(a[8], &status))
+    return nullptr;
+  const auto* table = static_cast<const sp_rope_table_t*>(PyLong_AsVoidPtr(a[2]));
+  if (table == nullptr) return nullptr;
+  const int64_t b = c.want.sizes[0], s = c.want.sizes[1];
+  const int64_t* positions = nullptr;
+  if (a[4] != Py_None) {
+    const at::Tensor* p = tensor(a[4]);
+    if (p == nullptr || p->dim() != 2 || p->size(0) != b || p->size(1) != s ||
+        p->scalar_type() != at::kLong || p->device() != c.want.device || !p->is_contiguous())
+      return nullptr;
+    positions = static_cast<const int64_t*>(p->data_ptr());
+  }
+  const int back = PyObject_IsTrue(a[0]);
+  if (back < 0) return nullptr;
+  return code((back ? g_rope_bwd : g_rope_fwd)(
+      x.as<const void>(), x.ld, x.head, b, s, c.want.sizes[2], c.want.sizes[3], c.t(), c.dtype,
+      table, layout, positions, first, cu, n_seqs, y.as<void>(), y.ld, y.head, status, c.stream));
+}
+
+// scan_fwd(gate, value, h0, tied, cu_seqlens, y, hT, states, status)
+PyObject* scan_fwd(PyObject* const* a, Py_ssize_t n_args) {
+  Call c;
+  Buffers gate, value, y, b0, bT, bs;
+  float* const *h0, *const *hT, *const *states;
+  int64_t n;
+  const int32_t* cu;
+  int32_t n_seqs, *status;
+  if (n_args != 9 || !c.open(a[0], 3) || !rows(a[0], c.want, &gate) ||
+      !rows(a[1], c.want, &value) || !rows(a[5], c.want, &y) ||
+      !c.seqs(a[4], &cu, &n_seqs, &n) || !c.status(a[8], &status))
+    return nullptr;
+  const int64_t b = c.want.sizes[0], s = c.want.sizes[1], ch = c.want.sizes[2];
+  const int tied = PyObject_IsTrue(a[3]);
+  if (tied < 0 || !floats(a[2], c.want, {n, ch}, &b0, &h0) ||
+      !floats(a[6], c.want, {n, ch}, &bT, &hT) ||
+      !floats(a[7], c.want, {b, (s + 15) / 16, ch}, &bs, &states))
+    return nullptr;
+  return code(g_scan_fwd(gate.as<const void>(), gate.ld, value.as<const void>(), value.ld, h0, b,
+                         s, ch, c.t(), c.dtype, tied, cu, n_seqs, y.as<void>(), y.ld, hT, states,
+                         status, c.stream));
+}
+
+// scan_bwd(gate, value, h0, tied, cu_seqlens, states, dy, dhT, dgate, dvalue, dh0, status)
+PyObject* scan_bwd(PyObject* const* a, Py_ssize_t n_args) {
+  Call c;
+  Buffers gate, value, dy, dgate, dvalue, b0, bT, bo, bs;
+  float* const *h0, *const *dhT, *const *dh0, *const *states;
+  int64_t n;
+  const int32_t* cu;
+  int32_t n_seqs, *status;
+  if (n_args != 12 || !c.open(a[0], 3) || !rows(a[0], c.want, &gate) ||
+      !rows(a[1], c.want, &value) || !rows(a[6], c.want, &dy) || !rows(a[8], c.want, &dgate) ||
+      !rows(a[9], c.want, &dvalue) || !c.seqs(a[4], &cu, &n_seqs, &n) ||
+      !c.status(a[11], &status))
+    return nullptr;
+  const int64_t b = c.want.sizes[0], s = c.want.sizes[1], ch = c.want.sizes[2];
+  const int tied = PyObject_IsTrue(a[3]);
+  if (tied < 0 || !floats(a[2], c.want, {n, ch}, &b0, &h0) ||
+      !floats(a[7], c.want, {n, ch}, &bT, &dhT) || !floats(a[10], c.want, {n, ch}, &bo, &dh0) ||
+      !floats(a[5], c.want, {b, (s + 15) / 16, ch}, &bs, &states))
+    return nullptr;
+  return code(g_scan_bwd(gate.as<const void>(), gate.ld, value.as<const void>(), value.ld, h0,
+                         states, dy.as<const void>(), dy.ld, dhT, b, s, ch, c.t(), c.dtype, tied,
+                         cu, n_seqs, dgate.as<void>(), dgate.ld, dvalue.as<void>(), dvalue.ld,
+                         dh0, status, c.stream));
+}
+
+// norm_fwd(x, gamma, beta, groups, eps, norm, act, y, mean, rstd)
+PyObject* norm_fwd(PyObject* const* a, Py_ssize_t n_args) {
+  Call c;
+  Buffers x, y, bm, br;
+  float* const *mean, *const *rstd;
+  int64_t groups;
+  sp_norm_t norm;
+  sp_act_t act;
+  void *gamma, *beta;
+  if (n_args != 10 || !c.open(a[0], 3) || !rows(a[0], c.want, &x) || !rows(a[7], c.want, &y) ||
+      !number(a[3], &groups) || !choice(a[5], &norm) || !choice(a[6], &act))
+    return nullptr;
+  const int64_t n = c.want.sizes[0], l = c.want.sizes[1], ch = c.want.sizes[2];
+  const bool ln = norm == SP_NORM_LAYERNORM;
+  const double eps = PyFloat_AsDouble(a[4]);
+  if (PyErr_Occurred() || !vector(a[1], c.want, c.want.type, c.t() * ch, &gamma) ||
+      !vector(ln ? a[2] : Py_None, c.want, c.want.type, c.t() * ch, &beta) ||
+      !floats(ln ? a[8] : Py_None, c.want, {n, groups}, &bm, &mean) ||
+      !floats(a[9], c.want, {n, groups}, &br, &rstd) || gamma == nullptr ||
+      (ln && (beta == nullptr || mean == nullptr)))
+    return nullptr;
+  return code(g_norm_fwd(x.as<const void>(), x.ld, gamma, beta, n, l, ch, groups, c.t(), c.dtype,
+                         static_cast<float>(eps), norm, act, y.as<void>(), y.ld, mean, rstd,
+                         c.stream));
+}
+
+// norm_bwd(dy, x, mean, rstd, gamma, beta, groups, norm, act, dx, dgamma, dbeta, workspace)
+PyObject* norm_bwd(PyObject* const* a, Py_ssize_t n_args) {
+  Call c;
+  Buffers dy, x, dx, bm, br;
+  float* const *mean, *const *rstd;
+  int64_t groups;
+  sp_norm_t norm;
+  sp_act_t act;
+  void *gamma, *beta, *dgamma, *dbeta, *workspace = nullptr;
+  size_t bytes = 0;
+  if (n_args != 13 || !c.open(a[1], 3) || !rows(a[0], c.want, &dy) || !rows(a[1], c.want, &x) ||
+      !rows(a[9], c.want, &dx) || !number(a[6], &groups) || !choice(a[7], &norm) ||
+      !choice(a[8], &act))
+    return nullptr;
+  const int64_t n = c.want.sizes[0], l = c.want.sizes[1], ch = c.want.sizes[2];
+  const bool ln = norm == SP_NORM_LAYERNORM;
+  if (!vector(a[4], c.want, c.want.type, c.t() * ch, &gamma) ||
+      !vector(ln ? a[5] : Py_None, c.want, c.want.type, c.t() * ch, &beta) ||
+      !vector(a[10], c.want, at::kFloat, c.t() * ch, &dgamma) ||
+      !vector(a[11], c.want, at::kFloat, c.t() * ch, &dbeta) ||
+      !floats(ln ? a[2] : Py_None, c.want, {n, groups}, &bm, &mean) ||
+      !floats(a[3], c.want, {n, groups}, &br, &rstd) || gamma == nullptr ||
+      (ln && (beta == nullptr || mean == nullptr)))
+    return nullptr;
+  if (a[12] != Py_None) {
+    const at::Tensor* w = tensor(a[12]);
+    if (w == nullptr || w->device() != c.want.device || !w->is_contiguous()) return nullptr;
+    workspace = w->data_ptr();
+    bytes = static_cast<size_t>(w->numel()) * w->element_size();
+  }
+  return code(g_norm_bwd(dy.as<const void>(), dy.ld, x.as<const void>(), x.ld, mean, rstd, gamma,
+                         beta, n, l, ch, groups, c.t(), c.dtype, norm, act, dx.as<void>(), dx.ld,
+                         static_cast<float*>(dgamma), ln ? static_cast<float*>(dbeta) : nullptr,
+                         workspace, bytes, c.stream));
 }
 
 // A call that found something else, or met a C++ exception (a tensor subclass
@@ -241,19 +391,58 @@ PyObject* or_none(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
   Py_RETURN_NONE;
 }
 
+// setup(addresses of the six entry points, function that gives the current device,
+// function that gives a device's current stream)
+PyObject* setup(PyObject*, PyObject* args) {
+  PyObject *entries, *device, *stream;
+  if (!PyArg_ParseTuple(args, "O!OO", &PyTuple_Type, &entries, &device, &stream)) return nullptr;
+  if (PyTuple_GET_SIZE(entries) != 6) {
+    PyErr_SetString(PyExc_ValueError, "six entry points");
+    return nullptr;
+  }
+  void* at[6];
+  for (int i = 0; i < 6; ++i) {
+    at[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(entries, i));
+    if (at[i] == nullptr) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "no entry point");
+      return nullptr;
+    }
+  }
+  g_rope_fwd = reinterpret_cast<decltype(g_rope_fwd)>(at[0]);
+  g_rope_bwd = reinterpret_cast<decltype(g_rope_bwd)>(at[1]);
+  g_scan_fwd = reinterpret_cast<decltype(g_scan_fwd)>(at[2]);
+  g_scan_bwd = reinterpret_cast<decltype(g_scan_bwd)>(at[3]);
+  g_norm_fwd = reinterpret_cast<decltype(g_norm_fwd)>(at[4]);
+  g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(at[5]);
+  Py_INCREF(device);
+  Py_INCREF(stream);
+  Py_XSETREF(g_get_device, device);
+  Py_XSETREF(g_get_stream, stream);
+  Py_RETURN_NONE;
+}
+
+// status(device index, address): the binding's own status word of a device
+PyObject* status(PyObject*, PyObject* args) {
+  int index;
+  PyObject* address;
+  if (!PyArg_ParseTuple(args, "iO", &index, &address)) return nullptr;
+  void* at = PyLong_AsVoidPtr(address);
+  if (PyErr_Occurred()) return nullptr;
+  if (index >= 0 && index < kMostDevices) g_status[index] = static_cast<int32_t*>(at);
+  Py_RETURN_NONE;
+}
+
 template <PyObject* (*kCall)(PyObject* const*, Py_ssize_t)>
-PyMethodDef method(const char* name, const char* doc) {
+PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&or_none<kCall>)),
-          METH_FASTCALL, doc};
+          METH_FASTCALL, "the entry point's status, or None where the call is not taken"};
 }
 
 PyMethodDef kMethods[] = {
-    method<rows>("rows", "rows(like, t, list, ...) -> (addresses, row stride, ...) or None"),
-    method<heads>("heads",
-                  "heads(like, t, list, ...) -> (addresses, token stride, head stride, ...) or None"),
-    method<floats>("floats",
-                   "floats(like, t, shape, list or None, ...) -> (addresses or None, ...) or None"),
-    method<params>("params", "params(like, n, tensor or None, ...) -> (address or None, ...) or None"),
+    method<rope>("rope"), method<scan_fwd>("scan_fwd"), method<scan_bwd>("scan_bwd"),
+    method<norm_fwd>("norm_fwd"), method<norm_bwd>("norm_bwd"),
+    {"setup", setup, METH_VARARGS, "entry points and torch's device and stream"},
+    {"status", status, METH_VARARGS, "a device's status word"},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_sptensors", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

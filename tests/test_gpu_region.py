@@ -696,47 +696,89 @@ def test_two_streams_at_once():
                     assert same(v, g[k]) if isinstance(v, list) else same([v], [g[k]]), k
 
 
-def test_list_readers_agree_with_the_checks():
-    """The compiled readers find the strides that the checks of single buffers find,
-    and give None where those refuse."""
-    base = torch.zeros(3, 6, 5, 64, dtype=torch.bfloat16, device="cuda")
+class LongWay:
+    """The compiled short way, taking nothing."""
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def test_short_and_long_way_agree(monkeypatch):
+    """The compiled call gives what the binding's own call gives, for every order of
+    strides: the same bits, or a refusal."""
+    quick, long = sp._quick(), LongWay()
+    base = rand((3, 6, 4, 64), torch.Generator().manual_seed(95), BF)
     whole = [slice(None), slice(None, 1), slice(1, None), slice(None, None, 2), slice(2, 2)]
-    last = [slice(None), slice(16, 32), slice(None, None, 2), slice(7, 8)]
-    read, seen = sp._readers(), {True: 0, False: 0}
+    last = [slice(None), slice(16, 32), slice(None, None, 2), slice(8, 16)]
+    tab, seen = sp.sp_rope_table(8), dict.fromkeys(("both", "neither"), 0)
+    g, bt = rand((2 * 64,), torch.Generator().manual_seed(96), BF), torch.zeros(128, dtype=BF, device=DEV)
+
+    def outcome(way, call):
+        monkeypatch.setattr(sp, "_module", way)
+        try:
+            return call()
+        except (ValueError, sp.SpError) as e:
+            return type(e)
+
     for i, j, k, m in itertools.product(whole, whole, whole, last):
         x = base[i, j, k, m]
         for v in (x, x.transpose(1, 2), x.transpose(0, 1)):
-            try:
-                want = sp._head_strides(v, "x")
-            except ValueError:
-                want = None
-            got = read.heads(v, 2, [v, v], (v, v))
-            assert (got is None) == (want is None)
-            if got is not None:
-                assert tuple(got[1:3]) == tuple(want) and got[1:3] == got[4:]
-                assert got[0] == bytes(sp._pointers([v, v])) == got[3]
-            for y in (v, v[:, :, 0], v[0, :, :1]) if 0 not in v.shape else (v,):
-                try:
-                    want = sp._row_stride(y.shape, y.stride(), "x")
-                except ValueError:
-                    want = None
-                got = read.rows(y, 1, [y])
-                assert (got is None) == (want is None)
-                assert got is None or got[1] == want
-                f = y.float()[..., :1]
-                dense = read.floats(y, 1, tuple(y.shape[:-1]) + (1,), [f], None)
-                assert (dense is not None) == f.is_contiguous() and (not dense or dense[1] is None)
-                seen[want is None] += 1
+            def rope():
+                y = [torch.zeros(v.shape, dtype=BF, device=DEV) for _ in range(2)]
+                sp.sp_rope_fwd([v, v], tab, y=y)
+                return y
+
+            def norm():
+                z, d = v[:, :, 0], v.shape[-1]
+                y = [torch.zeros(z.shape, dtype=BF, device=DEV) for _ in range(2)]
+                st = [[torch.zeros(z.shape[0], 1, device=DEV) for _ in range(2)] for _ in range(2)]
+                sp.sp_group_norm_fwd([z, z], g[:2 * d], bt[:2 * d], groups=1, eps=1e-5, y=y,
+                                     mean=st[0], rstd=st[1])
+                return y + st[0] + st[1]
+
+            for call in (rope, norm) if v.shape[2] else (rope,):
+                a, b = outcome(quick, call), outcome(long, call)
+                assert isinstance(a, list) == isinstance(b, list)
+                assert same(a, b) if isinstance(a, list) else a is b
+                seen["both" if isinstance(a, list) else "neither"] += 1
     assert min(seen.values()) > 50
-    x = base[0, 0]
-    for bad in (x.half(), x[:4], x.cpu(), x.t(), x[None], x.float()):
-        assert read.rows(x, 2, [x, bad]) is None
-    assert read.rows(x, 1, [x, x]) is None and read.rows(x, 2, [x, x[:, ::2]]) is None
-    v = torch.zeros(6, dtype=torch.bfloat16, device="cuda")
-    assert read.params(x, 6, v, None) == (v.data_ptr(), None)
-    assert read.params(x, 1, v[::7]) == (v.data_ptr(),)
-    for bad in (v[:5], v.half(), v.cpu(), torch.zeros(12, dtype=v.dtype, device="cuda")[::2], v[None]):
-        assert read.params(x, 6, bad) is None
+
+
+def test_short_and_long_way_agree_on_every_operator(monkeypatch):
+    quick = sp._quick()
+    cu = torch.tensor([0, 5, 5, 40], dtype=torch.int32, device=DEV)
+    i = scan_inputs(2, 3, 1, 40, 72, FP, 97, True)
+    n = norm_inputs(2, 5, 7, 64, F32, 98)
+    x = [rand((2, 5, 3, 32), torch.Generator().manual_seed(99), F32)]
+    pos = torch.arange(10, device=DEV).view(2, 5)
+    tab, own = sp.sp_rope_table(16), torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def everything():
+        y = [torch.zeros_like(x[0])]
+        sp.sp_rope_bwd(x, tab, positions=pos, layout="interleaved", dx=y, status=own)
+        o = [y[0]]
+        for r in (run_scan(i, 3, False, cu, True), run_norm(n, 4, "layernorm", "silu"),
+                  run_norm(n, 4, "rmsnorm", "none", params=False)):
+            for v in r.values():
+                o += v if isinstance(v, list) else [] if v is None else [v]
+        return o
+
+    a = everything()
+    monkeypatch.setattr(sp, "_module", LongWay())
+    b = everything()
+    assert len(a) == len(b) and same(a, b)
+    monkeypatch.setattr(sp, "_module", quick)
+    # what the short way must leave alone
+    bad = torch.zeros(1, dtype=torch.int32)
+    for how in (dict(status=bad), dict(status=own.float()), dict(positions=pos.int()),
+                dict(positions=pos.t()), dict(cu_seqlens=cu), dict(layout="both")):
+        with pytest.raises((ValueError, TypeError)):
+            sp.sp_rope_fwd(x, tab, y=[torch.zeros_like(x[0])], **how)
+    with pytest.raises(TypeError):
+        sp.sp_group_norm_fwd(n["x"], n["gamma"], None, groups=4, eps=1e-5, y=n["x"], mean=None,
+                             rstd=None)
+    with pytest.raises(ValueError):
+        sp.sp_group_norm_fwd(n["x"], n["gamma"][:-1], n["beta"], groups=4, eps=1e-5, y=n["x"],
+                             mean=None, rstd=None)
 
 
 def test_offsets_beyond_32_bits():

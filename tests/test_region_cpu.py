@@ -269,20 +269,22 @@ def test_row_strides():
         row(x[:, ::2, :16])
 
 
-def test_list_readers_take_only_matching_cuda_tensors():
-    """Everything that is not lists of equal CUDA tensors is left to the binding's
-    own checks (None), whatever it is."""
-    x = torch.zeros(2, 3, dtype=torch.bfloat16)
-    read = sp._readers()
-    for xs in ([x], [], [None], [3], "a", None, [x] * 65, (x,)):
-        assert read.rows(x, 1, xs) is None
-        assert read.heads(x[None, None], 1, xs) is None
-        assert read.floats(x, 1, (2, 3), xs) is None
-    for v in (x, x[0], None, 3, torch.zeros(3)):
-        assert read.params(x, 3, v) is None
-    for args in ((), (x,), (x, 1), (None, 1, [x]), (x, "a", [x]), (x, 0, []), (x, 1 << 70, [x]),
-                 (x[0, 0], 1, [x[0, 0]])):
-        assert read.rows(*args) is None
-        assert read.heads(*args) is None
-    for shape in (None, ("a", 3), (1,) * 9, (2, 1 << 70), (-1, 3), ()):
-        assert read.floats(x, 1, shape, [x]) is None
+def test_short_way_takes_only_cuda_tensors():
+    """Whatever is not lists of equal CUDA tensors gives None (the binding then goes
+    through it and says what is wrong), never an exception."""
+    x = torch.zeros(2, 3, 8, dtype=torch.bfloat16)
+    quick, table = sp._quick(), sp.sp_rope_table(4)
+    at = ctypes.addressof(table)
+    f = torch.zeros(2, 1)
+    for xs in ([x], [], [None], [3], "a", None, [x] * 17, (x,), [x[0]], [x.int()], 7):
+        assert quick.rope(False, xs, at, 0, None, 0, None, xs, None) is None
+        assert quick.scan_fwd(xs, xs, None, True, None, xs, None, None, None) is None
+        assert quick.scan_bwd(xs, xs, None, 1, None, xs, xs, None, xs, xs, None, None) is None
+        assert quick.norm_fwd(xs, x[0, 0], x[0, 0], 1, 1e-5, 0, 0, xs, [f], [f]) is None
+        assert quick.norm_bwd(xs, xs, [f], [f], x[0, 0], None, 1, 1, 0, xs, None, None, None) is None
+    for name in ("rope", "scan_fwd", "scan_bwd", "norm_fwd", "norm_bwd"):
+        for n in (0, 1, 9, 12, 20):
+            assert getattr(quick, name)(*[None] * n) is None
+    for wrong in ((), ((1, 2), None, None), ((0,) * 6, None, None), ("ab", None, None)):
+        with pytest.raises((TypeError, ValueError)):
+            quick.setup(*wrong)
