@@ -47,37 +47,66 @@ constexpr int rope_blocks(int dt, int v, int layout) {
   return bytes >= 32 ? 2 : 4;
 }
 
-// Copies what follows the rotated elements of a token's heads h0 .. h1 - 1, B
-// bytes a lane, several heads side by side and four rounds at once.
-template <int B>
-__device__ __forceinline__ void copy_rest(const RopeParams& P, int64_t tok, int h0, int h1) {
-  constexpr int kRounds = 4;
+// What follows the rotated elements of a token's heads h0 .. h1 - 1 is copied B
+// bytes a lane, several heads side by side and kRestRounds rounds at once; the
+// first of them are asked for before the angles and wait in `held`.
+constexpr int kRestRounds = 4;
+using Held = Pack<SP_BF16, 8>[kRestRounds];
+
+template <int B, typename Use>
+__device__ __forceinline__ void rest_rounds(const RopeParams& P, int hb, int h1, int abreast,
+                                            int sub, Use use) {
+#pragma unroll
+  for (int k = 0; k < kRestRounds; ++k) {
+    const int hh = hb + k * abreast + sub;
+    if (sub < abreast && hh < h1) {
+      const int r = rank_of_head(P, hh);
+      use(k, r, hh - r * P.heads);
+    }
+  }
+}
+
+// PHASE 0: asks for the first; 1: stores them and copies the others.
+template <int B, int PHASE>
+__device__ __forceinline__ void copy_rest(const RopeParams& P, int64_t tok, int h0, int h1,
+                                          Held& held) {
+  using Piece = Pack<SP_BF16, B / 2>;
   const int lane = threadIdx.x & 31;
   const int items = P.rest / B, width = items < 32 ? items : 32, abreast = 32 / width;
   const int my = lane % width, sub = lane / width;
-  for (int item = my; item < items; item += width) {
-    for (int hb = h0; hb < h1; hb += abreast * kRounds) {
-      Pack<SP_BF16, B / 2> p[kRounds];
+  const int64_t x_at = tok * P.x_row + P.rest_at, y_at = tok * P.y_row + P.rest_at;
+  auto load = [&](int item, int hb) {
+    rest_rounds<B>(P, hb, h1, abreast, sub, [&](int k, int r, int h) {
+      Piece p;
+      load_pack(p, P.x[r] + x_at + h * P.x_head + item * B);
 #pragma unroll
-      for (int k = 0; k < kRounds; ++k) {
-        const int hh = hb + k * abreast + sub;
-        if (sub < abreast && hh < h1) {
-          const int r = rank_of_head(P, hh);
-          load_pack(p[k], P.x[r] + tok * P.x_row + (hh - r * P.heads) * P.x_head + P.rest_at +
-                              item * B);
-        }
-      }
+      for (int i = 0; i < Piece::kWords; ++i) held[k].w[i] = p.w[i];
+    });
+  };
+  if constexpr (PHASE == 0) {
+    load(my, h0);
+  } else {
+    for (int item = my; item < items; item += width) {
+      for (int hb = h0; hb < h1; hb += abreast * kRestRounds) {
+        if (item != my || hb != h0) load(item, hb);
+        rest_rounds<B>(P, hb, h1, abreast, sub, [&](int k, int r, int h) {
+          Piece p;
 #pragma unroll
-      for (int k = 0; k < kRounds; ++k) {
-        const int hh = hb + k * abreast + sub;
-        if (sub < abreast && hh < h1) {
-          const int r = rank_of_head(P, hh);
-          store_pack(P.y[r] + tok * P.y_row + (hh - r * P.heads) * P.y_head + P.rest_at + item * B,
-                     p[k]);
-        }
+          for (int i = 0; i < Piece::kWords; ++i) p.w[i] = held[k].w[i];
+          store_pack(P.y[r] + y_at + h * P.y_head + item * B, p);
+        });
       }
     }
   }
+}
+template <int PHASE>
+__device__ __forceinline__ void copy_rest(const RopeParams& P, int64_t tok, int h0, int h1,
+                                          Held& held) {
+  if (P.rest == 0) return;
+  if (P.rest_bytes == 16) copy_rest<16, PHASE>(P, tok, h0, h1, held);
+  else if (P.rest_bytes == 8) copy_rest<8, PHASE>(P, tok, h0, h1, held);
+  else if (P.rest_bytes == 4) copy_rest<4, PHASE>(P, tok, h0, h1, held);
+  else copy_rest<2, PHASE>(P, tok, h0, h1, held);
 }
 
 // V elements a load.  Half layout: a lane's item is V pairs (V elements of
@@ -124,6 +153,8 @@ rope_kernel(const RopeParams P) {
     };
     // the first heads are on their way while the angles are computed
     fetch(h0, my);
+    Held held;
+    copy_rest<0>(P, tok, h0, h1, held);
     int64_t pos;
     if (P.positions != nullptr) {
       pos = __ldg(P.positions + tok);
@@ -189,13 +220,7 @@ rope_kernel(const RopeParams P) {
         }
       }
     }
-    // the part of the heads that is not rotated
-    if (P.rest > 0) {
-      if (P.rest_bytes == 16) copy_rest<16>(P, tok, h0, h1);
-      else if (P.rest_bytes == 8) copy_rest<8>(P, tok, h0, h1);
-      else if (P.rest_bytes == 4) copy_rest<4>(P, tok, h0, h1);
-      else copy_rest<2>(P, tok, h0, h1);
-    }
+    copy_rest<1>(P, tok, h0, h1, held);
   }
 }
 
