@@ -246,12 +246,15 @@ static const void* rope_fn(int layout, int vec) {
 
 cudaError_t launch_rope(RopeParams p, int dtype, int vec, cudaStream_t st) {
   // One warp a token, or few tokens' heads cut into pieces of whole lane rounds
-  // until every SM has its warps.
+  // until every SM has the warps that it holds at once.  (More pieces make a second
+  // wave: 4096 tokens of 9 heads of 128 7 us, cut until four times as many warps
+  // 14; 2 x 5997 tokens of 5 heads of 80 7.7 us, twice as many 10.4.)
   const int pairs = vec == 1 || p.layout == SP_ROPE_HALF ? vec : vec / 2;
   const int items = p.half / pairs;
   const int abreast = 32 / (items < 32 ? items : 32);
   const int rounds = (p.all_heads + abreast - 1) / abreast;
-  const int64_t want = static_cast<int64_t>(device_sm_count()) * 8 * kRopeWarps;
+  const int64_t want = static_cast<int64_t>(device_sm_count()) *
+                       rope_blocks(dtype, vec, p.layout) * kRopeWarps;
   int64_t chunks = p.tokens < want ? (want + p.tokens - 1) / p.tokens : 1;
   if (chunks > rounds) chunks = rounds;
   p.chunk_heads = static_cast<int>((rounds + chunks - 1) / chunks) * abreast;
