@@ -34,7 +34,8 @@ __device__ __forceinline__ void back_factors(const Shared& sh, int stage, uint32
     F2 e, d;
     nk[i] = neg_k<DT, true>(sh.template row<DT>(stage, 0, i), e);
     h = next_state<TIED>(nk[i], h, sh.template row<DT>(stage, 1, i), d);
-    dg[i] = mul2(mul2(mul2(nk[i], nk[i]), e), d);            // a k d, a = e k
+    // a k d, a = e k first: k k underflows from a gate of 44 on, a k from 87
+    dg[i] = mul2(mul2(mul2(nk[i], e), nk[i]), d);
     // a from e: 1 - k would lose a small one
     if (KIND != kPlainRun && i == i0) a0 = mul2(mul2(e, nk[i]), f2(-1.f, -1.f));
     dy[i] = sh.template raw<DT>(stage, 2, i);
