@@ -464,6 +464,8 @@ sp_status_t sp_rope_bwd(const void* const* dy, int64_t dy_ld, int64_t dy_head, i
  *   h[i] = a[i] h[i-1] + k[i] value[i]   (tied != 0)
  *   h[i] = a[i] h[i-1] + value[i]        (tied == 0)
  *   y[i] = h[i],  h[-1] = h0 of the sequence (0 without h0)
+ * a and k keep their relative digits down to 2^-126; beyond gates of +-87 the
+ * smaller of them is 2^-126 or 0.
  *
  * gate, value, y [t] (b, s, c)      c a multiple of 8, at most SP_MAX_HIDDEN
  * h0, hT         [t] (n, c) float32 or NULL arrays: the state before and after each

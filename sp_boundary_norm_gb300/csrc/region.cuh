@@ -194,15 +194,14 @@ __device__ __forceinline__ F2 rcp2(F2 v) {
 // reciprocal took half as long again for the whole recurrence: 4 x 65,536 tokens of
 // 256 float32 channels 244 us, so 168).  Float32 arguments are held where the
 // products are finite: 1 / (1 + exp(88.7)) is flushed to zero already, and
-// exp(-104) too.  CAP: below exp(87), 2^126, whose reciprocal is still normal.
-// SIGN: of exp(SIGN g).
+// exp(-104) too.  CAP (float32): exp(87) at most, whose reciprocal is still normal.
+// SIGN: of exp(SIGN g); the bounds are those of SIGN g.
 template <int DT, bool CAP, int SIGN = 1>
 __device__ __forceinline__ F2 exp2_of(F2 g) {
   const F2 log2e = f2(SIGN * 1.4426950408889634f, SIGN * 1.4426950408889634f);
   float2 x;
   F2 rest = f2(0.f, 0.f);
   if constexpr (DT == SP_F32) {
-    static_assert(SIGN == 1 || !CAP, "the bounds are those of exp(g)");
     if constexpr (SIGN < 0) g = mul2(g, f2(-1.f, -1.f));
     x = split(g);
     asm("max.NaN.f32 %0, %0, 0fC2D00000;" : "+f"(x.x));     // -104
@@ -221,11 +220,8 @@ __device__ __forceinline__ F2 exp2_of(F2 g) {
     rest = mul2(rest, f2(-0.69314718f, -0.69314718f));
     x = split(t);
   } else {
+    static_assert(!CAP, "16-bit arguments are held by their users");
     x = split(mul2(g, log2e));
-    if constexpr (CAP) {
-      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.x));   // 126
-      asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(x.y));
-    }
   }
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));

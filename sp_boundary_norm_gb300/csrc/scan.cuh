@@ -1,5 +1,5 @@
 // Shared parts of the gated recurrence's forward and backward:
-//   a = sigmoid(gate), k = 1 - a = sigmoid(-gate)
+//   a = sigmoid(gate), k = sigmoid(-gate) = 1 - a
 //   h[i] = a[i] h[i-1] + k[i] v[i]   (tied)   or   a[i] h[i-1] + v[i]   (free)
 // along the tokens of a sequence, each channel on its own.
 //
@@ -15,8 +15,8 @@
 //
 // Measured on a GB300, bf16 (the rate is of the bytes that have to move; the
 // measured copy rate is 6.8 TB/s): 8 ranks of 16,384 tokens x 1024 channels,
-// forward 147-151 us (5.4 TB/s), backward 232-236 (5.7); packed as 12 sequences
-// 177 and 267; 1 rank of 65,537 x 512 75 and 114, where the steps' joins are what
+// forward 158 us (5.1 TB/s), backward 240 (5.6); packed as 12 sequences
+// 181 and 275; 1 rank of 65,537 x 512 75 and 106, where the steps' joins are what
 // takes time: few channels cannot fill the SMs otherwise.
 //
 // Two exponentials' worth of special functions, a scan and a correction an
@@ -48,27 +48,52 @@ __device__ __forceinline__ Two<DT> pack2(F2 v) {
   return p;
 }
 
-// -k = -sigmoid(-g) = -1 / (1 + e), e = exp(g): small k keep their digits, and
-// h + k (v - h) and h - k h need no more.  An exponential that overflows (or
-// nearly: subnormal reciprocals are flushed) gives k = 0; CAP holds it below
-// that, for a = e k.  NaN stays NaN.
-template <int DT, bool CAP>
-__device__ __forceinline__ F2 neg_k(F2 g, F2& e) {
-  e = exp2_of<DT, CAP>(g);
-  return rcp2(fma2(e, f2(-1.f, -1.f), f2(-1.f, -1.f)));
+// Two gates held above -87, where exp(-g) and its reciprocal are normal numbers (16-bit
+// types: both at once; exp2_of does it for float32).  NaN stays NaN.
+template <int DT>
+__device__ __forceinline__ Two<DT> held_gate(Two<DT> g) {
+  if constexpr (DT == SP_BF16) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(g.w[0]) : "r"(0xC2AEC2AEu));
+  if constexpr (DT == SP_F16) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(g.w[0]) : "r"(0xD570D570u));
+  return g;
 }
 
-// The state after a token: h + k (v - h), or h - k h + v.  d: h - v (tied).
-template <bool TIED>
-__device__ __forceinline__ F2 next_state(F2 nk, F2 h, F2 v, F2& d) {
-  if constexpr (TIED) {
-    d = fma2(v, f2(-1.f, -1.f), h);
-    return fma2(nk, d, h);
-  } else {
-    d = h;
-    return add2(fma2(nk, h, h), v);
-  }
+// a = sigmoid(g) = 1 / (1 + e) from e = exp(-g), and k = e a: both keep their
+// relative digits however small they are.  (1 - k in place of a, as in h + k (v - h),
+// is off by 2^-24: all of a shut gate's a, which is what is left of a state that
+// gathered over thousands of tokens.)  Gates below -87 count as -87: a = 2^-126, and so
+// does k of gates above 87, which is flushed to 0.
+template <int DT>
+__device__ __forceinline__ F2 open_gate(Two<DT> g, F2& e) {
+  e = exp2_of<DT, DT == SP_F32, -1>(unpack2<DT>(held_gate<DT>(g)));
+  return rcp2(add2(e, f2(1.f, 1.f)));
 }
+
+// The state after a token: a h + k v, or a h + v.
+template <bool TIED>
+__device__ __forceinline__ F2 next_state(F2 a, F2 k, F2 h, F2 v) {
+  return fma2(a, h, TIED ? mul2(k, v) : v);
+}
+
+// The product of the a of a run, and 1 - that product, a sum of k a...a.  An open gate's
+// a, next to 1, is off by up to 2^-23, and products of such numbers round to one side:
+// over a memory of 1/k tokens that adds up (65,537 tokens with k around 1e-5: 2e-5 of
+// the state, against 8e-7).  So what passes from run to run is 1 - lost while that is at
+// least 1/2; the product, which has the digits of shut gates, otherwise and in the run.
+struct RunFactor {
+  F2 a = f2(1.f, 1.f), lost = f2(0.f, 0.f);
+  __device__ __forceinline__ void next(F2 ai, F2 ki) {
+    lost = fma2(a, ki, lost);
+    a = mul2(a, ai);
+  }
+  __device__ __forceinline__ void cut() {
+    a = f2(0.f, 0.f);
+    lost = f2(1.f, 1.f);
+  }
+  __device__ __forceinline__ F2 whole() const {
+    const float2 x = split(a), y = split(lost);
+    return f2(y.x <= 0.5f ? 1.f - y.x : x.x, y.y <= 0.5f ? 1.f - y.y : x.y);
+  }
+};
 
 // The affine maps of a thread's two channels over some tokens: x -> a x + h.
 struct alignas(16) Map2 {

@@ -8,7 +8,7 @@
 // each run, in float32: that reads a quarter byte an element instead of the
 // two of the rounded output, and the difference h - v keeps its digits.  Bound by
 // HBM for many channels, 84 % of the measured copy rate (scan.cuh has the
-// figures); three blocks an SM, because a run's 48 factors stay in registers
+// figures); three blocks an SM, because a run's 40 factors stay in registers
 // between the two directions.
 #include "scan.cuh"
 
@@ -18,52 +18,40 @@ namespace spb {
 // channels: three 235 us, two 262, four, with spilled registers, 377).
 constexpr int kBwdBlocks = 3;
 
-// The run's factors, from its rows in shared memory: nk = -k, and dg = dgate
-// without its factor dh.  i0, h0: the first token that begins a sequence and the
-// state before it, a0 its a; begin(i): the state before any other.
+// The run's factors, from its rows in shared memory: e = exp(-gate), from which the
+// way back takes a and k again (both kept would cost 32 registers more), and
+// dg = a k (h[i-1] - v[i]) or a k h[i-1], dgate without its factor dh.  i0, h0: the
+// first token that begins a sequence and the state before it; begin(i): that before any
+// other.  Returns q leaving the run's first token as a map of the q entering its last
+// one, gathered on the way: with A[i] the product of a[0 .. i],
+//   q leaving = sum over i of A[i] dy[i] + A[15] q entering,
+// up to the first token i1 that ends a sequence, which q1 enters.
 template <int DT, bool TIED, int KIND, typename Shared, typename Begin>
-__device__ __forceinline__ void back_factors(const Shared& sh, int stage, uint32_t starts,
-                                             int i0, F2 h0, F2 h,
-                                             F2 (&nk)[kScanRun], F2 (&dg)[kScanRun],
-                                             Two<DT> (&dy)[kScanRun], F2& a0,
-                                             Begin begin) {
+__device__ __forceinline__ Map2 back_factors(const Shared& sh, int stage, uint32_t starts,
+                                             int i0, F2 h0, int i1, F2 q1, F2 h,
+                                             F2 (&e)[kScanRun], F2 (&dg)[kScanRun],
+                                             Two<DT> (&dy)[kScanRun], Begin begin) {
+  F2 q = f2(0.f, 0.f);
+  RunFactor fac;
 #pragma unroll
   for (int i = 0; i < kScanRun; ++i) {
     if (KIND == kSingleRun && i == i0) h = h0;
-    if (KIND == kAnyRun && ((starts >> i) & 1u)) h = begin(i);
-    F2 e, d;
-    nk[i] = neg_k<DT, true>(sh.template row<DT>(stage, 0, i), e);
-    h = next_state<TIED>(nk[i], h, sh.template row<DT>(stage, 1, i), d);
-    // a k d, a = e k first: k k underflows from a gate of 44 on, a k from 87
-    dg[i] = mul2(mul2(mul2(nk[i], e), nk[i]), d);
-    // a from e: 1 - k would lose a small one
-    if (KIND != kPlainRun && i == i0) a0 = mul2(mul2(e, nk[i]), f2(-1.f, -1.f));
+    if (KIND == kAnyRun && ((starts >> i) & 1u)) h = i == i0 ? h0 : begin(i);
+    const F2 a = open_gate<DT>(sh.template raw<DT>(stage, 0, i), e[i]), k = mul2(e[i], a);
+    const F2 v = sh.template row<DT>(stage, 1, i);
+    // a k first: k k, or d times either, may underflow where the product does not
+    dg[i] = mul2(mul2(k, a), TIED ? fma2(v, f2(-1.f, -1.f), h) : h);
+    h = next_state<TIED>(a, k, h, v);
     dy[i] = sh.template raw<DT>(stage, 2, i);
-  }
-}
-
-// q leaving the run's first token as a map of the q entering its last one.
-// i1, q1: the last token that ends a sequence and the q entering it; end(i): the
-// q entering any other.
-template <int DT, int KIND, typename End>
-__device__ __forceinline__ Map2 back_map(uint32_t ends, int i1, F2 q1, const F2 (&nk)[kScanRun],
-                                         const Two<DT> (&dy)[kScanRun], End end) {
-  F2 q = f2(0.f, 0.f), fac = f2(1.f, 1.f);
-#pragma unroll
-  for (int i = kScanRun - 1; i >= 0; --i) {
-    if (KIND == kSingleRun && i == i1) {
-      q = q1;
-      fac = f2(0.f, 0.f);
+    // (i1 = -1: no end)
+    if (KIND == kPlainRun || static_cast<uint32_t>(i) <= static_cast<uint32_t>(i1)) {
+      fac.next(a, k);
+      q = fma2(fac.a, unpack2<DT>(dy[i]), q);
+      if (KIND != kPlainRun && i == i1) q = fma2(fac.a, q1, q);
     }
-    if (KIND == kAnyRun && ((ends >> i) & 1u)) {
-      q = end(i);
-      fac = f2(0.f, 0.f);
-    }
-    const F2 x = add2(unpack2<DT>(dy[i]), q);
-    q = fma2(nk[i], x, x);                                   // a x
-    fac = fma2(nk[i], fac, fac);
   }
-  return Map2{fac, q};
+  if (KIND != kPlainRun && i1 >= 0) fac.cut();
+  return Map2{fac.whole(), q};
 }
 
 template <int DT, bool TIED, bool PACKED, bool WIDE>
@@ -125,82 +113,63 @@ scan_bwd_kernel(const ScanParams P) {
     auto seq = [&](int i) { return seq_of_run<PACKED>(win, sh.first, marks.starts, bi, i); };
     auto begin = [&](int i) { return load_state(P.h0[r], seq(i), P.c, ch, on); };
     auto end = [&](int i) { return load_state(P.dhT[r], seq(i), P.c, ch, on); };
-    // (the first beginning's state and the last end's gradient are asked for
+    // (the first beginning's state and the first end's gradient are asked for
     // beneath the wait for the rows)
-    const int i0 = __ffs(marks.starts) - 1, i1 = 31 - __clz(marks.ends);
+    const int i0 = __ffs(marks.starts) - 1, i1 = __ffs(marks.ends) - 1;
     F2 h0 = f2(0.f, 0.f), q1 = h0;
     if (i0 >= 0) h0 = begin(i0);
     if (i1 >= 0) q1 = end(i1);
     Two<DT> dy[kScanRun];
-    F2 nk[kScanRun], dg[kScanRun], a0 = f2(0.f, 0.f);
+    F2 e[kScanRun], dg[kScanRun];
     sh.wait();
     const int stage = step % kStages;
     const F2 h = f2(entering.x, entering.y);
+    Map2 mine;
     if (kind == kPlainRun)
-      back_factors<DT, TIED, kPlainRun>(sh, stage, 0u, 0, h0, h, nk, dg, dy, a0, begin);
+      mine = back_factors<DT, TIED, kPlainRun>(sh, stage, 0u, 0, h0, 0, q1, h, e, dg, dy, begin);
     else if (kind == kSingleRun)
-      back_factors<DT, TIED, kSingleRun>(sh, stage, 0u, i0, h0, h, nk, dg, dy, a0, begin);
+      mine = back_factors<DT, TIED, kSingleRun>(sh, stage, 0u, i0, h0, i1, q1, h, e, dg, dy, begin);
     else
-      back_factors<DT, TIED, kAnyRun>(sh, stage, marks.starts, i0, h0, h, nk, dg, dy, a0, begin);
+      mine = back_factors<DT, TIED, kAnyRun>(sh, stage, marks.starts, i0, h0, i1, q1, h, e, dg, dy,
+                                             begin);
     __syncwarp();                     // every lane has read the rows
     fetch(stage, tok0 - kStages * stretch);
     fetch_entering(tok0 - stretch);
-    Map2 mine;
-    if (kind == kPlainRun) mine = back_map<DT, kPlainRun>(0u, 0, q1, nk, dy, end);
-    else if (kind == kSingleRun) mine = back_map<DT, kSingleRun>(0u, i1, q1, nk, dy, end);
-    else mine = back_map<DT, kAnyRun>(marks.ends, 0, q1, nk, dy, end);
     F2 into = join_runs<PACKED, -1>(sh.join, step, mine, C, rank, warp, nw, carry, alive);
     if (tok0 >= P.s) continue;
     char* at_g = dgate + tok0 * P.ld_out;
     char* at_v = dvalue + tok0 * P.ld_dvalue;
-    const F2 minus = f2(-1.f, -1.f);
-    auto put = [&](int i, F2 dh) {
+    // token i's gradients from the q entering it; leaves the q before it
+    auto back = [&](int i, bool there) {
+      const F2 a = rcp2(add2(e[i], f2(1.f, 1.f)));
+      const F2 dh = add2(unpack2<DT>(dy[i]), into);
+      into = mul2(a, dh);
+      if (!there) return;
       store_pack(at_g + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(mul2(dh, dg[i])));
       store_pack(at_v + static_cast<uint64_t>(P.ld_dvalue) * i,
-                 pack2<DT>(TIED ? mul2(mul2(dh, minus), nk[i]) : dh));
+                 pack2<DT>(TIED ? mul2(mul2(e[i], a), dh) : dh));
     };
     if (kind == kPlainRun) {
       if (on) {
 #pragma unroll
-        for (int i = kScanRun - 1; i >= 0; --i) {
-          const F2 dh = add2(unpack2<DT>(dy[i]), into);
-          into = fma2(nk[i], dh, dh);
-          put(i, dh);
-        }
+        for (int i = kScanRun - 1; i >= 0; --i) back(i, true);
       }
     } else if (kind == kSingleRun) {
       F2 first = f2(0.f, 0.f);
 #pragma unroll
       for (int i = kScanRun - 1; i >= 0; --i) {
         if (i == i1) into = q1;
-        const F2 dh = add2(unpack2<DT>(dy[i]), into);
-        into = fma2(nk[i], dh, dh);
-        if (i == i0) first = dh;
-        if (on) put(i, dh);
+        back(i, on);
+        if (i == i0) first = into;
       }
-      if (i0 >= 0) store_state(P.hT[r], seq(i0), P.c, ch, on, mul2(a0, first));
+      if (i0 >= 0) store_state(P.hT[r], seq(i0), P.c, ch, on, first);
     } else {
       const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
 #pragma unroll
       for (int i = kScanRun - 1; i >= 0; --i) {
-        if ((marks.ends >> i) & 1u) into = end(i);
-        const F2 dh = add2(unpack2<DT>(dy[i]), into);
-        into = fma2(nk[i], dh, dh);
-        if ((marks.starts >> i) & 1u)
-          store_state(P.hT[r], seq(i), P.c, ch, on, i == i0 ? mul2(a0, dh) : dh);
-        if (on && i < rows) put(i, dh);
-      }
-      if (P.hT[r] != nullptr && on) {
-        // further beginnings in the run: dh0 = a dh with a from the gate again
-        for (uint32_t left = marks.starts & (marks.starts - 1u); left != 0; left &= left - 1) {
-          const int i = __ffs(left) - 1, j = seq(i);
-          Two<DT> graw;
-          load_pack(graw, P.gate[r] + (row0 + tok0 + i) * P.ld_gate + col);
-          F2 e;
-          const F2 a = mul2(neg_k<DT, true>(unpack2<DT>(graw), e), e);
-          store_state(P.hT[r], j, P.c, ch, on,
-                      mul2(mul2(a, minus), load_state(P.hT[r], j, P.c, ch, on)));
-        }
+        if ((marks.ends >> i) & 1u) into = i == i1 ? q1 : end(i);
+        back(i, on && i < rows);
+        if ((marks.starts >> i) & 1u) store_state(P.hT[r], seq(i), P.c, ch, on, into);
       }
     }
   }

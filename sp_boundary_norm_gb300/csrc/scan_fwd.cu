@@ -7,11 +7,10 @@
 
 namespace spb {
 
-// Blocks an SM that the registers are held to; for packed batches, whose marks take
-// registers, one less (16,384 tokens x 8 ranks of 1024 channels: 151 us with four
-// blocks, 155 with three; as 12 packed sequences 177 with three, 318 with four and
-// spilled registers).
-constexpr int kFwdBlocks = 4;
+// Blocks an SM that the registers are held to (16,384 tokens x 8 ranks of 1024 channels:
+// 158 us with three, 169 with four, which spill a few registers; 16 rows of 512 tokens
+// 65 and 69; 12 packed sequences, whose marks take registers, 181 with three).
+constexpr int kFwdBlocks = 3;
 
 // One run: h[i], f[i] with h[i] + f[i] * (state entering the run) the state
 // after token i.  i0, h0: the first token that begins a sequence and the state
@@ -20,30 +19,31 @@ template <int DT, bool TIED, int KIND, typename Shared, typename Begin>
 __device__ __forceinline__ Map2 scan_run(const Shared& sh, int stage, uint32_t starts, int i0,
                                          F2 h0, F2 (&h)[kScanRun], F2 (&f)[kScanRun],
                                          Begin begin) {
-  F2 cur = f2(0.f, 0.f), fac = f2(1.f, 1.f);
+  F2 cur = f2(0.f, 0.f);
+  RunFactor fac;
 #pragma unroll
   for (int i = 0; i < kScanRun; ++i) {
     if (KIND == kSingleRun && i == i0) {
       cur = h0;
-      fac = f2(0.f, 0.f);
+      fac.cut();
     }
     if (KIND == kAnyRun && ((starts >> i) & 1u)) {
       cur = begin(i);
-      fac = f2(0.f, 0.f);
+      fac.cut();
     }
-    F2 e, d;
-    const F2 nk = neg_k<DT, false>(sh.template row<DT>(stage, 0, i), e);
-    cur = next_state<TIED>(nk, cur, sh.template row<DT>(stage, 1, i), d);
-    fac = fma2(nk, fac, fac);
+    F2 e;
+    const F2 a = open_gate<DT>(sh.template raw<DT>(stage, 0, i), e), k = mul2(e, a);
+    cur = next_state<TIED>(a, k, cur, sh.template row<DT>(stage, 1, i));
+    fac.next(a, k);
     h[i] = cur;
-    f[i] = fac;
+    f[i] = fac.a;
   }
-  return Map2{fac, cur};
+  return Map2{fac.whole(), cur};
 }
 
 template <int DT, bool TIED, bool PACKED, bool WIDE>
 __global__ void __launch_bounds__(32 * (WIDE ? kScanWideWarps : kScanWarps),
-                                  WIDE ? 1 : PACKED ? kFwdBlocks - 1 : kFwdBlocks)
+                                  WIDE ? 1 : kFwdBlocks)
 scan_fwd_kernel(const ScanParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ __align__(16) char smem[];
@@ -161,17 +161,22 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams P) {
     load_pack(vraw, P.value[r] + bi * P.ld_value + static_cast<int64_t>(ch) * E);
     if (P.h0[r] != nullptr)
       load_pack(h, reinterpret_cast<const char*>(P.h0[r] + bi * P.c + ch));
-    float g[8], v[8], x[8];
-    unpack(graw, g);
+    float v[8], x[8];
     unpack(vraw, v);
     unpack(h, x);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      F2 e, d;
-      const F2 nk = neg_k<DT, false>(f2(g[i], g[i + 1]), e);
+      F2 e;
+      Two<DT> g;
+#pragma unroll
+      for (int w = 0; w < Two<DT>::kWords; ++w) g.w[w] = graw.w[i / 2 * Two<DT>::kWords + w];
+      F2 a = open_gate<DT>(g, e);
+      const F2 k = mul2(e, a), minus = f2(-1.f, -1.f);
+      // a without the reciprocal's error, a + a (1 - a - k): a kept state takes many steps
+      a = fma2(a, fma2(k, minus, fma2(a, minus, f2(1.f, 1.f))), a);
       const F2 old = f2(x[i], x[i + 1]), val = f2(v[i], v[i + 1]);
-      const float2 y = split(P.tied ? next_state<true>(nk, old, val, d)
-                                    : next_state<false>(nk, old, val, d));
+      const float2 y = split(P.tied ? next_state<true>(a, k, old, val)
+                                    : next_state<false>(a, k, old, val));
       x[i] = y.x;
       x[i + 1] = y.y;
     }

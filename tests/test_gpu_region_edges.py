@@ -72,3 +72,158 @@ def test_scan_gradient_of_saturated_gates(dtype, tied):
     want = sigmoid(g) * sigmoid(-g)
     # a and k each once, two products, the difference h0 - v is exact
     within(dgate, want, want * (delta(g, dtype) + 2 * RHO + 3 * U), "dgate")
+
+
+def spans_of(b, s, cu):
+    """(batch row, first token, behind the last, sequence)."""
+    if cu is None:
+        return [(i, 0, s, i) for i in range(b)]
+    return [(0, lo, hi, j) for j, (lo, hi) in enumerate(zip(cu[:-1], cu[1:]))]
+
+
+def scan_exact(g, v, h0, tied, cu, dtype, dy, dhT):
+    """The recurrence and its gradients in float64, and beside each a bound on what
+    float32 arithmetic may lose of it, carried from token to token like the value.
+
+    A state passes a token as a product with a (k DELTA + RHO), rounded once there and,
+    in what carries it from run to run and block to block, less than twice more; k v
+    adds its own a DELTA + RHO and four roundings; a value is put together from its run's
+    entry and its place in at most 8.  The gradients' way back is the same with dy, one
+    sum more.  Terms of second order: a hundredth at 65,537 tokens."""
+    b, s, c = g.shape
+    a, k, d = sigmoid(g), sigmoid(-g), delta(g, dtype)
+    ra, rk = k * d + RHO, a * d + RHO + U
+    o = {n: np.zeros_like(g) for n in ("y", "dgate", "dvalue", "y_", "dgate_", "dvalue_")}
+    hT, hT_, dh0, dh0_ = h0.copy(), np.zeros_like(h0), dhT.copy(), np.zeros_like(h0)
+    for i, lo, hi, j in spans_of(b, s, cu):
+        h, m, e = h0[j], np.abs(h0[j]), np.zeros(c)
+        state = [(h, m, e)]
+        for p in range(lo, hi):
+            ai, ki = a[i, p], k[i, p] if tied else 1.0
+            w, x = ki * v[i, p], np.abs(ki * v[i, p])
+            h, e = ai * h + w, ai * (e + (ra[i, p] + 3 * U) * m) + (x * (rk[i, p] + 3 * U) if tied else 0)
+            m = ai * m + x
+            o["y"][i, p], o["y_"][i, p] = h, e + 8 * U * m
+            state.append((h, m, e + 8 * U * m))
+        if hi > lo:
+            hT[j], hT_[j] = h, e + 8 * U * m
+        q, m, e = dhT[j], np.abs(dhT[j]), np.zeros(c)
+        for p in reversed(range(lo, hi)):
+            ai, ki = a[i, p], k[i, p]
+            dh, dm = dy[i, p] + q, np.abs(dy[i, p]) + m
+            de = e + 8 * U * dm
+            prev, pm, pe = state[p - lo]
+            diff, fm = (prev - v[i, p], pm + np.abs(v[i, p])) if tied else (prev, pm)
+            o["dgate"][i, p] = dh * ai * ki * diff
+            o["dgate_"][i, p] = ai * ki * (de * fm + dm * (pe + U * fm)
+                                           + dm * fm * (ra[i, p] + rk[i, p] + 3 * U))
+            o["dvalue"][i, p] = dh * ki if tied else dh
+            o["dvalue_"][i, p] = ki * (de + dm * (rk[i, p] + U)) if tied else de
+            q, e, m = ai * dh, ai * (e + (ra[i, p] + 4 * U) * dm), ai * dm
+        dh0[j], dh0_[j] = q, e + 8 * U * m
+    o.update(hT=hT, hT_=hT_, dh0=dh0, dh0_=dh0_)
+    # products of many shut gates leave the range of normal numbers: not counted
+    return {n: 1.01 * x + 2.0 ** -100 if n.endswith("_") else x for n, x in o.items()}
+
+
+def run_scan(gate, value, dy, h0, dhT, tied, cu):
+    """Forward and backward of lists of rank buffers; every output."""
+    t, like = len(gate), gate[0]
+    y, dgate, dvalue = (empties(like, t) for _ in range(3))
+    hT, dh0 = empties(h0[0], t), empties(h0[0], t)
+    st = [torch.empty(sp.sp_gated_scan_states_shape(*like.shape), device=DEV) for _ in range(t)]
+    how = dict(h0=h0, tied=tied, cu_seqlens=cu)
+    sp.sp_gated_scan_fwd(gate, value, y=y, hT=hT, states=st, **how)
+    sp.sp_gated_scan_bwd(gate, value, st, dy, dhT=dhT, dgate=dgate, dvalue=dvalue, dh0=dh0, **how)
+    return dict(y=y, hT=hT, dgate=dgate, dvalue=dvalue, dh0=dh0)
+
+
+def offsets(lens):
+    cu = np.concatenate(([0], np.cumsum(lens)))
+    return cu, torch.tensor(cu, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("t,b,s,c,dtype,lens", [
+    (1, 1, 1, 8, F32, None), (3, 64, 1, 72, BF, None), (2, 7, 1, 64, F32, None), (2, 9, 1, 64, FP, None),
+    (2, 2, 17, 64, F32, None), (1, 3, 300, 72, FP, None), (1, 1, 700, 136, F32, None),
+    (8, 1, 3000, 64, BF, None), (1, 1, 20001, 8, F32, None), (4, 1, 9000, 72, BF, None),
+    (1, 1, 0, 72, F32, [5, 600, 0, 2, 1000, 31, 33]), (2, 1, 0, 64, BF, [1] * 40 + [0, 17, 3000]),
+    (1, 1, 0, 520, FP, [4000, 1, 1500])])
+@pytest.mark.parametrize("tied", [True, False])
+def test_scan_keeps_the_digits_of_shut_gates(t, b, s, c, dtype, lens, tied):
+    """Gates of -3 to -20 between open ones, after states of 1e4, and gradients that come
+    from the last tokens only: every element within its own rounding errors."""
+    cu_np, cu = (None, None) if lens is None else offsets(lens)
+    s = s if lens is None else sum(lens)
+    n = b if lens is None else len(lens)
+    gen = torch.Generator().manual_seed(s + c)
+    rnd = lambda *shape: torch.randn(shape, generator=gen)
+    gate, value, dy = [], [], []
+    for _ in range(t):
+        shut = torch.rand((b, s, c), generator=gen) < 0.15
+        gate.append(torch.where(shut, -3 - 17 * torch.rand((b, s, c), generator=gen),
+                                4 + 2 * rnd(b, s, c)).to(dtype).to(DEV))
+        value.append((rnd(b, s, c) * torch.exp(rnd(b, s, c))).to(dtype).to(DEV))
+        late = torch.zeros(b, s, c)
+        for i, lo, hi, _ in spans_of(b, s, cu_np):
+            late[i, max(lo, hi - 3):hi] = 1
+        late[..., ::2] = 1                       # every other channel: gradients everywhere
+        dy.append((rnd(b, s, c) * late).to(dtype).to(DEV))
+    h0 = [(1e4 * rnd(n, c)).to(DEV) for _ in range(t)]
+    dhT = [rnd(n, c).to(DEV) for _ in range(t)]
+    o = run_scan(gate, value, dy, h0, dhT, tied, cu)
+    for r in range(t):
+        w = scan_exact(f64(gate[r]), f64(value[r]), f64(h0[r]), tied, cu_np, dtype, f64(dy[r]),
+                       f64(dhT[r]))
+        for name, got in o.items():
+            within(got[r], w[name], w[name + "_"], f"{name}[{r}]")
+
+
+def scan_plain(g, v, h0, cu):
+    """y of the tied recurrence token by token in 32 bits: a = sigmoid(g), a h + k v."""
+    one = np.float32(1)
+    a = one / (one + np.exp(-g.astype(np.float64)).astype(np.float32))
+    kv = one / (one + np.exp(g.astype(np.float64)).astype(np.float32)) * v
+    y = np.zeros_like(g)
+    for i, lo, hi, j in spans_of(1, g.shape[1], cu):
+        h = h0[j]
+        for p in range(lo, hi):
+            h = a[i, p] * h + kv[i, p]
+            y[i, p] = h
+    return y
+
+
+@pytest.mark.parametrize("dtype,lens", [(F32, None), (BF, None), (F32, [40000, 25537])])
+def test_scan_keeps_the_digits_of_open_gates(dtype, lens):
+    """Memories of hundreds to 1e5 tokens over 65,537 of them: within the bound, and
+    (float32) no further from the exact values than the same formula token by token."""
+    cu_np, cu = (None, None) if lens is None else offsets(lens)
+    n = 1 if lens is None else 2
+    gen = torch.Generator().manual_seed(65)
+    rnd = lambda *shape: torch.randn(shape, generator=gen)
+    gate = (torch.linspace(6, 12, 16) + rnd(1, 65537, 16)).to(dtype).to(DEV)
+    value, dy = rnd(1, 65537, 16).to(dtype).to(DEV), rnd(1, 65537, 16).to(dtype).to(DEV)
+    h0, dhT = rnd(n, 16).to(DEV), rnd(n, 16).to(DEV)
+    o = run_scan([gate], [value], [dy], [h0], [dhT], True, cu)
+    w = scan_exact(f64(gate), f64(value), f64(h0), True, cu_np, dtype, f64(dy), f64(dhT))
+    for name, got in o.items():
+        within(got[0], w[name], w[name + "_"], name)
+    if dtype is F32:
+        plain = scan_plain(*(x.cpu().numpy() for x in (gate, value, h0)), cu_np)
+        off = lambda y: np.abs(y - w["y"]).max((0, 1))
+        mine, its = off(f64(o["y"][0])), off(plain)
+        print("off, of the state:", (mine / np.abs(w["y"]).max((0, 1))).max(),
+              "token by token:", (its / np.abs(w["y"]).max((0, 1))).max())
+        assert mine.max() <= its.max()
+
+
+@pytest.mark.parametrize("s", [1, 12])
+@pytest.mark.parametrize("tied", [True, False])
+def test_scan_infinite_states_stay_infinite(s, tied):
+    """a h + k v of an infinite h is infinite (a > 0), as the definition has it."""
+    gate = torch.linspace(-3, 6, 2 * s * 64).view(2, s, 64).to(DEV)
+    value, h0 = torch.randn_like(gate), torch.full((2, 64), float("inf"), device=DEV)
+    h0[1] = -h0[1]
+    y, hT = empties(gate, 1), empties(h0, 1)
+    sp.sp_gated_scan_fwd([gate], [value], h0=[h0], tied=tied, y=y, hT=hT)
+    assert torch.equal(y[0], h0[:, None].expand(2, s, 64)) and torch.equal(hT[0], h0)
