@@ -100,15 +100,33 @@ struct alignas(16) Map2 {
   F2 a, h;
 };
 
-// The map's value at x.  CUT: a sequence that begins inside the map's tokens
-// cuts off what comes before them: the factor is exactly zero, and what x holds
-// (an infinity, a NaN) must not pass.
+// The map's value at x.  CUT (packed batches): a sequence that begins inside the map's
+// tokens cuts off what comes before them, and what x holds (an infinity, a NaN) must
+// not pass.  A factor of zero says so, and nothing else does: a product of a's that
+// underflows inside a sequence counts as 2^-149, so that what is not finite there stays.
 template <bool CUT>
 __device__ __forceinline__ F2 through(F2 a, F2 h, F2 x) {
   const F2 y = fma2(a, x, h);
   if constexpr (!CUT) return y;
   const float2 f = split(a), g = split(h), w = split(y);
   return f2(f.x == 0.f ? g.x : w.x, f.y == 0.f ? g.y : w.y);
+}
+
+constexpr float kLeast = 0x1p-149f;
+__device__ __forceinline__ float at_least(float v, float least) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(least));
+  return v;
+}
+// The factor of a run's map: zero only for a cut.
+__device__ __forceinline__ F2 uncut(F2 a) {
+  const float2 v = split(a);
+  return f2(at_least(v.x, kLeast), at_least(v.y, kLeast));
+}
+// The factor of map a after map b: zero only if either's is, and if a's is, whatever b's.
+__device__ __forceinline__ F2 uncut_product(F2 a, F2 b) {
+  const float2 v = split(a), w = split(b), p = split(mul2(a, b));
+  return f2(v.x == 0.f ? 0.f : at_least(p.x, fminf(w.x, kLeast)),
+            v.y == 0.f ? 0.f : at_least(p.y, fminf(w.y, kLeast)));
 }
 
 // Map m into the cluster address `to`, counted in bytes on the mbarrier `bar`
@@ -228,7 +246,8 @@ __device__ __forceinline__ void pass_empty(const ScanParams& P, const float* src
 
 // Joins the runs' maps in token order (TIME = +1) or against it (-1): from the
 // value that enters the cluster's stretch (`carry`, which moves behind the
-// stretch) the value that enters this thread's run, whose map is `mine`.
+// stretch) the value that enters this thread's run, whose map is `mine`; `cut`: a
+// sequence begins (ends) in the run.
 //
 // The maps of a block meet in `run`; a warp folds those before its own, and the
 // last one's fold, the block's map, goes to every block of the cluster by
@@ -268,7 +287,7 @@ __device__ __forceinline__ F2 fold_value(const Map2* at, int step, int n, int pl
 template <bool CUT>
 __device__ __forceinline__ void fold_map(Map2& acc, const Map2& m) {
   acc.h = through<CUT>(m.a, m.h, acc.h);
-  acc.a = through<CUT>(m.a, f2(0.f, 0.f), acc.a);
+  acc.a = CUT ? uncut_product(m.a, acc.a) : mul2(m.a, acc.a);
 }
 template <bool CUT>
 __device__ __forceinline__ Map2 fold_maps(const Map2* at, int step, int n) {
@@ -286,8 +305,10 @@ __device__ __forceinline__ Map2 fold_maps(const Map2* at, int step, int n) {
 }
 
 template <bool CUT, int TIME>
-__device__ __forceinline__ F2 join_runs(const JoinBuffers& sh, int step, const Map2& mine, int C,
-                                        int rank, int warp, int nw, F2& carry, bool& alive) {
+__device__ __forceinline__ F2 join_runs(const JoinBuffers& sh, int step, Map2 mine, bool cut,
+                                        int C, int rank, int warp, int nw, F2& carry,
+                                        bool& alive) {
+  if (CUT && !cut) mine.a = uncut(mine.a);
   const int lane = threadIdx.x & 31;
   const int par = step & 1;
   Map2* run = sh.run + par * nw * 32 + lane;

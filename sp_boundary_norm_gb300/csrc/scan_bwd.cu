@@ -135,7 +135,8 @@ scan_bwd_kernel(const ScanParams P) {
     __syncwarp();                     // every lane has read the rows
     fetch(stage, tok0 - kStages * stretch);
     fetch_entering(tok0 - stretch);
-    F2 into = join_runs<PACKED, -1>(sh.join, step, mine, C, rank, warp, nw, carry, alive);
+    F2 into = join_runs<PACKED, -1>(sh.join, step, mine, marks.ends != 0u, C, rank, warp, nw, carry,
+                                    alive);
     if (tok0 >= P.s) continue;
     char* at_g = dgate + tok0 * P.ld_out;
     char* at_v = dvalue + tok0 * P.ld_dvalue;

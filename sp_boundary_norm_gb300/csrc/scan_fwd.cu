@@ -105,7 +105,8 @@ scan_fwd_kernel(const ScanParams P) {
       mine = scan_run<DT, TIED, kAnyRun>(sh, stage, marks.starts, 0, h0, h, f, begin);
     __syncwarp();                     // every lane has read the rows
     fetch(stage, tok0 + kStages * stretch);
-    const F2 entry = join_runs<PACKED, 1>(sh.join, step, mine, C, rank, warp, nw, carry, alive);
+    const F2 entry = join_runs<PACKED, 1>(sh.join, step, mine, marks.starts != 0u, C, rank, warp, nw,
+                                          carry, alive);
     if (tok0 >= P.s) continue;
     if (states != nullptr && on)
       __stcs(reinterpret_cast<float2*>(states + (tok0 / kScanRun) * P.c), split(entry));
@@ -120,7 +121,9 @@ scan_fwd_kernel(const ScanParams P) {
       F2 last = f2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < kScanRun; ++i) {
-        const F2 y = through<PACKED>(f[i], h[i], entry);
+        // (from its beginning on a packed sequence has all of its state in h)
+        const bool own = PACKED && static_cast<uint32_t>(i) >= static_cast<uint32_t>(i0);
+        const F2 y = own ? h[i] : fma2(f[i], entry, h[i]);
         if (i == i1) last = y;
         if (on) store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(y));
       }
@@ -129,7 +132,8 @@ scan_fwd_kernel(const ScanParams P) {
       const int rows = P.s - tok0 < kScanRun ? static_cast<int>(P.s - tok0) : kScanRun;
 #pragma unroll
       for (int i = 0; i < kScanRun; ++i) {
-        const F2 y = through<PACKED>(f[i], h[i], entry);
+        const bool own = PACKED && (marks.starts & ((2u << i) - 1u)) != 0u;
+        const F2 y = own ? h[i] : fma2(f[i], entry, h[i]);
         if ((marks.ends >> i) & 1u) store_state(P.hT[r], seq(i), P.c, ch, on, y);
         if (on && i < rows) store_pack(at + static_cast<uint64_t>(P.ld_out) * i, pack2<DT>(y));
       }

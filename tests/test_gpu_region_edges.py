@@ -227,3 +227,57 @@ def test_scan_infinite_states_stay_infinite(s, tied):
     y, hT = empties(gate, 1), empties(h0, 1)
     sp.sp_gated_scan_fwd([gate], [value], h0=[h0], tied=tied, y=y, hT=hT)
     assert torch.equal(y[0], h0[:, None].expand(2, s, 64)) and torch.equal(hT[0], h0)
+
+
+@pytest.mark.parametrize("t,c", [(1, 64), (8, 512)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scan_packed_sequences_keep_what_is_not_finite(t, c, dtype):
+    """One NaN in a sequence of 4000 tokens, where products of a underflow after some 150:
+    every later y and hT of the sequence is NaN, every earlier gradient for a NaN in dy, as
+    in a dense call of that sequence; nothing else changes."""
+    cu_np, cu = offsets([700, 4000, 0, 300])
+    lo, hi, s = 700, 4700, 5000
+    gen = torch.Generator().manual_seed(5)
+    rnd = lambda *shape: torch.randn(shape, generator=gen)
+    mk = lambda *shape, d=dtype: [rnd(*shape).to(d).to(DEV) for _ in range(t)]
+    gate, value, dy = mk(1, s, c), mk(1, s, c), mk(1, s, c)
+    h0, dhT = mk(4, c, d=F32), mk(4, c, d=F32)
+    nan = lambda x: torch.isnan(x).all()
+    clean = run_scan(gate, value, dy, h0, dhT, True, cu)
+    part = lambda xs: [x[:, lo:hi].contiguous() for x in xs]
+    one = lambda xs: [x[1:2].contiguous() for x in xs]
+
+    bad = [v.clone() for v in value]
+    for v in bad:
+        v[0, lo + 5] = float("nan")
+    o = run_scan(gate, bad, dy, h0, dhT, True, cu)
+    d = run_scan(part(gate), part(bad), part(dy), one(h0), one(dhT), True, None)
+    for r in range(t):
+        y = o["y"][r][0]
+        assert nan(y[lo + 5:hi]) and torch.isfinite(y[:lo + 5]).all() and torch.isfinite(y[hi:]).all()
+        assert nan(o["hT"][r][1]) and nan(d["hT"][r]) and nan(d["y"][r][0, 5:])
+        for name in ("y", "dgate", "dvalue"):
+            a, b = o[name][r][0], clean[name][r][0]
+            assert torch.equal(a[:lo], b[:lo]) and torch.equal(a[hi:], b[hi:]), name
+        for name in ("hT", "dh0"):
+            assert torch.equal(o[name][r][[0, 2, 3]], clean[name][r][[0, 2, 3]]), name
+
+    bad = [v.clone() for v in dy]
+    for v in bad:
+        v[0, hi - 7] = float("nan")
+    o = run_scan(gate, value, bad, h0, dhT, True, cu)
+    for r in range(t):
+        for name in ("dgate", "dvalue"):
+            a, b = o[name][r][0], clean[name][r][0]
+            assert nan(a[lo:hi - 6]) and torch.isfinite(a[hi - 6:]).all()
+            assert torch.equal(a[:lo], b[:lo]) and torch.equal(a[hi:], b[hi:]), name
+        assert nan(o["dh0"][r][1])
+        assert torch.equal(o["dh0"][r][[0, 2, 3]], clean["dh0"][r][[0, 2, 3]])
+
+    for h in h0:
+        h[1] = float("inf")
+    o = run_scan(gate, value, dy, h0, dhT, True, cu)
+    for r in range(t):
+        y = o["y"][r][0]
+        assert not torch.isfinite(y[lo:hi]).any() and not torch.isfinite(o["hT"][r][1]).any()
+        assert torch.isfinite(y[:lo]).all() and torch.isfinite(y[hi:]).all()
