@@ -565,6 +565,16 @@ int32_t sp_abi_version(void);
 sp_status_t sp_debug_inject(sp_status_t code);
 
 /*
+ * sp_debug_scan_withhold -- test hook: in the next sp_gated_scan_fwd or
+ * sp_gated_scan_bwd call that launches, block 0 does not send its part of the join
+ * of this step (from 0) to its cluster, if the launch has clusters and that many
+ * steps.  The cluster's bounded waits run out, each once (a few seconds in all), the
+ * call's dev_status reads SP_ERR_TIMEOUT and its outputs are undefined; nothing
+ * faults or hangs.  -1 disarms it.
+ */
+sp_status_t sp_debug_scan_withhold(int32_t step);
+
+/*
  * sp_debug_tune -- tuning hook: override the launch shape chosen for the
  * forward (kernel 0) or backward (kernel 1) row kernels: `stages` = cp.async
  * pipeline depth, `blocks_per_sm` = resident blocks per SM the grid is sized

@@ -127,6 +127,8 @@ def load():
     lib.sp_abi_version.argtypes = []
     lib.sp_debug_inject.restype = _i32
     lib.sp_debug_inject.argtypes = [_i32]
+    lib.sp_debug_scan_withhold.restype = _i32
+    lib.sp_debug_scan_withhold.argtypes = [_i32]
     lib.sp_debug_tune.restype = _i32
     lib.sp_debug_tune.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.sp_debug_last_shape.restype = _i32
@@ -922,6 +924,10 @@ def sp_group_norm_bwd(dy, x, mean, rstd, gamma, beta=None, *, groups, norm="laye
 
 def sp_debug_inject(code):
     load().sp_debug_inject(int(code))
+
+
+def sp_debug_scan_withhold(step):
+    _check(load().sp_debug_scan_withhold(int(step)))
 
 
 def sp_debug_tune(kernel, stages=0, blocks_per_sm=0, threads=0, chunks=0):

@@ -17,6 +17,7 @@ namespace {
 
 thread_local char g_err[512] = "";
 std::atomic<int> g_inject{SP_OK};
+std::atomic<int32_t> g_withhold{-1};
 // Launch-shape overrides for tuning sweeps: [kernel][stages, blocks per SM,
 // threads, chunks per row (backward only)]; 0 = the default rule.
 std::atomic<int> g_tune[2][4] = {{{0}, {0}, {0}, {0}}, {{0}, {0}, {0}, {0}}};
@@ -46,6 +47,8 @@ bool take_injected(sp_status_t* out) {
   *out = fail(static_cast<sp_status_t>(code), "injected failure (sp_debug_inject)");
   return true;
 }
+
+int32_t take_withheld_step() { return g_withhold.exchange(-1); }
 
 namespace {
 
@@ -1226,6 +1229,12 @@ int32_t sp_abi_version(void) { return SP_ABI_VERSION; }
 
 sp_status_t sp_debug_inject(sp_status_t code) {
   g_inject.store(static_cast<int>(code));
+  return SP_OK;
+}
+
+sp_status_t sp_debug_scan_withhold(int32_t step) {
+  if (step < -1) return fail(SP_ERR_INVALID_ARG, "sp_debug_scan_withhold: step = %d", step);
+  g_withhold.store(step);
   return SP_OK;
 }
 

@@ -14,6 +14,8 @@ sp_status_t fail(sp_status_t code, const char* fmt, ...);
 sp_status_t fail_cuda(cudaError_t e, const char* where);
 // An armed sp_debug_inject: true, and its status in *out.
 bool take_injected(sp_status_t* out);
+// The step of an armed sp_debug_scan_withhold, or -1.
+int32_t take_withheld_step();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

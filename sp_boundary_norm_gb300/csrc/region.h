@@ -58,6 +58,7 @@ struct ScanParams {
   const int32_t* cu_seqlens;
   int32_t n_seqs;
   int32_t* status;
+  int32_t withhold;                   // test hook: block 0 does not send this step's map; -1
 };
 
 cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st);

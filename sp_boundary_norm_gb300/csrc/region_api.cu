@@ -220,6 +220,7 @@ void fill_scan(ScanParams* P, const ScanCall& k, const void* const* gate, int64_
   P->cu_seqlens = k.cu_seqlens;
   P->n_seqs = k.n_seqs;
   P->status = dev_status;
+  P->withhold = take_withheld_step();
 }
 
 // ---------------------------------------------------------------- group norm --

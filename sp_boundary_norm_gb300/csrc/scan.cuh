@@ -254,13 +254,18 @@ __device__ __forceinline__ void pass_empty(const ScanParams& P, const float* src
 // asynchronous stores that count their bytes on the receiver's mbarrier.
 // Buffers and mbarriers alternate between two; a block's map of step n + 2 is
 // sent after all maps of step n + 1 have arrived, which their blocks sent after
-// they had read step n's, so nothing is overwritten before it is read.  The
-// wait is bounded: `alive` turns false when it ran out, and no later step waits.
+// they had read step n's, so nothing is overwritten before it is read.
+//
+// The wait is bounded: `late` is the step in which a thread's ran out (kNever), and it
+// waits no more.  The warp that sends the block's map also arms (lane 0) the mbarriers
+// for the partners' maps, one step after the other; a late lane does neither, so its
+// partners' waits run out too, and no mbarrier is armed again before its phase is over.
 struct JoinBuffers {
   Map2* run;        // [2][warps][32]
   Map2* block;      // [2][cluster][32]
   uint64_t* bar;    // [2]
 };
+constexpr int kNever = 0x7FFFFFFF;
 
 constexpr int kFold = 4;    // maps read at once
 constexpr int kStages = 2;  // runs of a warp on their way
@@ -306,16 +311,17 @@ __device__ __forceinline__ Map2 fold_maps(const Map2* at, int step, int n) {
 
 template <bool CUT, int TIME>
 __device__ __forceinline__ F2 join_runs(const JoinBuffers& sh, int step, Map2 mine, bool cut,
-                                        int C, int rank, int warp, int nw, F2& carry,
-                                        bool& alive) {
+                                        int C, int rank, int warp, int nw, int withhold,
+                                        F2& carry, int& late) {
   if (CUT && !cut) mine.a = uncut(mine.a);
   const int lane = threadIdx.x & 31;
   const int par = step & 1;
   Map2* run = sh.run + par * nw * 32 + lane;
   run[warp * 32] = mine;
-  if (C > 1 && threadIdx.x == 0) mbar_arrive_expect_tx(&sh.bar[par], C * 32 * sizeof(Map2));
-  __syncthreads();
   const int place = TIME > 0 ? warp : nw - 1 - warp;
+  const bool sends = place == nw - 1 && late == kNever;
+  if (C > 1 && sends && lane == 0) mbar_arrive_expect_tx(&sh.bar[par], C * 32 * sizeof(Map2));
+  __syncthreads();
   const Map2* run0 = TIME > 0 ? run : run + (nw - 1) * 32;
   F2 in = carry;
   if (C == 1) {
@@ -325,17 +331,35 @@ __device__ __forceinline__ F2 join_runs(const JoinBuffers& sh, int step, Map2 mi
   }
   const Map2 before = fold_maps<CUT>(run0, TIME * 32, place);
   Map2* block = sh.block + par * C * 32 + lane;
-  if (place == nw - 1) {
+  if (sends && !(blockIdx.x == 0 && step == withhold)) {
     Map2 all = before;
     fold_map<CUT>(all, mine);
     for (int peer = 0; peer < C; ++peer)
       st_async_map(cluster_map(block + rank * 32, peer), all, cluster_map(&sh.bar[par], peer));
   }
-  if (alive) alive = mbar_wait_cluster(&sh.bar[par], (step >> 1) & 1);
+  if (late == kNever && !mbar_wait_cluster(&sh.bar[par], (step >> 1) & 1)) late = step;
   const int place_c = TIME > 0 ? rank : C - 1 - rank;
   const Map2* block0 = TIME > 0 ? block : block + (C - 1) * 32;
   carry = fold_value<CUT>(block0, TIME * 32, C, place_c, carry, &in);
   return through<CUT>(before.a, before.h, in);
+}
+
+// The end of a cluster's blocks, of `steps` steps each.  Where the arming lane is late,
+// partners' maps may still be on their way here: of the step it was late in, and of the
+// next one, which partners go into that had all maps of the first (no further: they
+// miss this block's).  Both are waited for, again with a limit.  (Where it is not, all
+// maps of all steps are here.)
+template <int TIME>
+__device__ __forceinline__ void leave_cluster(const JoinBuffers& sh, int C, int warp, int nw,
+                                              int late, int steps, int32_t* status) {
+  cluster_sync_all();                          // no partner sends any more
+  if (late == kNever) return;
+  if (status != nullptr) *status = SP_ERR_TIMEOUT;
+  if (warp != (TIME > 0 ? nw - 1 : 0) || (threadIdx.x & 31) != 0) return;
+  const int next = late + 1;
+  if (next < steps) mbar_arrive_expect_tx(&sh.bar[next & 1], C * 32 * sizeof(Map2));
+  for (int step = late; step <= next && step < steps; ++step)
+    mbar_wait_cluster(&sh.bar[step & 1], (step >> 1) & 1);
 }
 
 // The shared memory of a block: the ring of `tensors` inputs' runs, the joins'

@@ -106,7 +106,7 @@ scan_bwd_kernel(const ScanParams P) {
   F2 carry = f2(0.f, 0.f);
   SeqWindow win = no_window();
   int step = 0;
-  bool alive = true;
+  int late = kNever;
   for (int64_t base = last; base >= 0; base -= stretch, tok0 -= stretch, ++step) {
     const RunMarks marks = run_marks<PACKED>(P, tok0, win, sh.first, 15);
     const int kind = run_kind(marks, P.s - tok0);
@@ -135,8 +135,8 @@ scan_bwd_kernel(const ScanParams P) {
     __syncwarp();                     // every lane has read the rows
     fetch(stage, tok0 - kStages * stretch);
     fetch_entering(tok0 - stretch);
-    F2 into = join_runs<PACKED, -1>(sh.join, step, mine, marks.ends != 0u, C, rank, warp, nw, carry,
-                                    alive);
+    F2 into = join_runs<PACKED, -1>(sh.join, step, mine, marks.ends != 0u, C, rank, warp, nw,
+                                    P.withhold, carry, late);
     if (tok0 >= P.s) continue;
     char* at_g = dgate + tok0 * P.ld_out;
     char* at_v = dvalue + tok0 * P.ld_dvalue;
@@ -175,8 +175,7 @@ scan_bwd_kernel(const ScanParams P) {
     }
   }
   cp_async_wait<0>();
-  if (!alive && P.status != nullptr) *P.status = SP_ERR_TIMEOUT;
-  if (C > 1) cluster_sync_all();                     // no partner still writes here
+  if (C > 1) leave_cluster<-1>(sh.join, C, warp, nw, late, step, P.status);
 }
 
 template <int DT, bool WIDE>

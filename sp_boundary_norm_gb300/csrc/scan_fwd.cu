@@ -83,7 +83,7 @@ scan_fwd_kernel(const ScanParams P) {
   F2 carry = f2(0.f, 0.f);
   SeqWindow win = no_window();
   int step = 0;
-  bool alive = true;
+  int late = kNever;
   for (int64_t base = 0; base < P.s; base += stretch, tok0 += stretch, ++step) {
     const RunMarks marks = run_marks<PACKED>(P, tok0, win, sh.first, 0);
     const int kind = run_kind(marks, P.s - tok0);
@@ -106,7 +106,7 @@ scan_fwd_kernel(const ScanParams P) {
     __syncwarp();                     // every lane has read the rows
     fetch(stage, tok0 + kStages * stretch);
     const F2 entry = join_runs<PACKED, 1>(sh.join, step, mine, marks.starts != 0u, C, rank, warp, nw,
-                                          carry, alive);
+                                          P.withhold, carry, late);
     if (tok0 >= P.s) continue;
     if (states != nullptr && on)
       __stcs(reinterpret_cast<float2*>(states + (tok0 / kScanRun) * P.c), split(entry));
@@ -140,8 +140,7 @@ scan_fwd_kernel(const ScanParams P) {
     }
   }
   cp_async_wait<0>();
-  if (!alive && P.status != nullptr) *P.status = SP_ERR_TIMEOUT;
-  if (C > 1) cluster_sync_all();                     // no partner still writes here
+  if (C > 1) leave_cluster<1>(sh.join, C, warp, nw, late, step, P.status);
 }
 
 // One token a sequence: nothing to join.  Eight channels a thread, 16-byte loads

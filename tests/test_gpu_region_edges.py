@@ -281,3 +281,37 @@ def test_scan_packed_sequences_keep_what_is_not_finite(t, c, dtype):
         y = o["y"][r][0]
         assert not torch.isfinite(y[lo:hi]).any() and not torch.isfinite(o["hT"][r][1]).any()
         assert torch.isfinite(y[:lo]).all() and torch.isfinite(y[hi:]).all()
+
+
+@pytest.mark.parametrize("s,step,back", [(20000, 0, False), (20000, 3, True), (1600, 0, False)])
+def test_scan_waits_end_and_say_so(s, step, back):
+    """Block 0 withholds a join's map once: every wait for it runs out, the call's status
+    word says so, and the next call is right."""
+    gen = torch.Generator().manual_seed(3)
+    rnd = lambda *shape: torch.randn(shape, generator=gen).to(DEV)
+    gate, value, dy, h0 = [rnd(1, s, 64)], [rnd(1, s, 64)], [rnd(1, s, 64)], [rnd(1, 64)]
+    y, dgate, dvalue = (empties(gate[0], 1) for _ in range(3))
+    st = [torch.empty(sp.sp_gated_scan_states_shape(1, s, 64), device=DEV)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call():
+        if back:
+            sp.sp_gated_scan_bwd(gate, value, st, dy, h0=h0, dgate=dgate, dvalue=dvalue,
+                                 status=status)
+            return dgate + dvalue
+        sp.sp_gated_scan_fwd(gate, value, h0=h0, y=y, states=st, status=status)
+        return y + st
+
+    sp.sp_gated_scan_fwd(gate, value, h0=h0, y=y, states=st)
+    want = [x.clone() for x in call()]
+    assert status.item() == 0
+    sp.sp_debug_scan_withhold(step)
+    call()
+    torch.cuda.synchronize()
+    assert status.item() == 5
+    status.zero_()
+    if back:
+        sp.sp_gated_scan_fwd(gate, value, h0=h0, y=y, states=st)
+    got = call()
+    torch.cuda.synchronize()
+    assert status.item() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
