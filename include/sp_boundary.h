@@ -605,6 +605,16 @@ sp_status_t sp_debug_tune(int32_t kernel, int32_t stages, int32_t blocks_per_sm,
 sp_status_t sp_debug_last_shape(int32_t kernel, int32_t* out);
 
 /*
+ * sp_debug_group_norm_shape -- test hook: how sp_group_norm_fwd (backward 0) or
+ * sp_group_norm_bwd (1) splits a call on the current device.  out: host int64 [8] =
+ * form (0 rows, 1 tiles, 2 held, 3 units), threads per block, blocks per cluster,
+ * 8-channel vectors of a slab, slabs of a row, rows side by side in a block, blocks of
+ * one rank's slab, dynamic shared memory bytes.
+ */
+sp_status_t sp_debug_group_norm_shape(int64_t n, int64_t l, int64_t c, int64_t groups, int32_t t,
+                                      sp_dtype_t dtype, int32_t backward, int64_t* out);
+
+/*
  * sp_debug_philox -- evaluate the library's device Philox4x32-10 on n
  * counter/key sets, for checking it against an independent implementation.
  * in  : device uint32 [n][6] = (c0, c1, c2, c3, k0, k1)

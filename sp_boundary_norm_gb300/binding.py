@@ -129,6 +129,9 @@ def load():
     lib.sp_debug_inject.argtypes = [_i32]
     lib.sp_debug_scan_withhold.restype = _i32
     lib.sp_debug_scan_withhold.argtypes = [_i32]
+    lib.sp_debug_group_norm_shape.restype = _i32
+    lib.sp_debug_group_norm_shape.argtypes = [_i64, _i64, _i64, _i64, _i32, _i32, _i32,
+                                              ctypes.POINTER(_i64)]
     lib.sp_debug_tune.restype = _i32
     lib.sp_debug_tune.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.sp_debug_last_shape.restype = _i32
@@ -941,6 +944,14 @@ def sp_debug_last_shape(kernel):
     out = (ctypes.c_int32 * 6)()
     _check(load().sp_debug_last_shape(int(kernel), ctypes.cast(out, _vp)))
     return dict(zip(("threads", "chunks", "stages", "grid", "cluster", "smem"), list(out)))
+
+
+def sp_debug_group_norm_shape(n, l, c, groups, t, dtype=torch.bfloat16, backward=False):
+    """How a group norm call is split on the current device."""
+    out = (ctypes.c_int64 * 8)()
+    _check(load().sp_debug_group_norm_shape(n, l, c, groups, t, DTYPES[dtype], int(backward), out))
+    return dict(zip(("form", "threads", "cluster", "cols", "slabs", "rows", "parts", "smem"),
+                    list(out)))
 
 
 def sp_debug_philox(ctr_key):

@@ -415,7 +415,8 @@ GroupShape group_norm_shape(int64_t n, int64_t l, int c, int groups, int t, int 
     // narrow slabs of at least 128 bytes of a row, whole 32-byte sectors where
     // that takes two groups at most, and many rows abreast
     fit_cols(q >= 8 ? q : (8 + q - 1) / q * q);
-    if (s.cols % 2 != 0 && 2 * s.cols <= nvec) fit_cols(2 * s.cols);
+    if (s.cols % 2 != 0 && 2 * s.cols <= (nvec < kGroupThreads ? nvec : kGroupThreads))
+      fit_cols(2 * s.cols);
     s.rows = 256 / s.cols > 0 ? 256 / s.cols : 1;
   };
   // held: samples of some rows whose slab, 160 to 1024 vectors, fits the registers

@@ -528,6 +528,20 @@ size_t sp_group_norm_bwd_workspace_bytes(int64_t n, int64_t l, int64_t c, int64_
   return static_cast<size_t>(s.parts) * 2 * static_cast<size_t>(t * c) * sizeof(float);
 }
 
+sp_status_t sp_debug_group_norm_shape(int64_t n, int64_t l, int64_t c, int64_t groups, int32_t t,
+                                      sp_dtype_t dtype, int32_t backward, int64_t* out) {
+  sp_status_t st;
+  if ((st = check_group(n, l, c, groups, t, dtype)) != SP_OK) return st;
+  if (n * l == 0 || out == nullptr)
+    return fail(SP_ERR_INVALID_ARG, "sp_debug_group_norm_shape: bad arguments");
+  const GroupShape s = group_norm_shape(n, l, static_cast<int>(c), static_cast<int>(groups), t,
+                                        dtype, backward != 0);
+  const int64_t v[8] = {s.form, s.threads, s.cluster, s.cols,
+                        s.slabs, s.rows, s.parts, static_cast<int64_t>(s.smem)};
+  for (int i = 0; i < 8; ++i) out[i] = v[i];
+  return SP_OK;
+}
+
 sp_status_t sp_group_norm_bwd(const void* const* dy, int64_t dy_ld, const void* const* x,
                               int64_t x_ld, const float* const* mean, const float* const* rstd,
                               const void* gamma, const void* beta, int64_t n, int64_t l, int64_t c,

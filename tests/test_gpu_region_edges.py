@@ -16,7 +16,7 @@ import pytest
 import torch
 
 from sp_boundary_norm_gb300 import binding as sp
-from test_gpu_region import BF, DEV, F32, FP, LEAST, STEP, f64, rand
+from test_gpu_region import (BF, DEV, F32, FP, LEAST, STEP, check_norm, f64, norm_inputs, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -315,3 +315,15 @@ def test_scan_waits_end_and_say_so(s, step, back):
     got = call()
     torch.cuda.synchronize()
     assert status.item() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------- group norm --
+
+@pytest.mark.parametrize("n,l,c,groups,dtype", [
+    (2, 5, 2 * 2056, 2, BF), (3, 3, 2 * 2056, 2, FP), (1, 300, 3 * 2056, 3, BF),
+    (2, 5, 2 * 4088, 2, F32), (1, 65, 4 * 4088, 4, BF), (1, 40, 5 * 3000, 5, F32)])
+@pytest.mark.parametrize("norm", ["layernorm", "rmsnorm"])
+def test_group_norm_wide_odd_groups(n, l, c, groups, dtype, norm):
+    """Groups of an odd number of vectors beyond 256, two and more in a row."""
+    i = norm_inputs(1, n, l, c, dtype, 51)
+    check_norm(i, run_norm(i, groups, norm, "silu"), groups, norm, "silu")
