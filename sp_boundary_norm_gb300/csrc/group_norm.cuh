@@ -151,48 +151,48 @@ __device__ __forceinline__ float pair_sum(const F2 (&v)[4]) {
   return w.x + w.y;
 }
 
-// Sum of (x - m)^2 of a vector.
-__device__ __forceinline__ float spread_sum(const F2 (&x)[4], float m) {
-  F2 d = add2(x[0], both(-m)), s = mul2(d, d);
+// The mean of values that sum to `sum`; inv: 1 / count rounded.  The product's error is
+// taken off again, so that the mean of equal values is their value.  An infinity stays.
+__device__ __forceinline__ float mean_of(float sum, float count, float inv) {
+  const float m = sum * inv, near = fmaf(fmaf(-m, count, sum), inv, m);
+  return isinf(m) ? m : near;
+}
+
+// x - m in place of a vector's x, before anything is multiplied: where all values are
+// alike, however large, nothing is left (x rstd - m rstd would leave 2^-24 of m rstd).
+__device__ __forceinline__ void centre(F2 (&x)[4], float m) {
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    d = add2(x[i], both(-m));
-    s = fma2(d, d, s);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = add2(x[i], both(-m));
+}
+
+// Sum of (x - m)^2 of a vector, which is left as x - m.
+__device__ __forceinline__ float spread_sum(F2 (&x)[4], float m) {
+  centre(x, m);
+  F2 s = mul2(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(x[i], x[i], s);
   const float2 w = split(s);
   return w.x + w.y;
 }
 
-// z = (x - mean) rstd.  For 16-bit inputs as x rstd - mean rstd, one operation:
-// its rounding, 2^-24 of |mean| rstd, is below the inputs' own, 2^-11 of it.
-template <int DT>
-__device__ __forceinline__ F2 standard(F2 x, float mean, float rstd) {
-  if constexpr (DT == SP_F32) return mul2(add2(x, both(-mean)), both(rstd));
-  return fma2(x, both(rstd), both(-mean * rstd));
-}
-
 __device__ __forceinline__ F2 neg(F2 v) { return mul2(v, both(-1.f)); }
 
-// The column's parameters with a group's statistics folded in, for many vectors
-// of that group: q = x gamma + beta then (16-bit inputs; else as they are).
+// rstd folded into the column's gamma, for many vectors of one group (16-bit inputs).
 template <int DT>
-__device__ __forceinline__ void fold_stats(Column<DT>& col, float mean, float rstd) {
+__device__ __forceinline__ void fold_rstd(Column<DT>& col, float rstd) {
   if constexpr (DT == SP_F32) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    col.gamma[i] = mul2(col.gamma[i], both(rstd));
-    col.beta[i] = fma2(neg(col.gamma[i]), both(mean), col.beta[i]);
-  }
+  for (int i = 0; i < 4; ++i) col.gamma[i] = mul2(col.gamma[i], both(rstd));
 }
 
-// One vector's result; FOLDED: the column's parameters hold the statistics.
+// The result of one vector of x - mean; FOLDED: the column's gamma holds rstd.
 template <int DT, bool FOLDED = false>
-__device__ __forceinline__ Vec8<DT> norm_act(const F2 (&x)[4], float mean, float rstd,
-                                             const Column<DT>& col, bool silu) {
+__device__ __forceinline__ Vec8<DT> norm_act(const F2 (&d)[4], float rstd, const Column<DT>& col,
+                                             bool silu) {
   F2 y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const F2 z = FOLDED && DT != SP_F32 ? x[i] : standard<DT>(x[i], mean, rstd);
+    const F2 z = FOLDED && DT != SP_F32 ? d[i] : mul2(d[i], both(rstd));
     y[i] = fma2(z, col.gamma[i], col.beta[i]);
   }
   if (silu) {
@@ -208,7 +208,8 @@ __device__ __forceinline__ Vec8<DT> norm_act(const F2 (&x)[4], float mean, float
 // vectors sums x - k and its square for each of the 8 channels, k the
 // stretch's first vector: one of the values themselves, so (x - k)^2 sums to at
 // most the count times the spread, and no mean, however far from zero, costs
-// digits.  Stretches then join by their means.
+// digits.  Stretches then join by their means.  An infinity (which is no k) makes the
+// mean infinite, as it would the sum.
 constexpr int kStretch = 64;
 struct Moments {
   F2 k[4], s[4], q[4];
@@ -218,7 +219,8 @@ struct Moments {
     if (n == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        k[i] = centred ? neg(v[i]) : both(0.f);
+        const float2 w = split(v[i]);
+        k[i] = centred ? f2(isinf(w.x) ? 0.f : -w.x, isinf(w.y) ? 0.f : -w.y) : both(0.f);
         s[i] = q[i] = both(0.f);
       }
     }
@@ -233,7 +235,7 @@ struct Moments {
   // Ends the stretch.  Not centred: mean stays 0 and M2 is the sum of squares.
   __device__ __forceinline__ void join(bool centred) {
     if (n == 0) return;
-    const float nf = static_cast<float>(n), inv = __fdividef(1.f, nf);
+    const float nf = static_cast<float>(n), inv = 1.f / nf;
     F2 mc[4], sum = both(0.f), rest = both(0.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -250,8 +252,8 @@ struct Moments {
       apart = fma2(d, d, apart);
     }
     const float2 r = split(rest), w = split(apart);
-    const float nb = 8.f * nf, all = cnt + nb, part = __fdividef(nb, all), d = mb - mean;
-    mean = fmaf(d, part, mean);
+    const float nb = 8.f * nf, all = cnt + nb, part = nb / all, d = mb - mean;
+    mean = isinf(d) ? mean + mb : fmaf(d, part, mean);
     m2 += (r.x + r.y) + (centred ? nf * (w.x + w.y) : 0.f) + d * d * cnt * part;
     cnt = all;
     n = 0;
@@ -263,7 +265,7 @@ template <int DT>
 __device__ __forceinline__ void back_act(F2 (&x)[4], F2 (&dy)[4], float mean, float rstd,
                                          const Column<DT>& col, bool silu) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = standard<DT>(x[i], mean, rstd);
+  for (int i = 0; i < 4; ++i) x[i] = mul2(add2(x[i], both(-mean)), both(rstd));
   if (silu) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -58,7 +58,7 @@ group_row_fwd_kernel(const GroupNormParams P) {
       for (int u = 0; u < kRows; ++u) mean[u] = pair_sum(v[u]);
       group.sum(mean);
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) mean[u] *= P.count_inv;
+      for (int u = 0; u < kRows; ++u) mean[u] = mean_of(mean[u], P.count, P.count_inv);
     }
     // (lanes that hold no vector hold zeros: they add nothing)
 #pragma unroll
@@ -69,7 +69,7 @@ group_row_fwd_kernel(const GroupNormParams P) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       if (!on || row + u >= P.n) continue;
-      store_pack(out + u * P.ld_out, norm_act<DT>(v[u], mean[u], rstd[u], col, silu));
+      store_pack(out + u * P.ld_out, norm_act<DT>(v[u], rstd[u], col, silu));
       if (tells) {
         rstd_at[u * P.groups] = rstd[u];
         if (ln) mean_at[u * P.groups] = mean[u];
@@ -158,8 +158,10 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
           for (int i = 0; i < l; ++i, at += P.cols)
             for (int j = lane; j < P.q; j += P.lanes) w += at[j];
         }
-        w = lanes_sum(w, P.lanes) * P.count_inv;
-        if (p < pairs && lane == 0) stat[pass * pairs + p] = pass == 0 ? w : rsqrtf(w + P.eps);
+        w = lanes_sum(w, P.lanes);
+        if (p < pairs && lane == 0)
+          stat[pass * pairs + p] = pass == 0 ? mean_of(w, P.count, P.count_inv)
+                                             : rsqrtf(w * P.count_inv + P.eps);
       }
       __syncthreads();
 #pragma unroll
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_tile_fwd_kernel(const Gro
     for (int u = 0; u < kTileRows; ++u) {
       const int row = ry + u * P.rows;
       if (!on || row >= here) continue;
-      store_pack(to + row * P.ld_out, norm_act<DT>(v[u], mean[u], rstd[u], col, silu));
+      store_pack(to + row * P.ld_out, norm_act<DT>(v[u], rstd[u], col, silu));
       if (leads[u]) {
         const int64_t at = (s0 + row / l) * P.groups + group;
         if (ln) P.mean[r][at] = mean[u];
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(256, kHeldBlocks) group_held_fwd_kernel(const 
   const int64_t skip_x = P.parts * P.l * P.ld_x, skip_out = P.parts * P.l * P.ld_out;
   Column<DT> col;
   col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
-  const float each = mine > 0 ? 0.125f / static_cast<float>(mine) : 0.f;
+  const float count = 8.f * static_cast<float>(mine), each = mine > 0 ? 1.f / count : 0.f;
   for (int64_t sample = part; sample < P.n; sample += P.parts, x += skip_x, out += skip_out) {
     Vec8<DT> raw[kMost];
     const char* from = x;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(256, kHeldBlocks) group_held_fwd_kernel(const 
           unpack_pairs(raw[u], v);
           mom.x += pair_sum(v);
         }
-      mom.x *= each;
+      mom.x = mean_of(mom.x, count, each);
     }
 #pragma unroll
     for (int u = 0; u < kMost; ++u)
@@ -297,7 +299,8 @@ __global__ void __launch_bounds__(256, kHeldBlocks) group_held_fwd_kernel(const 
       if (u < mine) {
         F2 v[4];
         unpack_pairs(raw[u], v);
-        store_pack(to, norm_act<DT>(v, st.x, st.y, col, silu));
+        centre(v, st.x);
+        store_pack(to, norm_act<DT>(v, st.y, col, silu));
       }
   }
 }
@@ -365,7 +368,7 @@ group_unit_fwd_kernel(const GroupNormParams P) {
   const float2 st = stat[cx / P.q];
   Column<DT> col;
   col.read(P, static_cast<int64_t>(r) * P.c + vec * 8, on);
-  fold_stats(col, st.x, st.y);
+  fold_rstd(col, st.y);
   char* out = P.out[r] + row0 * P.ld_out + static_cast<int64_t>(vec) * 8 * E;
   for (int i0 = 0; i0 < mine; i0 += kRing) {
 #pragma unroll
@@ -373,7 +376,8 @@ group_unit_fwd_kernel(const GroupNormParams P) {
       F2 v[4];
       unpack_pairs(raw[u], v);
       fetch(u, i0 + kRing + u, false);
-      if (i0 + u < mine) store_pack(out, norm_act<DT, true>(v, st.x, st.y, col, silu));
+      centre(v, st.x);
+      if (i0 + u < mine) store_pack(out, norm_act<DT, true>(v, st.y, col, silu));
     }
   }
 }

@@ -78,7 +78,7 @@ struct GroupNormParams {
   int64_t ld_x, ld_dy, ld_out;          // bytes between rows
   int64_t n, l;                         // samples, rows of a sample
   int32_t c, t, groups, norm, act;
-  float eps, count_inv;                 // 1 / (l * channels of a group)
+  float eps, count, count_inv;          // l * channels of a group, 1 / that
   // the split of a call, chosen on the host
   int32_t q;                            // 8-channel vectors of a group
   int32_t cols, slabs;                  // vectors of a slab (whole groups), slabs of a row

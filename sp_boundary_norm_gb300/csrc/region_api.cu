@@ -281,7 +281,9 @@ void fill_group(GroupNormParams* P, int64_t n, int64_t l, int64_t c, int64_t gro
   P->act = act;
   P->gamma = static_cast<const char*>(gamma);
   P->beta = static_cast<const char*>(beta);
-  P->count_inv = static_cast<float>(1.0 / (static_cast<double>(l) * static_cast<double>(c / groups)));
+  const double count = static_cast<double>(l) * static_cast<double>(c / groups);
+  P->count = static_cast<float>(count);
+  P->count_inv = static_cast<float>(1.0 / count);
 }
 
 }  // namespace

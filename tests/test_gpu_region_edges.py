@@ -327,3 +327,43 @@ def test_group_norm_wide_odd_groups(n, l, c, groups, dtype, norm):
     """Groups of an odd number of vectors beyond 256, two and more in a row."""
     i = norm_inputs(1, n, l, c, dtype, 51)
     check_norm(i, run_norm(i, groups, norm, "silu"), groups, norm, "silu")
+
+
+@pytest.mark.parametrize("n,l,c,groups", [
+    (9, 1, 128, 2), (7, 1, 240, 2), (3, 1, 4096, 1), (3, 6, 40, 1), (6, 4, 512, 8), (3, 50, 1360, 17),
+    (40, 24, 40, 5), (2, 800, 64, 4), (1, 5001, 72, 3), (1, 9000, 4096, 2), (2, 3000, 64, 1)])
+@pytest.mark.parametrize("dtype,value,eps", [(BF, 1000.0, 1e-5), (FP, 30000.0, 1e-6),
+                                             (F32, -1000.5, 1e-6)])
+def test_group_norm_without_spread(n, l, c, groups, dtype, value, eps):
+    """All values of a sample alike and far from zero, of which every sum is exact: x - mean
+    is zero, so y = beta and dgamma = 0 to the bit, in every form; dx = rstd (dz - mean dz)
+    within its own roundings."""
+    i = norm_inputs(1, n, l, c, dtype, 52)
+    i["x"][0].fill_(value)
+    o = run_norm(i, groups, "layernorm", "none", eps)
+    assert (o["mean"][0] == value).all()
+    assert torch.equal(o["y"][0], i["beta"].expand(n, l, c))
+    assert (o["dgamma"] == 0).all()
+    rstd = f64(o["rstd"][0])
+    assert np.abs(rstd * eps ** 0.5 - 1).max() < 4 * U     # 1 / sqrt, eps in 32 bits
+    dz = (f64(i["dy"][0]) * f64(i["gamma"])).reshape(n, l, groups, -1)
+    m = dz.mean((1, 3), keepdims=True)
+    want = (dz - m) * rstd[:, None, :, None]
+    # dz's product, the sum's roundings (below 2^7 in a row and its partial sums: 2^8) and
+    # the mean, a difference, a product
+    mag = np.abs(dz) + 2.0 ** 8 * np.abs(dz).mean((1, 3), keepdims=True)
+    bound = (4 * U * mag * rstd[:, None, :, None]).reshape(n, l, c)
+    within(o["dx"][0], want.reshape(n, l, c), bound, "dx")
+
+
+@pytest.mark.parametrize("n,l,c,groups", [(4, 1, 128, 2), (3, 6, 40, 1), (3, 50, 1360, 17), (2, 800, 64, 2)])
+def test_group_norm_infinite_mean(n, l, c, groups):
+    """One infinity in a group: its mean is infinite, other groups keep their bits."""
+    i = norm_inputs(1, n, l, c, BF, 53)
+    want = run_norm(i, groups, "layernorm", "silu")
+    i["x"][0][0, 0, 0] = float("inf")
+    o = run_norm(i, groups, "layernorm", "silu")
+    assert o["mean"][0][0, 0] == float("inf") and not torch.isfinite(o["y"][0][0, 0, 0])
+    for name in ("mean", "rstd"):
+        assert torch.equal(o[name][0].flatten()[1:], want[name][0].flatten()[1:])
+    assert torch.equal(o["y"][0][1:], want["y"][0][1:])
