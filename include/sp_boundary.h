@@ -388,7 +388,7 @@ typedef enum sp_dtype { SP_BF16 = 0, SP_F16 = 1, SP_F32 = 2 } sp_dtype_t;
 
 typedef enum sp_act {
   SP_ACT_NONE = 0,
-  SP_ACT_SILU = 1            /* q * sigmoid(q) */
+  SP_ACT_SILU = 1            /* q * sigmoid(q); a sigmoid below 2^-126 counts as 0 */
 } sp_act_t;
 
 typedef enum sp_rope_layout {
@@ -431,11 +431,12 @@ sp_status_t sp_rope_table(int32_t rot_dim, double base, sp_rope_scaling_t scalin
  * sp_rope_fwd -- rotary positions on the heads of all ranks.
  *   (u, v) -> mscale (u cos x - v sin x, v cos x + u sin x),  x = position * w_i
  * for the rotated pairs of every head; the d - rot_dim elements after them are
- * copied.  Angles are exact modulo one turn for positions of any size.
+ * copied.  Angles are exact modulo one turn at any position, for the table's
+ * frequencies; those are off by a few 2^-53 of themselves and 2^-65 turns.
  *
  * x, y [t] (b, s, heads, d)  rank r's heads; x_ld, y_ld between tokens,
- *                    x_head, y_head between heads (elements, >= d; row strides
- *                    of any value >= heads' extent)
+ *                    x_head, y_head between heads (elements, >= d; row strides of
+ *                    any value >= (heads - 1) * head + d: heads lie inside tokens)
  * positions          device int64 (b, s), or NULL: the token's index in its batch
  *                    row, or with cu_seqlens in its packed sequence,
  * first_position     plus this (ignored with positions)
@@ -486,7 +487,8 @@ sp_status_t sp_gated_scan_fwd(const void* const* gate, int64_t gate_ld, const vo
 
 /*
  * sp_gated_scan_bwd -- gradients of sp_gated_scan_fwd called with the same
- * gate, value, h0 and shape, from the states it saved.
+ * gate, value, h0 and shape, from the states it saved.  (Where hT was written over
+ * h0, h0 here is a copy of what it held before.)
  *
  * dy     [t] (b, s, c)        gradient of y
  * dhT    [t] (n, c) float32   gradient of hT, or a NULL array (zero)

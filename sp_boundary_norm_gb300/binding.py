@@ -795,8 +795,10 @@ def _rope_call(entry, x, table, layout, positions, first_position, cu_seqlens, y
 def sp_rope_fwd(x, table, *, layout="half", positions=None, first_position=0, cu_seqlens=None, y,
                 status=None):
     """Rotary positions: turns the pairs of every head of the (b, s, heads, d) rank
-    buffers x into y (y may be x: in place).  Strides between tokens and heads are
-    free.  A token's position: positions (int64 (b, s)), else first_position plus its
+    buffers x into y (y may be x: in place).  A token's heads may lie apart, and tokens
+    too, but heads between tokens: the stride from token to token spans a token's heads
+    (a heads-first tensor seen as (b, s, heads, d) is refused), and batch rows follow
+    each other.  A token's position: positions (int64 (b, s)), else first_position plus its
     index in its batch row, or with cu_seqlens in its packed sequence."""
     _rope_call("sp_rope_fwd", x, table, layout, positions, first_position, cu_seqlens, y, status)
 

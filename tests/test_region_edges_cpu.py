@@ -1,4 +1,6 @@
 """Host rules of the operators between g and the next g* over their whole range."""
+import ctypes
+
 import pytest
 import torch
 
@@ -51,3 +53,15 @@ def test_group_norm_split_refuses():
         how.update(bad)
         with pytest.raises(sp.SpError):
             sp.sp_debug_group_norm_shape(**how)
+
+
+def test_rope_refuses_heads_outside_tokens():
+    """(b, heads, s, d) memory seen as (b, s, heads, d): the stride between tokens is one
+    head's, below the extent of a token's heads."""
+    lib, tab = sp.load(), sp.sp_rope_table(64)
+    x, y = ((ctypes.c_void_p * 1)(at) for at in (0x7F0000000000, 0x7F1000000000))
+    for x_ld, x_head, y_ld, y_head in ((64, 8 * 64, 3 * 64, 64), (3 * 64, 64, 64, 8 * 64),
+                                       (2 * 80 + 63, 80, 3 * 64, 64)):
+        assert lib.sp_rope_fwd(x, x_ld, x_head, 1, 8, 3, 64, 1, 0, ctypes.byref(tab), 0, None, 0,
+                               None, 0, y, y_ld, y_head, None, None) == 1
+        assert b"strides" in lib.sp_last_error()
