@@ -15,8 +15,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import region as orc
 from sp_boundary_norm_gb300 import binding as sp
-from test_gpu_region import (BF, DEV, F32, FP, LEAST, STEP, check_norm, f64, norm_inputs, run_norm)
+from test_gpu_region import (BF, DEV, F32, FP, LEAST, STEP, check_norm, f64, norm_inputs,
+                             rand, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -367,3 +369,71 @@ def test_group_norm_infinite_mean(n, l, c, groups):
     for name in ("mean", "rstd"):
         assert torch.equal(o[name][0].flatten()[1:], want[name][0].flatten()[1:])
     assert torch.equal(o["y"][0][1:], want["y"][0][1:])
+
+
+# ------------------------------------------------------------------ sigmoids --
+
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+def test_sigmoids_of_the_recurrence(dtype):
+    """a and k of one token over all gates, as float32 states: h0 = 1 and no value gives a,
+    h0 = 0 and a value of 1 gives k."""
+    gate = torch.linspace(-86.5, 86.5, 1 << 16).view(64, 1, 1024).to(dtype).to(DEV)
+    one, zero = torch.ones((64, 1024), device=DEV), torch.zeros((64, 1024), device=DEV)
+    y, g = torch.empty_like(gate), f64(gate)[:, 0]
+    a, k = empties(one, 1)[0], empties(one, 1)[0]
+    sp.sp_gated_scan_fwd([gate], [torch.zeros_like(gate)], h0=[one], tied=False, y=[y], hT=[a])
+    sp.sp_gated_scan_fwd([gate], [torch.ones_like(gate)], h0=[zero], tied=True, y=[y], hT=[k])
+    d = delta(g, dtype)
+    within(a, sigmoid(g), sigmoid(g) * (sigmoid(-g) * d + RHO + U), "a")
+    within(k, sigmoid(-g), sigmoid(-g) * (sigmoid(g) * d + RHO + 2 * U), "k")
+    # beyond: at most 2^-125, and 1
+    gate = torch.tensor([88.0, 100.0, 3e4, float("inf")], device=DEV).to(dtype)
+    gate = torch.cat((-gate, gate)).view(8, 1, 1).expand(8, 1, 1024).contiguous()
+    y = torch.empty_like(gate)
+    sp.sp_gated_scan_fwd([gate], [torch.zeros_like(gate)], h0=[one[:8]], tied=False, y=[y], hT=[a[:8]])
+    sp.sp_gated_scan_fwd([gate], [torch.ones_like(gate)], h0=[zero[:8]], tied=True, y=[y], hT=[k[:8]])
+    assert (a[:4] >= 0).all() and (a[:4] <= 2.0 ** -125).all() and (a[4:8] == 1).all()
+    assert (k[4:8] >= 0).all() and (k[4:8] <= 2.0 ** -125).all() and (k[:4] - 1).abs().max() <= 4 * U
+
+
+@pytest.mark.parametrize("l", [1, 3, 40, 700])
+def test_silu_of_group_norm(l):
+    """gamma = 0: y = silu(beta), float32, in every form; beside it the library's own."""
+    beta = torch.linspace(-95, 95, 4096)
+    i = norm_inputs(1, 2, l, 4096, F32, 54)
+    i["gamma"].zero_()
+    i["beta"].copy_(beta)
+    o = run_norm(i, 8, "layernorm", "silu")
+    q = f64(i["beta"])
+    want = np.broadcast_to(q * sigmoid(q), (2, l, 4096))
+    # below -87.3 the sigmoid is flushed: at most 95 * 2^-125 is lost
+    bound = np.abs(want) * (sigmoid(-q) * delta(q, F32) + RHO + U) + 95 * 2.0 ** -125
+    within(o["y"][0], want, bound, "y")
+    near = np.abs(q) < 80
+    off = lambda y: (np.abs(y - want) / np.abs(want))[..., near].max() / U
+    print("off in 2^-24:", off(f64(o["y"][0])), "torch:",
+          off(f64(torch.nn.functional.silu(i["beta"])).reshape(1, 1, -1)))
+
+
+# -------------------------------------------------------------------- rotary --
+
+@pytest.mark.parametrize("t,heads,d,layout,dtype", [
+    (1, 9, 128, "half", BF), (2, 5, 80, "interleaved", FP), (1, 7, 24, "half", F32)])
+@pytest.mark.parametrize("s", [1, 37, 811, 1216, 2431, 2433, 4863, 4865, 9727, 9729, 20011])
+def test_rope_around_the_chunk_rule(t, heads, d, layout, dtype, s):
+    """Token counts on both sides of the rule that cuts few tokens' heads into pieces (of
+    whole lane rounds, the last one short) and of the grid's warps, beyond which a warp
+    takes one token after the other."""
+    gen = torch.Generator().manual_seed(s)
+    x = [rand((1, s, heads, d), gen, dtype) for _ in range(t)]
+    y = empties(x[0], t)
+    tab = sp.sp_rope_table(d - 8)
+    sp.sp_rope_fwd(x, tab, layout=layout, first_position=5, y=y)
+    at = np.unique(np.concatenate((np.arange(min(s, 20)), np.arange(max(0, s - 20), s),
+                                   np.random.default_rng(s).integers(0, s, 200))))
+    for r in range(t):
+        want, mag = orc.rope(f64(x[r])[:, at], orc.positions(1, s, 5)[:, at],
+                             orc.frequencies(d - 8), layout)
+        # under 8 units of 2^-24, as for the other rotary tests
+        within(y[r][:, at], want, 2.0 ** -21 * mag, f"rank {r}")
+        assert torch.isfinite(y[r]).all()
