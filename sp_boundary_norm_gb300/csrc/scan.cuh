@@ -15,8 +15,8 @@
 //
 // Measured on a GB300, bf16 (the rate is of the bytes that have to move; the
 // measured copy rate is 6.8 TB/s): 8 ranks of 16,384 tokens x 1024 channels,
-// forward 158 us (5.1 TB/s), backward 240 (5.6); packed as 12 sequences
-// 181 and 275; 1 rank of 65,537 x 512 75 and 106, where the steps' joins are what
+// forward 151 us (5.3 TB/s), backward 235 (5.7); packed as 12 sequences
+// 171 and 263; 1 rank of 65,537 x 512 77 and 107, where the steps' joins are what
 // takes time: few channels cannot fill the SMs otherwise.
 //
 // Two exponentials' worth of special functions, a scan and a correction an
@@ -77,7 +77,7 @@ __device__ __forceinline__ F2 next_state(F2 a, F2 k, F2 h, F2 v) {
 // The product of the a of a run, and 1 - that product, a sum of k a...a.  An open gate's
 // a, next to 1, is off by up to 2^-23, and products of such numbers round to one side:
 // over a memory of 1/k tokens that adds up (65,537 tokens with k around 1e-5: 2e-5 of
-// the state, against 8e-7).  So what passes from run to run is 1 - lost while that is at
+// the state, against 2e-6).  So what passes from run to run is 1 - lost while that is at
 // least 1/2; the product, which has the digits of shut gates, otherwise and in the run.
 struct RunFactor {
   F2 a = f2(1.f, 1.f), lost = f2(0.f, 0.f);
@@ -447,8 +447,14 @@ struct ScanCost {
   int tensors, passes;
 };
 
-// Chooses the split of a call and launches kernel `fn` (or `wide`).
-cudaError_t launch_scan(const void* fn, const void* wide, ScanParams& p, int elem,
+// A direction's kernels: small blocks, the same with one block an SM more (or NULL),
+// blocks that have an SM to themselves.
+struct ScanKernels {
+  const void *fn, *more, *wide;
+};
+
+// Chooses the split of a call and launches its kernel.
+cudaError_t launch_scan(const ScanKernels& kernels, ScanParams& p, int elem,
                         const ScanCost& cost, void** args, cudaStream_t st);
 
 }  // namespace spb

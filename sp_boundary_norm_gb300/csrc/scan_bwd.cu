@@ -197,10 +197,11 @@ static const void* scan_bwd_fn(int dtype, bool tied, bool packed) {
 cudaError_t launch_scan_bwd(ScanParams p, int dtype, cudaStream_t st) {
   void* args[] = {&p};
   const bool packed = p.cu_seqlens != nullptr;
-  const void* fn = scan_bwd_fn<false>(dtype, p.tied, packed);
-  const void* wide = scan_bwd_fn<true>(dtype, p.tied, packed);
-  const ScanCost cost{0.6, 0.7, 0.045, 0.2, 3, 5};
-  return launch_scan(fn, wide, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
+  const ScanKernels kernels{scan_bwd_fn<false>(dtype, p.tied, packed), nullptr,
+                            scan_bwd_fn<true>(dtype, p.tied, packed)};
+  const ScanCost cost = dtype == SP_F32 ? ScanCost{0.95, 1.34, 0.08, 0.3, 3, 5}
+                                        : ScanCost{0.46, 0.81, 0.06, 0.18, 3, 5};
+  return launch_scan(kernels, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
 }
 
 }  // namespace spb

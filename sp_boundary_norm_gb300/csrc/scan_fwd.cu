@@ -7,10 +7,11 @@
 
 namespace spb {
 
-// Blocks an SM that the registers are held to (16,384 tokens x 8 ranks of 1024 channels:
-// 158 us with three, 169 with four, which spill a few registers; 16 rows of 512 tokens
-// 65 and 69; 12 packed sequences, whose marks take registers, 181 with three).
-constexpr int kFwdBlocks = 3;
+// Blocks of up to four warps an SM that the registers are held to: three, or for dense
+// 16-bit batches of many short sequences four, which spill a few registers (8192
+// channels of 8 rows of 2048 tokens 139 us with three, 144 with four; 2048 of 16 rows of
+// 1000 46 and 40, 512 of 64 rows of 100 8.9 and 6.8, 1024 of 300 rows of 33 37 and 32).
+constexpr int kFwdBlocks = 3, kFwdMoreBlocks = 4;
 
 // One run: h[i], f[i] with h[i] + f[i] * (state entering the run) the state
 // after token i.  i0, h0: the first token that begins a sequence and the state
@@ -41,9 +42,9 @@ __device__ __forceinline__ Map2 scan_run(const Shared& sh, int stage, uint32_t s
   return Map2{fac.whole(), cur};
 }
 
-template <int DT, bool TIED, bool PACKED, bool WIDE>
-__global__ void __launch_bounds__(32 * (WIDE ? kScanWideWarps : kScanWarps),
-                                  WIDE ? 1 : kFwdBlocks)
+// BLOCKS: an SM's; 1: a wide block.
+template <int DT, bool TIED, bool PACKED, int BLOCKS>
+__global__ void __launch_bounds__(32 * (BLOCKS == 1 ? kScanWideWarps : kScanWarps), BLOCKS)
 scan_fwd_kernel(const ScanParams P) {
   constexpr int E = ElemSize<DT>::value;
   extern __shared__ __align__(16) char smem[];
@@ -193,50 +194,59 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const ScanParams P) {
   }
 }
 
-template <int DT, bool WIDE>
-static const void* scan_fwd_fn(bool tied, bool packed) {
-  if (tied)
-    return packed ? reinterpret_cast<const void*>(&scan_fwd_kernel<DT, true, true, WIDE>)
-                  : reinterpret_cast<const void*>(&scan_fwd_kernel<DT, true, false, WIDE>);
-  return packed ? reinterpret_cast<const void*>(&scan_fwd_kernel<DT, false, true, WIDE>)
-                : reinterpret_cast<const void*>(&scan_fwd_kernel<DT, false, false, WIDE>);
+template <int DT, bool TIED, bool PACKED>
+static ScanKernels scan_fwd_kernels() {
+  ScanKernels k{};
+  k.fn = reinterpret_cast<const void*>(&scan_fwd_kernel<DT, TIED, PACKED, kFwdBlocks>);
+  k.wide = reinterpret_cast<const void*>(&scan_fwd_kernel<DT, TIED, PACKED, 1>);
+  if constexpr (!PACKED && DT != SP_F32)
+    k.more = reinterpret_cast<const void*>(&scan_fwd_kernel<DT, TIED, false, kFwdMoreBlocks>);
+  return k;
+}
+template <int DT>
+static ScanKernels scan_fwd_kernels(bool tied, bool packed) {
+  if (tied) return packed ? scan_fwd_kernels<DT, true, true>() : scan_fwd_kernels<DT, true, false>();
+  return packed ? scan_fwd_kernels<DT, false, true>() : scan_fwd_kernels<DT, false, false>();
 }
 
-template <bool WIDE>
-static const void* scan_fwd_fn(int dtype, bool tied, bool packed) {
-  return dtype == SP_BF16  ? scan_fwd_fn<SP_BF16, WIDE>(tied, packed)
-         : dtype == SP_F16 ? scan_fwd_fn<SP_F16, WIDE>(tied, packed)
-                           : scan_fwd_fn<SP_F32, WIDE>(tied, packed);
-}
-
-// Blocks of up to four warps, of which an SM takes several, or of 8 or 12 that
-// have an SM to themselves (kernel `wide`); C blocks a cluster, for the split
-// with the least expected time: the clusters that fit the GPU at once run in
+// Blocks of up to four warps, of which an SM takes several (lone ones of kernel `more`
+// one more, each a tenth slower), or of 8 or 12 that have an SM to themselves (kernel
+// `wide`); C blocks a cluster, for the split with the least expected time: the clusters that fit the GPU at once run in
 // waves, and a step of a wave takes its shortest time and that of its bytes at
-// 6.0 TB/s (the cubes add up: the longer one rules).  Many channels fill the GPU
-// with small blocks, whose steps overlap; few channels need long steps, because
-// what a step costs grows less than its warps.  Measured, bf16, forward and
-// backward in us:
-//   16,384 tokens of 8192 channels: 4 warps, C = 3 172, 235; C = 4 151, 296;
-//     12 warps, C = 1 150, 246; C = 2 187, 273
-//   16,384 of 1024: 4 warps, C = 16 40, 53; 8, C = 12 47, 68; 12, C = 6 37, 55
-//   65,537 of 512: 4 warps, C = 16 141, 158; 8, C = 12 85, 119; 12, C = 12 75, 112
-cudaError_t launch_scan(const void* fn, const void* wide, ScanParams& p, int elem,
+// 6.0 TB/s: a lone block's copies lie beneath its arithmetic and the longer one
+// counts, a cluster's blocks wait for each other's (the cubes add up).  Many channels
+// fill the GPU with lone or small blocks; few channels need long steps, because what a
+// step costs grows less than its warps.  Measured, bf16, forward and backward in us:
+//   16,384 tokens of 8192 channels: 4 warps, C = 1 213, 362; C = 3 164, 241; C = 4
+//     200, 292; 12 warps, C = 1 151, 235; C = 2 197, 281
+//   the same in 12 packed sequences: 4 warps, C = 3 190, 276; 12, C = 1 171, 263
+//   8 rows of 2048 of 8192: 4 warps, C = 1 138, 236; C = 2 151, 236; 12, C = 1 149, 238
+//   16,384 of 1024: 4 warps, C = 16 39, 55; 8, C = 12 51, 67; 12, C = 6 40, 55
+//   65,537 of 512: 4 warps, C = 16 114, 162; 8, C = 12 89, 117; 12, C = 12 78, 107
+cudaError_t launch_scan(const ScanKernels& kernels, ScanParams& p, int elem,
                         const ScanCost& cost, void** args, cudaStream_t st) {
   const int64_t runs = (p.s + kScanRun - 1) / kScanRun;
   const int64_t units = static_cast<int64_t>(p.slabs) * p.t * p.b;
   static const int kClusters[] = {1, 2, 3, 4, 6, 8, 12, kScanMaxCluster};
   int few = 1;
   while (few < kScanWarps && few < runs) few *= 2;
-  const int blocks[] = {few, 8, kScanWideWarps};
+  const struct {
+    const void* kernel;
+    int warps, most;       // blocks of a cluster, at most
+    double slower;
+  } choices[] = {{kernels.fn, few, kScanMaxCluster, 1.0},
+                 {kernels.more, few, 1, 1.1},
+                 {kernels.wide, 8, kScanMaxCluster, 1.0},
+                 {kernels.wide, kScanWideWarps, kScanMaxCluster, 1.0}};
   double best = 0;
   size_t smem = 0;
   int threads = 0;
-  for (const int warps : blocks) {
-    if (warps > kScanWarps && runs <= kScanWarps) break;
-    const void* kernel = warps > kScanWarps ? wide : fn;
+  const void* chosen = nullptr;
+  for (const auto& k : choices) {
+    const int warps = k.warps;
+    if (k.kernel == nullptr || (warps > kScanWarps && runs <= kScanWarps)) continue;
     for (const int c : kClusters) {
-      if (c > 1 && static_cast<int64_t>(c - 1) * warps >= runs) break;
+      if (c > k.most || (c > 1 && static_cast<int64_t>(c - 1) * warps >= runs)) break;
       const size_t need = scan_smem(elem, cost.tensors, warps, c);
       if (need > kScanMaxShared) break;
       const double bytes = static_cast<double>(c) * warps * kScanRun * kScanChannels * elem *
@@ -247,12 +257,13 @@ cudaError_t launch_scan(const void* fn, const void* wide, ScanParams& p, int ele
       const double start = c == 1 ? 2.0 : 3.0;    // a wave's launch and first rows
       auto wave = [&](int64_t clusters) {
         const double moved = static_cast<double>(clusters) * bytes / 6.0e6;
-        return start + static_cast<double>(steps) *
-                           std::cbrt(least * least * least + moved * moved * moved);
+        return start + k.slower * static_cast<double>(steps) *
+                           (c == 1 ? (least > moved ? least : moved)
+                                   : std::cbrt(least * least * least + moved * moved * moved));
       };
       if (smem != 0 && wave(0) >= best) continue;
       int fit = 0;
-      const cudaError_t e = max_clusters(kernel, 32 * warps, need, c, &fit);
+      const cudaError_t e = max_clusters(k.kernel, 32 * warps, need, c, &fit);
       if (e != cudaSuccess) return e;
       if (fit < 1) continue;
       const double time = static_cast<double>(units / fit) * wave(fit) +
@@ -261,14 +272,14 @@ cudaError_t launch_scan(const void* fn, const void* wide, ScanParams& p, int ele
         best = time;
         smem = need;
         threads = 32 * warps;
+        chosen = k.kernel;
         p.cluster = c;
       }
     }
   }
   if (smem == 0 || units * p.cluster > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl(threads > 32 * kScanWarps ? wide : fn,
-                    dim3(static_cast<unsigned>(units * p.cluster)), dim3(threads), smem, args, st,
-                    p.cluster);
+  return launch_pdl(chosen, dim3(static_cast<unsigned>(units * p.cluster)), dim3(threads), smem,
+                    args, st, p.cluster);
 }
 
 cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st) {
@@ -283,10 +294,12 @@ cudaError_t launch_scan_fwd(ScanParams p, int dtype, cudaStream_t st) {
     return launch_pdl(fn, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(128), 0,
                       args, st);
   }
-  const void* fn = scan_fwd_fn<false>(dtype, p.tied, packed);
-  const void* wide = scan_fwd_fn<true>(dtype, p.tied, packed);
-  const ScanCost cost{0.66, 0.85, 0.06, 0.085, 2, 3};
-  return launch_scan(fn, wide, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
+  const ScanKernels kernels = dtype == SP_BF16  ? scan_fwd_kernels<SP_BF16>(p.tied, packed)
+                              : dtype == SP_F16 ? scan_fwd_kernels<SP_F16>(p.tied, packed)
+                                                : scan_fwd_kernels<SP_F32>(p.tied, packed);
+  const ScanCost cost = dtype == SP_F32 ? ScanCost{0.2, 0.53, 0.03, 0.19, 2, 3}
+                                        : ScanCost{0.26, 0.64, 0.038, 0.125, 2, 3};
+  return launch_scan(kernels, p, dtype == SP_F32 ? 4 : 2, cost, args, st);
 }
 
 }  // namespace spb
