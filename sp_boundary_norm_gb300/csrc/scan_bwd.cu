@@ -14,8 +14,8 @@
 
 namespace spb {
 
-// Blocks an SM that the registers are held to (16,384 tokens x 8 ranks of 1024
-// channels: three 235 us, two 262, four, with spilled registers, 377).
+// Blocks an SM that the registers are held to (8 ranks of 8 rows of 2048 tokens x 1024
+// channels: three 235 us, two 256, four, with spilled registers, 317).
 constexpr int kBwdBlocks = 3;
 
 // The run's factors, from its rows in shared memory: e = exp(-gate), from which the
