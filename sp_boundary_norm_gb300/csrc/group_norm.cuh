@@ -20,14 +20,14 @@
 //    copies beneath the stores 57 and 107.)
 // Measured on a GB300, bf16, LayerNorm and SiLU, forward and backward (the floor
 // is the time of x, y and dy, dx at the measured copy rate, 6.8 TB/s):
-//   rows: 16,384 of 8 ranks' 8 groups of 128, RMS 93 and 158 us (floor 79, 119),
+//   rows: 16,384 of 8 ranks' 8 groups of 128, RMS 93 and 159 us (floor 79, 119),
 //     bound by the arithmetic's latency at two blocks an SM, two thirds of the
 //     issue slots taken;
 //   tiles: 16,384 samples of 4 rows of 512 50 and 61 (20, 30), bound by the
 //     barriers around each tile's sums;
-//   held: 1365 samples of 48 rows of 512 39 and 71 (20, 30), bound by the time from
+//   held: 1365 samples of 48 rows of 512 39 and 72 (20, 30), bound by the time from
 //     a sample's loads to its stores;
-//   units: 8 samples of 4096 x 1280 45 and 78 (25, 37): the second reading, from
+//   units: 8 samples of 4096 x 1280 45 and 80 (25, 37): the second reading, from
 //     L2, and the joins add what is above the floor.
 // Sums run in a fixed order: results do not depend on timing.  Statistics are
 // two-pass (of values held in registers) and joined as (count, mean, M2), so a
