@@ -437,3 +437,37 @@ def test_rope_around_the_chunk_rule(t, heads, d, layout, dtype, s):
         # under 8 units of 2^-24, as for the other rotary tests
         within(y[r][:, at], want, 2.0 ** -21 * mag, f"rank {r}")
         assert torch.isfinite(y[r]).all()
+
+
+# ------------------------------------------------------------ the widest calls --
+
+@pytest.mark.parametrize("t,heads,d,rot", [(16, 4096, 8, 8), (16, 4095, 10, 4), (1, 1, 16384, 512)])
+def test_rope_most_heads_and_widest(t, heads, d, rot):
+    gen = torch.Generator().manual_seed(7)
+    x = [rand((1, 3, heads, d), gen, BF) for _ in range(t)]
+    y = empties(x[0], t)
+    sp.sp_rope_fwd(x, sp.sp_rope_table(rot), layout="interleaved", y=y)
+    for r in range(t):
+        want, mag = orc.rope(f64(x[r]), orc.positions(1, 3), orc.frequencies(rot), "interleaved")
+        within(y[r], want, 2.0 ** -21 * mag, f"rank {r}")
+
+
+@pytest.mark.parametrize("lens", [None, [0] * 3000 + [1, 0, 38] + [0] * 5000])
+def test_scan_most_channels_and_many_empty_sequences(lens):
+    cu_np, cu = (None, None) if lens is None else offsets(lens)
+    n, s, c = 1 if lens is None else len(lens), 39, 16384 if lens is None else 72
+    gen = torch.Generator().manual_seed(8)
+    mk = lambda shape, dt: [rand(shape, gen, dt) for _ in range(2)]
+    gate, value, dy = mk((1, s, c), BF), mk((1, s, c), BF), mk((1, s, c), BF)
+    h0, dhT = mk((n, c), F32), mk((n, c), F32)
+    o = run_scan(gate, value, dy, h0, dhT, True, cu)
+    for r in range(2):
+        w = scan_exact(f64(gate[r]), f64(value[r]), f64(h0[r]), True, cu_np, BF, f64(dy[r]), f64(dhT[r]))
+        for name, got in o.items():
+            within(got[r], w[name], w[name + "_"], f"{name}[{r}]")
+
+
+@pytest.mark.parametrize("n,l,groups", [(5, 1, 2048), (3, 9, 2048), (2, 300, 4), (70, 2, 16)])
+def test_group_norm_most_channels(n, l, groups):
+    i = norm_inputs(2, n, l, 16384, FP, 55)
+    check_norm(i, run_norm(i, groups, "layernorm", "silu"), groups, "layernorm", "silu")
