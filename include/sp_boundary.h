@@ -406,7 +406,19 @@ typedef enum sp_rope_scaling {
                                 fast pairs stay, slow ones are squeezed */
 } sp_rope_scaling_t;
 
+typedef enum sp_rope_order {
+  SP_ROPE_BLOCKS = 0,        /* the pairs of the first axis, then those of the next, ... */
+  SP_ROPE_CYCLIC = 1         /* pair by pair, the axes in turn; one that has all of its
+                                pairs is passed over */
+} sp_rope_order_t;
+
+typedef enum sp_rope_frequencies {
+  SP_ROPE_SHARED = 0,        /* pair i of the head: w_i = base^(-i / pairs), whatever its axis */
+  SP_ROPE_OWN = 1            /* the j-th pair of axis k: base^(-j / sections[k]) */
+} sp_rope_frequencies_t;
+
 #define SP_ROPE_MAX_PAIRS 256
+#define SP_ROPE_MAX_AXES 8
 #define SP_ROPE_MAX_HEADS 4096
 #define SP_MAX_GROUP_CHANNELS 4096
 
@@ -416,6 +428,14 @@ typedef struct sp_rope_table {
   float mscale;                         /* factor on cosine and sine */
   uint64_t turns[SP_ROPE_MAX_PAIRS];    /* turns per position, in units of 2^-64 */
 } sp_rope_table_t;
+
+/* The same for tokens with several coordinates, filled by sp_rope_axes_table. */
+typedef struct sp_rope_axes_table {
+  int32_t pairs, axes;
+  float mscale;
+  uint8_t axis[SP_ROPE_MAX_PAIRS];      /* the axis that a pair follows */
+  uint64_t turns[SP_ROPE_MAX_PAIRS];
+} sp_rope_axes_table_t;
 
 /*
  * sp_rope_table -- frequencies of rotary positions, on the host.  Nothing is
@@ -457,6 +477,39 @@ sp_status_t sp_rope_bwd(const void* const* dy, int64_t dy_ld, int64_t dy_head, i
                         const int64_t* positions, int64_t first_position,
                         const int32_t* cu_seqlens, int32_t n_seqs, void* const* dx, int64_t dx_ld,
                         int64_t dx_head, int32_t* dev_status, void* stream);
+
+/*
+ * sp_rope_axes_table -- rotary positions with a coordinate for each of `axes` axes
+ * (time, height, width, ...), on the host.  Nothing is enqueued.
+ *
+ * sections    [axes]: pairs of a head that follow each axis, >= 1; in all at most
+ *             SP_ROPE_MAX_PAIRS
+ * base        >= 1; `order` and `frequencies` say which pair is whose and how fast
+ * factors     [axes] or NULL: an axis' coordinates count 1 / factor as much; >= 1
+ * mscale      factor on cosine and sine
+ */
+sp_status_t sp_rope_axes_table(const int32_t* sections, int32_t axes, double base,
+                               sp_rope_order_t order, sp_rope_frequencies_t frequencies,
+                               const double* factors, double mscale, sp_rope_axes_table_t* out);
+
+/*
+ * sp_rope_axes_fwd -- rotary positions with several axes: as sp_rope_fwd, but a
+ * pair's x = coordinate on its axis * w_i.
+ *
+ * positions   device int64 (axes, b, s): every token's coordinates, of any sign
+ */
+sp_status_t sp_rope_axes_fwd(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b,
+                             int64_t s, int64_t heads, int64_t d, int32_t t, sp_dtype_t dtype,
+                             const sp_rope_axes_table_t* table, sp_rope_layout_t layout,
+                             const int64_t* positions, void* const* y, int64_t y_ld,
+                             int64_t y_head, void* stream);
+
+/* sp_rope_axes_bwd -- the transpose: x is dy, y is dx, the rotation goes back. */
+sp_status_t sp_rope_axes_bwd(const void* const* dy, int64_t dy_ld, int64_t dy_head, int64_t b,
+                             int64_t s, int64_t heads, int64_t d, int32_t t, sp_dtype_t dtype,
+                             const sp_rope_axes_table_t* table, sp_rope_layout_t layout,
+                             const int64_t* positions, void* const* dx, int64_t dx_ld,
+                             int64_t dx_head, void* stream);
 
 /*
  * sp_gated_scan_fwd -- gated linear recurrence along every sequence, each
@@ -547,6 +600,120 @@ sp_status_t sp_group_norm_bwd(const void* const* dy, int64_t dy_ld, const void* 
                               sp_act_t act, void* const* dx, int64_t dx_ld, float* dgamma,
                               float* dbeta, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * sp_causal_conv_fwd -- a short causal convolution along every sequence, each channel
+ * on its own:
+ *   y[i] = act(bias + sum_j weight[j] x[i - (width - 1) + j]),  j = 0 .. width - 1
+ * where the width - 1 inputs before a sequence's first are its state x0 (0 without).
+ *
+ * x, y     [t] (b, s, c)             c a multiple of 8, at most SP_MAX_HIDDEN
+ * weight   (t * c, width)            rank r's at r * c; width 2, 3 or 4
+ * bias     (t * c) or NULL
+ * x0, xT   [t] (n, width - 1, c) of x's type, or NULL arrays: the last inputs before
+ *          each sequence and at its end, oldest first, n = n_seqs or b; xT[r] == x0[r]
+ *          is allowed (a sequence without tokens: xT = x0)
+ * s == 1 without cu_seqlens is a decoding step of b sequences.
+ */
+sp_status_t sp_causal_conv_fwd(const void* const* x, int64_t x_ld, const void* weight,
+                               const void* bias, const void* const* x0, int64_t b, int64_t s,
+                               int64_t c, int32_t width, int32_t t, sp_dtype_t dtype, sp_act_t act,
+                               const int32_t* cu_seqlens, int32_t n_seqs, void* const* y,
+                               int64_t y_ld, void* const* xT, int32_t* dev_status, void* stream);
+
+/* Bytes of the workspace of sp_causal_conv_bwd on the current device (0 for an
+ * invalid shape). */
+size_t sp_causal_conv_bwd_workspace_bytes(int64_t b, int64_t s, int64_t c, int32_t width,
+                                          int32_t t, sp_dtype_t dtype);
+
+/*
+ * sp_causal_conv_bwd -- gradients of sp_causal_conv_fwd called with the same x, weight,
+ * bias, x0 and shape.  (Where xT was written over x0, x0 here is a copy of what it held
+ * before.)
+ *
+ * dy       [t] (b, s, c)             gradient of y
+ * dxT      [t] (n, width - 1, c)     gradient of xT, or a NULL array (zero)
+ * dx       [t] (b, s, c)             output
+ * dx0      [t] (n, width - 1, c)     output or a NULL array (dxT may not be the same buffer)
+ * dweight  (t * c, width) float32, dbias (t * c) float32: outputs, each may be NULL
+ * workspace                          device scratch of the size above (may be NULL if
+ *                                    neither parameter gradient is wanted); one for each
+ *                                    call that may run at the same time
+ */
+sp_status_t sp_causal_conv_bwd(const void* const* x, int64_t x_ld, const void* weight,
+                               const void* bias, const void* const* x0, const void* const* dy,
+                               int64_t dy_ld, const void* const* dxT, int64_t b, int64_t s,
+                               int64_t c, int32_t width, int32_t t, sp_dtype_t dtype, sp_act_t act,
+                               const int32_t* cu_seqlens, int32_t n_seqs, void* const* dx,
+                               int64_t dx_ld, void* const* dx0, float* dweight, float* dbias,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                               void* stream);
+
+/*
+ * Selective state space scan.  Every channel has `n` states (8, 16, 32 or 64); the
+ * channels of a group share B and C:
+ *   d[i] = softplus(dt[i] + dt_bias)     (softplus == 0: dt[i] + dt_bias)
+ *   h[i][j] = exp(d[i] A[j]) h[i-1][j] + d[i] u[i] B[i][j],   h[-1] = h0 of the sequence
+ *   y[i] = (sum_j C[i][j] h[i][j] + D u[i]) z[i] sigmoid(z[i])
+ *
+ * u, dt, z, y [t] (b, s, c)         c / groups a multiple of 8; z: NULL array for no gate
+ * B, C        [t] (b, s, groups * n)   ranks may share a buffer
+ * A           (t * c, n) float32, finite: rank r's at r * c; decaying for A < 0
+ * D, dt_bias  (t * c) float32 or NULL (zero)
+ * h0, hT      [t] (m, c, n) float32 or NULL arrays: the states before and after each
+ *             sequence (0 without h0), m = n_seqs or b; hT[r] == h0[r] is allowed
+ *             (a sequence without tokens: hT = h0)
+ * states      [t] (b, ceil(s / 16), c, n) float32 or a NULL array: the states the
+ *             backward starts from (output); their contents are internal
+ * workspace   device scratch of the size that the function below gives on the current
+ *             device (0 where none is needed: it may be NULL then); one for each call
+ *             that may run at the same time
+ * s == 1 without cu_seqlens is a decoding step of b sequences; it needs no workspace.
+ */
+size_t sp_selective_scan_fwd_workspace_bytes(int64_t b, int64_t s, int64_t c, int32_t n,
+                                             int32_t groups, int32_t t);
+
+sp_status_t sp_selective_scan_fwd(const void* const* u, int64_t u_ld, const void* const* dt,
+                                  int64_t dt_ld, const float* A, const void* const* B,
+                                  int64_t B_ld, const void* const* C, int64_t C_ld, const float* D,
+                                  const void* const* z, int64_t z_ld, const float* dt_bias,
+                                  int32_t softplus, const float* const* h0, int64_t b, int64_t s,
+                                  int64_t c, int32_t n, int32_t groups, int32_t t,
+                                  sp_dtype_t dtype, const int32_t* cu_seqlens, int32_t n_seqs,
+                                  void* const* y, int64_t y_ld, float* const* hT,
+                                  float* const* states, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_status, void* stream);
+
+size_t sp_selective_scan_bwd_workspace_bytes(int64_t b, int64_t s, int64_t c, int32_t n,
+                                             int32_t groups, int32_t t);
+
+/*
+ * sp_selective_scan_bwd -- gradients of sp_selective_scan_fwd called with the same
+ * inputs and shape, from the states it saved.  (Where hT was written over h0, h0 here
+ * is a copy of what it held before.)
+ *
+ * dy                       [t] (b, s, c)            gradient of y
+ * dhT                      [t] (m, c, n) float32    gradient of hT, or a NULL array (zero)
+ * du, ddt, dz              [t] (b, s, c)            outputs (dz: with z, else NULL)
+ * dB, dC                   [t] (b, s, groups * n)   outputs: each rank's own
+ * dA (t * c, n), dD (t * c), ddt_bias (t * c) float32: outputs, each may be NULL
+ * dh0                      [t] (m, c, n) float32    output or a NULL array (dhT may not be
+ *                                                   the same buffer)
+ */
+sp_status_t sp_selective_scan_bwd(const void* const* u, int64_t u_ld, const void* const* dt,
+                                  int64_t dt_ld, const float* A, const void* const* B,
+                                  int64_t B_ld, const void* const* C, int64_t C_ld, const float* D,
+                                  const void* const* z, int64_t z_ld, const float* dt_bias,
+                                  int32_t softplus, const float* const* h0,
+                                  const float* const* states, const void* const* dy, int64_t dy_ld,
+                                  const float* const* dhT, int64_t b, int64_t s, int64_t c,
+                                  int32_t n, int32_t groups, int32_t t, sp_dtype_t dtype,
+                                  const int32_t* cu_seqlens, int32_t n_seqs, void* const* du,
+                                  int64_t du_ld, void* const* ddt, int64_t ddt_ld, void* const* dB,
+                                  int64_t dB_ld, void* const* dC, int64_t dC_ld, void* const* dz,
+                                  int64_t dz_ld, float* dA, float* dD, float* ddt_bias,
+                                  float* const* dh0, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_status, void* stream);
 
 /* Thread-local text of the last non-OK status returned on this thread. */
 const char* sp_last_error(void);

@@ -34,13 +34,21 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ACTS = {"none": 0, "silu": 1}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
-SCAN_RUN = 16               # tokens per saved state of the gated recurrence
+ROPE_ORDERS = {"blocks": 0, "cyclic": 1}
+ROPE_FREQUENCIES = {"shared": 0, "own": 1}
+SCAN_RUN = 16               # tokens per saved state of the recurrences
 
 
 class RopeTable(ctypes.Structure):
     """Frequencies of a head's rotated pairs, made by sp_rope_table."""
     _fields_ = [("pairs", ctypes.c_int32), ("mscale", ctypes.c_float),
                 ("turns", ctypes.c_uint64 * 256)]
+
+
+class RopeAxesTable(ctypes.Structure):
+    """The same for tokens with several coordinates, made by sp_rope_axes_table."""
+    _fields_ = [("pairs", ctypes.c_int32), ("axes", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("axis", ctypes.c_uint8 * 256), ("turns", ctypes.c_uint64 * 256)]
 
 
 class SpError(RuntimeError):
@@ -121,6 +129,37 @@ def load():
     lib.sp_group_norm_bwd.argtypes = [
         _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _i32,
         _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    axes = ctypes.POINTER(RopeAxesTable)
+    lib.sp_rope_axes_table.restype = _i32
+    lib.sp_rope_axes_table.argtypes = [
+        ctypes.POINTER(_i32), _i32, ctypes.c_double, _i32, _i32, ctypes.POINTER(ctypes.c_double),
+        ctypes.c_double, axes]
+    for fn in (lib.sp_rope_axes_fwd, lib.sp_rope_axes_bwd):
+        fn.restype = _i32
+        fn.argtypes = [_vp, _i64, _i64, _i64, _i64, _i64, _i64, _i32, _i32, axes, _i32, _vp, _vp,
+                       _i64, _i64, _vp]
+    lib.sp_causal_conv_fwd.restype = _i32
+    lib.sp_causal_conv_fwd.argtypes = [
+        _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i64,
+        _vp, _vp, _vp]
+    lib.sp_causal_conv_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.sp_causal_conv_bwd_workspace_bytes.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32]
+    lib.sp_causal_conv_bwd.restype = _i32
+    lib.sp_causal_conv_bwd.argtypes = [
+        _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp,
+        _i32, _vp, _i64, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+    for fn in (lib.sp_selective_scan_fwd_workspace_bytes,
+               lib.sp_selective_scan_bwd_workspace_bytes):
+        fn.restype = ctypes.c_size_t
+        fn.argtypes = [_i64, _i64, _i64, _i32, _i32, _i32]
+    inputs = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp]
+    shape = [_i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i32]
+    lib.sp_selective_scan_fwd.restype = _i32
+    lib.sp_selective_scan_fwd.argtypes = inputs + shape + [
+        _vp, _i64, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+    lib.sp_selective_scan_bwd.restype = _i32
+    lib.sp_selective_scan_bwd.argtypes = inputs + [_vp, _vp, _i64, _vp] + shape + (
+        [_vp, _i64] * 5) + [_vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, _vp]
     lib.sp_last_error.restype = ctypes.c_char_p
     lib.sp_last_error.argtypes = []
     lib.sp_abi_version.restype = _i32
@@ -616,7 +655,10 @@ def _quick():
         spec.loader.exec_module(module)
         if hasattr(torch._C, "_cuda_getCurrentRawStream"):
             entries = (lib.sp_rope_fwd, lib.sp_rope_bwd, lib.sp_gated_scan_fwd,
-                       lib.sp_gated_scan_bwd, lib.sp_group_norm_fwd, lib.sp_group_norm_bwd)
+                       lib.sp_gated_scan_bwd, lib.sp_group_norm_fwd, lib.sp_group_norm_bwd,
+                       lib.sp_rope_axes_fwd, lib.sp_rope_axes_bwd, lib.sp_causal_conv_fwd,
+                       lib.sp_causal_conv_bwd, lib.sp_selective_scan_fwd,
+                       lib.sp_selective_scan_bwd)
             module.setup(tuple(ctypes.cast(e, _vp).value for e in entries),
                          torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
         _module = module
@@ -627,27 +669,32 @@ def _pointers(xs):
     return (_vp * len(xs))(*[x.data_ptr() for x in xs])
 
 
-def _rank_buffers(xs, x0, t, what):
-    """Checks that xs are t buffers of x0's shape, type and device, one by one."""
+def _rank_buffers(xs, x0, t, what, shape=None):
+    """Checks that xs are t buffers of x0's shape (or the one given), type and device, one
+    by one."""
+    shape = x0.shape if shape is None else shape
     if len(xs) != t:
         raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
     for i, x in enumerate(xs):
         if not isinstance(x, torch.Tensor):
             raise TypeError(f"{what}[{i}] must be a torch.Tensor")
-        if x.shape != x0.shape:
-            raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(x0.shape)}")
+        if tuple(x.shape) != tuple(shape):
+            raise ValueError(f"{what}[{i}]: shape {tuple(x.shape)} != {tuple(shape)}")
         if x.dtype is not x0.dtype:
             raise ValueError(f"{what}[{i}]: dtype {x.dtype} != {x0.dtype}")
         if x.device != x0.device:
             raise ValueError(f"{what}[{i}]: on {x.device}, expected {x0.device}")
 
 
-def _rank_rows(x0, t, **lists):
+def _rank_rows(x0, t, shape=None, **lists):
     """Pointer array and row stride of each list of t rank buffers, which are of x0's
-    shape, type and device."""
+    shape (or the one given), type and device (None: no array)."""
     out = []
     for what, xs in lists.items():
-        _rank_buffers(xs, x0, t, what)
+        if xs is None:
+            out += [None, 0]
+            continue
+        _rank_buffers(xs, x0, t, what, shape)
         lds = [_row_stride(x.shape, x.stride(), what) for x in xs]
         if any(ld != lds[0] for ld in lds):
             raise ValueError(f"{what}: every rank needs the same row stride")
@@ -655,8 +702,9 @@ def _rank_rows(x0, t, **lists):
     return out
 
 
-def _rank_floats(x0, t, shape, **lists):
-    """Pointer array of each list of t dense float32 rank buffers (None: no array)."""
+def _rank_floats(x0, t, shape, dtype=torch.float32, /, **lists):
+    """Pointer array of each list of t dense rank buffers, float32 or of the type given
+    (None: no array)."""
     out = []
     for what, xs in lists.items():
         if xs is None:
@@ -665,16 +713,17 @@ def _rank_floats(x0, t, shape, **lists):
         if len(xs) != t:
             raise ValueError(f"{what}: {len(xs)} ranks, expected {t}")
         for i, x in enumerate(xs):
-            _need(x, shape, torch.float32, x0.device, f"{what}[{i}]")
+            _need(x, shape, dtype, x0.device, f"{what}[{i}]")
         out.append(_pointers(xs))
     return out
 
 
-def _params(x0, n, **vectors):
-    """Address of each contiguous vector of n elements of x0's type (None: none)."""
+def _params(x0, n, dtype=None, **vectors):
+    """Address of each contiguous vector of n elements (or tensor of shape n) of x0's type,
+    or the one given (None: none)."""
     for what, v in vectors.items():
         if v is not None:
-            _need(v, (n,), x0.dtype, x0.device, what)
+            _need(v, n if isinstance(n, tuple) else (n,), dtype or x0.dtype, x0.device, what)
     return [_ptr(v) for v in vectors.values()]
 
 
@@ -807,6 +856,228 @@ def sp_rope_bwd(dy, table, *, layout="half", positions=None, first_position=0, c
                 dx, status=None):
     """Gradient of sp_rope_fwd (dx may be dy)."""
     _rope_call("sp_rope_bwd", dy, table, layout, positions, first_position, cu_seqlens, dx, status)
+
+
+def sp_rope_axes_table(sections, *, base=10000.0, order="blocks", frequencies="shared",
+                       factors=None, mscale=1.0):
+    """Frequencies of rotary positions with several axes (kept by the caller, one per
+    model).  sections: pairs of a head that follow each axis, so 2 * sum(sections) elements
+    turn.  order: "blocks" (the first axis' pairs, then the next one's) or "cyclic" (pair by
+    pair, an axis that has all of its pairs is passed over).  frequencies: "shared" (pair i
+    of the head turns base^(-i / pairs) a position) or "own" (the j-th pair of axis k
+    base^(-j / sections[k])).  factors: per axis, what its coordinates are divided by;
+    mscale multiplies cosine and sine."""
+    sections = [int(n) for n in sections]
+    if factors is not None and len(factors) != len(sections):
+        raise ValueError(f"factors: {len(factors)} axes, expected {len(sections)}")
+    out = RopeAxesTable()
+    n = len(sections)
+    _check(load().sp_rope_axes_table(
+        (_i32 * n)(*sections), n, float(base), _choice(ROPE_ORDERS, order, "order"),
+        _choice(ROPE_FREQUENCIES, frequencies, "frequencies"),
+        None if factors is None else (ctypes.c_double * n)(*[float(f) for f in factors]),
+        float(mscale), ctypes.byref(out)))
+    return out
+
+
+def _rope_axes_call(entry, x, table, layout, positions, y):
+    if type(table) is RopeAxesTable:
+        code = _quick().rope_axes(entry == "sp_rope_axes_bwd", x, ctypes.addressof(table),
+                                  ROPE_LAYOUTS.get(layout), positions, table.axes, y)
+        if code is not None:
+            return _check(code)
+    lib = load()
+    t, x0, dt = _first(x, 4, "x")
+    b, s, heads, d = x0.shape
+    dev = x0.device
+    if not isinstance(table, RopeAxesTable):
+        raise TypeError("table must come from sp_rope_axes_table")
+    xa, x_ld, x_head, ya, y_ld, y_head = _rank_heads(x0, t, x=x, y=y)
+    if not isinstance(positions, torch.Tensor):
+        raise TypeError("positions must be a torch.Tensor")
+    _need(positions, (table.axes, b, s), torch.int64, dev, "positions")
+    _call(dev, getattr(lib, entry), xa, x_ld, x_head, b, s, heads, d, t, dt, ctypes.byref(table),
+          _choice(ROPE_LAYOUTS, layout, "layout"), _ptr(positions), ya, y_ld, y_head)
+
+
+def sp_rope_axes_fwd(x, table, *, layout="half", positions, y):
+    """Rotary positions with several axes (see sp_rope_fwd for the buffers): positions is
+    int64 (axes, b, s), every token's coordinates."""
+    _rope_axes_call("sp_rope_axes_fwd", x, table, layout, positions, y)
+
+
+def sp_rope_axes_bwd(dy, table, *, layout="half", positions, dx):
+    """Gradient of sp_rope_axes_fwd (dx may be dy)."""
+    _rope_axes_call("sp_rope_axes_bwd", dy, table, layout, positions, dx)
+
+
+def _scratch(workspace, dev):
+    """Address and bytes of a workspace (None: none)."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def sp_causal_conv_fwd(x, weight, bias=None, *, act="none", x0=None, cu_seqlens=None, y, xT=None,
+                       status=None):
+    """Short causal convolution along s of (b, s, c) rank buffers, channel by channel:
+    y[i] = act(bias + sum_j weight[:, j] x[i - (width - 1) + j]).  weight: (t * c, width),
+    width 2 to 4; bias: (t * c).  x0, xT: (sequences, width - 1, c) of x's type, the inputs
+    before each sequence and its last ones (xT may be x0)."""
+    code = _quick().conv_fwd(x, weight, bias, ACTS.get(act), x0, cu_seqlens, y, xT, status)
+    if code is not None:
+        return _check(code)
+    lib = load()
+    t, first, dt = _first(x, 3, "x")
+    b, s, c = first.shape
+    dev = first.device
+    xa, x_ld, ya, y_ld = _rank_rows(first, t, x=x, y=y)
+    width = _width(weight)
+    wp, = _params(first, (t * c, width), weight=weight)
+    bp, = _params(first, t * c, bias=bias)
+    cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
+    n = b if cu is None else n_seqs
+    x0a, xTa = _rank_floats(first, t, (n, width - 1, c), first.dtype, x0=x0, xT=xT)
+    st = _status_word(dev, status)
+    _call(dev, lib.sp_causal_conv_fwd, xa, x_ld, wp, bp, x0a, b, s, c, width, t, dt,
+          _choice(ACTS, act, "act"), cu, n_seqs, ya, y_ld, xTa, st)
+
+
+def _width(weight):
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise TypeError("weight must be a (t * c, width) torch.Tensor")
+    return weight.shape[1]
+
+
+def sp_causal_conv_bwd_workspace_bytes(b, s, c, width, t, dtype=torch.bfloat16):
+    """Bytes of sp_causal_conv_bwd's workspace on the current device."""
+    return int(load().sp_causal_conv_bwd_workspace_bytes(b, s, c, width, t, DTYPES[dtype]))
+
+
+def sp_causal_conv_bwd(x, weight, bias, dy, *, act="none", x0=None, cu_seqlens=None, dxT=None, dx,
+                       dx0=None, dweight=None, dbias=None, workspace=None, status=None):
+    """Gradients of sp_causal_conv_fwd (same x, weight, bias, x0, cu_seqlens) from its
+    input; dxT: gradient of xT, dx0: gradient of x0; dweight, dbias: float32 (these need the
+    workspace of sp_causal_conv_bwd_workspace_bytes, one per call that may run at the same
+    time)."""
+    code = _quick().conv_bwd(x, weight, bias, ACTS.get(act), x0, cu_seqlens, dy, dxT, dx, dx0,
+                             dweight, dbias, workspace, status)
+    if code is not None:
+        return _check(code)
+    lib = load()
+    t, first, dt = _first(x, 3, "x")
+    b, s, c = first.shape
+    dev = first.device
+    xa, x_ld, da, d_ld, oa, o_ld = _rank_rows(first, t, x=x, dy=dy, dx=dx)
+    width = _width(weight)
+    wp, = _params(first, (t * c, width), weight=weight)
+    bp, = _params(first, t * c, bias=bias)
+    gw, = _params(first, (t * c, width), torch.float32, dweight=dweight)
+    gb, = _params(first, t * c, torch.float32, dbias=dbias)
+    cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
+    n = b if cu is None else n_seqs
+    x0a, dTa, d0a = _rank_floats(first, t, (n, width - 1, c), first.dtype, x0=x0, dxT=dxT, dx0=dx0)
+    ws, size = _scratch(workspace, dev)
+    st = _status_word(dev, status)
+    _call(dev, lib.sp_causal_conv_bwd, xa, x_ld, wp, bp, x0a, da, d_ld, dTa, b, s, c, width, t, dt,
+          _choice(ACTS, act, "act"), cu, n_seqs, oa, o_ld, d0a, gw, gb, ws, size, st)
+
+
+def sp_selective_scan_states_shape(b, s, c, n):
+    """Shape of one rank's float32 states buffer of sp_selective_scan_fwd."""
+    return (b, (s + SCAN_RUN - 1) // SCAN_RUN, c, n)
+
+
+def sp_selective_scan_fwd_workspace_bytes(b, s, c, n, groups, t):
+    """Bytes of sp_selective_scan_fwd's workspace on the current device (0: none needed)."""
+    return int(load().sp_selective_scan_fwd_workspace_bytes(b, s, c, n, groups, t))
+
+
+def sp_selective_scan_bwd_workspace_bytes(b, s, c, n, groups, t):
+    """Bytes of sp_selective_scan_bwd's workspace on the current device."""
+    return int(load().sp_selective_scan_bwd_workspace_bytes(b, s, c, n, groups, t))
+
+
+def _selective_shape(u, A, B):
+    """Ranks, first buffer, dtype code, states, groups and the shape of B and C."""
+    t, u0, dt = _first(u, 3, "u")
+    b, s, c = u0.shape
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise TypeError("A must be a (t * c, n) torch.Tensor")
+    _, b0, _ = _first(B, 3, "B")
+    n, width = A.shape[1], b0.shape[2]
+    if n < 1 or width < n or width % n:
+        raise ValueError(f"B: rows of {width} are not whole groups of {n} states")
+    return t, u0, dt, n, width // n, (b, s, width)
+
+
+def sp_selective_scan_fwd(u, dt, A, B, C, *, D=None, z=None, dt_bias=None, softplus=True, h0=None,
+                          cu_seqlens=None, y, hT=None, states=None, workspace=None, status=None):
+    """Selective state space scan along s of (b, s, c) rank buffers; every channel has n
+    states, and the channels of a group share B and C:
+    d = softplus(dt + dt_bias), h = exp(d A) h + d u B, y = (sum of C h + D u) silu(z).
+    A: float32 (t * c, n); B, C: (b, s, groups * n) rank buffers; D, dt_bias: float32
+    (t * c); z: gates or None.  h0, hT: float32 (sequences, c, n) states before and after
+    each sequence (hT may be h0); states: sp_selective_scan_states_shape buffers that
+    sp_selective_scan_bwd needs; workspace: sp_selective_scan_fwd_workspace_bytes, one per
+    call that may run at the same time."""
+    code = _quick().ssm_fwd(u, dt, A, B, C, D, z, dt_bias, softplus, h0, cu_seqlens, y, hT, states,
+                            workspace, status)
+    if code is not None:
+        return _check(code)
+    lib = load()
+    t, u0, kind, n, groups, shared = _selective_shape(u, A, B)
+    b, s, c = u0.shape
+    dev = u0.device
+    ua, u_ld, da, d_ld, ya, y_ld, za, z_ld = _rank_rows(u0, t, u=u, dt=dt, y=y, z=z)
+    ba, b_ld, ca, c_ld = _rank_rows(u0, t, shared, B=B, C=C)
+    ap, = _params(u0, (t * c, n), torch.float32, A=A)
+    dp, bp = _params(u0, t * c, torch.float32, D=D, dt_bias=dt_bias)
+    cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
+    ha, ta = _rank_floats(u0, t, (b if cu is None else n_seqs, c, n), h0=h0, hT=hT)
+    sa, = _rank_floats(u0, t, sp_selective_scan_states_shape(b, s, c, n), states=states)
+    ws, size = _scratch(workspace, dev)
+    st = _status_word(dev, status)
+    _call(dev, lib.sp_selective_scan_fwd, ua, u_ld, da, d_ld, ap, ba, b_ld, ca, c_ld, dp, za, z_ld,
+          bp, int(bool(softplus)), ha, b, s, c, n, groups, t, kind, cu, n_seqs, ya, y_ld, ta, sa,
+          ws, size, st)
+
+
+def sp_selective_scan_bwd(u, dt, A, B, C, states, dy, *, D=None, z=None, dt_bias=None,
+                          softplus=True, h0=None, cu_seqlens=None, dhT=None, du, ddt, dB, dC,
+                          dz=None, dA=None, dD=None, ddt_bias=None, dh0=None, workspace=None,
+                          status=None):
+    """Gradients of sp_selective_scan_fwd (same inputs) from the states it saved; dhT:
+    gradient of hT.  dz is needed with z; dA, dD, ddt_bias (float32) and dh0 may be left
+    out; dB and dC are each rank's own.  workspace: sp_selective_scan_bwd_workspace_bytes,
+    one per call that may run at the same time."""
+    code = _quick().ssm_bwd(u, dt, A, B, C, states, dy, D, z, dt_bias, softplus, h0, cu_seqlens,
+                            dhT, du, ddt, dB, dC, dz, dA, dD, ddt_bias, dh0, workspace, status)
+    if code is not None:
+        return _check(code)
+    lib = load()
+    t, u0, kind, n, groups, shared = _selective_shape(u, A, B)
+    b, s, c = u0.shape
+    dev = u0.device
+    if z is not None and dz is None:
+        raise ValueError("dz is required with z")
+    ua, u_ld, da, d_ld, ya, y_ld, za, z_ld = _rank_rows(u0, t, u=u, dt=dt, dy=dy, z=z)
+    gu, gu_ld, gd, gd_ld, gz, gz_ld = _rank_rows(u0, t, du=du, ddt=ddt,
+                                                 dz=None if z is None else dz)
+    ba, b_ld, ca, c_ld, gb, gb_ld, gc, gc_ld = _rank_rows(u0, t, shared, B=B, C=C, dB=dB, dC=dC)
+    ap, ga = _params(u0, (t * c, n), torch.float32, A=A, dA=dA)
+    dp, bp, gp, gbp = _params(u0, t * c, torch.float32, D=D, dt_bias=dt_bias, dD=dD,
+                              ddt_bias=ddt_bias)
+    cu, n_seqs = _seq_meta(cu_seqlens, b, dev)
+    ha, ta, oa = _rank_floats(u0, t, (b if cu is None else n_seqs, c, n), h0=h0, dhT=dhT, dh0=dh0)
+    sa, = _rank_floats(u0, t, sp_selective_scan_states_shape(b, s, c, n), states=states)
+    ws, size = _scratch(workspace, dev)
+    st = _status_word(dev, status)
+    _call(dev, lib.sp_selective_scan_bwd, ua, u_ld, da, d_ld, ap, ba, b_ld, ca, c_ld, dp, za, z_ld,
+          bp, int(bool(softplus)), ha, sa, ya, y_ld, ta, b, s, c, n, groups, t, kind, cu, n_seqs,
+          gu, gu_ld, gd, gd_ld, gb, gb_ld, gc, gc_ld, gz, gz_ld, ga, gp, gbp, oa, ws, size, st)
 
 
 def sp_gated_scan_states_shape(b, s, c):

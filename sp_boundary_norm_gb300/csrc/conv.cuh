@@ -1,0 +1,105 @@
+// Shared parts of the causal convolution along the tokens, each channel on its own:
+//   q[i] = bias + sum_j w[j] x[i - (W - 1) + j],   y[i] = act(q[i])
+// where inputs before a sequence's begin come from its state x0 (or are zero).
+#pragma once
+
+#include "region.cuh"
+
+namespace spb {
+
+constexpr int kConvThreads = 256;
+
+// The sequence that a thread's run is in: its number (states are found by it), first
+// token and end, all of one batch row.
+struct ConvSeq {
+  int id;
+  int64_t lo, hi;
+};
+template <bool PACKED>
+__device__ __forceinline__ ConvSeq conv_seq(const ConvParams& P, int64_t batch, int64_t tok) {
+  if constexpr (!PACKED) return ConvSeq{static_cast<int>(batch), 0, P.s};
+  ConvSeq q;
+  q.id = find_seq(P.cu_seqlens, P.n_seqs, tok);
+  const int64_t lo = __ldg(P.cu_seqlens + q.id), hi = __ldg(P.cu_seqlens + q.id + 1);
+  q.lo = lo < 0 ? 0 : lo > tok ? tok : lo;          // in bounds whatever cu holds
+  q.hi = hi > P.s || hi <= tok ? P.s : hi;
+  return q;
+}
+
+// Row of the state that stands for token `row` < q.lo.
+template <int W>
+__device__ __forceinline__ int state_row(const ConvSeq& q, int64_t row) {
+  const int64_t r = W - 1 + row - q.lo;
+  return r < 0 ? 0 : static_cast<int>(r);
+}
+
+// A lane's taps: for each the weights of its V channels, and its bias.
+template <int DT, int V, int W>
+struct Taps {
+  F2 w[W][V / 2], bias[V / 2];
+  __device__ __forceinline__ void load(const ConvParams& P, int64_t ch) {
+    constexpr int E = ElemSize<DT>::value;
+    float f[V * W];
+    Pack<DT, V * W> p;
+    constexpr int kPieces = sizeof(p.w) / 8;        // 8-byte pieces: V * W * E is a multiple
+    const char* src = P.weight + ch * W * E;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + i);
+      p.w[2 * i] = v.x;
+      p.w[2 * i + 1] = v.y;
+    }
+    unpack(p, f);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) w[j][k] = f2(f[2 * k * W + j], f[(2 * k + 1) * W + j]);
+    Pack<DT, V> q{};
+    if (P.bias != nullptr) load_pack(q, P.bias + ch * E);
+    unpack_pairs(q, bias);
+  }
+  // bias + the taps on the window (oldest first) and the token itself
+  __device__ __forceinline__ void apply(const F2 (&win)[W - 1][V / 2], const F2 (&x)[V / 2],
+                                        F2 (&q)[V / 2]) const {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      F2 a = bias[k];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) a = fma2(w[j][k], win[j][k], a);
+      q[k] = fma2(w[W - 1][k], x[k], a);
+    }
+  }
+};
+
+// Forgets the oldest row, takes x as the newest.
+template <int W, int K>
+__device__ __forceinline__ void shift(F2 (&win)[W - 1][K], const F2 (&x)[K]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int j = 0; j + 1 < W - 1; ++j) win[j][k] = win[j + 1][k];
+    win[W - 2][k] = x[k];
+  }
+}
+
+// The W - 1 inputs before token `tok` of sequence q; x, x0: this lane's channels
+// of the batch row's first token and of the call's first state (or NULL).
+template <int DT, int V, int W>
+__device__ __forceinline__ void load_window(const ConvParams& P, const char* x, const char* x0,
+                                            const ConvSeq& q, int64_t tok,
+                                            F2 (&win)[W - 1][V / 2]) {
+  constexpr int E = ElemSize<DT>::value;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    const int64_t row = tok - (W - 1) + j;
+    Pack<DT, V> p{};
+    if (row >= q.lo) {
+      load_pack(p, x + row * P.ld_x);
+    } else if (x0 != nullptr) {
+      load_pack(p, x0 + (static_cast<int64_t>(q.id) * (W - 1) + state_row<W>(q, row)) * P.c * E);
+    }
+    unpack_pairs(p, win[j]);
+  }
+}
+
+}  // namespace spb

@@ -1,0 +1,299 @@
+// Causal convolution, backward:
+//   dq[i] = dy[i] act'(q[i]),  dx[i] = sum_j w[j] dq[i + W - 1 - j] inside a sequence
+//   dw[j] = sum_i dq[i] x[i - (W - 1) + j],  dbias = sum_i dq[i]
+// A thread walks runs of tokens of its channels: q is computed again from the
+// inputs, and each token's gradient is added to those of the W - 1 tokens before it,
+// which wait in registers until they are whole.  A run goes on for W - 1 tokens beyond
+// its end for the gradients that come from there.
+#include "conv.cuh"
+
+namespace spb {
+
+// Four channels a thread: eight need 128 registers for weights, windows and sums.
+constexpr int kConvVecB = 4;
+constexpr int kConvRunB = 32;
+
+template <int DT, int W, bool PACKED>
+__global__ void __launch_bounds__(kConvThreads)
+conv_bwd_kernel(const ConvParams P) {
+  constexpr int V = kConvVecB, K = V / 2, E = ElemSize<DT>::value, U = 4, S = V * (W + 1);
+  __shared__ float sums[kConvThreads][S + 1];
+  pdl_wait();
+  if (PACKED && blockIdx.x == 0 && threadIdx.x < 32)
+    check_cu_seqlens(P.cu_seqlens, P.n_seqs, P.s, P.status);
+  const int slots = kConvThreads / P.lanes;
+  const int lane = threadIdx.x % P.lanes, slot = threadIdx.x / P.lanes;
+  const int part = blockIdx.x / P.slabs, slab = blockIdx.x % P.slabs;
+  const int per_rank = P.slabs / P.t;
+  const int r = slab / per_rank, vec = (slab - r * per_rank) * P.lanes + lane;
+  const bool on = vec < P.vecs;
+  const int64_t ch = static_cast<int64_t>(r) * P.c + (on ? vec : 0) * V;
+  const int64_t off = (on ? vec : 0) * V * E;
+  const char* x0 = P.x0[r] != nullptr ? P.x0[r] + off : nullptr;
+  const char* dxT = P.dxT[r] != nullptr ? P.dxT[r] + off : nullptr;
+  char* dx0 = P.xT[r] != nullptr ? P.xT[r] + off : nullptr;
+  Taps<DT, V, W> taps;
+  taps.load(P, ch);
+  F2 dw[W][K], db[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    db[k] = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j][k] = 0;
+  }
+  const int64_t all = P.runs * P.b;
+  for (int64_t at = static_cast<int64_t>(part) * slots + slot; on && at < all;
+       at += static_cast<int64_t>(P.parts) * slots) {
+    const int64_t batch = divide(at, P.runs, all), i0 = (at - batch * P.runs) * P.run;
+    const int64_t i1 = i0 + P.run < P.s ? i0 + P.run : P.s;
+    const int64_t i2 = i1 + W - 1 < P.s ? i1 + W - 1 : P.s;
+    const char* x = P.x[r] + batch * P.s * P.ld_x + off;
+    const char* dy = P.dy[r] + batch * P.s * P.ld_dy + off;
+    char* dx = P.out[r] + batch * P.s * P.ld_out + off;
+    Pack<DT, V> nx[U], nd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u < i2) {
+        load_pack(nx[u], x + (i0 + u) * P.ld_x);
+        load_pack(nd[u], dy + (i0 + u) * P.ld_dy);
+      }
+    ConvSeq q = conv_seq<PACKED>(P, batch, i0);
+    F2 win[W - 1][K], wait[W - 1][K];
+    load_window<DT, V, W>(P, x, x0, q, i0, win);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int k = 0; k < K; ++k) wait[j][k] = 0;
+
+    // the gradient of token `row`, or of the state's row that stands for it, is whole
+    auto emit = [&](int64_t row, const F2 (&v)[K]) {
+      if (row >= i1 || row < i0 && (row >= q.lo || q.lo < i0)) return;
+      char* dst;
+      if (row >= q.lo) dst = dx + row * P.ld_out;
+      else if (dx0 != nullptr)
+        dst = dx0 + (static_cast<int64_t>(q.id) * (W - 1) + state_row<W>(q, row)) * P.c * E;
+      else return;
+      F2 o[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) o[k] = v[k];
+      if (dxT != nullptr && row >= q.hi - (W - 1)) {
+        Pack<DT, V> p;
+        load_pack(p, dxT + (static_cast<int64_t>(q.id) * (W - 1) + (row - q.hi + W - 1)) * P.c * E);
+        F2 more[K];
+        unpack_pairs(p, more);
+#pragma unroll
+        for (int k = 0; k < K; ++k) o[k] = add2(o[k], more[k]);
+      }
+      Pack<DT, V> p;
+      pack_pairs(p, o);
+      store_pack(dst, p);
+    };
+    auto flush = [&](int64_t end) {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) emit(end - (W - 1) + j, wait[j]);
+    };
+
+    int64_t i = i0;
+    bool open = true;
+    for (; open && i < i2; i += U) {
+      Pack<DT, V> cx[U], cd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        cx[u] = nx[u];
+        cd[u] = nd[u];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + U + u < i2) {
+          load_pack(nx[u], x + (i + U + u) * P.ld_x);
+          load_pack(nd[u], dy + (i + U + u) * P.ld_dy);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t tok = i + u;
+        if (!open || tok >= i2) break;
+        if (PACKED && tok >= q.hi) {
+          flush(tok);
+          if (tok >= i1) {
+            open = false;
+            break;
+          }
+          q = conv_seq<PACKED>(P, batch, tok);
+          load_window<DT, V, W>(P, x, x0, q, tok, win);
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int k = 0; k < K; ++k) wait[j][k] = 0;
+        }
+        F2 v[K], g[K], o[K];
+        unpack_pairs(cx[u], v);
+        unpack_pairs(cd[u], g);
+        if (P.act == SP_ACT_SILU) {
+          taps.apply(win, v, o);
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            // sigmoid (1 + q (1 - sigmoid)), 1 - sigmoid = e sigmoid
+            // (exp(87) at most, whose reciprocal is normal: no product of infinity and 0)
+            const F2 e = exp2_of<DT, DT == SP_F32, -1>(DT == SP_F32 ? o[k] : held_above(o[k], -87.f));
+            const F2 sg = rcp2(add2(e, f2(1.f, 1.f)));
+            g[k] = mul2(g[k], fma2(mul2(o[k], mul2(e, sg)), sg, sg));
+          }
+        }
+        if (tok < i1) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            db[k] = add2(db[k], g[k]);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) dw[j][k] = fma2(g[k], win[j][k], dw[j][k]);
+            dw[W - 1][k] = fma2(g[k], v[k], dw[W - 1][k]);
+          }
+        }
+        F2 done[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          done[k] = fma2(taps.w[0][k], g[k], wait[0][k]);
+#pragma unroll
+          for (int j = 0; j + 1 < W - 1; ++j)
+            wait[j][k] = fma2(taps.w[j + 1][k], g[k], wait[j + 1][k]);
+          wait[W - 2][k] = mul2(taps.w[W - 1][k], g[k]);
+        }
+        shift<W, K>(win, v);
+        emit(tok - (W - 1), done);
+      }
+    }
+    if (open && i2 == P.s) flush(P.s);
+  }
+  if (P.ws == nullptr) return;
+
+  // the block's parameter gradients: its slots in order
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float2 v = split(dw[j][k]);
+      sums[threadIdx.x][2 * k * (W + 1) + j] = v.x;
+      sums[threadIdx.x][(2 * k + 1) * (W + 1) + j] = v.y;
+    }
+    const float2 v = split(db[k]);
+    sums[threadIdx.x][2 * k * (W + 1) + W] = v.x;
+    sums[threadIdx.x][(2 * k + 1) * (W + 1) + W] = v.y;
+  }
+  __syncthreads();
+  const int first = (slab - r * per_rank) * P.lanes;
+  const int live = P.vecs - first < P.lanes ? P.vecs - first : P.lanes;
+  float* ws = P.ws + (static_cast<int64_t>(part) * P.t * P.c + static_cast<int64_t>(r) * P.c +
+                      first * V) * (W + 1);
+  for (int i = threadIdx.x; i < live * S; i += kConvThreads) {
+    const int l = i / S, e = i - l * S;
+    float a = 0.f;
+    for (int k = 0; k < slots; ++k) a += sums[k * P.lanes + l][e];
+    ws[i] = a;
+  }
+}
+
+// dweight and dbias: the parts in order.
+__global__ void __launch_bounds__(kConvThreads)
+conv_params_kernel(const float* ws, int64_t channels, int width, int parts, float* dweight,
+                   float* dbias) {
+  pdl_wait();
+  const int64_t n = channels * (width + 1);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
+  if (i >= n) return;
+  float a = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < parts; ++k) a += ws[k * n + i];
+  const int64_t ch = i / (width + 1);
+  const int j = static_cast<int>(i - ch * (width + 1));
+  if (j < width) {
+    if (dweight != nullptr) dweight[ch * width + j] = a;
+  } else if (dbias != nullptr) {
+    dbias[ch] = a;
+  }
+}
+
+// The gradients of the states of packed sequences without a token pass.
+template <int DT, int W>
+__global__ void __launch_bounds__(kConvThreads)
+conv_empty_kernel(const ConvParams P) {
+  constexpr int V = kConvVecB, E = ElemSize<DT>::value;
+  pdl_wait();
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
+  const int64_t slot = id / P.vecs;
+  const int vec = static_cast<int>(id - slot * P.vecs);
+  const int64_t r = slot / P.n_seqs;
+  if (r >= P.t) return;
+  const int64_t j = slot - r * P.n_seqs;
+  if (__ldg(P.cu_seqlens + j) != __ldg(P.cu_seqlens + j + 1)) return;
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    const int64_t at = (j * (W - 1) + k) * P.c * E + vec * V * E;
+    Pack<DT, V> p{};
+    if (P.dxT[r] != nullptr) load_pack(p, P.dxT[r] + at);
+    store_pack(P.xT[r] + at, p);
+  }
+}
+
+template <int DT, int W>
+static cudaError_t launch_width(ConvParams& p, cudaStream_t st) {
+  void* args[] = {&p};
+  const bool packed = p.cu_seqlens != nullptr;
+  const void* fn = packed ? reinterpret_cast<const void*>(&conv_bwd_kernel<DT, W, true>)
+                          : reinterpret_cast<const void*>(&conv_bwd_kernel<DT, W, false>);
+  const cudaError_t e = launch_pdl(fn, dim3(static_cast<unsigned>(p.parts) * p.slabs),
+                                   dim3(kConvThreads), 0, args, st);
+  if (e != cudaSuccess || !packed || p.xT[0] == nullptr) return e;
+  const int64_t rows = static_cast<int64_t>(p.n_seqs) * p.t * p.vecs;
+  return launch_pdl(reinterpret_cast<const void*>(&conv_empty_kernel<DT, W>),
+                    dim3(static_cast<unsigned>((rows + kConvThreads - 1) / kConvThreads)),
+                    dim3(kConvThreads), 0, args, st);
+}
+
+template <int DT>
+static cudaError_t launch_dtype(ConvParams& p, cudaStream_t st) {
+  switch (p.width) {
+    case 2: return launch_width<DT, 2>(p, st);
+    case 3: return launch_width<DT, 3>(p, st);
+    default: return launch_width<DT, 4>(p, st);
+  }
+}
+
+// Vectors side by side in a block, and its slabs and runs.
+static void conv_bwd_split(ConvParams* p, int64_t b, int64_t s, int c, int t) {
+  p->vecs = c / kConvVecB;
+  p->lanes = 32;
+  while (p->lanes > 2 && p->lanes / 2 >= p->vecs) p->lanes /= 2;
+  p->slabs = t * ((p->vecs + p->lanes - 1) / p->lanes);
+  const int64_t want = static_cast<int64_t>(device_sm_count()) * 4;
+  const int slots = kConvThreads / p->lanes;
+  p->run = kConvRunB;
+  while (p->run > 4 && ((s + p->run - 1) / p->run * b + slots - 1) / slots * p->slabs < want)
+    p->run /= 2;
+  p->runs = (s + p->run - 1) / p->run;
+  const int64_t most = (p->runs * b + slots - 1) / slots;
+  int64_t parts = (want + p->slabs - 1) / p->slabs;
+  p->parts = static_cast<int32_t>(parts < most ? parts : most);
+}
+
+int conv_bwd_parts(int64_t b, int64_t s, int c, int t, int dtype) {
+  ConvParams p{};
+  conv_bwd_split(&p, b, s, c, t);
+  return p.parts;
+}
+
+cudaError_t launch_conv_bwd(ConvParams p, int dtype, float* dweight, float* dbias,
+                            cudaStream_t st) {
+  conv_bwd_split(&p, p.b, p.s, p.c, p.t);
+  cudaError_t e = dtype == SP_BF16  ? launch_dtype<SP_BF16>(p, st)
+                  : dtype == SP_F16 ? launch_dtype<SP_F16>(p, st)
+                                    : launch_dtype<SP_F32>(p, st);
+  if (e != cudaSuccess || p.ws == nullptr) return e;
+  int64_t channels = static_cast<int64_t>(p.t) * p.c;
+  const float* ws = p.ws;
+  void* args[] = {&ws, &channels, &p.width, &p.parts, &dweight, &dbias};
+  const int64_t n = channels * (p.width + 1);
+  return launch_pdl(reinterpret_cast<const void*>(&conv_params_kernel),
+                    dim3(static_cast<unsigned>((n + kConvThreads - 1) / kConvThreads)),
+                    dim3(kConvThreads), 0, args, st);
+}
+
+}  // namespace spb

@@ -161,6 +161,15 @@ __device__ __forceinline__ void pack_pairs(Pack<DT, N>& p, const F2 (&v)[N / 2])
   pack(p, f);
 }
 
+// a / b for 0 <= a < most: in 32 bits where they do (a 64-bit division costs a
+// hundred instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t most) {
+  if (b == 1) return a;
+  if (b >= most) return 0;
+  if (most <= 0x7FFFFFFF) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // The packed sequence of token `tok`: the largest j < n with cu[j] <= tok (the
 // last of several sequences that begin there: the others are empty).  One
 // warp, 32 probes a step; in bounds whatever cu holds.
@@ -230,6 +239,25 @@ __device__ __forceinline__ F2 exp2_of(F2 g) {
   const F2 e = f2(x.x, x.y);
   if constexpr (DT == SP_F32) return fma2(e, rest, e);
   return e;
+}
+
+// The larger of v and `least`; NaN stays.
+__device__ __forceinline__ F2 held_above(F2 v, float least) {
+  float2 x = split(v);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(least));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(least));
+  return f2(x.x, x.y);
+}
+
+// The sequence of token `tok` (see seq_of_token), found by one thread; in [0, n).
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int64_t tok) {
+  int lo = 0, hi = n;                  // cu[lo] <= tok < cu[hi], where cu is what it should be
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(__ldg(cu + mid)) <= tok) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 }  // namespace spb

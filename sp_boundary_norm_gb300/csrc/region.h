@@ -31,7 +31,13 @@ struct RopeParams {
   uint64_t turns[SP_ROPE_MAX_PAIRS];      // turns per position, fractions of 2^64
 };
 
-cudaError_t launch_rope(RopeParams p, int dtype, int vec, cudaStream_t st);
+// Several axes: `positions` is [axes][tokens], and every pair follows one axis.
+struct RopeAxesParams : RopeParams {
+  uint8_t axis[SP_ROPE_MAX_PAIRS];
+};
+
+cudaError_t launch_rope(const RopeParams& p, int dtype, int vec, cudaStream_t st);
+cudaError_t launch_rope_axes(const RopeAxesParams& p, int dtype, int vec, cudaStream_t st);
 
 // ---------------------------------------------------------- gated recurrence --
 constexpr int kScanRun = 16;        // tokens of one thread, and of one saved state
@@ -107,5 +113,98 @@ cudaError_t launch_group(const void* fn, GroupNormParams* p, const GroupShape& s
 cudaError_t launch_group_norm_fwd(GroupNormParams p, int dtype, cudaStream_t st);
 cudaError_t launch_group_norm_bwd(GroupNormParams p, int dtype, float* dgamma, float* dbeta,
                                   cudaStream_t st);
+
+
+// ------------------------------------------------------- causal convolution --
+struct ConvParams {
+  const char* x[SP_MAX_RANKS];
+  const char* dy[SP_MAX_RANKS];
+  char* out[SP_MAX_RANKS];              // forward: y; backward: dx
+  const char* x0[SP_MAX_RANKS];         // NULL: zero
+  const char* dxT[SP_MAX_RANKS];        // NULL: zero
+  char* xT[SP_MAX_RANKS];               // forward: xT; backward: dx0; NULL: not wanted
+  const char* weight;                   // [t * c][width]
+  const char* bias;                     // [t * c] or NULL
+  int64_t ld_x, ld_dy, ld_out;          // bytes between tokens
+  int64_t s;                            // tokens of a batch row
+  int32_t b, c, t, width, act;
+  const int32_t* cu_seqlens;
+  int32_t n_seqs;
+  int32_t* status;
+  // the split of a call
+  int32_t vecs, lanes;                  // vectors of a token; threads side by side on them
+  int32_t slabs;                        // pieces of `lanes` vectors of a token
+  int32_t run;                          // tokens of a thread's run
+  int64_t runs;                         // of a batch row
+  int32_t parts;                        // backward: blocks of one slab, [parts][t * c][width + 1]
+  float* ws;                            // NULL: no parameter gradient wanted
+};
+
+cudaError_t launch_conv_fwd(ConvParams p, int dtype, cudaStream_t st);
+cudaError_t launch_conv_bwd(ConvParams p, int dtype, float* dweight, float* dbias,
+                            cudaStream_t st);
+// Blocks of one slab in the backward of a call, which its workspace goes by.
+int conv_bwd_parts(int64_t b, int64_t s, int c, int t, int dtype);
+
+// ---------------------------------------------------------- selective scan --
+constexpr int kSsmRun = 16;             // tokens of one saved state
+constexpr int kSsmTile = 32;            // tokens of a block's step, forward
+constexpr int kSsmStepTokens = 4;       // most tokens of a decoding step
+
+struct SsmParams {
+  const char* u[SP_MAX_RANKS];
+  const char* dt[SP_MAX_RANKS];
+  const char* B[SP_MAX_RANKS];
+  const char* C[SP_MAX_RANKS];
+  const char* z[SP_MAX_RANKS];          // NULL: no gate
+  const char* dy[SP_MAX_RANKS];
+  char* y[SP_MAX_RANKS];                // forward
+  char* du[SP_MAX_RANKS];
+  char* ddt[SP_MAX_RANKS];
+  char* dB[SP_MAX_RANKS];
+  char* dC[SP_MAX_RANKS];
+  char* dz[SP_MAX_RANKS];
+  float* states[SP_MAX_RANKS];          // forward: NULL if not wanted
+  const float* h0[SP_MAX_RANKS];        // NULL: zero
+  const float* dhT[SP_MAX_RANKS];       // NULL: zero
+  float* hT[SP_MAX_RANKS];              // forward: hT; backward: dh0; NULL: not wanted
+  const float* A;                       // [t * c][n]
+  const float* D;                       // [t * c] or NULL
+  const float* dt_bias;                 // [t * c] or NULL
+  int64_t ld_u, ld_dt, ld_B, ld_C, ld_z, ld_dy, ld_y;     // bytes between tokens
+  int64_t ld_du, ld_ddt, ld_dB, ld_dC, ld_dz;
+  int64_t s;
+  int32_t b, c, t, n, groups, softplus, gated;
+  const int32_t* cu_seqlens;
+  int32_t n_seqs;
+  int32_t* status;
+  // the split of a call
+  int32_t slabs;                        // blocks of a group's channels
+  int32_t chunks;                       // pieces of a batch row that run side by side
+  int64_t chunk_len;                    // their tokens, a multiple of kSsmTile
+  float* carry;                         // [b][chunks][t * c][n]: the state (backward: its
+                                        // gradient) that enters a chunk
+  float* steps;                         // [b][chunks][t * c]: the sum of a chunk's steps
+  float* partial_bc;                    // backward: [t * groups * slabs][b * s][2n], or NULL
+  float* partial_params;                // backward: [b * chunks][t * c][n + 2], or NULL
+};
+
+// How a call is split on the current device.
+struct SsmSplit {
+  int32_t slabs, chunks;
+  int64_t chunk_len;
+  size_t carry, steps, partial_bc, partial_params;   // floats of each
+  size_t bytes() const { return (carry + steps + partial_bc + partial_params) * 4; }
+};
+SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bool bwd);
+
+cudaError_t launch_ssm_fwd(const SsmParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_ssm_step(const SsmParams& p, int dtype, cudaStream_t st);
+struct SsmParamGrads {
+  float* dA;
+  float* dD;
+  float* ddt_bias;
+};
+cudaError_t launch_ssm_bwd(const SsmParams& p, int dtype, const SsmParamGrads& g, cudaStream_t st);
 
 }  // namespace spb

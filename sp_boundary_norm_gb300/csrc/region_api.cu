@@ -2,71 +2,49 @@
 // and launch parameters.  Nothing here allocates device memory.
 #include <cmath>
 
-#include "host_common.h"
 #include "region.h"
+#include "region_checks.h"
 
 using namespace spb;
 
 namespace {
 
-constexpr int64_t kMostElements = int64_t(1) << 48;   // of one rank's tensor, strides included
-
-int elem_size(sp_dtype_t dtype) { return dtype == SP_F32 ? 4 : 2; }
-
-sp_status_t check_common(int32_t t, sp_dtype_t dtype, const int32_t* dev_status) {
-  if (t < 1 || t > SP_MAX_RANKS)
-    return fail(SP_ERR_INVALID_ARG, "t = %d outside [1, %d]", t, SP_MAX_RANKS);
-  if (dtype != SP_BF16 && dtype != SP_F16 && dtype != SP_F32)
-    return fail(SP_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
-  if (dev_status != nullptr && (reinterpret_cast<uintptr_t>(dev_status) & 3u))
-    return fail(SP_ERR_MISALIGNED, "dev_status misaligned");
-  return SP_OK;
-}
-
-sp_status_t check_seqs(int64_t b, int64_t s, const int32_t* cu_seqlens, int32_t n_seqs) {
-  if (b < 0 || s < 0) return fail(SP_ERR_INVALID_ARG, "negative b or s");
-  if (b > kMostElements || s > kMostElements || (s > 0 && b > kMostElements / s))
-    return fail(SP_ERR_INVALID_ARG, "b*s overflows");
-  if (cu_seqlens == nullptr) return SP_OK;
-  if (b != 1)
-    return fail(SP_ERR_INVALID_ARG, "cu_seqlens requires b == 1 (got %lld)", (long long)b);
-  if (n_seqs < 1) return fail(SP_ERR_INVALID_ARG, "n_seqs = %d must be >= 1", n_seqs);
-  if (s > 0x7FFFFFFF)
-    return fail(SP_ERR_INVALID_ARG, "cu_seqlens counts to 2^31 - 1 tokens (got %lld)", (long long)s);
-  if (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u)
-    return fail(SP_ERR_MISALIGNED, "cu_seqlens not 4-byte aligned");
-  return SP_OK;
-}
-
-template <typename T>
-sp_status_t check_ranks(T* const* arr, int t, const char* what) {
-  if (arr == nullptr) return fail(SP_ERR_INVALID_ARG, "%s array is NULL", what);
-  for (int i = 0; i < t; ++i) {
-    if (arr[i] == nullptr) return fail(SP_ERR_INVALID_ARG, "%s[%d] is NULL", what, i);
-    if (!aligned16(arr[i])) return fail(SP_ERR_MISALIGNED, "%s[%d] misaligned", what, i);
-  }
-  return SP_OK;
-}
-
-constexpr int64_t kMostLd = int64_t(1) << 28;   // a row stride in bytes fits 32 bits
-
-// A row stride: a multiple of 8 elements, at least the row, no overflow.
-sp_status_t check_ld(int64_t ld, int64_t width, int64_t rows, const char* what) {
-  if (ld < width || ld % 8 != 0)
-    return fail(SP_ERR_INVALID_ARG, "%s = %lld must be a multiple of 8 and at least %lld", what,
-                (long long)ld, (long long)width);
-  if (rows > 0 && ld > kMostElements / rows)
-    return fail(SP_ERR_INVALID_ARG, "%s: the tensor's extent overflows", what);
-  if (ld > kMostLd)
-    return fail(SP_ERR_UNSUPPORTED, "%s = %lld above %lld", what, (long long)ld,
-                (long long)kMostLd);
-  return SP_OK;
-}
-
 // ------------------------------------------------------------------ rotary --
+// What a table says: of one position a token, or (axis != NULL) of a coordinate for
+// each of several axes.
+struct RopeTurns {
+  int32_t pairs;
+  float mscale;
+  const uint64_t* turns;
+  const uint8_t* axis;
+  int32_t axes;
+};
+
+sp_status_t read_table(const sp_rope_table_t* table, RopeTurns* out) {
+  if (table == nullptr) return fail(SP_ERR_INVALID_ARG, "table is NULL");
+  if (table->pairs < 1 || table->pairs > SP_ROPE_MAX_PAIRS)
+    return fail(SP_ERR_INVALID_ARG, "table with %d pairs: fill it with sp_rope_table",
+                table->pairs);
+  *out = RopeTurns{table->pairs, table->mscale, table->turns, nullptr, 1};
+  return SP_OK;
+}
+
+sp_status_t read_table(const sp_rope_axes_table_t* table, RopeTurns* out) {
+  if (table == nullptr) return fail(SP_ERR_INVALID_ARG, "table is NULL");
+  bool good = table->pairs >= 1 && table->pairs <= SP_ROPE_MAX_PAIRS && table->axes >= 1 &&
+              table->axes <= SP_ROPE_MAX_AXES;
+  for (int i = 0; good && i < table->pairs; ++i) good = table->axis[i] < table->axes;
+  if (!good)
+    return fail(SP_ERR_INVALID_ARG, "table of %d pairs and %d axes: fill it with "
+                "sp_rope_axes_table", table->pairs, table->axes);
+  *out = RopeTurns{table->pairs, table->mscale, table->turns, table->axis, table->axes};
+  return SP_OK;
+}
+
+template <typename Table>
 sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, int64_t s,
                  int64_t heads, int64_t d, int32_t t, sp_dtype_t dtype,
-                 const sp_rope_table_t* table, sp_rope_layout_t layout, const int64_t* positions,
+                 const Table* table, sp_rope_layout_t layout, const int64_t* positions,
                  int64_t first, const int32_t* cu_seqlens, int32_t n_seqs, void* const* y,
                  int64_t y_ld, int64_t y_head, int32_t* dev_status, void* stream, float sign) {
   sp_status_t st;
@@ -75,14 +53,12 @@ sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, 
   if ((st = check_seqs(b, s, cu_seqlens, n_seqs)) != SP_OK) return st;
   if (layout != SP_ROPE_HALF && layout != SP_ROPE_INTERLEAVED)
     return fail(SP_ERR_INVALID_ARG, "unknown layout %d", (int)layout);
-  if (table == nullptr) return fail(SP_ERR_INVALID_ARG, "table is NULL");
-  if (table->pairs < 1 || table->pairs > SP_ROPE_MAX_PAIRS)
-    return fail(SP_ERR_INVALID_ARG, "table with %d pairs: fill it with sp_rope_table",
-                table->pairs);
+  RopeTurns turns;
+  if ((st = read_table(table, &turns)) != SP_OK) return st;
   if (heads < 1 || heads > SP_ROPE_MAX_HEADS)
     return fail(SP_ERR_INVALID_ARG, "heads = %lld outside [1, %d]", (long long)heads,
                 SP_ROPE_MAX_HEADS);
-  const int64_t rot = 2 * static_cast<int64_t>(table->pairs);
+  const int64_t rot = 2 * static_cast<int64_t>(turns.pairs);
   if (d < rot || d > SP_MAX_HIDDEN)
     return fail(SP_ERR_INVALID_ARG, "d = %lld outside [rot_dim = %lld, %d]", (long long)d,
                 (long long)rot, SP_MAX_HIDDEN);
@@ -100,6 +76,8 @@ sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, 
       return fail(SP_ERR_INVALID_ARG, "the tensor's extent overflows");
   }
   if (tokens == 0) return SP_OK;
+  if (turns.axis != nullptr && positions == nullptr)
+    return fail(SP_ERR_INVALID_ARG, "positions is NULL");
   if ((st = check_ranks(x, t, "x")) != SP_OK) return st;
   if ((st = check_ranks(y, t, "y")) != SP_OK) return st;
   const int size = elem_size(dtype);
@@ -113,18 +91,18 @@ sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, 
     if (!here) rg.add_rows(x[r], tokens, x_ld * size, xw, false, "x", r);
     rg.add_rows(y[r], tokens, y_ld * size, yw, true, "y", r);
   }
-  if (positions != nullptr) rg.add(positions, tokens * 8, false, "positions", 0);
+  if (positions != nullptr) rg.add(positions, tokens * 8 * turns.axes, false, "positions", 0);
   if (cu_seqlens != nullptr) rg.add(cu_seqlens, (n_seqs + size_t(1)) * 4, false, "cu_seqlens", 0);
   if ((st = rg.check()) != SP_OK) return st;
 
   // the widest accesses that the sizes and strides allow
-  const int64_t block = layout == SP_ROPE_HALF ? table->pairs : rot;
+  const int64_t block = layout == SP_ROPE_HALF ? turns.pairs : rot;
   int vec = 16 / size;
   while (vec > 1 && (block % vec != 0 || x_ld % vec != 0 || x_head % vec != 0 ||
                      y_ld % vec != 0 || y_head % vec != 0))
     vec /= 2;
 
-  RopeParams P{};
+  RopeAxesParams P{};
   for (int r = 0; r < t; ++r) {
     P.x[r] = static_cast<const char*>(x[r]);
     P.y[r] = static_cast<char*>(y[r]);
@@ -139,7 +117,7 @@ sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, 
   P.all_heads = static_cast<int32_t>(heads * t);
   P.heads_magic = heads == 1 ? 0u
                              : static_cast<uint32_t>(((uint64_t(1) << 32) + heads - 1) / heads);
-  P.half = table->pairs;
+  P.half = turns.pairs;
   P.rest_at = static_cast<int32_t>(rot) * size;
   P.rest = in_place ? 0 : static_cast<int32_t>(d - rot) * size;
   P.rest_bytes = 16;
@@ -152,11 +130,15 @@ sp_status_t rope(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b, 
   P.first = first;
   P.cu_seqlens = cu_seqlens;
   P.n_seqs = n_seqs;
-  P.cos_scale = table->mscale;
-  P.sin_scale = sign * table->mscale;
+  P.cos_scale = turns.mscale;
+  P.sin_scale = sign * turns.mscale;
   P.status = dev_status;
-  for (int i = 0; i < table->pairs; ++i) P.turns[i] = table->turns[i];
-  const cudaError_t e = launch_rope(P, dtype, vec, static_cast<cudaStream_t>(stream));
+  for (int i = 0; i < turns.pairs; ++i) P.turns[i] = turns.turns[i];
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (turns.axis != nullptr)
+    for (int i = 0; i < turns.pairs; ++i) P.axis[i] = turns.axis[i];
+  const cudaError_t e = turns.axis != nullptr ? launch_rope_axes(P, dtype, vec, cs)
+                                              : launch_rope(P, dtype, vec, cs);
   return e == cudaSuccess ? SP_OK : fail_cuda(e, "rotary launch");
 }
 
@@ -351,6 +333,71 @@ sp_status_t sp_rope_bwd(const void* const* dy, int64_t dy_ld, int64_t dy_head, i
                         int64_t dx_head, int32_t* dev_status, void* stream) {
   return rope(dy, dy_ld, dy_head, b, s, heads, d, t, dtype, table, layout, positions,
               first_position, cu_seqlens, n_seqs, dx, dx_ld, dx_head, dev_status, stream, -1.f);
+}
+
+sp_status_t sp_rope_axes_table(const int32_t* sections, int32_t axes, double base,
+                               sp_rope_order_t order, sp_rope_frequencies_t frequencies,
+                               const double* factors, double mscale, sp_rope_axes_table_t* out) {
+  if (out == nullptr || sections == nullptr)
+    return fail(SP_ERR_INVALID_ARG, "%s is NULL", out == nullptr ? "out" : "sections");
+  if (axes < 1 || axes > SP_ROPE_MAX_AXES)
+    return fail(SP_ERR_INVALID_ARG, "axes = %d outside [1, %d]", axes, SP_ROPE_MAX_AXES);
+  int64_t pairs = 0;
+  for (int k = 0; k < axes; ++k) {
+    if (sections[k] < 1)
+      return fail(SP_ERR_INVALID_ARG, "sections[%d] = %d must be >= 1", k, sections[k]);
+    pairs += sections[k];
+  }
+  if (pairs > SP_ROPE_MAX_PAIRS)
+    return fail(SP_ERR_INVALID_ARG, "%lld pairs above %d", (long long)pairs, SP_ROPE_MAX_PAIRS);
+  if (!(base >= 1.0) || !std::isfinite(base)) return fail(SP_ERR_INVALID_ARG, "base must be >= 1");
+  if (order != SP_ROPE_BLOCKS && order != SP_ROPE_CYCLIC)
+    return fail(SP_ERR_INVALID_ARG, "unknown order %d", (int)order);
+  if (frequencies != SP_ROPE_SHARED && frequencies != SP_ROPE_OWN)
+    return fail(SP_ERR_INVALID_ARG, "unknown frequencies %d", (int)frequencies);
+  if (!std::isfinite(mscale)) return fail(SP_ERR_INVALID_ARG, "mscale must be finite");
+  for (int k = 0; k < axes && factors != nullptr; ++k)
+    if (!(factors[k] >= 1.0) || !std::isfinite(factors[k]))
+      return fail(SP_ERR_INVALID_ARG, "factors[%d] must be >= 1", k);
+  const double kTau = 6.283185307179586476925286766559;
+  *out = sp_rope_axes_table_t{};
+  out->pairs = static_cast<int32_t>(pairs);
+  out->axes = axes;
+  out->mscale = static_cast<float>(mscale);
+  int32_t given[SP_ROPE_MAX_AXES] = {};
+  int32_t k = 0;
+  for (int i = 0; i < out->pairs; ++i) {
+    // blocks: the first axis with a pair left; cyclic: the next one
+    if (order == SP_ROPE_CYCLIC && i > 0) k = (k + 1) % axes;
+    while (given[k] == sections[k]) k = (k + 1) % axes;
+    const double rate = frequencies == SP_ROPE_SHARED
+                            ? static_cast<double>(i) / static_cast<double>(pairs)
+                            : static_cast<double>(given[k]) / static_cast<double>(sections[k]);
+    double w = std::pow(base, -rate);
+    if (factors != nullptr) w /= factors[k];
+    out->axis[i] = static_cast<uint8_t>(k);
+    out->turns[i] = static_cast<uint64_t>(std::ldexp(w / kTau, 64) + 0.5);   // w <= 1: below 2^62
+    ++given[k];
+  }
+  return SP_OK;
+}
+
+sp_status_t sp_rope_axes_fwd(const void* const* x, int64_t x_ld, int64_t x_head, int64_t b,
+                             int64_t s, int64_t heads, int64_t d, int32_t t, sp_dtype_t dtype,
+                             const sp_rope_axes_table_t* table, sp_rope_layout_t layout,
+                             const int64_t* positions, void* const* y, int64_t y_ld,
+                             int64_t y_head, void* stream) {
+  return rope(x, x_ld, x_head, b, s, heads, d, t, dtype, table, layout, positions, 0, nullptr, 0,
+              y, y_ld, y_head, nullptr, stream, 1.f);
+}
+
+sp_status_t sp_rope_axes_bwd(const void* const* dy, int64_t dy_ld, int64_t dy_head, int64_t b,
+                             int64_t s, int64_t heads, int64_t d, int32_t t, sp_dtype_t dtype,
+                             const sp_rope_axes_table_t* table, sp_rope_layout_t layout,
+                             const int64_t* positions, void* const* dx, int64_t dx_ld,
+                             int64_t dx_head, void* stream) {
+  return rope(dy, dy_ld, dy_head, b, s, heads, d, t, dtype, table, layout, positions, 0, nullptr,
+              0, dx, dx_ld, dx_head, nullptr, stream, -1.f);
 }
 
 sp_status_t sp_gated_scan_fwd(const void* const* gate, int64_t gate_ld, const void* const* value,

@@ -1,0 +1,56 @@
+// Selective scan, forward: launches of the walk.
+#include "ssm_fwd.cuh"
+
+namespace spb {
+
+template <int DT, int N>
+static cudaError_t launch_fwd(const SsmParams& p, cudaStream_t st) {
+  if (p.chunks > 1) {
+    cudaError_t e = launch_walk<DT, N, kSsmEnds>(p, st);
+    if (e == cudaSuccess) e = launch_join<false>(p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_walk<DT, N, kSsmOut>(p, st);
+}
+
+template <int DT>
+static cudaError_t launch_states(const SsmParams& p, cudaStream_t st) {
+  switch (p.n) {
+    case 8: return launch_fwd<DT, 8>(p, st);
+    case 16: return launch_fwd<DT, 16>(p, st);
+    case 32: return launch_fwd<DT, 32>(p, st);
+    default: return launch_fwd<DT, 64>(p, st);
+  }
+}
+
+SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bool bwd) {
+  const int block = bwd ? (n <= 16 ? 64 : n == 32 ? 32 : 16) : (n <= 32 ? 32 : 16);
+  const int64_t of_group = c / groups;
+  SsmSplit k{};
+  k.slabs = static_cast<int32_t>((of_group + block - 1) / block);
+  const int64_t blocks = b * t * groups * k.slabs, sms = device_sm_count();
+  int64_t chunks = 1;
+  if (blocks < sms) chunks = (bwd ? sms : 2 * sms) / blocks;
+  if (chunks > s / 128) chunks = s / 128 > 0 ? s / 128 : 1;
+  k.chunk_len = ((s + chunks - 1) / chunks + kSsmTile - 1) / kSsmTile * kSsmTile;
+  k.chunks = static_cast<int32_t>((s + k.chunk_len - 1) / k.chunk_len);
+  const int64_t parts = b * k.chunks, width = t * c;
+  if (k.chunks > 1) {
+    k.carry = static_cast<size_t>(parts * width * n);
+    k.steps = static_cast<size_t>(parts * width);
+  }
+  if (bwd) {
+    if (k.slabs > 1)
+      k.partial_bc = static_cast<size_t>(b * s) * t * groups * k.slabs * 2 * n;
+    k.partial_params = static_cast<size_t>(parts * width) * (n + 2);
+  }
+  return k;
+}
+
+cudaError_t launch_ssm_fwd(const SsmParams& p, int dtype, cudaStream_t st) {
+  return dtype == SP_BF16  ? launch_states<SP_BF16>(p, st)
+         : dtype == SP_F16 ? launch_states<SP_F16>(p, st)
+                           : launch_states<SP_F32>(p, st);
+}
+
+}  // namespace spb
