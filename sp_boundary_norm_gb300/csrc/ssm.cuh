@@ -72,10 +72,13 @@ __device__ __forceinline__ F2 pow2(F2 x) {
 // softplus(x) = max(x, 0) + log(1 + e), e = exp(-|x|), and its derivative
 // 1 / (1 + exp(-x)).  log(1 + e) = 2 artanh(s), s = e / (2 + e) <= 1/3, as s times a
 // polynomial in s^2 fitted to the least relative error over that range (2^-27): the
-// digits of a small e are kept.
+// digits of a small e are kept.  e itself is off by 2^-24 |x|, 2^-22 for float32 data.
+template <int DT>
 __device__ __forceinline__ F2 softplus2(F2 x, F2* slope) {
   const float2 v = split(x);
-  const F2 e = exp2_of<SP_F32, false>(f2(-fabsf(v.x), -fabsf(v.y)));
+  F2 e;
+  if constexpr (DT == SP_F32) e = exp2_of<SP_F32, false>(f2(-fabsf(v.x), -fabsf(v.y)));
+  else e = pow2(f2(fabsf(v.x) * -kLog2e, fabsf(v.y) * -kLog2e));
   const F2 s = mul2(e, rcp2(add2(e, f2(2.f, 2.f)))), q = mul2(s, s);
   F2 p = f2(0.28011987f, 0.28011987f);
   p = fma2(p, q, f2(0.28001806f, 0.28001806f));

@@ -73,14 +73,16 @@ ssm_bwd_kernel(const SsmParams P) {
   const char* src_c = P.C[r] + row0 * P.ld_C + at.group * N * E;
   const bool gated = P.gated != 0;
   const int n_runs = static_cast<int>((at.len + R - 1) / R);
-  const int pieces = at.live * E / 16;
+  const int live_bytes = at.live * E;
   auto ask = [&](int k) {
     char* st = smem + (k % W::kStages) * W::kStage;
     const int64_t t0 = static_cast<int64_t>(n_runs - 1 - k) * R;
     const int n_tok = at.len - t0 < R ? static_cast<int>(at.len - t0) : R;
-    const int rows = n_tok * pieces;
-    for (int i = tid; i < rows; i += W::kThreads) {
-      const int tok = i / pieces, p = (i - tok * pieces) * 16;
+    constexpr int kPieces = W::kBlockCh * E / 16;
+#pragma unroll
+    for (int i = tid; i < R * kPieces; i += W::kThreads) {
+      const int tok = i / kPieces, p = (i % kPieces) * 16;
+      if (tok >= n_tok || p >= live_bytes) continue;
       char* dst = st + tok * W::kRow + p;
       cp_async16(dst, src[0] + (t0 + tok) * P.ld_dt + p);
       cp_async16(dst + R * W::kRow, src[1] + (t0 + tok) * P.ld_u + p);
@@ -225,7 +227,7 @@ ssm_bwd_kernel(const SsmParams P) {
       F2 d = f2(f[0][0] + param[warp * CW + half + i], f[0][1] + param[warp * CW + half + i + M - 1]);
       const F2 u = f2(f[1][0], f[1][1]), dy = f2(f[2][0], f[2][1]);
       F2 slope = f2(1.f, 1.f), e = dy, dz = 0;
-      if (P.softplus) d = softplus2(d, &slope);
+      if (P.softplus) d = softplus2<DT>(d, &slope);
       if (gated) {
         const F2 z = f2(f[3][0], f[3][1]);
         const F2 x = exp2_of<DT, DT == SP_F32, -1>(DT == SP_F32 ? z : held_above(z, -87.f));

@@ -23,6 +23,7 @@ struct SsmWalk {
   using L = SsmLanes<N>;
   static constexpr int kWarps = N >= 32 ? 8 : 4;
   static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kBlocks = kWarps == 8 ? 2 : 3;          // of an SM, by their registers
   static constexpr int kBlockCh = kWarps * L::kChannels;
   static constexpr int E = ElemSize<DT>::value;
   static constexpr int kStages = 3;
@@ -40,7 +41,7 @@ struct SsmWalk {
 };
 
 template <int DT, int N, int MODE>
-__global__ void __launch_bounds__(SsmWalk<DT, N>::kThreads)
+__global__ void __launch_bounds__(SsmWalk<DT, N>::kThreads, SsmWalk<DT, N>::kBlocks)
 ssm_walk_kernel(const SsmParams P) {
   using W = SsmWalk<DT, N>;
   using L = SsmLanes<N>;
@@ -74,16 +75,18 @@ ssm_walk_kernel(const SsmParams P) {
   const int64_t ld_b = kBack ? P.ld_C : P.ld_B;
   const bool gated = MODE != kSsmEnds && P.gated;
   const int n_tiles = static_cast<int>((at.len + T - 1) / T);
-  const int pieces = at.live * E / 16;
+  const int live_bytes = at.live * E;
   // step k's tile, in the order of the walk
   auto tile_of = [&](int k) { return static_cast<int64_t>(kBack ? n_tiles - 1 - k : k) * T; };
   auto ask = [&](int k) {
     char* st = smem + (k % W::kStages) * W::kStage;
     const int64_t t0 = tile_of(k);
     const int n_tok = at.len - t0 < T ? static_cast<int>(at.len - t0) : T;
-    const int rows = n_tok * pieces;
-    for (int i = tid; i < rows; i += W::kThreads) {
-      const int tok = i / pieces, p = (i - tok * pieces) * 16;
+    constexpr int kPieces = W::kBlockCh * E / 16;
+#pragma unroll
+    for (int i = tid; i < T * kPieces; i += W::kThreads) {
+      const int tok = i / kPieces, p = (i % kPieces) * 16;
+      if (tok >= n_tok || p >= live_bytes) continue;
       char* dst = st + tok * W::kRow + p;
       cp_async16(dst, src[0] + (t0 + tok) * lds[0] + p);
       cp_async16(dst + T * W::kRow, src[1] + (t0 + tok) * lds[1] + p);
@@ -179,7 +182,7 @@ ssm_walk_kernel(const SsmParams P) {
       for (int i = 0; i < CW / 2; ++i) {
         const float2 bias = *reinterpret_cast<const float2*>(param + warp * CW + 2 * i);
         d[i] = add2(d[i], f2(bias.x, bias.y));
-        if (P.softplus) d[i] = softplus2(d[i], nullptr);
+        if (P.softplus) d[i] = softplus2<DT>(d[i], nullptr);
         if constexpr (!kBack) v[i] = mul2(d[i], v[i]);
       }
       if (kBack && gated) {
@@ -237,14 +240,27 @@ ssm_walk_kernel(const SsmParams P) {
       known = last + 1 < P.n_seqs ? __ldg(P.cu_seqlens + last + 1) : P.s;
     }
     if (marks.starts == 0u && n_tok == T) {
-      for (int g0 = 0; g0 < T; g0 += G) {
-        save(g0);
-        float part[G];
+      // a saved state's run at a time, its sums kept in registers: without a store in
+      // between, a run's loads and exponentials go ahead of its states
+#pragma unroll 1
+      for (int r0 = 0; r0 < T; r0 += kSsmRun) {
+        save(r0);
+        float kept[kSsmRun / G];
 #pragma unroll
-        for (int g = 0; g < G; ++g) part[g] = token(kBack ? T - 1 - g0 - g : g0 + g);
+        for (int g0 = 0; g0 < kSsmRun; g0 += G) {
+          float part[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) part[g] = token(kBack ? T - 1 - r0 - g0 - g : r0 + g0 + g);
+          if constexpr (MODE == kSsmOut) {
+            sum_over<G, G>(part, lane, 1);
+            kept[g0 / G] = part[0];
+          }
+        }
         if constexpr (MODE == kSsmOut) {
-          sum_over<G, G>(part, lane, 1);
-          *reinterpret_cast<float*>(ybuf + (g0 + lane % G) * W::kYRow + (lane / G) * 4) = part[0];
+#pragma unroll
+          for (int g0 = 0; g0 < kSsmRun; g0 += G)
+            *reinterpret_cast<float*>(ybuf + (r0 + g0 + lane % G) * W::kYRow + (lane / G) * 4) =
+                kept[g0 / G];
         }
       }
     } else {
