@@ -148,7 +148,7 @@ int conv_bwd_parts(int64_t b, int64_t s, int c, int t, int dtype);
 
 // ---------------------------------------------------------- selective scan --
 constexpr int kSsmRun = 16;             // tokens of one saved state
-constexpr int kSsmTile = 32;            // tokens of a block's step, forward
+constexpr int kSsmTile = 16;            // tokens of a step of a block
 constexpr int kSsmStepTokens = 4;       // most tokens of a decoding step
 
 struct SsmParams {

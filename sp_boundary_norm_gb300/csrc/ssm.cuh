@@ -4,11 +4,11 @@
 //   y = (sum_n C[n] h[n] + D u) silu(z)
 // B and C are shared by a group's channels.
 //
-// A thread holds four states of one channel (two for N = 8), so the lanes of a warp
-// are N / 4 to a channel and a warp has 128 / N channels.  A token costs a state one
-// exponential and four packed float32 operations a pair, and the sum over a channel's
-// states crosses N / 4 lanes: for as many tokens at once as a channel has lanes, so
-// that each lane is left with one token's sum.
+// A lane holds four states (two for N = 8) of two channels side by side, so B and C
+// of a token are read from shared memory once for both: a word there costs a warp as
+// much as four of its arithmetic instructions.  The sums over a channel's states cross
+// the N / 4 lanes of a channel, for as many tokens at once as a channel has lanes, so
+// that each lane is left with one token's.
 #pragma once
 
 #include "region.cuh"
@@ -17,10 +17,10 @@ namespace spb {
 
 template <int N>
 struct SsmLanes {
-  static constexpr int kStates = N >= 16 ? 4 : 2;   // of a lane
+  static constexpr int kStates = N >= 16 ? 4 : 2;   // of a channel, in a lane
   static constexpr int kPairs = kStates / 2;
   static constexpr int kLanes = N / kStates;        // of a channel: 4, 4, 8, 16
-  static constexpr int kChannels = 32 / kLanes;     // of a warp: 8, 8, 4, 2
+  static constexpr int kChannels = 2 * 32 / kLanes; // of a warp: 16, 16, 8, 4
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -116,6 +116,17 @@ __device__ __forceinline__ void lds_pack(Pack<DT, N>& p, const char* src) {
   } else {
     p.w[0] = *reinterpret_cast<const unsigned short*>(src);
   }
+}
+
+__device__ __forceinline__ float pow2(float x) {
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+
+// All of the block's threads; its halves come here from different code.
+template <int THREADS>
+__device__ __forceinline__ void meet() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 // The sums of M values over the L lanes `step`, 2 step, ... apart, of which each lane

@@ -1,5 +1,4 @@
 // Selective scan, backward: launches.
-#include "ssm_fwd.cuh"
 #include "ssm_bwd.cuh"
 
 namespace spb {

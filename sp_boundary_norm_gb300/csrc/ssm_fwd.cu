@@ -24,7 +24,7 @@ static cudaError_t launch_states(const SsmParams& p, cudaStream_t st) {
 }
 
 SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bool bwd) {
-  const int block = bwd ? (n <= 16 ? 64 : n == 32 ? 32 : 16) : (n <= 32 ? 32 : 16);
+  const int block = n <= 16 ? 64 : n == 32 ? 32 : 16;
   const int64_t of_group = c / groups;
   SsmSplit k{};
   k.slabs = static_cast<int32_t>((of_group + block - 1) / block);
