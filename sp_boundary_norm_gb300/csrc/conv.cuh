@@ -9,28 +9,29 @@ namespace spb {
 
 constexpr int kConvThreads = 256;
 
+// Four channels of a token a thread: eight 16-bit ones need half as many registers again
+// for weights and windows as leave an SM enough warps.
+constexpr int kConvVec = 4;
+
 // The sequence that a thread's run is in: its number (states are found by it), first
-// token and end, all of one batch row.
+// token and end, counted from the run's first token (an end far behind it: anything
+// large).
 struct ConvSeq {
-  int id;
-  int64_t lo, hi;
+  int id, lo, hi;
 };
 template <bool PACKED>
-__device__ __forceinline__ ConvSeq conv_seq(const ConvParams& P, int64_t batch, int64_t tok) {
-  if constexpr (!PACKED) return ConvSeq{static_cast<int>(batch), 0, P.s};
-  ConvSeq q;
-  q.id = find_seq(P.cu_seqlens, P.n_seqs, tok);
-  const int64_t lo = __ldg(P.cu_seqlens + q.id), hi = __ldg(P.cu_seqlens + q.id + 1);
-  q.lo = lo < 0 ? 0 : lo > tok ? tok : lo;          // in bounds whatever cu holds
-  q.hi = hi > P.s || hi <= tok ? P.s : hi;
-  return q;
-}
-
-// Row of the state that stands for token `row` < q.lo.
-template <int W>
-__device__ __forceinline__ int state_row(const ConvSeq& q, int64_t row) {
-  const int64_t r = W - 1 + row - q.lo;
-  return r < 0 ? 0 : static_cast<int>(r);
+__device__ __forceinline__ ConvSeq conv_seq(const ConvParams& P, int64_t batch, int64_t i0, int i) {
+  int64_t lo = 0, hi = P.s;
+  int id = static_cast<int>(batch);
+  if constexpr (PACKED) {              // in bounds whatever cu holds
+    id = find_seq(P.cu_seqlens, P.n_seqs, i0 + i);
+    lo = __ldg(P.cu_seqlens + id);
+    hi = __ldg(P.cu_seqlens + id + 1);
+    lo = lo < 0 ? 0 : lo > i0 + i ? i0 + i : lo;
+    hi = hi > P.s || hi <= i0 + i ? P.s : hi;
+  }
+  return ConvSeq{id, lo < i0 - 8 ? -8 : static_cast<int>(lo - i0),
+                 hi > i0 + (1 << 20) ? 1 << 20 : static_cast<int>(hi - i0)};
 }
 
 // A lane's taps: for each the weights of its V channels, and its bias.
@@ -82,21 +83,20 @@ __device__ __forceinline__ void shift(F2 (&win)[W - 1][K], const F2 (&x)[K]) {
   }
 }
 
-// The W - 1 inputs before token `tok` of sequence q; x, x0: this lane's channels
-// of the batch row's first token and of the call's first state (or NULL).
+// The W - 1 inputs before the run's token i, in sequence q; x: the run's first token, x0:
+// the call's first state (or NULL), both at this lane's channels.
 template <int DT, int V, int W>
 __device__ __forceinline__ void load_window(const ConvParams& P, const char* x, const char* x0,
-                                            const ConvSeq& q, int64_t tok,
-                                            F2 (&win)[W - 1][V / 2]) {
+                                            const ConvSeq& q, int i, F2 (&win)[W - 1][V / 2]) {
   constexpr int E = ElemSize<DT>::value;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
-    const int64_t row = tok - (W - 1) + j;
+    const int row = i - (W - 1) + j;
     Pack<DT, V> p{};
     if (row >= q.lo) {
       load_pack(p, x + row * P.ld_x);
     } else if (x0 != nullptr) {
-      load_pack(p, x0 + (static_cast<int64_t>(q.id) * (W - 1) + state_row<W>(q, row)) * P.c * E);
+      load_pack(p, x0 + (static_cast<int64_t>(q.id) * (W - 1) + (W - 1 + row - q.lo)) * P.c * E);
     }
     unpack_pairs(p, win[j]);
   }

@@ -9,14 +9,13 @@
 
 namespace spb {
 
-// Four channels a thread: eight need 128 registers for weights, windows and sums.
-constexpr int kConvVecB = 4;
 constexpr int kConvRunB = 32;
 
 template <int DT, int W, bool PACKED>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, 2)
 conv_bwd_kernel(const ConvParams P) {
-  constexpr int V = kConvVecB, K = V / 2, E = ElemSize<DT>::value, U = 4, S = V * (W + 1);
+  constexpr int V = kConvVec, K = V / 2, E = ElemSize<DT>::value, S = V * (W + 1);
+  constexpr int U = DT == SP_F32 ? 2 : 4;   // rows that a thread asks for at once
   __shared__ float sums[kConvThreads][S + 1];
   pdl_wait();
   if (PACKED && blockIdx.x == 0 && threadIdx.x < 32)
@@ -45,33 +44,38 @@ conv_bwd_kernel(const ConvParams P) {
   for (int64_t at = static_cast<int64_t>(part) * slots + slot; on && at < all;
        at += static_cast<int64_t>(P.parts) * slots) {
     const int64_t batch = divide(at, P.runs, all), i0 = (at - batch * P.runs) * P.run;
-    const int64_t i1 = i0 + P.run < P.s ? i0 + P.run : P.s;
-    const int64_t i2 = i1 + W - 1 < P.s ? i1 + W - 1 : P.s;
-    const char* x = P.x[r] + batch * P.s * P.ld_x + off;
-    const char* dy = P.dy[r] + batch * P.s * P.ld_dy + off;
-    char* dx = P.out[r] + batch * P.s * P.ld_out + off;
+    const int n = i0 + P.run < P.s ? P.run : static_cast<int>(P.s - i0);
+    const int all_n = i0 + n + W - 1 < P.s ? n + W - 1 : static_cast<int>(P.s - i0);
+    const char* x = P.x[r] + (batch * P.s + i0) * P.ld_x + off;
+    const char* dy = P.dy[r] + (batch * P.s + i0) * P.ld_dy + off;
+    char* dx = P.out[r] + (batch * P.s + i0) * P.ld_out + off;
     Pack<DT, V> nx[U], nd[U];
+    const char *ahead_x = x, *ahead_d = dy;
+    auto fetch = [&](int i) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u < i2) {
-        load_pack(nx[u], x + (i0 + u) * P.ld_x);
-        load_pack(nd[u], dy + (i0 + u) * P.ld_dy);
-      }
-    ConvSeq q = conv_seq<PACKED>(P, batch, i0);
+      for (int u = 0; u < U; ++u, ahead_x += P.ld_x, ahead_d += P.ld_dy)
+        if (i + u < all_n) {
+          load_pack(nx[u], ahead_x);
+          load_pack(nd[u], ahead_d);
+        }
+    };
+    fetch(0);
+    ConvSeq q = conv_seq<PACKED>(P, batch, i0, 0);
     F2 win[W - 1][K], wait[W - 1][K];
-    load_window<DT, V, W>(P, x, x0, q, i0, win);
+    load_window<DT, V, W>(P, x, x0, q, 0, win);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
       for (int k = 0; k < K; ++k) wait[j][k] = 0;
 
-    // the gradient of token `row`, or of the state's row that stands for it, is whole
-    auto emit = [&](int64_t row, const F2 (&v)[K]) {
-      if (row >= i1 || row < i0 && (row >= q.lo || q.lo < i0)) return;
+    // the gradient of the run's token `row`, or of the state's row that stands for it, is
+    // whole
+    auto emit = [&](int row, const F2 (&v)[K]) {
+      if (row >= n || (row < 0 && (row >= q.lo || q.lo < 0))) return;
       char* dst;
       if (row >= q.lo) dst = dx + row * P.ld_out;
       else if (dx0 != nullptr)
-        dst = dx0 + (static_cast<int64_t>(q.id) * (W - 1) + state_row<W>(q, row)) * P.c * E;
+        dst = dx0 + (static_cast<int64_t>(q.id) * (W - 1) + (W - 1 + row - q.lo)) * P.c * E;
       else return;
       F2 o[K];
 #pragma unroll
@@ -88,37 +92,31 @@ conv_bwd_kernel(const ConvParams P) {
       pack_pairs(p, o);
       store_pack(dst, p);
     };
-    auto flush = [&](int64_t end) {
+    auto flush = [&](int end) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) emit(end - (W - 1) + j, wait[j]);
     };
 
-    int64_t i = i0;
     bool open = true;
-    for (; open && i < i2; i += U) {
+    for (int i = 0; open && i < all_n; i += U) {
       Pack<DT, V> cx[U], cd[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         cx[u] = nx[u];
         cd[u] = nd[u];
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i + U + u < i2) {
-          load_pack(nx[u], x + (i + U + u) * P.ld_x);
-          load_pack(nd[u], dy + (i + U + u) * P.ld_dy);
-        }
+      fetch(i + U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t tok = i + u;
-        if (!open || tok >= i2) break;
+        const int tok = i + u;
+        if (!open || tok >= all_n) break;
         if (PACKED && tok >= q.hi) {
           flush(tok);
-          if (tok >= i1) {
+          if (tok >= n) {
             open = false;
             break;
           }
-          q = conv_seq<PACKED>(P, batch, tok);
+          q = conv_seq<PACKED>(P, batch, i0, tok);
           load_window<DT, V, W>(P, x, x0, q, tok, win);
 #pragma unroll
           for (int j = 0; j < W - 1; ++j)
@@ -139,7 +137,7 @@ conv_bwd_kernel(const ConvParams P) {
             g[k] = mul2(g[k], fma2(mul2(o[k], mul2(e, sg)), sg, sg));
           }
         }
-        if (tok < i1) {
+        if (tok < n) {
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             db[k] = add2(db[k], g[k]);
@@ -161,7 +159,7 @@ conv_bwd_kernel(const ConvParams P) {
         emit(tok - (W - 1), done);
       }
     }
-    if (open && i2 == P.s) flush(P.s);
+    if (open && i0 + all_n == P.s) flush(all_n);
   }
   if (P.ws == nullptr) return;
 
@@ -215,7 +213,7 @@ conv_params_kernel(const float* ws, int64_t channels, int width, int parts, floa
 template <int DT, int W>
 __global__ void __launch_bounds__(kConvThreads)
 conv_empty_kernel(const ConvParams P) {
-  constexpr int V = kConvVecB, E = ElemSize<DT>::value;
+  constexpr int V = kConvVec, E = ElemSize<DT>::value;
   pdl_wait();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
   const int64_t slot = id / P.vecs;
@@ -259,7 +257,7 @@ static cudaError_t launch_dtype(ConvParams& p, cudaStream_t st) {
 
 // Vectors side by side in a block, and its slabs and runs.
 static void conv_bwd_split(ConvParams* p, int64_t b, int64_t s, int c, int t) {
-  p->vecs = c / kConvVecB;
+  p->vecs = c / kConvVec;
   p->lanes = 32;
   while (p->lanes > 2 && p->lanes / 2 >= p->vecs) p->lanes /= 2;
   p->slabs = t * ((p->vecs + p->lanes - 1) / p->lanes);

@@ -1,26 +1,21 @@
-// Causal convolution, forward.  A thread takes a vector of channels (16 bytes) and a
-// run of tokens, with the last W - 1 inputs in registers, so that each input is read
-// once but for the W - 1 rows before a run.
+// Causal convolution, forward.  A thread takes four channels and a run of tokens, with
+// the last W - 1 inputs in registers, so that each input is read once but for the W - 1
+// rows before a run.
 #include "conv.cuh"
 
 namespace spb {
 
-template <int DT>
-struct ConvFwd {
-  static constexpr int kVec = 16 / ElemSize<DT>::value;
-};
 constexpr int kConvAhead = 4;          // rows that a thread asks for at once
 
 template <int DT, int W, bool PACKED>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, DT == SP_F32 ? 2 : 3)
 conv_fwd_kernel(const ConvParams P) {
-  constexpr int V = ConvFwd<DT>::kVec, K = V / 2, E = ElemSize<DT>::value, U = kConvAhead;
+  constexpr int V = kConvVec, K = V / 2, E = ElemSize<DT>::value, U = kConvAhead;
   pdl_wait();
   if (PACKED && blockIdx.x == 0 && threadIdx.x < 32)
     check_cu_seqlens(P.cu_seqlens, P.n_seqs, P.s, P.status);
-  const int64_t per_rank = P.runs * P.b * P.vecs;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
-  const int64_t most = per_rank * P.t;
+  const int64_t most = P.runs * P.b * P.vecs * P.t;
   if (id >= most) return;
   const int64_t slot = divide(id, P.vecs, most);
   const int vec = static_cast<int>(id - slot * P.vecs);
@@ -28,31 +23,32 @@ conv_fwd_kernel(const ConvParams P) {
   const int r = static_cast<int>(divide(row, P.b, most));
   const int64_t batch = row - static_cast<int64_t>(r) * P.b;
   const int64_t i0 = run * P.run;
-  const int64_t i1 = i0 + P.run < P.s ? i0 + P.run : P.s;
-  const char* x = P.x[r] + batch * P.s * P.ld_x + vec * 16;
-  char* y = P.out[r] + batch * P.s * P.ld_out + vec * 16;
-  const char* x0 = P.x0[r] != nullptr ? P.x0[r] + vec * 16 : nullptr;
+  const int n = i0 + P.run < P.s ? P.run : static_cast<int>(P.s - i0);
+  const char* x = P.x[r] + (batch * P.s + i0) * P.ld_x + vec * V * E;
+  char* y = P.out[r] + (batch * P.s + i0) * P.ld_out + vec * V * E;
+  const char* x0 = P.x0[r] != nullptr ? P.x0[r] + vec * V * E : nullptr;
   Pack<DT, V> next[U];
+  const char* ahead = x;
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (i0 + u < i1) load_pack(next[u], x + (i0 + u) * P.ld_x);
-  ConvSeq q = conv_seq<PACKED>(P, batch, i0);
+  for (int u = 0; u < U; ++u, ahead += P.ld_x)
+    if (u < n) load_pack(next[u], ahead);
+  ConvSeq q = conv_seq<PACKED>(P, batch, i0, 0);
   F2 win[W - 1][K];
-  load_window<DT, V, W>(P, x, x0, q, i0, win);
+  load_window<DT, V, W>(P, x, x0, q, 0, win);
   Taps<DT, V, W> taps;
   taps.load(P, static_cast<int64_t>(r) * P.c + vec * V);
-  for (int64_t i = i0; i < i1; i += U) {
+  for (int i = 0; i < n; i += U) {
     Pack<DT, V> now[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) now[u] = next[u];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i + U + u < i1) load_pack(next[u], x + (i + U + u) * P.ld_x);
+    for (int u = 0; u < U; ++u, ahead += P.ld_x)
+      if (i + U + u < n) load_pack(next[u], ahead);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i + u >= i1) break;
+    for (int u = 0; u < U; ++u, y += P.ld_out) {
+      if (i + u >= n) break;
       if (PACKED && i + u >= q.hi) {
-        q = conv_seq<PACKED>(P, batch, i + u);
+        q = conv_seq<PACKED>(P, batch, i0, i + u);
         load_window<DT, V, W>(P, x, x0, q, i + u, win);
       }
       F2 v[K], o[K];
@@ -65,7 +61,7 @@ conv_fwd_kernel(const ConvParams P) {
           o[k] = mul2(o[k], rcp2(add2(exp2_of<DT, false, -1>(o[k]), f2(1.f, 1.f))));
       }
       pack_pairs(now[u], o);
-      store_pack(y + (i + u) * P.ld_out, now[u]);
+      store_pack(y, now[u]);
     }
   }
   // The state after a dense sequence comes from the thread of its first run, the only
@@ -75,9 +71,9 @@ conv_fwd_kernel(const ConvParams P) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       Pack<DT, V> p;
-      if (i1 == P.s) pack_pairs(p, win[j]);
+      if (n == P.s) pack_pairs(p, win[j]);
       else load_pack(p, x + (P.s - (W - 1) + j) * P.ld_x);
-      store_pack(P.xT[r] + (batch * (W - 1) + j) * P.c * E + vec * 16, p);
+      store_pack(P.xT[r] + (batch * (W - 1) + j) * P.c * E + vec * V * E, p);
     }
   }
 }
@@ -87,7 +83,7 @@ conv_fwd_kernel(const ConvParams P) {
 template <int DT, int W>
 __global__ void __launch_bounds__(kConvThreads)
 conv_state_kernel(const ConvParams P) {
-  constexpr int V = ConvFwd<DT>::kVec, E = ElemSize<DT>::value;
+  constexpr int V = kConvVec, E = ElemSize<DT>::value;
   pdl_wait();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
   const int64_t slot = id / P.vecs;
@@ -103,13 +99,13 @@ conv_state_kernel(const ConvParams P) {
   for (int k = 0; k < W - 1; ++k) {
     const int64_t row = hi - (W - 1) + k;
     rows[k] = Pack<DT, V>{};
-    if (row >= lo) load_pack(rows[k], P.x[r] + row * P.ld_x + vec * 16);
+    if (row >= lo) load_pack(rows[k], P.x[r] + row * P.ld_x + vec * V * E);
     else if (P.x0[r] != nullptr)
-      load_pack(rows[k], P.x0[r] + (j * (W - 1) + (W - 1 + row - lo)) * P.c * E + vec * 16);
+      load_pack(rows[k], P.x0[r] + (j * (W - 1) + (W - 1 + row - lo)) * P.c * E + vec * V * E);
   }
 #pragma unroll
   for (int k = 0; k < W - 1; ++k)
-    store_pack(P.xT[r] + (j * (W - 1) + k) * P.c * E + vec * 16, rows[k]);
+    store_pack(P.xT[r] + (j * (W - 1) + k) * P.c * E + vec * V * E, rows[k]);
 }
 
 template <int DT, int W>
@@ -130,7 +126,7 @@ static cudaError_t launch_width(ConvParams& p, cudaStream_t st) {
 
 template <int DT>
 static cudaError_t launch_dtype(ConvParams& p, cudaStream_t st) {
-  p.vecs = p.c / ConvFwd<DT>::kVec;
+  p.vecs = p.c / kConvVec;
   // runs of 32 tokens, or shorter ones until every SM has its warps
   const int64_t want = static_cast<int64_t>(device_sm_count()) * 1024;
   p.run = 32;
