@@ -7,7 +7,7 @@
 
 namespace spb {
 
-constexpr int kConvThreads = 256;
+constexpr int kConvThreads = 128;
 
 // Four channels of a token a thread: eight 16-bit ones need half as many registers again
 // for weights and windows as leave an SM enough warps.
@@ -101,5 +101,55 @@ __device__ __forceinline__ void load_window(const ConvParams& P, const char* x, 
     unpack_pairs(p, win[j]);
   }
 }
+
+// Rows on their way to a thread: its own pieces of shared memory, a group of rows after
+// another, kConvAhead groups asked for before the first is used.  They take no registers
+// and no barrier.
+constexpr int kConvGroup = 4, kConvAhead = 2;
+template <int DT, int V, int TENSORS>
+struct RowRing {
+  static constexpr int kBytes = V * ElemSize<DT>::value;
+  static constexpr int kGroups = kConvAhead + 1;
+  static constexpr int kSize = kGroups * kConvGroup * TENSORS * kConvThreads * kBytes;
+  char* mine;
+  const char* src[TENSORS];
+  int64_t ld[TENSORS];
+  int put = 0, get = 0;                // groups' places, in bytes
+  static constexpr int kStep = kConvGroup * TENSORS * kConvThreads * kBytes;
+  __device__ __forceinline__ explicit RowRing(char* smem) : mine(smem + threadIdx.x * kBytes) {}
+  // asks for the next group's first `rows` rows
+  __device__ __forceinline__ void ask(int rows) {
+#pragma unroll
+    for (int u = 0; u < kConvGroup; ++u)
+#pragma unroll
+      for (int t = 0; t < TENSORS; ++t) {
+        char* dst = mine + put + (u * TENSORS + t) * kConvThreads * kBytes;
+        if (u < rows) {
+          if constexpr (kBytes == 16) cp_async16(dst, src[t]);
+          else cp_async8(dst, src[t]);
+        }
+        src[t] += ld[t];
+      }
+    cp_async_commit();
+    put = put == (kGroups - 1) * kStep ? 0 : put + kStep;
+  }
+  __device__ __forceinline__ void row(int u, int t, Pack<DT, V>& p) const {
+    const char* from = mine + get + (u * TENSORS + t) * kConvThreads * kBytes;
+    if constexpr (kBytes == 16) {
+      const uint4 v = lds16(from);
+      p.w[0] = v.x;
+      p.w[1] = v.y;
+      p.w[2] = v.z;
+      p.w[3] = v.w;
+    } else {
+      const uint2 v = lds8(from);
+      p.w[0] = v.x;
+      p.w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void next() {
+    get = get == (kGroups - 1) * kStep ? 0 : get + kStep;
+  }
+};
 
 }  // namespace spb

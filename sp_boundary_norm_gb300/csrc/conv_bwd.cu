@@ -9,14 +9,50 @@
 
 namespace spb {
 
-constexpr int kConvRunB = 32;
+constexpr int kConvRunB = 64;
+
+// Where a run's gradients go; this lane's channels.
+template <int V>
+struct RowOut {
+  char* dx;            // of the run's first token
+  char* dx0;           // of the call's first state, or NULL
+  const char* dxT;     // of its gradient, or NULL
+  int64_t ld, state;   // bytes between tokens, and between the rows of a state
+  int n;               // tokens of the run
+};
+
+// The gradient of the run's token `row`, or of the row of q's state that stands for it,
+// is whole: not the run's own are left out.  (Its own code, which few rows come to.)
+template <int DT, int V, int W>
+__device__ __noinline__ void put_row(RowOut<V> out, ConvSeq q, int row, F2 a, F2 b) {
+  static_assert(V == 4, "two pairs");
+  if (row >= out.n || (row < 0 && (row >= q.lo || q.lo < 0))) return;
+  char* dst;
+  if (row >= q.lo) dst = out.dx + row * out.ld;
+  else if (out.dx0 != nullptr)
+    dst = out.dx0 + (static_cast<int64_t>(q.id) * (W - 1) + (W - 1 + row - q.lo)) * out.state;
+  else return;
+  F2 o[2] = {a, b};
+  Pack<DT, V> p;
+  if (out.dxT != nullptr && row >= q.hi - (W - 1)) {
+    load_pack(p, out.dxT + (static_cast<int64_t>(q.id) * (W - 1) + (row - q.hi + W - 1)) * out.state);
+    F2 more[2];
+    unpack_pairs(p, more);
+    o[0] = add2(o[0], more[0]);
+    o[1] = add2(o[1], more[1]);
+  }
+  pack_pairs(p, o);
+  store_pack(dst, p);
+}
 
 template <int DT, int W, bool PACKED>
-__global__ void __launch_bounds__(kConvThreads, 2)
+__global__ void __launch_bounds__(kConvThreads, 4)
 conv_bwd_kernel(const ConvParams P) {
   constexpr int V = kConvVec, K = V / 2, E = ElemSize<DT>::value, S = V * (W + 1);
-  constexpr int U = DT == SP_F32 ? 2 : 4;   // rows that a thread asks for at once
-  __shared__ float sums[kConvThreads][S + 1];
+  constexpr int U = kConvGroup;
+  using Ring = RowRing<DT, V, 2>;
+  constexpr int kSums = kConvThreads * (S + 1) * 4;
+  __shared__ __align__(16) char space[Ring::kSize > kSums ? Ring::kSize : kSums];
   pdl_wait();
   if (PACKED && blockIdx.x == 0 && threadIdx.x < 32)
     check_cu_seqlens(P.cu_seqlens, P.n_seqs, P.s, P.status);
@@ -49,17 +85,14 @@ conv_bwd_kernel(const ConvParams P) {
     const char* x = P.x[r] + (batch * P.s + i0) * P.ld_x + off;
     const char* dy = P.dy[r] + (batch * P.s + i0) * P.ld_dy + off;
     char* dx = P.out[r] + (batch * P.s + i0) * P.ld_out + off;
-    Pack<DT, V> nx[U], nd[U];
-    const char *ahead_x = x, *ahead_d = dy;
-    auto fetch = [&](int i) {
+    Ring ring(space);
+    ring.src[0] = x;
+    ring.src[1] = dy;
+    ring.ld[0] = P.ld_x;
+    ring.ld[1] = P.ld_dy;
+    cp_async_wait<0>();
 #pragma unroll
-      for (int u = 0; u < U; ++u, ahead_x += P.ld_x, ahead_d += P.ld_dy)
-        if (i + u < all_n) {
-          load_pack(nx[u], ahead_x);
-          load_pack(nd[u], ahead_d);
-        }
-    };
-    fetch(0);
+    for (int g = 0; g < kConvAhead; ++g) ring.ask(all_n - g * U);
     ConvSeq q = conv_seq<PACKED>(P, batch, i0, 0);
     F2 win[W - 1][K], wait[W - 1][K];
     load_window<DT, V, W>(P, x, x0, q, 0, win);
@@ -68,102 +101,105 @@ conv_bwd_kernel(const ConvParams P) {
 #pragma unroll
       for (int k = 0; k < K; ++k) wait[j][k] = 0;
 
-    // the gradient of the run's token `row`, or of the state's row that stands for it, is
-    // whole
-    auto emit = [&](int row, const F2 (&v)[K]) {
-      if (row >= n || (row < 0 && (row >= q.lo || q.lo < 0))) return;
-      char* dst;
-      if (row >= q.lo) dst = dx + row * P.ld_out;
-      else if (dx0 != nullptr)
-        dst = dx0 + (static_cast<int64_t>(q.id) * (W - 1) + (W - 1 + row - q.lo)) * P.c * E;
-      else return;
-      F2 o[K];
-#pragma unroll
-      for (int k = 0; k < K; ++k) o[k] = v[k];
-      if (dxT != nullptr && row >= q.hi - (W - 1)) {
-        Pack<DT, V> p;
-        load_pack(p, dxT + (static_cast<int64_t>(q.id) * (W - 1) + (row - q.hi + W - 1)) * P.c * E);
-        F2 more[K];
-        unpack_pairs(p, more);
-#pragma unroll
-        for (int k = 0; k < K; ++k) o[k] = add2(o[k], more[k]);
-      }
-      Pack<DT, V> p;
-      pack_pairs(p, o);
-      store_pack(dst, p);
-    };
+    const RowOut<V> out{dx, dx0, dxT, P.ld_out, static_cast<int64_t>(P.c) * E, n};
+    auto emit = [&](int row, const F2 (&v)[K]) { put_row<DT, V, W>(out, q, row, v[0], v[1]); };
     auto flush = [&](int end) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) emit(end - (W - 1) + j, wait[j]);
     };
 
-    bool open = true;
-    for (int i = 0; open && i < all_n; i += U) {
-      Pack<DT, V> cx[U], cd[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        cx[u] = nx[u];
-        cd[u] = nd[u];
-      }
-      fetch(i + U);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int tok = i + u;
-        if (!open || tok >= all_n) break;
-        if (PACKED && tok >= q.hi) {
-          flush(tok);
-          if (tok >= n) {
-            open = false;
-            break;
-          }
-          q = conv_seq<PACKED>(P, batch, i0, tok);
-          load_window<DT, V, W>(P, x, x0, q, tok, win);
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-            for (int k = 0; k < K; ++k) wait[j][k] = 0;
-        }
-        F2 v[K], g[K], o[K];
-        unpack_pairs(cx[u], v);
-        unpack_pairs(cd[u], g);
-        if (P.act == SP_ACT_SILU) {
-          taps.apply(win, v, o);
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            // sigmoid (1 + q (1 - sigmoid)), 1 - sigmoid = e sigmoid
-            // (exp(87) at most, whose reciprocal is normal: no product of infinity and 0)
-            const F2 e = exp2_of<DT, DT == SP_F32, -1>(DT == SP_F32 ? o[k] : held_above(o[k], -87.f));
-            const F2 sg = rcp2(add2(e, f2(1.f, 1.f)));
-            g[k] = mul2(g[k], fma2(mul2(o[k], mul2(e, sg)), sg, sg));
-          }
-        }
-        if (tok < n) {
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            db[k] = add2(db[k], g[k]);
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) dw[j][k] = fma2(g[k], win[j][k], dw[j][k]);
-            dw[W - 1][k] = fma2(g[k], v[k], dw[W - 1][k]);
-          }
-        }
-        F2 done[K];
+    // One token: its gradient joins the parameters' (OWN) and those of the tokens before
+    // it, of which the one W - 1 back is whole.
+    auto one = [&](int u, bool own, F2 (&done)[K]) {
+      Pack<DT, V> p;
+      F2 v[K], g[K], o[K];
+      ring.row(u, 0, p);
+      unpack_pairs(p, v);
+      ring.row(u, 1, p);
+      unpack_pairs(p, g);
+      if (P.act == SP_ACT_SILU) {
+        taps.apply(win, v, o);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          done[k] = fma2(taps.w[0][k], g[k], wait[0][k]);
-#pragma unroll
-          for (int j = 0; j + 1 < W - 1; ++j)
-            wait[j][k] = fma2(taps.w[j + 1][k], g[k], wait[j + 1][k]);
-          wait[W - 2][k] = mul2(taps.w[W - 1][k], g[k]);
+          // sigmoid (1 + q (1 - sigmoid)), 1 - sigmoid = e sigmoid
+          // (exp(87) at most, whose reciprocal is normal: no product of infinity and 0)
+          const F2 e = exp2_of<DT, DT == SP_F32, -1>(DT == SP_F32 ? o[k] : held_above(o[k], -87.f));
+          const F2 sg = rcp2(add2(e, f2(1.f, 1.f)));
+          g[k] = mul2(g[k], fma2(mul2(o[k], mul2(e, sg)), sg, sg));
         }
-        shift<W, K>(win, v);
-        emit(tok - (W - 1), done);
       }
+      if (own) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          db[k] = add2(db[k], g[k]);
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) dw[j][k] = fma2(g[k], win[j][k], dw[j][k]);
+          dw[W - 1][k] = fma2(g[k], v[k], dw[W - 1][k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        done[k] = fma2(taps.w[0][k], g[k], wait[0][k]);
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j)
+          wait[j][k] = fma2(taps.w[j + 1][k], g[k], wait[j + 1][k]);
+        wait[W - 2][k] = mul2(taps.w[W - 1][k], g[k]);
+      }
+      shift<W, K>(win, v);
+    };
+    // Groups of rows from `lo` on and before `hi` are whole tokens of the run and of one
+    // sequence, stored as they are.
+    auto group_lo = [&] { return (q.lo > 0 ? q.lo : 0) + W - 1; };
+    auto group_hi = [&] { return (q.hi < n ? q.hi : n) - U; };
+    int lo = group_lo(), hi = group_hi();
+    char* to = dx - (W - 1) * P.ld_out;
+    bool open = true;
+    for (int i = 0; open && i < all_n; i += U) {
+      ring.ask(all_n - i - kConvAhead * U);
+      cp_async_wait<kConvAhead>();
+      if (i >= lo && i <= hi) {
+#pragma unroll
+        for (int u = 0; u < U; ++u, to += P.ld_out) {
+          F2 done[K];
+          one(u, true, done);
+          Pack<DT, V> p;
+          pack_pairs(p, done);
+          store_pack(to, p);
+        }
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u, to += P.ld_out) {
+          const int tok = i + u;
+          if (tok >= all_n) break;
+          if (PACKED && tok >= q.hi) {
+            flush(tok);
+            if (tok >= n) {
+              open = false;
+              break;
+            }
+            q = conv_seq<PACKED>(P, batch, i0, tok);
+            load_window<DT, V, W>(P, x, x0, q, tok, win);
+            lo = group_lo(), hi = group_hi();
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+              for (int k = 0; k < K; ++k) wait[j][k] = 0;
+          }
+          F2 done[K];
+          one(u, tok < n, done);
+          emit(tok - (W - 1), done);
+        }
+      }
+      ring.next();
     }
     if (open && i0 + all_n == P.s) flush(all_n);
   }
   if (P.ws == nullptr) return;
 
   // the block's parameter gradients: its slots in order
+  cp_async_wait<0>();
+  __syncthreads();                     // the rows' space is free
+  float(*sums)[S + 1] = reinterpret_cast<float(*)[S + 1]>(space);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll

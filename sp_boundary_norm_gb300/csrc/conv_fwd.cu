@@ -5,12 +5,11 @@
 
 namespace spb {
 
-constexpr int kConvAhead = 4;          // rows that a thread asks for at once
-
 template <int DT, int W, bool PACKED>
-__global__ void __launch_bounds__(kConvThreads, DT == SP_F32 ? 2 : 3)
+__global__ void __launch_bounds__(kConvThreads, 6)
 conv_fwd_kernel(const ConvParams P) {
-  constexpr int V = kConvVec, K = V / 2, E = ElemSize<DT>::value, U = kConvAhead;
+  constexpr int V = kConvVec, K = V / 2, E = ElemSize<DT>::value, U = kConvGroup;
+  __shared__ __align__(16) char ring_space[RowRing<DT, V, 1>::kSize];
   pdl_wait();
   if (PACKED && blockIdx.x == 0 && threadIdx.x < 32)
     check_cu_seqlens(P.cu_seqlens, P.n_seqs, P.s, P.status);
@@ -27,42 +26,48 @@ conv_fwd_kernel(const ConvParams P) {
   const char* x = P.x[r] + (batch * P.s + i0) * P.ld_x + vec * V * E;
   char* y = P.out[r] + (batch * P.s + i0) * P.ld_out + vec * V * E;
   const char* x0 = P.x0[r] != nullptr ? P.x0[r] + vec * V * E : nullptr;
-  Pack<DT, V> next[U];
-  const char* ahead = x;
+  RowRing<DT, V, 1> ring(ring_space);
+  ring.src[0] = x;
+  ring.ld[0] = P.ld_x;
 #pragma unroll
-  for (int u = 0; u < U; ++u, ahead += P.ld_x)
-    if (u < n) load_pack(next[u], ahead);
+  for (int g = 0; g < kConvAhead; ++g) ring.ask(n - g * U);
   ConvSeq q = conv_seq<PACKED>(P, batch, i0, 0);
   F2 win[W - 1][K];
   load_window<DT, V, W>(P, x, x0, q, 0, win);
   Taps<DT, V, W> taps;
   taps.load(P, static_cast<int64_t>(r) * P.c + vec * V);
-  for (int i = 0; i < n; i += U) {
-    Pack<DT, V> now[U];
+  auto one = [&](int u, char* dst) {
+    Pack<DT, V> p;
+    F2 v[K], o[K];
+    ring.row(u, 0, p);
+    unpack_pairs(p, v);
+    taps.apply(win, v, o);
+    shift<W, K>(win, v);
+    if (P.act == SP_ACT_SILU) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) now[u] = next[u];
-#pragma unroll
-    for (int u = 0; u < U; ++u, ahead += P.ld_x)
-      if (i + U + u < n) load_pack(next[u], ahead);
-#pragma unroll
-    for (int u = 0; u < U; ++u, y += P.ld_out) {
-      if (i + u >= n) break;
-      if (PACKED && i + u >= q.hi) {
-        q = conv_seq<PACKED>(P, batch, i0, i + u);
-        load_window<DT, V, W>(P, x, x0, q, i + u, win);
-      }
-      F2 v[K], o[K];
-      unpack_pairs(now[u], v);
-      taps.apply(win, v, o);
-      shift<W, K>(win, v);
-      if (P.act == SP_ACT_SILU) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          o[k] = mul2(o[k], rcp2(add2(exp2_of<DT, false, -1>(o[k]), f2(1.f, 1.f))));
-      }
-      pack_pairs(now[u], o);
-      store_pack(y, now[u]);
+      for (int k = 0; k < K; ++k)
+        o[k] = mul2(o[k], rcp2(add2(exp2_of<DT, false, -1>(o[k]), f2(1.f, 1.f))));
     }
+    pack_pairs(p, o);
+    store_pack(dst, p);
+  };
+  for (int i = 0; i < n; i += U) {
+    ring.ask(n - i - kConvAhead * U);
+    cp_async_wait<kConvAhead>();
+    if (i + U <= n && (!PACKED || i + U <= q.hi)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u, y += P.ld_out) one(u, y);
+    } else {                           // the run's end, or a sequence's
+#pragma unroll 1
+      for (int u = 0; u < U && i + u < n; ++u, y += P.ld_out) {
+        if (PACKED && i + u >= q.hi) {
+          q = conv_seq<PACKED>(P, batch, i0, i + u);
+          load_window<DT, V, W>(P, x, x0, q, i + u, win);
+        }
+        one(u, y);
+      }
+    }
+    ring.next();
   }
   // The state after a dense sequence comes from the thread of its first run, the only
   // one that reads x0 (a run has W - 1 tokens at least, or the whole sequence), so xT
@@ -127,9 +132,9 @@ static cudaError_t launch_width(ConvParams& p, cudaStream_t st) {
 template <int DT>
 static cudaError_t launch_dtype(ConvParams& p, cudaStream_t st) {
   p.vecs = p.c / kConvVec;
-  // runs of 32 tokens, or shorter ones until every SM has its warps
+  // runs of 64 tokens, or shorter ones until every SM has its warps
   const int64_t want = static_cast<int64_t>(device_sm_count()) * 1024;
-  p.run = 32;
+  p.run = 64;
   while (p.run > 4 && (p.s + p.run - 1) / p.run * p.b * p.t * p.vecs < want) p.run /= 2;
   p.runs = (p.s + p.run - 1) / p.run;
   switch (p.width) {
