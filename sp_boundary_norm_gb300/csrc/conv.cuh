@@ -119,19 +119,24 @@ struct RowRing {
   __device__ __forceinline__ explicit RowRing(char* smem) : mine(smem + threadIdx.x * kBytes) {}
   // asks for the next group's first `rows` rows
   __device__ __forceinline__ void ask(int rows) {
+    if (rows >= kConvGroup) {
 #pragma unroll
-    for (int u = 0; u < kConvGroup; ++u)
-#pragma unroll
-      for (int t = 0; t < TENSORS; ++t) {
-        char* dst = mine + put + (u * TENSORS + t) * kConvThreads * kBytes;
-        if (u < rows) {
-          if constexpr (kBytes == 16) cp_async16(dst, src[t]);
-          else cp_async8(dst, src[t]);
-        }
-        src[t] += ld[t];
-      }
+      for (int u = 0; u < kConvGroup; ++u) ask_row(u);
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < rows; ++u) ask_row(u);
+    }
     cp_async_commit();
     put = put == (kGroups - 1) * kStep ? 0 : put + kStep;
+  }
+  __device__ __forceinline__ void ask_row(int u) {
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t) {
+      char* dst = mine + put + (u * TENSORS + t) * kConvThreads * kBytes;
+      if constexpr (kBytes == 16) cp_async16(dst, src[t]);
+      else cp_async8(dst, src[t]);
+      src[t] += ld[t];
+    }
   }
   __device__ __forceinline__ void row(int u, int t, Pack<DT, V>& p) const {
     const char* from = mine + get + (u * TENSORS + t) * kConvThreads * kBytes;

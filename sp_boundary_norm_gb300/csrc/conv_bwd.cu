@@ -9,7 +9,7 @@
 
 namespace spb {
 
-constexpr int kConvRunB = 64;
+constexpr int kConvBlocksB = 4;        // of an SM, by their registers
 
 // Where a run's gradients go; this lane's channels.
 template <int V>
@@ -46,7 +46,7 @@ __device__ __noinline__ void put_row(RowOut<V> out, ConvSeq q, int row, F2 a, F2
 }
 
 template <int DT, int W, bool PACKED>
-__global__ void __launch_bounds__(kConvThreads, 4)
+__global__ void __launch_bounds__(kConvThreads, kConvBlocksB)
 conv_bwd_kernel(const ConvParams P) {
   constexpr int V = kConvVec, K = V / 2, E = ElemSize<DT>::value, S = V * (W + 1);
   constexpr int U = kConvGroup;
@@ -121,11 +121,9 @@ conv_bwd_kernel(const ConvParams P) {
         taps.apply(win, v, o);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          // sigmoid (1 + q (1 - sigmoid)), 1 - sigmoid = e sigmoid
-          // (exp(87) at most, whose reciprocal is normal: no product of infinity and 0)
-          const F2 e = exp2_of<DT, DT == SP_F32, -1>(DT == SP_F32 ? o[k] : held_above(o[k], -87.f));
-          const F2 sg = rcp2(add2(e, f2(1.f, 1.f)));
-          g[k] = mul2(g[k], fma2(mul2(o[k], mul2(e, sg)), sg, sg));
+          // sigmoid + silu (1 - sigmoid)
+          const F2 sg = rcp2(add2(exp2_of<DT, false, -1>(o[k]), f2(1.f, 1.f)));
+          g[k] = mul2(g[k], fma2(mul2(o[k], sg), fma2(sg, f2(-1.f, -1.f), f2(1.f, 1.f)), sg));
         }
       }
       if (own) {
@@ -225,17 +223,15 @@ conv_bwd_kernel(const ConvParams P) {
   }
 }
 
-// dweight and dbias: the parts in order.
-__global__ void __launch_bounds__(kConvThreads)
+// dweight and dbias from the blocks' parts.
+__global__ void __launch_bounds__(kPartThreads)
 conv_params_kernel(const float* ws, int64_t channels, int width, int parts, float* dweight,
                    float* dbias) {
   pdl_wait();
   const int64_t n = channels * (width + 1);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
-  if (i >= n) return;
-  float a = 0.f;
-#pragma unroll 8
-  for (int k = 0; k < parts; ++k) a += ws[k * n + i];
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
+  const float a = sum_parts(ws, n, parts, i);
+  if (threadIdx.x >= 32 || i >= n) return;
   const int64_t ch = i / (width + 1);
   const int j = static_cast<int>(i - ch * (width + 1));
   if (j < width) {
@@ -291,20 +287,28 @@ static cudaError_t launch_dtype(ConvParams& p, cudaStream_t st) {
   }
 }
 
-// Vectors side by side in a block, and its slabs and runs.
+// Vectors side by side in a block, its slabs, parts and runs.
 static void conv_bwd_split(ConvParams* p, int64_t b, int64_t s, int c, int t) {
   p->vecs = c / kConvVec;
+  // as many lanes side by side as leave few of them without a vector
   p->lanes = 32;
-  while (p->lanes > 2 && p->lanes / 2 >= p->vecs) p->lanes /= 2;
+  auto idle = [&] { return (p->lanes - p->vecs % p->lanes) % p->lanes; };
+  while (p->lanes > 8 && idle() * 8 > p->vecs) p->lanes /= 2;
   p->slabs = t * ((p->vecs + p->lanes - 1) / p->lanes);
-  const int64_t want = static_cast<int64_t>(device_sm_count()) * 4;
-  const int slots = kConvThreads / p->lanes;
-  p->run = kConvRunB;
-  while (p->run > 4 && ((s + p->run - 1) / p->run * b + slots - 1) / slots * p->slabs < want)
-    p->run /= 2;
-  p->runs = (s + p->run - 1) / p->run;
+  const int64_t slots = kConvThreads / p->lanes, tokens = b * s;
+  // one wave of blocks, whose threads have runs of 64 tokens or more, all as many
+  const int64_t wave = static_cast<int64_t>(device_sm_count()) * kConvBlocksB;
+  int64_t parts = wave / p->slabs > 1 ? wave / p->slabs : 1;
+  const int64_t least = (tokens + 4 * slots - 1) / (4 * slots);
+  if (parts > least) parts = least;
+  int64_t rounds = tokens / (slots * parts * 64);
+  if (rounds < 1) rounds = 1;
+  const int64_t pieces = slots * parts * rounds / b;             // of a batch row
+  int64_t run = pieces > 1 ? (s + pieces - 1) / pieces : s;
+  run = run < 4 ? 4 : run > 256 ? 256 : (run + 3) / 4 * 4;
+  p->run = static_cast<int32_t>(run);
+  p->runs = (s + run - 1) / run;
   const int64_t most = (p->runs * b + slots - 1) / slots;
-  int64_t parts = (want + p->slabs - 1) / p->slabs;
   p->parts = static_cast<int32_t>(parts < most ? parts : most);
 }
 
@@ -326,8 +330,7 @@ cudaError_t launch_conv_bwd(ConvParams p, int dtype, float* dweight, float* dbia
   void* args[] = {&ws, &channels, &p.width, &p.parts, &dweight, &dbias};
   const int64_t n = channels * (p.width + 1);
   return launch_pdl(reinterpret_cast<const void*>(&conv_params_kernel),
-                    dim3(static_cast<unsigned>((n + kConvThreads - 1) / kConvThreads)),
-                    dim3(kConvThreads), 0, args, st);
+                    dim3(static_cast<unsigned>((n + 31) / 32)), dim3(kPartThreads), 0, args, st);
 }
 
 }  // namespace spb

@@ -260,4 +260,24 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int64_t tok) {
   return lo;
 }
 
+// The sum of column i of from[parts][n], for blocks of kPartThreads threads of which 32
+// columns are side by side: each warp takes every eighth part, and the warps are added in
+// order.  The first warp has the sums.
+constexpr int kPartThreads = 256;
+__device__ __forceinline__ float sum_parts(const float* from, int64_t n, int64_t parts, int64_t i) {
+  __shared__ float rows[kPartThreads / 32][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float a = 0.f;
+  if (i < n) {
+#pragma unroll 4
+    for (int64_t k = warp; k < parts; k += kPartThreads / 32) a += __ldcs(from + k * n + i);
+  }
+  rows[warp][lane] = a;
+  __syncthreads();
+  a = 0.f;
+#pragma unroll
+  for (int w = 0; w < kPartThreads / 32; ++w) a += rows[w][lane];
+  return a;
+}
+
 }  // namespace spb

@@ -24,9 +24,9 @@ static cudaError_t launch_bwd(const SsmParams& p, const SsmParamGrads& g, cudaSt
     int n = p.n;
     SsmParamGrads grads = g;
     void* args[] = {&from, &channels, &n, &parts, &grads};
-    const int64_t threads = channels * (n + 2);
+    const int64_t columns = channels * (n + 2);
     e = launch_pdl(reinterpret_cast<const void*>(&ssm_params_kernel),
-                   dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, args, st);
+                   dim3(static_cast<unsigned>((columns + 31) / 32)), dim3(kPartThreads), 0, args, st);
   }
   return e;
 }

@@ -539,16 +539,14 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const SsmParams P) {
   else store_pack(P.dC[r] + row * P.ld_dC + n, p);
 }
 
-// The parameters' gradients: the blocks of a channel in order.
-__global__ void __launch_bounds__(256)
+// The parameters' gradients from the blocks of a channel.
+__global__ void __launch_bounds__(kPartThreads)
 ssm_params_kernel(const float* from, int64_t channels, int n, int64_t parts, SsmParamGrads g) {
   pdl_wait();
   const int64_t all = channels * (n + 2);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= all) return;
-  float a = 0.f;
-#pragma unroll 8
-  for (int64_t k = 0; k < parts; ++k) a += from[k * all + i];
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
+  const float a = sum_parts(from, all, parts, i);
+  if (threadIdx.x >= 32 || i >= all) return;
   if (i < channels * n) {
     if (g.dA != nullptr) g.dA[i] = a;
   } else if (i < channels * (n + 1)) {
