@@ -135,6 +135,20 @@ rope_kernel(const RopeArgs<AXES> P) {
   // bytes from an item's first load to its second
   const uint32_t second = LAYOUT == SP_ROPE_HALF ? static_cast<uint32_t>(P.half) * E : E;
   const int64_t n_tasks = P.tokens * P.chunks;
+  // Several axes: the frequencies and axes of a lane's first pairs stay in registers, and
+  // their coordinates are asked for before the heads (lanes that read different words of a
+  // parameter wait for each other).
+  constexpr int kHeld = AXES ? 2 : 0;
+  uint64_t held_turns[kHeld + 1];
+  int64_t held_axis[kHeld + 1], coords[kHeld + 1];
+  if constexpr (AXES) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int i = lane + 32 * k < P.half ? lane + 32 * k : 0;
+      held_turns[k] = P.turns[i];
+      held_axis[k] = P.axis[i] * P.tokens;
+    }
+  }
   for (int64_t task = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; task < n_tasks;
        task += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
     const int64_t tok = divide(task, P.chunks, n_tasks);
@@ -154,6 +168,10 @@ rope_kernel(const RopeArgs<AXES> P) {
         }
       }
     };
+    if constexpr (AXES) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) coords[k] = __ldg(P.positions + held_axis[k] + tok);
+    }
     // the first heads are on their way while the angles are computed
     fetch(h0, my);
     Held held;
@@ -169,14 +187,22 @@ rope_kernel(const RopeArgs<AXES> P) {
       pos = tok - divide(tok, P.s, P.tokens) * P.s + P.first;
     }
     __syncwarp();
-    for (int i = lane; i < P.half; i += 32) {
-      if constexpr (AXES) pos = __ldg(P.positions + P.axis[i] * P.tokens + tok);
-      const uint64_t turn = static_cast<uint64_t>(pos) * P.turns[i];
+    auto angle = [&](int i, int64_t at, uint64_t frequency) {
+      const uint64_t turn = static_cast<uint64_t>(at) * frequency;
       const float half_turns =
           static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
       float sn, cn;
       sincospif(half_turns, &sn, &cn);
       cs[warp][i] = make_float2(cn * P.cos_scale, sn * P.sin_scale);
+    };
+    if constexpr (AXES) {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (lane + 32 * k < P.half) angle(lane + 32 * k, coords[k], held_turns[k]);
+      for (int i = lane + 32 * kHeld; i < P.half; i += 32)
+        angle(i, __ldg(P.positions + P.axis[i] * P.tokens + tok), P.turns[i]);
+    } else {
+      for (int i = lane; i < P.half; i += 32) angle(i, pos, P.turns[i]);
     }
     __syncwarp();
     for (int v0 = 0; v0 < items; v0 += width) {
