@@ -123,7 +123,7 @@ __device__ __forceinline__ float pow2(float x) {
   return x;
 }
 
-// All of the block's threads; its halves come here from different code.
+// All of the block's threads; its parts come here from different code.
 template <int THREADS>
 __device__ __forceinline__ void meet() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");

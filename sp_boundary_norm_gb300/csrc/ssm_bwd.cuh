@@ -23,9 +23,9 @@ struct SsmBack {
   using L = SsmLanes<N>;
   static constexpr int E = ElemSize<DT>::value;
   static constexpr int T = kSsmRun;
-  static constexpr int kWarps = kSsmHalf / 32;                 // that hold states
+  static constexpr int kWarps = kSsmPart / 32;                 // that hold states
   static constexpr int kBlockCh = kWarps * L::kChannels;
-  static constexpr int V = kBlockCh * T / kSsmHalf;
+  static constexpr int V = kBlockCh * T / kSsmPart;
   static constexpr int kStages = 3;
   static constexpr int kRow = kBlockCh * E + 16;
   static constexpr int kShared = 2 * N * E;
@@ -40,7 +40,7 @@ struct SsmBack {
 };
 
 template <int DT, int N>
-__global__ void __launch_bounds__(2 * kSsmHalf, 1)
+__global__ void __launch_bounds__(2 * kSsmPart, 1)
 ssm_bwd_kernel(const SsmParams P) {
   using W = SsmBack<DT, N>;
   using L = SsmLanes<N>;
@@ -67,7 +67,7 @@ ssm_bwd_kernel(const SsmParams P) {
 
   if (warp >= W::kWarps) {
     // ------------------------------------------------------------ preparing --
-    const int ht = tid - kSsmHalf;
+    const int ht = tid - kSsmPart;
     const char* src[4] = {P.dt[r] + row0 * P.ld_dt + at.ch0 * E,
                           P.u[r] + row0 * P.ld_u + at.ch0 * E,
                           P.dy[r] + row0 * P.ld_dy + at.ch0 * E,
@@ -81,7 +81,7 @@ ssm_bwd_kernel(const SsmParams P) {
       const int n_tok = tokens_of(t0);
       constexpr int kPieces = W::kBlockCh * E / 16;
 #pragma unroll
-      for (int i = ht; i < T * kPieces; i += kSsmHalf) {
+      for (int i = ht; i < T * kPieces; i += kSsmPart) {
         const int tok = i / kPieces, p = (i % kPieces) * 16;
         if (tok >= n_tok || p >= live_bytes) continue;
         char* dst = st + tok * W::kRow + p;
@@ -93,7 +93,7 @@ ssm_bwd_kernel(const SsmParams P) {
       constexpr int kP = N * E / 16;
       char* sh = st + 4 * T * W::kRow;
 #pragma unroll
-      for (int i = ht; i < T * kP; i += kSsmHalf) {
+      for (int i = ht; i < T * kP; i += kSsmPart) {
         const int tok = i / kP, p = (i % kP) * 16;
         if (tok >= n_tok) continue;
         cp_async16(sh + tok * W::kShared + p, src_b + (t0 + tok) * P.ld_B + p);
@@ -151,7 +151,7 @@ ssm_bwd_kernel(const SsmParams P) {
       const char* sh = smem + (k % W::kStages) * W::kStage + 4 * T * W::kRow;
       float* bc = reinterpret_cast<float*>(bcs + (k & 1) * W::kBC);
 #pragma unroll
-      for (int i = ht; i < T * 2 * N / 4; i += kSsmHalf) {
+      for (int i = ht; i < T * 2 * N / 4; i += kSsmPart) {
         Pack<DT, 4> q;
         float f[4];
         lds_pack(q, sh + i * 4 * E);
@@ -166,7 +166,7 @@ ssm_bwd_kernel(const SsmParams P) {
       // dB and dC: the block's warps in order
       const char* from = sums + (k & 1) * W::kWarps * W::kSum;
 #pragma unroll
-      for (int i = ht; i < T * 2 * N / 4; i += kSsmHalf) {
+      for (int i = ht; i < T * 2 * N / 4; i += kSsmPart) {
         const int tok = i / (N / 2), e = (i % (N / 2)) * 4;
         if (tok >= n_tok) continue;
         F2 a = 0, b = 0;
@@ -223,7 +223,7 @@ ssm_bwd_kernel(const SsmParams P) {
     Kept even, odd;                    // of even and of odd steps
     auto step = [&](int k, Kept& next) {
       cp_async_wait<1>();              // step k + 1's rows
-      meet<2 * kSsmHalf>();
+      meet<2 * kSsmPart>();
       // (step k's rows have been prepared: step k + 3 takes their place)
       if (k + 3 < n_runs) ask(k + 3);
       cp_async_commit();
@@ -233,7 +233,7 @@ ssm_bwd_kernel(const SsmParams P) {
     if (n_runs > 2) ask(2);
     cp_async_commit();
     cp_async_wait<2>();                // step 0's rows
-    meet<2 * kSsmHalf>();
+    meet<2 * kSsmPart>();
     if (n_runs > 0) prepare(0, even);
     for (int k = 0; k <= n_runs; k += 2) {
       step(k, odd);
@@ -249,7 +249,7 @@ ssm_bwd_kernel(const SsmParams P) {
       sum[my * (W::kBlockCh / 2) + part * (V / 2) + i] = dD[i];
       sum[(T + my) * (W::kBlockCh / 2) + part * (V / 2) + i] = dbias[i];
     }
-    asm volatile("bar.sync 2, %0;" ::"n"(kSsmHalf) : "memory");
+    asm volatile("bar.sync 2, %0;" ::"n"(kSsmPart) : "memory");
     if (ht < W::kBlockCh && ht / (W::kBlockCh / 2) < 2) {
       const int which = ht / (W::kBlockCh / 2), c = ht % (W::kBlockCh / 2);
       F2 a = 0;
@@ -317,9 +317,9 @@ ssm_bwd_kernel(const SsmParams P) {
   const int kept = lane / G / kSame * kKept;
   const int put_at = (kept / S) * N + n0 + kept % S;
 
-  meet<2 * kSsmHalf>();                // (step 0 is prepared)
+  meet<2 * kSsmPart>();                // (step 0 is prepared)
   for (int k = 0; k < n_runs; ++k) {
-    meet<2 * kSsmHalf>();
+    meet<2 * kSsmPart>();
     const float* shared = reinterpret_cast<const float*>(bcs + (k & 1) * W::kBC) + n0;
     const char* dd = dds + (k & 1) * T * W::kDRow + dd_at;
     const char* ee = es + (k & 1) * T * W::kYRow + ch * 4;
@@ -501,7 +501,7 @@ ssm_bwd_kernel(const SsmParams P) {
     if (marks.starts == 0u && n_tok == T) go(std::false_type{});
     else go(std::true_type{});
   }
-  meet<2 * kSsmHalf>();                // (the preparers finish the last step)
+  meet<2 * kSsmPart>();                // (the preparers finish the last step)
   if (!packed && at.chunk == 0 && P.hT[r] != nullptr)
     store_both(P.hT[r], at.batch * state_step + state_at, back);
   if (P.partial_params != nullptr)
@@ -564,7 +564,7 @@ static cudaError_t launch_back(const SsmParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<SsmParams*>(&p)};
   const int64_t grid = static_cast<int64_t>(p.b) * p.chunks * p.t * p.groups * p.slabs;
-  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(2 * kSsmHalf), W::kSmem, args, st);
+  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(2 * kSsmPart), W::kSmem, args, st);
 }
 
 }  // namespace spb

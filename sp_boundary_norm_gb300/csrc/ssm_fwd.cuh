@@ -3,9 +3,10 @@
 //
 // A block takes 64 channels of one rank's group (32 and 16 of 32 and 64 states) and
 // walks its chunk of a batch row, 16 tokens a step.  Four warps hold the states and do
-// nothing else; four others ask for rows ahead (16-byte asynchronous copies), prepare
-// the next step's tokens (softplus, d u, B and C as float32) and finish the last one's
-// (D u, silu(z), the stores).  Both halves meet once a step.
+// nothing else; four ask for rows ahead (16-byte asynchronous copies) and prepare the
+// next step's tokens (softplus, d u, B and C as float32); four add a channel's lanes'
+// parts of the last step's sums and finish it (D u, silu(z), the stores).  All meet once
+// a step.
 #include "ssm.cuh"
 
 namespace spb {
@@ -16,7 +17,10 @@ constexpr int kSsmEnds = 1;    // a chunk's last state from a zero one, the sum 
 constexpr int kSsmBack = 2;    // a chunk's gradient for the state before it, from a zero
                                // one, and the sum of its steps
 
-constexpr int kSsmHalf = 128;          // threads that hold states, and that prepare
+constexpr int kSsmPart = 128;          // threads that hold states, that prepare, that finish
+__host__ __device__ constexpr int walk_threads(int mode) {
+  return mode == kSsmOut ? 3 * kSsmPart : 2 * kSsmPart;
+}
 
 // Rows in shared memory are padded so that the lanes of an access use different banks.
 template <int DT, int N>
@@ -24,8 +28,8 @@ struct SsmWalk {
   using L = SsmLanes<N>;
   static constexpr int E = ElemSize<DT>::value;
   static constexpr int T = kSsmTile;
-  static constexpr int kBlockCh = kSsmHalf / 32 * L::kChannels;
-  static constexpr int V = kBlockCh * T / kSsmHalf;            // channels of a preparer's token
+  static constexpr int kBlockCh = kSsmPart / 32 * L::kChannels;
+  static constexpr int V = kBlockCh * T / kSsmPart;            // channels of a preparer's token
   static constexpr int kStages = 5;
   static constexpr int kRow = kBlockCh * E + 16;
   static constexpr int kShared = 2 * N * E;                    // B and C of a token
@@ -34,11 +38,12 @@ struct SsmWalk {
   static constexpr int kDPart = V * 8 + (V > 2 ? 16 : 0);      // (d, d u) of V channels
   static constexpr int kDRow = kBlockCh / V * kDPart;
   static constexpr int kYRow = kBlockCh * 4 + 32;
-  static constexpr size_t kSmem = kStages * kStage + 2 * (kBC + T * (kDRow + kYRow));
+  static constexpr int kY = T * L::kLanes * kYRow;             // of each lane of a channel
+  static constexpr size_t kSmem = kStages * kStage + 2 * (kBC + T * kDRow + kY);
 };
 
 template <int DT, int N, int MODE>
-__global__ void __launch_bounds__(2 * kSsmHalf, 2)
+__global__ void __launch_bounds__(walk_threads(MODE), 1)
 ssm_walk_kernel(const SsmParams P) {
   using W = SsmWalk<DT, N>;
   using L = SsmLanes<N>;
@@ -62,43 +67,60 @@ ssm_walk_kernel(const SsmParams P) {
   auto tile_of = [&](int k) { return static_cast<int64_t>(kBack ? n_tiles - 1 - k : k) * T; };
   auto tokens_of = [&](int64_t t0) { return at.len - t0 < T ? static_cast<int>(at.len - t0) : T; };
 
-  if (warp >= kSsmHalf / 32) {
+  if (warp >= kSsmPart / 32) {
     // ------------------------------------------------------------ preparing --
-    const int ht = tid - kSsmHalf;
+    const bool finisher = warp >= 2 * kSsmPart / 32;
+    const int ht = tid - (finisher ? 2 : 1) * kSsmPart;
     const bool gated = MODE != kSsmEnds && P.gated;
-    // the rows that a walk reads: dt, u (back: dy), z (not for ends); B (back: C), and C
-    const char* src[3] = {P.dt[r] + row0 * P.ld_dt + at.ch0 * E,
-                          (kBack ? P.dy[r] + row0 * P.ld_dy : P.u[r] + row0 * P.ld_u) + at.ch0 * E,
-                          gated ? P.z[r] + row0 * P.ld_z + at.ch0 * E : nullptr};
+    // The rows that a walk reads: dt, u (back: dy), z (not for ends); B (back: C), and C.
+    // A thread's pieces of 16 bytes lie `kRows` (`kRowsB`) tokens apart.
+    constexpr int kPieces = W::kBlockCh * E / 16, kRows = kSsmPart / kPieces;
+    constexpr int kPiecesB = N * E / 16, kRowsB = kSsmPart / kPiecesB;
+    static_assert(kSsmPart % kPieces == 0 && kSsmPart % kPiecesB == 0, "whole rows");
+    const int tok_p = ht / kPieces, at_p = ht % kPieces * 16;
+    const int tok_b = ht / kPiecesB, at_b = ht % kPiecesB * 16;
+    const bool live_p = at_p < at.live * E;
     const int64_t lds[3] = {P.ld_dt, kBack ? P.ld_dy : P.ld_u, P.ld_z};
-    const char* src_b = (kBack ? P.C[r] + row0 * P.ld_C : P.B[r] + row0 * P.ld_B) + at.group * N * E;
-    const char* src_c = P.C[r] + row0 * P.ld_C + at.group * N * E;
     const int64_t ld_b = kBack ? P.ld_C : P.ld_B;
-    const int live_bytes = at.live * E;
-    auto ask = [&](int k) {
-      char* st = smem + (k % W::kStages) * W::kStage;
-      const int64_t t0 = tile_of(k);
-      const int n_tok = tokens_of(t0);
-      constexpr int kPieces = W::kBlockCh * E / 16;
+    const int64_t row_p = row0 + tile_of(0) + tok_p, row_b = row0 + tile_of(0) + tok_b;
+    const char* src[3] = {P.dt[r] + row_p * P.ld_dt + at.ch0 * E + at_p,
+                          (kBack ? P.dy[r] : P.u[r]) + row_p * lds[1] + at.ch0 * E + at_p,
+                          gated ? P.z[r] + row_p * P.ld_z + at.ch0 * E + at_p : nullptr};
+    const char* src_b = (kBack ? P.C[r] : P.B[r]) + row_b * ld_b + at.group * N * E + at_b;
+    const char* src_c = P.C[r] + row_b * P.ld_C + at.group * N * E + at_b;
+    char* put = smem;                  // the stage of the next step asked for
+    int asked = 0;
+    auto ask = [&] {                   // the rows of the next step that is not yet asked for
+      if (asked < n_tiles) {
+        const int n_tok = tokens_of(tile_of(asked));
+        char* dst = put + tok_p * W::kRow + at_p;
 #pragma unroll
-      for (int i = ht; i < T * kPieces; i += kSsmHalf) {
-        const int tok = i / kPieces, p = (i % kPieces) * 16;
-        if (tok >= n_tok || p >= live_bytes) continue;
-        char* dst = st + tok * W::kRow + p;
-        cp_async16(dst, src[0] + (t0 + tok) * lds[0] + p);
-        cp_async16(dst + T * W::kRow, src[1] + (t0 + tok) * lds[1] + p);
-        if (gated) cp_async16(dst + 2 * T * W::kRow, src[2] + (t0 + tok) * lds[2] + p);
-      }
-      constexpr int kP = N * E / 16;
-      char* sh = st + 3 * T * W::kRow;
+        for (int i = 0; i * kRows < T; ++i) {
+          if (live_p && tok_p + i * kRows < n_tok && tok_p + i * kRows < T) {
+            cp_async16(dst + i * kRows * W::kRow, src[0] + i * kRows * lds[0]);
+            cp_async16(dst + (T + i * kRows) * W::kRow, src[1] + i * kRows * lds[1]);
+            if (gated) cp_async16(dst + (2 * T + i * kRows) * W::kRow, src[2] + i * kRows * lds[2]);
+          }
+        }
+        char* sh = put + 3 * T * W::kRow + tok_b * W::kShared + at_b;
 #pragma unroll
-      for (int i = ht; i < T * kP; i += kSsmHalf) {
-        const int tok = i / kP, p = (i % kP) * 16;
-        if (tok >= n_tok) continue;
-        cp_async16(sh + tok * W::kShared + p, src_b + (t0 + tok) * ld_b + p);
-        if (MODE == kSsmOut)
-          cp_async16(sh + tok * W::kShared + N * E + p, src_c + (t0 + tok) * P.ld_C + p);
+        for (int i = 0; i * kRowsB < T; ++i) {
+          if (tok_b + i * kRowsB < n_tok && tok_b + i * kRowsB < T) {
+            cp_async16(sh + i * kRowsB * W::kShared, src_b + i * kRowsB * ld_b);
+            if (MODE == kSsmOut)
+              cp_async16(sh + i * kRowsB * W::kShared + N * E, src_c + i * kRowsB * P.ld_C);
+          }
+        }
+        constexpr int kStep = kBack ? -T : T;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < 2 || gated) src[i] += kStep * lds[i];
+        src_b += kStep * ld_b;
+        src_c += kStep * P.ld_C;
+        put = put == smem + (W::kStages - 1) * W::kStage ? smem : put + W::kStage;
+        ++asked;
       }
+      cp_async_commit();
     };
     // a token's V channels
     const int my = ht / (W::kBlockCh / V), part = ht % (W::kBlockCh / V);
@@ -120,8 +142,11 @@ ssm_walk_kernel(const SsmParams P) {
       for (int i = 0; i < V / 2; ++i)
         v[i] = mul2(v[i], mul2(z[i], rcp2(add2(exp2_of<DT, false, -1>(z[i]), f2(1.f, 1.f)))));
     };
+    const char* st = smem;             // the stage of the step being prepared, or finished
+    auto next_stage = [&] {
+      st = st == smem + (W::kStages - 1) * W::kStage ? smem : st + W::kStage;
+    };
     auto prepare = [&](int k) {
-      const char* st = smem + (k % W::kStages) * W::kStage;
       Pack<DT, V> p;
       F2 d[V / 2], v[V / 2];
       lds_pack(p, st + my * W::kRow + part * V * E);
@@ -141,7 +166,7 @@ ssm_walk_kernel(const SsmParams P) {
       const char* sh = st + 3 * T * W::kRow;
       float* bc = reinterpret_cast<float*>(bcs + (k & 1) * W::kBC);
 #pragma unroll
-      for (int i = ht; i < T * 2 * N / 4; i += kSsmHalf) {
+      for (int i = ht; i < T * 2 * N / 4; i += kSsmPart) {
         if (MODE != kSsmOut && (i * 4) % (2 * N) >= N) continue;
         Pack<DT, 4> q;
         float f[4];
@@ -150,33 +175,45 @@ ssm_walk_kernel(const SsmParams P) {
         *reinterpret_cast<float4*>(bc + i * 4) = make_float4(f[0], f[1], f[2], f[3]);
       }
     };
+    char* y = P.y[r] == nullptr ? nullptr
+                                : P.y[r] + (row0 + my) * P.ld_y + (at.ch0 + part * V) * E;
     auto finish = [&](int k) {
-      const int64_t t0 = tile_of(k);
-      if (!on || my >= tokens_of(t0)) return;
-      const char* st = smem + (k % W::kStages) * W::kStage;
-      const char* from = ys + (k & 1) * T * W::kYRow + my * W::kYRow + part * V * 4;
+      if (!on || my >= tokens_of(tile_of(k))) return;
+      const char* from = ys + (k & 1) * W::kY + my * G * W::kYRow + part * V * 4;
       Pack<DT, V> p;
-      F2 u[V / 2], y[V / 2];
+      F2 u[V / 2], v[V / 2];
       lds_pack(p, st + (T + my) * W::kRow + part * V * E);
       unpack_pairs(p, u);
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        y[i] = fma2(skip[i], u[i], *reinterpret_cast<const F2*>(from + 8 * i));
-      if (gated) gate(st, y);
-      pack_pairs(p, y);
-      store_pack(P.y[r] + (row0 + t0 + my) * P.ld_y + (at.ch0 + part * V) * E, p);
+      for (int i = 0; i < V / 2; ++i) {
+        F2 a = mul2(skip[i], u[i]);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          a = add2(a, *reinterpret_cast<const F2*>(from + g * W::kYRow + 8 * i));
+        v[i] = a;
+      }
+      if (gated) gate(st, v);
+      pack_pairs(p, v);
+      store_pack(y + tile_of(k) * P.ld_y, p);
     };
-    if (n_tiles > 0) ask(0);
-    cp_async_commit();
-    if (n_tiles > 1) ask(1);
-    cp_async_commit();
+    if (finisher) {
+      for (int k = -1; k < n_tiles + 1; ++k) {
+        meet<walk_threads(MODE)>();
+        if (k < 1) continue;
+        finish(k - 1);
+        next_stage();
+      }
+      return;
+    }
+    ask();
+    ask();
     for (int k = -1; k < n_tiles + (MODE == kSsmOut ? 1 : 0); ++k) {
       cp_async_wait<1>();              // step k + 1's rows
-      meet<2 * kSsmHalf>();
-      if (k + 3 < n_tiles) ask(k + 3);
-      cp_async_commit();
-      if (k + 1 < n_tiles) prepare(k + 1);
-      if (MODE == kSsmOut && k >= 1) finish(k - 1);
+      meet<walk_threads(MODE)>();
+      ask();
+      if (k + 1 >= n_tiles) continue;
+      prepare(k + 1);
+      next_stage();
     }
     return;
   }
@@ -233,17 +270,17 @@ ssm_walk_kernel(const SsmParams P) {
   const int dd_at = ch / V * W::kDPart + ch % V * 8;
   const int64_t runs = (P.s + kSsmRun - 1) / kSsmRun;
 
-  meet<2 * kSsmHalf>();                // (the preparers' step -1)
+  meet<walk_threads(MODE)>();                // (the preparers' step -1)
   for (int k = 0; k < n_tiles; ++k) {
-    meet<2 * kSsmHalf>();
+    meet<walk_threads(MODE)>();
     const float* shared = reinterpret_cast<const float*>(bcs + (k & 1) * W::kBC) + n0;
     const char* dd = dds + (k & 1) * T * W::kDRow + dd_at;
-    char* ybuf = ys + (k & 1) * T * W::kYRow + ch * 4;
+    char* ybuf = ys + (k & 1) * W::kY + (lane % G) * W::kYRow + (warp * CW + lane / G * 2) * 4;
     const int64_t t0 = tile_of(k), tok0 = at.tok0 + t0;
     const int n_tok = tokens_of(t0);
     float steps[2] = {0.f, 0.f};
-    // one token: the states after it, and a lane's parts of its channels' sums with C
-    auto token = [&](int t, float (&part)[2]) {
+    // one token: the states after it, and this lane's parts of its channels' sums with C
+    auto token = [&](int t) -> float2 {
       const float4 v = *reinterpret_cast<const float4*>(dd + t * W::kDRow);
       const float d[2] = {v.x, v.z}, in[2] = {v.y, v.w};
       F2 b[K];
@@ -253,18 +290,18 @@ ssm_walk_kernel(const SsmParams P) {
         if constexpr (MODE != kSsmOut) steps[c] += d[c];
 #pragma unroll
         for (int p = 0; p < K; ++p) {
-          const F2 a = f2(pow2(d[c] * a2[c][2 * p]), pow2(d[c] * a2[c][2 * p + 1]));
-          const float2 x = split(b[p]);
+          const F2 a = pow2(mul2(f2(d[c], d[c]), f2(a2[c][2 * p], a2[c][2 * p + 1])));
           if constexpr (kBack) {
             h[c][p] = mul2(a, fma2(f2(in[c], in[c]), b[p], h[c][p]));
           } else {
-            h[c][p] = fma2(a, h[c][p], f2(in[c] * x.x, in[c] * x.y));
+            h[c][p] = fma2(a, h[c][p], mul2(f2(in[c], in[c]), b[p]));
           }
         }
       }
       if constexpr (MODE == kSsmOut) {
         F2 q[K];
         load_states(shared + t * 2 * N + N, q);
+        float part[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           F2 acc = mul2(h[c][0], q[0]);
@@ -272,7 +309,12 @@ ssm_walk_kernel(const SsmParams P) {
           const float2 x = split(acc);
           part[c] = x.x + x.y;
         }
+        return make_float2(part[0], part[1]);
       }
+      return make_float2(0.f, 0.f);
+    };
+    auto put = [&](int t, float2 part) {
+      if constexpr (MODE == kSsmOut) *reinterpret_cast<float2*>(ybuf + t * G * W::kYRow) = part;
     };
     if (MODE == kSsmOut && P.states[r] != nullptr)
       store_both(P.states[r], (at.batch * runs + tok0 / kSsmRun) * state_step + state_at, h);
@@ -285,31 +327,11 @@ ssm_walk_kernel(const SsmParams P) {
     if (marks.starts == 0u && n_tok == T) {
       // the sums wait in registers: without a store in between, a step's loads and
       // exponentials go ahead of its states
-      float2 kept[T / G];
+      float2 part[T];
 #pragma unroll
-      for (int g0 = 0; g0 < T; g0 += G) {
-        float part[2 * G];
+      for (int t = 0; t < T; ++t) part[t] = token(kBack ? T - 1 - t : t);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float x[2];
-          token(kBack ? T - 1 - g0 - g : g0 + g, x);
-          if constexpr (MODE == kSsmOut) {
-            part[2 * g] = x[0];
-            part[2 * g + 1] = x[1];
-          }
-        }
-        if constexpr (MODE == kSsmOut) {
-          sum_over<2 * G, G>(part, lane, 1);
-          kept[g0 / G] = make_float2(part[0], part[1]);
-        }
-      }
-      if constexpr (MODE == kSsmOut) {
-        if (active) {
-#pragma unroll
-          for (int g0 = 0; g0 < T; g0 += G)
-            *reinterpret_cast<float2*>(ybuf + (g0 + lane % G) * W::kYRow) = kept[g0 / G];
-        }
-      }
+      for (int t = 0; t < T; ++t) put(t, part[t]);
     } else {
 #pragma unroll 1
       for (int i = 0; i < n_tok; ++i) {
@@ -322,15 +344,7 @@ ssm_walk_kernel(const SsmParams P) {
           cur = seq;
           load_both(P.h0[r], cur * state_step + state_at, h);
         }
-        float x[2];
-        token(t, x);
-        if constexpr (MODE == kSsmOut) {
-          float one[1] = {x[0]}, two[1] = {x[1]};
-          sum_over<1, G>(one, lane, 1);
-          sum_over<1, G>(two, lane, 1);
-          if (active && lane % G == 0)
-            *reinterpret_cast<float2*>(ybuf + t * W::kYRow) = make_float2(one[0], two[0]);
-        }
+        put(t, token(t));
         if (kBack && start && tok0 + t > 0) {
           cur = find_seq(P.cu_seqlens, P.n_seqs, tok0 + t - 1);
           load_both(P.dhT[r], cur * state_step + state_at, h);
@@ -341,7 +355,7 @@ ssm_walk_kernel(const SsmParams P) {
     sum[1] += steps[1];
   }
   if constexpr (MODE == kSsmOut) {
-    meet<2 * kSsmHalf>();              // (the preparers finish the last step)
+    meet<walk_threads(MODE)>();              // (the preparers finish the last step)
     if (at.tok0 + at.len == P.s && P.hT[r] != nullptr) {
       const int64_t seq = packed ? cur : at.batch;
       if (seq >= 0) store_both(P.hT[r], seq * state_step + state_at, h);
@@ -402,7 +416,7 @@ static cudaError_t launch_walk(const SsmParams& p, cudaStream_t st) {
   q.slabs = (p.c / p.groups + W::kBlockCh - 1) / W::kBlockCh;
   void* args[] = {&q};
   const int64_t grid = static_cast<int64_t>(q.b) * q.chunks * q.t * q.groups * q.slabs;
-  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(2 * kSsmHalf), W::kSmem, args, st);
+  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(walk_threads(MODE)), W::kSmem, args, st);
 }
 
 template <bool BACK>
