@@ -17,9 +17,10 @@ constexpr int kSsmEnds = 1;    // a chunk's last state from a zero one, the sum 
 constexpr int kSsmBack = 2;    // a chunk's gradient for the state before it, from a zero
                                // one, and the sum of its steps
 
-constexpr int kSsmPart = 128;          // threads that hold states, that prepare, that finish
+constexpr int kSsmPart = 128;          // threads that hold states, and that finish
+constexpr int kSsmPrep = 256;          // that prepare
 __host__ __device__ constexpr int walk_threads(int mode) {
-  return mode == kSsmOut ? 3 * kSsmPart : 2 * kSsmPart;
+  return kSsmPart + kSsmPrep + (mode == kSsmOut ? kSsmPart : 0);
 }
 
 // Rows in shared memory are padded so that the lanes of an access use different banks.
@@ -29,7 +30,9 @@ struct SsmWalk {
   static constexpr int E = ElemSize<DT>::value;
   static constexpr int T = kSsmTile;
   static constexpr int kBlockCh = kSsmPart / 32 * L::kChannels;
-  static constexpr int V = kBlockCh * T / kSsmPart;            // channels of a preparer's token
+  // channels of a token that a thread prepares, and finishes
+  static constexpr int V = kBlockCh * T / kSsmPrep > 2 ? kBlockCh * T / kSsmPrep : 2;
+  static constexpr int VF = kBlockCh * T / kSsmPart;
   static constexpr int kStages = 5;
   static constexpr int kRow = kBlockCh * E + 16;
   static constexpr int kShared = 2 * N * E;                    // B and C of a token
@@ -48,7 +51,7 @@ ssm_walk_kernel(const SsmParams P) {
   using W = SsmWalk<DT, N>;
   using L = SsmLanes<N>;
   constexpr int E = W::E, S = L::kStates, K = L::kPairs, CW = L::kChannels, G = L::kLanes;
-  constexpr int T = W::T, V = W::V;
+  constexpr int T = W::T, V = W::V, VF = W::VF;
   constexpr bool kBack = MODE == kSsmBack;
   extern __shared__ __align__(16) char smem[];
   pdl_wait();
@@ -69,14 +72,14 @@ ssm_walk_kernel(const SsmParams P) {
 
   if (warp >= kSsmPart / 32) {
     // ------------------------------------------------------------ preparing --
-    const bool finisher = warp >= 2 * kSsmPart / 32;
-    const int ht = tid - (finisher ? 2 : 1) * kSsmPart;
+    const bool finisher = warp >= (kSsmPart + kSsmPrep) / 32;
+    const int ht = tid - kSsmPart - (finisher ? kSsmPrep : 0);
     const bool gated = MODE != kSsmEnds && P.gated;
     // The rows that a walk reads: dt, u (back: dy), z (not for ends); B (back: C), and C.
     // A thread's pieces of 16 bytes lie `kRows` (`kRowsB`) tokens apart.
-    constexpr int kPieces = W::kBlockCh * E / 16, kRows = kSsmPart / kPieces;
-    constexpr int kPiecesB = N * E / 16, kRowsB = kSsmPart / kPiecesB;
-    static_assert(kSsmPart % kPieces == 0 && kSsmPart % kPiecesB == 0, "whole rows");
+    constexpr int kPieces = W::kBlockCh * E / 16, kRows = kSsmPrep / kPieces;
+    constexpr int kPiecesB = N * E / 16, kRowsB = kSsmPrep / kPiecesB;
+    static_assert(kSsmPrep % kPieces == 0 && kSsmPrep % kPiecesB == 0, "whole rows");
     const int tok_p = ht / kPieces, at_p = ht % kPieces * 16;
     const int tok_b = ht / kPiecesB, at_b = ht % kPiecesB * 16;
     const bool live_p = at_p < at.live * E;
@@ -122,51 +125,84 @@ ssm_walk_kernel(const SsmParams P) {
       }
       cp_async_commit();
     };
-    // a token's V channels
-    const int my = ht / (W::kBlockCh / V), part = ht % (W::kBlockCh / V);
-    const bool on = part * V < at.live;
-    F2 bias[V / 2], skip[V / 2];
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const int64_t c = rc + at.ch0 + part * V + 2 * i;
-      bias[i] = on && P.dt_bias != nullptr ? *reinterpret_cast<const F2*>(P.dt_bias + c) : 0;
-      skip[i] = on && P.D != nullptr ? *reinterpret_cast<const F2*>(P.D + c) : 0;
-    }
-    // silu(z), or 1, times v
-    auto gate = [&](const char* st, F2 (&v)[V / 2]) {
-      Pack<DT, V> p;
-      F2 z[V / 2];
-      lds_pack(p, st + (2 * T + my) * W::kRow + part * V * E);
+    // v times silu(z) of VG channels, which lie at `z`
+    auto gate = [&](const char* at_z, auto& v) {
+      constexpr int VG = 2 * sizeof(v) / sizeof(F2);
+      Pack<DT, VG> p;
+      F2 z[VG / 2];
+      lds_pack(p, at_z);
       unpack_pairs(p, z);
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i)
+      for (int i = 0; i < VG / 2; ++i)
         v[i] = mul2(v[i], mul2(z[i], rcp2(add2(exp2_of<DT, false, -1>(z[i]), f2(1.f, 1.f)))));
+    };
+    // two of the block's channels' parameters (0 where there are none)
+    auto param = [&](const float* from, int c) {
+      return from != nullptr && c < at.live ? *reinterpret_cast<const F2*>(from + rc + at.ch0 + c)
+                                            : F2(0);
     };
     const char* st = smem;             // the stage of the step being prepared, or finished
     auto next_stage = [&] {
       st = st == smem + (W::kStages - 1) * W::kStage ? smem : st + W::kStage;
     };
-    auto prepare = [&](int k) {
-      Pack<DT, V> p;
-      F2 d[V / 2], v[V / 2];
-      lds_pack(p, st + my * W::kRow + part * V * E);
-      unpack_pairs(p, d);
-      lds_pack(p, st + (T + my) * W::kRow + part * V * E);
-      unpack_pairs(p, v);
-      if (kBack && gated) gate(st, v);
-      char* dst = dds + (k & 1) * T * W::kDRow + my * W::kDRow + part * W::kDPart;
+    if (finisher) {
+      const int my = ht / (W::kBlockCh / VF), ch = ht % (W::kBlockCh / VF) * VF;
+      F2 skip[VF / 2];
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        d[i] = add2(d[i], bias[i]);
-        if (P.softplus) d[i] = softplus2<DT>(d[i], nullptr);
-        if constexpr (!kBack) v[i] = mul2(d[i], v[i]);
-        const float2 a = split(d[i]), b = split(v[i]);
-        *reinterpret_cast<float4*>(dst + 16 * i) = make_float4(a.x, b.x, a.y, b.y);
+      for (int i = 0; i < VF / 2; ++i) skip[i] = param(P.D, ch + 2 * i);
+      char* y = MODE == kSsmOut ? P.y[r] + (row0 + my) * P.ld_y + (at.ch0 + ch) * E : nullptr;
+      for (int k = -1; k < n_tiles + 1; ++k) {
+        meet<walk_threads(MODE)>();
+        if (k < 1) continue;
+        if (ch < at.live && my < tokens_of(tile_of(k - 1))) {
+          const char* from = ys + ((k - 1) & 1) * W::kY + my * G * W::kYRow + ch * 4;
+          Pack<DT, VF> p;
+          F2 u[VF / 2], v[VF / 2];
+          lds_pack(p, st + (T + my) * W::kRow + ch * E);
+          unpack_pairs(p, u);
+#pragma unroll
+          for (int i = 0; i < VF / 2; ++i) {
+            v[i] = mul2(skip[i], u[i]);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              v[i] = add2(v[i], *reinterpret_cast<const F2*>(from + g * W::kYRow + 8 * i));
+          }
+          if (gated) gate(st + (2 * T + my) * W::kRow + ch * E, v);
+          pack_pairs(p, v);
+          store_pack(y, p);
+        }
+        y += T * P.ld_y;
+        next_stage();
+      }
+      return;
+    }
+    const int my = ht / (W::kBlockCh / V), part = ht % (W::kBlockCh / V);
+    F2 bias[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) bias[i] = param(P.dt_bias, part * V + 2 * i);
+    auto prepare = [&](int k) {
+      if (my < T) {
+        Pack<DT, V> p;
+        F2 d[V / 2], v[V / 2];
+        lds_pack(p, st + my * W::kRow + part * V * E);
+        unpack_pairs(p, d);
+        lds_pack(p, st + (T + my) * W::kRow + part * V * E);
+        unpack_pairs(p, v);
+        if (kBack && gated) gate(st + (2 * T + my) * W::kRow + part * V * E, v);
+        char* dst = dds + (k & 1) * T * W::kDRow + my * W::kDRow + part * W::kDPart;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          d[i] = add2(d[i], bias[i]);
+          if (P.softplus) d[i] = softplus2<DT>(d[i], nullptr);
+          if constexpr (!kBack) v[i] = mul2(d[i], v[i]);
+          const float2 a = split(d[i]), b = split(v[i]);
+          *reinterpret_cast<float4*>(dst + 16 * i) = make_float4(a.x, b.x, a.y, b.y);
+        }
       }
       const char* sh = st + 3 * T * W::kRow;
       float* bc = reinterpret_cast<float*>(bcs + (k & 1) * W::kBC);
 #pragma unroll
-      for (int i = ht; i < T * 2 * N / 4; i += kSsmPart) {
+      for (int i = ht; i < T * 2 * N / 4; i += kSsmPrep) {
         if (MODE != kSsmOut && (i * 4) % (2 * N) >= N) continue;
         Pack<DT, 4> q;
         float f[4];
@@ -175,36 +211,6 @@ ssm_walk_kernel(const SsmParams P) {
         *reinterpret_cast<float4*>(bc + i * 4) = make_float4(f[0], f[1], f[2], f[3]);
       }
     };
-    char* y = P.y[r] == nullptr ? nullptr
-                                : P.y[r] + (row0 + my) * P.ld_y + (at.ch0 + part * V) * E;
-    auto finish = [&](int k) {
-      if (!on || my >= tokens_of(tile_of(k))) return;
-      const char* from = ys + (k & 1) * W::kY + my * G * W::kYRow + part * V * 4;
-      Pack<DT, V> p;
-      F2 u[V / 2], v[V / 2];
-      lds_pack(p, st + (T + my) * W::kRow + part * V * E);
-      unpack_pairs(p, u);
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        F2 a = mul2(skip[i], u[i]);
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-          a = add2(a, *reinterpret_cast<const F2*>(from + g * W::kYRow + 8 * i));
-        v[i] = a;
-      }
-      if (gated) gate(st, v);
-      pack_pairs(p, v);
-      store_pack(y + tile_of(k) * P.ld_y, p);
-    };
-    if (finisher) {
-      for (int k = -1; k < n_tiles + 1; ++k) {
-        meet<walk_threads(MODE)>();
-        if (k < 1) continue;
-        finish(k - 1);
-        next_stage();
-      }
-      return;
-    }
     ask();
     ask();
     for (int k = -1; k < n_tiles + (MODE == kSsmOut ? 1 : 0); ++k) {
