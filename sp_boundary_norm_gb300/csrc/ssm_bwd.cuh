@@ -3,258 +3,270 @@
 //   dC[i] = sum over a group's channels of e h,  dB[i] = the same of G d u
 //   g = a G h[i-1],   d(d u) = sum_n G B,   d(d) = sum_n g A + u d(d u)
 //   dA = sum over tokens of g d
-// A block takes its channels' chunk from the end, a run of 16 tokens a step, with the
-// same halves as the forward's walk.  The warps that hold states start from the one that
-// the forward saved for the run: eight tokens at a time, the upper ones first, they go
-// once forwards, keeping states and decays in registers, and once backwards (16 tokens
-// of both do not fit, so the run's lower states are computed twice).  dB and dC of a
-// token are summed over a lane's two channels, a warp's lanes, the block's warps, and
-// by a second kernel over the blocks of a group's channels: always in the same order.
-// The other warps keep what they have prepared of a token (u, e, the slopes of softplus
-// and silu) in their registers until its sums are there.
+// A block takes its channels' chunk from the end, eight tokens a step, with warps that
+// hold states and warps that prepare and finish as in the forward's walk.  Two steps are
+// a run of 16 tokens: the warps that hold states start from the one that the forward
+// saved for it, the upper step first.  They go through a step's tokens once forwards,
+// keeping states and decays in registers, and once backwards (16 tokens of both do not
+// fit, so the lower step's states are computed twice).  A channel's sums over its states
+// are added up by the finishing warps from its lanes' parts.  dB and dC of a token are
+// summed over a lane's two channels, a warp's lanes, the block's warps, and by a second
+// kernel over the blocks of a group's channels: always in the same order.
+//
+// The sums over a warp's lanes need no selections: the lanes' states are in an order of
+// their own, state (j xor m) in place j for the lane m of a channel's, so that a lane
+// keeps its even places and hands on its odd ones whichever it is; B and C lie in shared
+// memory in each of these orders.
 #include <type_traits>
 
 #include "ssm_fwd.cuh"
 
 namespace spb {
 
+constexpr int kBackHelp = 256;         // threads that prepare and finish
+constexpr int kBackThreads = kSsmPart + kBackHelp;
+
 template <int DT, int N>
 struct SsmBack {
   using L = SsmLanes<N>;
   static constexpr int E = ElemSize<DT>::value;
-  static constexpr int T = kSsmRun;
+  static constexpr int H = kSsmRun / 2;                        // tokens of a step
   static constexpr int kWarps = kSsmPart / 32;                 // that hold states
   static constexpr int kBlockCh = kWarps * L::kChannels;
-  static constexpr int V = kBlockCh * T / kSsmPart;
-  static constexpr int kStages = 3;
+  static constexpr int kAbreast = 32 / L::kLanes;              // lanes of a warp with the same states
+  static constexpr int kOrders = kAbreast < L::kStates ? kAbreast : L::kStates;
   static constexpr int kRow = kBlockCh * E + 16;
   static constexpr int kShared = 2 * N * E;
-  static constexpr int kStage = T * (4 * kRow + kShared);      // dt, u, dy, z; B and C
-  static constexpr int kBC = T * 2 * N * 4;
-  static constexpr int kDPart = V * 8 + (V > 2 ? 16 : 0);
-  static constexpr int kDRow = kBlockCh / V * kDPart;
-  static constexpr int kYRow = kBlockCh * 4 + 32;              // e; a channel's three sums
-  static constexpr int kSum = T * 2 * N * 4;                   // dB and dC of a warp's run
+  static constexpr int kStage = H * (4 * kRow + kShared);      // dt, u, dy, z; B and C
+  static constexpr int kBC = H * kOrders * 2 * N * 4;          // B, then C, in every order
+  static constexpr int kDRow = kBlockCh * 8;                   // (d, d u) of a channel
+  static constexpr int kERow = kBlockCh * 4;
+  static constexpr int kYRow = kBlockCh * 4 + 32;
+  static constexpr int kY = H * L::kLanes * kYRow;             // a lane's parts of one sum
+  static constexpr int kSum = H * 2 * N * 4;                   // dB and dC of a warp's step
+  // four steps' rows, and what is prepared of them; two steps' sums
   static constexpr size_t kSmem =
-      kStages * kStage + 2 * (kBC + T * (kDRow + 4 * kYRow) + kWarps * kSum);
+      4 * (kStage + kBC + H * (kDRow + kERow)) + 2 * (3 * kY + kWarps * kSum);
 };
 
 template <int DT, int N>
-__global__ void __launch_bounds__(2 * kSsmPart, 1)
+__global__ void __launch_bounds__(kBackThreads, 1)
 ssm_bwd_kernel(const SsmParams P) {
   using W = SsmBack<DT, N>;
   using L = SsmLanes<N>;
   constexpr int E = W::E, S = L::kStates, K = L::kPairs, CW = L::kChannels, G = L::kLanes;
-  constexpr int T = W::T, V = W::V;
+  constexpr int H = W::H, T = kSsmRun, CB = W::kBlockCh, O = W::kOrders;
   extern __shared__ __align__(16) char smem[];
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x == 0 && warp == 0)
     check_cu_seqlens(P.cu_seqlens, P.n_seqs, P.s, P.status);
-  const SsmPlace<W::kBlockCh> at(P);
+  const SsmPlace<CB> at(P);
   const int r = at.r;
   const int64_t rc = static_cast<int64_t>(r) * P.c;
-  char* bcs = smem + W::kStages * W::kStage;
-  char* dds = bcs + 2 * W::kBC;
-  char* es = dds + 2 * T * W::kDRow;
-  char* outs = es + 2 * T * W::kYRow;                          // [2][3][T] rows of sums
-  char* sums = outs + 6 * T * W::kYRow;
+  char* bcs = smem + 4 * W::kStage;
+  char* dds = bcs + 4 * W::kBC;
+  char* es = dds + 4 * H * W::kDRow;
+  char* outs = es + 4 * H * W::kERow;                          // [2][3] of kY
+  char* sums = outs + 6 * W::kY;
   const int64_t row0 = at.batch * P.s + at.tok0;
-  const int n_runs = static_cast<int>((at.len + T - 1) / T);
-  auto run_of = [&](int k) { return static_cast<int64_t>(n_runs - 1 - k) * T; };
-  auto tokens_of = [&](int64_t t0) { return at.len - t0 < T ? static_cast<int>(at.len - t0) : T; };
+  const int n_runs = static_cast<int>((at.len + T - 1) / T), n_steps = 2 * n_runs;
+  // step k's first token of the chunk, and its tokens: the upper half of a run, the lower
+  auto first_of = [&](int k) {
+    return static_cast<int64_t>(n_runs - 1 - (k >> 1)) * T + (k & 1 ? 0 : H);
+  };
+  auto tokens_of = [&](int k) {
+    const int64_t left = at.len - first_of(k);
+    return left < 0 ? 0 : left < H ? static_cast<int>(left) : H;
+  };
   const bool gated = P.gated != 0;
 
   if (warp >= W::kWarps) {
-    // ------------------------------------------------------------ preparing --
+    // ------------------------------------------------- preparing, finishing --
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     const int ht = tid - kSsmPart;
-    const char* src[4] = {P.dt[r] + row0 * P.ld_dt + at.ch0 * E,
-                          P.u[r] + row0 * P.ld_u + at.ch0 * E,
-                          P.dy[r] + row0 * P.ld_dy + at.ch0 * E,
-                          gated ? P.z[r] + row0 * P.ld_z + at.ch0 * E : nullptr};
-    const char* src_b = P.B[r] + row0 * P.ld_B + at.group * N * E;
-    const char* src_c = P.C[r] + row0 * P.ld_C + at.group * N * E;
-    const int live_bytes = at.live * E;
+    constexpr int kPieces = CB * E / 16, kPiecesB = N * E / 16;
+    const int tok_p = ht / kPieces, at_p = ht % kPieces * 16;
+    const int tok_b = ht / kPiecesB, at_b = ht % kPiecesB * 16;
+    static_assert(kBackHelp / kPieces >= H && kBackHelp / kPiecesB >= H, "a piece a thread");
+    const bool live_p = at_p < at.live * E;
+    const char* src[4] = {P.dt[r] + at.ch0 * E + at_p, P.u[r] + at.ch0 * E + at_p,
+                          P.dy[r] + at.ch0 * E + at_p, gated ? P.z[r] + at.ch0 * E + at_p : nullptr};
+    const char* src_b = P.B[r] + at.group * N * E + at_b;
+    const char* src_c = P.C[r] + at.group * N * E + at_b;
     auto ask = [&](int k) {
-      char* st = smem + (k % W::kStages) * W::kStage;
-      const int64_t t0 = run_of(k);
-      const int n_tok = tokens_of(t0);
-      constexpr int kPieces = W::kBlockCh * E / 16;
-#pragma unroll
-      for (int i = ht; i < T * kPieces; i += kSsmPart) {
-        const int tok = i / kPieces, p = (i % kPieces) * 16;
-        if (tok >= n_tok || p >= live_bytes) continue;
-        char* dst = st + tok * W::kRow + p;
-        cp_async16(dst, src[0] + (t0 + tok) * P.ld_dt + p);
-        cp_async16(dst + T * W::kRow, src[1] + (t0 + tok) * P.ld_u + p);
-        cp_async16(dst + 2 * T * W::kRow, src[2] + (t0 + tok) * P.ld_dy + p);
-        if (gated) cp_async16(dst + 3 * T * W::kRow, src[3] + (t0 + tok) * P.ld_z + p);
-      }
-      constexpr int kP = N * E / 16;
-      char* sh = st + 4 * T * W::kRow;
-#pragma unroll
-      for (int i = ht; i < T * kP; i += kSsmPart) {
-        const int tok = i / kP, p = (i % kP) * 16;
-        if (tok >= n_tok) continue;
-        cp_async16(sh + tok * W::kShared + p, src_b + (t0 + tok) * P.ld_B + p);
-        cp_async16(sh + tok * W::kShared + N * E + p, src_c + (t0 + tok) * P.ld_C + p);
-      }
-    };
-    const int my = ht / (W::kBlockCh / V), part = ht % (W::kBlockCh / V);
-    const bool on = part * V < at.live;
-    F2 bias[V / 2], skip[V / 2], dD[V / 2], dbias[V / 2];
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const int64_t c = rc + at.ch0 + part * V + 2 * i;
-      bias[i] = on && P.dt_bias != nullptr ? *reinterpret_cast<const F2*>(P.dt_bias + c) : 0;
-      skip[i] = on && P.D != nullptr ? *reinterpret_cast<const F2*>(P.D + c) : 0;
-      dD[i] = dbias[i] = 0;
-    }
-    // what is kept of a token's channels until its sums are there
-    struct Kept {
-      F2 d[V / 2], u[V / 2], e[V / 2], slope[V / 2], dz[V / 2];
-    };
-    auto prepare = [&](int k, Kept& x) {
-      const char* st = smem + (k % W::kStages) * W::kStage + my * W::kRow + part * V * E;
-      Pack<DT, V> p;
-      lds_pack(p, st);
-      unpack_pairs(p, x.d);
-      lds_pack(p, st + T * W::kRow);
-      unpack_pairs(p, x.u);
-      lds_pack(p, st + 2 * T * W::kRow);
-      unpack_pairs(p, x.e);
-      if (gated) {
-        F2 z[V / 2];
-        lds_pack(p, st + 3 * T * W::kRow);
-        unpack_pairs(p, z);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          // sg = sigmoid(z); silu' = sg (1 + z (1 - sg)), 1 - sg = exp(-z) sg
-          // (exp(87) at most, whose reciprocal is normal: no product of infinity and 0)
-          const F2 w = exp2_of<DT, DT == SP_F32, -1>(DT == SP_F32 ? z[i] : held_above(z[i], -87.f));
-          const F2 sg = rcp2(add2(w, f2(1.f, 1.f)));
-          x.dz[i] = mul2(x.e[i], fma2(mul2(z[i], mul2(w, sg)), sg, sg));
-          x.e[i] = mul2(x.e[i], mul2(z[i], sg));
+      if (k < n_steps) {
+        const int n_tok = tokens_of(k);
+        const int64_t row = row0 + first_of(k);
+        char* st = smem + (k & 3) * W::kStage;
+        if (live_p && tok_p < n_tok) {
+          char* dst = st + tok_p * W::kRow + at_p;
+          cp_async16(dst, src[0] + (row + tok_p) * P.ld_dt);
+          cp_async16(dst + H * W::kRow, src[1] + (row + tok_p) * P.ld_u);
+          cp_async16(dst + 2 * H * W::kRow, src[2] + (row + tok_p) * P.ld_dy);
+          if (gated) cp_async16(dst + 3 * H * W::kRow, src[3] + (row + tok_p) * P.ld_z);
+        }
+        if (tok_b < n_tok) {
+          char* sh = st + 4 * H * W::kRow + tok_b * W::kShared + at_b;
+          cp_async16(sh, src_b + (row + tok_b) * P.ld_B);
+          cp_async16(sh + N * E, src_c + (row + tok_b) * P.ld_C);
         }
       }
-      char* dd = dds + ((k & 1) * T + my) * W::kDRow + part * W::kDPart;
-      char* ee = es + ((k & 1) * T + my) * W::kYRow + part * V * 4;
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        x.d[i] = add2(x.d[i], bias[i]);
-        x.slope[i] = f2(1.f, 1.f);
-        if (P.softplus) x.d[i] = softplus2<DT>(x.d[i], &x.slope[i]);
-        const float2 a = split(x.d[i]), b = split(mul2(x.d[i], x.u[i]));
-        *reinterpret_cast<float4*>(dd + 16 * i) = make_float4(a.x, b.x, a.y, b.y);
-        *reinterpret_cast<F2*>(ee + 8 * i) = x.e[i];
+      cp_async_commit();
+    };
+    // a thread's two channels of a token
+    const int my = ht / (CB / 2), ch = ht % (CB / 2) * 2;
+    const bool mine = my < H, live = ch < at.live;
+    auto param = [&](const float* from) {
+      return from != nullptr && live ? *reinterpret_cast<const F2*>(from + rc + at.ch0 + ch) : F2(0);
+    };
+    const F2 bias = param(P.dt_bias), skip = param(P.D);
+    F2 dD = 0, dbias = 0;
+    // what is kept of a token's channels until its sums are there
+    struct Kept {
+      F2 d, u, e, slope, dz;
+    };
+    auto prepare = [&](int k, Kept& x) {
+      const char* st = smem + (k & 3) * W::kStage;
+      if (mine) {
+        const char* from = st + my * W::kRow + ch * E;
+        Pack<DT, 2> p;
+        F2 one[1];
+        auto read = [&](int a) {
+          lds_pack(p, from + a * H * W::kRow);
+          unpack_pairs(p, one);
+          return live ? one[0] : F2(0);                        // (a dead channel adds zeros)
+        };
+        x.d = add2(read(0), bias);
+        x.u = read(1);
+        x.e = read(2);
+        x.dz = 0;
+        x.slope = f2(1.f, 1.f);
+        if (P.softplus) x.d = softplus2<DT>(x.d, &x.slope);
+        if (gated) {
+          // sg = sigmoid(z); silu' = sg + z sg (1 - sg)
+          const F2 z = read(3);
+          const F2 sg = rcp2(add2(exp2_of<DT, false, -1>(z), f2(1.f, 1.f)));
+          const F2 silu = mul2(z, sg);
+          x.dz = mul2(x.e, fma2(silu, fma2(sg, f2(-1.f, -1.f), f2(1.f, 1.f)), sg));
+          x.e = mul2(x.e, silu);
+        }
+        const float2 a = split(x.d), b = split(mul2(x.d, x.u));
+        *reinterpret_cast<float4*>(dds + ((k & 3) * H + my) * W::kDRow + ch * 8) =
+            make_float4(a.x, b.x, a.y, b.y);
+        *reinterpret_cast<F2*>(es + ((k & 3) * H + my) * W::kERow + ch * 4) = x.e;
       }
-      const char* sh = smem + (k % W::kStages) * W::kStage + 4 * T * W::kRow;
-      float* bc = reinterpret_cast<float*>(bcs + (k & 1) * W::kBC);
+      // B and C, four (two) states at a time, in every order
+      const char* sh = st + 4 * H * W::kRow;
+      float* bc = reinterpret_cast<float*>(bcs + (k & 3) * W::kBC);
+      constexpr int kQuads = H * 2 * N / S;
 #pragma unroll
-      for (int i = ht; i < T * 2 * N / 4; i += kSsmPart) {
-        Pack<DT, 4> q;
-        float f[4];
-        lds_pack(q, sh + i * 4 * E);
-        unpack(q, f);
-        *reinterpret_cast<float4*>(bc + i * 4) = make_float4(f[0], f[1], f[2], f[3]);
+      for (int i = ht; i < kQuads * O; i += kBackHelp) {
+        const int m = i % O, quad = i / O;
+        const int tok = quad / (2 * N / S), e = quad % (2 * N / S) * S;
+        Pack<DT, S> p;
+        float f[S];
+        lds_pack(p, sh + tok * W::kShared + e * E);
+        unpack(p, f);
+        float* to = bc + ((tok * 2 + (e >= N)) * O + m) * N + e % N;
+        if (m & 1) {
+#pragma unroll
+          for (int j = 0; j < S; j += 2) {
+            const float v = f[j];
+            f[j] = f[j + 1];
+            f[j + 1] = v;
+          }
+        }
+        if constexpr (S == 4) {
+          const bool far = m & 2;
+          *reinterpret_cast<float4*>(to) = make_float4(far ? f[2] : f[0], far ? f[3] : f[1],
+                                                       far ? f[0] : f[2], far ? f[1] : f[3]);
+        } else {
+          *reinterpret_cast<float2*>(to) = make_float2(f[0], f[1]);
+        }
       }
     };
     const int live_warps = (at.live + CW - 1) / CW;
     auto finish = [&](int k, const Kept& x) {
-      const int64_t t0 = run_of(k);
-      const int n_tok = tokens_of(t0);
+      const int n_tok = tokens_of(k);
+      const int64_t row = row0 + first_of(k);
       // dB and dC: the block's warps in order
       const char* from = sums + (k & 1) * W::kWarps * W::kSum;
 #pragma unroll
-      for (int i = ht; i < T * 2 * N / 4; i += kSsmPart) {
+      for (int i = ht; i < H * 2 * N / 4; i += kBackHelp) {
         const int tok = i / (N / 2), e = (i % (N / 2)) * 4;
         if (tok >= n_tok) continue;
-        F2 a = 0, b = 0;
+        F2 both[2] = {0, 0};
         for (int w = 0; w < live_warps; ++w) {
           const float4 v = *reinterpret_cast<const float4*>(from + w * W::kSum + i * 16);
-          a = add2(a, f2(v.x, v.y));
-          b = add2(b, f2(v.z, v.w));
+          both[0] = add2(both[0], f2(v.x, v.y));
+          both[1] = add2(both[1], f2(v.z, v.w));
         }
-        const int64_t row = row0 + t0 + tok;
         if (P.partial_bc != nullptr) {
           const int64_t rows = static_cast<int64_t>(P.b) * P.s;
-          const F2 both[2] = {a, b};
-          store_states(P.partial_bc + (at.slab * rows + row) * 2 * N + e, both);
+          store_states(P.partial_bc + (at.slab * rows + row + tok) * 2 * N + e, both);
         } else {
           Pack<DT, 4> p;
-          const F2 both[2] = {a, b};
           pack_pairs(p, both);
           const int n = e % N + at.group * N;
-          if (e < N) store_pack(P.dB[r] + row * P.ld_dB + n * E, p);
-          else store_pack(P.dC[r] + row * P.ld_dC + n * E, p);
+          if (e < N) store_pack(P.dB[r] + (row + tok) * P.ld_dB + n * E, p);
+          else store_pack(P.dC[r] + (row + tok) * P.ld_dC + n * E, p);
         }
       }
-      if (!on || my >= n_tok) return;
-      const char* out = outs + ((k & 1) * 3 * T + my) * W::kYRow + part * V * 4;
-      F2 du[V / 2], ddt[V / 2], dz[V / 2];
+      if (!live || my >= n_tok) return;
+      // the channels' sums over their lanes
+      const char* out = outs + (k & 1) * 3 * W::kY + my * G * W::kYRow + ch * 4;
+      F2 through = 0, decay = 0, inner = 0;
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        const F2 through = *reinterpret_cast<const F2*>(out + 8 * i);
-        const F2 decay = *reinterpret_cast<const F2*>(out + T * W::kYRow + 8 * i);
-        du[i] = fma2(x.d[i], through, mul2(skip[i], x.e[i]));
-        ddt[i] = mul2(fma2(x.u[i], through, mul2(decay, f2(kLn2, kLn2))), x.slope[i]);
-        if (gated) {
-          const F2 inner = *reinterpret_cast<const F2*>(out + 2 * T * W::kYRow + 8 * i);
-          dz[i] = mul2(x.dz[i], fma2(skip[i], x.u[i], inner));
-        }
-        dD[i] = fma2(x.e[i], x.u[i], dD[i]);
-        dbias[i] = add2(dbias[i], ddt[i]);
+      for (int g = 0; g < G; ++g) {
+        through = add2(through, *reinterpret_cast<const F2*>(out + g * W::kYRow));
+        decay = add2(decay, *reinterpret_cast<const F2*>(out + W::kY + g * W::kYRow));
+        if (gated) inner = add2(inner, *reinterpret_cast<const F2*>(out + 2 * W::kY + g * W::kYRow));
       }
-      const int64_t row = row0 + t0 + my, off = (at.ch0 + part * V) * E;
-      Pack<DT, V> p;
-      pack_pairs(p, du);
-      store_pack(P.du[r] + row * P.ld_du + off, p);
-      pack_pairs(p, ddt);
-      store_pack(P.ddt[r] + row * P.ld_ddt + off, p);
-      if (gated) {
-        pack_pairs(p, dz);
-        store_pack(P.dz[r] + row * P.ld_dz + off, p);
-      }
+      const F2 ddt = mul2(fma2(x.u, through, mul2(decay, f2(kLn2, kLn2))), x.slope);
+      dD = fma2(x.e, x.u, dD);
+      dbias = add2(dbias, ddt);
+      const int64_t to = row + my, off = (at.ch0 + ch) * E;
+      auto store = [&](char* dst, F2 v) {
+        Pack<DT, 2> p;
+        const F2 w[1] = {v};
+        pack_pairs(p, w);
+        store_pack(dst + off, p);
+      };
+      store(P.du[r] + to * P.ld_du, fma2(x.d, through, mul2(skip, x.e)));
+      store(P.ddt[r] + to * P.ld_ddt, ddt);
+      if (gated) store(P.dz[r] + to * P.ld_dz, mul2(x.dz, fma2(skip, x.u, inner)));
     };
-    if (n_runs > 0) ask(0);
-    cp_async_commit();
-    if (n_runs > 1) ask(1);
-    cp_async_commit();
-    Kept even, odd;                    // of even and of odd steps
-    auto step = [&](int k, Kept& next) {
-      cp_async_wait<1>();              // step k + 1's rows
-      meet<2 * kSsmPart>();
-      // (step k's rows have been prepared: step k + 3 takes their place)
-      if (k + 3 < n_runs) ask(k + 3);
-      cp_async_commit();
-      if (k >= 1) finish(k - 1, next);
-      if (k + 1 < n_runs) prepare(k + 1, next);
+    ask(0);
+    ask(1);
+    Kept kept[3];                      // of steps k - 1, k, k + 1: by k modulo 3
+    auto step = [&](int k, Kept& x) {
+      cp_async_wait<1>();              // step k + 2's rows
+      meet<kBackThreads>();
+      ask(k + 4);                      // (in the place of step k's, which are prepared)
+      if (k >= 1) finish(k - 1, x);
+      if (k + 2 < n_steps) prepare(k + 2, x);
     };
-    if (n_runs > 2) ask(2);
-    cp_async_commit();
-    cp_async_wait<2>();                // step 0's rows
-    meet<2 * kSsmPart>();
-    if (n_runs > 0) prepare(0, even);
-    for (int k = 0; k <= n_runs; k += 2) {
-      step(k, odd);
-      if (k + 1 <= n_runs) step(k + 1, even);
+    for (int k = -2; k <= n_steps; k += 3) {
+      step(k, kept[0]);
+      if (k + 1 <= n_steps) step(k + 1, kept[1]);
+      if (k + 2 <= n_steps) step(k + 2, kept[2]);
     }
     if (P.partial_params == nullptr) return;
     // the block's tokens of a channel, in the order of its threads
     float* to = P.partial_params + (at.batch * P.chunks + at.chunk) * P.t * P.c * (N + 2) +
                 static_cast<int64_t>(P.t) * P.c * N;
-    F2* sum = reinterpret_cast<F2*>(es);                       // [2][T][kBlockCh / 2]
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      sum[my * (W::kBlockCh / 2) + part * (V / 2) + i] = dD[i];
-      sum[(T + my) * (W::kBlockCh / 2) + part * (V / 2) + i] = dbias[i];
+    F2* sum = reinterpret_cast<F2*>(smem);                     // [2][H][CB / 2]
+    if (mine) {
+      sum[my * (CB / 2) + ch / 2] = dD;
+      sum[(H + my) * (CB / 2) + ch / 2] = dbias;
     }
-    asm volatile("bar.sync 2, %0;" ::"n"(kSsmPart) : "memory");
-    if (ht < W::kBlockCh && ht / (W::kBlockCh / 2) < 2) {
-      const int which = ht / (W::kBlockCh / 2), c = ht % (W::kBlockCh / 2);
+    asm volatile("bar.sync 2, %0;" ::"n"(kBackHelp) : "memory");
+    if (ht < CB) {
+      const int which = ht / (CB / 2), c = ht % (CB / 2);
       F2 a = 0;
 #pragma unroll
-      for (int i = 0; i < T; ++i) a = add2(a, sum[(which * T + i) * (W::kBlockCh / 2) + c]);
+      for (int i = 0; i < H; ++i) a = add2(a, sum[(which * H + i) * (CB / 2) + c]);
       if (2 * c < at.live)
         *reinterpret_cast<F2*>(to + static_cast<int64_t>(which) * P.t * P.c + rc + at.ch0 + 2 * c) = a;
     }
@@ -262,32 +274,62 @@ ssm_bwd_kernel(const SsmParams P) {
   }
 
   // ---------------------------------------------------------------- states --
-  const bool active = warp * CW + lane / G * 2 < at.live;
-  const int n0 = (lane % G) * S, ch = active ? warp * CW + lane / G * 2 : 0;
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+  // the lane's two channels (dead ones go by the block's first, and add zeros), its order
+  const int my_ch = warp * CW + lane / G * 2;
+  const bool active = my_ch < at.live;
+  const int order = lane / G & (O - 1), n0 = (lane % G) * S, ch = active ? my_ch : 0;
   const int64_t mine = (rc + at.ch0 + ch) * N + n0;
   const int64_t state_at = static_cast<int64_t>(at.ch0 + ch) * N + n0;
   const int64_t state_step = static_cast<int64_t>(P.c) * N;
   const int64_t all_runs = (P.s + T - 1) / T;
   const bool packed = P.cu_seqlens != nullptr;
+  // to the lane's order, and back (the same)
+  auto reorder = [&](F2 (&x)[2][K]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int p = 0; p < K; ++p) {
+        const float2 v = split(x[c][p]);
+        x[c][p] = order & 1 ? f2(v.y, v.x) : x[c][p];
+      }
+      if constexpr (K == 2) {
+        const F2 v = x[c][0];
+        x[c][0] = order & 2 ? x[c][1] : v;
+        x[c][1] = order & 2 ? v : x[c][1];
+      }
+    }
+  };
   auto load_both = [&](const float* base, int64_t i, F2 (&x)[2][K]) {
     load_states_or_zero(base, i, x[0]);
     load_states_or_zero(base, i + N, x[1]);
+    if (!active) {
+      clear(x[0]);
+      clear(x[1]);
+    }
+    reorder(x);
   };
   auto store_both = [&](float* base, int64_t i, const F2 (&x)[2][K]) {
+    F2 y[2][K];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int p = 0; p < K; ++p) y[c][p] = x[c][p];
+    reorder(y);
     if (!active) return;
-    store_states(base + i, x[0]);
-    store_states(base + i + N, x[1]);
+    store_states(base + i, y[0]);
+    store_states(base + i + N, y[1]);
   };
   // the gradient that comes from behind (times the decay in between); the decay rates
-  // in powers of two, their gradients' sums; the state before the next run
-  F2 back[2][K], a2[2][K], dA[2][K], next[2][K];
+  // in powers of two, their gradients' sums; the state before the run, and the next run's
+  F2 back[2][K], a2[2][K], dA[2][K], first[2][K], next[2][K];
   load_both(P.A, mine, a2);
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int p = 0; p < K; ++p) {
       a2[c][p] = mul2(a2[c][p], f2(kLog2e, kLog2e));
-      dA[c][p] = 0;
+      dA[c][p] = first[c][p] = 0;
     }
   if (P.chunks > 1) {
     load_both(P.carry, (at.batch * P.chunks + at.chunk) * P.t * P.c * N + mine, back);
@@ -304,52 +346,57 @@ ssm_bwd_kernel(const SsmParams P) {
       store_both(P.hT[r], j * state_step + state_at, v);
     }
   }
-  auto run_state = [&](int k) {
-    const int64_t run = (at.tok0 + run_of(k)) / T;
-    load_both(P.states[r], (at.batch * all_runs + run) * state_step + state_at, next);
+  auto run_state = [&](int run) {      // (as it lies in memory)
+    const int64_t i = (at.batch * all_runs + at.tok0 / T + n_runs - 1 - run) * state_step + state_at;
+    load_states(P.states[r] + i, next[0]);
+    load_states(P.states[r] + i + N, next[1]);
   };
   if (n_runs > 0) run_state(0);
-  const int dd_at = ch / V * W::kDPart + ch % V * 8;
-  // which of a lane's 2 S sums of dB's and dC's states it keeps, of the 32 / G lanes
-  constexpr int CL = 32 / G;
-  constexpr int kKept = 2 * S > CL ? 2 * S / CL : 1;
-  constexpr int kSame = CL > 2 * S ? CL / (2 * S) : 1;         // lanes with the same
-  const int kept = lane / G / kSame * kKept;
-  const int put_at = (kept / S) * N + n0 + kept % S;
+  SsmMarks marks{0u, 0};
 
-  meet<2 * kSsmPart>();                // (step 0 is prepared)
-  for (int k = 0; k < n_runs; ++k) {
-    meet<2 * kSsmPart>();
-    const float* shared = reinterpret_cast<const float*>(bcs + (k & 1) * W::kBC) + n0;
-    const char* dd = dds + (k & 1) * T * W::kDRow + dd_at;
-    const char* ee = es + (k & 1) * T * W::kYRow + ch * 4;
-    char* out = outs + (k & 1) * 3 * T * W::kYRow + ch * 4;
-    float* put = reinterpret_cast<float*>(sums + ((k & 1) * W::kWarps + warp) * W::kSum) + put_at;
-    const int64_t tok0 = at.tok0 + run_of(k);
-    const int n_tok = tokens_of(run_of(k));
-    F2 first[2][K];
+  meet<kBackThreads>();
+  meet<kBackThreads>();                // (steps 0 and 1 are prepared)
+  for (int k = 0; k < n_steps; ++k) {
+    meet<kBackThreads>();
+    const int half = k & 1 ? 0 : H;    // the step's first token in its run
+    const int64_t run0 = at.tok0 + first_of(k) - half;
+    const int n_tok = tokens_of(k);
+    // what is prepared of a step
+    auto shared_of = [&](int j) {
+      return reinterpret_cast<const float*>(bcs + (j & 3) * W::kBC) + order * N + n0;
+    };
+    auto dd_of = [&](int j) { return dds + (j & 3) * H * W::kDRow + my_ch * 8; };
+    const float* shared = shared_of(k);
+    const char* dd = dd_of(k);
+    const char* ee = es + (k & 3) * H * W::kERow + my_ch * 4;
+    char* out = outs + (k & 1) * 3 * W::kY + (lane % G) * W::kYRow + my_ch * 4;
+    float* put = reinterpret_cast<float*>(sums + ((k & 1) * W::kWarps + warp) * W::kSum);
+    if (half != 0) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int p = 0; p < K; ++p) first[c][p] = next[c][p];
-    if (k + 1 < n_runs) run_state(k + 1);
-    SsmMarks marks{0u, 0};
-    if (packed) marks = ssm_marks(P, tok0, n_tok);
+        for (int p = 0; p < K; ++p) first[c][p] = active ? next[c][p] : F2(0);
+      reorder(first);
+      if (k + 2 < n_steps) run_state((k >> 1) + 1);
+      if (packed) marks = ssm_marks(P, run0, n_tok > 0 ? H + n_tok : tokens_of(k + 1));
+    }
+    constexpr int kOrderStride = 2 * O * N;            // floats between tokens' B
 
-    // SLOW: runs with less than 16 tokens, or where a sequence begins
+    // SLOW: runs with less than 16 tokens, or where a sequence begins: token by token,
+    // with the states and decays in local memory
     auto go = [&](auto slow) {
       constexpr bool SLOW = decltype(slow)::value;
-      constexpr int H = T / 2;
+      constexpr int kUnroll = SLOW ? 1 : H;
       auto begins = [&](int t) { return SLOW && (marks.starts >> t & 1u); };
       auto forget = [&](int t, F2 (&h)[2][K]) {        // the state before a sequence
         load_both(P.h0[r], __shfl_sync(kAll, marks.seq, t) * state_step + state_at, h);
       };
-      // the states after token t, and its decays
-      auto token = [&](int t, F2 (&h)[2][K], F2 (&a)[2][K]) {
-        const float4 v = *reinterpret_cast<const float4*>(dd + t * W::kDRow);
+      // the states after token t of a step, and its decays
+      auto token = [&](const char* dt, const float* bt, F2 (&h)[2][K], F2 (&a)[2][K]) {
+        const float4 v = *reinterpret_cast<const float4*>(dt);
         const float d[2] = {v.x, v.z}, in[2] = {v.y, v.w};
         F2 b[K];
-        load_states(shared + t * 2 * N, b);
+        load_states(bt, b);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -363,145 +410,165 @@ ssm_bwd_kernel(const SsmParams P) {
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int p = 0; p < K; ++p) begin[c][p] = first[c][p];
-      if (!SLOW || n_tok > H) {
-#pragma unroll
-        for (int t = 0; t < H; ++t) {
+      if (half != 0 && n_tok > 0) {                    // through the lower step first
+        const float* low = shared_of(k + 1);
+        const char* low_d = dd_of(k + 1);
+#pragma unroll kUnroll
+        for (int i = 0; i < H; ++i) {
           F2 a[2][K];
-          if (begins(t)) forget(t, begin);
-          token(t, begin, a);
+          if (begins(i)) forget(i, begin);
+          token(low_d + i * W::kDRow, low + i * kOrderStride, begin, a);
         }
       }
-#pragma unroll 1
-      for (int t0 = H; t0 >= 0; t0 -= H) {
-        if (t0 == 0) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int p = 0; p < K; ++p) begin[c][p] = first[c][p];
-        }
-        F2 h[H][2][K], a[H][2][K], now[2][K];
+      F2 h[H][2][K], a[H][2][K];
+      {
+        F2 now[2][K];
+        float2 inner[H];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int p = 0; p < K; ++p) now[c][p] = begin[c][p];
-        float inner[8];
-#pragma unroll
+#pragma unroll kUnroll
         for (int i = 0; i < H; ++i) {
-          const int t = t0 + i;
-          inner[i % 4 * 2] = inner[i % 4 * 2 + 1] = 0.f;
-          if (!SLOW || t < n_tok) {
-            if (begins(t)) forget(t, now);
-            token(t, now, a[i]);
+          inner[i] = make_float2(0.f, 0.f);
+          if (!SLOW || i < n_tok) {
+            if (begins(half + i)) forget(half + i, now);
+            token(dd + i * W::kDRow, shared + i * kOrderStride, now, a[i]);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int p = 0; p < K; ++p) h[i][c][p] = now[c][p];
             if (gated) {
               F2 q[K];
-              load_states(shared + t * 2 * N + N, q);
+              load_states(shared + i * kOrderStride + O * N, q);
+              float sum[2];
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 F2 acc = mul2(now[c][0], q[0]);
                 if constexpr (K == 2) acc = fma2(now[c][1], q[1], acc);
                 const float2 x = split(acc);
-                inner[i % 4 * 2 + c] = x.x + x.y;
+                sum[c] = x.x + x.y;
               }
-            }
-          }
-          if (gated && i % 4 == 3) {
-            sum_over<8, G>(inner, lane, 1);
-            constexpr int kEach = G >= 8 ? 1 : 8 / G;
-            const int id = (lane % G) / (G >= 8 ? G / 8 : 1) * kEach;  // token 2, channel 1
-            char* dst = out + (2 * T + t - 3 + id / 2) * W::kYRow + id % 2 * 4;
-            if (active) {
-              if constexpr (kEach == 2) *reinterpret_cast<float2*>(dst) = make_float2(inner[0], inner[1]);
-              else *reinterpret_cast<float*>(dst) = inner[0];
+              inner[i] = make_float2(sum[0], sum[1]);
             }
           }
         }
-        float part[16];
+        if (gated) {
+#pragma unroll kUnroll
+          for (int i = 0; i < H; ++i)
+            *reinterpret_cast<float2*>(out + 2 * W::kY + i * G * W::kYRow) = inner[i];
+        }
+      }
+      // what a token of the way back needs, asked for a token ahead of its use (the
+      // compiler keeps loads behind the stores of sums)
+      struct Operands {
+        float4 d;
+        float2 e;
+        F2 b[K], q[K];
+      };
+      auto operands = [&](int i) {
+        Operands x;
+        x.d = *reinterpret_cast<const float4*>(dd + i * W::kDRow);
+        x.e = *reinterpret_cast<const float2*>(ee + i * W::kERow);
+        load_states(shared + i * kOrderStride, x.b);
+        load_states(shared + i * kOrderStride + O * N, x.q);
+        return x;
+      };
+      Operands ahead = operands(H - 1);
+#pragma unroll kUnroll
+      for (int i = H - 1; i >= 0; --i) {
+        const Operands x = ahead;
+        if (i > 0) ahead = operands(i - 1);
+        if (!SLOW || i < n_tok) {
+          const int t = half + i;
+          const float d[2] = {x.d.x, x.d.z}, in[2] = {x.d.y, x.d.w}, e[2] = {x.e.x, x.e.y};
+          F2 db[K], dc[K], before[2][K];
 #pragma unroll
-        for (int i = H - 1; i >= 0; --i) {
-          const int t = t0 + i;
-          float* sum4 = part + i % 4 * 4;              // of a token: through, decay; channels
-          sum4[0] = sum4[1] = sum4[2] = sum4[3] = 0.f;
-          if (!SLOW || t < n_tok) {
-            const float4 x = *reinterpret_cast<const float4*>(dd + t * W::kDRow);
-            const float2 ev = *reinterpret_cast<const float2*>(ee + t * W::kYRow);
-            const float d[2] = {x.x, x.z}, in[2] = {x.y, x.w}, e[2] = {ev.x, ev.y};
-            F2 b[K], q[K], db[K], dc[K], before[2][K];
-            load_states(shared + t * 2 * N, b);
-            load_states(shared + t * 2 * N + N, q);
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int p = 0; p < K; ++p)
+              before[c][p] = i > 0 ? h[i > 0 ? i - 1 : 0][c][p] : begin[c][p];
+          if (begins(t)) forget(t, before);
+          float through[2], decay[2];
 #pragma unroll
-              for (int p = 0; p < K; ++p)
-                before[c][p] = i > 0 ? h[i > 0 ? i - 1 : 0][c][p] : begin[c][p];
-            if (begins(t)) forget(t, before);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const F2 e2 = f2(e[c], e[c]), in2 = f2(in[c], in[c]), d2 = f2(d[c], d[c]);
-              F2 through = 0, decay = 0;
-#pragma unroll
-              for (int p = 0; p < K; ++p) {
-                const F2 gr = fma2(q[p], e2, back[c][p]);
-                dc[p] = c == 0 ? mul2(h[i][c][p], e2) : fma2(h[i][c][p], e2, dc[p]);
-                db[p] = c == 0 ? mul2(gr, in2) : fma2(gr, in2, db[p]);
-                through = p == 0 ? mul2(gr, b[p]) : fma2(gr, b[p], through);
-                back[c][p] = mul2(a[i][c][p], gr);
-                const F2 g = mul2(back[c][p], before[c][p]);
-                decay = p == 0 ? mul2(g, a2[c][p]) : fma2(g, a2[c][p], decay);
-                dA[c][p] = fma2(g, d2, dA[c][p]);
-              }
-              const float2 y = split(through), w = split(decay);
-              sum4[c] = y.x + y.y;
-              sum4[2 + c] = w.x + w.y;
-            }
-            if (begins(t)) {
-              const int64_t seq = __shfl_sync(kAll, marks.seq, t);
-              if (P.hT[r] != nullptr) store_both(P.hT[r], seq * state_step + state_at, back);
-              const float* from = tok0 + t > 0 ? P.dhT[r] : nullptr;
-              const int64_t prev =
-                  tok0 + t > 0 ? find_seq(P.cu_seqlens, P.n_seqs, tok0 + t - 1) : 0;
-              load_both(from, prev * state_step + state_at, back);
-            }
-            float v[2 * S];
+          for (int c = 0; c < 2; ++c) {
+            const F2 e2 = f2(e[c], e[c]), in2 = f2(in[c], in[c]), d2 = f2(d[c], d[c]);
+            F2 to_u = 0, to_d = 0;
 #pragma unroll
             for (int p = 0; p < K; ++p) {
-              const float2 y = split(db[p]), w = split(dc[p]);
-              v[2 * p] = active ? y.x : 0.f;
-              v[2 * p + 1] = active ? y.y : 0.f;
-              v[S + 2 * p] = active ? w.x : 0.f;
-              v[S + 2 * p + 1] = active ? w.y : 0.f;
+              const F2 gr = fma2(x.q[p], e2, back[c][p]);
+              dc[p] = c == 0 ? mul2(h[i][c][p], e2) : fma2(h[i][c][p], e2, dc[p]);
+              db[p] = c == 0 ? mul2(gr, in2) : fma2(gr, in2, db[p]);
+              to_u = p == 0 ? mul2(gr, x.b[p]) : fma2(gr, x.b[p], to_u);
+              back[c][p] = mul2(a[i][c][p], gr);
+              const F2 g = mul2(back[c][p], before[c][p]);
+              to_d = p == 0 ? mul2(g, a2[c][p]) : fma2(g, a2[c][p], to_d);
+              dA[c][p] = fma2(g, d2, dA[c][p]);
             }
-            sum_over<2 * S, CL>(v, lane, G);
-#pragma unroll
-            for (int j = 0; j < kKept; ++j) put[t * 2 * N + j] = v[j];
+            const float2 y = split(to_u), w = split(to_d);
+            through[c] = y.x + y.y;
+            decay[c] = w.x + w.y;
           }
-          if (i % 4 == 0) {
-            sum_over<16, G>(part, lane, 1);
-            constexpr int kEach = 16 / G;
-            const int id = lane % G * kEach;           // token 4, sum 2, channel 1
-            char* dst = out + (t + id / 4) * W::kYRow;
-            if (active) {
-              if constexpr (kEach == 4) {
-                *reinterpret_cast<float2*>(dst) = make_float2(part[0], part[1]);
-                *reinterpret_cast<float2*>(dst + T * W::kYRow) = make_float2(part[2], part[3]);
-              } else if constexpr (kEach == 2) {
-                *reinterpret_cast<float2*>(dst + id / 2 % 2 * T * W::kYRow) =
-                    make_float2(part[0], part[1]);
-              } else {
-                *reinterpret_cast<float*>(dst + id / 2 % 2 * T * W::kYRow + id % 2 * 4) = part[0];
-              }
-            }
+          if (begins(t)) {
+            const int64_t seq = __shfl_sync(kAll, marks.seq, t);
+            if (P.hT[r] != nullptr) store_both(P.hT[r], seq * state_step + state_at, back);
+            const float* from = run0 + t > 0 ? P.dhT[r] : nullptr;
+            const int64_t prev =
+                run0 + t > 0 ? find_seq(P.cu_seqlens, P.n_seqs, run0 + t - 1) : 0;
+            load_both(from, prev * state_step + state_at, back);
+          }
+          *reinterpret_cast<float2*>(out + i * G * W::kYRow) = make_float2(through[0], through[1]);
+          *reinterpret_cast<float2*>(out + W::kY + i * G * W::kYRow) =
+              make_float2(decay[0], decay[1]);
+          // dB and dC over the warp's lanes with the same states: keep the even places,
+          // hand on the odd ones; then of two states; then dB or dC
+          float v[2][S];
+#pragma unroll
+          for (int p = 0; p < K; ++p) {
+            const float2 y = split(db[p]), w = split(dc[p]);
+            v[0][2 * p] = y.x;
+            v[0][2 * p + 1] = y.y;
+            v[1][2 * p] = w.x;
+            v[1][2 * p + 1] = w.y;
+          }
+          constexpr int kLevels = O == 4 ? 2 : 1;      // that halve the states
+#pragma unroll
+          for (int level = 0; level < kLevels; ++level) {
+            const int step = 1 << level;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int j = 0; j < S; j += 2 * step)
+                v[w][j] += __shfl_xor_sync(kAll, v[w][j + step], G * step);
+          }
+          constexpr int kLeft = S >> kLevels;          // states of dB and of dC: v[.][0], v[.][2]
+          float* to = put + i * 2 * N + n0;
+          if constexpr (W::kAbreast > O) {
+            // lanes left over: one takes dB, the other dC (and others the same)
+            static_assert(kLeft == 1, "one state");
+            const bool up = lane & G * O;
+            const float give = up ? v[0][0] : v[1][0];
+            float keep = up ? v[1][0] : v[0][0];
+            keep += __shfl_xor_sync(kAll, give, G * O);
+#pragma unroll
+            for (int m = 2 * O; m < W::kAbreast; m *= 2)
+              keep += __shfl_xor_sync(kAll, keep, G * m);
+            to[(up ? N : 0) + order] = keep;
+          } else {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int j = 0; j < kLeft; ++j) to[w * N + (2 * j ^ order)] = v[w][2 * j];
           }
         }
       }
     };
-    if (marks.starts == 0u && n_tok == T) go(std::false_type{});
+    if (n_tok == 0) continue;
+    if (marks.starts == 0u && n_tok == H)
+      go(std::false_type{});
     else go(std::true_type{});
   }
-  meet<2 * kSsmPart>();                // (the preparers finish the last step)
+  meet<kBackThreads>();                // (the others finish the last step)
   if (!packed && at.chunk == 0 && P.hT[r] != nullptr)
     store_both(P.hT[r], at.batch * state_step + state_at, back);
   if (P.partial_params != nullptr)
@@ -564,7 +631,7 @@ static cudaError_t launch_back(const SsmParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<SsmParams*>(&p)};
   const int64_t grid = static_cast<int64_t>(p.b) * p.chunks * p.t * p.groups * p.slabs;
-  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(2 * kSsmPart), W::kSmem, args, st);
+  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kBackThreads), W::kSmem, args, st);
 }
 
 }  // namespace spb
