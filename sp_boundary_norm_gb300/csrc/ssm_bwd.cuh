@@ -23,7 +23,7 @@
 
 namespace spb {
 
-constexpr int kBackHelp = 256;         // threads that prepare and finish
+constexpr int kBackHelp = 128;         // threads that prepare and finish
 constexpr int kBackThreads = kSsmPart + kBackHelp;
 
 template <int DT, int N>
@@ -34,6 +34,8 @@ struct SsmBack {
   static constexpr int kWarps = kSsmPart / 32;                 // that hold states
   static constexpr int kBlockCh = kWarps * L::kChannels;
   static constexpr int kAbreast = 32 / L::kLanes;              // lanes of a warp with the same states
+  static constexpr int V = kBlockCh * H / kBackHelp > 2 ? kBlockCh * H / kBackHelp : 2;   // channels that
+                                                               // a thread prepares of a token
   static constexpr int kOrders = kAbreast < L::kStates ? kAbreast : L::kStates;
   static constexpr int kRow = kBlockCh * E + 16;
   static constexpr int kShared = 2 * N * E;
@@ -83,12 +85,13 @@ ssm_bwd_kernel(const SsmParams P) {
 
   if (warp >= W::kWarps) {
     // ------------------------------------------------- preparing, finishing --
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     const int ht = tid - kSsmPart;
-    constexpr int kPieces = CB * E / 16, kPiecesB = N * E / 16;
+    // pieces of 16 bytes of a step's rows, a thread's `kRows` tokens apart
+    constexpr int kPieces = CB * E / 16, kRows = kBackHelp / kPieces;
+    constexpr int kPiecesB = N * E / 16, kRowsB = kBackHelp / kPiecesB;
+    static_assert(kBackHelp % kPieces == 0 && kBackHelp % kPiecesB == 0, "whole rows");
     const int tok_p = ht / kPieces, at_p = ht % kPieces * 16;
     const int tok_b = ht / kPiecesB, at_b = ht % kPiecesB * 16;
-    static_assert(kBackHelp / kPieces >= H && kBackHelp / kPiecesB >= H, "a piece a thread");
     const bool live_p = at_p < at.live * E;
     const char* src[4] = {P.dt[r] + at.ch0 * E + at_p, P.u[r] + at.ch0 * E + at_p,
                           P.dy[r] + at.ch0 * E + at_p, gated ? P.z[r] + at.ch0 * E + at_p : nullptr};
@@ -99,62 +102,81 @@ ssm_bwd_kernel(const SsmParams P) {
         const int n_tok = tokens_of(k);
         const int64_t row = row0 + first_of(k);
         char* st = smem + (k & 3) * W::kStage;
-        if (live_p && tok_p < n_tok) {
-          char* dst = st + tok_p * W::kRow + at_p;
-          cp_async16(dst, src[0] + (row + tok_p) * P.ld_dt);
-          cp_async16(dst + H * W::kRow, src[1] + (row + tok_p) * P.ld_u);
-          cp_async16(dst + 2 * H * W::kRow, src[2] + (row + tok_p) * P.ld_dy);
-          if (gated) cp_async16(dst + 3 * H * W::kRow, src[3] + (row + tok_p) * P.ld_z);
+#pragma unroll
+        for (int i = 0; i < H; i += kRows) {
+          const int tok = tok_p + i;
+          if (live_p && tok < n_tok) {
+            char* dst = st + tok * W::kRow + at_p;
+            cp_async16(dst, src[0] + (row + tok) * P.ld_dt);
+            cp_async16(dst + H * W::kRow, src[1] + (row + tok) * P.ld_u);
+            cp_async16(dst + 2 * H * W::kRow, src[2] + (row + tok) * P.ld_dy);
+            if (gated) cp_async16(dst + 3 * H * W::kRow, src[3] + (row + tok) * P.ld_z);
+          }
         }
-        if (tok_b < n_tok) {
-          char* sh = st + 4 * H * W::kRow + tok_b * W::kShared + at_b;
-          cp_async16(sh, src_b + (row + tok_b) * P.ld_B);
-          cp_async16(sh + N * E, src_c + (row + tok_b) * P.ld_C);
+#pragma unroll
+        for (int i = 0; i < H; i += kRowsB) {
+          const int tok = tok_b + i;
+          if (tok < n_tok) {
+            char* sh = st + 4 * H * W::kRow + tok * W::kShared + at_b;
+            cp_async16(sh, src_b + (row + tok) * P.ld_B);
+            cp_async16(sh + N * E, src_c + (row + tok) * P.ld_C);
+          }
         }
       }
       cp_async_commit();
     };
-    // a thread's two channels of a token
-    const int my = ht / (CB / 2), ch = ht % (CB / 2) * 2;
+    // a thread's channels of a token
+    constexpr int V = W::V;
+    const int my = ht / (CB / V), ch = ht % (CB / V) * V;
     const bool mine = my < H, live = ch < at.live;
-    auto param = [&](const float* from) {
-      return from != nullptr && live ? *reinterpret_cast<const F2*>(from + rc + at.ch0 + ch) : F2(0);
-    };
-    const F2 bias = param(P.dt_bias), skip = param(P.D);
-    F2 dD = 0, dbias = 0;
+    F2 bias[V / 2], skip[V / 2], dD[V / 2], dbias[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      auto param = [&](const float* from) {
+        return from != nullptr && live ? *reinterpret_cast<const F2*>(from + rc + at.ch0 + ch + 2 * i)
+                                       : F2(0);
+      };
+      bias[i] = param(P.dt_bias);
+      skip[i] = param(P.D);
+      dD[i] = dbias[i] = 0;
+    }
     // what is kept of a token's channels until its sums are there
     struct Kept {
-      F2 d, u, e, slope, dz;
+      F2 d[V / 2], u[V / 2], e[V / 2], slope[V / 2], dz[V / 2];
     };
     auto prepare = [&](int k, Kept& x) {
       const char* st = smem + (k & 3) * W::kStage;
       if (mine) {
         const char* from = st + my * W::kRow + ch * E;
-        Pack<DT, 2> p;
-        F2 one[1];
-        auto read = [&](int a) {
+        Pack<DT, V> p;
+        auto read = [&](int a, F2 (&v)[V / 2]) {
           lds_pack(p, from + a * H * W::kRow);
-          unpack_pairs(p, one);
-          return live ? one[0] : F2(0);                        // (a dead channel adds zeros)
+          unpack_pairs(p, v);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) v[i] = live ? v[i] : F2(0);   // (a dead channel adds zeros)
         };
-        x.d = add2(read(0), bias);
-        x.u = read(1);
-        x.e = read(2);
-        x.dz = 0;
-        x.slope = f2(1.f, 1.f);
-        if (P.softplus) x.d = softplus2<DT>(x.d, &x.slope);
-        if (gated) {
-          // sg = sigmoid(z); silu' = sg + z sg (1 - sg)
-          const F2 z = read(3);
-          const F2 sg = rcp2(add2(exp2_of<DT, false, -1>(z), f2(1.f, 1.f)));
-          const F2 silu = mul2(z, sg);
-          x.dz = mul2(x.e, fma2(silu, fma2(sg, f2(-1.f, -1.f), f2(1.f, 1.f)), sg));
-          x.e = mul2(x.e, silu);
+        F2 z[V / 2];
+        read(0, x.d);
+        read(1, x.u);
+        read(2, x.e);
+        if (gated) read(3, z);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          x.d[i] = add2(x.d[i], bias[i]);
+          x.slope[i] = f2(1.f, 1.f);
+          if (P.softplus) x.d[i] = softplus2<DT>(x.d[i], &x.slope[i]);
+          if (gated) {
+            // sg = sigmoid(z); silu' = sg + z sg (1 - sg)
+            const F2 sg = rcp2(add2(exp2_of<DT, false, -1>(z[i]), f2(1.f, 1.f)));
+            const F2 silu = mul2(z[i], sg);
+            x.dz[i] = mul2(x.e[i], fma2(silu, fma2(sg, f2(-1.f, -1.f), f2(1.f, 1.f)), sg));
+            x.e[i] = mul2(x.e[i], silu);
+          }
+          const float2 a = split(x.d[i]), b = split(mul2(x.d[i], x.u[i]));
+          *reinterpret_cast<float4*>(dds + ((k & 3) * H + my) * W::kDRow + (ch + 2 * i) * 8) =
+              make_float4(a.x, b.x, a.y, b.y);
+          *reinterpret_cast<F2*>(es + ((k & 3) * H + my) * W::kERow + (ch + 2 * i) * 4) = x.e[i];
         }
-        const float2 a = split(x.d), b = split(mul2(x.d, x.u));
-        *reinterpret_cast<float4*>(dds + ((k & 3) * H + my) * W::kDRow + ch * 8) =
-            make_float4(a.x, b.x, a.y, b.y);
-        *reinterpret_cast<F2*>(es + ((k & 3) * H + my) * W::kERow + ch * 4) = x.e;
       }
       // B and C, four (two) states at a time, in every order
       const char* sh = st + 4 * H * W::kRow;
@@ -216,26 +238,33 @@ ssm_bwd_kernel(const SsmParams P) {
       if (!live || my >= n_tok) return;
       // the channels' sums over their lanes
       const char* out = outs + (k & 1) * 3 * W::kY + my * G * W::kYRow + ch * 4;
-      F2 through = 0, decay = 0, inner = 0;
+      F2 du[V / 2], ddt[V / 2], dz[V / 2];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        through = add2(through, *reinterpret_cast<const F2*>(out + g * W::kYRow));
-        decay = add2(decay, *reinterpret_cast<const F2*>(out + W::kY + g * W::kYRow));
-        if (gated) inner = add2(inner, *reinterpret_cast<const F2*>(out + 2 * W::kY + g * W::kYRow));
+      for (int i = 0; i < V / 2; ++i) {
+        F2 through = 0, decay = 0, inner = 0;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const char* from = out + g * W::kYRow + 8 * i;
+          through = add2(through, *reinterpret_cast<const F2*>(from));
+          decay = add2(decay, *reinterpret_cast<const F2*>(from + W::kY));
+          if (gated) inner = add2(inner, *reinterpret_cast<const F2*>(from + 2 * W::kY));
+        }
+        du[i] = fma2(x.d[i], through, mul2(skip[i], x.e[i]));
+        ddt[i] = mul2(fma2(x.u[i], through, mul2(decay, f2(kLn2, kLn2))), x.slope[i]);
+        if (gated) dz[i] = mul2(x.dz[i], fma2(skip[i], x.u[i], inner));
+        dD[i] = fma2(x.e[i], x.u[i], dD[i]);
+        dbias[i] = add2(dbias[i], ddt[i]);
       }
-      const F2 ddt = mul2(fma2(x.u, through, mul2(decay, f2(kLn2, kLn2))), x.slope);
-      dD = fma2(x.e, x.u, dD);
-      dbias = add2(dbias, ddt);
       const int64_t to = row + my, off = (at.ch0 + ch) * E;
-      auto store = [&](char* dst, F2 v) {
-        Pack<DT, 2> p;
-        const F2 w[1] = {v};
-        pack_pairs(p, w);
-        store_pack(dst + off, p);
-      };
-      store(P.du[r] + to * P.ld_du, fma2(x.d, through, mul2(skip, x.e)));
-      store(P.ddt[r] + to * P.ld_ddt, ddt);
-      if (gated) store(P.dz[r] + to * P.ld_dz, mul2(x.dz, fma2(skip, x.u, inner)));
+      Pack<DT, V> p;
+      pack_pairs(p, du);
+      store_pack(P.du[r] + to * P.ld_du + off, p);
+      pack_pairs(p, ddt);
+      store_pack(P.ddt[r] + to * P.ld_ddt + off, p);
+      if (gated) {
+        pack_pairs(p, dz);
+        store_pack(P.dz[r] + to * P.ld_dz + off, p);
+      }
     };
     ask(0);
     ask(1);
@@ -257,9 +286,11 @@ ssm_bwd_kernel(const SsmParams P) {
     float* to = P.partial_params + (at.batch * P.chunks + at.chunk) * P.t * P.c * (N + 2) +
                 static_cast<int64_t>(P.t) * P.c * N;
     F2* sum = reinterpret_cast<F2*>(smem);                     // [2][H][CB / 2]
-    if (mine) {
-      sum[my * (CB / 2) + ch / 2] = dD;
-      sum[(H + my) * (CB / 2) + ch / 2] = dbias;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if (!mine) continue;
+      sum[my * (CB / 2) + ch / 2 + i] = dD[i];
+      sum[(H + my) * (CB / 2) + ch / 2 + i] = dbias[i];
     }
     asm volatile("bar.sync 2, %0;" ::"n"(kBackHelp) : "memory");
     if (ht < CB) {
@@ -274,7 +305,6 @@ ssm_bwd_kernel(const SsmParams P) {
   }
 
   // ---------------------------------------------------------------- states --
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
   // the lane's two channels (dead ones go by the block's first, and add zeros), its order
   const int my_ch = warp * CW + lane / G * 2;
   const bool active = my_ch < at.live;
@@ -391,8 +421,8 @@ ssm_bwd_kernel(const SsmParams P) {
       auto forget = [&](int t, F2 (&h)[2][K]) {        // the state before a sequence
         load_both(P.h0[r], __shfl_sync(kAll, marks.seq, t) * state_step + state_at, h);
       };
-      // the states after token t of a step, and its decays
-      auto token = [&](const char* dt, const float* bt, F2 (&h)[2][K], F2 (&a)[2][K]) {
+      // the states after a token of a step
+      auto token = [&](const char* dt, const float* bt, F2 (&h)[2][K]) {
         const float4 v = *reinterpret_cast<const float4*>(dt);
         const float d[2] = {v.x, v.z}, in[2] = {v.y, v.w};
         F2 b[K];
@@ -401,8 +431,8 @@ ssm_bwd_kernel(const SsmParams P) {
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int p = 0; p < K; ++p) {
-            a[c][p] = pow2(mul2(f2(d[c], d[c]), a2[c][p]));
-            h[c][p] = fma2(a[c][p], h[c][p], mul2(f2(in[c], in[c]), b[p]));
+            const F2 a = pow2(mul2(f2(d[c], d[c]), a2[c][p]));
+            h[c][p] = fma2(a, h[c][p], mul2(f2(in[c], in[c]), b[p]));
           }
       };
       F2 begin[2][K];
@@ -415,12 +445,11 @@ ssm_bwd_kernel(const SsmParams P) {
         const char* low_d = dd_of(k + 1);
 #pragma unroll kUnroll
         for (int i = 0; i < H; ++i) {
-          F2 a[2][K];
           if (begins(i)) forget(i, begin);
-          token(low_d + i * W::kDRow, low + i * kOrderStride, begin, a);
+          token(low_d + i * W::kDRow, low + i * kOrderStride, begin);
         }
       }
-      F2 h[H][2][K], a[H][2][K];
+      F2 h[H][2][K];
       {
         F2 now[2][K];
         float2 inner[H];
@@ -433,24 +462,23 @@ ssm_bwd_kernel(const SsmParams P) {
           inner[i] = make_float2(0.f, 0.f);
           if (!SLOW || i < n_tok) {
             if (begins(half + i)) forget(half + i, now);
-            token(dd + i * W::kDRow, shared + i * kOrderStride, now, a[i]);
+            token(dd + i * W::kDRow, shared + i * kOrderStride, now);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int p = 0; p < K; ++p) h[i][c][p] = now[c][p];
-            if (gated) {
-              F2 q[K];
-              load_states(shared + i * kOrderStride + O * N, q);
-              float sum[2];
+            // (also without a gate: a branch here would keep the tokens apart)
+            F2 q[K];
+            load_states(shared + i * kOrderStride + O * N, q);
+            float sum[2];
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                F2 acc = mul2(now[c][0], q[0]);
-                if constexpr (K == 2) acc = fma2(now[c][1], q[1], acc);
-                const float2 x = split(acc);
-                sum[c] = x.x + x.y;
-              }
-              inner[i] = make_float2(sum[0], sum[1]);
+            for (int c = 0; c < 2; ++c) {
+              F2 acc = mul2(now[c][0], q[0]);
+              if constexpr (K == 2) acc = fma2(now[c][1], q[1], acc);
+              const float2 x = split(acc);
+              sum[c] = x.x + x.y;
             }
+            inner[i] = make_float2(sum[0], sum[1]);
           }
         }
         if (gated) {
@@ -459,30 +487,23 @@ ssm_bwd_kernel(const SsmParams P) {
             *reinterpret_cast<float2*>(out + 2 * W::kY + i * G * W::kYRow) = inner[i];
         }
       }
-      // what a token of the way back needs, asked for a token ahead of its use (the
-      // compiler keeps loads behind the stores of sums)
-      struct Operands {
-        float4 d;
-        float2 e;
-        F2 b[K], q[K];
-      };
-      auto operands = [&](int i) {
-        Operands x;
-        x.d = *reinterpret_cast<const float4*>(dd + i * W::kDRow);
-        x.e = *reinterpret_cast<const float2*>(ee + i * W::kERow);
-        load_states(shared + i * kOrderStride, x.b);
-        load_states(shared + i * kOrderStride + O * N, x.q);
-        return x;
-      };
-      Operands ahead = operands(H - 1);
+      // Back.  The sums wait in registers, which the states give up, until the step's last:
+      // without a store in between, loads go ahead of what is being summed.
+      constexpr int kLevels = O == 4 ? 2 : 1;          // of lanes, that halve the states
+      constexpr int kLeft = S >> kLevels;              // states of dB and of dC then
+      constexpr int kBoth = W::kAbreast > O ? 1 : 2;   // dB and dC, or one of them
+      float4 wait[H];
+      float wait_bc[H][kBoth * kLeft];
 #pragma unroll kUnroll
       for (int i = H - 1; i >= 0; --i) {
-        const Operands x = ahead;
-        if (i > 0) ahead = operands(i - 1);
         if (!SLOW || i < n_tok) {
           const int t = half + i;
-          const float d[2] = {x.d.x, x.d.z}, in[2] = {x.d.y, x.d.w}, e[2] = {x.e.x, x.e.y};
-          F2 db[K], dc[K], before[2][K];
+          const float4 dv = *reinterpret_cast<const float4*>(dd + i * W::kDRow);
+          const float2 ev = *reinterpret_cast<const float2*>(ee + i * W::kERow);
+          const float d[2] = {dv.x, dv.z}, in[2] = {dv.y, dv.w}, e[2] = {ev.x, ev.y};
+          F2 b[K], q[K], db[K], dc[K], before[2][K];
+          load_states(shared + i * kOrderStride, b);
+          load_states(shared + i * kOrderStride + O * N, q);
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -496,11 +517,11 @@ ssm_bwd_kernel(const SsmParams P) {
             F2 to_u = 0, to_d = 0;
 #pragma unroll
             for (int p = 0; p < K; ++p) {
-              const F2 gr = fma2(x.q[p], e2, back[c][p]);
+              const F2 gr = fma2(q[p], e2, back[c][p]);
               dc[p] = c == 0 ? mul2(h[i][c][p], e2) : fma2(h[i][c][p], e2, dc[p]);
               db[p] = c == 0 ? mul2(gr, in2) : fma2(gr, in2, db[p]);
-              to_u = p == 0 ? mul2(gr, x.b[p]) : fma2(gr, x.b[p], to_u);
-              back[c][p] = mul2(a[i][c][p], gr);
+              to_u = p == 0 ? mul2(gr, b[p]) : fma2(gr, b[p], to_u);
+              back[c][p] = mul2(pow2(mul2(d2, a2[c][p])), gr);
               const F2 g = mul2(back[c][p], before[c][p]);
               to_d = p == 0 ? mul2(g, a2[c][p]) : fma2(g, a2[c][p], to_d);
               dA[c][p] = fma2(g, d2, dA[c][p]);
@@ -517,9 +538,7 @@ ssm_bwd_kernel(const SsmParams P) {
                 run0 + t > 0 ? find_seq(P.cu_seqlens, P.n_seqs, run0 + t - 1) : 0;
             load_both(from, prev * state_step + state_at, back);
           }
-          *reinterpret_cast<float2*>(out + i * G * W::kYRow) = make_float2(through[0], through[1]);
-          *reinterpret_cast<float2*>(out + W::kY + i * G * W::kYRow) =
-              make_float2(decay[0], decay[1]);
+          wait[i] = make_float4(through[0], through[1], decay[0], decay[1]);
           // dB and dC over the warp's lanes with the same states: keep the even places,
           // hand on the odd ones; then of two states; then dB or dC
           float v[2][S];
@@ -531,7 +550,6 @@ ssm_bwd_kernel(const SsmParams P) {
             v[1][2 * p] = w.x;
             v[1][2 * p + 1] = w.y;
           }
-          constexpr int kLevels = O == 4 ? 2 : 1;      // that halve the states
 #pragma unroll
           for (int level = 0; level < kLevels; ++level) {
             const int step = 1 << level;
@@ -541,9 +559,7 @@ ssm_bwd_kernel(const SsmParams P) {
               for (int j = 0; j < S; j += 2 * step)
                 v[w][j] += __shfl_xor_sync(kAll, v[w][j + step], G * step);
           }
-          constexpr int kLeft = S >> kLevels;          // states of dB and of dC: v[.][0], v[.][2]
-          float* to = put + i * 2 * N + n0;
-          if constexpr (W::kAbreast > O) {
+          if constexpr (kBoth == 1) {
             // lanes left over: one takes dB, the other dC (and others the same)
             static_assert(kLeft == 1, "one state");
             const bool up = lane & G * O;
@@ -553,13 +569,29 @@ ssm_bwd_kernel(const SsmParams P) {
 #pragma unroll
             for (int m = 2 * O; m < W::kAbreast; m *= 2)
               keep += __shfl_xor_sync(kAll, keep, G * m);
-            to[(up ? N : 0) + order] = keep;
+            wait_bc[i][0] = keep;
           } else {
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
-              for (int j = 0; j < kLeft; ++j) to[w * N + (2 * j ^ order)] = v[w][2 * j];
+              for (int j = 0; j < kLeft; ++j) wait_bc[i][w * kLeft + j] = v[w][2 * j];
           }
+        }
+      }
+#pragma unroll kUnroll
+      for (int i = 0; i < H; ++i) {
+        if (SLOW && i >= n_tok) break;
+        char* to = out + i * G * W::kYRow;
+        *reinterpret_cast<float2*>(to) = make_float2(wait[i].x, wait[i].y);
+        *reinterpret_cast<float2*>(to + W::kY) = make_float2(wait[i].z, wait[i].w);
+        float* bc = put + i * 2 * N + n0;
+        if constexpr (kBoth == 1) {
+          bc[(lane & G * O ? N : 0) + order] = wait_bc[i][0];
+        } else {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int j = 0; j < kLeft; ++j) bc[w * N + (2 * j ^ order)] = wait_bc[i][w * kLeft + j];
         }
       }
     };
