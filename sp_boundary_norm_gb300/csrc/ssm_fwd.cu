@@ -30,7 +30,7 @@ SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bo
   k.slabs = static_cast<int32_t>((of_group + block - 1) / block);
   const int64_t blocks = b * t * groups * k.slabs, sms = device_sm_count();
   int64_t chunks = 1;
-  if (blocks * 2 <= sms) chunks = (bwd ? sms : 2 * sms) / blocks;
+  if (blocks * 2 <= sms) chunks = sms / blocks;
   if (chunks > s / 128) chunks = s / 128 > 0 ? s / 128 : 1;
   k.chunk_len = ((s + chunks - 1) / chunks + kSsmTile - 1) / kSsmTile * kSsmTile;
   k.chunks = static_cast<int32_t>((s + k.chunk_len - 1) / k.chunk_len);
