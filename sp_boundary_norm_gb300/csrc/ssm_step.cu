@@ -9,7 +9,7 @@
 namespace spb {
 
 constexpr int kStepThreads = 256;
-constexpr int kStepBlocks = 3;         // of an SM, by their registers
+constexpr int kStepBlocks = 4;         // of an SM, by their registers
 constexpr int kStepRows = 4;           // sequences of a step
 
 template <int DT, int N>
