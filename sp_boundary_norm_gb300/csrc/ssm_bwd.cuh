@@ -23,6 +23,9 @@
 
 namespace spb {
 
+// Sums over tokens are taken up by second ones every so many steps: 8192 terms added one
+// by one lost a quarter more of dA's digits than the rest of the arithmetic does.
+constexpr int kSumSteps = 32;
 constexpr int kBackHelp = 128;         // threads that prepare and finish
 constexpr int kBackThreads = kSsmPart + kBackHelp;
 
@@ -129,7 +132,7 @@ ssm_bwd_kernel(const SsmParams P) {
     constexpr int V = W::V;
     const int my = ht / (CB / V), ch = ht % (CB / V) * V;
     const bool mine = my < H, live = ch < at.live;
-    F2 bias[V / 2], skip[V / 2], dD[V / 2], dbias[V / 2];
+    F2 bias[V / 2], skip[V / 2], dD[V / 2], dbias[V / 2], all_D[V / 2], all_bias[V / 2];
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       auto param = [&](const float* from) {
@@ -138,8 +141,16 @@ ssm_bwd_kernel(const SsmParams P) {
       };
       bias[i] = param(P.dt_bias);
       skip[i] = param(P.D);
-      dD[i] = dbias[i] = 0;
+      dD[i] = dbias[i] = all_D[i] = all_bias[i] = 0;
     }
+    auto take_up = [&] {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        all_D[i] = add2(all_D[i], dD[i]);
+        all_bias[i] = add2(all_bias[i], dbias[i]);
+        dD[i] = dbias[i] = 0;
+      }
+    };
     // what is kept of a token's channels until its sums are there
     struct Kept {
       F2 d[V / 2], u[V / 2], e[V / 2], slope[V / 2], dz[V / 2];
@@ -274,6 +285,7 @@ ssm_bwd_kernel(const SsmParams P) {
       meet<kBackThreads>();
       ask(k + 4);                      // (in the place of step k's, which are prepared)
       if (k >= 1) finish(k - 1, x);
+      if (k % kSumSteps == 0) take_up();
       if (k + 2 < n_steps) prepare(k + 2, x);
     };
     for (int k = -2; k <= n_steps; k += 3) {
@@ -282,6 +294,7 @@ ssm_bwd_kernel(const SsmParams P) {
       if (k + 2 <= n_steps) step(k + 2, kept[2]);
     }
     if (P.partial_params == nullptr) return;
+    take_up();
     // the block's tokens of a channel, in the order of its threads
     float* to = P.partial_params + (at.batch * P.chunks + at.chunk) * P.t * P.c * (N + 2) +
                 static_cast<int64_t>(P.t) * P.c * N;
@@ -289,8 +302,8 @@ ssm_bwd_kernel(const SsmParams P) {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       if (!mine) continue;
-      sum[my * (CB / 2) + ch / 2 + i] = dD[i];
-      sum[(H + my) * (CB / 2) + ch / 2 + i] = dbias[i];
+      sum[my * (CB / 2) + ch / 2 + i] = all_D[i];
+      sum[(H + my) * (CB / 2) + ch / 2 + i] = all_bias[i];
     }
     asm volatile("bar.sync 2, %0;" ::"n"(kBackHelp) : "memory");
     if (ht < CB) {
@@ -352,14 +365,14 @@ ssm_bwd_kernel(const SsmParams P) {
   };
   // the gradient that comes from behind (times the decay in between); the decay rates
   // in powers of two, their gradients' sums; the state before the run, and the next run's
-  F2 back[2][K], a2[2][K], dA[2][K], first[2][K], next[2][K];
+  F2 back[2][K], a2[2][K], dA[2][K], all_A[2][K], first[2][K], next[2][K];
   load_both(P.A, mine, a2);
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int p = 0; p < K; ++p) {
       a2[c][p] = mul2(a2[c][p], f2(kLog2e, kLog2e));
-      dA[c][p] = first[c][p] = 0;
+      dA[c][p] = all_A[c][p] = first[c][p] = 0;
     }
   if (P.chunks > 1) {
     load_both(P.carry, (at.batch * P.chunks + at.chunk) * P.t * P.c * N + mine, back);
@@ -595,6 +608,15 @@ ssm_bwd_kernel(const SsmParams P) {
         }
       }
     };
+    if (k % kSumSteps == 0) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int p = 0; p < K; ++p) {
+          all_A[c][p] = add2(all_A[c][p], dA[c][p]);
+          dA[c][p] = 0;
+        }
+    }
     if (n_tok == 0) continue;
     if (marks.starts == 0u && n_tok == H)
       go(std::false_type{});
@@ -603,6 +625,10 @@ ssm_bwd_kernel(const SsmParams P) {
   meet<kBackThreads>();                // (the others finish the last step)
   if (!packed && at.chunk == 0 && P.hT[r] != nullptr)
     store_both(P.hT[r], at.batch * state_step + state_at, back);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int p = 0; p < K; ++p) dA[c][p] = add2(all_A[c][p], dA[c][p]);
   if (P.partial_params != nullptr)
     store_both(P.partial_params + (at.batch * P.chunks + at.chunk) * P.t * P.c * (N + 2), mine, dA);
 }
