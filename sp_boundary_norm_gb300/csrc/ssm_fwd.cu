@@ -29,10 +29,20 @@ SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bo
   SsmSplit k{};
   k.slabs = static_cast<int32_t>((of_group + block - 1) / block);
   const int64_t blocks = b * t * groups * k.slabs, sms = device_sm_count();
-  int64_t chunks = 1;
-  if (blocks * 2 <= sms) chunks = sms / blocks;
-  if (chunks > s / 128) chunks = s / 128 > 0 ? s / 128 : 1;
-  k.chunk_len = ((s + chunks - 1) / chunks + kSsmTile - 1) / kSsmTile * kSsmTile;
+  // A block has an SM to itself, so a call takes as many waves of blocks as they need, each
+  // as long as a chunk.  Chunks cost a walk for what enters them: 66 clocks a token beside
+  // the forward's 118 and the backward's 400, and some 48 tokens' time to begin.
+  const double walk = bwd ? 1.2 : 1.6;
+  double least = 0;
+  for (int64_t n = 1; n <= 64 && (n == 1 || n * 128 <= s); ++n) {
+    const int64_t len = ((s + n - 1) / n + kSsmTile - 1) / kSsmTile * kSsmTile;
+    const int64_t waves = (blocks * n + sms - 1) / sms;
+    const double cost = static_cast<double>(waves) * static_cast<double>(len + 48) *
+                        (n > 1 ? walk : 1.0);
+    if (n > 1 && cost > 0.97 * least) continue;
+    least = cost;
+    k.chunk_len = len;
+  }
   k.chunks = static_cast<int32_t>((s + k.chunk_len - 1) / k.chunk_len);
   const int64_t parts = b * k.chunks, width = t * c;
   if (k.chunks > 1) {
