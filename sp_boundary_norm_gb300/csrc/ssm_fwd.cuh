@@ -398,17 +398,31 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const SsmParams P) {
   }
   float* carry = P.carry + batch * P.chunks * width + i;
   const float* steps = P.steps + batch * P.chunks * P.t * P.c + chan;
-  for (int n = 0; n < P.chunks; ++n) {
-    const int64_t k = BACK ? P.chunks - 1 - n : n;
-    bool cut = false;                  // a sequence begins in the chunk
-    if (packed) {
-      const int64_t end = (k + 1) * P.chunk_len < P.s ? (k + 1) * P.chunk_len : P.s;
-      cut = k == 0 || find_seq(P.cu_seqlens, P.n_seqs, end - 1) !=
-                          find_seq(P.cu_seqlens, P.n_seqs, k * P.chunk_len - 1);
+  // eight chunks' values are asked for before the first is used
+  constexpr int kAhead = 8;
+  for (int n0 = 0; n0 < P.chunks; n0 += kAhead) {
+    float handed[kAhead], decay[kAhead];
+    bool cut[kAhead];                  // a sequence begins in the chunk
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (n0 + i >= P.chunks) break;
+      const int64_t k = BACK ? P.chunks - 1 - n0 - i : n0 + i;
+      handed[i] = carry[k * width];
+      decay[i] = steps[k * P.t * P.c];
+      cut[i] = false;
+      if (packed) {
+        const int64_t end = (k + 1) * P.chunk_len < P.s ? (k + 1) * P.chunk_len : P.s;
+        cut[i] = k == 0 || find_seq(P.cu_seqlens, P.n_seqs, end - 1) !=
+                               find_seq(P.cu_seqlens, P.n_seqs, k * P.chunk_len - 1);
+      }
     }
-    const float handed = carry[k * width];
-    carry[k * width] = x;
-    x = cut ? handed : fmaf(pow2(a2 * steps[k * P.t * P.c]), x, handed);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (n0 + i >= P.chunks) break;
+      const int64_t k = BACK ? P.chunks - 1 - n0 - i : n0 + i;
+      carry[k * width] = x;
+      x = cut[i] ? handed[i] : fmaf(pow2(a2 * decay[i]), x, handed[i]);
+    }
   }
 }
 
