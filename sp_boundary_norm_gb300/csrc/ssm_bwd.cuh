@@ -49,9 +49,10 @@ struct SsmBack {
   static constexpr int kYRow = kBlockCh * 4 + 32;
   static constexpr int kY = H * L::kLanes * kYRow;             // a lane's parts of one sum
   static constexpr int kSum = H * 2 * N * 4;                   // dB and dC of a warp's step
+  static constexpr int kWhole = kSsmPart * L::kStates * 2 * 4; // dA so far, a lane's
   // four steps' rows, and what is prepared of them; two steps' sums
   static constexpr size_t kSmem =
-      4 * (kStage + kBC + H * (kDRow + kERow)) + 2 * (3 * kY + kWarps * kSum);
+      4 * (kStage + kBC + H * (kDRow + kERow)) + 2 * (3 * kY + kWarps * kSum) + kWhole;
 };
 
 template <int DT, int N>
@@ -365,14 +366,14 @@ ssm_bwd_kernel(const SsmParams P) {
   };
   // the gradient that comes from behind (times the decay in between); the decay rates
   // in powers of two, their gradients' sums; the state before the run, and the next run's
-  F2 back[2][K], a2[2][K], dA[2][K], all_A[2][K], first[2][K], next[2][K];
+  F2 back[2][K], a2[2][K], dA[2][K], first[2][K], next[2][K];
   load_both(P.A, mine, a2);
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int p = 0; p < K; ++p) {
       a2[c][p] = mul2(a2[c][p], f2(kLog2e, kLog2e));
-      dA[c][p] = all_A[c][p] = first[c][p] = 0;
+      dA[c][p] = first[c][p] = 0;
     }
   if (P.chunks > 1) {
     load_both(P.carry, (at.batch * P.chunks + at.chunk) * P.t * P.c * N + mine, back);
@@ -395,6 +396,19 @@ ssm_bwd_kernel(const SsmParams P) {
     load_states(P.states[r] + i + N, next[1]);
   };
   if (n_runs > 0) run_state(0);
+  // dA so far, in shared memory (its registers would cost 2 % of the walk)
+  F2* whole = reinterpret_cast<F2*>(sums + 2 * W::kWarps * W::kSum) + tid;
+#pragma unroll
+  for (int i = 0; i < 2 * K; ++i) whole[i * kSsmPart] = 0;
+  auto take_up = [&] {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int p = 0; p < K; ++p) {
+        whole[(c * K + p) * kSsmPart] = add2(whole[(c * K + p) * kSsmPart], dA[c][p]);
+        dA[c][p] = 0;
+      }
+  };
   SsmMarks marks{0u, 0};
 
   meet<kBackThreads>();
@@ -608,15 +622,7 @@ ssm_bwd_kernel(const SsmParams P) {
         }
       }
     };
-    if (k % kSumSteps == 0) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int p = 0; p < K; ++p) {
-          all_A[c][p] = add2(all_A[c][p], dA[c][p]);
-          dA[c][p] = 0;
-        }
-    }
+    if (k % kSumSteps == 0) take_up();
     if (n_tok == 0) continue;
     if (marks.starts == 0u && n_tok == H)
       go(std::false_type{});
@@ -628,7 +634,7 @@ ssm_bwd_kernel(const SsmParams P) {
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int p = 0; p < K; ++p) dA[c][p] = add2(all_A[c][p], dA[c][p]);
+    for (int p = 0; p < K; ++p) dA[c][p] = add2(whole[(c * K + p) * kSsmPart], dA[c][p]);
   if (P.partial_params != nullptr)
     store_both(P.partial_params + (at.batch * P.chunks + at.chunk) * P.t * P.c * (N + 2), mine, dA);
 }
