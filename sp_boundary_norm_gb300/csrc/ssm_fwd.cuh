@@ -421,7 +421,9 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const SsmParams P) {
       if (n0 + i >= P.chunks) break;
       const int64_t k = BACK ? P.chunks - 1 - n0 - i : n0 + i;
       carry[k * width] = x;
-      x = cut[i] ? handed[i] : fmaf(pow2(a2 * decay[i]), x, handed[i]);
+      // (A > 0: a chunk's decay may overflow where the state behind it is zero or small)
+      const float half = pow2(0.5f * a2 * decay[i]);
+      x = cut[i] || x == 0.f ? handed[i] : fmaf(half, half * x, handed[i]);
     }
   }
 }

@@ -553,6 +553,57 @@ def test_ssm_what_is_not_finite_stays_in_its_sequence(c):
         assert not torch.isfinite(o["y"][0][0, 300:520]).any()
 
 
+def test_ssm_states_that_grow_behind_padding():
+    """A > 0: a chunk's decay overflows while the state that enters it is still zero.
+    A decay of d A = 1 is off by at most 2^-19 of itself, so 20 tokens' product by 2^-14,
+    inside check_ssm's bound of 2^-9."""
+    i = ssm_inputs(1, 1, 1, 2048, 16, 16, 1, F32, 33, False, gated=False)
+    i["A"] = i["A"].abs() * 0 + 1
+    i["dt"], i["dt_bias"] = [torch.full_like(x, 0.5) for x in i["dt"]], None
+    i["u"][0][:, :-20] = 0
+    o = run_ssm(i, 1, None, False, back=False)
+    assert torch.isfinite(o["y"][0]).all() and (o["y"][0][:, :-20] == 0).all()
+    check_ssm(i, o, None, False)
+
+
+def test_ssm_small_states_that_grow():
+    """The same from a first state of 2^-100: d A = 0.1 a token, so e^204.8 2^-100 = 2^195
+    is too much for float32, but not before token 1580; compared are 1500.  Each decay is
+    off by 2^-22.8 and the rounding of d A, below 0.1 2^-23: 1500 tokens 2^-12."""
+    i = ssm_inputs(1, 1, 1, 2048, 16, 16, 1, F32, 34, True, gated=False)
+    i["A"] = i["A"].abs() * 0 + 0.1
+    i["dt"], i["dt_bias"] = [torch.ones_like(x) for x in i["dt"]], None
+    i["u"][0].zero_()
+    i["h0"][0].fill_(2.0 ** -100)
+    i["C"] = [torch.full_like(x, 1 / 16) for x in i["C"]]
+    y = f64(run_ssm(i, 1, None, True, soft=False, back=False)["y"][0])[0, :1500]
+    want = 2.0 ** -100 * np.exp(0.1 * np.arange(1, 1501))[:, None]
+    assert (np.abs(y - want) <= 2.0 ** -11 * want).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP, F32])
+@pytest.mark.parametrize("s", [1, 3, 600])
+def test_ssm_masked_tokens(dtype, s):
+    """Steps of -infinity or of the type's lowest value: such a token leaves the state as
+    it is, takes no part of u, and every gradient is finite."""
+    i = ssm_inputs(2, 2, 2, s, 72, 16, 1, dtype, 35, True)
+    for x in i["dt"]:
+        x[0, : (s + 1) // 2] = -float("inf")
+        x[1, s // 2:] = torch.finfo(dtype).min
+    o = run_ssm(i, 2, None, True)
+    check_ssm(i, o, None, True)
+    assert all((o["ddt"][r][0, : (s + 1) // 2] == 0).all() for r in range(2))
+    check_ssm(i, run_ssm(i, 2, None, True, back=False), None, True)
+
+
+def test_sixteen_ranks():
+    """The most ranks, with every argument."""
+    i = ssm_inputs(16, 2, 2, 33, 16, 16, 2, BF, 36, True)
+    check_ssm(i, run_ssm(i, 2, None, True), None, True)
+    c = conv_inputs(16, 3, 1, 50, 16, 4, BF, 36, True)
+    check_conv(c, run_conv(c, 3, "silu", offsets([20, 2, 28]), True), "silu", [20, 2, 28], True)
+
+
 def test_long_memory_keeps_its_digits():
     """Steps near 0.001: states that gather over thousands of tokens, in norm."""
     i = ssm_inputs(1, 1, 1, 6000, 64, 16, 1, F32, 30, True)
