@@ -149,7 +149,7 @@ int conv_bwd_parts(int64_t b, int64_t s, int c, int t, int dtype);
 // ---------------------------------------------------------- selective scan --
 constexpr int kSsmRun = 16;             // tokens of one saved state
 constexpr int kSsmTile = 16;            // tokens of a step of a block
-constexpr int kSsmStepTokens = 4;       // most tokens of a decoding step
+constexpr int kSsmStepTokens = 16;      // most tokens of a sequence in a decoding step
 
 struct SsmParams {
   const char* u[SP_MAX_RANKS];

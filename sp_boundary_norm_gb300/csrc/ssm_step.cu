@@ -1,25 +1,32 @@
-// Selective scan of a few tokens, as in decoding: bound by reading and writing the
-// states once.  A block takes the channels of eight warps and walks sequences, four a
-// step.  A step's states and tokens are asked for one step ahead; the tokens are prepared
-// (softplus, d u, D u, silu(z)) once for each channel in shared memory, where a channel's
-// lanes then find them.  Measured on a GB300, bf16, 64 sequences of 8 ranks' 1024 channels
-// of 16 states: SSM_STEP_FIGURE.
+// Selective scan of a few tokens of many sequences, as in decoding: bound by reading and
+// writing the states once.  A block takes the channels of eight warps and walks sequences,
+// as many a step as have 16 tokens (at most four).  A step's states and tokens are asked
+// for one step ahead; the tokens are prepared (softplus, d u, D u, silu(z)) once for each
+// channel in shared memory, where a channel's lanes then find them.  Measured on a GB300,
+// bf16, 64 sequences of 8 ranks' 1024 channels of 16 states: 72 MB in 17.2 us, 4.2 TB/s;
+// the same accesses without the arithmetic took 17.7.  (A block for every sequence and 32
+// channels, which prepared its tokens itself: 23 us; three blocks an SM 21.)
+//
+// Up to 16 tokens a sequence (kSsmStepTokens) come here.  The other form's blocks start up
+// for one sequence each: 64 sequences of 1, 4, 8 and 16 tokens took 13, 26, 45 and 82 us
+// here (in place, replayed) and 123, 138, 160 and 165 there; one sequence of 1, 8 and 16
+// tokens 2.2, 3.1 and 3.7 here and 3.1, 3.7 and 3.5 there.
 #include "ssm.cuh"
 
 namespace spb {
 
 constexpr int kStepThreads = 256;
 constexpr int kStepBlocks = 4;         // of an SM, by their registers
-constexpr int kStepRows = 4;           // sequences of a step
 
-template <int DT, int N>
+// R: sequences of a step, with kSsmStepTokens tokens in all at most
+template <int DT, int N, int R>
 __global__ void __launch_bounds__(kStepThreads, kStepBlocks)
 ssm_step_kernel(const SsmParams P) {
   using L = SsmLanes<N>;
-  constexpr int E = ElemSize<DT>::value, K = L::kPairs, G = L::kLanes, R = kStepRows;
+  constexpr int E = ElemSize<DT>::value, K = L::kPairs, G = L::kLanes;
   constexpr int CB = kStepThreads / G;
-  __shared__ float4 prepared[2][R * kSsmStepTokens][CB];       // d, d u, D u, silu(z)
-  __shared__ __align__(16) float shared[2][R * kSsmStepTokens][2 * N];
+  __shared__ float4 prepared[2][kSsmStepTokens][CB];       // d, d u, D u, silu(z)
+  __shared__ __align__(16) float shared[2][kSsmStepTokens][2 * N];
   pdl_wait();
   const int tid = threadIdx.x;
   const int per_part = P.t * P.groups * P.slabs;
@@ -150,30 +157,37 @@ ssm_step_kernel(const SsmParams P) {
   }
 }
 
-template <int DT, int N>
+template <int DT, int N, int R>
 static cudaError_t launch_step(const SsmParams& p, cudaStream_t st) {
   constexpr int CB = kStepThreads / SsmLanes<N>::kLanes;
   SsmParams q = p;
   q.slabs = (p.c / p.groups + CB - 1) / CB;
   // one wave of blocks, each with as many whole steps of the sequences
   const int64_t across = static_cast<int64_t>(p.t) * p.groups * q.slabs;
-  const int64_t steps = (p.b + kStepRows - 1) / kStepRows;
+  const int64_t steps = (p.b + R - 1) / R;
   int64_t parts = static_cast<int64_t>(device_sm_count()) * kStepBlocks / across;
   parts = parts < 1 ? 1 : parts < steps ? parts : steps;
-  q.chunk_len = (steps + parts - 1) / parts * kStepRows;
+  q.chunk_len = (steps + parts - 1) / parts * R;
   parts = (p.b + q.chunk_len - 1) / q.chunk_len;
   void* args[] = {&q};
-  return launch_pdl(reinterpret_cast<const void*>(&ssm_step_kernel<DT, N>),
+  return launch_pdl(reinterpret_cast<const void*>(&ssm_step_kernel<DT, N, R>),
                     dim3(static_cast<unsigned>(parts * across)), dim3(kStepThreads), 0, args, st);
+}
+
+template <int DT, int N>
+static cudaError_t launch_rows(const SsmParams& p, cudaStream_t st) {
+  return p.s * 4 <= kSsmStepTokens   ? launch_step<DT, N, 4>(p, st)
+         : p.s * 2 <= kSsmStepTokens ? launch_step<DT, N, 2>(p, st)
+                                     : launch_step<DT, N, 1>(p, st);
 }
 
 template <int DT>
 static cudaError_t launch_states(const SsmParams& p, cudaStream_t st) {
   switch (p.n) {
-    case 8: return launch_step<DT, 8>(p, st);
-    case 16: return launch_step<DT, 16>(p, st);
-    case 32: return launch_step<DT, 32>(p, st);
-    default: return launch_step<DT, 64>(p, st);
+    case 8: return launch_rows<DT, 8>(p, st);
+    case 16: return launch_rows<DT, 16>(p, st);
+    case 32: return launch_rows<DT, 32>(p, st);
+    default: return launch_rows<DT, 64>(p, st);
   }
 }
 
