@@ -1,5 +1,6 @@
 // Device helpers of the operators between g and the next g* (rotary
-// positions, gated recurrence, group norm): element types and packed loads.
+// positions, gated recurrence, group norm, causal convolution, selective scan): element
+// types and packed loads.
 //
 // These tensors hold the whole sequence and one rank's channels.  DT is an
 // sp_dtype_t: bf16, fp16 or float32 elements; all arithmetic is float32, each

@@ -19,9 +19,9 @@
 // memory in each of these orders.
 //
 // What bounds it is, as in the forward's walk, one warp of states a scheduler: 400 clocks a
-// token, in which it issues 200 instructions (the schedulers issue in 42 % of the time,
-// shared memory moves in 36 %).  Measured on a GB300, bf16, 8 x 8192 x 1024 tokens of 16
-// states, gated: 1667 us, of which 936 MB would take 138.  Not faster: decays kept in
+// token, in which the scheduler issues 183 instructions of its two warps (in 44 % of the
+// time; shared memory moves in 48 %).  Measured on a GB300, bf16, 8 x 8192 x 1024 tokens of 16
+// states, gated: 1646 us; its 950 MB would take 140.  Not faster: decays kept in
 // registers (the same), two states a lane in twice the warps (a quarter slower: d, B, C
 // and the parts go through shared memory twice as often), the next step's way there beside
 // this one's way back (a quarter slower), eight helping warps or registers handed between

@@ -31,7 +31,10 @@ SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bo
   const int64_t blocks = b * t * groups * k.slabs, sms = device_sm_count();
   // A block has an SM to itself, so a call takes as many waves of blocks as they need, each
   // as long as a chunk.  Chunks cost a walk for what enters them: 66 clocks a token beside
-  // the forward's 118 and the backward's 400, and some 48 tokens' time to begin.
+  // the forward's 118 and the backward's 400, and some 48 tokens' time to begin.  (Measured:
+  // 8 x 8192 x 1024, 128 blocks, forward 531 us whole, 675 cut; 32,769 x 512, 8 blocks that
+  // would walk 1.9 ms, cut in 19 170 us; 2 x 3 x 701 x 272 of 32 states, float32, both
+  // directions, cut until two blocks an SM 135 us, by this rule 127.)
   const double walk = bwd ? 1.2 : 1.6;
   double least = 0;
   for (int64_t n = 1; n <= 64 && (n == 1 || n * 128 <= s); ++n) {

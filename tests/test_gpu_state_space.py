@@ -750,6 +750,50 @@ def test_layer_and_its_graph():
         assert (a.double().cpu() - b).norm() < 6 * 2.0 ** -8 * b.norm(), k
 
 
+def test_layer_decodes_in_a_graph():
+    """A prompt through the convolution and the scan, then tokens one by one from a captured
+    step that keeps its states in place: as one call over all tokens.  Both round u and y to
+    bf16 once and differ before that by the arithmetic, 2^-15 of a magnitude of at most 16
+    times the result in norm: 2 2^-8 + 2^-10 < 3 2^-8."""
+    t, b, s, c, n, prompt = 2, 3, 40, 64, 16, 29
+    gen = torch.Generator().manual_seed(42)
+    i = ssm_inputs(t, b, b, s, c, n, 1, BF, 43, False)
+    x = [rand((b, s, c), gen, BF) for _ in range(t)]
+    weight, bias = rand((t * c, 4), gen, BF, 0.5), rand((t * c,), gen, BF, 0.1)
+    how = dict(D=i["D"], dt_bias=i["dt_bias"])
+
+    def run(x, dt, z, B, C, x0, h0, xT, hT):
+        u, y = nans(t, x[0].shape, BF), nans(t, x[0].shape, BF)
+        sp.sp_causal_conv_fwd(x, weight, bias, act="silu", x0=x0, y=u, xT=xT)
+        ws = scratch(sp.sp_selective_scan_fwd_workspace_bytes(b, x[0].shape[1], c, n, 1, t))
+        sp.sp_selective_scan_fwd(u, dt, i["A"], B, C, z=z, h0=h0, y=y, hT=hT, workspace=ws, **how)
+        return y
+
+    rows = [x, i["dt"], i["z"], i["B"], i["C"]]
+    piece = lambda lo, hi: [[r[:, lo:hi].contiguous() for r in k] for k in rows]
+    xT, hT = nans(t, (b, 3, c), BF), nans(t, (b, c, n), F32)
+    want = run(*piece(0, s), None, None, nans(t, (b, 3, c), BF), nans(t, (b, c, n), F32))
+    got = [[y] for y in run(*piece(0, prompt), None, None, xT, hT)]
+    token = piece(prompt, prompt + 1)
+    before = [v.clone() for v in xT + hT]
+    run(*token, xT, hT, xT, hT)                          # (a first call outside the capture)
+    for v, k in zip(xT + hT, before):
+        v.copy_(k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run(*token, xT, hT, xT, hT)
+    for k in range(prompt, s):
+        for have, new in zip(token, piece(k, k + 1)):
+            for a, v in zip(have, new):
+                a.copy_(v)
+        graph.replay()
+        for r in range(t):
+            got[r].append(y[r].clone())
+    for r in range(t):
+        a, w = torch.cat(got[r], 1).double(), want[r].double()
+        assert (a - w).norm() < 3 * 2.0 ** -8 * w.norm(), r
+
+
 def test_layer_over_ranks_is_each_rank():
     """Eight ranks in one call give the bits of eight calls."""
     i = ssm_inputs(8, 2, 2, 70, 24, 16, 1, BF, 42, True)
