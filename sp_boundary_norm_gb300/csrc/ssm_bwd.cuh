@@ -35,6 +35,8 @@ namespace spb {
 // Sums over tokens are taken up by second ones every so many steps: 8192 terms added one
 // by one lost a quarter more of dA's digits than the rest of the arithmetic does.
 constexpr int kSumSteps = 32;
+// Kinds of runs.
+constexpr int kBackWhole = 0, kBackCut = 1, kBackSlow = 2;
 constexpr int kBackHelp = 128;         // threads that prepare and finish
 constexpr int kBackThreads = kSsmPart + kBackHelp;
 
@@ -64,7 +66,10 @@ struct SsmBack {
       4 * (kStage + kBC + H * (kDRow + kERow)) + 2 * (3 * kY + kWarps * kSum) + kWhole;
 };
 
-template <int DT, int N>
+// CUTS: packed sequences that begin from zeros: four ranks' 3984 x 1280 tokens of 52 of them
+// 721 us, where runs with a beginning were walked token by token 917.  (A kernel of its own:
+// beside that code the other's registers spill, 8 x 8192 x 1024 both directions 2122 -> 2345.)
+template <int DT, int N, bool CUTS>
 __global__ void __launch_bounds__(kBackThreads, 1)
 ssm_bwd_kernel(const SsmParams P) {
   using W = SsmBack<DT, N>;
@@ -419,6 +424,8 @@ ssm_bwd_kernel(const SsmParams P) {
       }
   };
   SsmMarks marks{0u, 0};
+  int64_t known = P.s;                 // packed: where the sequence of the next run's last
+                                       // token begins, or behind it
 
   meet<kBackThreads>();
   meet<kBackThreads>();                // (steps 0 and 1 are prepared)
@@ -444,18 +451,34 @@ ssm_bwd_kernel(const SsmParams P) {
         for (int p = 0; p < K; ++p) first[c][p] = active ? next[c][p] : F2(0);
       reorder(first);
       if (k + 2 < n_steps) run_state((k >> 1) + 1);
-      if (packed) marks = ssm_marks(P, run0, n_tok > 0 ? H + n_tok : tokens_of(k + 1));
+      if (packed) {
+        marks.starts = 0;
+        if (known >= run0) {
+          marks = ssm_marks(P, run0, n_tok > 0 ? H + n_tok : tokens_of(k + 1));
+          known = run0 > 0 ? __ldg(P.cu_seqlens + find_seq(P.cu_seqlens, P.n_seqs, run0 - 1)) : 0;
+        }
+      }
     }
     constexpr int kOrderStride = 2 * O * N;            // floats between tokens' B
 
-    // SLOW: runs with less than 16 tokens, or where a sequence begins: token by token,
-    // with the states and decays in local memory
-    auto go = [&](auto slow) {
-      constexpr bool SLOW = decltype(slow)::value;
+    // SLOW: runs with less than 16 tokens, or where a sequence with states of its own
+    // begins: token by token, with the states in local memory.  CUT: runs where one begins
+    // from zeros.
+    auto go = [&](auto mode) {
+      constexpr bool SLOW = decltype(mode)::value == kBackSlow, CUT = decltype(mode)::value == kBackCut;
       constexpr int kUnroll = SLOW ? 1 : H;
-      auto begins = [&](int t) { return SLOW && (marks.starts >> t & 1u); };
-      auto forget = [&](int t, F2 (&h)[2][K]) {        // the state before a sequence
-        load_both(P.h0[r], __shfl_sync(kAll, marks.seq, t) * state_step + state_at, h);
+      auto begins = [&](int t) { return (SLOW || CUT) && (marks.starts >> t & 1u); };
+      auto enter = [&](int t, F2 (&h)[2][K]) {         // the state before token t
+        if constexpr (SLOW) {
+          if (begins(t))
+            load_both(P.h0[r], __shfl_sync(kAll, marks.seq, t) * state_step + state_at, h);
+        } else if constexpr (CUT) {
+          const bool zero = begins(t);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int p = 0; p < K; ++p) h[c][p] = zero ? F2(0) : h[c][p];
+        }
       };
       // the states after a token of a step
       auto token = [&](const char* dt, const float* bt, F2 (&h)[2][K]) {
@@ -481,7 +504,7 @@ ssm_bwd_kernel(const SsmParams P) {
         const char* low_d = dd_of(k + 1);
 #pragma unroll kUnroll
         for (int i = 0; i < H; ++i) {
-          if (begins(i)) forget(i, begin);
+          enter(i, begin);
           token(low_d + i * W::kDRow, low + i * kOrderStride, begin);
         }
       }
@@ -497,7 +520,7 @@ ssm_bwd_kernel(const SsmParams P) {
         for (int i = 0; i < H; ++i) {
           inner[i] = make_float2(0.f, 0.f);
           if (!SLOW || i < n_tok) {
-            if (begins(half + i)) forget(half + i, now);
+            enter(half + i, now);
             token(dd + i * W::kDRow, shared + i * kOrderStride, now);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -545,7 +568,7 @@ ssm_bwd_kernel(const SsmParams P) {
 #pragma unroll
             for (int p = 0; p < K; ++p)
               before[c][p] = i > 0 ? h[i > 0 ? i - 1 : 0][c][p] : begin[c][p];
-          if (begins(t)) forget(t, before);
+          enter(t, before);
           float through[2], decay[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -566,12 +589,13 @@ ssm_bwd_kernel(const SsmParams P) {
             through[c] = y.x + y.y;
             decay[c] = w.x + w.y;
           }
-          if (begins(t)) {
+          if constexpr (CUT) enter(t, back);           // (and none comes from behind)
+          if (SLOW && begins(t)) {
             const int64_t seq = __shfl_sync(kAll, marks.seq, t);
             if (P.hT[r] != nullptr) store_both(P.hT[r], seq * state_step + state_at, back);
             const float* from = run0 + t > 0 ? P.dhT[r] : nullptr;
             const int64_t prev =
-                run0 + t > 0 ? find_seq(P.cu_seqlens, P.n_seqs, run0 + t - 1) : 0;
+                from != nullptr ? find_seq(P.cu_seqlens, P.n_seqs, run0 + t - 1) : 0;
             load_both(from, prev * state_step + state_at, back);
           }
           wait[i] = make_float4(through[0], through[1], decay[0], decay[1]);
@@ -634,8 +658,9 @@ ssm_bwd_kernel(const SsmParams P) {
     if (k % kSumSteps == 0) take_up();
     if (n_tok == 0) continue;
     if (marks.starts == 0u && n_tok == H)
-      go(std::false_type{});
-    else go(std::true_type{});
+      go(std::integral_constant<int, kBackWhole>{});
+    else if (CUTS && n_tok == H) go(std::integral_constant<int, CUTS ? kBackCut : kBackSlow>{});
+    else go(std::integral_constant<int, kBackSlow>{});
   }
   meet<kBackThreads>();                // (the others finish the last step)
   if (!packed && at.chunk == 0 && P.hT[r] != nullptr)
@@ -699,7 +724,10 @@ ssm_params_kernel(const float* from, int64_t channels, int n, int64_t parts, Ssm
 template <int DT, int N>
 static cudaError_t launch_back(const SsmParams& p, cudaStream_t st) {
   using W = SsmBack<DT, N>;
-  const void* fn = reinterpret_cast<const void*>(&ssm_bwd_kernel<DT, N>);
+  const bool cuts = p.cu_seqlens != nullptr && p.h0[0] == nullptr && p.dhT[0] == nullptr &&
+                    p.hT[0] == nullptr;
+  const void* fn = cuts ? reinterpret_cast<const void*>(&ssm_bwd_kernel<DT, N, true>)
+                        : reinterpret_cast<const void*>(&ssm_bwd_kernel<DT, N, false>);
   const cudaError_t e = ensure_smem_attr(fn, W::kSmem);
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<SsmParams*>(&p)};

@@ -23,6 +23,8 @@ static cudaError_t launch_states(const SsmParams& p, cudaStream_t st) {
   }
 }
 
+constexpr int64_t kMostChunks = 160;
+
 SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bool bwd) {
   const int block = n <= 16 ? 64 : n == 32 ? 32 : 16;
   const int64_t of_group = c / groups;
@@ -30,18 +32,18 @@ SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bo
   k.slabs = static_cast<int32_t>((of_group + block - 1) / block);
   const int64_t blocks = b * t * groups * k.slabs, sms = device_sm_count();
   // A block has an SM to itself, so a call takes as many waves of blocks as they need, each
-  // as long as a chunk.  Chunks cost a walk for what enters them: 66 clocks a token beside
-  // the forward's 118 and the backward's 400, and some 48 tokens' time to begin.  (Measured:
-  // 8 x 8192 x 1024, 128 blocks, forward 531 us whole, 675 cut; 32,769 x 512, 8 blocks that
-  // would walk 1.9 ms, cut in 19 170 us; 2 x 3 x 701 x 272 of 32 states, float32, both
-  // directions, cut until two blocks an SM 135 us, by this rule 127.)
-  const double walk = bwd ? 1.2 : 1.6;
+  // as long as a chunk and some 48 tokens' time to begin.  Chunks cost a walk for what
+  // enters them, 66 clocks a token beside the forward's 118 and the backward's 400, two
+  // launches, and their joining.  (Measured: 8 x 8192 x 1024, 128 blocks, forward 531 us whole, 675 cut; 32,769
+  // x 512, 8 blocks that would walk 1.9 ms, cut in 19 170 us; 256 x 64, forward and backward
+  // in two chunks 18 and 38 us, in 16 10 and 15.)
+  const double walk = bwd ? 1.2 : 1.6, start = bwd ? 15 : 50, join = bwd ? 0.7 : 2;
   double least = 0;
-  for (int64_t n = 1; n <= 64 && (n == 1 || n * 128 <= s); ++n) {
+  for (int64_t n = 1; n <= kMostChunks && (n == 1 || n * kSsmTile <= s); ++n) {
     const int64_t len = ((s + n - 1) / n + kSsmTile - 1) / kSsmTile * kSsmTile;
     const int64_t waves = (blocks * n + sms - 1) / sms;
-    const double cost = static_cast<double>(waves) * static_cast<double>(len + 48) *
-                        (n > 1 ? walk : 1.0);
+    const double whole = static_cast<double>(waves) * static_cast<double>(len + 48);
+    const double cost = n > 1 ? whole * walk + start + static_cast<double>(n) * join : whole;
     if (n > 1 && cost > 0.97 * least) continue;
     least = cost;
     k.chunk_len = len;

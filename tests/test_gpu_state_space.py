@@ -553,6 +553,51 @@ def test_ssm_what_is_not_finite_stays_in_its_sequence(c):
         assert not torch.isfinite(o["y"][0][0, 300:520]).any()
 
 
+BEGINNINGS = [1, 2, 5, 16, 0, 16, 3, 40, 1, 1, 130, 7, 8, 8, 17]
+
+
+@pytest.mark.parametrize("dtype,c,n,groups", [(BF, 72, 16, 1), (F32, 64, 8, 2), (FP, 48, 32, 1), (BF, 24, 64, 1),
+                                              (F32, 136, 16, 1), (FP, 640, 16, 1)])
+@pytest.mark.parametrize("gated", [True, False])
+def test_ssm_packed_from_zeros(dtype, c, n, groups, gated):
+    """Sequences that begin anywhere in a run of 16 tokens, several in one, without states."""
+    lens = BEGINNINGS
+    i = ssm_inputs(2, len(lens), 1, sum(lens), c, n, groups, dtype, 44, False, gated)
+    o = run_ssm(i, len(lens), offsets(lens), False)
+    check_ssm(i, o, lens, False)
+    assert same_runs(o, run_ssm(i, len(lens), offsets(lens), False))
+
+
+@pytest.mark.parametrize("which", ["dhT", "h0"])
+def test_ssm_packed_with_one_kind_of_state(which):
+    """Only the gradient of the last states, or only the first states."""
+    lens = BEGINNINGS
+    i = ssm_inputs(1, len(lens), 1, sum(lens), 40, 16, 1, F32, 45, True)
+    if which == "dhT":
+        i["h0"] = None
+    else:
+        i["dhT"] = None
+    check_ssm(i, run_ssm(i, len(lens), offsets(lens), True), lens, True)
+
+
+@pytest.mark.parametrize("c", [8, 4096])
+def test_ssm_what_is_not_finite_stays_without_states(c):
+    lens = [20, 0, 500, 33, 100]
+    cu = offsets(lens)
+    i = ssm_inputs(1, 5, 1, 653, c, 16, 1, BF, 46, False)
+    clean = run_ssm(i, 5, cu, False)
+    keep = torch.ones(653, dtype=torch.bool, device=DEV)
+    keep[20:520] = False
+    for value in (NAN, float("inf")):
+        i2 = {k: [x.clone() for x in v] if isinstance(v, list) else v for k, v in i.items()}
+        i2["u"][0][0, 300] = value
+        i2["dy"][0][0, 400] = value
+        o = run_ssm(i2, 5, cu, False)
+        for k in ("y", "du", "ddt", "dz", "dB", "dC"):
+            assert torch.equal(bits(o[k][0][0, keep]), bits(clean[k][0][0, keep])), k
+        assert not torch.isfinite(o["y"][0][0, 300:520]).any()
+
+
 def test_ssm_states_that_grow_behind_padding():
     """A > 0: a chunk's decay overflows while the state that enters it is still zero.
     A decay of d A = 1 is off by at most 2^-19 of itself, so 20 tokens' product by 2^-14,
@@ -653,6 +698,32 @@ def test_bad_prefix_sums_are_reported():
             call()
             assert own.item() == 6          # SP_ERR_DEVICE_CHECK
             assert (guard[..., :8] == 7).all() and (guard[..., 24:] == 7).all()
+
+
+@pytest.mark.parametrize("state", [True, False])
+def test_bad_prefix_sums_of_the_scan_and_its_gradients(state):
+    """The same for the backward, and where sequences have no states."""
+    own = torch.zeros(1, dtype=torch.int32, device=DEV)
+    i = ssm_inputs(1, 3, 1, 600, 16, 16, 1, BF, 47, state)
+    A, B, C = i["A"], i["B"], i["C"]
+    for cu in ([0, 50, 20, 600], [5, 10, 20, 600], [0, 10, 20, 60], [0, 10, 900, 600], [-7, 10, 20, 600]):
+        cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        guard = torch.full((1, 600, 4 * 32), 7.0, dtype=BF, device=DEV)
+        y, du, ddt, dz = ([guard[..., 32 * k + 8:32 * k + 24]] for k in range(4))
+        saved = nans(1, sp.sp_selective_scan_states_shape(1, 600, 16, 16), F32)
+        m = lambda: nans(1, (3, 16, 16), F32) if state else None
+        how = dict(D=i["D"], z=i["z"], dt_bias=i["dt_bias"], h0=i["h0"], cu_seqlens=cu, status=own)
+        sp.sp_selective_scan_fwd(i["u"], i["dt"], A, B, C, y=y, hT=m(), states=saved, **how,
+                                 workspace=scratch(sp.sp_selective_scan_fwd_workspace_bytes(1, 600, 16, 16, 1, 1)))
+        assert own.item() == 6
+        own.zero_()
+        sp.sp_selective_scan_bwd(i["u"], i["dt"], A, B, C, saved, i["dy"], dhT=i["dhT"], du=du, ddt=ddt, dz=dz,
+                                 dB=nans(1, (1, 600, 16), BF), dC=nans(1, (1, 600, 16), BF), dh0=m(), **how,
+                                 workspace=scratch(sp.sp_selective_scan_bwd_workspace_bytes(1, 600, 16, 16, 1, 1)))
+        assert own.item() == 6
+        own.zero_()
+        around = guard.view(1, 600, 4, 32)
+        assert (around[..., :8] == 7).all() and (around[..., 24:] == 7).all()
 
 
 # ----------------------------------------------------------------- together --
