@@ -34,16 +34,16 @@ SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bo
   // A block has an SM to itself, so a call takes as many waves of blocks as they need, each
   // as long as a chunk and some 48 tokens' time to begin.  Chunks cost a walk for what
   // enters them, 66 clocks a token beside the forward's 118 and the backward's 400, two
-  // launches, and their joining.  (Measured: 8 x 8192 x 1024, 128 blocks, forward 531 us whole, 675 cut; 32,769
-  // x 512, 8 blocks that would walk 1.9 ms, cut in 19 170 us; 256 x 64, forward and backward
-  // in two chunks 18 and 38 us, in 16 10 and 15.)
-  const double walk = bwd ? 1.2 : 1.6, start = bwd ? 15 : 50, join = bwd ? 0.7 : 2;
+  // launches, and their joining.  (Measured: 8 x 8192 x 1024, 128 blocks, forward 531 us
+  // whole, 675 cut; 32,769 x 512, 8 blocks that would walk 1.9 ms, cut in 19 170 us; 256 x
+  // 64, forward and backward in two chunks 18 and 38 us, in 16 10 and 15.)
+  const double walk = bwd ? 1.2 : 1.6, start = bwd ? 15 : 50, join = bwd ? 6 : 16;
   double least = 0;
   for (int64_t n = 1; n <= kMostChunks && (n == 1 || n * kSsmTile <= s); ++n) {
     const int64_t len = ((s + n - 1) / n + kSsmTile - 1) / kSsmTile * kSsmTile;
-    const int64_t waves = (blocks * n + sms - 1) / sms;
-    const double whole = static_cast<double>(waves) * static_cast<double>(len + 48);
-    const double cost = n > 1 ? whole * walk + start + static_cast<double>(n) * join : whole;
+    const int64_t waves = (blocks * n + sms - 1) / sms, joins = (n + kJoinAhead - 1) / kJoinAhead;
+    double cost = static_cast<double>(waves) * static_cast<double>(len + 48);
+    if (n > 1) cost = cost * walk + start + static_cast<double>(joins) * join;
     if (n > 1 && cost > 0.97 * least) continue;
     least = cost;
     k.chunk_len = len;

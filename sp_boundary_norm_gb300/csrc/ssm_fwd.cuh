@@ -409,6 +409,9 @@ ssm_walk_kernel(const SsmParams P) {
   }
 }
 
+// Chunks whose values are asked for before the first is used (32: no faster).
+constexpr int kJoinAhead = 8;
+
 // The state that enters each chunk of a batch row, in the place of the chunk's own
 // last one (BACK: the gradient that enters from behind, in the place of what it hands
 // on): a thread takes one state of a channel through the chunks.
@@ -433,8 +436,7 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const SsmParams P) {
   }
   float* carry = P.carry + batch * P.chunks * width + i;
   const float* steps = P.steps + batch * P.chunks * P.t * P.c + chan;
-  // eight chunks' values are asked for before the first is used
-  constexpr int kAhead = 8;
+  constexpr int kAhead = kJoinAhead;
   for (int n0 = 0; n0 < P.chunks; n0 += kAhead) {
     float handed[kAhead], decay[kAhead];
     bool cut[kAhead];                  // a sequence begins in the chunk
