@@ -659,6 +659,9 @@ sp_status_t sp_causal_conv_bwd(const void* const* x, int64_t x_ld, const void* w
  * u, dt, z, y [t] (b, s, c)         c / groups a multiple of 8; z: NULL array for no gate
  * B, C        [t] (b, s, groups * n)   ranks may share a buffer
  * A           (t * c, n) float32, finite: rank r's at r * c; decaying for A < 0
+ *             (States and decays are float32 whatever the type.  A decay is off by 2^-22.8
+ *             at most, and for A < 0 not to one side: what a state keeps over n tokens is
+ *             off by about sqrt(n) 2^-24.  Decays below 2^-126 are 0.)
  * D, dt_bias  (t * c) float32 or NULL (zero)
  * h0, hT      [t] (m, c, n) float32 or NULL arrays: the states before and after each
  *             sequence (0 without h0), m = n_seqs or b; hT[r] == h0[r] is allowed

@@ -467,6 +467,7 @@ ssm_bwd_kernel(const SsmParams P) {
     auto go = [&](auto mode) {
       constexpr bool SLOW = decltype(mode)::value == kBackSlow, CUT = decltype(mode)::value == kBackCut;
       constexpr int kUnroll = SLOW ? 1 : H;
+      constexpr bool kSettled = !SLOW && !CUT;
       auto begins = [&](int t) { return (SLOW || CUT) && (marks.starts >> t & 1u); };
       auto enter = [&](int t, F2 (&h)[2][K]) {         // the state before token t
         if constexpr (SLOW) {
@@ -551,6 +552,12 @@ ssm_bwd_kernel(const SsmParams P) {
       constexpr int kLevels = O == 4 ? 2 : 1;          // of lanes, that halve the states
       constexpr int kLeft = S >> kLevels;              // states of dB and of dC then
       constexpr int kBoth = W::kAbreast > O ? 1 : 2;   // dB and dC, or one of them
+      F2 all[2][K];                                    // the step's decays together
+      float steps[2] = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int p = 0; p < K; ++p) all[c][p] = f2(1.f, 1.f);
       float4 wait[H];
       float wait_bc[H][kBoth * kLeft];
 #pragma unroll kUnroll
@@ -574,13 +581,16 @@ ssm_bwd_kernel(const SsmParams P) {
           for (int c = 0; c < 2; ++c) {
             const F2 e2 = f2(e[c], e[c]), in2 = f2(in[c], in[c]), d2 = f2(d[c], d[c]);
             F2 to_u = 0, to_d = 0;
+            if constexpr (kSettled) steps[c] += d[c];
 #pragma unroll
             for (int p = 0; p < K; ++p) {
               const F2 gr = fma2(q[p], e2, back[c][p]);
               dc[p] = c == 0 ? mul2(h[i][c][p], e2) : fma2(h[i][c][p], e2, dc[p]);
               db[p] = c == 0 ? mul2(gr, in2) : fma2(gr, in2, db[p]);
               to_u = p == 0 ? mul2(gr, b[p]) : fma2(gr, b[p], to_u);
-              back[c][p] = mul2(pow2(mul2(d2, a2[c][p])), gr);
+              const F2 x = mul2(d2, a2[c][p]), a = SLOW ? decay2(x) : pow2(x);
+              if constexpr (kSettled) all[c][p] = mul2(all[c][p], a);
+              back[c][p] = mul2(a, gr);
               const F2 g = mul2(back[c][p], before[c][p]);
               to_d = p == 0 ? mul2(g, a2[c][p]) : fma2(g, a2[c][p], to_d);
               dA[c][p] = fma2(g, d2, dA[c][p]);
@@ -637,6 +647,13 @@ ssm_bwd_kernel(const SsmParams P) {
               for (int j = 0; j < kLeft; ++j) wait_bc[i][w * kLeft + j] = v[w][2 * j];
           }
         }
+      }
+      if constexpr (kSettled) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int p = 0; p < K; ++p)
+            back[c][p] = mul2(back[c][p], settle2(mul2(f2(steps[c], steps[c]), a2[c][p]), all[c][p]));
       }
 #pragma unroll kUnroll
       for (int i = 0; i < H; ++i) {

@@ -21,6 +21,8 @@
 // A call with few blocks is cut into chunks in time: each chunk's last state
 // from a zero one and the sum of its steps (a walk of 66 clocks a token), the states that
 // enter each chunk (ssm_join_kernel), and then all chunks at once.
+#include <type_traits>
+
 #include "ssm.cuh"
 
 namespace spb {
@@ -36,6 +38,12 @@ constexpr int kSsmPrep = 256;          // that prepare
 __host__ __device__ constexpr int walk_threads(int mode) {
   return kSsmPart + kSsmPrep + (mode == kSsmOut ? kSsmPart : 0);
 }
+// Registers of a thread for outputs: 16 tokens' sums and decays wait in those that hold
+// states (at 128 for all of them they spill, and 522 us become 666).  The block starts with
+// 128 each, which is what both shares add up to.
+constexpr int kSsmStateRegisters = 200, kSsmHelpRegisters = 104, kSsmRegisters = 128;
+static_assert(kSsmPart * kSsmStateRegisters + (kSsmPrep + kSsmPart) * kSsmHelpRegisters ==
+                  walk_threads(kSsmOut) * kSsmRegisters, "what a block has");
 
 // Rows in shared memory are padded so that the lanes of an access use different banks.
 template <int DT, int N>
@@ -88,6 +96,8 @@ ssm_walk_kernel(const SsmParams P) {
 
   if (warp >= kSsmPart / 32) {
     // ------------------------------------------------------------ preparing --
+    if constexpr (MODE == kSsmOut)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSsmHelpRegisters));
     const bool finisher = warp >= (kSsmPart + kSsmPrep) / 32;
     const int ht = tid - kSsmPart - (finisher ? kSsmPrep : 0);
     const bool gated = MODE != kSsmEnds && P.gated;
@@ -212,7 +222,7 @@ ssm_walk_kernel(const SsmParams P) {
           if (P.softplus) d[i] = softplus2<DT>(d[i], nullptr);
           if constexpr (!kBack) v[i] = mul2(d[i], v[i]);
           const float2 a = split(d[i]), b = split(v[i]);
-          *reinterpret_cast<float4*>(dst + 16 * i) = make_float4(a.x, b.x, a.y, b.y);
+          *reinterpret_cast<float4*>(dst + 16 * i) = make_float4(a.x, a.y, b.x, b.y);
         }
       }
       const char* sh = st + 3 * T * W::kRow;
@@ -241,6 +251,8 @@ ssm_walk_kernel(const SsmParams P) {
   }
 
   // ---------------------------------------------------------------- states --
+  if constexpr (MODE == kSsmOut)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSsmStateRegisters));
   const bool active = warp * CW + lane / G * 2 < at.live;      // of a lane: its two channels
   const int n0 = (lane % G) * S, ch = active ? warp * CW + lane / G * 2 : 0;
   // this lane's states: of [t * c][n], and of a rank's [sequences][c][n]; of its second
@@ -288,7 +300,7 @@ ssm_walk_kernel(const SsmParams P) {
       store_both(P.hT[r], j * state_step + state_at, v);
     }
   }
-  float sum[2] = {0.f, 0.f};           // of the chunk's steps
+  F2 sum = 0;                          // of the chunk's steps
   const int dd_at = ch / V * W::kDPart + ch % V * 8;
   const int64_t runs = (P.s + kSsmRun - 1) / kSsmRun;
 
@@ -300,19 +312,24 @@ ssm_walk_kernel(const SsmParams P) {
     char* ybuf = ys + (k & 1) * W::kY + (lane % G) * W::kYRow + (warp * CW + lane / G * 2) * 4;
     const int64_t t0 = tile_of(k), tok0 = at.tok0 + t0;
     const int n_tok = tokens_of(t0);
-    float steps[2] = {0.f, 0.f};
-    // one token: the states after it, and this lane's parts of its channels' sums with C
-    auto token = [&](int t) -> float2 {
+    F2 steps = 0;
+    F2 all[2][K];                      // the product of the step's decays (settle2)
+    // one token: the states after it, and this lane's parts of its channels' sums with C;
+    // ALONE: with a decay of its own
+    auto token = [&](int t, auto alone) -> float2 {
+      constexpr bool ALONE = decltype(alone)::value;
       const float4 v = *reinterpret_cast<const float4*>(dd + t * W::kDRow);
-      const float d[2] = {v.x, v.z}, in[2] = {v.y, v.w};
+      const float d[2] = {v.x, v.y}, in[2] = {v.z, v.w};
+      steps = add2(steps, f2(v.x, v.y));
       F2 b[K];
       load_states(shared + t * 2 * N, b);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if constexpr (MODE != kSsmOut) steps[c] += d[c];
 #pragma unroll
         for (int p = 0; p < K; ++p) {
-          const F2 a = pow2(mul2(f2(d[c], d[c]), f2(a2[c][2 * p], a2[c][2 * p + 1])));
+          const F2 x = mul2(f2(d[c], d[c]), f2(a2[c][2 * p], a2[c][2 * p + 1]));
+          const F2 a = ALONE ? decay2(x) : pow2(x);
+          if constexpr (!ALONE) all[c][p] = mul2(all[c][p], a);
           if constexpr (kBack) {
             h[c][p] = mul2(a, fma2(f2(in[c], in[c]), b[p], h[c][p]));
           } else {
@@ -351,11 +368,22 @@ ssm_walk_kernel(const SsmParams P) {
       // exponentials go ahead of its states
       float2 part[T];
 #pragma unroll
-      for (int t = 0; t < T; ++t) part[t] = token(kBack ? T - 1 - t : t);
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int p = 0; p < K; ++p) all[c][p] = f2(1.f, 1.f);
+#pragma unroll
+      for (int t = 0; t < T; ++t) part[t] = token(kBack ? T - 1 - t : t, std::false_type{});
+      const float2 step = split(steps);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int p = 0; p < K; ++p)
+          h[c][p] = mul2(h[c][p], settle2(mul2(c == 0 ? f2(step.x, step.x) : f2(step.y, step.y),
+                                               f2(a2[c][2 * p], a2[c][2 * p + 1])), all[c][p]));
 #pragma unroll
       for (int t = 0; t < T; ++t) put(t, part[t]);
     } else if (CUTS && n_tok == T) {
-      // the same, and sequences begin
+      // the same, and sequences begin (16 tokens' lost digits at most, once a sequence)
       float2 part[T];
       auto cut = [&](int t) {
         const bool zero = (marks.starts >> t) & 1u;
@@ -368,7 +396,7 @@ ssm_walk_kernel(const SsmParams P) {
       for (int i = 0; i < T; ++i) {
         const int t = kBack ? T - 1 - i : i;
         if constexpr (!kBack) cut(t);
-        part[i] = token(t);
+        part[i] = token(t, std::false_type{});
         if constexpr (kBack) cut(t);
       }
 #pragma unroll
@@ -385,15 +413,14 @@ ssm_walk_kernel(const SsmParams P) {
           cur = seq;
           load_both(P.h0[r], cur * state_step + state_at, h);
         }
-        put(t, token(t));
+        put(t, token(t, std::true_type{}));
         if (kBack && start && tok0 + t > 0) {
           cur = find_seq(P.cu_seqlens, P.n_seqs, tok0 + t - 1);
           load_both(P.dhT[r], cur * state_step + state_at, h);
         }
       }
     }
-    sum[0] += steps[0];
-    sum[1] += steps[1];
+    sum = add2(sum, steps);
   }
   if constexpr (MODE == kSsmOut) {
     meet<walk_threads(MODE)>();              // (the preparers finish the last step)
@@ -404,8 +431,8 @@ ssm_walk_kernel(const SsmParams P) {
   } else {
     store_both(P.carry, carry_at, h);
     if (active && lane % G == 0)
-      *reinterpret_cast<float2*>(P.steps + (at.batch * P.chunks + at.chunk) * P.t * P.c + rc +
-                                 at.ch0 + ch) = make_float2(sum[0], sum[1]);
+      *reinterpret_cast<F2*>(P.steps + (at.batch * P.chunks + at.chunk) * P.t * P.c + rc +
+                                 at.ch0 + ch) = sum;
   }
 }
 
@@ -465,6 +492,13 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const SsmParams P) {
   }
 }
 
+// Registers that a thread of the kernel starts with (0: unknown).
+template <typename F>
+static int registers_of(F* fn) {
+  cudaFuncAttributes a{};
+  return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(fn)) == cudaSuccess ? a.numRegs : 0;
+}
+
 template <int DT, int N, int MODE>
 static cudaError_t launch_walk(const SsmParams& p, cudaStream_t st) {
   using W = SsmWalk<DT, N>;
@@ -475,6 +509,12 @@ static cudaError_t launch_walk(const SsmParams& p, cudaStream_t st) {
                         : reinterpret_cast<const void*>(&ssm_walk_kernel<DT, N, MODE, false>);
   const cudaError_t e = ensure_smem_attr(fn, W::kSmem);
   if (e != cudaSuccess) return e;
+  if constexpr (MODE == kSsmOut) {
+    // (with fewer to start with, the threads that hold states would wait for ever)
+    static const int registers[2] = {registers_of(&ssm_walk_kernel<DT, N, MODE, false>),
+                                     registers_of(&ssm_walk_kernel<DT, N, MODE, true>)};
+    if (registers[cuts] < kSsmRegisters) return cudaErrorLaunchOutOfResources;
+  }
   SsmParams q = p;
   q.slabs = (p.c / p.groups + W::kBlockCh - 1) / W::kBlockCh;
   void* args[] = {&q};

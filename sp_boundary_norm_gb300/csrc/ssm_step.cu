@@ -135,7 +135,7 @@ ssm_step_kernel(const SsmParams P) {
         load_states(bc + N, c);
 #pragma unroll
         for (int p = 0; p < K; ++p)
-          h[i][p] = fma2(pow2(mul2(step, a2[p])), h[i][p], mul2(in, b[p]));
+          h[i][p] = fma2(decay2(mul2(step, a2[p])), h[i][p], mul2(in, b[p]));
         F2 acc = mul2(h[i][0], c[0]);
         if constexpr (K == 2) acc = fma2(h[i][1], c[1], acc);
         const float2 v = split(acc);

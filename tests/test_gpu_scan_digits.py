@@ -1,0 +1,123 @@
+"""What a state of the selective scan keeps of its digits over thousands of tokens.
+
+Decays alone (u = 0, dy = 0): a last state is its first one times exp(sum of d A), and
+the gradient of the first state that of the last times the same.  In units of U = 2^-24,
+as roundings whose errors follow no pattern (rms below U / sqrt(3) each): a token multiplies
+the state and the product of a step's decays, and each decay has an error of its own, below
+2^-22.8 or 2.3 U, which is 0.6 U in the rms.  Four such a token, so sqrt(4 n / 3) U over n
+tokens, 3.2e-6 for 2048.  To one side only the power of a step's summed exponents is off,
+by at most 2^-25 on the mean where these states have theirs (between -0.5 and 0), once in
+eight tokens: 2048 / 8 2^-25 = 7.6e-6 at most.  Their sum in norm is below 2^-16.5; tokens
+that take the hardware's power alone are off by 2e-8 each to one side, 4e-5 in all.
+"""
+import numpy as np
+import pytest
+import torch
+
+from sp_boundary_norm_gb300 import binding as sp
+from test_gpu_state_space import BF, DEV, F32, FP, f64, nans, offsets, scratch
+
+pytestmark = pytest.mark.gpu
+
+WITHIN = 2.0 ** -16.5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(lib):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    yield
+    sp.check_device_status(DEV)
+
+
+def decays(b, s, c, n, dtype, seed):
+    """Steps between 2^-8 and 3 2^-8, rates between -1.5 and -0.3: exponents (of two)
+    between -0.026 and -0.0017 a token."""
+    gen = torch.Generator().manual_seed(seed)
+    uniform = lambda shape, lo, hi: torch.rand(shape, generator=gen) * (hi - lo) + lo
+    return dict(dt=uniform((b, s, c), 1.0, 3.0).mul_(2.0 ** -8).to(dtype).to(DEV),
+                A=-uniform((c, n), 0.3, 1.5).to(DEV), h=uniform((b, c, n), 1.0, 2.0).to(DEV),
+                zero=torch.zeros((b, s, c), dtype=dtype, device=DEV),
+                B=uniform((b, s, n), -1.0, 1.0).to(dtype).to(DEV),
+                C=uniform((b, s, n), -1.0, 1.0).to(dtype).to(DEV))
+
+
+def off(got, i, tokens):
+    """Relative errors in norm of a state that went through the call's tokens."""
+    total = i["dt"][:, tokens].double().sum(1)
+    want = i["h"].double() * torch.exp(total[..., None] * i["A"].double())
+    return float(((got.double() - want) / want).square().mean().sqrt())
+
+
+@pytest.mark.parametrize("c,n", [(9728, 16), (2432, 64), (64, 16), (24, 8), (40, 32)])
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+def test_slow_states_keep_their_digits(dtype, c, n):
+    """In one walk (many channels), in chunks (few)."""
+    s = 2048
+    i = decays(1, s, c, n, dtype, 51)
+    y, hT = nans(1, (1, s, c), dtype), nans(1, (1, c, n), F32)
+    states = nans(1, sp.sp_selective_scan_states_shape(1, s, c, n), F32)
+    args = ([i["zero"]], [i["dt"]], i["A"], [i["B"]], [i["C"]])
+    how = dict(softplus=False, h0=[i["h"]])
+    sp.sp_selective_scan_fwd(*args, y=y, hT=hT, states=states, **how,
+                             workspace=scratch(sp.sp_selective_scan_fwd_workspace_bytes(1, s, c, n, 1, 1)))
+    assert off(hT[0], i, slice(None)) <= WITHIN
+    out = {k: nans(1, (1, s, c), dtype) for k in ("du", "ddt")}
+    out.update({k: nans(1, (1, s, n), dtype) for k in ("dB", "dC")})
+    dh0 = nans(1, (1, c, n), F32)
+    sp.sp_selective_scan_bwd(*args, states, [i["zero"]], dhT=[i["h"]], dh0=dh0, **out, **how,
+                             workspace=scratch(sp.sp_selective_scan_bwd_workspace_bytes(1, s, c, n, 1, 1)))
+    assert off(dh0[0], i, slice(None)) <= WITHIN
+
+
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype,tokens", [(F32, 1), (BF, 2), (F32, 8), (FP, 16), (F32, 23)])
+def test_a_state_updated_in_place_keeps_its_digits(dtype, tokens, n):
+    """2048 tokens in calls of a few (decoding), and of more than a whole step."""
+    s, c, b = 2048 // tokens * tokens, 40, 3
+    i = decays(b, s, c, n, dtype, 52)
+    state = [i["h"].clone()]
+    for lo in range(0, s, tokens):
+        cut = lambda k: [i[k][:, lo:lo + tokens].contiguous()]
+        sp.sp_selective_scan_fwd(cut("zero"), cut("dt"), i["A"], cut("B"), cut("C"), softplus=False, h0=state,
+                                 y=nans(1, (b, tokens, c), dtype), hT=state)
+    assert off(state[0], i, slice(None)) <= WITHIN
+
+
+@pytest.mark.parametrize("tokens", [1, 15])
+def test_packed_states_updated_in_place_keep_their_digits(tokens):
+    """The same, the sequences of a call given by their prefix sums."""
+    s, c, n, b = 2048 // tokens * tokens, 40, 16, 3
+    i = decays(b, s, c, n, F32, 53)
+    state, cu = [i["h"].clone()], offsets([tokens] * b)
+    for lo in range(0, s, tokens):
+        cut = lambda k: [i[k][:, lo:lo + tokens].reshape(1, b * tokens, -1)]
+        sp.sp_selective_scan_fwd(cut("zero"), cut("dt"), i["A"], cut("B"), cut("C"), softplus=False, h0=state,
+                                 cu_seqlens=cu, y=nans(1, (1, b * tokens, c), F32), hT=state,
+                                 workspace=scratch(sp.sp_selective_scan_fwd_workspace_bytes(1, b * tokens, c, n, 1, 1)))
+    assert off(state[0], i, slice(None)) <= WITHIN
+
+
+def test_products_that_leave_the_range_on_the_way():
+    """Steps of both signs (softplus off): decays of 2^100 and back.  What a step's decays
+    have lost is not made up for where their product overflowed or vanished: the states
+    stay what their tokens make of them, each off by its decays' 2^-22.8 and by 2^-24 of
+    exponents up to 150: below 16 150 2^-24 = 2^-12.7."""
+    c, n, s = 8, 16, 64
+    for up in ([100.0, 100.0, -120.0, -80.0], [-90.0, -60.0, 75.0, 75.0], [-20.0, 30.0, -20.0, 10.0]):
+        x = torch.tensor(up + [0.0] * 12).repeat(4)
+        start = 2.0 ** -90 if up[0] > 0 else 1.0
+        dt = (x / 1.4426950408889634).view(1, s, 1).expand(1, s, c).contiguous().to(DEV)
+        A, h0 = torch.ones(c, n, device=DEV), [torch.full((1, c, n), start, device=DEV)]
+        zero, one = torch.zeros(1, s, c, device=DEV), torch.ones(1, s, n, device=DEV)
+        hT, y = nans(1, (1, c, n), F32), nans(1, (1, s, c), F32)
+        states = nans(1, sp.sp_selective_scan_states_shape(1, s, c, n), F32)
+        sp.sp_selective_scan_fwd([zero], [dt], A, [one], [one], softplus=False, h0=h0, y=y, hT=hT, states=states,
+                                 workspace=scratch(sp.sp_selective_scan_fwd_workspace_bytes(1, s, c, n, 1, 1)))
+        steps = f64(dt[0, :, 0])
+        h, want = start, []
+        for d in steps:
+            h = h * np.exp(d)
+            h = h if abs(h) >= 2.0 ** -126 else 0.0          # (a decay below that is flushed)
+            want.append(16 * h)
+        assert (np.abs(f64(y[0])[0] - np.array(want)[:, None]) <= 2.0 ** -12 * np.array(want)[:, None]).all(), up
