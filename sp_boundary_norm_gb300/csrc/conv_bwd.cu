@@ -4,9 +4,9 @@
 // A thread walks runs of tokens of its channels: q is computed again from the
 // inputs, and each token's gradient is added to those of the W - 1 tokens before it,
 // which wait in registers until they are whole.  A run goes on for W - 1 tokens beyond
-// its end for the gradients that come from there.  The parameters' sums stay in registers
-// over all of a thread's runs, are added up in the block and, over the blocks, by
-// sum_parts: always in the same order.
+// its end for the gradients that come from there.  The parameters' sums of 128 tokens stay
+// in registers; a thread's, a block's and (by sum_parts) all blocks' are added up from them,
+// always in the same order.
 //
 // Bound by reading x and dy and writing dx: on a GB300, bf16, 8 ranks' 16,384 x 1024 with
 // four taps and silu, 805 MB in 151 us, 5.3 TB/s; per channel and token two reciprocals,
@@ -18,6 +18,12 @@
 namespace spb {
 
 constexpr int kConvBlocksB = 4;        // of an SM, by their registers
+// Tokens that are added one by one before their sums join the others, in local memory.  (One
+// sum for all of a thread's tokens, as many as a call has for its channels, loses digits with
+// their number: 4096 of them 4e-7 in norm, so 1e-7.  8 ranks' 16,384 x 1024, both
+// directions: 235 us and dweight off by 3.9e-7, every 128 tokens 240 and 2.2e-7, every 64 241
+// and 1.8e-7; with the other sums in registers 248.)
+constexpr int kSumTokens = 128;
 
 // Where a run's gradients go; this lane's channels.
 template <int V>
@@ -77,12 +83,27 @@ conv_bwd_kernel(const ConvParams P) {
   char* dx0 = P.xT[r] != nullptr ? P.xT[r] + off : nullptr;
   Taps<DT, V, W> taps;
   taps.load(P, ch);
-  F2 dw[W][K], db[K];
+  // the parameters' gradients: the last tokens', and in local memory those before them
+  F2 dw[W][K], db[K], whole[W + 1][K];
+  auto take_up = [&] {
+    asm volatile("" ::"l"(&whole) : "memory");
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        whole[j][k] = add2(whole[j][k], dw[j][k]);
+        dw[j][k] = 0;
+      }
+      whole[W][k] = add2(whole[W][k], db[k]);
+      db[k] = 0;
+    }
+    asm volatile("" ::"l"(&whole) : "memory");
+  };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    db[k] = 0;
+    db[k] = whole[W][k] = 0;
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][k] = 0;
+    for (int j = 0; j < W; ++j) dw[j][k] = whole[j][k] = 0;
   }
   const int64_t all = P.runs * P.b;
   for (int64_t at = static_cast<int64_t>(part) * slots + slot; on && at < all;
@@ -197,8 +218,10 @@ conv_bwd_kernel(const ConvParams P) {
         }
       }
       ring.next();
+      if ((i + U) % kSumTokens == 0) take_up();
     }
     if (open && i0 + all_n == P.s) flush(all_n);
+    take_up();
   }
   if (P.ws == nullptr) return;
 
@@ -210,11 +233,11 @@ conv_bwd_kernel(const ConvParams P) {
   for (int k = 0; k < K; ++k) {
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-      const float2 v = split(dw[j][k]);
+      const float2 v = split(whole[j][k]);
       sums[threadIdx.x][2 * k * (W + 1) + j] = v.x;
       sums[threadIdx.x][(2 * k + 1) * (W + 1) + j] = v.y;
     }
-    const float2 v = split(db[k]);
+    const float2 v = split(whole[W][k]);
     sums[threadIdx.x][2 * k * (W + 1) + W] = v.x;
     sums[threadIdx.x][(2 * k + 1) * (W + 1) + W] = v.y;
   }
