@@ -15,7 +15,8 @@ import pytest
 import torch
 
 from sp_boundary_norm_gb300 import binding as sp
-from test_gpu_state_space import BF, DEV, F32, FP, f64, nans, offsets, scratch
+from _scan_norms import off_in_norm
+from test_gpu_state_space import BF, DEV, F32, FP, f64, nans, offsets, run_ssm, scratch, ssm_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +122,31 @@ def test_products_that_leave_the_range_on_the_way():
             h = h if abs(h) >= 2.0 ** -126 else 0.0          # (a decay below that is flushed)
             want.append(16 * h)
         assert (np.abs(f64(y[0])[0] - np.array(want)[:, None]) <= 2.0 ** -12 * np.array(want)[:, None]).all(), up
+
+
+@pytest.mark.parametrize("lens,state", [(None, True), ([1, 700, 0, 15, 17, 1276], True),
+                                        ([1, 700, 0, 15, 17, 1276], False), ([2009], True)],
+                         ids=["dense", "packed", "zeros", "one"])
+@pytest.mark.parametrize("dtype,n,groups,gated", [(F32, 8, 3, True), (F32, 16, 1, False), (F32, 32, 1, True),
+                                                  (F32, 64, 3, True), (BF, 16, 3, True), (FP, 32, 1, True)])
+def test_every_rank_in_norm(lens, state, dtype, n, groups, gated):
+    """Long sequences in chunks: every output of every rank, in norm."""
+    t, c, m = 3, 24, 1 if lens is None else len(lens)
+    assert sp.sp_selective_scan_fwd_workspace_bytes(1, 2009, c, n, groups, t) > 0
+    i = ssm_inputs(t, m, 1, 2009, c, n, groups, dtype, 54 + n, state, gated)
+    o = run_ssm(i, m, None if lens is None else offsets(lens), state)
+    for r in range(t):
+        assert off_in_norm(o, i, r, lens) == [], r
+
+
+@pytest.mark.parametrize("dtype,t,c,n,groups", [(F32, 2, 136, 16, 1), (BF, 3, 72, 8, 3), (F32, 5, 16, 32, 1),
+                                                (FP, 2, 40, 64, 1)])
+@pytest.mark.parametrize("lens", [[40], [0, 0, 70, 0, 3, 1, 1, 1, 0], [16] * 9 + [0] * 4 + [17],
+                                  [5, 60, 0, 2, 100, 31, 33]], ids=range(4))
+@pytest.mark.parametrize("state", [True, False])
+def test_every_rank_packed_in_norm(lens, dtype, t, c, n, groups, state):
+    """Packed sequences with and without states of their own: every rank."""
+    i = ssm_inputs(t, len(lens), 1, sum(lens), c, n, groups, dtype, 55, state)
+    o = run_ssm(i, len(lens), offsets(lens), state)
+    for r in range(t):
+        assert off_in_norm(o, i, r, lens) == [], r
