@@ -613,7 +613,8 @@ sp_status_t sp_group_norm_bwd(const void* const* dy, int64_t dy_ld, const void* 
  * x0, xT   [t] (n, width - 1, c) of x's type, or NULL arrays: the last inputs before
  *          each sequence and at its end, oldest first, n = n_seqs or b; xT[r] == x0[r]
  *          is allowed (a sequence without tokens: xT = x0)
- * s == 1 without cu_seqlens is a decoding step of b sequences.
+ * s == 1 without cu_seqlens is a decoding step of b sequences.  n_seqs: at most 2^30, as
+ * in the scan.
  */
 sp_status_t sp_causal_conv_fwd(const void* const* x, int64_t x_ld, const void* weight,
                                const void* bias, const void* const* x0, int64_t b, int64_t s,

@@ -250,7 +250,8 @@ __device__ __forceinline__ F2 held_above(F2 v, float least) {
   return f2(x.x, x.y);
 }
 
-// The sequence of token `tok` (see seq_of_token), found by one thread; in [0, n).
+// The sequence of token `tok` (see seq_of_token), found by one thread; in [0, n), n at most
+// 2^30.
 __device__ __forceinline__ int find_seq(const int32_t* cu, int n, int64_t tok) {
   int lo = 0, hi = n;                  // cu[lo] <= tok < cu[hi], where cu is what it should be
   while (hi - lo > 1) {

@@ -21,6 +21,14 @@ sp_status_t check_channels(int64_t b, int64_t c) {
   return SP_OK;
 }
 
+// Tokens find their sequence by halving, in 32 bits: the sum of two bounds has to fit.
+sp_status_t check_count(const int32_t* cu_seqlens, int32_t n_seqs) {
+  constexpr int32_t kMostSeqs = 1 << 30;
+  if (cu_seqlens != nullptr && n_seqs > kMostSeqs)
+    return fail(SP_ERR_UNSUPPORTED, "n_seqs = %d above %d", n_seqs, kMostSeqs);
+  return SP_OK;
+}
+
 // Without a token every state (or gradient of one) passes through.
 sp_status_t pass_states(const void* const* src, void* const* dst, size_t bytes, int t,
                         void* stream) {
@@ -66,6 +74,7 @@ sp_status_t check_conv(int64_t b, int64_t s, int64_t c, int32_t width, int32_t t
   sp_status_t st;
   if ((st = check_common(t, dtype, dev_status)) != SP_OK) return st;
   if ((st = check_seqs(b, s, cu_seqlens, n_seqs)) != SP_OK) return st;
+  if ((st = check_count(cu_seqlens, n_seqs)) != SP_OK) return st;
   if ((st = check_channels(b, c)) != SP_OK) return st;
   if (width < 2 || width > 4)
     return fail(SP_ERR_UNSUPPORTED, "width = %d outside [2, 4]", width);
@@ -115,6 +124,7 @@ sp_status_t check_scan(const Scan& k, const int32_t* dev_status) {
   sp_status_t st;
   if ((st = check_common(k.t, k.dtype, dev_status)) != SP_OK) return st;
   if ((st = check_seqs(k.b, k.s, k.cu_seqlens, k.n_seqs)) != SP_OK) return st;
+  if ((st = check_count(k.cu_seqlens, k.n_seqs)) != SP_OK) return st;
   if ((st = check_channels(k.b, k.c)) != SP_OK) return st;
   if (k.n != 8 && k.n != 16 && k.n != 32 && k.n != 64)
     return fail(SP_ERR_UNSUPPORTED, "n = %d states: 8, 16, 32 or 64", k.n);
