@@ -4,11 +4,10 @@
 //   y = (sum_n C[n] h[n] + D u) silu(z)
 // B and C are shared by a group's channels.
 //
-// A lane holds four states (two for N = 8) of two channels side by side, so B and C
-// of a token are read from shared memory once for both: a word there costs a warp as
-// much as four of its arithmetic instructions.  The sums over a channel's states cross
-// the N / 4 lanes of a channel, for as many tokens at once as a channel has lanes, so
-// that each lane is left with one token's.
+// In the walks a lane holds four states (two for N = 8) of two channels side by side, so B
+// and C of a token are read from shared memory once for both: a word there costs a warp as
+// much as four of its arithmetic instructions.  A channel's lanes put their parts of its
+// sums over states into shared memory, where the warps that finish tokens add them up.
 #pragma once
 
 #include "region.cuh"
@@ -159,29 +158,6 @@ __device__ __forceinline__ void lds_pack(Pack<DT, N>& p, const char* src) {
 template <int THREADS>
 __device__ __forceinline__ void meet() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
-}
-
-// The sums of M values over the L lanes `step`, 2 step, ... apart, of which each lane
-// keeps M / L (at least one: then several lanes have the same).  The kept ones are
-// v[0] .., the values [part, part + M / L) with part = the lane's number among the
-// L times M / L.  In a fixed order.
-template <int M, int L>
-__device__ __forceinline__ void sum_over(float* v, int lane, int step) {
-  if constexpr (L > 1) {
-    constexpr int kHalf = L / 2;
-    if constexpr (M > 1) {
-      const bool up = (lane & (step * kHalf)) != 0;
-#pragma unroll
-      for (int i = 0; i < M / 2; ++i) {
-        const float give = up ? v[i] : v[i + M / 2], keep = up ? v[i + M / 2] : v[i];
-        v[i] = keep + __shfl_xor_sync(kAll, give, step * kHalf);
-      }
-      sum_over<M / 2, kHalf>(v, lane, step);
-    } else {
-      v[0] += __shfl_xor_sync(kAll, v[0], step * kHalf);
-      sum_over<1, kHalf>(v, lane, step);
-    }
-  }
 }
 
 // Which of a tile's tokens (at most 32, one a lane) begin a packed sequence.

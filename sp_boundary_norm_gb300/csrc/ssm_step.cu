@@ -18,6 +18,14 @@ namespace spb {
 constexpr int kStepThreads = 256;
 constexpr int kStepBlocks = 4;         // of an SM, by their registers
 
+// The sum over a channel's L lanes, in a fixed order.
+template <int L>
+__device__ __forceinline__ float over_lanes(float v) {
+#pragma unroll
+  for (int step = L / 2; step > 0; step /= 2) v += __shfl_xor_sync(kAll, v, step);
+  return v;
+}
+
 // R: sequences of a step, with kSsmStepTokens tokens in all at most
 template <int DT, int N, int R>
 __global__ void __launch_bounds__(kStepThreads, kStepBlocks)
@@ -139,11 +147,10 @@ ssm_step_kernel(const SsmParams P) {
         F2 acc = mul2(h[i][0], c[0]);
         if constexpr (K == 2) acc = fma2(h[i][1], c[1], acc);
         const float2 v = split(acc);
-        float sum[1] = {v.x + v.y};
-        sum_over<1, G>(sum, tid, 1);
+        const float sum = over_lanes<G>(v.x + v.y);
         if (on && tid % G == 0) {
           Pack<DT, 1> p;
-          const float f[1] = {(sum[0] + x.z) * x.w};
+          const float f[1] = {(sum + x.z) * x.w};
           pack(p, f);
           store_pack(y, p);
         }
