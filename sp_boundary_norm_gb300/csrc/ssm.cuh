@@ -96,8 +96,10 @@ __device__ __forceinline__ F2 decay2(F2 x) {
 // makes the same digits: 8 x 8192 x 1024 packed forward 607 us, so 522; without either 467,
 // and a state that remembers 1000 tokens off by 1e-5.)  Growing states, and products that
 // left float32's range on the way, are left as they are.
+// EXACT: for a call's only step.
+template <bool EXACT = false>
 __device__ __forceinline__ F2 settle2(F2 x, F2 all) {
-  const F2 lost = fma2(all, f2(-1.f, -1.f), pow2(x));
+  const F2 lost = fma2(all, f2(-1.f, -1.f), EXACT ? decay2(x) : pow2(x));
   const F2 inverse = fma2(all, f2(-1.f, -1.f), f2(2.f, 2.f));
   const float2 v = split(x), c = split(mul2(lost, inverse));
   constexpr float kMost = 0x1p-12f;

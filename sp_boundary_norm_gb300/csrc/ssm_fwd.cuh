@@ -39,8 +39,8 @@ __host__ __device__ constexpr int walk_threads(int mode) {
   return kSsmPart + kSsmPrep + (mode == kSsmOut ? kSsmPart : 0);
 }
 // Registers of a thread for outputs: 16 tokens' sums and decays wait in those that hold
-// states (at 128 for all of them they spill, and 522 us become 666).  The block starts with
-// 128 each, which is what both shares add up to.
+// states (at 128 for all of them they spill, and 522 us become 666; at 176 and 112 565, at
+// 224 and 96 534).  The block starts with 128 each, which is what both shares add up to.
 constexpr int kSsmStateRegisters = 200, kSsmHelpRegisters = 104, kSsmRegisters = 128;
 static_assert(kSsmPart * kSsmStateRegisters + (kSsmPrep + kSsmPart) * kSsmHelpRegisters ==
                   walk_threads(kSsmOut) * kSsmRegisters, "what a block has");

@@ -3,14 +3,15 @@
 // as many a step as have 16 tokens (at most four).  A step's states and tokens are asked
 // for one step ahead; the tokens are prepared (softplus, d u, D u, silu(z)) once for each
 // channel in shared memory, where a channel's lanes then find them.  Measured on a GB300,
-// bf16, 64 sequences of 8 ranks' 1024 channels of 16 states: 72 MB in 17.2 us, 4.2 TB/s;
-// the same accesses without the arithmetic took 17.7.  (A block for every sequence and 32
-// channels, which prepared its tokens itself: 23 us; three blocks an SM 21.)
+// bf16, 64 sequences of 8 ranks' 1024 channels of 16 states: 72 MB in 18.3 us, 3.9 TB/s; with
+// the hardware's power alone for a decay 17.7, as the same accesses without the arithmetic.
+// (A block for every sequence and 32 channels, which prepared its tokens itself: 23 us; three
+// blocks an SM 21.)
 //
 // Up to 16 tokens a sequence (kSsmStepTokens) come here.  The other form's blocks start up
-// for one sequence each: 64 sequences of 1, 4, 8 and 16 tokens took 13, 26, 45 and 82 us
+// for one sequence each: 64 sequences of 1, 4, 8 and 16 tokens took 15, 33, 53 and 95 us
 // here (in place, replayed) and 123, 138, 160 and 165 there; one sequence of 1, 8 and 16
-// tokens 2.2, 3.1 and 3.7 here and 3.1, 3.7 and 3.5 there.
+// tokens 2.3, 3.1 and 4.1 here and 3.1, 3.7 and 3.5 there.
 #include "ssm.cuh"
 
 namespace spb {
@@ -33,6 +34,9 @@ ssm_step_kernel(const SsmParams P) {
   using L = SsmLanes<N>;
   constexpr int E = ElemSize<DT>::value, K = L::kPairs, G = L::kLanes;
   constexpr int CB = kStepThreads / G;
+  // Up to four tokens have exact decays each; of more, the call's are made up for together
+  // (64 sequences of 16 tokens 95 us, so 109, without either 82; of four 32, so 33).
+  constexpr bool kSettled = R < 4;
   __shared__ float4 prepared[2][kSsmStepTokens][CB];       // d, d u, D u, silu(z)
   __shared__ __align__(16) float shared[2][kSsmStepTokens][2 * N];
   pdl_wait();
@@ -135,6 +139,9 @@ ssm_step_kernel(const SsmParams P) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (i0 + i >= rows) break;
+      F2 all[K], steps = 0;
+#pragma unroll
+      for (int p = 0; p < K; ++p) all[p] = f2(1.f, 1.f);
       for (int t = 0; t < s; ++t, token += CB, bc += 2 * N, y += P.ld_y) {
         const float4 x = *token;
         const F2 step = f2(x.x, x.x), in = f2(x.y, x.y);
@@ -142,8 +149,12 @@ ssm_step_kernel(const SsmParams P) {
         load_states(bc, b);
         load_states(bc + N, c);
 #pragma unroll
-        for (int p = 0; p < K; ++p)
-          h[i][p] = fma2(decay2(mul2(step, a2[p])), h[i][p], mul2(in, b[p]));
+        for (int p = 0; p < K; ++p) {
+          const F2 e = mul2(step, a2[p]), a = kSettled ? pow2(e) : decay2(e);
+          if constexpr (kSettled) all[p] = mul2(all[p], a);
+          h[i][p] = fma2(a, h[i][p], mul2(in, b[p]));
+        }
+        if constexpr (kSettled) steps = add2(steps, step);
         F2 acc = mul2(h[i][0], c[0]);
         if constexpr (K == 2) acc = fma2(h[i][1], c[1], acc);
         const float2 v = split(acc);
@@ -154,6 +165,11 @@ ssm_step_kernel(const SsmParams P) {
           pack(p, f);
           store_pack(y, p);
         }
+      }
+      if constexpr (kSettled) {
+#pragma unroll
+        for (int p = 0; p < K; ++p)
+          h[i][p] = mul2(h[i][p], settle2<true>(mul2(steps, a2[p]), all[p]));
       }
       if (hT != nullptr) {
         store_states(hT, h[i]);
