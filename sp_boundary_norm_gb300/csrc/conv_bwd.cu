@@ -9,7 +9,7 @@
 // always in the same order.
 //
 // Bound by reading x and dy and writing dx: on a GB300, bf16, 8 ranks' 16,384 x 1024 with
-// four taps and silu, 805 MB in 151 us, 5.3 TB/s; per channel and token two reciprocals,
+// four taps and silu, 805 MB in 155 us, 5.2 TB/s; per channel and token two reciprocals,
 // two exponentials and 13 products are then on their way in 16 warps an SM.  Two channels a
 // thread, for twice the warps, took a third longer (every load is half as wide); five
 // blocks an SM spilled and took 30 % longer.

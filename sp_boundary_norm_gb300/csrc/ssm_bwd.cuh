@@ -18,10 +18,12 @@
 // keeps its even places and hands on its odd ones whichever it is; B and C lie in shared
 // memory in each of these orders.
 //
-// What bounds it is, as in the forward's walk, one warp of states a scheduler: 400 clocks a
-// token, in which the scheduler issues 183 instructions of its two warps (in 44 % of the
-// time; shared memory moves in 48 %).  Measured on a GB300, bf16, 8 x 8192 x 1024 tokens of 16
-// states, gated: 1646 us; its 950 MB would take 140.  Not faster: decays kept in
+// What bounds it is, as in the forward's walk, one warp of states a scheduler: 447 clocks a
+// token, in which the scheduler issues 199 instructions of its two warps (in 46 % of the
+// time; shared memory moves in 45 %).  Measured on a GB300, bf16, 8 x 8192 x 1024 tokens of 16
+// states, gated: 1768 us, 1646 without what settle2 needs.  Its inputs and outputs, 944 MB,
+// the saved states, 268, and its parts of dB and dC, 134, would take 200, its products 430.
+// Not faster: decays kept in
 // registers (the same), two states a lane in twice the warps (a quarter slower: d, B, C
 // and the parts go through shared memory twice as often), the next step's way there beside
 // this one's way back (a quarter slower), eight helping warps or registers handed between

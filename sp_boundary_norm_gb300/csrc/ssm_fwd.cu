@@ -33,10 +33,10 @@ SsmSplit ssm_split(int64_t b, int64_t s, int64_t c, int n, int groups, int t, bo
   const int64_t blocks = b * t * groups * k.slabs, sms = device_sm_count();
   // A block has an SM to itself, so a call takes as many waves of blocks as they need, each
   // as long as a chunk and some 48 tokens' time to begin.  Chunks cost a walk for what
-  // enters them, 66 clocks a token beside the forward's 118 and the backward's 400, two
+  // enters them, 75 clocks a token beside the forward's 132 and the backward's 447, two
   // launches, and their joining.  (Measured: 8 x 8192 x 1024, 128 blocks, forward 531 us
-  // whole, 675 cut; 32,769 x 512, 8 blocks that would walk 1.9 ms, cut in 19 170 us; 256 x
-  // 64, forward and backward in two chunks 18 and 38 us, in 16 10 and 15.)
+  // whole, 675 cut; 32,769 x 512, 8 blocks that would walk 2.0 ms, cut
+  // in 19 191 us; 256 x 64, forward and backward in two chunks 18 and 38 us, in 16 10 and 17.)
   const double walk = bwd ? 1.2 : 1.6, start = bwd ? 15 : 50, join = bwd ? 6 : 16;
   double least = 0;
   for (int64_t n = 1; n <= kMostChunks && (n == 1 || n * kSsmTile <= s); ++n) {

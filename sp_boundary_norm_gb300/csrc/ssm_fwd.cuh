@@ -10,16 +10,16 @@
 //
 // What bounds it is the chain of a token's work in the one warp of states that each of an
 // SM's schedulers has: loads from shared memory, an exponential and two products a state,
-// 118 clocks a token, in which the scheduler issues 64 instructions of all of its warps
-// (states saved).  Of a busy SM's time its schedulers issue in 55 %, shared memory moves in 70 % (without the loads of B and C at
-// all the walk took 2 % less), the exponentials take 34 %.  Measured on a GB300, bf16,
-// 8 x 8192 x 1024 packed tokens of 16 states, gated: 468 us (556 MB; the products alone
-// 118 us).  One role for all warps took 675 us, four preparing warps 472, 32 tokens a step
-// 612, storing the sums every eight tokens 509; rows asked for further ahead changed
-// nothing.
+// 132 clocks a token, in which the scheduler issues 74 instructions of all of its warps
+// (states saved).  Of a busy SM's time its schedulers issue in 56 %, shared memory moves in
+// 63 % (without the loads of B and C at all the walk took 2 % less), the exponentials take
+// 32 %.  Measured on a GB300, bf16, 8 x 8192 x 1024 packed tokens of 16 states, gated: 522 us
+// (556 MB; the products alone 118 us).  Without what settle2 needs it was 468, and then one
+// role for all warps took 675 us, four preparing warps 472, 32 tokens a step 612, storing the
+// sums every eight tokens 509; rows asked for further ahead changed nothing.
 //
 // A call with few blocks is cut into chunks in time: each chunk's last state
-// from a zero one and the sum of its steps (a walk of 66 clocks a token), the states that
+// from a zero one and the sum of its steps (a walk of 75 clocks a token), the states that
 // enter each chunk (ssm_join_kernel), and then all chunks at once.
 #include <type_traits>
 
