@@ -314,6 +314,10 @@ ssm_walk_kernel(const SsmParams P) {
     const int n_tok = tokens_of(t0);
     F2 steps = 0;
     F2 all[2][K];                      // the product of the step's decays (settle2)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int p = 0; p < K; ++p) all[c][p] = f2(1.f, 1.f);
     // one token: the states after it, and this lane's parts of its channels' sums with C;
     // ALONE: with a decay of its own
     auto token = [&](int t, auto alone) -> float2 {
@@ -367,10 +371,6 @@ ssm_walk_kernel(const SsmParams P) {
       // the sums wait in registers: without a store in between, a step's loads and
       // exponentials go ahead of its states
       float2 part[T];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int p = 0; p < K; ++p) all[c][p] = f2(1.f, 1.f);
 #pragma unroll
       for (int t = 0; t < T; ++t) part[t] = token(kBack ? T - 1 - t : t, std::false_type{});
       const float2 step = split(steps);
@@ -465,14 +465,14 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const SsmParams P) {
   const float* steps = P.steps + batch * P.chunks * P.t * P.c + chan;
   constexpr int kAhead = kJoinAhead;
   for (int n0 = 0; n0 < P.chunks; n0 += kAhead) {
-    float handed[kAhead], decay[kAhead];
+    float handed[kAhead], passed[kAhead];
     bool cut[kAhead];                  // a sequence begins in the chunk
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (n0 + i >= P.chunks) break;
       const int64_t k = BACK ? P.chunks - 1 - n0 - i : n0 + i;
       handed[i] = carry[k * width];
-      decay[i] = steps[k * P.t * P.c];
+      passed[i] = steps[k * P.t * P.c];
       cut[i] = false;
       if (packed) {
         const int64_t end = (k + 1) * P.chunk_len < P.s ? (k + 1) * P.chunk_len : P.s;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(const SsmParams P) {
       const int64_t k = BACK ? P.chunks - 1 - n0 - i : n0 + i;
       carry[k * width] = x;
       // (A > 0: a chunk's decay may overflow where the state behind it is zero or small)
-      const float half = pow2(0.5f * a2 * decay[i]);
+      const float half = decay(0.5f * a2 * passed[i]);
       x = cut[i] || x == 0.f ? handed[i] : fmaf(half, half * x, handed[i]);
     }
   }

@@ -71,6 +71,32 @@ def test_slow_states_keep_their_digits(dtype, c, n):
     assert off(dh0[0], i, slice(None)) <= WITHIN
 
 
+@pytest.mark.parametrize("c,n", [(8, 8), (8, 16), (16, 32)])
+def test_slow_states_through_many_chunks(c, n):
+    """32,768 tokens of few channels, in some 150 chunks: a state goes through the chunks'
+    decays, and through the last one's tokens.  A chunk's decay is applied in two halves:
+    four roundings each, sqrt(4 150 / 3) U; 220 tokens behind them sqrt(4 220 / 3) U, and
+    28 2^-25 to one side: 36 U at most, of which 2^-18.5 is 45.  Halves by the hardware's
+    power alone would be off to one side by 1e-8 to 2.5e-8 each, 5e-6 in all (84 U)."""
+    s = 1 << 15
+    i = decays(1, s, c, n, F32, 56)
+    i["dt"] *= 2.0 ** -6
+    i["A"] *= 2.0 / 3
+    args = ([i["zero"]], [i["dt"]], i["A"], [i["B"]], [i["C"]])
+    how = dict(softplus=False, h0=[i["h"]])
+    y, hT = nans(1, (1, s, c), F32), nans(1, (1, c, n), F32)
+    states = nans(1, sp.sp_selective_scan_states_shape(1, s, c, n), F32)
+    sp.sp_selective_scan_fwd(*args, y=y, hT=hT, states=states, **how,
+                             workspace=scratch(sp.sp_selective_scan_fwd_workspace_bytes(1, s, c, n, 1, 1)))
+    assert off(hT[0], i, slice(None)) <= 2.0 ** -18.5
+    out = {k: nans(1, (1, s, c), F32) for k in ("du", "ddt")}
+    out.update({k: nans(1, (1, s, n), F32) for k in ("dB", "dC")})
+    dh0 = nans(1, (1, c, n), F32)
+    sp.sp_selective_scan_bwd(*args, states, [i["zero"]], dhT=[i["h"]], dh0=dh0, **out, **how,
+                             workspace=scratch(sp.sp_selective_scan_bwd_workspace_bytes(1, s, c, n, 1, 1)))
+    assert off(dh0[0], i, slice(None)) <= 2.0 ** -18.5
+
+
 @pytest.mark.parametrize("n", [8, 16, 32, 64])
 @pytest.mark.parametrize("dtype,tokens", [(F32, 1), (BF, 2), (F32, 8), (FP, 16), (F32, 23)])
 def test_a_state_updated_in_place_keeps_its_digits(dtype, tokens, n):
